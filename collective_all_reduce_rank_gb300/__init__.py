@@ -44,7 +44,12 @@ RRA_ALGO_DIRECT = 4
 RRA_ALGO_COPY_ENGINE = 5
 RRA_ALGO_TREE = 6
 
+RRA_ACT_SILU = 0
+RRA_ACT_GELU_TANH = 1
+
 RRA_MAX_RANKS = 8
+
+RRA_CKPT_BLOCK = 128  # columns that share a scale in an 8-bit checkpoint
 
 DTYPE_NAMES = {RRA_INT32: "int32", RRA_FLOAT32: "float32", RRA_BFLOAT16: "bfloat16"}
 ALGO_NAMES = {RRA_ALGO_AUTO: "auto", RRA_ALGO_RING: "ring", RRA_ALGO_ONE_SHOT: "one_shot",
@@ -85,6 +90,7 @@ def _declare(lib):
     vp = ctypes.c_void_p
     vpp = ctypes.POINTER(ctypes.c_void_p)
     i, sz, u32, u64 = ctypes.c_int, ctypes.c_size_t, ctypes.c_uint32, ctypes.c_uint64
+    szp, i64 = ctypes.POINTER(ctypes.c_size_t), ctypes.c_int64
     sigs = {
         "rra_init": (i, [i, sz]),
         "rra_finalize": (i, []),
@@ -93,6 +99,16 @@ def _declare(lib):
         "rra_reduce_scatter": (i, [vpp, vpp, i, sz, i, i, i, vp]),
         "rra_all_gather": (i, [vpp, vpp, i, sz, i, i, vp]),
         "rra_allreduce_rmsnorm": (i, [vpp, vpp, i, sz, sz, vp, ctypes.c_float, i, vp]),
+        "rra_allreduce_rmsnorm_save8": (i, [vpp, vpp, i, sz, sz, vp, ctypes.c_float, vp, vp, vp, i, vp]),
+        "rra_rmsnorm_restore8": (i, [vp, vp, vp, vp, vp, sz, sz, i, vp]),
+        "rra_allreduce_rmsnorm_backward8_workspace_bytes": (sz, [sz, sz]),
+        "rra_allreduce_rmsnorm_backward8": (i, [vpp, vpp, i, sz, sz, vp, vp, vp, vp, vp, vp, sz, i, vp]),
+        "rra_gated_ffn_workspace_bytes": (sz, [i, sz, sz, sz, i]),
+        "rra_gated_ffn": (i, [vp, vpp, vpp, vpp, i, sz, sz, sz, i, i, vp, sz, vp]),
+        "rra_gated_ffn_backward": (i, [vp, vpp, vpp, vpp, vp, vpp, vpp, i, sz, sz, sz, i, i, vp, sz, vp]),
+        "rra_vocab_loss_workspace_bytes": (sz, [i, sz, sz, szp, i]),
+        "rra_vocab_loss": (i, [vp, vpp, szp, vp, i, sz, sz, i64, vp, vp, i, vp, sz, vp]),
+        "rra_vocab_loss_backward": (i, [vp, vpp, szp, vp, vp, vp, vp, vpp, i, sz, sz, i64, i, vp, sz, vp]),
         "rra_ll_wire_bytes": (sz, [sz]),
         "rra_ll128_wire_bytes": (sz, [sz]),
         "rra_ll_pack": (i, [vp, sz, vp, u32, vp]),
@@ -248,6 +264,204 @@ def rra_allreduce_rmsnorm(bufs, outs, gamma, hidden, eps=1e-6, rows=None, dtype=
     st = load().rra_allreduce_rmsnorm(_ptr_array(bufs), _ptr_array(outs), n, rows, hidden, _ptr(gamma),
                                       eps, dtype, _stream(stream, bufs[0] if bufs else None))
     return _ret(st, "rra_allreduce_rmsnorm", check)
+
+
+# -- the training step around a tensor-parallel all-reduce -------------------
+
+def _scratch(nbytes, like, stream, workspace):
+    """(tensor or pointer, bytes) of the caller's workspace, or of one made
+    here on the caller's stream (PyTorch's allocator reuses it in order)."""
+    if workspace is not None:
+        if isinstance(workspace, int):
+            raise TypeError("pass a workspace as a tensor")
+        return workspace, _nbytes(workspace)
+    import torch
+
+    ws = torch.empty(max(256, nbytes), dtype=torch.uint8, device=like.device)
+    if stream is not None:
+        if isinstance(stream, int):
+            raise ValueError("a raw stream handle needs an explicit workspace")
+        ws.record_stream(stream)
+    return ws, _nbytes(ws)
+
+
+def _expect(what, t, dtype, shape):
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must be %s of shape %s, got %s %s" % (what, dtype, tuple(shape), t.dtype, tuple(t.shape)))
+
+
+def _on_one_device(*ts):
+    first = ts[0].device
+    for t in ts:
+        if t is not None and t.device != first:
+            raise ValueError("tensors of one call must be on one device (%s and %s)" % (first, t.device))
+
+
+def _norm_shapes(bufs, outs, gamma, codes, scales, rstd, hidden):
+    import torch
+
+    rows = int(bufs[0].numel()) // hidden
+    nb = -(-hidden // RRA_CKPT_BLOCK)
+    if len(bufs) != len(outs):
+        raise ValueError("as many outputs as inputs are needed")
+    for t in list(bufs) + list(outs):
+        if t.dtype != bufs[0].dtype or t.numel() != rows * hidden:
+            raise ValueError("every rank's buffer must be %s with %d x %d elements" % (bufs[0].dtype, rows, hidden))
+    _expect("gamma", gamma, bufs[0].dtype, (hidden,))
+    if codes.element_size() != 1 or codes.numel() != rows * hidden:
+        raise ValueError("codes must be %d x %d bytes (uint8 or float8_e4m3fn)" % (rows, hidden))
+    _expect("scales", scales, torch.uint8, (rows, nb))
+    _expect("rstd", rstd, torch.float32, (rows,))
+    _on_one_device(*bufs, *outs, gamma, codes, scales, rstd)
+    return rows
+
+
+def rra_allreduce_rmsnorm_save8(bufs, outs, gamma, hidden, codes, scales, rstd, eps=1e-6, stream=None,
+                                check=True) -> int:
+    """All-reduce + RMSNorm that saves the sum in 8 bits for the backward
+    pass: codes [rows, hidden] (float8_e4m3fn or uint8), scales
+    [rows, ceil(hidden / 128)] uint8, rstd [rows] float32."""
+    rows = _norm_shapes(bufs, outs, gamma, codes, scales, rstd, hidden)
+    st = load().rra_allreduce_rmsnorm_save8(_ptr_array(bufs), _ptr_array(outs), len(bufs), rows, hidden, _ptr(gamma),
+                                            eps, _ptr(codes), _ptr(scales), _ptr(rstd), _dtype_of(bufs[0]),
+                                            _stream(stream, bufs[0]))
+    return _ret(st, "rra_allreduce_rmsnorm_save8", check)
+
+
+def rra_rmsnorm_restore8(codes, scales, rstd, gamma, out, stream=None, check=True) -> int:
+    """out = the checkpoint's values, times rstd and gamma unless None."""
+    import torch
+
+    rows, hidden = codes.shape
+    if codes.element_size() != 1 or tuple(out.shape) != (rows, hidden):
+        raise ValueError("codes must be bytes and out of the same shape")
+    _expect("scales", scales, torch.uint8, (rows, -(-hidden // RRA_CKPT_BLOCK)))
+    if rstd is not None:
+        _expect("rstd", rstd, torch.float32, (rows,))
+    if gamma is not None:
+        _expect("gamma", gamma, out.dtype, (hidden,))
+    _on_one_device(out, codes, scales, rstd, gamma)
+    st = load().rra_rmsnorm_restore8(_ptr(codes), _ptr(scales), _ptr(rstd), _ptr(gamma), _ptr(out), rows, hidden,
+                                     _dtype_of(out), _stream(stream, out))
+    return _ret(st, "rra_rmsnorm_restore8", check)
+
+
+def rra_allreduce_rmsnorm_backward8_workspace_bytes(rows: int, hidden: int) -> int:
+    return int(load().rra_allreduce_rmsnorm_backward8_workspace_bytes(rows, hidden))
+
+
+def rra_allreduce_rmsnorm_backward8(grads, dxs, codes, scales, rstd, gamma, dgamma, workspace=None, stream=None,
+                                    check=True) -> int:
+    """Sum of the ranks' gradients through the norm, from the checkpoint."""
+    import torch
+
+    hidden = int(gamma.numel())
+    rows = _norm_shapes(grads, dxs, gamma, codes, scales, rstd, hidden)
+    _expect("dgamma", dgamma, torch.float32, (hidden,))
+    _on_one_device(gamma, dgamma)
+    ws, nb = _scratch(rra_allreduce_rmsnorm_backward8_workspace_bytes(rows, hidden), gamma, stream, workspace)
+    st = load().rra_allreduce_rmsnorm_backward8(_ptr_array(grads), _ptr_array(dxs), len(grads), rows, hidden,
+                                                _ptr(codes), _ptr(scales), _ptr(rstd), _ptr(gamma), _ptr(dgamma),
+                                                _ptr(ws), nb, _dtype_of(grads[0]), _stream(stream, gamma))
+    return _ret(st, "rra_allreduce_rmsnorm_backward8", check)
+
+
+def rra_gated_ffn_workspace_bytes(nranks: int, tokens: int, hidden: int, width: int, backward) -> int:
+    return int(load().rra_gated_ffn_workspace_bytes(nranks, tokens, hidden, width, int(backward)))
+
+
+def _ffn_shapes(x, gates, ups, *per_token):
+    tokens, hidden = x.shape
+    width = int(gates[0].shape[0])
+    for w in list(gates) + list(ups):
+        _expect("a gate or up shard", w, x.dtype, (width, hidden))
+    for group in per_token:
+        for a in group:
+            _expect("a rank's activations", a, x.dtype, (tokens, width))
+        if len(group) != len(gates):
+            raise ValueError("one buffer per rank is needed")
+    if len(gates) != len(ups):
+        raise ValueError("as many up shards as gate shards are needed")
+    _on_one_device(x, *gates, *ups, *[a for group in per_token for a in group])
+    return tokens, hidden, width
+
+
+def rra_gated_ffn(x, gates, ups, acts, act=RRA_ACT_SILU, workspace=None, stream=None, check=True) -> int:
+    """acts[r] = act(x gates[r]^T) * (x ups[r]^T)."""
+    T, D, F = _ffn_shapes(x, gates, ups, acts)
+    n = len(gates)
+    ws, nb = _scratch(rra_gated_ffn_workspace_bytes(n, T, D, F, 0), x, stream, workspace)
+    st = load().rra_gated_ffn(_ptr(x), _ptr_array(gates), _ptr_array(ups), _ptr_array(acts), n, T, D, F, act,
+                              _dtype_of(x), _ptr(ws), nb, _stream(stream, x))
+    return _ret(st, "rra_gated_ffn", check)
+
+
+def rra_gated_ffn_backward(x, gates, ups, dacts, dx, dgates, dups, act=RRA_ACT_SILU, workspace=None, stream=None,
+                           check=True) -> int:
+    """Gradients of rra_gated_ffn: dx summed over the ranks, dgates, dups."""
+    T, D, F = _ffn_shapes(x, gates, ups, dacts)
+    n = len(gates)
+    _expect("dx", dx, x.dtype, (T, D))
+    if len(dgates) != n or len(dups) != n:
+        raise ValueError("one gradient per shard is needed")
+    for g in list(dgates) + list(dups):
+        _expect("a shard's gradient", g, x.dtype, (F, D))
+    _on_one_device(x, dx, *dgates, *dups)
+    ws, nb = _scratch(rra_gated_ffn_workspace_bytes(n, T, D, F, 1), x, stream, workspace)
+    st = load().rra_gated_ffn_backward(_ptr(x), _ptr_array(gates), _ptr_array(ups), _ptr_array(dacts), _ptr(dx),
+                                       _ptr_array(dgates), _ptr_array(dups), n, T, D, F, act, _dtype_of(x), _ptr(ws),
+                                       nb, _stream(stream, x))
+    return _ret(st, "rra_gated_ffn_backward", check)
+
+
+def _sizes(xs):
+    return (ctypes.c_size_t * len(xs))(*[int(v) for v in xs])
+
+
+def rra_vocab_loss_workspace_bytes(tokens: int, hidden: int, vocab, backward) -> int:
+    """vocab: the ranks' shard heights; backward 2: the least bytes the
+    backward pass runs with."""
+    return int(load().rra_vocab_loss_workspace_bytes(len(vocab), tokens, hidden, _sizes(vocab), int(backward)))
+
+
+def _loss_shapes(x, weights, targets, *rows):
+    import torch
+
+    T, D = x.shape
+    for w in weights:
+        _expect("a vocabulary shard", w, x.dtype, (w.shape[0], D))
+    _expect("targets", targets, torch.int64, (T,))
+    for r in rows:
+        _expect("a per-token buffer", r, torch.float32, (T,))
+    _on_one_device(x, *weights, targets, *rows)
+    return T, D, [int(w.shape[0]) for w in weights]
+
+
+def rra_vocab_loss(x, weights, targets, loss, lse, ignore_index=-100, workspace=None, stream=None, check=True) -> int:
+    """loss[t] = lse[t] - logit of targets[t], logits x W^T never kept; the
+    vocabulary is the ranks' weight shards, one after another."""
+    T, D, vocab = _loss_shapes(x, weights, targets, loss, lse)
+    ws, nb = _scratch(rra_vocab_loss_workspace_bytes(T, D, vocab, 0), x, stream, workspace)
+    st = load().rra_vocab_loss(_ptr(x), _ptr_array(weights), _sizes(vocab), _ptr(targets), len(weights), T, D,
+                               ignore_index, _ptr(loss), _ptr(lse), _dtype_of(x), _ptr(ws), nb, _stream(stream, x))
+    return _ret(st, "rra_vocab_loss", check)
+
+
+def rra_vocab_loss_backward(x, weights, targets, lse, grad_loss, dx, dweights, ignore_index=-100, workspace=None,
+                            stream=None, check=True) -> int:
+    """Gradients of rra_vocab_loss with respect to x and every shard."""
+    T, D, vocab = _loss_shapes(x, weights, targets, lse, grad_loss)
+    _expect("dx", dx, x.dtype, (T, D))
+    if len(dweights) != len(weights):
+        raise ValueError("one gradient per shard is needed")
+    for w, g in zip(weights, dweights):
+        _expect("a shard's gradient", g, x.dtype, w.shape)
+    _on_one_device(x, dx, *dweights)
+    ws, nb = _scratch(rra_vocab_loss_workspace_bytes(T, D, vocab, 1), x, stream, workspace)
+    st = load().rra_vocab_loss_backward(_ptr(x), _ptr_array(weights), _sizes(vocab), _ptr(targets), _ptr(lse),
+                                        _ptr(grad_loss), _ptr(dx), _ptr_array(dweights), len(weights), T, D,
+                                        ignore_index, _dtype_of(x), _ptr(ws), nb, _stream(stream, x))
+    return _ret(st, "rra_vocab_loss_backward", check)
 
 
 def rra_ll_wire_bytes(payload_bytes: int) -> int:

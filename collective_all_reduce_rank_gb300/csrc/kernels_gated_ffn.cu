@@ -1,0 +1,102 @@
+// kernels_gated_ffn.cu -- the column-parallel half of a gated feed-forward
+// block over the virtual ranks' weight shards:
+//
+//   g_r = x G_r^T,  u_r = x U_r^T,  a_r = act(g_r) * u_r
+//
+// Both projections, the activation and the product run in one kernel: a
+// tile's 256 accumulator columns are 128 gate columns and the same 128 up
+// columns (the first CTA of a pair stages gate rows, the second up rows), so
+// a thread finds g and u of one element in its own tensor-memory lane.  The
+// backward pass computes g and u again the same way and its epilogue turns
+// them and da into dg = da u act'(g) and du = da act(g), rounded to
+// bfloat16 (operands of the two gradient products, kernels_tc_store.cu).
+//
+//   silu(g) = g / (1 + exp(-g))
+//   gelu_tanh(g) = g / (1 + exp(-2z)), z = sqrt(2/pi) (g + 0.044715 g^3):
+//     0.5 (1 + tanh z) is the logistic function of 2z, which keeps its
+//     relative accuracy where 1 + tanh z cancels.
+#include "tc_epilogue.cuh"
+
+namespace rra {
+
+// sigma = logistic(k(g)), *slope = k'(g)
+template <int ACT>
+__device__ __forceinline__ float gate_sigma(float g, float* slope) {
+  float k = g;
+  *slope = 1.f;
+  if constexpr (ACT == RRA_ACT_GELU_TANH) {
+    constexpr float c = 1.5957691216057308f;  // 2 sqrt(2/pi)
+    k = c * g * fmaf(0.044715f * g, g, 1.f);
+    *slope = c * fmaf(3.f * 0.044715f * g, g, 1.f);
+  }
+  return __fdividef(1.f, 1.f + __expf(-k));
+}
+
+template <int ACT>
+struct EpiGate {
+  static __device__ __forceinline__ void run(const TcArgs& p, const TcTile& x, int row, int half, uint32_t addr) {
+    const TcGroup& g = p.group[x.group];
+    const int c0 = x.n * 128 + half * 64;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(g.out) + (long long)row * g.ld + c0;
+#pragma unroll 1
+    for (int c = 0; c < 64; c += 32) {
+      const int valid = g.N - c0 - c;
+      if (valid <= 0) break;
+      float a[32], b[32];
+      tc_ld32(addr + half * 64 + c, a);
+      tc_ld32(addr + 128 + half * 64 + c, b);
+      tc_ld_wait();
+      if (row >= g.M) continue;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        float unused;
+        a[j] = a[j] * gate_sigma<ACT>(a[j], &unused) * b[j];
+      }
+      tc_store_bf16(out + c, a, valid, g.vec, false);
+    }
+  }
+};
+
+template <int ACT>
+struct EpiGateBack {
+  static __device__ __forceinline__ void run(const TcArgs& p, const TcTile& x, int row, int half, uint32_t addr) {
+    const TcGroup& g = p.group[x.group];
+    const int c0 = x.n * 128 + half * 64;
+    const long long off = (long long)row * g.ld + c0;
+    const __nv_bfloat16* in = static_cast<const __nv_bfloat16*>(g.in) + (long long)row * g.ld_in + c0;
+#pragma unroll 1
+    for (int c = 0; c < 64; c += 32) {
+      const int valid = g.N - c0 - c;
+      if (valid <= 0) break;
+      float a[32], b[32], d[32];
+      tc_ld32(addr + half * 64 + c, a);
+      tc_ld32(addr + 128 + half * 64 + c, b);
+      tc_ld_wait();
+      if (row >= g.M) continue;
+      tc_load_bf16(in + c, d, valid, g.vec);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        float k;
+        const float s = gate_sigma<ACT>(a[j], &k);
+        const float h = a[j] * s;                            // act(g)
+        const float slope = s * fmaf(a[j] * k, 1.f - s, 1.f);  // act'(g)
+        a[j] = d[j] * b[j] * slope;
+        b[j] = d[j] * h;
+      }
+      tc_store_bf16(static_cast<__nv_bfloat16*>(g.out) + off + c, a, valid, true, true);
+      tc_store_bf16(static_cast<__nv_bfloat16*>(g.out2) + off + c, b, valid, true, true);
+    }
+  }
+};
+
+cudaError_t launch_tc_gate(const TcArgs& p, cudaStream_t s, int* grid) {
+  return p.act == RRA_ACT_SILU ? tc_launch<false, false, EpiGate<RRA_ACT_SILU>>(p, s, grid)
+                               : tc_launch<false, false, EpiGate<RRA_ACT_GELU_TANH>>(p, s, grid);
+}
+
+cudaError_t launch_tc_gate_back(const TcArgs& p, cudaStream_t s, int* grid) {
+  return p.act == RRA_ACT_SILU ? tc_launch<false, false, EpiGateBack<RRA_ACT_SILU>>(p, s, grid)
+                               : tc_launch<false, false, EpiGateBack<RRA_ACT_GELU_TANH>>(p, s, grid);
+}
+
+}  // namespace rra

@@ -18,6 +18,7 @@
 
 #include "rra.h"
 #include "rra_internal.h"
+#include "tc_host.h"
 
 using namespace rra;
 
@@ -765,6 +766,13 @@ void rra::decode_status(const DevStatus& h, int32_t info[4]) {
   info[2] = peer == 0xFFFF ? -1 : peer;
   info[3] = (int)((d >> 32) & 0x7FFFFFFF);
 }
+
+DevStatus* rra::device_status() {
+  DevState* st = current_state(nullptr);
+  return st && st->ready ? st->ws.status : nullptr;
+}
+
+int rra::device_sms() { return sm_count(); }
 
 int rra::max_ctas_cap() {
   int m = g_max_ctas.load();

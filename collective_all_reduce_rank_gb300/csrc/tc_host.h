@@ -1,0 +1,110 @@
+// tc_host.h -- what the host planning of the training operators and their
+// tensor-core kernels share: argument structs, tensor maps, launchers.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "rra_internal.h"
+
+namespace rra {
+
+constexpr int kTcMaxGroups = 2 * kMaxRanks;
+constexpr int kTcKBlock = 64;              // K elements per stage (128 bytes)
+constexpr int kTcBand = 8;  // tile rows per band of the tile walk
+
+// One output of a launch: an M x N product tiled 256 x 256.  `a` and `b`
+// index the tensor maps (unused when the launch walks K segments).
+struct TcGroup {
+  int a, b;
+  int tile0;   // first tile of the group
+  int mt, nt;  // tiles
+  int M, N;    // extents of the output (rows and columns stored)
+  int m0, n0;  // where the group starts along A's and B's M / N axes
+  void* out;
+  void* out2;
+  const void* in;
+  long long ld;     // elements between rows of out (and out2)
+  long long ld_in;  // elements between rows of in
+  int vec;          // rows of out (and in) start on 16 bytes
+  long long col0;   // global column of this group's column 0
+  int part0;        // column tiles of the groups before this one
+};
+
+struct TcArgs {
+  CUtensorMap a[kTcMaxGroups];
+  CUtensorMap b[kTcMaxGroups];
+  TcGroup group[kTcMaxGroups];
+  int seg_k0[kTcMaxGroups];  // first K block of each segment
+  int ngroups, nsegs;
+  int tiles;    // tiles of all groups (per split)
+  int splits;   // parts of the K axis, each with an output of its own
+  int kblocks;  // K blocks of 64 over all segments
+  int pair_b;   // CTA c of a pair takes map b + c (gate and up weights), 128 columns per tile each
+  // epilogue operands
+  long long split_stride;  // elements between the outputs of two splits
+  int accumulate;          // add to the float32 output
+  int act;
+  const long long* targets;
+  long long ignore_index, vocab;
+  const float* lse;
+  const float* grad;
+  float2* part;      // [column part][part_ld] running maximum and sum
+  long long part_ld;
+  float* hit;        // logit of the row's target
+  DevStatus* status;
+};
+
+// Clusters of two CTAs to launch for `tiles` tiles: one per SM pair, at
+// most the SM budget.
+int tc_clusters(int tiles);
+
+// Tensor maps over a dense matrix of bfloat16: `inner` contiguous elements,
+// `rows` rows, `ld` elements from row to row (a multiple of 8), 16-byte
+// aligned base.  K-major boxes are 64 x 128 (K x rows of M or N), MN-major
+// boxes 64 x 64 (M or N x rows of K).  False if the driver refuses.
+bool tc_map(CUtensorMap* m, const void* base, size_t inner, size_t rows, size_t ld, bool mn_major);
+
+// Products (kernels_vocab_loss.cu, kernels_gated_ffn.cu, kernels_tc_store.cu)
+cudaError_t launch_tc_lse(const TcArgs& p, cudaStream_t s, int* grid);        // K-major x K-major
+cudaError_t launch_tc_dlogits(const TcArgs& p, cudaStream_t s, int* grid);    // K-major x K-major
+cudaError_t launch_tc_gate(const TcArgs& p, cudaStream_t s, int* grid);       // K-major x K-major
+cudaError_t launch_tc_gate_back(const TcArgs& p, cudaStream_t s, int* grid);  // K-major x K-major
+// out = A B for A K-major, B MN-major (the gradient of the input): bfloat16
+// rows, or float32 rows (added to when p.accumulate).
+cudaError_t launch_tc_input_grad(const TcArgs& p, bool f32, cudaStream_t s, int* grid);
+// out = A^T B, both MN-major (the gradient of the weights): bfloat16 rows.
+cudaError_t launch_tc_weight_grad(const TcArgs& p, cudaStream_t s, int* grid);
+
+// Row-wise helpers
+cudaError_t launch_loss_join(const float2* part, long long part_ld, int parts, const float* hit,
+                             const long long* targets, long long ignore_index, long long vocab, int rows,
+                             float* loss, float* lse, cudaStream_t s);
+// out[i] = bfloat16(sum over s of slots[s * stride + i])
+cudaError_t launch_join_slots(const float* slots, int n, long long stride, void* out, long long count,
+                              cudaStream_t s);
+// dst[r][0..cols) = src[r][0..cols), dst rows ld elements apart
+cudaError_t launch_pad_rows(const void* src, void* dst, long long rows, long long cols, long long ld,
+                            cudaStream_t s);
+
+// Training-side norm kernels (kernels_norm8.cu)
+constexpr int kCkptBlock = 128;
+cudaError_t launch_norm_save8(int n, int dt, bool vec, const void* const* in, void* const* out, const void* gamma,
+                              size_t rows, size_t hidden, float eps, void* codes, void* scales, float* rstd,
+                              cudaStream_t s);
+cudaError_t launch_norm_restore8(int dt, bool vec, const void* codes, const void* scales, const float* rstd,
+                                 const void* gamma, void* out, size_t rows, size_t hidden, cudaStream_t s);
+// CTAs of the backward kernel (each leaves one row of dgamma partials)
+int norm_back8_ctas(size_t rows);
+cudaError_t launch_norm_back8(int n, int dt, bool vec, const void* const* grads, void* const* dxs,
+                              const void* codes, const void* scales, const float* rstd, const void* gamma,
+                              float* dgamma, float* part, size_t rows, size_t hidden, cudaStream_t s);
+
+// Device status word of rra_init on the current device (null: not initialised).
+DevStatus* device_status();
+int device_sms();
+
+}  // namespace rra

@@ -299,6 +299,159 @@ rra_status_t rra_allreduce_rmsnorm(const void* const* bufs, void* const* outs, i
                                    rra_dtype_t dtype, rra_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* the training step around a tensor-parallel all-reduce                    */
+/* ------------------------------------------------------------------------ */
+/*
+ * Operators that sit next to the all-reduce in a tensor-parallel training
+ * step ([ILP] "Deep dive": a column-parallel layer, then a row-parallel
+ * layer, then the all-reduce; [AIH] "Source code": the fused all-reduce +
+ * RMSNorm).  Weights are held as one shard per virtual rank, separate
+ * buffers; activations that every rank holds alike are passed once (their
+ * n copies are the same bytes).  Where a multi-GPU step would all-reduce a
+ * partial result (the softmax statistics, the input gradients), the sum
+ * over ranks is part of the operator, in float32.
+ *
+ * Matrices are dense and row-major; dtype is RRA_BFLOAT16 for the
+ * operators with matrix products (products of bfloat16 operands summed in
+ * float32; others are RRA_ERR_UNSUPPORTED) and RRA_FLOAT32 or RRA_BFLOAT16
+ * for the norm.  Matrices that a product reads (x, gates, ups, weights)
+ * must be 16-byte aligned (else RRA_ERR_UNSUPPORTED: they are read by bulk
+ * tensor copies); rows that are not whole 16-byte units (hidden % 8 != 0)
+ * are first copied to padded rows in the workspace.  Every other buffer
+ * needs its element's alignment only.
+ *
+ * The products need rra_init (their bounded internal waits report to the
+ * device status word).  `workspace` is a device buffer of the caller,
+ * 256-byte aligned, of at least the bytes the *_workspace_bytes function
+ * gives; its contents need no preparation and mean nothing between calls.
+ * Calls with different workspaces may overlap on the GPU; calls that share
+ * one must be ordered.  Results do not depend on timing (no atomics).
+ * Outputs must not overlap inputs, the workspace or one another
+ * (RRA_ERR_ALIAS), but for the in-place forms named below.  A buffer of no
+ * elements may be NULL. */
+
+/** Activation of the gated feed-forward block. */
+typedef enum {
+  RRA_ACT_SILU = 0,     /* g / (1 + exp(-g)) */
+  RRA_ACT_GELU_TANH = 1 /* 0.5 g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) */
+} rra_act_t;
+
+/** rra_allreduce_rmsnorm that also saves what the backward pass needs
+ *  ([AIH] "Source code": the fused all-reduce + RMSNorm; its training
+ *  counterpart).  outs as there, bit for bit; and
+ *  - codes: rows x hidden bytes, s in 8 bits: per block of 128 columns of a
+ *    row (the last one may be short), b = bfloat16(s), e the smallest
+ *    integer in [-127, 120] with max |b| <= 448 * 2^e over the block's
+ *    finite values, code = e4m3(b * 2^-e), nearest even; a value that is
+ *    not finite becomes the NaN code;
+ *  - scales: rows x ceil(hidden / 128) bytes, e + 127;
+ *  - rstd: rows float32, 1 / sqrt(mean_j(s^2) + eps).
+ *  Errors as rra_allreduce_rmsnorm (null codes, scales or rstd too). */
+rra_status_t rra_allreduce_rmsnorm_save8(const void* const* bufs, void* const* outs, int nranks, size_t rows,
+                                         size_t hidden, const void* gamma, float eps, void* codes, void* scales,
+                                         float* rstd, rra_dtype_t dtype, rra_stream_t stream);
+
+/** The activations a checkpoint of rra_allreduce_rmsnorm_save8 stands for
+ *  ([AIH] "Source code", as above; the recomputation of a backward pass):
+ *  out[i][j] = code * 2^e * rstd[i] * gamma[j], rounded to dtype once.
+ *  rstd or gamma (dtype) may be NULL: that factor is left out (both NULL:
+ *  the saved sum itself).  Errors: RRA_ERR_INVALID_ARG, RRA_ERR_UNSUPPORTED
+ *  (hidden > 51200), RRA_ERR_ALIAS, RRA_ERR_CUDA. */
+rra_status_t rra_rmsnorm_restore8(const void* codes, const void* scales, const float* rstd, const void* gamma,
+                                  void* out, size_t rows, size_t hidden, rra_dtype_t dtype, rra_stream_t stream);
+
+/** Workspace bytes of rra_allreduce_rmsnorm_backward8 ([AIH] "Source code";
+ *  column sums of dgamma). */
+size_t rra_allreduce_rmsnorm_backward8_workspace_bytes(size_t rows, size_t hidden);
+
+/** Backward pass of rra_allreduce_rmsnorm_save8 ([AIH] "Source code", as
+ *  above).  The ranks' gradients of the normalised rows are summed (float32,
+ *  ascending ranks: the all-reduce a column-parallel layer's backward
+ *  needs) and taken through the norm, the saved sum read from its 8-bit
+ *  checkpoint:
+ *    dy = SUM_k grads[k],  h = code * 2^e * rstd,  w = dy * gamma,
+ *    dxs[r] = rstd * (w - h * mean_j(w * h))    for every r,
+ *    dgamma[j] = SUM_i dy[i][j] * h[i][j]       (float32)
+ *  dxs is the gradient of the sum and so of every rank's addend.  In place
+ *  (dxs[r] == grads[r]) is allowed.  rows == 0 writes zeros to dgamma.
+ *  Errors as rra_allreduce_rmsnorm; RRA_ERR_WORKSPACE. */
+rra_status_t rra_allreduce_rmsnorm_backward8(const void* const* grads, void* const* dxs, int nranks, size_t rows,
+                                             size_t hidden, const void* codes, const void* scales,
+                                             const float* rstd, const void* gamma, float* dgamma, void* workspace,
+                                             size_t workspace_bytes, rra_dtype_t dtype, rra_stream_t stream);
+
+/** Workspace bytes of rra_gated_ffn (backward == 0) or
+ *  rra_gated_ffn_backward ([ILP] "Deep dive": the column-parallel layer). */
+size_t rra_gated_ffn_workspace_bytes(int nranks, size_t tokens, size_t hidden, size_t width, int backward);
+
+/** Column-parallel half of a gated feed-forward block ([ILP] "Deep dive":
+ *  column-parallel, then row-parallel).  x: tokens x hidden; gates[r],
+ *  ups[r]: width x hidden; acts[r]: tokens x width,
+ *    acts[r] = act(x gates[r]^T) * (x ups[r]^T),
+ *  both projections, the activation and the product in one kernel, float32
+ *  until the one rounding of acts.  tokens == 0 or width == 0 launches
+ *  nothing.  Errors: RRA_ERR_INVALID_ARG (null, hidden 0, bad act,
+ *  misaligned), RRA_ERR_UNSUPPORTED (dtype, a matrix not 16-byte aligned,
+ *  an extent of 2^31 or more, nranks > RRA_MAX_RANKS),
+ *  RRA_ERR_NOT_INITIALIZED, RRA_ERR_ALIAS, RRA_ERR_WORKSPACE,
+ *  RRA_ERR_CUDA. */
+rra_status_t rra_gated_ffn(const void* x, const void* const* gates, const void* const* ups, void* const* acts,
+                           int nranks, size_t tokens, size_t hidden, size_t width, rra_act_t act,
+                           rra_dtype_t dtype, void* workspace, size_t workspace_bytes, rra_stream_t stream);
+
+/** Backward pass of rra_gated_ffn ([ILP] "Deep dive"): dacts[r] tokens x
+ *  width in; dx tokens x hidden (the SUM over ranks, what a multi-GPU step
+ *  all-reduces), dgates[r] and dups[r] width x hidden out.  The projections
+ *  are computed again from x, not read; dg = dacts * u * act'(g) and
+ *  du = dacts * act(g) are rounded to bfloat16 as operands of the gradient
+ *  products, whose sums are float32.  tokens == 0 writes zeros to dgates
+ *  and dups; width == 0 zeros to dx.  Errors as rra_gated_ffn. */
+rra_status_t rra_gated_ffn_backward(const void* x, const void* const* gates, const void* const* ups,
+                                    const void* const* dacts, void* dx, void* const* dgates, void* const* dups,
+                                    int nranks, size_t tokens, size_t hidden, size_t width, rra_act_t act,
+                                    rra_dtype_t dtype, void* workspace, size_t workspace_bytes,
+                                    rra_stream_t stream);
+
+/** Workspace bytes of rra_vocab_loss (backward == 0) or
+ *  rra_vocab_loss_backward ([ILP] "Deep dive": a layer's weights split over
+ *  the ranks).  vocab: host array of nranks shard heights.  For the backward
+ *  pass this holds pieces of the vocabulary of up to 512 MiB; it also
+ *  accepts less, down to rra_vocab_loss_workspace_bytes(..., 2), which holds
+ *  a piece of 256 columns (smaller pieces are slower, not different but for
+ *  the rounding of dx's float32 sums). */
+size_t rra_vocab_loss_workspace_bytes(int nranks, size_t tokens, size_t hidden, const size_t* vocab, int backward);
+
+/** Softmax cross entropy over a vocabulary held as shards of the ranks
+ *  ([ILP] "Deep dive"), the logits never kept.  x: tokens x hidden;
+ *  weights[r]: vocab[r] x hidden (ranks' rows follow one another in the
+ *  vocabulary; a shard may be empty); targets: tokens int64 (device);
+ *    l = x W^T,  lse[t] = log SUM_v exp l[t][v],
+ *    loss[t] = lse[t] - l[t][targets[t]]   (float32)
+ *  loss[t] is 0 where targets[t] == ignore_index and NaN where it is any
+ *  other value outside the vocabulary.  tokens == 0 launches nothing.
+ *  Errors: RRA_ERR_INVALID_ARG (an empty vocabulary too), and as
+ *  rra_gated_ffn. */
+rra_status_t rra_vocab_loss(const void* x, const void* const* weights, const size_t* vocab, const int64_t* targets,
+                            int nranks, size_t tokens, size_t hidden, int64_t ignore_index, float* loss,
+                            float* lse, rra_dtype_t dtype, void* workspace, size_t workspace_bytes,
+                            rra_stream_t stream);
+
+/** Gradient of rra_vocab_loss ([ILP] "Deep dive"): grad_loss[t] float32 and
+ *  the lse that call gave in; dx (tokens x hidden, summed over all shards)
+ *  and dweights[r] (vocab[r] x hidden) out.  Piece by piece of the
+ *  vocabulary the logits are computed again,
+ *    dl[t][v] = (exp(l[t][v] - lse[t]) - [v == targets[t]]) * grad_loss[t]
+ *  is rounded to bfloat16 as operand of the two gradient products, and
+ *  their sums are float32.  A row whose target is ignore_index or outside
+ *  the vocabulary has a zero gradient, whatever grad_loss holds there.
+ *  tokens == 0 writes zeros to dweights.  Errors as rra_vocab_loss. */
+rra_status_t rra_vocab_loss_backward(const void* x, const void* const* weights, const size_t* vocab,
+                                     const int64_t* targets, const float* lse, const float* grad_loss, void* dx,
+                                     void* const* dweights, int nranks, size_t tokens, size_t hidden,
+                                     int64_t ignore_index, rra_dtype_t dtype, void* workspace,
+                                     size_t workspace_bytes, rra_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* LL and LL128 wire formats ([AIH] "Protocols")                            */
 /* ------------------------------------------------------------------------ */
 
