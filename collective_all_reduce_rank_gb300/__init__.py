@@ -16,6 +16,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 import threading
 
 from . import build as _build
@@ -90,7 +91,7 @@ def _declare(lib):
     vp = ctypes.c_void_p
     vpp = ctypes.POINTER(ctypes.c_void_p)
     i, sz, u32, u64 = ctypes.c_int, ctypes.c_size_t, ctypes.c_uint32, ctypes.c_uint64
-    szp, i64 = ctypes.POINTER(ctypes.c_size_t), ctypes.c_int64
+    i64 = ctypes.c_int64
     sigs = {
         "rra_init": (i, [i, sz]),
         "rra_finalize": (i, []),
@@ -99,16 +100,17 @@ def _declare(lib):
         "rra_reduce_scatter": (i, [vpp, vpp, i, sz, i, i, i, vp]),
         "rra_all_gather": (i, [vpp, vpp, i, sz, i, i, vp]),
         "rra_allreduce_rmsnorm": (i, [vpp, vpp, i, sz, sz, vp, ctypes.c_float, i, vp]),
-        "rra_allreduce_rmsnorm_save8": (i, [vpp, vpp, i, sz, sz, vp, ctypes.c_float, vp, vp, vp, i, vp]),
+        # host arrays of these calls travel as packed bytes
+        "rra_allreduce_rmsnorm_save8": (i, [vp, vp, i, sz, sz, vp, ctypes.c_float, vp, vp, vp, i, vp]),
         "rra_rmsnorm_restore8": (i, [vp, vp, vp, vp, vp, sz, sz, i, vp]),
         "rra_allreduce_rmsnorm_backward8_workspace_bytes": (sz, [sz, sz]),
-        "rra_allreduce_rmsnorm_backward8": (i, [vpp, vpp, i, sz, sz, vp, vp, vp, vp, vp, vp, sz, i, vp]),
+        "rra_allreduce_rmsnorm_backward8": (i, [vp, vp, i, sz, sz, vp, vp, vp, vp, vp, vp, sz, i, vp]),
         "rra_gated_ffn_workspace_bytes": (sz, [i, sz, sz, sz, i]),
-        "rra_gated_ffn": (i, [vp, vpp, vpp, vpp, i, sz, sz, sz, i, i, vp, sz, vp]),
-        "rra_gated_ffn_backward": (i, [vp, vpp, vpp, vpp, vp, vpp, vpp, i, sz, sz, sz, i, i, vp, sz, vp]),
-        "rra_vocab_loss_workspace_bytes": (sz, [i, sz, sz, szp, i]),
-        "rra_vocab_loss": (i, [vp, vpp, szp, vp, i, sz, sz, i64, vp, vp, i, vp, sz, vp]),
-        "rra_vocab_loss_backward": (i, [vp, vpp, szp, vp, vp, vp, vp, vpp, i, sz, sz, i64, i, vp, sz, vp]),
+        "rra_gated_ffn": (i, [vp, vp, vp, vp, i, sz, sz, sz, i, i, vp, sz, vp]),
+        "rra_gated_ffn_backward": (i, [vp, vp, vp, vp, vp, vp, vp, i, sz, sz, sz, i, i, vp, sz, vp]),
+        "rra_vocab_loss_workspace_bytes": (sz, [i, sz, sz, vp, i]),
+        "rra_vocab_loss": (i, [vp, vp, vp, vp, i, sz, sz, i64, vp, vp, i, vp, sz, vp]),
+        "rra_vocab_loss_backward": (i, [vp, vp, vp, vp, vp, vp, vp, vp, i, sz, sz, i64, i, vp, sz, vp]),
         "rra_ll_wire_bytes": (sz, [sz]),
         "rra_ll128_wire_bytes": (sz, [sz]),
         "rra_ll_pack": (i, [vp, sz, vp, u32, vp]),
@@ -267,53 +269,113 @@ def rra_allreduce_rmsnorm(bufs, outs, gamma, hidden, eps=1e-6, rows=None, dtype=
 
 
 # -- the training step around a tensor-parallel all-reduce -------------------
+#
+# These calls check shapes, types, devices and contiguity of every tensor.
+# The small ones are bound by the host, so the checks read each attribute
+# once and nothing is imported or looked up twice.
 
-def _scratch(nbytes, like, stream, workspace):
-    """(tensor or pointer, bytes) of the caller's workspace, or of one made
-    here on the caller's stream (PyTorch's allocator reuses it in order)."""
-    if workspace is not None:
-        if isinstance(workspace, int):
-            raise TypeError("pass a workspace as a tensor")
-        return workspace, _nbytes(workspace)
-    import torch
+_PTRS = [struct.Struct("%dP" % n).pack for n in range(RRA_MAX_RANKS + 1)]
+_SIZES = [struct.Struct("%dN" % n).pack for n in range(RRA_MAX_RANKS + 1)]
+_torch_mod = None
 
-    ws = torch.empty(max(256, nbytes), dtype=torch.uint8, device=like.device)
-    if stream is not None:
-        if isinstance(stream, int):
+
+def _t():
+    global _torch_mod
+    if _torch_mod is None:
+        import torch
+
+        _torch_mod = torch
+    return _torch_mod
+
+
+def _refuse(what, t, dtype, shape, device):
+    if not t.is_contiguous():
+        raise ValueError("tensors passed to rra must be contiguous (%s)" % what)
+    if t.get_device() != device:
+        raise ValueError("tensors of one call must be on one device (%s is on %s)" % (what, t.device))
+    raise ValueError("%s must be %s of %s, got %s of shape %s" % (what, dtype, shape, t.dtype, tuple(t.shape)))
+
+
+def _one(what, t, dtype, shape, device):
+    """Pointer of a tensor of this type, shape and device, contiguous."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+        _refuse(what, t, dtype, shape, device)
+    return t.data_ptr()
+
+
+def _flat(what, t, dtype, numel, device):
+    """The same for a tensor of any shape with this many elements."""
+    if t.dtype is not dtype or t.numel() != numel or t.get_device() != device or not t.is_contiguous():
+        _refuse(what, t, dtype, "%d elements" % numel, device)
+    return t.data_ptr()
+
+
+def _ranks(what, ts, dtype, shape, device):
+    """The pointers of one tensor per rank, as the C array of them."""
+    ps = [t.data_ptr() for t in ts
+          if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous()]
+    if len(ps) != len(ts):
+        for t in ts:
+            _one(what, t, dtype, shape, device)
+    return _PTRS[len(ps)](*ps)
+
+
+def _flat_ranks(what, ts, dtype, numel, device):
+    """The same for tensors of any shape with this many elements."""
+    ps = [t.data_ptr() for t in ts
+          if t.dtype is dtype and t.numel() == numel and t.get_device() == device and t.is_contiguous()]
+    if len(ps) != len(ts):
+        for t in ts:
+            _flat(what, t, dtype, numel, device)
+    return _PTRS[len(ps)](*ps)
+
+
+def _same_count(n, *groups):
+    if not 1 <= n <= RRA_MAX_RANKS:
+        raise RraError(RRA_ERR_INVALID_ARG if n < 1 else RRA_ERR_UNSUPPORTED, "number of ranks")
+    for g in groups:
+        if len(g) != n:
+            raise ValueError("one buffer per rank is needed")
+
+
+def _on(stream, device):
+    """The raw stream of the call (default: PyTorch's current one)."""
+    if stream is None:
+        if device < 0:
+            return 0
+        return _t()._C._cuda_getCurrentRawStream(device)
+    return stream if isinstance(stream, int) else int(stream.cuda_stream)
+
+
+def _scratch(workspace, device, stream, size, *args):
+    """(pointer, bytes, tensor) of the caller's workspace, or of one made here
+    on the caller's stream (PyTorch's allocator reuses it in stream order).
+    The tensor is kept until the call has been issued."""
+    if workspace is None:
+        if isinstance(stream, int) and stream:
             raise ValueError("a raw stream handle needs an explicit workspace")
-        ws.record_stream(stream)
-    return ws, _nbytes(ws)
+        torch = _t()
+        workspace = torch.empty(max(256, size(*args)), dtype=torch.uint8, device="cpu" if device < 0 else device)
+        if stream is not None and stream:
+            workspace.record_stream(stream)
+    elif not workspace.is_contiguous() or workspace.get_device() != device:
+        raise ValueError("the workspace must be contiguous and on the tensors' device")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
-def _expect(what, t, dtype, shape):
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
-        raise ValueError("%s must be %s of shape %s, got %s %s" % (what, dtype, tuple(shape), t.dtype, tuple(t.shape)))
+def _code_type(t):
+    if t.element_size() != 1:
+        raise ValueError("codes must be uint8 or float8_e4m3fn")
+    return t.dtype
 
 
-def _on_one_device(*ts):
-    first = ts[0].device
-    for t in ts:
-        if t is not None and t.device != first:
-            raise ValueError("tensors of one call must be on one device (%s and %s)" % (first, t.device))
-
-
-def _norm_shapes(bufs, outs, gamma, codes, scales, rstd, hidden):
-    import torch
-
-    rows = int(bufs[0].numel()) // hidden
-    nb = -(-hidden // RRA_CKPT_BLOCK)
-    if len(bufs) != len(outs):
-        raise ValueError("as many outputs as inputs are needed")
-    for t in list(bufs) + list(outs):
-        if t.dtype != bufs[0].dtype or t.numel() != rows * hidden:
-            raise ValueError("every rank's buffer must be %s with %d x %d elements" % (bufs[0].dtype, rows, hidden))
-    _expect("gamma", gamma, bufs[0].dtype, (hidden,))
-    if codes.element_size() != 1 or codes.numel() != rows * hidden:
-        raise ValueError("codes must be %d x %d bytes (uint8 or float8_e4m3fn)" % (rows, hidden))
-    _expect("scales", scales, torch.uint8, (rows, nb))
-    _expect("rstd", rstd, torch.float32, (rows,))
-    _on_one_device(*bufs, *outs, gamma, codes, scales, rstd)
-    return rows
+def _norm_dtype(t):
+    torch = _t()
+    if t.dtype is torch.bfloat16:
+        return RRA_BFLOAT16
+    if t.dtype is torch.float32:
+        return RRA_FLOAT32
+    raise TypeError("unsupported dtype %s (float32, bfloat16)" % t.dtype)
 
 
 def rra_allreduce_rmsnorm_save8(bufs, outs, gamma, hidden, codes, scales, rstd, eps=1e-6, stream=None,
@@ -321,28 +383,35 @@ def rra_allreduce_rmsnorm_save8(bufs, outs, gamma, hidden, codes, scales, rstd, 
     """All-reduce + RMSNorm that saves the sum in 8 bits for the backward
     pass: codes [rows, hidden] (float8_e4m3fn or uint8), scales
     [rows, ceil(hidden / 128)] uint8, rstd [rows] float32."""
-    rows = _norm_shapes(bufs, outs, gamma, codes, scales, rstd, hidden)
-    st = load().rra_allreduce_rmsnorm_save8(_ptr_array(bufs), _ptr_array(outs), len(bufs), rows, hidden, _ptr(gamma),
-                                            eps, _ptr(codes), _ptr(scales), _ptr(rstd), _dtype_of(bufs[0]),
-                                            _stream(stream, bufs[0]))
+    n = len(bufs)
+    _same_count(n, outs)
+    torch = _t()
+    x = bufs[0]
+    dev, dt, count = x.get_device(), x.dtype, x.numel()
+    rows = count // hidden
+    if rows * hidden != count:
+        raise ValueError("a rank's buffer must hold whole rows of %d" % hidden)
+    ins = _flat_ranks("a rank's buffer", bufs, dt, count, dev)
+    os_ = _flat_ranks("a rank's output", outs, dt, count, dev)
+    st = load().rra_allreduce_rmsnorm_save8(
+        ins, os_, n, rows, hidden, _one("gamma", gamma, dt, (hidden,), dev), eps,
+        _flat("codes", codes, _code_type(codes), count, dev),
+        _one("scales", scales, torch.uint8, (rows, (hidden + 127) // 128), dev),
+        _one("rstd", rstd, torch.float32, (rows,), dev), _norm_dtype(x), _on(stream, dev))
     return _ret(st, "rra_allreduce_rmsnorm_save8", check)
 
 
 def rra_rmsnorm_restore8(codes, scales, rstd, gamma, out, stream=None, check=True) -> int:
     """out = the checkpoint's values, times rstd and gamma unless None."""
-    import torch
-
-    rows, hidden = codes.shape
-    if codes.element_size() != 1 or tuple(out.shape) != (rows, hidden):
-        raise ValueError("codes must be bytes and out of the same shape")
-    _expect("scales", scales, torch.uint8, (rows, -(-hidden // RRA_CKPT_BLOCK)))
-    if rstd is not None:
-        _expect("rstd", rstd, torch.float32, (rows,))
-    if gamma is not None:
-        _expect("gamma", gamma, out.dtype, (hidden,))
-    _on_one_device(out, codes, scales, rstd, gamma)
-    st = load().rra_rmsnorm_restore8(_ptr(codes), _ptr(scales), _ptr(rstd), _ptr(gamma), _ptr(out), rows, hidden,
-                                     _dtype_of(out), _stream(stream, out))
+    torch = _t()
+    rows, hidden = out.shape
+    dev = out.get_device()
+    st = load().rra_rmsnorm_restore8(
+        _flat("codes", codes, _code_type(codes), rows * hidden, dev),
+        _one("scales", scales, torch.uint8, (rows, (hidden + 127) // 128), dev),
+        None if rstd is None else _one("rstd", rstd, torch.float32, (rows,), dev),
+        None if gamma is None else _one("gamma", gamma, out.dtype, (hidden,), dev),
+        _one("out", out, out.dtype, (rows, hidden), dev), rows, hidden, _norm_dtype(out), _on(stream, dev))
     return _ret(st, "rra_rmsnorm_restore8", check)
 
 
@@ -353,16 +422,22 @@ def rra_allreduce_rmsnorm_backward8_workspace_bytes(rows: int, hidden: int) -> i
 def rra_allreduce_rmsnorm_backward8(grads, dxs, codes, scales, rstd, gamma, dgamma, workspace=None, stream=None,
                                     check=True) -> int:
     """Sum of the ranks' gradients through the norm, from the checkpoint."""
-    import torch
-
-    hidden = int(gamma.numel())
-    rows = _norm_shapes(grads, dxs, gamma, codes, scales, rstd, hidden)
-    _expect("dgamma", dgamma, torch.float32, (hidden,))
-    _on_one_device(gamma, dgamma)
-    ws, nb = _scratch(rra_allreduce_rmsnorm_backward8_workspace_bytes(rows, hidden), gamma, stream, workspace)
-    st = load().rra_allreduce_rmsnorm_backward8(_ptr_array(grads), _ptr_array(dxs), len(grads), rows, hidden,
-                                                _ptr(codes), _ptr(scales), _ptr(rstd), _ptr(gamma), _ptr(dgamma),
-                                                _ptr(ws), nb, _dtype_of(grads[0]), _stream(stream, gamma))
+    n = len(grads)
+    _same_count(n, dxs)
+    torch = _t()
+    x = grads[0]
+    dev, dt, count, hidden = x.get_device(), x.dtype, x.numel(), gamma.numel()
+    rows = count // hidden if hidden else 0
+    if rows * hidden != count:
+        raise ValueError("a rank's gradient must hold whole rows of %d" % hidden)
+    gs = _flat_ranks("a rank's gradient", grads, dt, count, dev)
+    ds = _flat_ranks("a rank's output", dxs, dt, count, dev)
+    ws, nb, _keep = _scratch(workspace, dev, stream, rra_allreduce_rmsnorm_backward8_workspace_bytes, rows, hidden)
+    st = load().rra_allreduce_rmsnorm_backward8(
+        gs, ds, n, rows, hidden, _flat("codes", codes, _code_type(codes), count, dev),
+        _one("scales", scales, torch.uint8, (rows, (hidden + 127) // 128), dev),
+        _one("rstd", rstd, torch.float32, (rows,), dev), _one("gamma", gamma, dt, (hidden,), dev),
+        _one("dgamma", dgamma, torch.float32, (hidden,), dev), ws, nb, _norm_dtype(x), _on(stream, dev))
     return _ret(st, "rra_allreduce_rmsnorm_backward8", check)
 
 
@@ -370,97 +445,84 @@ def rra_gated_ffn_workspace_bytes(nranks: int, tokens: int, hidden: int, width: 
     return int(load().rra_gated_ffn_workspace_bytes(nranks, tokens, hidden, width, int(backward)))
 
 
-def _ffn_shapes(x, gates, ups, *per_token):
-    tokens, hidden = x.shape
-    width = int(gates[0].shape[0])
-    for w in list(gates) + list(ups):
-        _expect("a gate or up shard", w, x.dtype, (width, hidden))
-    for group in per_token:
-        for a in group:
-            _expect("a rank's activations", a, x.dtype, (tokens, width))
-        if len(group) != len(gates):
-            raise ValueError("one buffer per rank is needed")
-    if len(gates) != len(ups):
-        raise ValueError("as many up shards as gate shards are needed")
-    _on_one_device(x, *gates, *ups, *[a for group in per_token for a in group])
-    return tokens, hidden, width
-
-
 def rra_gated_ffn(x, gates, ups, acts, act=RRA_ACT_SILU, workspace=None, stream=None, check=True) -> int:
     """acts[r] = act(x gates[r]^T) * (x ups[r]^T)."""
-    T, D, F = _ffn_shapes(x, gates, ups, acts)
     n = len(gates)
-    ws, nb = _scratch(rra_gated_ffn_workspace_bytes(n, T, D, F, 0), x, stream, workspace)
-    st = load().rra_gated_ffn(_ptr(x), _ptr_array(gates), _ptr_array(ups), _ptr_array(acts), n, T, D, F, act,
-                              _dtype_of(x), _ptr(ws), nb, _stream(stream, x))
+    _same_count(n, ups, acts)
+    T, D = x.shape
+    F, dev, dt = gates[0].shape[0], x.get_device(), x.dtype
+    gs = _ranks("a gate or up shard", gates, dt, (F, D), dev)
+    us = _ranks("a gate or up shard", ups, dt, (F, D), dev)
+    os_ = _ranks("a rank's activations", acts, dt, (T, F), dev)
+    ws, nb, _keep = _scratch(workspace, dev, stream, rra_gated_ffn_workspace_bytes, n, T, D, F, 0)
+    st = load().rra_gated_ffn(_one("x", x, dt, (T, D), dev), gs, us, os_, n, T, D, F, act, _dtype_of(x), ws, nb,
+                              _on(stream, dev))
     return _ret(st, "rra_gated_ffn", check)
 
 
 def rra_gated_ffn_backward(x, gates, ups, dacts, dx, dgates, dups, act=RRA_ACT_SILU, workspace=None, stream=None,
                            check=True) -> int:
     """Gradients of rra_gated_ffn: dx summed over the ranks, dgates, dups."""
-    T, D, F = _ffn_shapes(x, gates, ups, dacts)
     n = len(gates)
-    _expect("dx", dx, x.dtype, (T, D))
-    if len(dgates) != n or len(dups) != n:
-        raise ValueError("one gradient per shard is needed")
-    for g in list(dgates) + list(dups):
-        _expect("a shard's gradient", g, x.dtype, (F, D))
-    _on_one_device(x, dx, *dgates, *dups)
-    ws, nb = _scratch(rra_gated_ffn_workspace_bytes(n, T, D, F, 1), x, stream, workspace)
-    st = load().rra_gated_ffn_backward(_ptr(x), _ptr_array(gates), _ptr_array(ups), _ptr_array(dacts), _ptr(dx),
-                                       _ptr_array(dgates), _ptr_array(dups), n, T, D, F, act, _dtype_of(x), _ptr(ws),
-                                       nb, _stream(stream, x))
+    _same_count(n, ups, dacts, dgates, dups)
+    T, D = x.shape
+    F, dev, dt = gates[0].shape[0], x.get_device(), x.dtype
+    gs = _ranks("a gate or up shard", gates, dt, (F, D), dev)
+    us = _ranks("a gate or up shard", ups, dt, (F, D), dev)
+    das = _ranks("a rank's activations", dacts, dt, (T, F), dev)
+    dgs = _ranks("a shard's gradient", dgates, dt, (F, D), dev)
+    dus = _ranks("a shard's gradient", dups, dt, (F, D), dev)
+    ws, nb, _keep = _scratch(workspace, dev, stream, rra_gated_ffn_workspace_bytes, n, T, D, F, 1)
+    st = load().rra_gated_ffn_backward(_one("x", x, dt, (T, D), dev), gs, us, das, _one("dx", dx, dt, (T, D), dev),
+                                       dgs, dus, n, T, D, F, act, _dtype_of(x), ws, nb, _on(stream, dev))
     return _ret(st, "rra_gated_ffn_backward", check)
 
 
 def _sizes(xs):
-    return (ctypes.c_size_t * len(xs))(*[int(v) for v in xs])
+    return _SIZES[len(xs)](*xs)
 
 
 def rra_vocab_loss_workspace_bytes(tokens: int, hidden: int, vocab, backward) -> int:
     """vocab: the ranks' shard heights; backward 2: the least bytes the
     backward pass runs with."""
+    _same_count(len(vocab))
     return int(load().rra_vocab_loss_workspace_bytes(len(vocab), tokens, hidden, _sizes(vocab), int(backward)))
-
-
-def _loss_shapes(x, weights, targets, *rows):
-    import torch
-
-    T, D = x.shape
-    for w in weights:
-        _expect("a vocabulary shard", w, x.dtype, (w.shape[0], D))
-    _expect("targets", targets, torch.int64, (T,))
-    for r in rows:
-        _expect("a per-token buffer", r, torch.float32, (T,))
-    _on_one_device(x, *weights, targets, *rows)
-    return T, D, [int(w.shape[0]) for w in weights]
 
 
 def rra_vocab_loss(x, weights, targets, loss, lse, ignore_index=-100, workspace=None, stream=None, check=True) -> int:
     """loss[t] = lse[t] - logit of targets[t], logits x W^T never kept; the
     vocabulary is the ranks' weight shards, one after another."""
-    T, D, vocab = _loss_shapes(x, weights, targets, loss, lse)
-    ws, nb = _scratch(rra_vocab_loss_workspace_bytes(T, D, vocab, 0), x, stream, workspace)
-    st = load().rra_vocab_loss(_ptr(x), _ptr_array(weights), _sizes(vocab), _ptr(targets), len(weights), T, D,
-                               ignore_index, _ptr(loss), _ptr(lse), _dtype_of(x), _ptr(ws), nb, _stream(stream, x))
+    n = len(weights)
+    _same_count(n)
+    torch = _t()
+    T, D = x.shape
+    dev, dt = x.get_device(), x.dtype
+    vocab = [w.shape[0] for w in weights]
+    wp = _PTRS[n](*[_one("a vocabulary shard", w, dt, (v, D), dev) for w, v in zip(weights, vocab)])
+    ws, nb, _keep = _scratch(workspace, dev, stream, rra_vocab_loss_workspace_bytes, T, D, vocab, 0)
+    st = load().rra_vocab_loss(_one("x", x, dt, (T, D), dev), wp, _sizes(vocab),
+                               _one("targets", targets, torch.int64, (T,), dev), n, T, D, ignore_index,
+                               _one("loss", loss, torch.float32, (T,), dev), _one("lse", lse, torch.float32, (T,), dev),
+                               _dtype_of(x), ws, nb, _on(stream, dev))
     return _ret(st, "rra_vocab_loss", check)
 
 
 def rra_vocab_loss_backward(x, weights, targets, lse, grad_loss, dx, dweights, ignore_index=-100, workspace=None,
                             stream=None, check=True) -> int:
     """Gradients of rra_vocab_loss with respect to x and every shard."""
-    T, D, vocab = _loss_shapes(x, weights, targets, lse, grad_loss)
-    _expect("dx", dx, x.dtype, (T, D))
-    if len(dweights) != len(weights):
-        raise ValueError("one gradient per shard is needed")
-    for w, g in zip(weights, dweights):
-        _expect("a shard's gradient", g, x.dtype, w.shape)
-    _on_one_device(x, dx, *dweights)
-    ws, nb = _scratch(rra_vocab_loss_workspace_bytes(T, D, vocab, 1), x, stream, workspace)
-    st = load().rra_vocab_loss_backward(_ptr(x), _ptr_array(weights), _sizes(vocab), _ptr(targets), _ptr(lse),
-                                        _ptr(grad_loss), _ptr(dx), _ptr_array(dweights), len(weights), T, D,
-                                        ignore_index, _dtype_of(x), _ptr(ws), nb, _stream(stream, x))
+    n = len(weights)
+    _same_count(n, dweights)
+    torch = _t()
+    T, D = x.shape
+    dev, dt = x.get_device(), x.dtype
+    vocab = [w.shape[0] for w in weights]
+    wp = _PTRS[n](*[_one("a vocabulary shard", w, dt, (v, D), dev) for w, v in zip(weights, vocab)])
+    dp = _PTRS[n](*[_one("a shard's gradient", g, dt, (v, D), dev) for g, v in zip(dweights, vocab)])
+    ws, nb, _keep = _scratch(workspace, dev, stream, rra_vocab_loss_workspace_bytes, T, D, vocab, 1)
+    st = load().rra_vocab_loss_backward(
+        _one("x", x, dt, (T, D), dev), wp, _sizes(vocab), _one("targets", targets, torch.int64, (T,), dev),
+        _one("lse", lse, torch.float32, (T,), dev), _one("grad_loss", grad_loss, torch.float32, (T,), dev),
+        _one("dx", dx, dt, (T, D), dev), dp, n, T, D, ignore_index, _dtype_of(x), ws, nb, _on(stream, dev))
     return _ret(st, "rra_vocab_loss_backward", check)
 
 

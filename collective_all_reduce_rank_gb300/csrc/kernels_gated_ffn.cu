@@ -34,35 +34,38 @@ __device__ __forceinline__ float gate_sigma(float g, float* slope) {
 
 template <int ACT>
 struct EpiGate {
-  static __device__ __forceinline__ void run(const TcArgs& p, const TcTile& x, int row, int half, uint32_t addr) {
+  static __device__ __forceinline__ void run(const TcArgs& p, const TcTile& x, int row0, int half, uint32_t addr,
+                                             uint8_t* buf) {
     const TcGroup& g = p.group[x.group];
     const int c0 = x.n * 128 + half * 64;
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(g.out) + (long long)row * g.ld + c0;
+    const int valid = g.N - c0;
+    if (valid <= 0) return;
 #pragma unroll 1
     for (int c = 0; c < 64; c += 32) {
-      const int valid = g.N - c0 - c;
-      if (valid <= 0) break;
       float a[32], b[32];
       tc_ld32(addr + half * 64 + c, a);
       tc_ld32(addr + 128 + half * 64 + c, b);
       tc_ld_wait();
-      if (row >= g.M) continue;
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
         float unused;
         a[j] = a[j] * gate_sigma<ACT>(a[j], &unused) * b[j];
       }
-      tc_store_bf16(out + c, a, valid, g.vec, false);
+      tc_stage_bf16(buf, a, c / 8);
     }
+    tc_flush_bf16(buf, static_cast<__nv_bfloat16*>(g.out) + (long long)row0 * g.ld + c0, g.ld, g.M - row0, valid,
+                  g.vec, false);
   }
 };
 
 template <int ACT>
 struct EpiGateBack {
-  static __device__ __forceinline__ void run(const TcArgs& p, const TcTile& x, int row, int half, uint32_t addr) {
+  static __device__ __forceinline__ void run(const TcArgs& p, const TcTile& x, int row0, int half, uint32_t addr,
+                                             uint8_t* buf) {
     const TcGroup& g = p.group[x.group];
     const int c0 = x.n * 128 + half * 64;
-    const long long off = (long long)row * g.ld + c0;
+    const int row = row0 + (threadIdx.x & 31), rows = g.M - row0;
+    const long long off = (long long)row0 * g.ld + c0;
     const __nv_bfloat16* in = static_cast<const __nv_bfloat16*>(g.in) + (long long)row * g.ld_in + c0;
 #pragma unroll 1
     for (int c = 0; c < 64; c += 32) {
@@ -71,9 +74,8 @@ struct EpiGateBack {
       float a[32], b[32], d[32];
       tc_ld32(addr + half * 64 + c, a);
       tc_ld32(addr + 128 + half * 64 + c, b);
+      tc_load_bf16(in + c, d, row < g.M ? valid : 0, g.vec);
       tc_ld_wait();
-      if (row >= g.M) continue;
-      tc_load_bf16(in + c, d, valid, g.vec);
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
         float k;
@@ -83,8 +85,11 @@ struct EpiGateBack {
         a[j] = d[j] * b[j] * slope;
         b[j] = d[j] * h;
       }
-      tc_store_bf16(static_cast<__nv_bfloat16*>(g.out) + off + c, a, valid, true, true);
-      tc_store_bf16(static_cast<__nv_bfloat16*>(g.out2) + off + c, b, valid, true, true);
+      // 32 columns of dg in the first half of the staged rows, of du in the second
+      tc_stage_bf16(buf, a, 0);
+      tc_stage_bf16(buf, b, 4);
+      tc_flush_pair(buf, static_cast<__nv_bfloat16*>(g.out) + off + c, static_cast<__nv_bfloat16*>(g.out2) + off + c,
+                    g.ld, rows, valid);
     }
   }
 };

@@ -11,37 +11,30 @@ namespace rra {
 
 template <bool F32>
 struct EpiStore {
-  static __device__ __forceinline__ void run(const TcArgs& p, const TcTile& x, int row, int half, uint32_t addr) {
+  static __device__ __forceinline__ void run(const TcArgs& p, const TcTile& x, int row0, int half, uint32_t addr,
+                                             uint8_t* buf) {
     const TcGroup& g = p.group[x.group];
     const int c0 = x.n * 256 + half * 128;
-    const long long off = (long long)row * g.ld + c0;
+    const int rows = g.M - row0;
+    const long long off = (long long)row0 * g.ld + c0;
+    constexpr int STEP = F32 ? 32 : 64;
 #pragma unroll 1
-    for (int c = 0; c < 128; c += 32) {
+    for (int c = 0; c < 128; c += STEP) {
       const int valid = g.N - c0 - c;
       if (valid <= 0) break;
       float v[32];
       tc_ld32(addr + half * 128 + c, v);
-      tc_ld_wait();
-      if (row >= g.M) continue;
       if constexpr (F32) {
+        tc_ld_wait();
         float* o = static_cast<float*>(g.out) + x.split * p.split_stride + off + c;
-        if (g.vec && valid >= 32) {
-#pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            float4 w = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-            if (p.accumulate) {
-              const float4 q = *reinterpret_cast<const float4*>(o + j);
-              w = make_float4(q.x + w.x, q.y + w.y, q.z + w.z, q.w + w.w);
-            }
-            *reinterpret_cast<float4*>(o + j) = w;
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (j < valid) o[j] = p.accumulate ? o[j] + v[j] : v[j];
-        }
+        tc_store_f32(buf, v, o, g.ld, rows, valid, g.vec, p.accumulate);
       } else {
-        tc_store_bf16(static_cast<__nv_bfloat16*>(g.out) + off + c, v, valid, g.vec, false);
+        float w[32];
+        tc_ld32(addr + half * 128 + c + 32, w);
+        tc_ld_wait();
+        tc_stage_bf16(buf, v, 0);
+        tc_stage_bf16(buf, w, 4);
+        tc_flush_bf16(buf, static_cast<__nv_bfloat16*>(g.out) + off + c, g.ld, rows, valid, g.vec, false);
       }
     }
   }
@@ -78,17 +71,33 @@ cudaError_t launch_join_slots(const float* slots, int n, long long stride, void*
   return cudaGetLastError();
 }
 
-__global__ void __launch_bounds__(kRowThreads) pad_rows_kernel(const uint16_t* src, uint16_t* dst, long long rows,
-                                                               long long cols, long long ld) {
-  for (long long r = blockIdx.x; r < rows; r += gridDim.x)
-    for (long long c = threadIdx.x; c < cols; c += kRowThreads) dst[r * ld + c] = __ldg(src + r * cols + c);
+// Rows of up to 17 matrices to padded rows (16-byte units), one launch: a
+// thread writes one unit of a destination row.
+__global__ void __launch_bounds__(kRowThreads) pad_rows_kernel(const __grid_constant__ PadArgs a) {
+  const long long step = (long long)gridDim.x * kRowThreads;
+  int m = 0;
+  for (long long i = (long long)blockIdx.x * kRowThreads + threadIdx.x; i < a.first[a.n]; i += step) {
+    while (i >= a.first[m + 1]) ++m;
+    const long long u = i - a.first[m];
+    const long long row = u < 0xFFFFFFFFll ? (long long)((uint32_t)u / (uint32_t)a.units) : u / a.units;
+    const int c = (int)(u - row * a.units) * 8;
+    const uint16_t* src = static_cast<const uint16_t*>(a.src[m]) + row * a.cols + c;
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t lo = c + 2 * j < a.cols ? __ldg(src + 2 * j) : 0u;
+      const uint32_t hi = c + 2 * j + 1 < a.cols ? __ldg(src + 2 * j + 1) : 0u;
+      w[j] = lo | (hi << 16);
+    }
+    reinterpret_cast<uint4*>(a.dst[m])[u] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
 }
 
-cudaError_t launch_pad_rows(const void* src, void* dst, long long rows, long long cols, long long ld,
-                            cudaStream_t s) {
-  const int cap = max_ctas_cap() > 0 ? max_ctas_cap() : device_sms() * 8;
-  pad_rows_kernel<<<(int)(rows < cap ? rows : cap), kRowThreads, 0, s>>>(
-      static_cast<const uint16_t*>(src), static_cast<uint16_t*>(dst), rows, cols, ld);
+cudaError_t launch_pad_rows(const PadArgs& a, cudaStream_t s) {
+  const long long want = (a.first[a.n] + kRowThreads - 1) / kRowThreads;
+  if (want == 0) return cudaSuccess;
+  const long long cap = max_ctas_cap() > 0 ? max_ctas_cap() : device_sms() * 8;
+  pad_rows_kernel<<<(int)(want < cap ? want : cap), kRowThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 

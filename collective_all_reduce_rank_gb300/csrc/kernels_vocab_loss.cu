@@ -18,8 +18,10 @@ namespace rra {
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct EpiLse {
-  static __device__ __forceinline__ void run(const TcArgs& p, const TcTile& x, int row, int half, uint32_t addr) {
+  static __device__ __forceinline__ void run(const TcArgs& p, const TcTile& x, int row0, int half, uint32_t addr,
+                                             uint8_t*) {
     const TcGroup& g = p.group[x.group];
+    const int row = row0 + (threadIdx.x & 31);
     const int c0 = x.n * 256 + half * 128;
     float m = -INFINITY, s = 0.f;
     long long t = -1;
@@ -41,11 +43,10 @@ struct EpiLse {
       }
       const long long d = t - c;
       if (d >= 0 && d < 32 && d < valid) {
-        float h = v[0];
+        uint32_t h = 0;  // as bits: a select per column, no indexed registers
 #pragma unroll
-        for (int j = 1; j < 32; ++j)
-          if (j == (int)d) h = v[j];
-        p.hit[row] = h;
+        for (int j = 0; j < 32; ++j) h |= j == (int)d ? __float_as_uint(v[j]) : 0u;
+        p.hit[row] = __uint_as_float(h);
       }
       float q = v[0];
 #pragma unroll
@@ -72,8 +73,10 @@ struct EpiLse {
 };
 
 struct EpiDlogits {
-  static __device__ __forceinline__ void run(const TcArgs& p, const TcTile& x, int row, int half, uint32_t addr) {
+  static __device__ __forceinline__ void run(const TcArgs& p, const TcTile& x, int row0, int half, uint32_t addr,
+                                             uint8_t* buf) {
     const TcGroup& g = p.group[x.group];
+    const int row = row0 + (threadIdx.x & 31);
     const int c0 = x.n * 256 + half * 128;
     long long t = -1;
     float base = 0.f, w = 0.f;
@@ -86,22 +89,26 @@ struct EpiDlogits {
       base = p.lse[row] * kLog2e;
       w = p.grad[row];
     }
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(g.out) + (long long)row * g.ld + c0;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(g.out) + (long long)row0 * g.ld + c0;
 #pragma unroll 1
-    for (int c = 0; c < 128; c += 32) {
+    for (int c = 0; c < 128; c += 64) {
       const int valid = g.N - c0 - c;
       if (valid <= 0) break;
-      float v[32];
-      tc_ld32(addr + half * 128 + c, v);
-      tc_ld_wait();
-      if (row >= g.M) continue;
-      const int d = t - c >= 0 && t - c < 32 ? (int)(t - c) : -1;
+#pragma unroll 1
+      for (int k = 0; k < 64; k += 32) {
+        float v[32];
+        tc_ld32(addr + half * 128 + c + k, v);
+        tc_ld_wait();
+        const long long q = t - c - k;
+        const int d = q >= 0 && q < 32 ? (int)q : -1;
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        const float e = exp2f(fmaf(v[j], kLog2e, -base)) - (j == d ? 1.f : 0.f);
-        v[j] = live ? e * w : 0.f;
+        for (int j = 0; j < 32; ++j) {
+          const float e = exp2f(fmaf(v[j], kLog2e, -base)) - (j == d ? 1.f : 0.f);
+          v[j] = live ? e * w : 0.f;
+        }
+        tc_stage_bf16(buf, v, k / 8);
       }
-      tc_store_bf16(out + c, v, valid, true, true);
+      tc_flush_bf16(buf, out + c, g.ld, g.M - row0, valid, true, true);
     }
   }
 };
@@ -114,52 +121,158 @@ cudaError_t launch_tc_dlogits(const TcArgs& p, cudaStream_t s, int* grid) {
   return tc_launch<false, false, EpiDlogits>(p, s, grid);
 }
 
-// Join the column parts of 32 rows per CTA: 8 threads a row, each over every
-// 8th part, then across the 8 through shared memory, in a fixed order.
-__global__ void __launch_bounds__(256)
-    loss_join_kernel(const float2* part, long long part_ld, int parts, const float* hit, const long long* targets,
-                     long long ignore_index, long long vocab, int rows, float* loss, float* lse) {
-  __shared__ float2 red[8][32];
-  const int lane = threadIdx.x & 31, k = threadIdx.x >> 5;
-  const int row = blockIdx.x * 32 + lane;
-  float m = -INFINITY, s = 0.f;
-  if (row < rows) {
-    for (int i = k; i < parts; i += 8) {
-      const float2 q = __ldg(part + (long long)i * part_ld + row);
-      const float nm = fmaxf(m, q.x);
-      if (nm == -INFINITY) {
-        s += q.y;  // 0, or NaN
-      } else {
-        s = s * expf(m - nm) + q.y * expf(q.x - nm);
-        m = nm;
-      }
-    }
-  }
-  red[k][lane] = make_float2(m, s);
-  __syncthreads();
-  if (k == 0 && row < rows) {
-    for (int i = 1; i < 8; ++i) {
-      const float2 q = red[i][lane];
-      const float nm = fmaxf(m, q.x);
-      if (nm == -INFINITY) {
-        s += q.y;
-      } else {
-        s = s * expf(m - nm) + q.y * expf(q.x - nm);
-        m = nm;
-      }
-    }
-    const float l = s != s ? s : m + logf(s);
-    lse[row] = l;
-    const long long t = targets[row];
-    if (loss) loss[row] = t == ignore_index ? 0.f : (t < 0 || t >= vocab ? NAN : l - hit[row]);
+// Join the column parts of each row, R rows per CTA (256 threads: 256 / R
+// threads a row, lanes of neighbouring rows side by side so that loads of
+// the [part][row] array stay whole sectors), and refine the target's logit.
+//
+// The tensor cores truncate each partial sum of a product: 320 of them at
+// hidden 5120 leave a logit about 2e-6 low relative to its terms, and the
+// loss carries that of the target's logit in full.  So the target's logit l
+// is computed once more as a plain float32 sum, and takes the place of the
+// product's value l' both in the loss and inside lse:
+//   d = l - l',  c = log(1 + exp(l' - lse')(exp(d) - 1))
+//   lse = lse' + c,  loss = (lse' - l') - d + c
+// which stays accurate when the target carries nearly all of the mass, where
+// lse' - l alone would lose d.
+struct JoinArgs {
+  const float2* part;
+  long long part_ld;
+  int parts, rows, nranks;
+  const float* hit;
+  const long long* targets;
+  long long ignore_index;
+  const __nv_bfloat16* x;
+  const __nv_bfloat16* w[kMaxRanks];
+  long long first[kMaxRanks + 1];  // the shards' first columns
+  long long hidden;
+  int vec;  // rows of x and w start on 16 bytes
+  float* loss;
+  float* lse;
+};
+
+__device__ __forceinline__ void join_one(float& m, float& s, float2 q) {
+  const float nm = fmaxf(m, q.x);
+  if (nm == -INFINITY) {
+    s += q.y;  // 0, or NaN
+  } else {
+    s = s * expf(m - nm) + q.y * expf(q.x - nm);
+    m = nm;
   }
 }
 
-cudaError_t launch_loss_join(const float2* part, long long part_ld, int parts, const float* hit,
-                             const long long* targets, long long ignore_index, long long vocab, int rows,
-                             float* loss, float* lse, cudaStream_t s) {
-  loss_join_kernel<<<(rows + 31) / 32, 256, 0, s>>>(part, part_ld, parts, hit, targets, ignore_index, vocab, rows,
-                                                    loss, lse);
+template <int R>
+__global__ void __launch_bounds__(256) loss_join_kernel(const __grid_constant__ JoinArgs a) {
+  constexpr int PER = 256 / R;  // threads a row
+  __shared__ float2 red[256];
+  __shared__ float dots[8];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int r = tid % R, k = tid / R;
+  const int row0 = blockIdx.x * R;
+  const int row = row0 + r;
+  float m = -INFINITY, s = 0.f;
+  if (row < a.rows) {
+    const float2* p = a.part + row;
+    int i = k;
+    for (; i + 3 * PER < a.parts; i += 4 * PER) {
+      float2 q[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) q[j] = __ldg(p + (long long)(i + j * PER) * a.part_ld);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) join_one(m, s, q[j]);
+    }
+    for (; i < a.parts; i += PER) join_one(m, s, __ldg(p + (long long)i * a.part_ld));
+  }
+  red[tid] = make_float2(m, s);
+
+  // the target's logit in float32: a warp per row (R = 8), or all for the one
+  const int drow = R == 1 ? row0 : row0 + warp;
+  const int dt = R == 1 ? tid : lane, dn = R == 1 ? 256 : 32;
+  float dot = 0.f;
+  bool inside = false;
+  if (drow < a.rows) {
+    const long long t = a.targets[drow];
+    inside = t != a.ignore_index && t >= 0 && t < a.first[a.nranks];
+    if (inside) {
+      int g = 0;
+      while (t >= a.first[g + 1]) ++g;
+      const __nv_bfloat16* w = a.w[g] + (t - a.first[g]) * a.hidden;
+      const __nv_bfloat16* x = a.x + (long long)drow * a.hidden;
+      if (a.vec) {
+        for (long long c = dt * 8; c < a.hidden; c += dn * 8) {
+          const uint4 u = __ldg(reinterpret_cast<const uint4*>(x + c)), v = __ldg(reinterpret_cast<const uint4*>(w + c));
+          const uint32_t p[4] = {u.x, u.y, u.z, u.w}, q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            dot = fmaf(__uint_as_float(p[j] << 16), __uint_as_float(q[j] << 16), dot);
+            dot = fmaf(__uint_as_float(p[j] & 0xFFFF0000u), __uint_as_float(q[j] & 0xFFFF0000u), dot);
+          }
+        }
+      } else {
+        for (long long c = dt; c < a.hidden; c += dn) dot = fmaf(__bfloat162float(x[c]), __bfloat162float(w[c]), dot);
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+  if (lane == 0) dots[warp] = dot;
+#pragma unroll
+  for (int half = PER / 2; half > 0; half >>= 1) {
+    __syncthreads();
+    if (k < half) {
+      join_one(m, s, red[tid + half * R]);
+      red[tid] = make_float2(m, s);
+    }
+  }
+  __syncthreads();
+  if (k == 0 && row < a.rows) {
+    float l = s != s ? s : m + logf(s);
+    const long long t = a.targets[row];
+    float out = 0.f;
+    if (t != a.ignore_index) {
+      if (t < 0 || t >= a.first[a.nranks]) {
+        out = NAN;
+      } else {
+        float fine = dots[R == 1 ? 0 : r];
+        if (R == 1)
+          for (int i = 1; i < 8; ++i) fine += dots[i];
+        const float rough = a.hit[row];
+        const float d = fabsf(fine) < INFINITY && fabsf(rough) < INFINITY ? fine - rough : 0.f;
+        const float c = d != 0.f ? log1pf(expf(rough - l) * expm1f(d)) : 0.f;
+        out = (l - rough) - d + c;
+        l += c;
+      }
+    }
+    a.lse[row] = l;
+    a.loss[row] = out;
+  }
+}
+
+cudaError_t launch_loss_join(const float2* part, int parts, const float* hit, const long long* targets,
+                             long long ignore_index, const void* x, const void* const* w, const size_t* vocab, int n,
+                             size_t hidden, int rows, float* loss, float* lse, cudaStream_t s) {
+  JoinArgs a{};
+  a.part = part;
+  a.part_ld = rows;
+  a.parts = parts;
+  a.rows = rows;
+  a.nranks = n;
+  a.hit = hit;
+  a.targets = targets;
+  a.ignore_index = ignore_index;
+  a.x = static_cast<const __nv_bfloat16*>(x);
+  a.hidden = (long long)hidden;
+  a.vec = hidden % 8 == 0;  // the matrices themselves are 16-byte aligned
+  for (int r = 0; r < n; ++r) {
+    a.w[r] = static_cast<const __nv_bfloat16*>(w[r]);
+    a.first[r + 1] = a.first[r] + (long long)vocab[r];
+  }
+  a.loss = loss;
+  a.lse = lse;
+  // one row per CTA while that leaves SMs idle, else 8 (whole sectors of parts)
+  if (rows < 8 * device_sms())
+    loss_join_kernel<1><<<rows, 256, 0, s>>>(a);
+  else
+    loss_join_kernel<8><<<(rows + 7) / 8, 256, 0, s>>>(a);
   return cudaGetLastError();
 }
 

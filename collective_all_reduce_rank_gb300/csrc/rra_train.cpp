@@ -71,15 +71,28 @@ struct Bump {
 bool padded(size_t hidden) { return hidden % 8 != 0; }
 size_t pad_ld(size_t hidden) { return up(hidden, 8); }
 
-// The rows a product reads of `p`: copied to padded rows when needed.
-cudaError_t place(Mat* m, const void* p, size_t rows, size_t cols, Bump& ws, cudaStream_t s) {
-  *m = Mat{p, rows, cols, cols};
-  if (!padded(cols) || rows == 0) return cudaSuccess;
-  m->ld = pad_ld(cols);
-  void* q = ws.take(rows * m->ld * 2);
-  m->p = q;
-  return launch_pad_rows(p, q, (long long)rows, (long long)cols, (long long)m->ld, s);
-}
+// The rows products read of the caller's matrices: copied to padded rows
+// when needed, all of them in one launch.
+struct Placer {
+  Bump& ws;
+  PadArgs a{};
+  explicit Placer(Bump& w) : ws(w) {}
+  Mat operator()(const void* p, size_t rows, size_t cols) {
+    Mat m{p, rows, cols, cols};
+    if (!padded(cols)) return m;
+    m.ld = pad_ld(cols);
+    m.p = ws.take(rows * m.ld * 2);
+    if (rows == 0) return m;
+    a.src[a.n] = p;
+    a.dst[a.n] = const_cast<void*>(m.p);
+    a.cols = (long long)cols;
+    a.units = (int)(m.ld / 8);
+    a.first[a.n + 1] = a.first[a.n] + (long long)rows * a.units;
+    ++a.n;
+    return m;
+  }
+  bool launch(cudaStream_t s) { return a.n == 0 || launch_pad_rows(a, s) == cudaSuccess; }
+};
 
 bool map_k(CUtensorMap* m, const Mat& x) { return tc_map(m, x.p, x.cols, x.rows, x.ld, false); }
 bool map_mn(CUtensorMap* m, const Mat& x) { return tc_map(m, x.p, x.cols, x.rows, x.ld, true); }
@@ -365,13 +378,12 @@ rra_status_t rra_gated_ffn(const void* x, const void* const* gates, const void* 
   Bump ws{static_cast<char*>(workspace)};
   auto p = std::make_unique<TcArgs>();
   std::memset(p.get(), 0, sizeof(TcArgs));
-  Mat X;
-  cudaError_t e = place(&X, x, T, D, ws, s);
-  bool ok = e == cudaSuccess && map_k(&p->a[0], X);
+  Placer place(ws);
+  const Mat X = place(x, T, D);
+  bool ok = map_k(&p->a[0], X);
   for (int r = 0; r < nranks && ok; ++r) {
-    Mat G, U;
-    ok = place(&G, gates[r], F, D, ws, s) == cudaSuccess && place(&U, ups[r], F, D, ws, s) == cudaSuccess &&
-         map_k(&p->b[2 * r], G) && map_k(&p->b[2 * r + 1], U);
+    const Mat G = place(gates[r], F, D), U = place(ups[r], F, D);
+    ok = map_k(&p->b[2 * r], G) && map_k(&p->b[2 * r + 1], U);
     TcGroup g{};
     g.a = 0;
     g.b = 2 * r;
@@ -382,13 +394,13 @@ rra_status_t rra_gated_ffn(const void* x, const void* const* gates, const void* 
     g.vec = aligned(acts[r], 16) && F % 8 == 0;
     ok = ok && add_group(p.get(), g, true);
   }
-  if (!ok) return done(call, nranks, count, dtype, 0, RRA_ERR_CUDA);
+  if (!ok || !place.launch(s)) return done(call, nranks, count, dtype, 0, RRA_ERR_CUDA);
   one_k_axis(p.get(), D);
   p->pair_b = 1;
   p->act = act;
   p->status = device_status();
   int grid = 0;
-  e = launch_tc_gate(*p, s, &grid);
+  const cudaError_t e = launch_tc_gate(*p, s, &grid);
   return done(call, nranks, count, dtype, grid, cuda_st(e));
 }
 
@@ -425,21 +437,21 @@ rra_status_t rra_gated_ffn_backward(const void* x, const void* const* gates, con
   }
   if (!device_status()) return done(call, nranks, count, dtype, 0, RRA_ERR_NOT_INITIALIZED);
   Bump ws{static_cast<char*>(workspace)};
-  Mat X, W[2 * kMaxRanks], dW[2 * kMaxRanks];
-  bool ok = place(&X, x, T, D, ws, s) == cudaSuccess;
-  for (int i = 0; i < 2 * nranks && ok; ++i)
-    ok = place(&W[i], i % 2 ? ups[i / 2] : gates[i / 2], F, D, ws, s) == cudaSuccess;
+  Placer place(ws);
+  const Mat X = place(x, T, D);
+  Mat W[2 * kMaxRanks], dW[2 * kMaxRanks];
+  for (int i = 0; i < 2 * nranks; ++i) W[i] = place(i % 2 ? ups[i / 2] : gates[i / 2], F, D);
   const size_t ldf = up(F, 64);
   for (int i = 0; i < 2 * nranks; ++i) dW[i] = Mat{ws.take(T * ldf * 2), T, F, ldf};
   const size_t kb_seg = (F + 63) / 64, kb = 2 * (size_t)nranks * kb_seg;
   const int splits = pick_splits(T, D, kb);
   float* slots = splits > 1 ? static_cast<float*>(ws.take((size_t)splits * T * D * 4)) : nullptr;
-  if (!ok) return done(call, nranks, count, dtype, 0, RRA_ERR_CUDA);
+  if (!place.launch(s)) return done(call, nranks, count, dtype, 0, RRA_ERR_CUDA);
 
   // dg, du
   auto p = std::make_unique<TcArgs>();
   std::memset(p.get(), 0, sizeof(TcArgs));
-  ok = map_k(&p->a[0], X);
+  bool ok = map_k(&p->a[0], X);
   for (int r = 0; r < nranks && ok; ++r) {
     ok = map_k(&p->b[2 * r], W[2 * r]) && map_k(&p->b[2 * r + 1], W[2 * r + 1]);
     TcGroup g{};
@@ -616,14 +628,15 @@ rra_status_t rra_vocab_loss(const void* x, const void* const* weights, const siz
   Bump ws{static_cast<char*>(workspace)};
   auto p = std::make_unique<TcArgs>();
   std::memset(p.get(), 0, sizeof(TcArgs));
-  Mat X;
-  bool ok = place(&X, x, T, D, ws, s) == cudaSuccess && map_k(&p->a[0], X);
+  Placer place(ws);
+  const Mat X = place(x, T, D);
+  bool ok = map_k(&p->a[0], X);
   long long col0 = 0;
   int parts = 0;
   for (int r = 0; r < nranks && ok; ++r) {
     if (vocab[r]) {
-      Mat W;
-      ok = place(&W, weights[r], vocab[r], D, ws, s) == cudaSuccess && map_k(&p->b[r], W);
+      const Mat W = place(weights[r], vocab[r], D);
+      ok = map_k(&p->b[r], W);
       TcGroup g{};
       g.b = r;
       g.M = (int)T;
@@ -635,7 +648,7 @@ rra_status_t rra_vocab_loss(const void* x, const void* const* weights, const siz
     col0 += (long long)vocab[r];
     parts += (int)tiles256(vocab[r]);
   }
-  if (!ok) return done(call, nranks, T * V, dtype, 0, RRA_ERR_CUDA);
+  if (!ok || !place.launch(s)) return done(call, nranks, T * V, dtype, 0, RRA_ERR_CUDA);
   one_k_axis(p.get(), D);
   p->part = static_cast<float2*>(ws.take(2 * (size_t)parts * T * sizeof(float2)));
   p->part_ld = (long long)T;
@@ -647,8 +660,8 @@ rra_status_t rra_vocab_loss(const void* x, const void* const* weights, const siz
   int grid = 0;
   cudaError_t e = launch_tc_lse(*p, s, &grid);
   if (e == cudaSuccess)
-    e = launch_loss_join(p->part, p->part_ld, 2 * parts, p->hit, p->targets, ignore_index, (long long)V, (int)T, loss,
-                         lse, s);
+    e = launch_loss_join(p->part, 2 * parts, p->hit, p->targets, ignore_index, x, weights, vocab, nranks, D, (int)T,
+                         loss, lse, s);
   return done(call, nranks, T * V, dtype, grid, cuda_st(e));
 }
 
@@ -688,9 +701,11 @@ rra_status_t rra_vocab_loss_backward(const void* x, const void* const* weights, 
   if (!device_status()) return done(call, nranks, T * V, dtype, 0, RRA_ERR_NOT_INITIALIZED);
 
   Bump ws{static_cast<char*>(workspace)};
-  Mat X, W[kMaxRanks];
-  bool ok = place(&X, x, T, D, ws, s) == cudaSuccess;
-  for (int r = 0; r < nranks && ok; ++r) ok = place(&W[r], weights[r], vocab[r], D, ws, s) == cudaSuccess;
+  Placer place(ws);
+  const Mat X = place(x, T, D);
+  Mat W[kMaxRanks];
+  for (int r = 0; r < nranks; ++r) W[r] = place(weights[r], vocab[r], D);
+  bool ok = place.launch(s);
   if (!ok) return done(call, nranks, T * V, dtype, 0, RRA_ERR_CUDA);
   float* slots = q.slots ? static_cast<float*>(ws.take(q.slots * T * D * 4)) : nullptr;
   char* dl = ws.base + ws.at;

@@ -1,6 +1,6 @@
 // tc_epilogue.cuh -- row pieces between registers and memory for the
-// epilogues of tc_gemm.cuh: one thread holds 32 consecutive columns of a
-// row in float32.
+// epilogues of tc_gemm.cuh: one lane holds 32 consecutive columns of a row
+// in float32.
 #pragma once
 
 #include "tc_gemm.cuh"
@@ -12,21 +12,121 @@ __device__ __forceinline__ uint32_t tc_pack2(float a, float b) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
-// Store the first `valid` (clipped to [0, 32]) of 32 values as bfloat16.
-// vec: 16-byte stores for whole groups of 8; `pad`: the row has room up to
-// the next multiple of 8, so a partial group is stored whole.
-__device__ __forceinline__ void tc_store_bf16(__nv_bfloat16* dst, const float* v, int valid, bool vec, bool pad) {
+// Stores go through a warp's staging buffer: a lane holds 128 bytes of one
+// row (64 bfloat16 or 32 float32), which it writes as 16-byte chunks in a
+// swizzled order (chunk c of row r at c ^ (r & 7): no bank conflicts either
+// way), and the warp then stores whole rows, 8 lanes a row, so that every
+// store covers full 128-byte lines.  Straight from registers a warp's store
+// touched 32 rows: rows of 515 bfloat16 (no 16-byte stores) took 268 us for
+// the 333 x 515 x 50021 weight gradient.
+__device__ __forceinline__ void tc_stage_bf16(uint8_t* buf, const float* v, int first_chunk) {
+  const int r = threadIdx.x & 31;
 #pragma unroll
-  for (int c = 0; c < 32; c += 8) {
-    if (vec && (c + 8 <= valid || (pad && c < valid))) {
-      *reinterpret_cast<uint4*>(dst + c) = make_uint4(tc_pack2(v[c], v[c + 1]), tc_pack2(v[c + 2], v[c + 3]),
-                                                      tc_pack2(v[c + 4], v[c + 5]), tc_pack2(v[c + 6], v[c + 7]));
-    } else {
+  for (int c = 0; c < 4; ++c)
+    *reinterpret_cast<uint4*>(buf + r * 128 + (((first_chunk + c) ^ (r & 7)) << 4)) =
+        make_uint4(tc_pack2(v[8 * c], v[8 * c + 1]), tc_pack2(v[8 * c + 2], v[8 * c + 3]),
+                   tc_pack2(v[8 * c + 4], v[8 * c + 5]), tc_pack2(v[8 * c + 6], v[8 * c + 7]));
+}
+
+// Store `rows` rows (clipped to [0, 32]) of `valid` bfloat16 (clipped to [0,
+// 64]) from the staging buffer to dst, rows ld elements apart.  vec: dst
+// rows start on 16 bytes; `pad`: they have room up to the next multiple of
+// 8, so a partial chunk is stored whole.
+__device__ __forceinline__ void tc_flush_bf16(const uint8_t* buf, __nv_bfloat16* dst, long long ld, int rows, int valid,
+                                              bool vec, bool pad) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+  if (vec) {
+    const int c = lane & 7;
+    const int left = valid - 8 * c;
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (c + j < valid) dst[c + j] = __float2bfloat16_rn(v[c + j]);
+    for (int i = 0; i < 8; ++i) {
+      const int r = i * 4 + (lane >> 3);
+      if (r >= rows || left <= 0) continue;
+      const uint4 u = *reinterpret_cast<const uint4*>(buf + r * 128 + ((c ^ (r & 7)) << 4));
+      __nv_bfloat16* o = dst + r * ld + 8 * c;
+      if (left >= 8 || pad) {
+        *reinterpret_cast<uint4*>(o) = u;
+      } else {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        for (int j = 0; j < left; ++j)
+          reinterpret_cast<uint16_t*>(o)[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+      }
+    }
+  } else {
+    // rows of any alignment: pairs of elements in 4-byte stores, shifted by
+    // one element in the rows that start between two of them
+    const uint16_t* e = reinterpret_cast<const uint16_t*>(buf);
+    for (int r = 0; r < rows && r < 32; ++r) {
+      uint16_t* o = reinterpret_cast<uint16_t*>(dst + r * ld);
+      const int odd = (int)(((uintptr_t)o >> 1) & 1);
+      const int j = 2 * lane + odd;
+      const uint16_t a = j < 64 ? e[r * 64 + (((j >> 3) ^ (r & 7)) << 3) + (j & 7)] : 0;
+      const int k = j + 1;
+      const uint16_t b = k < 64 ? e[r * 64 + (((k >> 3) ^ (r & 7)) << 3) + (k & 7)] : 0;
+      if (k < valid && k < 64)
+        *reinterpret_cast<uint32_t*>(o + j) = (uint32_t)a | ((uint32_t)b << 16);
+      else if (j < valid && j < 64)
+        o[j] = a;
+      if (odd && lane == 0 && valid > 0) o[0] = e[r * 64 + ((r & 7) << 3)];
     }
   }
+  __syncwarp();
+}
+
+// Rows of 32 + 32 bfloat16 to two destinations with 16-byte rows padded to
+// whole chunks.
+__device__ __forceinline__ void tc_flush_pair(const uint8_t* buf, __nv_bfloat16* d0, __nv_bfloat16* d1, long long ld,
+                                              int rows, int valid) {
+  const int lane = threadIdx.x & 31, c = lane & 7;
+  __nv_bfloat16* dst = c < 4 ? d0 : d1;
+  __syncwarp();
+  if (8 * (c & 3) < valid) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = i * 4 + (lane >> 3);
+      if (r < rows)
+        *reinterpret_cast<uint4*>(dst + r * ld + 8 * (c & 3)) =
+            *reinterpret_cast<const uint4*>(buf + r * 128 + ((c ^ (r & 7)) << 4));
+    }
+  }
+  __syncwarp();
+}
+
+// The same for 32 float32 a row (vec: 16-byte rows); add: dst += row.
+__device__ __forceinline__ void tc_store_f32(uint8_t* buf, const float* v, float* dst, long long ld, int rows,
+                                             int valid, bool vec, bool add) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    *reinterpret_cast<float4*>(buf + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+        make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+  __syncwarp();
+  if (vec && valid >= 32) {
+    const int c = lane & 7;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = i * 4 + (lane >> 3);
+      if (r >= rows) continue;
+      float4 u = *reinterpret_cast<const float4*>(buf + r * 128 + ((c ^ (r & 7)) << 4));
+      float4* o = reinterpret_cast<float4*>(dst + r * ld + 4 * c);
+      if (add) {
+        const float4 q = *o;
+        u = make_float4(q.x + u.x, q.y + u.y, q.z + u.z, q.w + u.w);
+      }
+      *o = u;
+    }
+  } else {
+    const float* e = reinterpret_cast<const float*>(buf);
+    for (int r = 0; r < rows && r < 32; ++r) {
+      float* o = dst + r * ld + lane;
+      if (lane < valid) {
+        const float u = e[r * 32 + (((lane >> 2) ^ (r & 7)) << 2) + (lane & 3)];
+        *o = add ? *o + u : u;
+      }
+    }
+  }
+  __syncwarp();
 }
 
 // Load 32 bfloat16 (zeros from `valid` on).

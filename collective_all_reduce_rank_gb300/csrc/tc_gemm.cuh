@@ -45,7 +45,8 @@ constexpr int kTcBK = kTcKBlock;
 constexpr int kTcHalfBytes = 128 * kTcBK * 2;  // one operand's half tile of a CTA
 constexpr int kTcStageBytes = 2 * kTcHalfBytes;
 constexpr int kTcStages = 6;
-constexpr int kTcSmem = kTcStages * kTcStageBytes + 1024;  // + alignment slack
+constexpr int kTcStoreBytes = 4096;  // store staging of one epilogue warp (tc_epilogue.cuh)
+constexpr int kTcSmem = kTcStages * kTcStageBytes + kTcEpiWarps * kTcStoreBytes + 1024;  // + alignment slack
 constexpr unsigned long long kTcWaitNs = 2000ull * 1000 * 1000;
 
 // ---------------------------------------------------------------------------
@@ -238,8 +239,9 @@ __device__ __forceinline__ void tc_krange(const TcArgs& p, int split, int& k0, i
 }
 
 // ---------------------------------------------------------------------------
-// kernel.  Epi::run(p, tile, row, half, addr) consumes one accumulator: each
-// thread its row of C and the columns of half `half` (0 or 1) of the tile.
+// kernel.  Epi::run(p, tile, row0, half, addr, buf) consumes one accumulator:
+// each lane of a warp row row0 + lane of C and the columns of half `half` (0
+// or 1) of the tile, with kTcStoreBytes of shared memory for its stores.
 // ---------------------------------------------------------------------------
 template <bool AMN, bool BMN, class Epi>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
@@ -354,8 +356,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
       const uint32_t buf = tile & 1;
       if (!__all_sync(0xffffffffu, tc_wait(tc_smem(&sh.acc_full[buf]), (tile >> 1) & 1, &sh, p.status, 4))) break;
       tc_fence_after();
-      const int row = x.m * 256 + (int)rank * 128 + quad * 32 + lane;
-      Epi::run(p, x, row, half, tmem + buf * 256 + ((uint32_t)(quad * 32) << 16));
+      Epi::run(p, x, x.m * 256 + (int)rank * 128 + quad * 32, half,
+               tmem + buf * 256 + ((uint32_t)(quad * 32) << 16),
+               raw + (stages - tc_smem(raw)) + kTcStages * kTcStageBytes + (warp - 4) * kTcStoreBytes);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) tc_bar_arrive_remote(tc_smem(&sh.acc_empty[buf]), 0);

@@ -80,15 +80,24 @@ cudaError_t launch_tc_input_grad(const TcArgs& p, bool f32, cudaStream_t s, int*
 cudaError_t launch_tc_weight_grad(const TcArgs& p, cudaStream_t s, int* grid);
 
 // Row-wise helpers
-cudaError_t launch_loss_join(const float2* part, long long part_ld, int parts, const float* hit,
-                             const long long* targets, long long ignore_index, long long vocab, int rows,
-                             float* loss, float* lse, cudaStream_t s);
+// part: [parts][rows] running maximum and sum of each column part; hit: the
+// product's logit of each row's target.
+cudaError_t launch_loss_join(const float2* part, int parts, const float* hit, const long long* targets,
+                             long long ignore_index, const void* x, const void* const* w, const size_t* vocab, int n,
+                             size_t hidden, int rows, float* loss, float* lse, cudaStream_t s);
 // out[i] = bfloat16(sum over s of slots[s * stride + i])
 cudaError_t launch_join_slots(const float* slots, int n, long long stride, void* out, long long count,
                               cudaStream_t s);
-// dst[r][0..cols) = src[r][0..cols), dst rows ld elements apart
-cudaError_t launch_pad_rows(const void* src, void* dst, long long rows, long long cols, long long ld,
-                            cudaStream_t s);
+// Rows of `cols` elements of each src to rows of 8 * units elements of dst.
+struct PadArgs {
+  const void* src[kTcMaxGroups + 1];
+  void* dst[kTcMaxGroups + 1];
+  long long first[kTcMaxGroups + 2];  // first 16-byte unit of each matrix
+  long long cols;
+  int units;  // 16-byte units of a destination row
+  int n;
+};
+cudaError_t launch_pad_rows(const PadArgs& a, cudaStream_t s);
 
 // Training-side norm kernels (kernels_norm8.cu)
 constexpr int kCkptBlock = 128;
