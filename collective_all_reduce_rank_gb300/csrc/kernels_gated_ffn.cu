@@ -10,27 +10,10 @@
 // backward pass computes g and u again the same way and its epilogue turns
 // them and da into dg = da u act'(g) and du = da act(g), rounded to
 // bfloat16 (operands of the two gradient products, kernels_tc_store.cu).
-//
-//   silu(g) = g / (1 + exp(-g))
-//   gelu_tanh(g) = g / (1 + exp(-2z)), z = sqrt(2/pi) (g + 0.044715 g^3):
-//     0.5 (1 + tanh z) is the logistic function of 2z, which keeps its
-//     relative accuracy where 1 + tanh z cancels.
+#include "act.cuh"
 #include "tc_epilogue.cuh"
 
 namespace rra {
-
-// sigma = logistic(k(g)), *slope = k'(g)
-template <int ACT>
-__device__ __forceinline__ float gate_sigma(float g, float* slope) {
-  float k = g;
-  *slope = 1.f;
-  if constexpr (ACT == RRA_ACT_GELU_TANH) {
-    constexpr float c = 1.5957691216057308f;  // 2 sqrt(2/pi)
-    k = c * g * fmaf(0.044715f * g, g, 1.f);
-    *slope = c * fmaf(3.f * 0.044715f * g, g, 1.f);
-  }
-  return __fdividef(1.f, 1.f + __expf(-k));
-}
 
 template <int ACT>
 struct EpiGate {

@@ -18,6 +18,39 @@ namespace rra {
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct EpiLse {
+  // One row's 32 logits into its running maximum and sum.
+  static __device__ __forceinline__ void chunk(const TcArgs& p, float* v, int valid, long long d, int row, float& m,
+                                               float& s) {
+    if (valid < 32) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (j >= valid) v[j] = -INFINITY;
+    }
+    if (d >= 0 && d < 32 && d < valid) {
+      float h = v[0];  // a select per column: an indexed read would put v in local memory
+#pragma unroll
+      for (int j = 1; j < 32; ++j)
+        asm("{\n.reg .pred p;\nsetp.eq.s32 p, %1, %2;\n@p mov.f32 %0, %3;\n}\n" : "+f"(h) : "r"((int)d), "r"(j), "f"(v[j]));
+      p.hit[row] = h;
+    }
+    float q[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+    for (int j = 4; j < 32; ++j) q[j & 3] = fmaxf(q[j & 3], v[j]);
+    const float nm = fmaxf(m, fmaxf(fmaxf(q[0], q[1]), fmaxf(q[2], q[3])));
+    if (nm == -INFINITY) {  // nothing but -inf so far (or NaN, which the maximum skips)
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (v[j] != v[j]) s = v[j];
+    } else {
+      const float base = nm * kLog2e;
+      float e[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < 32; ++j) e[j & 3] += tc_exp2(fmaf(v[j], kLog2e, -base));
+      s = s * tc_exp2(fmaf(m, kLog2e, -base)) + ((e[0] + e[1]) + (e[2] + e[3]));
+      m = nm;
+    }
+  }
+
   static __device__ __forceinline__ void run(const TcArgs& p, const TcTile& x, int row0, int half, uint32_t addr,
                                              uint8_t*) {
     const TcGroup& g = p.group[x.group];
@@ -29,44 +62,18 @@ struct EpiLse {
       t = p.targets[row];
       t = t == p.ignore_index ? -1 : t - (g.col0 + c0);
     }
-#pragma unroll 1
-    for (int c = 0; c < 128; c += 32) {
-      const int valid = g.N - c0 - c;
-      if (valid <= 0) break;
-      float v[32];
-      tc_ld32(addr + half * 128 + c, v);
-      tc_ld_wait();
-      if (valid < 32) {
+    const int valid = g.N - c0;
+    if (valid > 0) {
+      // the next 32 columns are read from tensor memory under the exponentials of these
+      float v[2][32];
+      tc_ld32(addr + half * 128, v[0]);
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (j >= valid) v[j] = -INFINITY;
+      for (int c = 0; c < 4; ++c) {
+        tc_ld_ready(v[c & 1]);
+        if (c < 3) tc_ld32(addr + half * 128 + 32 * (c + 1), v[(c + 1) & 1]);
+        if (32 * c < valid) chunk(p, v[c & 1], valid - 32 * c, t - 32 * c, row, m, s);
       }
-      const long long d = t - c;
-      if (d >= 0 && d < 32 && d < valid) {
-        uint32_t h = 0;  // as bits: a select per column, no indexed registers
-#pragma unroll
-        for (int j = 0; j < 32; ++j) h |= j == (int)d ? __float_as_uint(v[j]) : 0u;
-        p.hit[row] = __uint_as_float(h);
-      }
-      float q = v[0];
-#pragma unroll
-      for (int j = 1; j < 32; ++j) q = fmaxf(q, v[j]);
-      const float nm = fmaxf(m, q);
-      if (nm == -INFINITY) {  // nothing but -inf so far (or NaN, which the maximum skips)
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (v[j] != v[j]) s = v[j];
-        continue;
-      }
-      const float base = nm * kLog2e;
-      float a = 0.f, b = 0.f;
-#pragma unroll
-      for (int j = 0; j < 32; j += 2) {
-        a += exp2f(fmaf(v[j], kLog2e, -base));
-        b += exp2f(fmaf(v[j + 1], kLog2e, -base));
-      }
-      s = s * exp2f(fmaf(m, kLog2e, -base)) + (a + b);
-      m = nm;
+      __syncwarp();
     }
     if (row < g.M) p.part[(long long)((g.part0 + x.n) * 2 + half) * p.part_ld + row] = make_float2(m, s);
   }
@@ -98,12 +105,12 @@ struct EpiDlogits {
       for (int k = 0; k < 64; k += 32) {
         float v[32];
         tc_ld32(addr + half * 128 + c + k, v);
-        tc_ld_wait();
+        tc_ld_ready(v);
         const long long q = t - c - k;
         const int d = q >= 0 && q < 32 ? (int)q : -1;
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
-          const float e = exp2f(fmaf(v[j], kLog2e, -base)) - (j == d ? 1.f : 0.f);
+          const float e = tc_exp2(fmaf(v[j], kLog2e, -base)) - (j == d ? 1.f : 0.f);
           v[j] = live ? e * w : 0.f;
         }
         tc_stage_bf16(buf, v, k / 8);

@@ -69,7 +69,7 @@ struct Bump {
 };
 
 bool padded(size_t hidden) { return hidden % 8 != 0; }
-size_t pad_ld(size_t hidden) { return up(hidden, 8); }
+size_t pad_ld(size_t hidden) { return up(hidden, 64); }  // rows of whole 128-byte lines
 
 // The rows products read of the caller's matrices: copied to padded rows
 // when needed, all of them in one launch.
@@ -310,9 +310,11 @@ rra_status_t rra_allreduce_rmsnorm_backward8(const void* const* grads, void* con
 namespace {
 
 // Workspace of a call, in the order the call takes it.
+bool skinny(size_t T, size_t D) { return T <= kSkinnyTokens && D >= kSkinnyHidden; }
+
 size_t ffn_bytes(int n, size_t T, size_t D, size_t F, bool back) {
   Bump b{nullptr};
-  if (padded(D)) {
+  if (padded(D) && (back || !skinny(T, D))) {
     b.take(T * pad_ld(D) * 2);
     for (int i = 0; i < 2 * n; ++i) b.take(F * pad_ld(D) * 2);
   }
@@ -375,6 +377,24 @@ rra_status_t rra_gated_ffn(const void* x, const void* const* gates, const void* 
   if (T == 0 || F == 0) return done(call, nranks, 0, dtype, 0, RRA_SUCCESS);
   if (!device_status()) return done(call, nranks, count, dtype, 0, RRA_ERR_NOT_INITIALIZED);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (skinny(T, D)) {
+    SkinnyArgs a{};
+    a.x = x;
+    a.tokens = (int)T;
+    a.hidden = (int)D;
+    a.width = (int)F;
+    const size_t units = (size_t)nranks * ((F + 7) / 8);
+    if (units > INT_MAX / 2) return done(call, nranks, count, dtype, 0, RRA_ERR_UNSUPPORTED);
+    a.units = (int)units;
+    for (int r = 0; r < nranks; ++r) {
+      a.w[2 * r] = gates[r];
+      a.w[2 * r + 1] = ups[r];
+      a.out[r] = acts[r];
+    }
+    int grid = 0;
+    const cudaError_t e = launch_skinny_gate(a, act, s, &grid);
+    return done(call, nranks, count, dtype, grid, cuda_st(e));
+  }
   Bump ws{static_cast<char*>(workspace)};
   auto p = std::make_unique<TcArgs>();
   std::memset(p.get(), 0, sizeof(TcArgs));
@@ -544,9 +564,21 @@ struct LossPlan {
   size_t slots = 0;        // float32 copies of dx kept
 };
 
+long long skinny_units(int n, const size_t* vocab) {
+  long long u = 0;
+  for (int r = 0; r < n; ++r) u += (long long)((vocab[r] + 15) / 16);
+  return u;
+}
+
 LossPlan loss_plan(int n, size_t T, size_t D, const size_t* vocab, bool back, size_t room) {
   LossPlan q;
   Bump b{nullptr};
+  if (!back && skinny(T, D)) {
+    b.take((size_t)skinny_grid(skinny_units(n, vocab)) * T * sizeof(float2));
+    b.take(T * 4);
+    q.fixed = b.at;
+    return q;
+  }
   if (padded(D)) {
     b.take(T * pad_ld(D) * 2);
     for (int r = 0; r < n; ++r) b.take(vocab[r] * pad_ld(D) * 2);
@@ -626,6 +658,32 @@ rra_status_t rra_vocab_loss(const void* x, const void* const* weights, const siz
   if (!device_status()) return done(call, nranks, T * V, dtype, 0, RRA_ERR_NOT_INITIALIZED);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   Bump ws{static_cast<char*>(workspace)};
+  if (skinny(T, D)) {
+    SkinnyArgs a{};
+    a.x = x;
+    a.tokens = (int)T;
+    a.hidden = (int)D;
+    long long col = 0;
+    for (int r = 0; r < nranks; ++r) {
+      a.w[r] = weights[r];
+      a.rows[r] = (long long)vocab[r];
+      a.col0[r] = col;
+      a.unit0[r + 1] = a.unit0[r] + (int)((vocab[r] + 15) / 16);
+      col += (long long)vocab[r];
+    }
+    a.units = a.unit0[nranks];
+    for (int r = nranks; r < kMaxRanks; ++r) a.unit0[r + 1] = a.units;
+    a.targets = reinterpret_cast<const long long*>(targets);
+    a.ignore_index = ignore_index;
+    a.part = static_cast<float2*>(ws.take((size_t)skinny_grid(a.units) * T * sizeof(float2)));
+    a.hit = static_cast<float*>(ws.take(T * 4));
+    int grid = 0;
+    cudaError_t e = launch_skinny_lse(a, s, &grid);
+    if (e == cudaSuccess)
+      e = launch_loss_join(a.part, grid, a.hit, a.targets, ignore_index, x, weights, vocab, nranks, D, (int)T, loss,
+                           lse, s);
+    return done(call, nranks, T * V, dtype, grid, cuda_st(e));
+  }
   auto p = std::make_unique<TcArgs>();
   std::memset(p.get(), 0, sizeof(TcArgs));
   Placer place(ws);

@@ -57,7 +57,9 @@ __device__ __forceinline__ void tc_flush_bf16(const uint8_t* buf, __nv_bfloat16*
     // rows of any alignment: pairs of elements in 4-byte stores, shifted by
     // one element in the rows that start between two of them
     const uint16_t* e = reinterpret_cast<const uint16_t*>(buf);
-    for (int r = 0; r < rows && r < 32; ++r) {
+    const int top = rows < 32 ? rows : 32;
+#pragma unroll 4
+    for (int r = 0; r < top; ++r) {
       uint16_t* o = reinterpret_cast<uint16_t*>(dst + r * ld);
       const int odd = (int)(((uintptr_t)o >> 1) & 1);
       const int j = 2 * lane + odd;

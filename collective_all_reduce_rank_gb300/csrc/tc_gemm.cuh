@@ -72,7 +72,7 @@ __device__ __forceinline__ bool tc_bar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n.reg .pred p;\n"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
       "selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
       : "r"(bar), "r"(parity), "r"(20000u)
@@ -80,12 +80,15 @@ __device__ __forceinline__ bool tc_bar_try(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-// Arrive on the barrier at the same offset in CTA `cta` of the cluster.
+// Arrive on the barrier at the same offset in CTA `cta` of the cluster.  What
+// it reports is the end of tensor-memory reads, whose values are in registers
+// (tcgen05.wait::ld): no memory needs publishing to the cluster, and a release
+// at that scope would wait for the epilogue's global stores.
 __device__ __forceinline__ void tc_bar_arrive_remote(uint32_t bar, uint32_t cta) {
   asm volatile(
       "{\n.reg .b32 a;\n"
       "mapa.shared::cluster.u32 a, %0, %1;\n"
-      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n}\n" ::"r"(bar),
+      "mbarrier.arrive.shared::cluster.b64 _, [a];\n}\n" ::"r"(bar),
       "r"(cta)
       : "memory");
 }
@@ -135,6 +138,14 @@ __device__ __forceinline__ void tc_commit(uint32_t bar) {
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
+// 2^x by the special function unit (two units in the last place, results
+// below 2^-126 flushed to zero: nothing beside the 1 of a row's maximum).
+__device__ __forceinline__ float tc_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // 32 lanes x 32 columns of float32: lane l of the warp gets row l.
 __device__ __forceinline__ void tc_ld32(uint32_t addr, float* v) {
   uint32_t r[32];
@@ -151,6 +162,19 @@ __device__ __forceinline__ void tc_ld32(uint32_t addr, float* v) {
       : "memory");
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Wait for this thread's tensor-memory reads; the values become usable here
+// (they are operands, so no use can move above the wait).
+__device__ __forceinline__ void tc_ld_ready(float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]),
+                 "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]),
+                 "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]),
+                 "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
+               :
+               : "memory");
 }
 
 __device__ __forceinline__ void tc_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }

@@ -79,6 +79,27 @@ cudaError_t launch_tc_input_grad(const TcArgs& p, bool f32, cudaStream_t s, int*
 // out = A^T B, both MN-major (the gradient of the weights): bfloat16 rows.
 cudaError_t launch_tc_weight_grad(const TcArgs& p, cudaStream_t s, int* grid);
 
+// Few tokens (kernels_skinny.cu): at most kSkinnyTokens, hidden of
+// kSkinnyHidden or more.
+constexpr size_t kSkinnyTokens = 16;
+constexpr size_t kSkinnyHidden = 512;
+struct SkinnyArgs {
+  const void* x;
+  const void* w[2 * kMaxRanks];  // gate and up shards in turn, or vocabulary shards
+  void* out[kMaxRanks];
+  int tokens, hidden, width;
+  int units;
+  int unit0[kMaxRanks + 1];  // loss: first unit of each shard
+  long long rows[kMaxRanks], col0[kMaxRanks];
+  const long long* targets;
+  long long ignore_index;
+  float2* part;  // [grid][tokens]
+  float* hit;
+};
+int skinny_grid(long long units);
+cudaError_t launch_skinny_gate(const SkinnyArgs& a, int act, cudaStream_t s, int* grid);
+cudaError_t launch_skinny_lse(const SkinnyArgs& a, cudaStream_t s, int* grid);
+
 // Row-wise helpers
 // part: [parts][rows] running maximum and sum of each column part; hit: the
 // product's logit of each row's target.

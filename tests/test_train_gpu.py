@@ -52,6 +52,9 @@ FFN = [  # n, tokens, hidden, width, act
     (1, 1, 64, 128, 0), (1, 128, 64, 128, 0), (1, 256, 256, 128, 1), (2, 256, 128, 256, 0), (1, 300, 200, 130, 1),
     (3, 77, 88, 33, 0), (2, 1, 512, 520, 1), (8, 16, 128, 40, 0), (2, 129, 1027, 65, 0), (3, 5, 7, 3, 1),
     (2, 513, 640, 384, 0), (1, 1, 1, 1, 0), (4, 700, 72, 1000, 0),
+    # few tokens: the register path, rows on and off 16 bytes
+    (1, 1, 5120, 24, 0), (8, 8, 1024, 17, 1), (3, 9, 2056, 64, 0), (2, 16, 515, 33, 0), (1, 7, 1027, 8, 1), (2, 3, 771, 100, 0),
+    (1, 17, 1024, 72, 0), (2, 40, 520, 136, 1),
 ]
 
 
@@ -93,6 +96,9 @@ def test_gated_ffn_backward(n, T, D, F, act):
 LOSS = [  # tokens, hidden, shard heights
     (1, 64, (256,)), (256, 64, (256,)), (5, 64, (300, 300)), (300, 128, (512, 511)), (33, 200, (1000, 1000, 997)),
     (129, 1027, (257, 0, 64)), (7, 515, (1,)), (64, 72, (100,) * 8), (2, 8, (3, 2)), (513, 256, (2048, 2048)),
+    # few tokens: the register path
+    (1, 5120, (700, 700)), (8, 1024, (16, 15, 0, 33)), (16, 515, (401, 400)), (9, 1027, (3000,)), (5, 771, (17,)),
+    (17, 1024, (500,)),
 ]
 
 
