@@ -16,8 +16,17 @@
 // code (only a rounding border of bfloat16 itself could).
 //
 // All three kernels are bound by HBM: each input byte is read once, each
-// output byte written once; the float32 row stays in shared memory between
-// the two passes over a row.
+// output byte written once.  A CTA of 256 threads takes a row; a thread's
+// columns are 16-byte units (unit u: thread u mod 256).  Rows of up to 6144
+// columns of 16-byte aligned buffers stay in registers between the two
+// passes over a row ("reg" kernels, 24 float32 a thread); longer rows, and
+// rows that start anywhere, keep the sums in shared memory ("gen" kernels):
+// their loads combine the two aligned 16-byte blocks around a unit, their
+// stores go through shared memory so that a warp still writes whole words of
+// neighbouring columns.
+//
+// The sum of squares is added in the order of the kernel that saves nothing
+// (kernels_rmsnorm.cu), so that both give the same bits.
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -26,6 +35,8 @@
 namespace rra {
 
 constexpr int kN8Threads = 256;
+constexpr int kN8Regs = 24;                  // float32 of a row a thread keeps
+constexpr float kBf16Max = 3.3895314e38f;    // largest finite bfloat16
 
 struct Save8Args {
   const void* in[kMaxRanks];
@@ -36,6 +47,8 @@ struct Save8Args {
   float* rstd;
   size_t rows, hidden;
   float eps;
+  int vec;
+  int stage_codes;
 };
 
 struct Back8Args {
@@ -45,8 +58,10 @@ struct Back8Args {
   const uint8_t* codes;
   const uint8_t* scales;
   const float* rstd;
-  float* part;  // [CTA][hidden] float32: this CTA's rows' share of dgamma
+  float* part;   // [CTA][pitch] float32: this CTA's rows' share of dgamma
+  size_t pitch;  // hidden rounded up to whole units
   size_t rows, hidden;
+  int vec;
 };
 
 template <int DT>
@@ -55,6 +70,44 @@ __device__ __forceinline__ void unit_floats(uint4 v, float* f) {
   acc_init<DT>(a, v);
 #pragma unroll
   for (int i = 0; i < Elem<DT>::kPerUnit; ++i) f[i] = __uint_as_float(a.w[i]);
+}
+
+// A unit of a row that starts on any element: the aligned 16-byte blocks
+// that hold its first and its last byte (both hold bytes of the row), the
+// second fetched by the next thread too and so an L1 hit.
+template <int DT>
+__device__ __forceinline__ uint4 load_any(const char* row, size_t u, int valid) {
+  const char* p = row + u * 16;
+  if (valid < Elem<DT>::kPerUnit) return ld_partial<DT>(p, valid);
+  const uint32_t off = (uint32_t)((uintptr_t)p & 15);
+  const uint4* lo = reinterpret_cast<const uint4*>(p - off);
+  const uint4 a = __ldg(lo);
+  if (off == 0) return a;
+  const uint4 b = __ldg(lo + 1);
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  if (off & 8) {
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  }
+  if (off & 4) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  }
+  const uint32_t sh = (off & 2) * 8;
+  return make_uint4(__funnelshift_r(w[0], w[1], sh), __funnelshift_r(w[1], w[2], sh), __funnelshift_r(w[2], w[3], sh),
+                    __funnelshift_r(w[3], w[4], sh));
+}
+
+template <int DT>
+__device__ __forceinline__ uint4 load_row(const char* row, size_t u, int valid, bool vec) {
+  return vec ? ld_stream(row + u * 16) : load_any<DT>(row, u, valid);
+}
+
+// gamma is read again by every row: kept in L1
+template <int DT>
+__device__ __forceinline__ void load_gamma(const void* gamma, size_t u, int valid, bool vec, float* f) {
+  const char* g = static_cast<const char*>(gamma);
+  unit_floats<DT>(vec ? __ldg(reinterpret_cast<const uint4*>(g) + u) : load_any<DT>(g, u, valid), f);
 }
 
 // Block reduction in a fixed order; every thread gets the sum.
@@ -91,266 +144,491 @@ __device__ __forceinline__ float2 values2(uint32_t two) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// Codes of one unit (8 or 4 columns) from column u * PU of a row.
+// Codes of one unit (8 or 4 columns), raw.
 template <int DT>
-__device__ __forceinline__ void load_codes(const uint8_t* row, size_t u, int valid, bool vec, float* f) {
+__device__ __forceinline__ uint2 load_codes(const uint8_t* row, size_t u, int valid, bool vec) {
   constexpr int PU = Elem<DT>::kPerUnit;
   const uint8_t* p = row + u * PU;
-  uint32_t w[2] = {0u, 0u};
-  if (vec && valid == PU) {
-    if constexpr (PU == 8) {
-      const uint2 q = __ldg(reinterpret_cast<const uint2*>(p));
-      w[0] = q.x;
-      w[1] = q.y;
-    } else {
-      w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-    }
-  } else {
-    for (int i = 0; i < valid; ++i) w[i >> 2] |= (uint32_t)__ldg(p + i) << (8 * (i & 3));
+  if (vec) {
+    if constexpr (PU == 8) return __ldg(reinterpret_cast<const uint2*>(p));
+    return make_uint2(__ldg(reinterpret_cast<const uint32_t*>(p)), 0u);
   }
+  uint32_t w[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < PU; ++i)
+    if (i < valid) w[i >> 2] |= (uint32_t)__ldg(p + i) << (8 * (i & 3));
+  return make_uint2(w[0], w[1]);
+}
+
+template <int DT>
+__device__ __forceinline__ void code_floats(uint2 c, float mul, float* f) {
+  constexpr int PU = Elem<DT>::kPerUnit;
+  const uint32_t w[2] = {c.x, c.y};
 #pragma unroll
   for (int i = 0; i < PU; i += 2) {
     const float2 v = values2((w[i >> 2] >> (8 * (i & 3))) & 0xFFFFu);
-    f[i] = v.x;
-    f[i + 1] = v.y;
+    f[i] = __fmul_rn(v.x, mul);
+    f[i + 1] = __fmul_rn(v.y, mul);
   }
 }
 
-template <int N, int DT, bool VEC>
-__global__ void __launch_bounds__(kN8Threads) norm_save8_kernel(const __grid_constant__ Save8Args a) {
+// Codes of a unit's sums f, in all lanes of a warp at once: lanes of one
+// block of 128 columns share its largest value.  *e gets the block's
+// exponent.
+template <int DT>
+__device__ __forceinline__ uint2 encode_unit(const float* f, int* e) {
   constexpr int PU = Elem<DT>::kPerUnit;
-  constexpr int ES = Elem<DT>::kSize;
-  constexpr int LANES = kCkptBlock / PU;  // lanes that hold one block
-  extern __shared__ float srow[];
+  float b[PU], top = 0.f;
+#pragma unroll
+  for (int i = 0; i < PU; ++i) {
+    b[i] = __bfloat162float(__float2bfloat16_rn(f[i]));
+    const float m = fabsf(b[i]);
+    top = m <= kBf16Max ? fmaxf(top, m) : top;  // finite
+  }
+#pragma unroll
+  for (int o = kCkptBlock / PU / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  *e = ckpt_exponent(top);
+  const float mul = pow2(-*e);
+  uint32_t w[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < PU; i += 2) {
+    const float lo = fabsf(b[i]) <= kBf16Max ? b[i] * mul : NAN;
+    const float hi = fabsf(b[i + 1]) <= kBf16Max ? b[i + 1] * mul : NAN;
+    w[i >> 2] |= codes2(lo, hi) << (8 * (i & 3));
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// The sum over ranks of one unit.
+template <int N, int DT>
+__device__ __forceinline__ void sum_ranks(const void* const* in, size_t row_off, size_t u, int valid, bool vec, Acc& s) {
+  uint4 x[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) x[k] = load_row<DT>(static_cast<const char*>(in[k]) + row_off, u, valid, vec);
+  acc_init<DT>(s, x[0]);
+#pragma unroll
+  for (int k = 1; k < N; ++k) acc_add<DT>(s, x[k]);
+}
+
+template <int DT>
+__device__ __forceinline__ void put_codes(uint8_t* c, uint2 w, int valid, bool vec) {
+  if (vec) {
+    if constexpr (Elem<DT>::kPerUnit == 8)
+      *reinterpret_cast<uint2*>(c) = w;
+    else
+      *reinterpret_cast<uint32_t*>(c) = w.x;
+  } else {
+    const uint32_t q[2] = {w.x, w.y};
+#pragma unroll
+    for (int i = 0; i < Elem<DT>::kPerUnit; ++i)
+      if (i < valid) c[i] = (uint8_t)(q[i >> 2] >> (8 * (i & 3)));
+  }
+}
+
+// Store a row held in shared memory (unit u's 16 bytes at u * stride) to a
+// row of global memory that starts on any element, in 4-byte words.
+template <int DT>
+__device__ __forceinline__ void store_row_any(char* dst, const char* units, int stride, size_t hidden) {
+  if constexpr (Elem<DT>::kSize == 4) {
+    for (size_t i = threadIdx.x; i < hidden; i += kN8Threads)
+      reinterpret_cast<uint32_t*>(dst)[i] = *reinterpret_cast<const uint32_t*>(units + (i >> 2) * stride + (i & 3) * 4);
+  } else {
+    auto at = [&](size_t i) { return *reinterpret_cast<const uint16_t*>(units + (i >> 3) * stride + (i & 7) * 2); };
+    uint16_t* o = reinterpret_cast<uint16_t*>(dst);
+    const size_t head = ((uintptr_t)dst >> 1) & 1;  // one element before the first whole word
+    if (threadIdx.x == 0 && head) o[0] = at(0);
+    for (size_t i = head + 2 * threadIdx.x; i < hidden; i += 2 * kN8Threads) {
+      if (i + 1 < hidden)
+        *reinterpret_cast<uint32_t*>(o + i) = (uint32_t)at(i) | ((uint32_t)at(i + 1) << 16);
+      else
+        o[i] = at(i);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// forward
+// ---------------------------------------------------------------------------
+template <int N, int DT>
+__global__ void __launch_bounds__(kN8Threads) save8_reg_kernel(const __grid_constant__ Save8Args a) {
+  constexpr int PU = Elem<DT>::kPerUnit, U = kN8Regs / PU;
   __shared__ float s_part[kN8Threads / 32];
-  const size_t hidden = a.hidden;
-  const size_t units = (hidden + PU - 1) / PU;
-  const size_t row = blockIdx.x;
-  const size_t row_off = row * hidden * ES;
+  const int units = (int)(a.hidden / PU), tid = threadIdx.x;
+  const size_t row = blockIdx.x, row_off = row * a.hidden * Elem<DT>::kSize;
+  const size_t nblk = (a.hidden + kCkptBlock - 1) / kCkptBlock;
+  float f[U][PU];
+  float ss = 0.f;
+#pragma unroll
+  for (int j = 0; j < U; ++j) {
+    if (j * kN8Threads >= units) break;
+    const int u = j * kN8Threads + tid;
+#pragma unroll
+    for (int i = 0; i < PU; ++i) f[j][i] = 0.f;
+    if (u < units) {
+      Acc s;
+      sum_ranks<N, DT>(a.in, row_off, u, PU, true, s);
+#pragma unroll
+      for (int i = 0; i < PU; ++i) {
+        f[j][i] = __uint_as_float(s.w[i]);
+        ss = __fmaf_rn(f[j][i], f[j][i], ss);
+      }
+    }
+  }
+  const float tot = block_sum(ss, s_part);
+  const float inv = rsqrtf(tot / (float)a.hidden + a.eps);
+  if (tid == 0) a.rstd[row] = inv;
+#pragma unroll
+  for (int j = 0; j < U; ++j) {
+    if (j * kN8Threads >= units) break;
+    const int u = j * kN8Threads + tid;
+    int e;
+    const uint2 c = encode_unit<DT>(f[j], &e);
+    if (u >= units) continue;
+    float g[PU];
+    load_gamma<DT>(a.gamma, u, PU, true, g);
+    Acc y;
+#pragma unroll
+    for (int i = 0; i < PU; ++i) y.w[i] = __float_as_uint(__fmul_rn(__fmul_rn(f[j][i], inv), g[i]));
+    const uint4 o = acc_narrow<DT>(y);
+#pragma unroll
+    for (int r = 0; r < N; ++r) st_stream(static_cast<char*>(a.out[r]) + row_off + (size_t)u * 16, o);
+    put_codes<DT>(a.codes + row * a.hidden + (size_t)u * PU, c, PU, true);
+    if (u % (kCkptBlock / PU) == 0) a.scales[row * nblk + u / (kCkptBlock / PU)] = (uint8_t)(e + 127);
+  }
+}
+
+template <int N, int DT>
+__global__ void __launch_bounds__(kN8Threads) save8_gen_kernel(const __grid_constant__ Save8Args a) {
+  constexpr int PU = Elem<DT>::kPerUnit;
+  extern __shared__ __align__(16) char smem[];  // PU float32 per unit, then (stage_codes) the row's codes
+  __shared__ float s_part[kN8Threads / 32];
+  const size_t hidden = a.hidden, units = (hidden + PU - 1) / PU, row = blockIdx.x;
+  const size_t row_off = row * hidden * Elem<DT>::kSize;
   const size_t nblk = (hidden + kCkptBlock - 1) / kCkptBlock;
   const int tid = threadIdx.x;
   uint8_t* crow = a.codes + row * hidden;
-  const bool cvec = VEC && hidden % PU == 0;
-
+  uint8_t* cstage = reinterpret_cast<uint8_t*>(smem + units * PU * 4);
   float ss = 0.f;
   for (size_t u0 = 0; u0 < units; u0 += kN8Threads) {
     const size_t u = u0 + tid;
     const int v = u < units ? unit_valid<DT>(u, hidden) : 0;
     float f[PU];
+#pragma unroll
+    for (int i = 0; i < PU; ++i) f[i] = 0.f;
     if (v) {
-      uint4 x[N];
-#pragma unroll
-      for (int k = 0; k < N; ++k) x[k] = load_in<DT, VEC>(static_cast<const char*>(a.in[k]) + row_off, u, v);
       Acc s;
-      acc_init<DT>(s, x[0]);
-#pragma unroll
-      for (int k = 1; k < N; ++k) acc_add<DT>(s, x[k]);
+      sum_ranks<N, DT>(a.in, row_off, u, v, a.vec, s);
 #pragma unroll
       for (int i = 0; i < PU; ++i) {
         f[i] = i < v ? __uint_as_float(s.w[i]) : 0.f;
-        srow[u * PU + i] = f[i];
         ss = __fmaf_rn(f[i], f[i], ss);
       }
-    } else {
+      float4* o = reinterpret_cast<float4*>(smem + u * PU * 4);
 #pragma unroll
-      for (int i = 0; i < PU; ++i) f[i] = 0.f;
+      for (int i = 0; i < PU / 4; ++i) o[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
     }
-    float top = 0.f;
-#pragma unroll
-    for (int i = 0; i < PU; ++i) {
-      f[i] = __bfloat162float(__float2bfloat16_rn(f[i]));
-      const float m = fabsf(f[i]);
-      if (m <= 3.3895314e38f) top = fmaxf(top, m);  // finite
-    }
-#pragma unroll
-    for (int o = LANES / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    int e;
+    const uint2 c = encode_unit<DT>(f, &e);
     if (v) {
-      const int e = ckpt_exponent(top);
-      const float mul = pow2(-e);
-      uint32_t w[2] = {0u, 0u};
-#pragma unroll
-      for (int i = 0; i < PU; i += 2) {
-        const float lo = fabsf(f[i]) <= 3.3895314e38f ? f[i] * mul : NAN;
-        const float hi = fabsf(f[i + 1]) <= 3.3895314e38f ? f[i + 1] * mul : NAN;
-        w[i >> 2] |= codes2(lo, hi) << (8 * (i & 3));
-      }
-      uint8_t* c = crow + u * PU;
-      if (cvec && v == PU) {
-        if constexpr (PU == 8)
-          *reinterpret_cast<uint2*>(c) = make_uint2(w[0], w[1]);
-        else
-          *reinterpret_cast<uint32_t*>(c) = w[0];
-      } else {
-        for (int i = 0; i < v; ++i) c[i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
-      }
-      if (u % LANES == 0) a.scales[row * nblk + u / LANES] = (uint8_t)(e + 127);
+      if (a.stage_codes)
+        put_codes<DT>(cstage + u * PU, c, PU, true);
+      else
+        put_codes<DT>(crow + u * PU, c, v, a.vec);
+      if (u % (kCkptBlock / PU) == 0) a.scales[row * nblk + u / (kCkptBlock / PU)] = (uint8_t)(e + 127);
     }
   }
   const float tot = block_sum(ss, s_part);
   const float inv = rsqrtf(tot / (float)hidden + a.eps);
   if (tid == 0) a.rstd[row] = inv;
-
   for (size_t u = tid; u < units; u += kN8Threads) {
     const int v = unit_valid<DT>(u, hidden);
     float g[PU];
-    unit_floats<DT>(load_in<DT, VEC>(a.gamma, u, v), g);
+    load_gamma<DT>(a.gamma, u, v, a.vec, g);
+    const float* f = reinterpret_cast<const float*>(smem + u * PU * 4);
     Acc y;
 #pragma unroll
-    for (int i = 0; i < PU; ++i) y.w[i] = __float_as_uint(__fmul_rn(__fmul_rn(srow[u * PU + i], inv), g[i]));
+    for (int i = 0; i < PU; ++i) y.w[i] = __float_as_uint(__fmul_rn(__fmul_rn(f[i], inv), g[i]));
     const uint4 o = acc_narrow<DT>(y);
+    if (a.vec) {
 #pragma unroll
-    for (int r = 0; r < N; ++r) store_out<DT, VEC, true>(static_cast<char*>(a.out[r]) + row_off, u, v, o);
+      for (int r = 0; r < N; ++r) st_stream(static_cast<char*>(a.out[r]) + row_off + u * 16, o);
+    } else {
+      *reinterpret_cast<uint4*>(smem + u * PU * 4) = o;  // over this thread's own sums
+    }
+  }
+  if (!a.vec) {
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < N; ++r) store_row_any<DT>(static_cast<char*>(a.out[r]) + row_off, smem, PU * 4, hidden);
+    if (a.stage_codes) {  // whole words of the row of bytes
+      const size_t head = (4 - ((uintptr_t)crow & 3)) & 3;
+      if (tid < head && tid < hidden) crow[tid] = cstage[tid];
+      for (size_t i = head + 4 * tid; i < hidden; i += 4 * kN8Threads) {
+        if (i + 4 <= hidden)
+          *reinterpret_cast<uint32_t*>(crow + i) = (uint32_t)cstage[i] | ((uint32_t)cstage[i + 1] << 8) |
+                                                   ((uint32_t)cstage[i + 2] << 16) | ((uint32_t)cstage[i + 3] << 24);
+        else
+          for (size_t k = i; k < hidden; ++k) crow[k] = cstage[k];
+      }
+    }
   }
 }
 
 // out = code 2^e, times rstd of the row and gamma of the column where given.
 template <int DT, bool VEC>
 __global__ void __launch_bounds__(kN8Threads)
-    norm_restore8_kernel(const uint8_t* codes, const uint8_t* scales, const float* rstd, const void* gamma, void* out,
-                         size_t rows, size_t hidden) {
+    restore8_kernel(const uint8_t* codes, const uint8_t* scales, const float* rstd, const void* gamma, void* out,
+                    size_t rows, size_t hidden) {
   constexpr int PU = Elem<DT>::kPerUnit;
+  extern __shared__ __align__(16) char smem[];
   const size_t units = (hidden + PU - 1) / PU;
   const size_t nblk = (hidden + kCkptBlock - 1) / kCkptBlock;
-  const bool cvec = VEC && hidden % PU == 0;
   for (size_t row = blockIdx.x; row < rows; row += gridDim.x) {
     const float q = rstd ? __ldg(rstd + row) : 1.f;
+    char* orow = static_cast<char*>(out) + row * hidden * Elem<DT>::kSize;
     for (size_t u = threadIdx.x; u < units; u += kN8Threads) {
-      const int v = unit_valid<DT>(u, hidden);
+      const int v = VEC ? PU : unit_valid<DT>(u, hidden);
       float f[PU], g[PU];
-      load_codes<DT>(codes + row * hidden, u, v, cvec, f);
-      if (gamma) unit_floats<DT>(load_in<DT, VEC>(gamma, u, v), g);
-      const float mul = pow2((int)__ldg(scales + row * nblk + u * PU / kCkptBlock) - 127);
+      code_floats<DT>(load_codes<DT>(codes + row * hidden, u, v, VEC),
+                      pow2((int)__ldg(scales + row * nblk + u * PU / kCkptBlock) - 127), f);
+      if (gamma) load_gamma<DT>(gamma, u, v, VEC, g);
       Acc y;
 #pragma unroll
       for (int i = 0; i < PU; ++i) {
-        float t = __fmul_rn(__fmul_rn(f[i], mul), q);
+        float t = __fmul_rn(f[i], q);
         if (gamma) t = __fmul_rn(t, g[i]);
         y.w[i] = __float_as_uint(t);
       }
-      store_out<DT, VEC, true>(static_cast<char*>(out) + row * hidden * Elem<DT>::kSize, u, v, acc_narrow<DT>(y));
+      if constexpr (VEC)
+        st_stream(orow + u * 16, acc_narrow<DT>(y));
+      else
+        *reinterpret_cast<uint4*>(smem + u * 16) = acc_narrow<DT>(y);
+    }
+    if constexpr (!VEC) {
+      __syncthreads();
+      store_row_any<DT>(orow, smem, 16, hidden);
+      __syncthreads();
     }
   }
 }
 
-// A CTA takes every gridDim-th row and keeps its rows' share of dgamma in
-// its row of `part` (each thread the columns of its own units, so no atomics
-// and a fixed order of the sum).
-template <int N, int DT, bool VEC>
-__global__ void __launch_bounds__(kN8Threads) norm_back8_kernel(const __grid_constant__ Back8Args a) {
-  constexpr int PU = Elem<DT>::kPerUnit;
-  constexpr int ES = Elem<DT>::kSize;
-  extern __shared__ float srow[];  // the summed gradient of the row
+// ---------------------------------------------------------------------------
+// backward.  A CTA takes every gridDim-th row; a thread's columns are the
+// same in every row, so it adds up its share of dgamma with no atomics and
+// in a fixed order, and leaves it in the CTA's row of `part`.
+// ---------------------------------------------------------------------------
+template <int N, int DT>
+__global__ void __launch_bounds__(kN8Threads, 2) back8_reg_kernel(const __grid_constant__ Back8Args a) {
+  constexpr int PU = Elem<DT>::kPerUnit, U = kN8Regs / PU;
   __shared__ float s_part[2][kN8Threads / 32];
-  const size_t hidden = a.hidden;
-  const size_t units = (hidden + PU - 1) / PU;
+  const int units = (int)(a.hidden / PU), tid = threadIdx.x;
+  const size_t nblk = (a.hidden + kCkptBlock - 1) / kCkptBlock;
+  float dg[U][PU];
+#pragma unroll
+  for (int j = 0; j < U; ++j)
+#pragma unroll
+    for (int i = 0; i < PU; ++i) dg[j][i] = 0.f;
+  int flip = 0;
+  for (size_t row = blockIdx.x; row < a.rows; row += gridDim.x, flip ^= 1) {
+    const size_t row_off = row * a.hidden * Elem<DT>::kSize;
+    const float q = __ldg(a.rstd + row);
+    float dy[U][PU], mul[U];
+    uint2 code[U];
+    float acc = 0.f;
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      if (j * kN8Threads >= units) break;
+      const int u = j * kN8Threads + tid;
+      if (u >= units) continue;
+      code[j] = load_codes<DT>(a.codes + row * a.hidden, u, PU, true);
+      mul[j] = pow2((int)__ldg(a.scales + row * nblk + u * PU / kCkptBlock) - 127);
+      Acc s;
+      sum_ranks<N, DT>(a.in, row_off, u, PU, true, s);
+      float h[PU], g[PU];
+      code_floats<DT>(code[j], mul[j], h);
+      load_gamma<DT>(a.gamma, u, PU, true, g);
+#pragma unroll
+      for (int i = 0; i < PU; ++i) {
+        dy[j][i] = __uint_as_float(s.w[i]);
+        const float hq = __fmul_rn(h[i], q);
+        acc = __fmaf_rn(__fmul_rn(dy[j][i], g[i]), hq, acc);
+        dg[j][i] = __fmaf_rn(dy[j][i], hq, dg[j][i]);
+      }
+    }
+    const float mean = block_sum(acc, s_part[flip]) / (float)a.hidden;
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      if (j * kN8Threads >= units) break;
+      const int u = j * kN8Threads + tid;
+      if (u >= units) continue;
+      float h[PU], g[PU];
+      code_floats<DT>(code[j], mul[j], h);
+      load_gamma<DT>(a.gamma, u, PU, true, g);
+      Acc y;
+#pragma unroll
+      for (int i = 0; i < PU; ++i)
+        y.w[i] = __float_as_uint(
+            __fmul_rn(q, __fmaf_rn(-__fmul_rn(h[i], q), mean, __fmul_rn(dy[j][i], g[i]))));
+      const uint4 o = acc_narrow<DT>(y);
+#pragma unroll
+      for (int r = 0; r < N; ++r) st_stream(static_cast<char*>(a.out[r]) + row_off + (size_t)u * 16, o);
+    }
+  }
+  float4* part = reinterpret_cast<float4*>(a.part + (size_t)blockIdx.x * a.pitch);
+#pragma unroll
+  for (int j = 0; j < U; ++j) {
+    const int u = j * kN8Threads + tid;
+    if (u >= units) continue;
+#pragma unroll
+    for (int i = 0; i < PU / 4; ++i)
+      part[u * (PU / 4) + i] = make_float4(dg[j][4 * i], dg[j][4 * i + 1], dg[j][4 * i + 2], dg[j][4 * i + 3]);
+  }
+}
+
+template <int N, int DT>
+__global__ void __launch_bounds__(kN8Threads) back8_gen_kernel(const __grid_constant__ Back8Args a) {
+  constexpr int PU = Elem<DT>::kPerUnit;
+  extern __shared__ __align__(16) char smem[];  // PU float32 per unit: the row's summed gradient
+  __shared__ float s_part[2][kN8Threads / 32];
+  const size_t hidden = a.hidden, units = (hidden + PU - 1) / PU;
   const size_t nblk = (hidden + kCkptBlock - 1) / kCkptBlock;
-  const bool cvec = VEC && hidden % PU == 0;
-  float* dg = a.part + (size_t)blockIdx.x * hidden;
+  const int tid = threadIdx.x;
+  float4* part = reinterpret_cast<float4*>(a.part + (size_t)blockIdx.x * a.pitch);
   int flip = 0;
   bool first = true;
   for (size_t row = blockIdx.x; row < a.rows; row += gridDim.x, flip ^= 1, first = false) {
-    const size_t row_off = row * hidden * ES;
+    const size_t row_off = row * hidden * Elem<DT>::kSize;
     const float q = __ldg(a.rstd + row);
     const uint8_t* crow = a.codes + row * hidden;
-    const uint8_t* srow8 = a.scales + row * nblk;
+    const uint8_t* erow = a.scales + row * nblk;
     float acc = 0.f;
-    for (size_t u = threadIdx.x; u < units; u += kN8Threads) {
-      const int v = unit_valid<DT>(u, hidden);
-      uint4 x[N];
-#pragma unroll
-      for (int k = 0; k < N; ++k) x[k] = load_in<DT, VEC>(static_cast<const char*>(a.in[k]) + row_off, u, v);
-      float f[PU], g[PU];
-      load_codes<DT>(crow, u, v, cvec, f);
-      unit_floats<DT>(load_in<DT, VEC>(a.gamma, u, v), g);
-      const float mul = pow2((int)__ldg(srow8 + u * PU / kCkptBlock) - 127);
+    for (size_t u = tid; u < units; u += kN8Threads) {
+      const int v = a.vec ? PU : unit_valid<DT>(u, hidden);
+      float h[PU], g[PU], d[PU];
+      code_floats<DT>(load_codes<DT>(crow, u, v, a.vec), pow2((int)__ldg(erow + u * PU / kCkptBlock) - 127), h);
+      load_gamma<DT>(a.gamma, u, v, a.vec, g);
       Acc s;
-      acc_init<DT>(s, x[0]);
-#pragma unroll
-      for (int k = 1; k < N; ++k) acc_add<DT>(s, x[k]);
+      sum_ranks<N, DT>(a.in, row_off, u, v, a.vec, s);
+      float4* sm = reinterpret_cast<float4*>(smem + u * PU * 4);
 #pragma unroll
       for (int i = 0; i < PU; ++i) {
-        if (i >= v) break;
-        const float dy = __uint_as_float(s.w[i]);
-        const float h = __fmul_rn(__fmul_rn(f[i], mul), q);
-        srow[u * PU + i] = dy;
-        acc = __fmaf_rn(__fmul_rn(dy, g[i]), h, acc);
-        float* d = dg + u * PU + i;
-        *d = first ? dy * h : __fmaf_rn(dy, h, *d);
+        d[i] = i < v ? __uint_as_float(s.w[i]) : 0.f;
+        h[i] = __fmul_rn(h[i], q);
+        if (i < v) acc = __fmaf_rn(__fmul_rn(d[i], g[i]), h[i], acc);
+      }
+#pragma unroll
+      for (int i = 0; i < PU / 4; ++i) {
+        sm[i] = make_float4(d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3]);
+        float4 t = first ? make_float4(0.f, 0.f, 0.f, 0.f) : part[u * (PU / 4) + i];
+        // columns past the end have d = 0 and are not read again
+        t.x = __fmaf_rn(d[4 * i], h[4 * i], t.x);
+        t.y = __fmaf_rn(d[4 * i + 1], h[4 * i + 1], t.y);
+        t.z = __fmaf_rn(d[4 * i + 2], h[4 * i + 2], t.z);
+        t.w = __fmaf_rn(d[4 * i + 3], h[4 * i + 3], t.w);
+        part[u * (PU / 4) + i] = t;
       }
     }
     const float mean = block_sum(acc, s_part[flip]) / (float)hidden;
-    for (size_t u = threadIdx.x; u < units; u += kN8Threads) {
-      const int v = unit_valid<DT>(u, hidden);
-      float f[PU], g[PU];
-      load_codes<DT>(crow, u, v, cvec, f);
-      unit_floats<DT>(load_in<DT, VEC>(a.gamma, u, v), g);
-      const float mul = pow2((int)__ldg(srow8 + u * PU / kCkptBlock) - 127);
+    for (size_t u = tid; u < units; u += kN8Threads) {
+      const int v = a.vec ? PU : unit_valid<DT>(u, hidden);
+      float h[PU], g[PU];
+      code_floats<DT>(load_codes<DT>(crow, u, v, a.vec), pow2((int)__ldg(erow + u * PU / kCkptBlock) - 127), h);
+      load_gamma<DT>(a.gamma, u, v, a.vec, g);
+      const float* d = reinterpret_cast<const float*>(smem + u * PU * 4);
       Acc y;
 #pragma unroll
-      for (int i = 0; i < PU; ++i) {
-        const float h = __fmul_rn(__fmul_rn(f[i], mul), q);
-        const float w = i < v ? __fmul_rn(srow[u * PU + i], g[i]) : 0.f;
-        y.w[i] = __float_as_uint(__fmul_rn(q, __fmaf_rn(-h, mean, w)));
-      }
+      for (int i = 0; i < PU; ++i)
+        y.w[i] = __float_as_uint(__fmul_rn(q, __fmaf_rn(-__fmul_rn(h[i], q), mean, __fmul_rn(d[i], g[i]))));
       const uint4 o = acc_narrow<DT>(y);
+      if (a.vec) {
 #pragma unroll
-      for (int r = 0; r < N; ++r) store_out<DT, VEC, true>(static_cast<char*>(a.out[r]) + row_off, u, v, o);
+        for (int r = 0; r < N; ++r) st_stream(static_cast<char*>(a.out[r]) + row_off + u * 16, o);
+      } else {
+        *reinterpret_cast<uint4*>(smem + u * PU * 4) = o;
+      }
+    }
+    if (!a.vec) {
+      __syncthreads();
+#pragma unroll
+      for (int r = 0; r < N; ++r) store_row_any<DT>(static_cast<char*>(a.out[r]) + row_off, smem, PU * 4, hidden);
+      __syncthreads();
     }
   }
 }
 
-// dgamma[c] = sum over the CTAs' partial rows, in order: 32 columns x 8
+// dgamma[c] = sum over the CTAs' partial rows, in order: 32 columns x 32
 // strided row groups per CTA.
-__global__ void __launch_bounds__(256) dgamma_join_kernel(const float* part, int parts, size_t hidden, float* dgamma) {
-  __shared__ float red[8][32];
+__global__ void __launch_bounds__(1024) dgamma_join_kernel(const float* part, int parts, size_t pitch, size_t hidden,
+                                                           float* dgamma) {
+  __shared__ float red[32][33];
   const int lane = threadIdx.x & 31, k = threadIdx.x >> 5;
   const size_t c = (size_t)blockIdx.x * 32 + lane;
   float v = 0.f;
-  if (c < hidden)
-    for (int i = k; i < parts; i += 8) v += part[(size_t)i * hidden + c];
+  if (c < hidden) {
+#pragma unroll 4
+    for (int i = k; i < parts; i += 32) v += part[(size_t)i * pitch + c];
+  }
   red[k][lane] = v;
   __syncthreads();
-  if (k == 0 && c < hidden) {
-    for (int i = 1; i < 8; ++i) v += red[i][lane];
-    dgamma[c] = v;
-  }
+  // thread (k, lane) takes row group `lane` of column k: one warp a column
+  float t = red[lane][k];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  const size_t cc = (size_t)blockIdx.x * 32 + k;
+  if (lane == 0 && cc < hidden) dgamma[cc] = t;
 }
 
 // ---------------------------------------------------------------------------
 // launchers
 // ---------------------------------------------------------------------------
 
+constexpr int kN8SmemMax = 210 * 1024;
 static size_t row_smem(size_t hidden) { return (hidden + 7) / 8 * 8 * sizeof(float); }
+static bool fits_regs(int dt, bool vec, size_t hidden) {
+  const size_t pu = dt == RRA_BFLOAT16 ? 8 : 4;
+  return vec && hidden / pu <= kN8Regs / pu * kN8Threads;
+}
 
-template <int N, int DT, bool VEC>
-static cudaError_t save_go(const Save8Args& a, cudaStream_t s) {
-  static const cudaError_t attr = cudaFuncSetAttribute(norm_save8_kernel<N, DT, VEC>,
-                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+template <int N, int DT>
+static cudaError_t save_go(Save8Args a, cudaStream_t s) {
+  if (fits_regs(DT, a.vec, a.hidden)) {
+    save8_reg_kernel<N, DT><<<(unsigned)a.rows, kN8Threads, 0, s>>>(a);
+    return cudaGetLastError();
+  }
+  static const cudaError_t attr =
+      cudaFuncSetAttribute(save8_gen_kernel<N, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kN8SmemMax);
   if (attr != cudaSuccess) return attr;
-  norm_save8_kernel<N, DT, VEC><<<(unsigned)a.rows, kN8Threads, row_smem(a.hidden), s>>>(a);
+  size_t smem = row_smem(a.hidden);
+  if (!a.vec && smem + smem / 4 <= kN8SmemMax) {
+    a.stage_codes = 1;
+    smem += smem / 4;
+  }
+  save8_gen_kernel<N, DT><<<(unsigned)a.rows, kN8Threads, smem, s>>>(a);
   return cudaGetLastError();
 }
 
-template <int N, int DT, bool VEC>
-static cudaError_t back_go(const Back8Args& a, int ctas, cudaStream_t s) {
-  static const cudaError_t attr = cudaFuncSetAttribute(norm_back8_kernel<N, DT, VEC>,
-                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+template <int N, int DT>
+static cudaError_t back_go(const Back8Args& a, int* ctas, cudaStream_t s) {
+  if (fits_regs(DT, a.vec, a.hidden)) {
+    *ctas = *ctas < 2 * device_sms() ? *ctas : 2 * device_sms();
+    back8_reg_kernel<N, DT><<<*ctas, kN8Threads, 0, s>>>(a);
+    return cudaGetLastError();
+  }
+  static const cudaError_t attr =
+      cudaFuncSetAttribute(back8_gen_kernel<N, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kN8SmemMax);
   if (attr != cudaSuccess) return attr;
-  norm_back8_kernel<N, DT, VEC><<<ctas, kN8Threads, row_smem(a.hidden), s>>>(a);
+  back8_gen_kernel<N, DT><<<*ctas, kN8Threads, row_smem(a.hidden), s>>>(a);
   return cudaGetLastError();
 }
 
 template <int N>
-static cudaError_t save_n(int dt, bool vec, const Save8Args& a, cudaStream_t s) {
-  if (dt == RRA_FLOAT32) return vec ? save_go<N, RRA_FLOAT32, true>(a, s) : save_go<N, RRA_FLOAT32, false>(a, s);
-  return vec ? save_go<N, RRA_BFLOAT16, true>(a, s) : save_go<N, RRA_BFLOAT16, false>(a, s);
+static cudaError_t save_n(int dt, const Save8Args& a, cudaStream_t s) {
+  return dt == RRA_FLOAT32 ? save_go<N, RRA_FLOAT32>(a, s) : save_go<N, RRA_BFLOAT16>(a, s);
 }
 
 template <int N>
-static cudaError_t back_n(int dt, bool vec, const Back8Args& a, int ctas, cudaStream_t s) {
-  if (dt == RRA_FLOAT32)
-    return vec ? back_go<N, RRA_FLOAT32, true>(a, ctas, s) : back_go<N, RRA_FLOAT32, false>(a, ctas, s);
-  return vec ? back_go<N, RRA_BFLOAT16, true>(a, ctas, s) : back_go<N, RRA_BFLOAT16, false>(a, ctas, s);
+static cudaError_t back_n(int dt, const Back8Args& a, int* ctas, cudaStream_t s) {
+  return dt == RRA_FLOAT32 ? back_go<N, RRA_FLOAT32>(a, ctas, s) : back_go<N, RRA_BFLOAT16>(a, ctas, s);
 }
 
 cudaError_t launch_norm_save8(int n, int dt, bool vec, const void* const* in, void* const* out, const void* gamma,
@@ -368,17 +646,28 @@ cudaError_t launch_norm_save8(int n, int dt, bool vec, const void* const* in, vo
   a.rows = rows;
   a.hidden = hidden;
   a.eps = eps;
+  a.vec = vec;
   switch (n) {
-    case 1: return save_n<1>(dt, vec, a, s);
-    case 2: return save_n<2>(dt, vec, a, s);
-    case 3: return save_n<3>(dt, vec, a, s);
-    case 4: return save_n<4>(dt, vec, a, s);
-    case 5: return save_n<5>(dt, vec, a, s);
-    case 6: return save_n<6>(dt, vec, a, s);
-    case 7: return save_n<7>(dt, vec, a, s);
-    case 8: return save_n<8>(dt, vec, a, s);
+    case 1: return save_n<1>(dt, a, s);
+    case 2: return save_n<2>(dt, a, s);
+    case 3: return save_n<3>(dt, a, s);
+    case 4: return save_n<4>(dt, a, s);
+    case 5: return save_n<5>(dt, a, s);
+    case 6: return save_n<6>(dt, a, s);
+    case 7: return save_n<7>(dt, a, s);
+    case 8: return save_n<8>(dt, a, s);
     default: return cudaErrorInvalidValue;
   }
+}
+
+template <int DT, bool VEC>
+static cudaError_t restore_go(const uint8_t* c, const uint8_t* e, const float* rstd, const void* gamma, void* out,
+                              size_t rows, size_t hidden, int grid, cudaStream_t s) {
+  static const cudaError_t attr =
+      cudaFuncSetAttribute(restore8_kernel<DT, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, kN8SmemMax);
+  if (attr != cudaSuccess) return attr;
+  restore8_kernel<DT, VEC><<<grid, kN8Threads, VEC ? 0 : row_smem(hidden), s>>>(c, e, rstd, gamma, out, rows, hidden);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_norm_restore8(int dt, bool vec, const void* codes, const void* scales, const float* rstd,
@@ -387,24 +676,19 @@ cudaError_t launch_norm_restore8(int dt, bool vec, const void* codes, const void
   const int grid = (int)(rows < cap ? rows : cap);
   const uint8_t* c = static_cast<const uint8_t*>(codes);
   const uint8_t* e = static_cast<const uint8_t*>(scales);
-  if (dt == RRA_FLOAT32) {
-    if (vec)
-      norm_restore8_kernel<RRA_FLOAT32, true><<<grid, kN8Threads, 0, s>>>(c, e, rstd, gamma, out, rows, hidden);
-    else
-      norm_restore8_kernel<RRA_FLOAT32, false><<<grid, kN8Threads, 0, s>>>(c, e, rstd, gamma, out, rows, hidden);
-  } else {
-    if (vec)
-      norm_restore8_kernel<RRA_BFLOAT16, true><<<grid, kN8Threads, 0, s>>>(c, e, rstd, gamma, out, rows, hidden);
-    else
-      norm_restore8_kernel<RRA_BFLOAT16, false><<<grid, kN8Threads, 0, s>>>(c, e, rstd, gamma, out, rows, hidden);
-  }
-  return cudaGetLastError();
+  if (dt == RRA_FLOAT32)
+    return vec ? restore_go<RRA_FLOAT32, true>(c, e, rstd, gamma, out, rows, hidden, grid, s)
+               : restore_go<RRA_FLOAT32, false>(c, e, rstd, gamma, out, rows, hidden, grid, s);
+  return vec ? restore_go<RRA_BFLOAT16, true>(c, e, rstd, gamma, out, rows, hidden, grid, s)
+             : restore_go<RRA_BFLOAT16, false>(c, e, rstd, gamma, out, rows, hidden, grid, s);
 }
 
 int norm_back8_ctas(size_t rows) {
   const size_t cap = 608;  // 4 per SM of 152
   return (int)(rows < cap ? rows : cap);
 }
+
+size_t norm_back8_pitch(size_t hidden) { return (hidden + 7) / 8 * 8; }
 
 cudaError_t launch_norm_back8(int n, int dt, bool vec, const void* const* grads, void* const* dxs,
                               const void* codes, const void* scales, const float* rstd, const void* gamma,
@@ -419,24 +703,26 @@ cudaError_t launch_norm_back8(int n, int dt, bool vec, const void* const* grads,
   a.scales = static_cast<const uint8_t*>(scales);
   a.rstd = rstd;
   a.part = part;
+  a.pitch = norm_back8_pitch(hidden);
   a.rows = rows;
   a.hidden = hidden;
+  a.vec = vec;
   int ctas = norm_back8_ctas(rows);
   if (max_ctas_cap() > 0 && max_ctas_cap() < ctas) ctas = max_ctas_cap();
   cudaError_t e;
   switch (n) {
-    case 1: e = back_n<1>(dt, vec, a, ctas, s); break;
-    case 2: e = back_n<2>(dt, vec, a, ctas, s); break;
-    case 3: e = back_n<3>(dt, vec, a, ctas, s); break;
-    case 4: e = back_n<4>(dt, vec, a, ctas, s); break;
-    case 5: e = back_n<5>(dt, vec, a, ctas, s); break;
-    case 6: e = back_n<6>(dt, vec, a, ctas, s); break;
-    case 7: e = back_n<7>(dt, vec, a, ctas, s); break;
-    case 8: e = back_n<8>(dt, vec, a, ctas, s); break;
+    case 1: e = back_n<1>(dt, a, &ctas, s); break;
+    case 2: e = back_n<2>(dt, a, &ctas, s); break;
+    case 3: e = back_n<3>(dt, a, &ctas, s); break;
+    case 4: e = back_n<4>(dt, a, &ctas, s); break;
+    case 5: e = back_n<5>(dt, a, &ctas, s); break;
+    case 6: e = back_n<6>(dt, a, &ctas, s); break;
+    case 7: e = back_n<7>(dt, a, &ctas, s); break;
+    case 8: e = back_n<8>(dt, a, &ctas, s); break;
     default: return cudaErrorInvalidValue;
   }
   if (e != cudaSuccess) return e;
-  dgamma_join_kernel<<<(int)((hidden + 31) / 32), 256, 0, s>>>(part, ctas, hidden, dgamma);
+  dgamma_join_kernel<<<(int)((hidden + 31) / 32), 1024, 0, s>>>(part, ctas, a.pitch, hidden, dgamma);
   return cudaGetLastError();
 }
 

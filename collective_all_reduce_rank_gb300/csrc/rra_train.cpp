@@ -264,7 +264,7 @@ rra_status_t rra_rmsnorm_restore8(const void* codes, const void* scales, const f
 }
 
 size_t rra_allreduce_rmsnorm_backward8_workspace_bytes(size_t rows, size_t hidden) {
-  return up((size_t)norm_back8_ctas(rows) * hidden * 4, kAlign);
+  return up((size_t)norm_back8_ctas(rows) * norm_back8_pitch(hidden) * 4, kAlign);
 }
 
 rra_status_t rra_allreduce_rmsnorm_backward8(const void* const* grads, void* const* dxs, int nranks, size_t rows,

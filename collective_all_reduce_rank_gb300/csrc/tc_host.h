@@ -129,6 +129,7 @@ cudaError_t launch_norm_restore8(int dt, bool vec, const void* codes, const void
                                  const void* gamma, void* out, size_t rows, size_t hidden, cudaStream_t s);
 // CTAs of the backward kernel (each leaves one row of dgamma partials)
 int norm_back8_ctas(size_t rows);
+size_t norm_back8_pitch(size_t hidden);  // float32 per row of partials
 cudaError_t launch_norm_back8(int n, int dt, bool vec, const void* const* grads, void* const* dxs,
                               const void* codes, const void* scales, const float* rstd, const void* gamma,
                               float* dgamma, float* part, size_t rows, size_t hidden, cudaStream_t s);

@@ -227,3 +227,71 @@ def test_norm_backward(n, T, D, dtype):
         assert torch.equal(dxs[r], dxs[0])
     chain = (math.ceil(T / 608) + math.ceil(608 / 8) + 8 + n + 3) * ref.F32
     ref.assert_within(dgamma, (dy * h).sum(0), chain * (mag * h.abs()).sum(0) + 1e-40, "dgamma")
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("shift", [0, 1, 3])
+@pytest.mark.parametrize("n,T,D", [(2, 6, 256), (3, 5, 131), (1, 4, 6272)])
+def test_norm_in_place_and_off_16_bytes(n, T, D, shift, dtype):
+    """Buffers that start `shift` elements off 16 bytes, and outputs over
+    their inputs, give the bits of aligned separate buffers."""
+    dt = getattr(torch, dtype)
+    gen = torch.Generator().manual_seed(D + shift)
+    gamma = (1 + 0.1 * torch.randn(D, generator=gen)).to(dt).cuda()
+    xs = [torch.randn(T, D, generator=gen).to(dt).cuda() for _ in range(n)]
+
+    def off(t):
+        room = torch.empty(t.numel() + shift, dtype=t.dtype, device="cuda")
+        room[shift:].copy_(t.reshape(-1))
+        return room[shift:].view(t.shape)
+
+    def saved():
+        return (torch.empty(T, D, dtype=torch.uint8, device="cuda"),
+                torch.empty(T, -(-D // 128), dtype=torch.uint8, device="cuda"), torch.empty(T, device="cuda"))
+
+    want = [torch.empty_like(x) for x in xs]
+    keep = saved()
+    rra.rra_allreduce_rmsnorm_save8(xs, want, gamma, D, *keep)
+    ins, again = [off(x) for x in xs], saved()
+    c = off(again[0])
+    rra.rra_allreduce_rmsnorm_save8(ins, ins, off(gamma), D, c, again[1], again[2])
+    assert all(torch.equal(a, b) for a, b in zip(ins, want))
+    assert torch.equal(c, keep[0]) and torch.equal(again[1], keep[1]) and torch.equal(again[2], keep[2])
+
+    y, y2 = torch.empty_like(xs[0]), off(xs[0])
+    rra.rra_rmsnorm_restore8(*keep, gamma, y)
+    rra.rra_rmsnorm_restore8(c, keep[1], keep[2], off(gamma), y2)
+    assert torch.equal(y, y2)
+
+    dxs, dg, dg2 = [torch.empty_like(x) for x in xs], torch.empty(D, device="cuda"), torch.empty(D, device="cuda")
+    rra.rra_allreduce_rmsnorm_backward8(xs, dxs, *keep, gamma, dg)
+    gs = [off(x) for x in xs]
+    rra.rra_allreduce_rmsnorm_backward8(gs, gs, c, keep[1], keep[2], off(gamma), dg2)
+    # the row's mean may be added in another order: one step of the type
+    for a, b in zip(gs, dxs):
+        half = ref.BF if dtype == "bfloat16" else 32 * ref.F32
+        assert float((a.double() - b.double()).abs().max()) <= 2 * half * float(b.double().abs().max())
+    assert float((dg - dg2).abs().max()) <= 64 * ref.F32 * float(sum(x.double().abs().sum(0).max() for x in xs) * 8)
+
+
+def test_norm_checkpoint_of_extreme_values():
+    """Zeros, subnormals, the type's largest values, infinities and NaN."""
+    D = 384
+    s = torch.zeros(6, D)
+    s[1, :4] = torch.tensor([1e-40, -3e-39, 2.0 ** -133, 1.0e-38])
+    s[2, :3] = torch.tensor([3.3895e38, -1e38, 1e30])
+    s[3, 5], s[3, 6], s[3, 7] = math.inf, -math.inf, 2.5
+    s[4, 130], s[4, 131] = math.nan, -7.0
+    s[5] = torch.linspace(-1e-3, 1e3, D)
+    x = s.cuda()
+    codes = torch.empty(6, D, dtype=torch.float8_e4m3fn, device="cuda")
+    scales, rstd = torch.empty(6, 3, dtype=torch.uint8, device="cuda"), torch.empty(6, device="cuda")
+    rra.rra_allreduce_rmsnorm_save8([x], [torch.empty_like(x)], torch.ones(D, device="cuda"), D, codes, scales, rstd)
+    val, sc = ref.codes_of(s)
+    assert torch.equal(scales.cpu(), sc)
+    val = val.float().double()  # restored values are rounded to float32: a code of 2^128 is infinite there
+    out = torch.empty_like(x)
+    rra.rra_rmsnorm_restore8(codes, scales, None, None, out)
+    got = out.cpu().double()
+    assert torch.equal(torch.isnan(got), torch.isnan(val))
+    assert torch.equal(torch.nan_to_num(got), torch.nan_to_num(val))
