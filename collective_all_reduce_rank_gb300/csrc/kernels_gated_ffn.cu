@@ -47,9 +47,9 @@ struct EpiGateBack {
                                              uint8_t* buf) {
     const TcGroup& g = p.group[x.group];
     const int c0 = x.n * 128 + half * 64;
-    const int row = row0 + (threadIdx.x & 31), rows = g.M - row0;
+    const int rows = g.M - row0;
     const long long off = (long long)row0 * g.ld + c0;
-    const __nv_bfloat16* in = static_cast<const __nv_bfloat16*>(g.in) + (long long)row * g.ld_in + c0;
+    const __nv_bfloat16* in = static_cast<const __nv_bfloat16*>(g.in) + (long long)row0 * g.ld_in + c0;
 #pragma unroll 1
     for (int c = 0; c < 64; c += 32) {
       const int valid = g.N - c0 - c;
@@ -57,7 +57,7 @@ struct EpiGateBack {
       float a[32], b[32], d[32];
       tc_ld32(addr + half * 64 + c, a);
       tc_ld32(addr + 128 + half * 64 + c, b);
-      tc_load_bf16(in + c, d, row < g.M ? valid : 0, g.vec);
+      tc_load_bf16(buf, in + c, g.ld_in, rows, valid, g.vec, d);
       tc_ld_wait();
 #pragma unroll
       for (int j = 0; j < 32; ++j) {

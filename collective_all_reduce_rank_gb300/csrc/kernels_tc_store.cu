@@ -52,22 +52,44 @@ cudaError_t launch_tc_weight_grad(const TcArgs& p, cudaStream_t s, int* grid) {
 
 constexpr int kRowThreads = 256;
 
-__global__ void __launch_bounds__(kRowThreads) join_slots_kernel(const float* slots, int n, long long stride,
-                                                                 __nv_bfloat16* out, long long count) {
-  const long long step = (long long)gridDim.x * kRowThreads;
-  for (long long i = (long long)blockIdx.x * kRowThreads + threadIdx.x; i < count; i += step) {
-    float v = slots[i];
-    for (int k = 1; k < n; ++k) v += slots[k * stride + i];
-    out[i] = __float2bfloat16_rn(v);
+// out[r][c] = bfloat16(sum over the slots), slots' rows ld (a multiple of 8)
+// elements apart; a thread takes 8 columns, a CTA whole rows.
+__global__ void __launch_bounds__(kRowThreads)
+    join_slots_kernel(const float* slots, int n, long long stride, int ld, __nv_bfloat16* out, int rows, int cols,
+                      int vec) {
+  const int units = ld / 8;
+  const long long total = (long long)rows * units, step = (long long)gridDim.x * kRowThreads;
+  for (long long i = (long long)blockIdx.x * kRowThreads + threadIdx.x; i < total; i += step) {
+    const int r = total <= 0xFFFFFFFFll ? (int)((uint32_t)i / (uint32_t)units) : (int)(i / units);
+    const int c = (int)(i - (long long)r * units) * 8;
+    const float4* p = reinterpret_cast<const float4*>(slots + (long long)r * ld + c);
+    float4 a = __ldcs(p), b = __ldcs(p + 1);
+    for (int k = 1; k < n; ++k) {
+      const float4* q = reinterpret_cast<const float4*>(slots + k * stride + (long long)r * ld + c);
+      const float4 x = __ldcs(q), y = __ldcs(q + 1);
+      a = make_float4(a.x + x.x, a.y + x.y, a.z + x.z, a.w + x.w);
+      b = make_float4(b.x + y.x, b.y + y.y, b.z + y.z, b.w + y.w);
+    }
+    __nv_bfloat16* o = out + (long long)r * cols + c;
+    const uint32_t w[4] = {tc_pack2(a.x, a.y), tc_pack2(a.z, a.w), tc_pack2(b.x, b.y), tc_pack2(b.z, b.w)};
+    if (vec && c + 8 <= cols) {
+      *reinterpret_cast<uint4*>(o) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (c + j < cols) reinterpret_cast<uint16_t*>(o)[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+    }
   }
 }
 
-cudaError_t launch_join_slots(const float* slots, int n, long long stride, void* out, long long count,
+cudaError_t launch_join_slots(const float* slots, int n, long long stride, int ld, void* out, int rows, int cols,
                               cudaStream_t s) {
-  const int cap = max_ctas_cap() > 0 ? max_ctas_cap() : device_sms() * 8;
-  const long long want = (count + kRowThreads - 1) / kRowThreads;
-  join_slots_kernel<<<(int)(want < cap ? want : cap), kRowThreads, 0, s>>>(slots, n, stride,
-                                                                          static_cast<__nv_bfloat16*>(out), count);
+  const long long cap = max_ctas_cap() > 0 ? max_ctas_cap() : device_sms() * 8;
+  const long long want = ((long long)rows * (ld / 8) + kRowThreads - 1) / kRowThreads;
+  const int vec = cols % 8 == 0 && ((uintptr_t)out & 15) == 0;
+  join_slots_kernel<<<(int)(want < cap ? want : cap), kRowThreads, 0, s>>>(slots, n, stride, ld,
+                                                                          static_cast<__nv_bfloat16*>(out), rows, cols,
+                                                                          vec);
   return cudaGetLastError();
 }
 

@@ -68,6 +68,7 @@ struct Bump {
   }
 };
 
+size_t slot_ld(size_t hidden) { return up(hidden, 8); }  // float32 rows of dx's parts
 bool padded(size_t hidden) { return hidden % 8 != 0; }
 size_t pad_ld(size_t hidden) { return up(hidden, 64); }  // rows of whole 128-byte lines
 
@@ -322,7 +323,7 @@ size_t ffn_bytes(int n, size_t T, size_t D, size_t F, bool back) {
     for (int i = 0; i < 2 * n; ++i) b.take(T * up(F, 64) * 2);
     const size_t kb = 2 * (size_t)n * ((F + 63) / 64);
     const int splits = pick_splits(T, D, kb);
-    if (splits > 1) b.take((size_t)splits * T * D * 4);
+    if (splits > 1) b.take((size_t)splits * T * slot_ld(D) * 4);
   }
   return b.at;
 }
@@ -465,7 +466,7 @@ rra_status_t rra_gated_ffn_backward(const void* x, const void* const* gates, con
   for (int i = 0; i < 2 * nranks; ++i) dW[i] = Mat{ws.take(T * ldf * 2), T, F, ldf};
   const size_t kb_seg = (F + 63) / 64, kb = 2 * (size_t)nranks * kb_seg;
   const int splits = pick_splits(T, D, kb);
-  float* slots = splits > 1 ? static_cast<float*>(ws.take((size_t)splits * T * D * 4)) : nullptr;
+  float* slots = splits > 1 ? static_cast<float*>(ws.take((size_t)splits * T * slot_ld(D) * 4)) : nullptr;
   if (!place.launch(s)) return done(call, nranks, count, dtype, 0, RRA_ERR_CUDA);
 
   // dg, du
@@ -504,19 +505,19 @@ rra_status_t rra_gated_ffn_backward(const void* x, const void* const* gates, con
   }
   p->kblocks = (int)kb;
   p->splits = splits;
-  p->split_stride = (long long)(T * D);
+  p->split_stride = (long long)(T * slot_ld(D));
   TcGroup g{};
   g.M = (int)T;
   g.N = (int)D;
-  g.ld = (long long)D;
+  g.ld = (long long)(splits > 1 ? slot_ld(D) : D);
   g.out = splits > 1 ? (void*)slots : dx;
-  g.vec = splits > 1 ? D % 4 == 0 : aligned(dx, 16) && D % 8 == 0;
+  g.vec = splits > 1 || (aligned(dx, 16) && D % 8 == 0);
   ok = ok && add_group(p.get(), g, false);
   p->status = device_status();
   if (!ok) return done(call, nranks, count, dtype, 0, RRA_ERR_CUDA);
   e = launch_tc_input_grad(*p, splits > 1, s, &grid);
   if (e == cudaSuccess && splits > 1)
-    e = launch_join_slots(slots, splits, (long long)(T * D), dx, (long long)(T * D), s);
+    e = launch_join_slots(slots, splits, (long long)(T * slot_ld(D)), (int)slot_ld(D), dx, (int)T, (int)D, s);
   if (e != cudaSuccess) return done(call, nranks, count, dtype, grid, RRA_ERR_CUDA);
 
   // dG, dU
@@ -598,7 +599,7 @@ LossPlan loss_plan(int n, size_t T, size_t D, const size_t* vocab, bool back, si
   for (;; --piece) {
     q.splits = pick_splits(T, D, piece * 4);
     q.slots = piece < tiles || q.splits > 1 ? (size_t)q.splits : 0;
-    q.fixed = base + (q.slots ? up(q.slots * T * D * 4, kAlign) : 0);
+    q.fixed = base + (q.slots ? up(q.slots * T * slot_ld(D) * 4, kAlign) : 0);
     q.piece_tiles = piece;
     if (piece == 1 || room == SIZE_MAX || q.fixed + piece * col <= room) break;
     // jump to what the room allows at most
@@ -765,7 +766,7 @@ rra_status_t rra_vocab_loss_backward(const void* x, const void* const* weights, 
   for (int r = 0; r < nranks; ++r) W[r] = place(weights[r], vocab[r], D);
   bool ok = place.launch(s);
   if (!ok) return done(call, nranks, T * V, dtype, 0, RRA_ERR_CUDA);
-  float* slots = q.slots ? static_cast<float*>(ws.take(q.slots * T * D * 4)) : nullptr;
+  float* slots = q.slots ? static_cast<float*>(ws.take(q.slots * T * slot_ld(D) * 4)) : nullptr;
   char* dl = ws.base + ws.at;
   const size_t ld = q.piece_tiles * 256;
 
@@ -831,14 +832,14 @@ rra_status_t rra_vocab_loss_backward(const void* x, const void* const* weights, 
     }
     p->kblocks = (int)kb;
     p->splits = (int)std::max<size_t>(1, std::min<size_t>((size_t)q.splits, kb));
-    p->split_stride = (long long)(T * D);
+    p->split_stride = (long long)(T * slot_ld(D));
     p->accumulate = t0 > 0;
     TcGroup g{};
     g.M = (int)T;
     g.N = (int)D;
-    g.ld = (long long)D;
+    g.ld = (long long)(q.slots ? slot_ld(D) : D);
     g.out = q.slots ? (void*)slots : dx;
-    g.vec = q.slots ? D % 4 == 0 : aligned(dx, 16) && D % 8 == 0;
+    g.vec = q.slots || (aligned(dx, 16) && D % 8 == 0);
     ok = ok && add_group(p.get(), g, false);
     p->status = device_status();
     if (!ok) return done(call, nranks, T * V, dtype, 0, RRA_ERR_CUDA);
@@ -867,7 +868,7 @@ rra_status_t rra_vocab_loss_backward(const void* x, const void* const* weights, 
     e = launch_tc_weight_grad(*p, s, &grid);
   }
   if (e == cudaSuccess && q.slots)
-    e = launch_join_slots(slots, q.splits, (long long)(T * D), dx, (long long)(T * D), s);
+    e = launch_join_slots(slots, q.splits, (long long)(T * slot_ld(D)), (int)slot_ld(D), dx, (int)T, (int)D, s);
   return done(call, nranks, T * V, dtype, grid, cuda_st(e));
 }
 

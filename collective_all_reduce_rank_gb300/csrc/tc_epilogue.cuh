@@ -54,23 +54,25 @@ __device__ __forceinline__ void tc_flush_bf16(const uint8_t* buf, __nv_bfloat16*
       }
     }
   } else {
-    // rows of any alignment: pairs of elements in 4-byte stores, shifted by
-    // one element in the rows that start between two of them
-    const uint16_t* e = reinterpret_cast<const uint16_t*>(buf);
+    // rows of any alignment: lane l holds elements 2l and 2l + 1 as one
+    // word; in a row that starts between two words of memory every lane
+    // takes its second element and its neighbour's first instead
     const int top = rows < 32 ? rows : 32;
+    const uint8_t* src = buf + ((lane & 3) << 2);
+    uint16_t* o = reinterpret_cast<uint16_t*>(dst);
+    const int j0 = 2 * lane;
 #pragma unroll 4
-    for (int r = 0; r < top; ++r) {
-      uint16_t* o = reinterpret_cast<uint16_t*>(dst + r * ld);
+    for (int r = 0; r < top; ++r, o += ld) {
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(src + r * 128 + (((lane >> 2) ^ (r & 7)) << 4));
+      const uint32_t next = __shfl_down_sync(0xffffffffu, w, 1);
       const int odd = (int)(((uintptr_t)o >> 1) & 1);
-      const int j = 2 * lane + odd;
-      const uint16_t a = j < 64 ? e[r * 64 + (((j >> 3) ^ (r & 7)) << 3) + (j & 7)] : 0;
-      const int k = j + 1;
-      const uint16_t b = k < 64 ? e[r * 64 + (((k >> 3) ^ (r & 7)) << 3) + (k & 7)] : 0;
-      if (k < valid && k < 64)
-        *reinterpret_cast<uint32_t*>(o + j) = (uint32_t)a | ((uint32_t)b << 16);
-      else if (j < valid && j < 64)
-        o[j] = a;
-      if (odd && lane == 0 && valid > 0) o[0] = e[r * 64 + ((r & 7) << 3)];
+      const int j = j0 + odd;
+      const uint32_t v = odd ? __funnelshift_r(w, next, 16) : w;
+      if (j + 1 < valid && j < 63)
+        *reinterpret_cast<uint32_t*>(o + j) = v;
+      else if (j < valid)
+        o[j] = (uint16_t)v;
+      if (odd && lane == 0 && valid > 0) o[0] = (uint16_t)w;
     }
   }
   __syncwarp();
@@ -131,23 +133,46 @@ __device__ __forceinline__ void tc_store_f32(uint8_t* buf, const float* v, float
   __syncwarp();
 }
 
-// Load 32 bfloat16 (zeros from `valid` on).
-__device__ __forceinline__ void tc_load_bf16(const __nv_bfloat16* src, float* v, int valid, bool vec) {
+// Load 32 rows of 32 bfloat16 (zeros outside `rows` x `valid`), each lane its
+// row's, through the staging buffer so that the loads cover whole rows.
+__device__ __forceinline__ void tc_load_bf16(uint8_t* buf, const __nv_bfloat16* src, long long ld, int rows, int valid,
+                                             bool vec, float* v) {
+  const int lane = threadIdx.x & 31;
+  if (vec && valid >= 32) {
+    uint4 u[4];
 #pragma unroll
-  for (int c = 0; c < 32; c += 8) {
-    if (vec && c + 8 <= valid) {
-      const uint4 u = __ldg(reinterpret_cast<const uint4*>(src + c));
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    for (int i = 0; i < 4; ++i) {
+      const int r = i * 8 + (lane >> 2);
+      u[i] = r < rows ? __ldg(reinterpret_cast<const uint4*>(src + r * ld + 8 * (lane & 3))) : make_uint4(0u, 0u, 0u, 0u);
+    }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[c + 2 * j] = __uint_as_float(w[j] << 16);
-        v[c + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[c + j] = c + j < valid ? __bfloat162float(src[c + j]) : 0.f;
+    for (int i = 0; i < 4; ++i) {
+      const int r = i * 8 + (lane >> 2);
+      *reinterpret_cast<uint4*>(buf + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4)) = u[i];
+    }
+  } else {
+    const int c = 2 * (lane & 15);
+#pragma unroll 4
+    for (int i = 0; i < 16; ++i) {
+      const int r = 2 * i + (lane >> 4);
+      const uint16_t* p = reinterpret_cast<const uint16_t*>(src) + r * ld + c;
+      const uint32_t a = r < rows && c < valid ? __ldg(p) : 0u;
+      const uint32_t b = r < rows && c + 1 < valid ? __ldg(p + 1) : 0u;
+      *reinterpret_cast<uint32_t*>(buf + r * 64 + (((c >> 3) ^ ((r >> 1) & 3)) << 4) + 2 * (c & 7)) = a | (b << 16);
     }
   }
+  __syncwarp();
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const uint4 q = *reinterpret_cast<const uint4*>(buf + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4));
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[8 * c + 2 * j] = __uint_as_float(w[j] << 16);
+      v[8 * c + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    }
+  }
+  __syncwarp();
 }
 
 }  // namespace rra

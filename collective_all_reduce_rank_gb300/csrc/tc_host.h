@@ -106,8 +106,8 @@ cudaError_t launch_skinny_lse(const SkinnyArgs& a, cudaStream_t s, int* grid);
 cudaError_t launch_loss_join(const float2* part, int parts, const float* hit, const long long* targets,
                              long long ignore_index, const void* x, const void* const* w, const size_t* vocab, int n,
                              size_t hidden, int rows, float* loss, float* lse, cudaStream_t s);
-// out[i] = bfloat16(sum over s of slots[s * stride + i])
-cudaError_t launch_join_slots(const float* slots, int n, long long stride, void* out, long long count,
+// out[r][c] = bfloat16(sum over k < n of slots[k * stride + r * ld + c])
+cudaError_t launch_join_slots(const float* slots, int n, long long stride, int ld, void* out, int rows, int cols,
                               cudaStream_t s);
 // Rows of `cols` elements of each src to rows of 8 * units elements of dst.
 struct PadArgs {
