@@ -106,12 +106,17 @@ struct EpiDlogits {
         float v[32];
         tc_ld32(addr + half * 128 + c + k, v);
         tc_ld_ready(v);
-        const long long q = t - c - k;
-        const int d = q >= 0 && q < 32 ? (int)q : -1;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const float e = tc_exp2(fmaf(v[j], kLog2e, -base)) - (j == d ? 1.f : 0.f);
-          v[j] = live ? e * w : 0.f;
+        for (int j = 0; j < 32; ++j) v[j] = tc_exp2(fmaf(v[j], kLog2e, -base)) * w;
+        const long long d = t - c - k;
+        if (d >= 0 && d < 32) {  // the target's column, in one chunk of a row
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            asm("{\n.reg .pred p;\nsetp.eq.s32 p, %1, %2;\n@p sub.f32 %0, %0, %3;\n}\n" : "+f"(v[j]) : "r"((int)d), "r"(j), "f"(w));
+        }
+        if (!live) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = 0.f;
         }
         tc_stage_bf16(buf, v, k / 8);
       }

@@ -57,22 +57,48 @@ __device__ __forceinline__ void tc_flush_bf16(const uint8_t* buf, __nv_bfloat16*
     // rows of any alignment: lane l holds elements 2l and 2l + 1 as one
     // word; in a row that starts between two words of memory every lane
     // takes its second element and its neighbour's first instead
-    const int top = rows < 32 ? rows : 32;
     const uint8_t* src = buf + ((lane & 3) << 2);
     uint16_t* o = reinterpret_cast<uint16_t*>(dst);
-    const int j0 = 2 * lane;
-#pragma unroll 4
-    for (int r = 0; r < top; ++r, o += ld) {
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(src + r * 128 + (((lane >> 2) ^ (r & 7)) << 4));
-      const uint32_t next = __shfl_down_sync(0xffffffffu, w, 1);
-      const int odd = (int)(((uintptr_t)o >> 1) & 1);
-      const int j = j0 + odd;
-      const uint32_t v = odd ? __funnelshift_r(w, next, 16) : w;
-      if (j + 1 < valid && j < 63)
-        *reinterpret_cast<uint32_t*>(o + j) = v;
-      else if (j < valid)
-        o[j] = (uint16_t)v;
-      if (odd && lane == 0 && valid > 0) o[0] = (uint16_t)w;
+    if (rows >= 32 && valid >= 64) {
+      // whole block: 8 rows at a time, so that the shared-memory reads, the
+      // shuffles and the stores of different rows overlap
+      const bool edge = lane == 0 || lane == 31;
+#pragma unroll 1
+      for (int r0 = 0; r0 < 32; r0 += 8) {
+        uint32_t w[8], v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          w[i] = *reinterpret_cast<const uint32_t*>(src + (r0 + i) * 128 + (((lane >> 2) ^ i) << 4));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __funnelshift_r(w[i], __shfl_down_sync(0xffffffffu, w[i], 1), 16);
+#pragma unroll
+        for (int i = 0; i < 8; ++i, o += ld) {
+          // stores under predicates, not branches, so that the rows stay in flight together
+          const uint32_t odd = ((uint32_t)(uintptr_t)o >> 1) & 1;
+          asm volatile(
+              "{\n.reg .pred p, q;\n"
+              "setp.ne.u32 p, %2, 0;\n@p st.global.u32 [%0], %1;\n"
+              "setp.ne.u32 q, %5, 0;\n@q st.global.u16 [%3], %4;\n}\n" ::"l"(o + 2 * lane + odd),
+              "r"(odd ? v[i] : w[i]), "r"((uint32_t)(lane < 31 || !odd)), "l"(o + (lane == 0 ? 0 : 63)),
+              "h"((uint16_t)(lane == 0 ? w[i] : w[i] >> 16)), "r"((uint32_t)(odd && edge))
+              : "memory");
+        }
+      }
+    } else {
+      const int top = rows < 32 ? rows : 32;
+      const int j0 = 2 * lane;
+      for (int r = 0; r < top; ++r, o += ld) {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(src + r * 128 + (((lane >> 2) ^ (r & 7)) << 4));
+        const uint32_t next = __shfl_down_sync(0xffffffffu, w, 1);
+        const int odd = (int)(((uintptr_t)o >> 1) & 1);
+        const int j = j0 + odd;
+        const uint32_t v = odd ? __funnelshift_r(w, next, 16) : w;
+        if (j + 1 < valid && j < 63)
+          *reinterpret_cast<uint32_t*>(o + j) = v;
+        else if (j < valid)
+          o[j] = (uint16_t)v;
+        if (odd && lane == 0 && valid > 0) o[0] = (uint16_t)w;
+      }
     }
   }
   __syncwarp();
