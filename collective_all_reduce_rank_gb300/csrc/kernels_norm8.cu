@@ -30,11 +30,13 @@
 #include <cuda_fp8.h>
 
 #include "common.cuh"
+#include "pdl.cuh"
 #include "tc_host.h"
 
 namespace rra {
 
 constexpr int kN8Threads = 256;
+constexpr int kN8MaxThreads = 320;           // backward of long or unaligned rows
 constexpr int kN8Regs = 24;                  // float32 of a row a thread keeps
 constexpr float kBf16Max = 3.3895314e38f;    // largest finite bfloat16
 
@@ -117,8 +119,12 @@ __device__ __forceinline__ float block_sum(float v, float* part) {
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
   __syncthreads();
   float t = 0.f;
+  if (blockDim.x == kN8Threads) {
 #pragma unroll
-  for (int w = 0; w < kN8Threads / 32; ++w) t += part[w];
+    for (int w = 0; w < kN8Threads / 32; ++w) t += part[w];
+  } else {
+    for (int w = 0; w < (int)blockDim.x / 32; ++w) t += part[w];
+  }
   return t;
 }
 
@@ -230,14 +236,14 @@ __device__ __forceinline__ void put_codes(uint8_t* c, uint2 w, int valid, bool v
 template <int DT>
 __device__ __forceinline__ void store_row_any(char* dst, const char* units, int stride, size_t hidden) {
   if constexpr (Elem<DT>::kSize == 4) {
-    for (size_t i = threadIdx.x; i < hidden; i += kN8Threads)
+    for (size_t i = threadIdx.x; i < hidden; i += blockDim.x)
       reinterpret_cast<uint32_t*>(dst)[i] = *reinterpret_cast<const uint32_t*>(units + (i >> 2) * stride + (i & 3) * 4);
   } else {
     auto at = [&](size_t i) { return *reinterpret_cast<const uint16_t*>(units + (i >> 3) * stride + (i & 7) * 2); };
     uint16_t* o = reinterpret_cast<uint16_t*>(dst);
     const size_t head = ((uintptr_t)dst >> 1) & 1;  // one element before the first whole word
     if (threadIdx.x == 0 && head) o[0] = at(0);
-    for (size_t i = head + 2 * threadIdx.x; i < hidden; i += 2 * kN8Threads) {
+    for (size_t i = head + 2 * threadIdx.x; i < hidden; i += 2 * blockDim.x) {
       if (i + 1 < hidden)
         *reinterpret_cast<uint32_t*>(o + i) = (uint32_t)at(i) | ((uint32_t)at(i + 1) << 16);
       else
@@ -258,6 +264,8 @@ __global__ void __launch_bounds__(kN8Threads) save8_reg_kernel(const __grid_cons
   const size_t nblk = (a.hidden + kCkptBlock - 1) / kCkptBlock;
   float f[U][PU];
   float ss = 0.f;
+  pdl_wait();
+  pdl_next();
 #pragma unroll
   for (int j = 0; j < U; ++j) {
     if (j * kN8Threads >= units) break;
@@ -309,6 +317,8 @@ __global__ void __launch_bounds__(kN8Threads) save8_gen_kernel(const __grid_cons
   uint8_t* crow = a.codes + row * hidden;
   uint8_t* cstage = reinterpret_cast<uint8_t*>(smem + units * PU * 4);
   float ss = 0.f;
+  pdl_wait();
+  pdl_next();
   for (size_t u0 = 0; u0 < units; u0 += kN8Threads) {
     const size_t u = u0 + tid;
     const int v = u < units ? unit_valid<DT>(u, hidden) : 0;
@@ -383,6 +393,8 @@ __global__ void __launch_bounds__(kN8Threads)
   extern __shared__ __align__(16) char smem[];
   const size_t units = (hidden + PU - 1) / PU;
   const size_t nblk = (hidden + kCkptBlock - 1) / kCkptBlock;
+  pdl_wait();
+  pdl_next();
   for (size_t row = blockIdx.x; row < rows; row += gridDim.x) {
     const float q = rstd ? __ldg(rstd + row) : 1.f;
     char* orow = static_cast<char*>(out) + row * hidden * Elem<DT>::kSize;
@@ -429,6 +441,8 @@ __global__ void __launch_bounds__(kN8Threads, 2) back8_reg_kernel(const __grid_c
 #pragma unroll
     for (int i = 0; i < PU; ++i) dg[j][i] = 0.f;
   int flip = 0;
+  pdl_wait();
+  pdl_next();
   for (size_t row = blockIdx.x; row < a.rows; row += gridDim.x, flip ^= 1) {
     const size_t row_off = row * a.hidden * Elem<DT>::kSize;
     const float q = __ldg(a.rstd + row);
@@ -486,23 +500,25 @@ __global__ void __launch_bounds__(kN8Threads, 2) back8_reg_kernel(const __grid_c
 }
 
 template <int N, int DT>
-__global__ void __launch_bounds__(kN8Threads) back8_gen_kernel(const __grid_constant__ Back8Args a) {
+__global__ void __launch_bounds__(kN8MaxThreads) back8_gen_kernel(const __grid_constant__ Back8Args a) {
   constexpr int PU = Elem<DT>::kPerUnit;
   extern __shared__ __align__(16) char smem[];  // PU float32 per unit: the row's summed gradient
-  __shared__ float s_part[2][kN8Threads / 32];
+  __shared__ float s_part[2][kN8MaxThreads / 32];
   const size_t hidden = a.hidden, units = (hidden + PU - 1) / PU;
   const size_t nblk = (hidden + kCkptBlock - 1) / kCkptBlock;
   const int tid = threadIdx.x;
   float4* part = reinterpret_cast<float4*>(a.part + (size_t)blockIdx.x * a.pitch);
   int flip = 0;
   bool first = true;
+  pdl_wait();
+  pdl_next();
   for (size_t row = blockIdx.x; row < a.rows; row += gridDim.x, flip ^= 1, first = false) {
     const size_t row_off = row * hidden * Elem<DT>::kSize;
     const float q = __ldg(a.rstd + row);
     const uint8_t* crow = a.codes + row * hidden;
     const uint8_t* erow = a.scales + row * nblk;
     float acc = 0.f;
-    for (size_t u = tid; u < units; u += kN8Threads) {
+    for (size_t u = tid; u < units; u += blockDim.x) {
       const int v = a.vec ? PU : unit_valid<DT>(u, hidden);
       float h[PU], g[PU], d[PU];
       code_floats<DT>(load_codes<DT>(crow, u, v, a.vec), pow2((int)__ldg(erow + u * PU / kCkptBlock) - 127), h);
@@ -529,7 +545,7 @@ __global__ void __launch_bounds__(kN8Threads) back8_gen_kernel(const __grid_cons
       }
     }
     const float mean = block_sum(acc, s_part[flip]) / (float)hidden;
-    for (size_t u = tid; u < units; u += kN8Threads) {
+    for (size_t u = tid; u < units; u += blockDim.x) {
       const int v = a.vec ? PU : unit_valid<DT>(u, hidden);
       float h[PU], g[PU];
       code_floats<DT>(load_codes<DT>(crow, u, v, a.vec), pow2((int)__ldg(erow + u * PU / kCkptBlock) - 127), h);
@@ -564,6 +580,8 @@ __global__ void __launch_bounds__(1024) dgamma_join_kernel(const float* part, in
   const int lane = threadIdx.x & 31, k = threadIdx.x >> 5;
   const size_t c = (size_t)blockIdx.x * 32 + lane;
   float v = 0.f;
+  pdl_wait();
+  pdl_next();
   if (c < hidden) {
 #pragma unroll 4
     for (int i = k; i < parts; i += 32) v += part[(size_t)i * pitch + c];
@@ -592,8 +610,7 @@ static bool fits_regs(int dt, bool vec, size_t hidden) {
 template <int N, int DT>
 static cudaError_t save_go(Save8Args a, cudaStream_t s) {
   if (fits_regs(DT, a.vec, a.hidden)) {
-    save8_reg_kernel<N, DT><<<(unsigned)a.rows, kN8Threads, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_pdl(save8_reg_kernel<N, DT>, (int)a.rows, kN8Threads, 0, s, a);
   }
   static const cudaError_t attr =
       cudaFuncSetAttribute(save8_gen_kernel<N, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kN8SmemMax);
@@ -603,22 +620,23 @@ static cudaError_t save_go(Save8Args a, cudaStream_t s) {
     a.stage_codes = 1;
     smem += smem / 4;
   }
-  save8_gen_kernel<N, DT><<<(unsigned)a.rows, kN8Threads, smem, s>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(save8_gen_kernel<N, DT>, (int)a.rows, kN8Threads, smem, s, a);
 }
 
 template <int N, int DT>
 static cudaError_t back_go(const Back8Args& a, int* ctas, cudaStream_t s) {
   if (fits_regs(DT, a.vec, a.hidden)) {
     *ctas = *ctas < 2 * device_sms() ? *ctas : 2 * device_sms();
-    back8_reg_kernel<N, DT><<<*ctas, kN8Threads, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_pdl(back8_reg_kernel<N, DT>, *ctas, kN8Threads, 0, s, a);
   }
   static const cudaError_t attr =
       cudaFuncSetAttribute(back8_gen_kernel<N, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kN8SmemMax);
   if (attr != cudaSuccess) return attr;
-  back8_gen_kernel<N, DT><<<*ctas, kN8Threads, row_smem(a.hidden), s>>>(a);
-  return cudaGetLastError();
+  // as few trips over a row as kN8MaxThreads allow, all of them full
+  const int units = (int)((a.hidden + 16 / Elem<DT>::kSize - 1) / (16 / Elem<DT>::kSize));
+  const int trips = (units + kN8MaxThreads - 1) / kN8MaxThreads;
+  const int threads = ((units + trips - 1) / trips + 31) / 32 * 32;
+  return launch_pdl(back8_gen_kernel<N, DT>, *ctas, threads, row_smem(a.hidden), s, a);
 }
 
 template <int N>
@@ -666,8 +684,8 @@ static cudaError_t restore_go(const uint8_t* c, const uint8_t* e, const float* r
   static const cudaError_t attr =
       cudaFuncSetAttribute(restore8_kernel<DT, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, kN8SmemMax);
   if (attr != cudaSuccess) return attr;
-  restore8_kernel<DT, VEC><<<grid, kN8Threads, VEC ? 0 : row_smem(hidden), s>>>(c, e, rstd, gamma, out, rows, hidden);
-  return cudaGetLastError();
+  return launch_pdl(restore8_kernel<DT, VEC>, grid, kN8Threads, VEC ? 0 : row_smem(hidden), s, c, e, rstd, gamma, out,
+                    rows, hidden);
 }
 
 cudaError_t launch_norm_restore8(int dt, bool vec, const void* codes, const void* scales, const float* rstd,
@@ -722,8 +740,7 @@ cudaError_t launch_norm_back8(int n, int dt, bool vec, const void* const* grads,
     default: return cudaErrorInvalidValue;
   }
   if (e != cudaSuccess) return e;
-  dgamma_join_kernel<<<(int)((hidden + 31) / 32), 1024, 0, s>>>(part, ctas, a.pitch, hidden, dgamma);
-  return cudaGetLastError();
+  return launch_pdl(dgamma_join_kernel, (int)((hidden + 31) / 32), 1024, 0, s, part, ctas, a.pitch, hidden, dgamma);
 }
 
 }  // namespace rra

@@ -26,6 +26,7 @@
 #include <cstdint>
 
 #include "act.cuh"
+#include "pdl.cuh"
 #include "tc_host.h"
 
 namespace rra {
@@ -164,6 +165,8 @@ __global__ void __launch_bounds__(kSkThreads, 2) skinny_gate_kernel(const __grid
   const int g = (threadIdx.x & 31) >> 2;
   const int per = (a.width + 7) / 8;  // units per rank
   const size_t bytes = (size_t)a.width * a.hidden * 2;
+  pdl_wait();
+  pdl_next();
   for (int u = blockIdx.x; u < a.units; u += gridDim.x) {
     const int r = u / per, f0 = (u - r * per) * 8;
     const char* gb = static_cast<const char*>(a.w[2 * r]);
@@ -193,6 +196,8 @@ __global__ void __launch_bounds__(kSkThreads, 2) skinny_lse_kernel(const __grid_
   const int lane = threadIdx.x & 31, g = lane >> 2;
   const int slot = threadIdx.x / (8 * NT), token = threadIdx.x % (8 * NT);  // row slot of the unit, token
   const bool mine = slot < 16 && token < a.tokens;
+  pdl_wait();
+  pdl_next();
   long long target = -1;
   if (mine) {
     target = a.targets[token];
@@ -248,38 +253,24 @@ int skinny_grid(long long units) {
 }
 
 template <int NT, bool VEC>
-static void gate_go(const SkinnyArgs& a, int act, int grid, cudaStream_t s) {
-  if (act == RRA_ACT_SILU)
-    skinny_gate_kernel<NT, VEC, RRA_ACT_SILU><<<grid, kSkThreads, 0, s>>>(a);
-  else
-    skinny_gate_kernel<NT, VEC, RRA_ACT_GELU_TANH><<<grid, kSkThreads, 0, s>>>(a);
+static cudaError_t gate_go(const SkinnyArgs& a, int act, int grid, cudaStream_t s) {
+  if (act == RRA_ACT_SILU) return launch_pdl(skinny_gate_kernel<NT, VEC, RRA_ACT_SILU>, grid, kSkThreads, 0, s, a);
+  return launch_pdl(skinny_gate_kernel<NT, VEC, RRA_ACT_GELU_TANH>, grid, kSkThreads, 0, s, a);
 }
 
 cudaError_t launch_skinny_gate(const SkinnyArgs& a, int act, cudaStream_t s, int* grid) {
   *grid = skinny_grid(a.units);
   const bool vec = a.hidden % 8 == 0;  // the matrices themselves are 16-byte aligned
-  if (a.tokens <= 8)
-    vec ? gate_go<1, true>(a, act, *grid, s) : gate_go<1, false>(a, act, *grid, s);
-  else
-    vec ? gate_go<2, true>(a, act, *grid, s) : gate_go<2, false>(a, act, *grid, s);
-  return cudaGetLastError();
+  if (a.tokens <= 8) return vec ? gate_go<1, true>(a, act, *grid, s) : gate_go<1, false>(a, act, *grid, s);
+  return vec ? gate_go<2, true>(a, act, *grid, s) : gate_go<2, false>(a, act, *grid, s);
 }
 
 cudaError_t launch_skinny_lse(const SkinnyArgs& a, cudaStream_t s, int* grid) {
   *grid = skinny_grid(a.units);
   const bool vec = a.hidden % 8 == 0;
-  if (a.tokens <= 8) {
-    if (vec)
-      skinny_lse_kernel<1, true><<<*grid, kSkThreads, 0, s>>>(a);
-    else
-      skinny_lse_kernel<1, false><<<*grid, kSkThreads, 0, s>>>(a);
-  } else {
-    if (vec)
-      skinny_lse_kernel<2, true><<<*grid, kSkThreads, 0, s>>>(a);
-    else
-      skinny_lse_kernel<2, false><<<*grid, kSkThreads, 0, s>>>(a);
-  }
-  return cudaGetLastError();
+  if (a.tokens <= 8)
+    return launch_pdl(vec ? skinny_lse_kernel<1, true> : skinny_lse_kernel<1, false>, *grid, kSkThreads, 0, s, a);
+  return launch_pdl(vec ? skinny_lse_kernel<2, true> : skinny_lse_kernel<2, false>, *grid, kSkThreads, 0, s, a);
 }
 
 }  // namespace rra

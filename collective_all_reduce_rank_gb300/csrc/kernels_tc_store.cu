@@ -57,6 +57,8 @@ constexpr int kRowThreads = 256;
 __global__ void __launch_bounds__(kRowThreads)
     join_slots_kernel(const float* slots, int n, long long stride, int ld, __nv_bfloat16* out, int rows, int cols,
                       int vec) {
+  pdl_wait();
+  pdl_next();
   const int units = ld / 8;
   const long long total = (long long)rows * units, step = (long long)gridDim.x * kRowThreads;
   for (long long i = (long long)blockIdx.x * kRowThreads + threadIdx.x; i < total; i += step) {
@@ -87,15 +89,15 @@ cudaError_t launch_join_slots(const float* slots, int n, long long stride, int l
   const long long cap = max_ctas_cap() > 0 ? max_ctas_cap() : device_sms() * 8;
   const long long want = ((long long)rows * (ld / 8) + kRowThreads - 1) / kRowThreads;
   const int vec = cols % 8 == 0 && ((uintptr_t)out & 15) == 0;
-  join_slots_kernel<<<(int)(want < cap ? want : cap), kRowThreads, 0, s>>>(slots, n, stride, ld,
-                                                                          static_cast<__nv_bfloat16*>(out), rows, cols,
-                                                                          vec);
-  return cudaGetLastError();
+  return launch_pdl(join_slots_kernel, (int)(want < cap ? want : cap), kRowThreads, 0, s, slots, n, stride, ld,
+                    static_cast<__nv_bfloat16*>(out), rows, cols, vec);
 }
 
 // Rows of up to 17 matrices to padded rows (16-byte units), one launch: a
 // thread writes one unit of a destination row.
 __global__ void __launch_bounds__(kRowThreads) pad_rows_kernel(const __grid_constant__ PadArgs a) {
+  pdl_wait();
+  pdl_next();
   const long long step = (long long)gridDim.x * kRowThreads;
   int m = 0;
   for (long long i = (long long)blockIdx.x * kRowThreads + threadIdx.x; i < a.first[a.n]; i += step) {
@@ -119,8 +121,7 @@ cudaError_t launch_pad_rows(const PadArgs& a, cudaStream_t s) {
   const long long want = (a.first[a.n] + kRowThreads - 1) / kRowThreads;
   if (want == 0) return cudaSuccess;
   const long long cap = max_ctas_cap() > 0 ? max_ctas_cap() : device_sms() * 8;
-  pad_rows_kernel<<<(int)(want < cap ? want : cap), kRowThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(pad_rows_kernel, (int)(want < cap ? want : cap), kRowThreads, 0, s, a);
 }
 
 }  // namespace rra

@@ -181,6 +181,8 @@ __global__ void __launch_bounds__(256) loss_join_kernel(const __grid_constant__ 
   const int r = tid % R, k = tid / R;
   const int row0 = blockIdx.x * R;
   const int row = row0 + r;
+  pdl_wait();
+  pdl_next();
   float m = -INFINITY, s = 0.f;
   if (row < a.rows) {
     const float2* p = a.part + row;
@@ -282,10 +284,8 @@ cudaError_t launch_loss_join(const float2* part, int parts, const float* hit, co
   a.lse = lse;
   // one row per CTA while that leaves SMs idle, else 8 (whole sectors of parts)
   if (rows < 8 * device_sms())
-    loss_join_kernel<1><<<rows, 256, 0, s>>>(a);
-  else
-    loss_join_kernel<8><<<(rows + 7) / 8, 256, 0, s>>>(a);
-  return cudaGetLastError();
+    return launch_pdl(loss_join_kernel<1>, rows, 256, 0, s, a);
+  return launch_pdl(loss_join_kernel<8>, (rows + 7) / 8, 256, 0, s, a);
 }
 
 }  // namespace rra

@@ -1,0 +1,36 @@
+// pdl.cuh -- launches that may start while the kernel before them on the
+// stream finishes.  The training operators issue two to a few dozen short
+// kernels per call; with the programmatic launch attribute a kernel's CTAs
+// are placed, and its barriers and tensor memory set up, under the tail of
+// the one before it.  Every kernel launched this way calls pdl_wait() before
+// it touches global memory: it returns when all earlier kernels have
+// finished and their stores are visible (each of them has waited in turn).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <utility>
+
+namespace rra {
+
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Lets the next kernel's CTAs be placed as this one's leave.
+__device__ __forceinline__ void pdl_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <class... P, class... A>
+cudaError_t launch_pdl(void (*kernel)(P...), int grid, int threads, size_t smem, cudaStream_t s, A&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
+
+}  // namespace rra

@@ -34,6 +34,7 @@
 
 #include <cstdint>
 
+#include "pdl.cuh"
 #include "rra_internal.h"
 #include "tc_host.h"
 
@@ -300,6 +301,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
   tc_cluster_sync();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
+  pdl_wait();
+  pdl_next();
 
   uint32_t issued = 0;  // producer: stages loaded so far
   if (warp == 0) {
@@ -416,8 +419,7 @@ cudaError_t tc_launch(const TcArgs& p, cudaStream_t s, int* grid_out) {
   if (attr != cudaSuccess) return attr;
   const int grid = 2 * tc_clusters(p.tiles * p.splits);
   if (grid_out) *grid_out = grid;
-  kern<<<grid, kTcThreads, kTcSmem, s>>>(p);
-  return cudaGetLastError();
+  return launch_pdl(kern, grid, kTcThreads, kTcSmem, s, p);
 }
 
 }  // namespace rra
