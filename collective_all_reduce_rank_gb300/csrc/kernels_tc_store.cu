@@ -16,25 +16,35 @@ struct EpiStore {
     const TcGroup& g = p.group[x.group];
     const int c0 = x.n * 256 + half * 128;
     const int rows = g.M - row0;
-    const long long off = (long long)row0 * g.ld + c0;
-    constexpr int STEP = F32 ? 32 : 64;
+    const bool part = x.slot >= 0 && p.splits > 1;
+    if (F32 || part) {
+      // float32 rows of the output, or the tile's own slot
+      const long long ld = part ? 256 : g.ld;
+      float* o = part ? p.slots + (long long)x.slot * 65536 + (row0 - x.m * 256) * 256 + half * 128
+                      : static_cast<float*>(g.out) + (long long)row0 * g.ld + c0;
 #pragma unroll 1
-    for (int c = 0; c < 128; c += STEP) {
-      const int valid = g.N - c0 - c;
-      if (valid <= 0) break;
-      float v[32];
-      tc_ld32(addr + half * 128 + c, v);
-      if constexpr (F32) {
-        tc_ld_wait();
-        float* o = static_cast<float*>(g.out) + x.split * p.split_stride + off + c;
-        tc_store_f32(buf, v, o, g.ld, rows, valid, g.vec, p.accumulate);
-      } else {
-        float w[32];
+      for (int c = 0; c < 128; c += 32) {
+        const int valid = g.N - c0 - c;
+        if (valid <= 0) break;
+        float v[32];
+        tc_ld32(addr + half * 128 + c, v);
+        tc_ld_ready(v);
+        tc_store_f32(buf, v, o + c, ld, rows, part ? 32 : valid, part || g.vec, p.accumulate);
+      }
+    } else {
+      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(g.out) + (long long)row0 * g.ld + c0;
+#pragma unroll 1
+      for (int c = 0; c < 128; c += 64) {
+        const int valid = g.N - c0 - c;
+        if (valid <= 0) break;
+        float v[32], w[32];
+        tc_ld32(addr + half * 128 + c, v);
         tc_ld32(addr + half * 128 + c + 32, w);
-        tc_ld_wait();
+        tc_ld_ready(v);
         tc_stage_bf16(buf, v, 0);
+        tc_ld_ready(w);
         tc_stage_bf16(buf, w, 4);
-        tc_flush_bf16(buf, static_cast<__nv_bfloat16*>(g.out) + off + c, g.ld, rows, valid, g.vec, false);
+        tc_flush_bf16(buf, o + c, g.ld, rows, valid, g.vec, false);
       }
     }
   }
@@ -52,45 +62,51 @@ cudaError_t launch_tc_weight_grad(const TcArgs& p, cudaStream_t s, int* grid) {
 
 constexpr int kRowThreads = 256;
 
-// out[r][c] = bfloat16(sum over the slots), slots' rows ld (a multiple of 8)
-// elements apart; a thread takes 8 columns, a CTA whole rows.
-__global__ void __launch_bounds__(kRowThreads)
-    join_slots_kernel(const float* slots, int n, long long stride, int ld, __nv_bfloat16* out, int rows, int cols,
-                      int vec) {
+// One CTA per 8 rows of a tile; a thread takes 8 columns of one.
+__global__ void __launch_bounds__(kRowThreads) join_tiles_kernel(const __grid_constant__ JoinTiles j, int first) {
   pdl_wait();
   pdl_next();
-  const int units = ld / 8;
-  const long long total = (long long)rows * units, step = (long long)gridDim.x * kRowThreads;
-  for (long long i = (long long)blockIdx.x * kRowThreads + threadIdx.x; i < total; i += step) {
-    const int r = total <= 0xFFFFFFFFll ? (int)((uint32_t)i / (uint32_t)units) : (int)(i / units);
-    const int c = (int)(i - (long long)r * units) * 8;
-    const float4* p = reinterpret_cast<const float4*>(slots + (long long)r * ld + c);
-    float4 a = __ldcs(p), b = __ldcs(p + 1);
-    for (int k = 1; k < n; ++k) {
-      const float4* q = reinterpret_cast<const float4*>(slots + k * stride + (long long)r * ld + c);
-      const float4 x = __ldcs(q), y = __ldcs(q + 1);
-      a = make_float4(a.x + x.x, a.y + x.y, a.z + x.z, a.w + x.w);
-      b = make_float4(b.x + y.x, b.y + y.y, b.z + y.z, b.w + y.w);
+  const int tile = first + blockIdx.x / 32, slab = blockIdx.x % 32;
+  int m, n;
+  tc_walk(tile, j.mt, j.nt, m, n);
+  const bool vec = j.cols % 8 == 0 && ((uintptr_t)j.out & 15) == 0;
+  const int lr = slab * 8 + (threadIdx.x >> 5), lc = (threadIdx.x & 31) * 8;
+  const int r = m * 256 + lr, c = n * 256 + lc;
+  if (r < j.rows && c < j.cols) {
+    float4 a, b;
+    if (tile < j.full || j.splits == 1) {
+      const float4* q = reinterpret_cast<const float4*>(j.acc + (long long)r * j.ld + c);
+      a = __ldcs(q);
+      b = __ldcs(q + 1);
+    } else {
+      const float* q = j.slots + (long long)(tile - j.full) * j.splits * 65536 + lr * 256 + lc;
+      a = __ldcs(reinterpret_cast<const float4*>(q));
+      b = __ldcs(reinterpret_cast<const float4*>(q) + 1);
+#pragma unroll 4
+      for (int k = 1; k < j.splits; ++k) {
+        const float4* z = reinterpret_cast<const float4*>(q + k * 65536);
+        const float4 x = __ldcs(z), y = __ldcs(z + 1);
+        a = make_float4(a.x + x.x, a.y + x.y, a.z + x.z, a.w + x.w);
+        b = make_float4(b.x + y.x, b.y + y.y, b.z + y.z, b.w + y.w);
+      }
     }
-    __nv_bfloat16* o = out + (long long)r * cols + c;
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(j.out) + (long long)r * j.cols + c;
     const uint32_t w[4] = {tc_pack2(a.x, a.y), tc_pack2(a.z, a.w), tc_pack2(b.x, b.y), tc_pack2(b.z, b.w)};
-    if (vec && c + 8 <= cols) {
+    if (vec) {
       *reinterpret_cast<uint4*>(o) = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (c + j < cols) reinterpret_cast<uint16_t*>(o)[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+      for (int k = 0; k < 8; ++k)
+        if (c + k < j.cols) reinterpret_cast<uint16_t*>(o)[k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
     }
   }
 }
 
-cudaError_t launch_join_slots(const float* slots, int n, long long stride, int ld, void* out, int rows, int cols,
-                              cudaStream_t s) {
-  const long long cap = max_ctas_cap() > 0 ? max_ctas_cap() : device_sms() * 8;
-  const long long want = ((long long)rows * (ld / 8) + kRowThreads - 1) / kRowThreads;
-  const int vec = cols % 8 == 0 && ((uintptr_t)out & 15) == 0;
-  return launch_pdl(join_slots_kernel, (int)(want < cap ? want : cap), kRowThreads, 0, s, slots, n, stride, ld,
-                    static_cast<__nv_bfloat16*>(out), rows, cols, vec);
+cudaError_t launch_join_tiles(const JoinTiles& j, cudaStream_t s) {
+  // without `acc` the whole tiles are in the output already
+  const int first = j.acc ? 0 : j.full, tiles = j.mt * j.nt;
+  if (first >= tiles || (!j.acc && j.splits == 1)) return cudaSuccess;
+  return launch_pdl(join_tiles_kernel, (tiles - first) * 32, kRowThreads, 0, s, j, first);
 }
 
 // Rows of up to 17 matrices to padded rows (16-byte units), one launch: a

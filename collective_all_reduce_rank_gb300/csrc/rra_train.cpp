@@ -98,25 +98,37 @@ struct Placer {
 bool map_k(CUtensorMap* m, const Mat& x) { return tc_map(m, x.p, x.cols, x.rows, x.ld, false); }
 bool map_mn(CUtensorMap* m, const Mat& x) { return tc_map(m, x.p, x.cols, x.rows, x.ld, true); }
 
-// How many parts to split the K axis of an input gradient into: the tiles of
-// a short batch fill few of the clusters, so the parts run side by side and
-// a join sums their float32 outputs.  The count minimises the waves of
-// products (0.27 us for the 64-deep step of a tile, measured on the full
-// kernel) plus the traffic of writing and joining the parts (at 5 TB/s).
-int pick_splits(size_t tokens, size_t hidden, size_t kblocks) {
-  const double tiles = (double)(tiles256(tokens) * tiles256(hidden));
-  const int clusters = std::max(1, device_sms() / 2);
-  int best = 1;
-  double best_us = 1e30;
-  for (int s = 1; s <= 32 && (size_t)s * 4 <= std::max<size_t>(kblocks, 4); ++s) {
-    const double waves = std::max(1.0, (double)(((long long)tiles * s + clusters - 1) / clusters));
-    const double us = waves * 0.27 * (double)kblocks / s + (s > 1 ? 3.0 + s * (double)tokens * hidden * 8 / 5e6 : 0.0);
-    if (us < best_us * 0.97) {
-      best_us = us;
-      best = s;
+// How an input gradient's tiles are spread over the clusters: `full` whole
+// tiles in whole waves, and the rest split into `splits` parts of the K axis
+// that run side by side, so that the last wave is as short as its share of
+// the work (4096 x 5120: 320 tiles on 76 clusters are 4 waves and 16 tiles,
+// which unsplit take a fifth: 0.72 against 0.64 ms).  The count minimises
+// the waves of products (0.27 us for the 64-deep step of a tile, measured on
+// the full kernel) plus the join: 5 us, and 0.05 us for each part's 256 KB
+// written and read (777 tokens x 1027, 20 tiles of 66 steps: 28 us unsplit,
+// 16 + 6 us in 3 parts).
+struct Split {
+  int full = 0, splits = 1;
+  size_t slot_bytes = 0;
+};
+
+Split pick_split(size_t tokens, size_t hidden, size_t kblocks) {
+  Split q;
+  const long long tiles = (long long)(tiles256(tokens) * tiles256(hidden));
+  const long long clusters = std::max(1, device_sms() / 2);
+  const long long full = tiles / clusters * clusters, rest = tiles - full;
+  double best = 1e30;
+  for (int s = 1; s <= 64 && (size_t)s * 4 <= std::max<size_t>(kblocks, 4); ++s) {
+    const double waves = (double)((rest * s + clusters - 1) / clusters) / s;
+    const double us = waves * 0.27 * (double)kblocks + (s > 1 ? 5.0 + (double)(rest * s) * 0.05 : 0.0);
+    if (us < best * 0.97) {
+      best = us;
+      q.splits = s;
     }
   }
-  return best;
+  q.full = (int)(q.splits > 1 ? full : tiles);
+  q.slot_bytes = q.splits > 1 ? (size_t)rest * q.splits * 65536 * 4 : 0;
+  return q;
 }
 
 bool add_group(TcArgs* p, const TcGroup& g0, bool narrow) {
@@ -136,6 +148,7 @@ void one_k_axis(TcArgs* p, size_t k) {
   p->seg_k0[0] = 0;
   p->kblocks = (int)((k + kTcKBlock - 1) / kTcKBlock);
   p->splits = 1;
+  p->full = p->tiles;
 }
 
 bool bad_extent(size_t a) { return a > (size_t)INT_MAX - 1024; }
@@ -322,8 +335,7 @@ size_t ffn_bytes(int n, size_t T, size_t D, size_t F, bool back) {
   if (back) {
     for (int i = 0; i < 2 * n; ++i) b.take(T * up(F, 64) * 2);
     const size_t kb = 2 * (size_t)n * ((F + 63) / 64);
-    const int splits = pick_splits(T, D, kb);
-    if (splits > 1) b.take((size_t)splits * T * slot_ld(D) * 4);
+    b.take(pick_split(T, D, kb).slot_bytes);
   }
   return b.at;
 }
@@ -465,8 +477,8 @@ rra_status_t rra_gated_ffn_backward(const void* x, const void* const* gates, con
   const size_t ldf = up(F, 64);
   for (int i = 0; i < 2 * nranks; ++i) dW[i] = Mat{ws.take(T * ldf * 2), T, F, ldf};
   const size_t kb_seg = (F + 63) / 64, kb = 2 * (size_t)nranks * kb_seg;
-  const int splits = pick_splits(T, D, kb);
-  float* slots = splits > 1 ? static_cast<float*>(ws.take((size_t)splits * T * slot_ld(D) * 4)) : nullptr;
+  const Split sp = pick_split(T, D, kb);
+  float* slots = static_cast<float*>(ws.take(sp.slot_bytes));
   if (!place.launch(s)) return done(call, nranks, count, dtype, 0, RRA_ERR_CUDA);
 
   // dg, du
@@ -504,20 +516,21 @@ rra_status_t rra_gated_ffn_backward(const void* x, const void* const* gates, con
     p->seg_k0[i] = (int)(i * kb_seg);
   }
   p->kblocks = (int)kb;
-  p->splits = splits;
-  p->split_stride = (long long)(T * slot_ld(D));
+  p->full = sp.full;
+  p->splits = sp.splits;
+  p->slots = slots;
   TcGroup g{};
   g.M = (int)T;
   g.N = (int)D;
-  g.ld = (long long)(splits > 1 ? slot_ld(D) : D);
-  g.out = splits > 1 ? (void*)slots : dx;
-  g.vec = splits > 1 || (aligned(dx, 16) && D % 8 == 0);
+  g.ld = (long long)D;
+  g.out = dx;
+  g.vec = aligned(dx, 16) && D % 8 == 0;
   ok = ok && add_group(p.get(), g, false);
   p->status = device_status();
   if (!ok) return done(call, nranks, count, dtype, 0, RRA_ERR_CUDA);
-  e = launch_tc_input_grad(*p, splits > 1, s, &grid);
-  if (e == cudaSuccess && splits > 1)
-    e = launch_join_slots(slots, splits, (long long)(T * slot_ld(D)), (int)slot_ld(D), dx, (int)T, (int)D, s);
+  e = launch_tc_input_grad(*p, false, s, &grid);
+  if (e == cudaSuccess)
+    e = launch_join_tiles({nullptr, slots, dx, 0, (int)T, (int)D, p->group[0].mt, p->group[0].nt, sp.full, sp.splits}, s);
   if (e != cudaSuccess) return done(call, nranks, count, dtype, grid, RRA_ERR_CUDA);
 
   // dG, dU
@@ -561,8 +574,8 @@ size_t vocab_tiles(int n, const size_t* vocab) {
 struct LossPlan {
   size_t fixed = 0;        // bytes before the piece
   size_t piece_tiles = 0;  // 256-column tiles per piece
-  int splits = 1;          // parts of dx's K axis per piece
-  size_t slots = 0;        // float32 copies of dx kept
+  Split split;             // of dx's tiles
+  bool acc = false;        // dx is summed over pieces in float32
 };
 
 long long skinny_units(int n, const size_t* vocab) {
@@ -597,9 +610,9 @@ LossPlan loss_plan(int n, size_t T, size_t D, const size_t* vocab, bool back, si
   // their slots leave: take the largest piece that fits with its own slots
   size_t piece = std::max<size_t>(1, std::min(tiles, kPieceBytes / std::max<size_t>(col, 1)));
   for (;; --piece) {
-    q.splits = pick_splits(T, D, piece * 4);
-    q.slots = piece < tiles || q.splits > 1 ? (size_t)q.splits : 0;
-    q.fixed = base + (q.slots ? up(q.slots * T * slot_ld(D) * 4, kAlign) : 0);
+    q.split = pick_split(T, D, piece * 4);
+    q.acc = piece < tiles;
+    q.fixed = base + up(q.split.slot_bytes, kAlign) + (q.acc ? up(T * slot_ld(D) * 4, kAlign) : 0);
     q.piece_tiles = piece;
     if (piece == 1 || room == SIZE_MAX || q.fixed + piece * col <= room) break;
     // jump to what the room allows at most
@@ -766,7 +779,8 @@ rra_status_t rra_vocab_loss_backward(const void* x, const void* const* weights, 
   for (int r = 0; r < nranks; ++r) W[r] = place(weights[r], vocab[r], D);
   bool ok = place.launch(s);
   if (!ok) return done(call, nranks, T * V, dtype, 0, RRA_ERR_CUDA);
-  float* slots = q.slots ? static_cast<float*>(ws.take(q.slots * T * slot_ld(D) * 4)) : nullptr;
+  float* slots = static_cast<float*>(ws.take(q.split.slot_bytes));
+  float* acc = q.acc ? static_cast<float*>(ws.take(T * slot_ld(D) * 4)) : nullptr;
   char* dl = ws.base + ws.at;
   const size_t ld = q.piece_tiles * 256;
 
@@ -831,19 +845,20 @@ rra_status_t rra_vocab_loss_backward(const void* x, const void* const* weights, 
       p->seg_k0[0] = 0;
     }
     p->kblocks = (int)kb;
-    p->splits = (int)std::max<size_t>(1, std::min<size_t>((size_t)q.splits, kb));
-    p->split_stride = (long long)(T * slot_ld(D));
+    p->full = q.split.full;
+    p->splits = q.split.splits;
+    p->slots = slots;
     p->accumulate = t0 > 0;
     TcGroup g{};
     g.M = (int)T;
     g.N = (int)D;
-    g.ld = (long long)(q.slots ? slot_ld(D) : D);
-    g.out = q.slots ? (void*)slots : dx;
-    g.vec = q.slots || (aligned(dx, 16) && D % 8 == 0);
+    g.ld = (long long)(acc ? slot_ld(D) : D);
+    g.out = acc ? (void*)acc : dx;
+    g.vec = acc || (aligned(dx, 16) && D % 8 == 0);
     ok = ok && add_group(p.get(), g, false);
     p->status = device_status();
     if (!ok) return done(call, nranks, T * V, dtype, 0, RRA_ERR_CUDA);
-    e = launch_tc_input_grad(*p, q.slots != 0, s, &grid);
+    e = launch_tc_input_grad(*p, q.acc, s, &grid);
     if (e != cudaSuccess) break;
 
     // dW of the piece's rows
@@ -867,8 +882,9 @@ rra_status_t rra_vocab_loss_backward(const void* x, const void* const* weights, 
     p->status = device_status();
     e = launch_tc_weight_grad(*p, s, &grid);
   }
-  if (e == cudaSuccess && q.slots)
-    e = launch_join_slots(slots, q.splits, (long long)(T * slot_ld(D)), (int)slot_ld(D), dx, (int)T, (int)D, s);
+  if (e == cudaSuccess)
+    e = launch_join_tiles({acc, slots, dx, (int)slot_ld(D), (int)T, (int)D, (int)tiles256(T), (int)tiles256(D),
+                           q.split.full, q.split.splits}, s);
   return done(call, nranks, T * V, dtype, grid, cuda_st(e));
 }
 

@@ -235,32 +235,46 @@ __device__ __forceinline__ bool tc_wait(uint32_t bar, uint32_t parity, TcShared*
 // tiles
 // ---------------------------------------------------------------------------
 struct TcTile {
-  int group, m, n, split;
+  int group, m, n;
+  int slot;    // which part of the split tiles this is (-1: a whole tile)
+  int k0, k1;  // K blocks
 };
 
-// Tiles of one split are walked group by group; inside a group, bands of
-// kTcBand tile rows, down the band first, so that the tiles running at one
-// time share few rows of A and columns of B in L2.
+// K blocks of unit t: all of them, or one of the parts of a split tile.
+__device__ __forceinline__ void tc_krange(const TcArgs& p, int t, int& k0, int& k1) {
+  k0 = 0;
+  k1 = p.kblocks;
+  if (t >= p.full) {
+    const int part = (t - p.full) % p.splits;
+    k0 = (int)((long long)p.kblocks * part / p.splits);
+    k1 = (int)((long long)p.kblocks * (part + 1) / p.splits);
+  }
+}
+
+// Where tile u of a group of mt x nt tiles lies: bands of kTcBand tile rows,
+// down the band first, so that the tiles running at one time share few rows
+// of A and columns of B in L2.
+__device__ __forceinline__ void tc_walk(int u, int mt, int nt, int& m, int& n) {
+  const int band = u / (kTcBand * nt);
+  const int rows = min(kTcBand, mt - band * kTcBand);
+  const int v = u - band * kTcBand * nt;
+  m = band * kTcBand + v % rows;
+  n = v / rows;
+}
+
+// Unit t of the launch: whole tiles first, group by group, then the parts of
+// the split tiles.
 __device__ __forceinline__ TcTile tc_tile(const TcArgs& p, int t) {
   TcTile x;
-  x.split = t / p.tiles;
-  int u = t - x.split * p.tiles;
+  tc_krange(p, t, x.k0, x.k1);
+  x.slot = t - p.full;
+  int u = x.slot < 0 ? t : p.full + x.slot / p.splits;
   int g = 0;
   while (g + 1 < p.ngroups && u >= p.group[g + 1].tile0) ++g;
   x.group = g;
   u -= p.group[g].tile0;
-  const int mt = p.group[g].mt, nt = p.group[g].nt;
-  const int band = u / (kTcBand * nt);
-  const int rows = min(kTcBand, mt - band * kTcBand);
-  const int v = u - band * kTcBand * nt;
-  x.m = band * kTcBand + v % rows;
-  x.n = v / rows;
+  tc_walk(u, p.group[g].mt, p.group[g].nt, x.m, x.n);
   return x;
-}
-
-__device__ __forceinline__ void tc_krange(const TcArgs& p, int split, int& k0, int& k1) {
-  k0 = (int)((long long)p.kblocks * split / p.splits);
-  k1 = (int)((long long)p.kblocks * (split + 1) / p.splits);
 }
 
 // ---------------------------------------------------------------------------
@@ -277,7 +291,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = tc_cta_rank();
   const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
-  const int total = p.tiles * p.splits;
+  const int total = tc_units(p);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kTcStages; ++s) {
@@ -311,11 +325,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
       for (int t = cluster; t < total && ok; t += clusters) {
         const TcTile x = tc_tile(p, t);
         const TcGroup& g = p.group[x.group];
-        int k0, k1;
-        tc_krange(p, x.split, k0, k1);
         int seg = 0;
-        while (seg + 1 < p.nsegs && k0 >= p.seg_k0[seg + 1]) ++seg;
-        for (int k = k0; k < k1; ++k, ++issued) {
+        for (int k = x.k0; k < x.k1; ++k, ++issued) {
           while (seg + 1 < p.nsegs && k >= p.seg_k0[seg + 1]) ++seg;
           const int kk = (k - p.seg_k0[seg]) * kTcBK;
           const int s = issued % kTcStages;
@@ -351,9 +362,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     if (rank == 0 && lane == 0) {
       uint32_t it = 0, tile = 0;
       bool ok = true;
-      for (int t = cluster; t < total && ok; t += clusters, ++tile) {
+      for (int t = cluster; t < total && ok; t += clusters) {
         int k0, k1;
-        tc_krange(p, t / p.tiles, k0, k1);
+        tc_krange(p, t, k0, k1);
+        if (k0 == k1) continue;  // a part of a K axis shorter than its parts
         const uint32_t buf = tile & 1, d = tmem + buf * 256;
         if (!tc_wait(tc_smem(&sh.acc_empty[buf]), ((tile >> 1) & 1) ^ 1, &sh, p.status, 2)) break;
         tc_fence_after();
@@ -372,14 +384,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
           tc_commit(tc_smem(&sh.empty[s]));
         }
         if (ok) tc_commit(tc_smem(&sh.acc_full[buf]));
+        ++tile;
       }
     }
     __syncwarp();
   } else if (warp >= 4) {
     const int quad = warp & 3, half = (warp - 4) >> 2;
     uint32_t tile = 0;
-    for (int t = cluster; t < total; t += clusters, ++tile) {
+    for (int t = cluster; t < total; t += clusters) {
       const TcTile x = tc_tile(p, t);
+      if (x.k0 == x.k1) continue;
       const uint32_t buf = tile & 1;
       if (!__all_sync(0xffffffffu, tc_wait(tc_smem(&sh.acc_full[buf]), (tile >> 1) & 1, &sh, p.status, 4))) break;
       tc_fence_after();
@@ -389,6 +403,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) tc_bar_arrive_remote(tc_smem(&sh.acc_empty[buf]), 0);
+      ++tile;
     }
   }
 
@@ -417,7 +432,7 @@ cudaError_t tc_launch(const TcArgs& p, cudaStream_t s, int* grid_out) {
   static const cudaError_t attr =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
   if (attr != cudaSuccess) return attr;
-  const int grid = 2 * tc_clusters(p.tiles * p.splits);
+  const int grid = 2 * tc_clusters(tc_units(p));
   if (grid_out) *grid_out = grid;
   return launch_pdl(kern, grid, kTcThreads, kTcSmem, s, p);
 }

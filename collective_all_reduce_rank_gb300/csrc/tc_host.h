@@ -40,13 +40,14 @@ struct TcArgs {
   TcGroup group[kTcMaxGroups];
   int seg_k0[kTcMaxGroups];  // first K block of each segment
   int ngroups, nsegs;
-  int tiles;    // tiles of all groups (per split)
-  int splits;   // parts of the K axis, each with an output of its own
+  int tiles;    // tiles of all groups
+  int full;     // the first `full` tiles of the walk take the whole K axis,
+  int splits;   // the others one of `splits` parts of it at a time (tc_units)
   int kblocks;  // K blocks of 64 over all segments
   int pair_b;   // CTA c of a pair takes map b + c (gate and up weights), 128 columns per tile each
   // epilogue operands
-  long long split_stride;  // elements between the outputs of two splits
-  int accumulate;          // add to the float32 output
+  float* slots;    // split tiles: 256 x 256 float32 per part, part v of tile full + v / splits
+  int accumulate;  // add to the float32 outputs
   int act;
   const long long* targets;
   long long ignore_index, vocab;
@@ -74,7 +75,8 @@ cudaError_t launch_tc_dlogits(const TcArgs& p, cudaStream_t s, int* grid);    //
 cudaError_t launch_tc_gate(const TcArgs& p, cudaStream_t s, int* grid);       // K-major x K-major
 cudaError_t launch_tc_gate_back(const TcArgs& p, cudaStream_t s, int* grid);  // K-major x K-major
 // out = A B for A K-major, B MN-major (the gradient of the input): bfloat16
-// rows, or float32 rows (added to when p.accumulate).
+// rows, or float32 rows (added to when p.accumulate); split tiles go to
+// p.slots either way.
 cudaError_t launch_tc_input_grad(const TcArgs& p, bool f32, cudaStream_t s, int* grid);
 // out = A^T B, both MN-major (the gradient of the weights): bfloat16 rows.
 cudaError_t launch_tc_weight_grad(const TcArgs& p, cudaStream_t s, int* grid);
@@ -106,9 +108,21 @@ cudaError_t launch_skinny_lse(const SkinnyArgs& a, cudaStream_t s, int* grid);
 cudaError_t launch_loss_join(const float2* part, int parts, const float* hit, const long long* targets,
                              long long ignore_index, const void* x, const void* const* w, const size_t* vocab, int n,
                              size_t hidden, int rows, float* loss, float* lse, cudaStream_t s);
-// out[r][c] = bfloat16(sum over k < n of slots[k * stride + r * ld + c])
-cudaError_t launch_join_slots(const float* slots, int n, long long stride, int ld, void* out, int rows, int cols,
-                              cudaStream_t s);
+// dx from what the products of its one group of tiles left: tiles that took
+// the whole K axis are in `acc` (float32 rows of ld; null: already in out),
+// the others the sum of their parts in `slots`.
+struct JoinTiles {
+  const float* acc;
+  const float* slots;
+  void* out;
+  int ld, rows, cols, mt, nt, full, splits;
+};
+cudaError_t launch_join_tiles(const JoinTiles& j, cudaStream_t s);
+// Units of work of a launch: whole tiles, then parts of the others.
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+inline int tc_units(const TcArgs& p) { return p.full + (p.tiles - p.full) * p.splits; }
 // Rows of `cols` elements of each src to rows of 8 * units elements of dst.
 struct PadArgs {
   const void* src[kTcMaxGroups + 1];

@@ -129,7 +129,7 @@ def test_vocab_loss(T, D, shards):
     ref.assert_within(loss, *want["loss"], "loss")
 
 
-@pytest.mark.parametrize("room", ["default", "least"])
+@pytest.mark.parametrize("room", ["default", "least", "some"])
 @pytest.mark.parametrize("T,D,shards", LOSS)
 def test_vocab_loss_backward(T, D, shards, room):
     x, W, tgt, grad = loss_inputs(T, D, shards, T + 3 * D)
@@ -138,7 +138,9 @@ def test_vocab_loss_backward(T, D, shards, room):
     want = ref.vocab_loss(x, W, tgt, IGN, grad)
     lse = want["lse"][0].float().cuda()
     dx, dW = poison(T, D), [poison(v, D) for v in shards]
-    nb = rra.rra_vocab_loss_workspace_bytes(T, D, shards, 2 if room == "least" else 1)
+    nb = rra.rra_vocab_loss_workspace_bytes(T, D, shards, 1 if room == "default" else 2)
+    if room == "some":  # pieces of a few tiles, whose products split their K axis
+        nb += 6 * T * 512 + (24 << 20)
     ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
     rra.rra_vocab_loss_backward(xc, Wc, tc, lse, grad.cuda(), dx, dW, ignore_index=IGN, workspace=ws)
     status_ok()
@@ -295,3 +297,226 @@ def test_norm_checkpoint_of_extreme_values():
     got = out.cpu().double()
     assert torch.equal(torch.isnan(got), torch.isnan(val))
     assert torch.equal(torch.nan_to_num(got), torch.nan_to_num(val))
+
+
+# -- how the calls behave ----------------------------------------------------
+
+def step_inputs(T=96, D=256, F=200, V=777, n=2, seed=5):
+    gen = torch.Generator().manual_seed(seed)
+    d = dict(x=rnd(gen, T, D), G=[rnd(gen, F, D, scale=D ** -0.5) for _ in range(n)],
+             U=[rnd(gen, F, D, scale=D ** -0.5) for _ in range(n)], da=[rnd(gen, T, F, scale=1e-2) for _ in range(n)],
+             W=[rnd(gen, V, D, scale=D ** -0.5) for _ in range(n)], tgt=torch.randint(0, V * n, (T,), generator=gen),
+             grad=torch.rand(T, generator=gen) / T)
+    return {k: cuda(v) if isinstance(v, list) else v.cuda() for k, v in d.items()}
+
+
+def step_outputs(d):
+    e = lambda t: torch.empty_like(t)
+    return dict(acts=[e(a) for a in d["da"]], dx=e(d["x"]), dG=[e(w) for w in d["G"]], dU=[e(w) for w in d["U"]],
+                loss=torch.empty_like(d["grad"]), lse=torch.empty_like(d["grad"]), dx2=e(d["x"]),
+                dW=[e(w) for w in d["W"]])
+
+
+def run_step(d, o, ws, stream=None):
+    rra.rra_gated_ffn(d["x"], d["G"], d["U"], o["acts"], workspace=ws, stream=stream)
+    rra.rra_gated_ffn_backward(d["x"], d["G"], d["U"], d["da"], o["dx"], o["dG"], o["dU"], workspace=ws, stream=stream)
+    rra.rra_vocab_loss(d["x"], d["W"], d["tgt"], o["loss"], o["lse"], workspace=ws, stream=stream)
+    rra.rra_vocab_loss_backward(d["x"], d["W"], d["tgt"], o["lse"], d["grad"], o["dx2"], o["dW"], workspace=ws,
+                                stream=stream)
+
+
+def flat(o):
+    return [t for v in o.values() for t in (v if isinstance(v, list) else [v])]
+
+
+def test_repeat_stream_and_graph_give_the_same_bits():
+    d = step_inputs()
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    want = step_outputs(d)
+    run_step(d, want, ws)
+    torch.cuda.synchronize()
+    again = step_outputs(d)
+    run_step(d, again, ws)
+    side = step_outputs(d)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    run_step(d, side, ws, stream=s)  # a stream that is not the current one
+    s.synchronize()
+    own = step_outputs(d)
+    with torch.cuda.stream(s):
+        run_step(d, own, None)  # workspaces made by the calls
+    s.synchronize()
+    graphed = step_outputs(d)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        run_step(d, graphed, ws)
+    for t in flat(graphed):
+        t.zero_()
+    g.replay()
+    g.replay()
+    torch.cuda.synchronize()
+    status_ok()
+    for other in (again, side, own, graphed):
+        for a, b in zip(flat(want), flat(other)):
+            assert torch.equal(a, b)
+
+
+def test_no_tokens_and_no_columns():
+    dev = dict(device="cuda", dtype=torch.bfloat16)
+    x, w = torch.empty(0, 64, **dev), [torch.ones(40, 64, **dev)]
+    a, dx, dg, du = [torch.empty(0, 40, **dev)], torch.empty(0, 64, **dev), [poison(40, 64)], [poison(40, 64)]
+    rra.rra_gated_ffn(x, w, w, a)
+    rra.rra_gated_ffn_backward(x, w, w, a, dx, dg, du)
+    assert not dg[0].any() and not du[0].any()
+    none = torch.empty(0, device="cuda")
+    tgt = torch.empty(0, dtype=torch.int64, device="cuda")
+    dw = [poison(40, 64)]
+    rra.rra_vocab_loss(x, w, tgt, none, none.clone())
+    rra.rra_vocab_loss_backward(x, w, tgt, none, none.clone(), dx, dw)
+    assert not dw[0].any()
+    dgamma = poison(64, dtype=torch.float32)
+    codes, scales = torch.empty(0, 64, device="cuda", dtype=torch.uint8), torch.empty(0, 1, device="cuda", dtype=torch.uint8)
+    rra.rra_allreduce_rmsnorm_backward8([x], [torch.empty_like(x)], codes, scales, none, torch.ones(64, **dev), dgamma)
+    assert not dgamma.any()
+    # no columns: dx is zero
+    x2, w0, dx2 = torch.ones(3, 64, **dev), [torch.empty(0, 64, **dev)], poison(3, 64)
+    rra.rra_gated_ffn_backward(x2, w0, w0, [torch.empty(3, 0, **dev)], dx2, [torch.empty(0, 64, **dev)],
+                               [torch.empty(0, 64, **dev)])
+    assert not dx2.any()
+    status_ok()
+
+
+def test_every_target_ignored():
+    x, W, tgt, grad = loss_inputs(40, 128, (300, 200), 3)
+    tgt[:] = IGN
+    xc, Wc, tc = x.cuda(), cuda(W), tgt.cuda()
+    loss, lse = poison(40, dtype=torch.float32), poison(40, dtype=torch.float32)
+    rra.rra_vocab_loss(xc, Wc, tc, loss, lse)
+    assert not loss.any() and torch.isfinite(lse).all()
+    dx, dW = poison(40, 128), [poison(300, 128), poison(200, 128)]
+    rra.rra_vocab_loss_backward(xc, Wc, tc, lse, torch.full((40,), math.inf, device="cuda"), dx, dW)
+    status_ok()
+    assert not dx.any() and not any(w.any() for w in dW)
+
+
+@pytest.mark.parametrize("T", [3, 40])
+def test_what_is_not_finite_stays_in_its_row(T):
+    D, shards = 640, (300, 200)
+    x, W, tgt, grad = loss_inputs(T, D, shards, 11)
+    tgt = torch.full((T,), 7)
+    clean = [torch.empty(T, device="cuda"), torch.empty(T, device="cuda")]
+    rra.rra_vocab_loss(x.cuda(), cuda(W), tgt.cuda(), *clean)
+    x[1, 5] = math.nan
+    loss, lse = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    rra.rra_vocab_loss(x.cuda(), cuda(W), tgt.cuda(), loss, lse)
+    assert bool(torch.isnan(loss[1])) and bool(torch.isnan(lse[1]))
+    rest = [t for t in range(T) if t != 1]
+    assert torch.equal(loss[rest], clean[0][rest]) and torch.equal(lse[rest], clean[1][rest])
+    acts, ref_acts = [torch.empty(T, 24, dtype=torch.bfloat16, device="cuda")], [
+        torch.empty(T, 24, dtype=torch.bfloat16, device="cuda")]
+    w = [W[0][:24].contiguous().cuda()]
+    rra.rra_gated_ffn(x.cuda(), w, w, acts)
+    x[1, 5] = 0
+    rra.rra_gated_ffn(x.cuda(), w, w, ref_acts)
+    assert torch.isnan(acts[0][1].float()).all() and torch.equal(acts[0][rest], ref_acts[0][rest])
+    status_ok()
+
+
+def test_masked_logits_of_minus_infinity():
+    """Vocabulary rows that are out of play: weights whose logits are -inf
+    carry no probability and get no gradient beyond their own."""
+    T, D = 20, 64
+    gen = torch.Generator().manual_seed(2)
+    x = rnd(gen, T, D).abs() + 0.25
+    W = rnd(gen, 300, D, scale=0.1)
+    dead = torch.zeros(300, dtype=torch.bool)
+    dead[100:160] = True
+    dead[299] = True
+    Wd = W.clone()
+    Wd[dead] = -math.inf  # every product with a positive x is -inf
+    tgt = torch.randint(0, 100, (T,), generator=gen)
+    loss, lse = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    rra.rra_vocab_loss(x.cuda(), [Wd.cuda()], tgt.cuda(), loss, lse)
+    want = ref.vocab_loss(x, [W[~dead]], tgt, IGN)  # the targets lie before the dead rows
+    ref.assert_within(lse, *want["lse"], "lse")
+    ref.assert_within(loss, *want["loss"], "loss")
+    tgt[4] = 120  # a target out of play: its loss is infinite
+    rra.rra_vocab_loss(x.cuda(), [Wd.cuda()], tgt.cuda(), loss, lse)
+    assert float(loss[4]) == math.inf and torch.isfinite(loss[torch.arange(T) != 4]).all()
+    status_ok()
+
+
+def test_gradients_against_differences():
+    """Central differences of the loss in float64 along random directions."""
+    T, D, shards = 24, 64, (150, 83)
+    x, W, tgt, grad = loss_inputs(T, D, shards, 8)
+    tgt = torch.where((tgt < 0) | (tgt >= sum(shards)), torch.full_like(tgt, IGN), tgt)
+    lse, loss = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    dx, dW = torch.empty(T, D, dtype=torch.bfloat16, device="cuda"), [torch.empty_like(w, device="cuda") for w in W]
+    rra.rra_vocab_loss(x.cuda(), cuda(W), tgt.cuda(), loss, lse)
+    rra.rra_vocab_loss_backward(x.cuda(), cuda(W), tgt.cuda(), lse, grad.cuda(), dx, dW)
+
+    def total(xx, ww):
+        return float((ref.vocab_loss(xx, ww, tgt, IGN)["loss"][0] * grad.double()).sum())
+
+    gen = torch.Generator().manual_seed(1)
+    for _ in range(4):
+        vx = torch.randn(T, D, generator=gen, dtype=torch.float64)
+        vw = [torch.randn(w.shape, generator=gen, dtype=torch.float64) for w in W]
+        h = 1e-4
+        num = (total(x.double() + h * vx, [w.double() + h * v for w, v in zip(W, vw)])
+               - total(x.double() - h * vx, [w.double() - h * v for w, v in zip(W, vw)])) / (2 * h)
+        parts = [(dx.cpu().double() * vx)] + [g.cpu().double() * v for g, v in zip(dW, vw)]
+        # each gradient is off by at most two bfloat16 half steps of its terms' size
+        slack = 4 * ref.BF * sum(float(p.norm()) for p in parts) + 1e-6 * abs(num)
+        assert abs(num - sum(float(p.sum()) for p in parts)) <= slack
+
+
+def test_sm_budget_and_the_recorder():
+    d = step_inputs(T=300)
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    want, small = step_outputs(d), step_outputs(d)
+    run_step(d, want, ws)
+    rra.rra_set_max_ctas(8)
+    try:
+        run_step(d, small, ws)
+        line = [l for l in rra.rra_dump_recent().splitlines() if "gated_ffn " in l][-1]
+        assert "grid=8" in line
+    finally:
+        rra.rra_set_max_ctas(0)
+    torch.cuda.synchronize()
+    status_ok()
+    for a, b in zip(flat(want), flat(small)):
+        assert torch.equal(a, b)
+
+
+def test_weights_past_four_gigabytes():
+    """A shard of more than 2^32 bytes: the last rows land where they belong."""
+    D, V = 4096, 540_001  # 4.42 GB
+    T = 20
+    W = torch.zeros(V, D, dtype=torch.bfloat16, device="cuda")
+    x = torch.zeros(T, D, dtype=torch.bfloat16, device="cuda")
+    x[:, 0] = 1.0
+    gen = torch.Generator().manual_seed(4)
+    pick = torch.randint(V - 5000, V, (T,), generator=gen)
+    W[pick, 0] = 9.0
+    loss, lse = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    rra.rra_vocab_loss(x, [W], pick.cuda(), loss, lse)
+    uniq = len(set(pick.tolist()))
+    want = math.log((V - uniq) + uniq * math.exp(9.0))
+    assert torch.allclose(lse.cpu().double(), torch.full((T,), want, dtype=torch.float64), rtol=1e-5)
+    assert torch.allclose(loss.cpu().double(), torch.full((T,), want - 9.0, dtype=torch.float64), rtol=1e-5)
+    grad = torch.ones(T, device="cuda")
+    dx, dW = torch.empty_like(x), torch.empty_like(W)
+    rra.rra_vocab_loss_backward(x, [W], pick.cuda(), lse, grad, dx, [dW])
+    status_ok()
+    p9, p1 = math.exp(9.0 - want), math.exp(-want)
+    col = dW[:, 0].float().cpu().double()
+    assert torch.equal(dW[:, 1].float().cpu(), torch.zeros(V))
+    count = torch.zeros(V, dtype=torch.float64)
+    for t in pick.tolist():
+        count[t] += 1
+    full = torch.full((V,), T * p1, dtype=torch.float64)
+    full[count > 0] = T * p9 - count[count > 0]
+    assert float((col - full).abs().max()) <= 4 * ref.BF * float(full.abs().max())
+    assert float((col - full)[count == 0].abs().max()) <= 4 * ref.BF * T * p1
