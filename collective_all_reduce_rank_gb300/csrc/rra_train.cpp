@@ -8,8 +8,7 @@
 #include <algorithm>
 #include <climits>
 #include <cstring>
-#include <memory>
-#include <vector>
+#include <initializer_list>
 
 #include "rra.h"
 #include "rra_internal.h"
@@ -36,9 +35,22 @@ bool meet(const Range& a, const Range& b) {
   return a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
 }
 
+// A call's address ranges (no allocation, so nothing here can throw).
+struct Ranges {
+  Range r[5 + 3 * kMaxRanks];
+  size_t n = 0;
+  Ranges() = default;
+  Ranges(std::initializer_list<Range> l) {
+    for (const Range& x : l) push_back(x);
+  }
+  void push_back(const Range& x) { r[n++] = x; }
+  size_t size() const { return n; }
+  const Range& operator[](size_t i) const { return r[i]; }
+};
+
 // An output meets an input or another output; of the first `inplace` pairs,
 // output i may be input i.
-bool clash(const std::vector<Range>& in, const std::vector<Range>& out, int inplace = 0) {
+bool clash(const Ranges& in, const Ranges& out, int inplace = 0) {
   for (size_t i = 0; i < out.size(); ++i) {
     for (size_t j = i + 1; j < out.size(); ++j)
       if (meet(out[i], out[j])) return true;
@@ -136,7 +148,7 @@ bool add_group(TcArgs* p, const TcGroup& g0, bool narrow) {
   g.mt = (int)tiles256((size_t)g.M);
   g.nt = narrow ? (g.N + 127) / 128 : (int)tiles256((size_t)g.N);
   const long long t = (long long)g.mt * g.nt + p->tiles;
-  if (t > INT_MAX / 64 || p->ngroups >= kTcMaxGroups) return false;
+  if (t > INT_MAX / 2 || p->ngroups >= kTcMaxGroups) return false;
   g.tile0 = p->tiles;
   p->group[p->ngroups++] = g;
   p->tiles = (int)t;
@@ -149,6 +161,12 @@ void one_k_axis(TcArgs* p, size_t k) {
   p->kblocks = (int)((k + kTcKBlock - 1) / kTcKBlock);
   p->splits = 1;
   p->full = p->tiles;
+}
+
+// More 256 x 256 tiles than the walk can count (`extra`: shards, each of
+// which may end in a partial tile).
+bool too_many_tiles(size_t m, size_t n, size_t extra) {
+  return (tiles256(m) + extra) * (tiles256(n) + extra) > (size_t)INT_MAX / 4;
 }
 
 bool bad_extent(size_t a) { return a > (size_t)INT_MAX - 1024; }
@@ -236,7 +254,7 @@ rra_status_t rra_allreduce_rmsnorm_save8(const void* const* bufs, void* const* o
   if (st == RRA_SUCCESS && ((rows && (!codes || !scales || !rstd)) || !aligned(rstd, 4) || !(eps >= 0.f))) st = RRA_ERR_INVALID_ARG;
   if (st != RRA_SUCCESS) return done(call, nranks, count, dtype, 0, st);
   const size_t e = dtype == RRA_BFLOAT16 ? 2 : 4, S = count * e, nblk = (hidden + kCkptBlock - 1) / kCkptBlock;
-  std::vector<Range> in, out;
+  Ranges in, out;
   for (int r = 0; r < nranks; ++r) {
     in.push_back({bufs[r], S});
     out.push_back({outs[r], S});
@@ -295,7 +313,7 @@ rra_status_t rra_allreduce_rmsnorm_backward8(const void* const* grads, void* con
   if (st == RRA_SUCCESS && workspace_bytes < need) st = RRA_ERR_WORKSPACE;
   if (st != RRA_SUCCESS) return done(call, nranks, count, dtype, 0, st);
   const size_t e = dtype == RRA_BFLOAT16 ? 2 : 4, S = count * e, nblk = (hidden + kCkptBlock - 1) / kCkptBlock;
-  std::vector<Range> in, out;
+  Ranges in, out;
   for (int r = 0; r < nranks; ++r) {
     in.push_back({grads[r], S});
     out.push_back({dxs[r], S});
@@ -349,7 +367,9 @@ rra_status_t ffn_check(const void* x, const void* const* gates, const void* cons
   if (dt != RRA_BFLOAT16)
     return dt == RRA_FLOAT32 || dt == RRA_INT32 ? RRA_ERR_UNSUPPORTED : RRA_ERR_INVALID_ARG;
   if (bad_extent(T) || bad_extent(D) || bad_extent(F)) return RRA_ERR_UNSUPPORTED;
-  if (T && (T * D > SIZE_MAX / 1024 || T * F > SIZE_MAX / 1024)) return RRA_ERR_UNSUPPORTED;
+  if (T * D > SIZE_MAX / 1024 || T * F > SIZE_MAX / 1024 || F * D > SIZE_MAX / 1024) return RRA_ERR_UNSUPPORTED;
+  if (too_many_tiles(T, 2 * F * n, 2 * n) || too_many_tiles(2 * F * n, D, 2 * n) || too_many_tiles(T, D, 0))
+    return RRA_ERR_UNSUPPORTED;
   for (int r = 0; r < n; ++r) {
     if ((F && (!gates[r] || !ups[r])) || (T && F && !acts[r]) || !aligned(acts[r], 2) || !aligned(gates[r], 2) || !aligned(ups[r], 2))
       return RRA_ERR_INVALID_ARG;
@@ -380,7 +400,7 @@ rra_status_t rra_gated_ffn(const void* x, const void* const* gates, const void* 
   rra_status_t st = ffn_check(x, gates, ups, (const void* const*)acts, nranks, T, D, F, act, dtype, workspace,
                               workspace_bytes, false);
   if (st != RRA_SUCCESS) return done(call, nranks, count, dtype, 0, st);
-  std::vector<Range> in{{x, T * D * 2}}, out{{workspace, ffn_bytes(nranks, T, D, F, false)}};
+  Ranges in{{x, T * D * 2}}, out{{workspace, ffn_bytes(nranks, T, D, F, false)}};
   for (int r = 0; r < nranks; ++r) {
     in.push_back({gates[r], F * D * 2});
     in.push_back({ups[r], F * D * 2});
@@ -409,8 +429,9 @@ rra_status_t rra_gated_ffn(const void* x, const void* const* gates, const void* 
     return done(call, nranks, count, dtype, grid, cuda_st(e));
   }
   Bump ws{static_cast<char*>(workspace)};
-  auto p = std::make_unique<TcArgs>();
-  std::memset(p.get(), 0, sizeof(TcArgs));
+  TcArgs args;
+  TcArgs* const p = &args;
+  std::memset(p, 0, sizeof(TcArgs));
   Placer place(ws);
   const Mat X = place(x, T, D);
   bool ok = map_k(&p->a[0], X);
@@ -425,10 +446,10 @@ rra_status_t rra_gated_ffn(const void* x, const void* const* gates, const void* 
     g.out = acts[r];
     g.ld = (long long)F;
     g.vec = aligned(acts[r], 16) && F % 8 == 0;
-    ok = ok && add_group(p.get(), g, true);
+    ok = ok && add_group(p, g, true);
   }
   if (!ok || !place.launch(s)) return done(call, nranks, count, dtype, 0, RRA_ERR_CUDA);
-  one_k_axis(p.get(), D);
+  one_k_axis(p, D);
   p->pair_b = 1;
   p->act = act;
   p->status = device_status();
@@ -450,7 +471,7 @@ rra_status_t rra_gated_ffn_backward(const void* x, const void* const* gates, con
   for (int r = 0; r < nranks && st == RRA_SUCCESS; ++r)
     if ((F && (!dgates[r] || !dups[r])) || !aligned(dgates[r], 2) || !aligned(dups[r], 2)) st = RRA_ERR_INVALID_ARG;
   if (st != RRA_SUCCESS) return done(call, nranks, count, dtype, 0, st);
-  std::vector<Range> in{{x, T * D * 2}}, out{{workspace, ffn_bytes(nranks, T, D, F, true)}, {dx, T * D * 2}};
+  Ranges in{{x, T * D * 2}}, out{{workspace, ffn_bytes(nranks, T, D, F, true)}, {dx, T * D * 2}};
   for (int r = 0; r < nranks; ++r) {
     in.push_back({gates[r], F * D * 2});
     in.push_back({ups[r], F * D * 2});
@@ -482,8 +503,9 @@ rra_status_t rra_gated_ffn_backward(const void* x, const void* const* gates, con
   if (!place.launch(s)) return done(call, nranks, count, dtype, 0, RRA_ERR_CUDA);
 
   // dg, du
-  auto p = std::make_unique<TcArgs>();
-  std::memset(p.get(), 0, sizeof(TcArgs));
+  TcArgs args;
+  TcArgs* const p = &args;
+  std::memset(p, 0, sizeof(TcArgs));
   bool ok = map_k(&p->a[0], X);
   for (int r = 0; r < nranks && ok; ++r) {
     ok = map_k(&p->b[2 * r], W[2 * r]) && map_k(&p->b[2 * r + 1], W[2 * r + 1]);
@@ -497,10 +519,10 @@ rra_status_t rra_gated_ffn_backward(const void* x, const void* const* gates, con
     g.in = dacts[r];
     g.ld_in = (long long)F;
     g.vec = aligned(dacts[r], 16) && F % 8 == 0;
-    ok = ok && add_group(p.get(), g, true);
+    ok = ok && add_group(p, g, true);
   }
   if (!ok) return done(call, nranks, count, dtype, 0, RRA_ERR_CUDA);
-  one_k_axis(p.get(), D);
+  one_k_axis(p, D);
   p->pair_b = 1;
   p->act = act;
   p->status = device_status();
@@ -509,7 +531,7 @@ rra_status_t rra_gated_ffn_backward(const void* x, const void* const* gates, con
   if (e != cudaSuccess) return done(call, nranks, count, dtype, grid, RRA_ERR_CUDA);
 
   // dx: the shards' products as segments of one K axis
-  std::memset(p.get(), 0, sizeof(TcArgs));
+  std::memset(p, 0, sizeof(TcArgs));
   p->nsegs = 2 * nranks;
   for (int i = 0; i < 2 * nranks && ok; ++i) {
     ok = map_k(&p->a[i], dW[i]) && map_mn(&p->b[i], W[i]);
@@ -525,7 +547,7 @@ rra_status_t rra_gated_ffn_backward(const void* x, const void* const* gates, con
   g.ld = (long long)D;
   g.out = dx;
   g.vec = aligned(dx, 16) && D % 8 == 0;
-  ok = ok && add_group(p.get(), g, false);
+  ok = ok && add_group(p, g, false);
   p->status = device_status();
   if (!ok) return done(call, nranks, count, dtype, 0, RRA_ERR_CUDA);
   e = launch_tc_input_grad(*p, false, s, &grid);
@@ -534,7 +556,7 @@ rra_status_t rra_gated_ffn_backward(const void* x, const void* const* gates, con
   if (e != cudaSuccess) return done(call, nranks, count, dtype, grid, RRA_ERR_CUDA);
 
   // dG, dU
-  std::memset(p.get(), 0, sizeof(TcArgs));
+  std::memset(p, 0, sizeof(TcArgs));
   ok = map_mn(&p->b[0], X);
   for (int i = 0; i < 2 * nranks && ok; ++i) {
     ok = map_mn(&p->a[i], dW[i]);
@@ -546,10 +568,10 @@ rra_status_t rra_gated_ffn_backward(const void* x, const void* const* gates, con
     h.out = o;
     h.ld = (long long)D;
     h.vec = aligned(o, 16) && D % 8 == 0;
-    ok = ok && add_group(p.get(), h, false);
+    ok = ok && add_group(p, h, false);
   }
   if (!ok) return done(call, nranks, count, dtype, 0, RRA_ERR_CUDA);
-  one_k_axis(p.get(), T);
+  one_k_axis(p, T);
   p->status = device_status();
   e = launch_tc_weight_grad(*p, s, &grid);
   return done(call, nranks, count, dtype, grid, cuda_st(e));
@@ -638,6 +660,9 @@ rra_status_t loss_check(const void* x, const void* const* weights, const size_t*
   }
   if (V == 0 || !aligned(x, 2) || !aligned(targets, 8) || !aligned(ws, kAlign)) return RRA_ERR_INVALID_ARG;
   if (!aligned(x, 16) || bad_extent(V)) return RRA_ERR_UNSUPPORTED;
+  if (T * D > SIZE_MAX / 1024 || V * D > SIZE_MAX / 1024 || too_many_tiles(T, V, n) || too_many_tiles(V, D, n) ||
+      too_many_tiles(T, D, 0))
+    return RRA_ERR_UNSUPPORTED;
   *total = V;
   return RRA_SUCCESS;
 }
@@ -665,7 +690,7 @@ rra_status_t rra_vocab_loss(const void* x, const void* const* weights, const siz
   const size_t need = loss_plan(nranks, T, D, vocab, false, SIZE_MAX).fixed;
   if (need && !workspace) return done(call, nranks, T * V, dtype, 0, RRA_ERR_INVALID_ARG);
   if (workspace_bytes < need) return done(call, nranks, T * V, dtype, 0, RRA_ERR_WORKSPACE);
-  std::vector<Range> in{{x, T * D * 2}, {targets, T * 8}}, out{{workspace, need}, {loss, T * 4}, {lse, T * 4}};
+  Ranges in{{x, T * D * 2}, {targets, T * 8}}, out{{workspace, need}, {loss, T * 4}, {lse, T * 4}};
   for (int r = 0; r < nranks; ++r) in.push_back({weights[r], vocab[r] * D * 2});
   if (clash(in, out)) return done(call, nranks, T * V, dtype, 0, RRA_ERR_ALIAS);
   if (T == 0) return done(call, nranks, 0, dtype, 0, RRA_SUCCESS);
@@ -698,8 +723,9 @@ rra_status_t rra_vocab_loss(const void* x, const void* const* weights, const siz
                            lse, s);
     return done(call, nranks, T * V, dtype, grid, cuda_st(e));
   }
-  auto p = std::make_unique<TcArgs>();
-  std::memset(p.get(), 0, sizeof(TcArgs));
+  TcArgs args;
+  TcArgs* const p = &args;
+  std::memset(p, 0, sizeof(TcArgs));
   Placer place(ws);
   const Mat X = place(x, T, D);
   bool ok = map_k(&p->a[0], X);
@@ -715,13 +741,13 @@ rra_status_t rra_vocab_loss(const void* x, const void* const* weights, const siz
       g.N = (int)vocab[r];
       g.col0 = col0;
       g.part0 = parts;
-      ok = ok && add_group(p.get(), g, false);
+      ok = ok && add_group(p, g, false);
     }
     col0 += (long long)vocab[r];
     parts += (int)tiles256(vocab[r]);
   }
   if (!ok || !place.launch(s)) return done(call, nranks, T * V, dtype, 0, RRA_ERR_CUDA);
-  one_k_axis(p.get(), D);
+  one_k_axis(p, D);
   p->part = static_cast<float2*>(ws.take(2 * (size_t)parts * T * sizeof(float2)));
   p->part_ld = (long long)T;
   p->hit = static_cast<float*>(ws.take(T * 4));
@@ -756,7 +782,7 @@ rra_status_t rra_vocab_loss_backward(const void* x, const void* const* weights, 
   const LossPlan q = loss_plan(nranks, T, D, vocab, true, workspace_bytes);
   const size_t need = q.fixed + q.piece_tiles * T * 512;
   if (workspace_bytes < need) return done(call, nranks, T * V, dtype, 0, RRA_ERR_WORKSPACE);
-  std::vector<Range> in{{x, T * D * 2}, {targets, T * 8}, {lse, T * 4}, {grad_loss, T * 4}},
+  Ranges in{{x, T * D * 2}, {targets, T * 8}, {lse, T * 4}, {grad_loss, T * 4}},
       out{{workspace, need}, {dx, T * D * 2}};
   for (int r = 0; r < nranks; ++r) {
     in.push_back({weights[r], vocab[r] * D * 2});
@@ -784,7 +810,8 @@ rra_status_t rra_vocab_loss_backward(const void* x, const void* const* weights, 
   char* dl = ws.base + ws.at;
   const size_t ld = q.piece_tiles * 256;
 
-  auto p = std::make_unique<TcArgs>();
+  TcArgs args;
+  TcArgs* const p = &args;
   const size_t tiles = vocab_tiles(nranks, vocab);
   int grid = 0;
   cudaError_t e = cudaSuccess;
@@ -804,7 +831,7 @@ rra_status_t rra_vocab_loss_backward(const void* x, const void* const* weights, 
       col += vocab[r];
     }
     // dl of the piece
-    std::memset(p.get(), 0, sizeof(TcArgs));
+    std::memset(p, 0, sizeof(TcArgs));
     ok = map_k(&p->a[0], X);
     for (int r = 0; r < nranks && ok; ++r) {
       if (hi[r] <= lo[r]) continue;
@@ -817,10 +844,10 @@ rra_status_t rra_vocab_loss_backward(const void* x, const void* const* weights, 
       g.col0 = first[r];
       g.out = dl + at[r] * 2;
       g.ld = (long long)ld;
-      ok = ok && add_group(p.get(), g, false);
+      ok = ok && add_group(p, g, false);
     }
     if (!ok) return done(call, nranks, T * V, dtype, 0, RRA_ERR_CUDA);
-    one_k_axis(p.get(), D);
+    one_k_axis(p, D);
     p->targets = reinterpret_cast<const long long*>(targets);
     p->ignore_index = ignore_index;
     p->vocab = (long long)V;
@@ -831,7 +858,7 @@ rra_status_t rra_vocab_loss_backward(const void* x, const void* const* weights, 
     if (e != cudaSuccess) break;
 
     // dx (+)= dl W over the piece
-    std::memset(p.get(), 0, sizeof(TcArgs));
+    std::memset(p, 0, sizeof(TcArgs));
     size_t kb = 0;
     for (int r = 0; r < nranks && ok; ++r) {
       if (hi[r] <= lo[r]) continue;
@@ -855,14 +882,14 @@ rra_status_t rra_vocab_loss_backward(const void* x, const void* const* weights, 
     g.ld = (long long)(acc ? slot_ld(D) : D);
     g.out = acc ? (void*)acc : dx;
     g.vec = acc || (aligned(dx, 16) && D % 8 == 0);
-    ok = ok && add_group(p.get(), g, false);
+    ok = ok && add_group(p, g, false);
     p->status = device_status();
     if (!ok) return done(call, nranks, T * V, dtype, 0, RRA_ERR_CUDA);
     e = launch_tc_input_grad(*p, q.acc, s, &grid);
     if (e != cudaSuccess) break;
 
     // dW of the piece's rows
-    std::memset(p.get(), 0, sizeof(TcArgs));
+    std::memset(p, 0, sizeof(TcArgs));
     ok = map_mn(&p->b[0], X);
     for (int r = 0; r < nranks && ok; ++r) {
       if (hi[r] <= lo[r]) continue;
@@ -875,10 +902,10 @@ rra_status_t rra_vocab_loss_backward(const void* x, const void* const* weights, 
       h.ld = (long long)D;
       h.out = static_cast<char*>(dweights[r]) + lo[r] * D * 2;
       h.vec = aligned(h.out, 16) && D % 8 == 0;
-      ok = ok && add_group(p.get(), h, false);
+      ok = ok && add_group(p, h, false);
     }
     if (!ok) return done(call, nranks, T * V, dtype, 0, RRA_ERR_CUDA);
-    one_k_axis(p.get(), T);
+    one_k_axis(p, T);
     p->status = device_status();
     e = launch_tc_weight_grad(*p, s, &grid);
   }
