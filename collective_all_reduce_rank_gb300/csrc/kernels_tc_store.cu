@@ -17,6 +17,8 @@ struct EpiStore {
     const int c0 = x.n * 256 + half * 128;
     const int rows = g.M - row0;
     const bool part = x.slot >= 0 && p.splits > 1;
+    const int row = row0 + (threadIdx.x & 31);
+    const float scale = p.row_scale && row < g.M ? p.row_scale[(long long)row * 4] : 1.f;
     if (F32 || part) {
       // float32 rows of the output, or the tile's own slot
       const long long ld = part ? 256 : g.ld;
@@ -29,6 +31,8 @@ struct EpiStore {
         float v[32];
         tc_ld32(addr + half * 128 + c, v);
         tc_ld_ready(v);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] *= scale;
         tc_store_f32(buf, v, o + c, ld, rows, part ? 32 : valid, part || g.vec, p.accumulate);
       }
     } else {
@@ -41,8 +45,12 @@ struct EpiStore {
         tc_ld32(addr + half * 128 + c, v);
         tc_ld32(addr + half * 128 + c + 32, w);
         tc_ld_ready(v);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] *= scale;
         tc_stage_bf16(buf, v, 0);
         tc_ld_ready(w);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) w[j] *= scale;
         tc_stage_bf16(buf, w, 4);
         tc_flush_bf16(buf, o + c, g.ld, rows, valid, g.vec, false);
       }

@@ -619,6 +619,10 @@ LossPlan loss_plan(int n, size_t T, size_t D, const size_t* vocab, bool back, si
     b.take(T * pad_ld(D) * 2);
     for (int r = 0; r < n; ++r) b.take(vocab[r] * pad_ld(D) * 2);
   }
+  if (back) {
+    b.take(T * sizeof(float4));
+    b.take(T * pad_ld(D) * 2);  // x s
+  }
   const size_t tiles = vocab_tiles(n, vocab);
   if (!back) {
     b.take(2 * tiles * T * sizeof(float2));
@@ -753,7 +757,6 @@ rra_status_t rra_vocab_loss(const void* x, const void* const* weights, const siz
   p->hit = static_cast<float*>(ws.take(T * 4));
   p->targets = reinterpret_cast<const long long*>(targets);
   p->ignore_index = ignore_index;
-  p->vocab = (long long)V;
   p->status = device_status();
   int grid = 0;
   cudaError_t e = launch_tc_lse(*p, s, &grid);
@@ -803,7 +806,11 @@ rra_status_t rra_vocab_loss_backward(const void* x, const void* const* weights, 
   const Mat X = place(x, T, D);
   Mat W[kMaxRanks];
   for (int r = 0; r < nranks; ++r) W[r] = place(weights[r], vocab[r], D);
-  bool ok = place.launch(s);
+  float4* rows = static_cast<float4*>(ws.take(T * sizeof(float4)));
+  const Mat XS{ws.take(T * pad_ld(D) * 2), T, D, pad_ld(D)};
+  bool ok = place.launch(s) &&
+            launch_loss_scale(x, weights, vocab, nranks, D, (int)T, reinterpret_cast<const long long*>(targets),
+                              ignore_index, lse, grad_loss, rows, const_cast<void*>(XS.p), XS.ld, s) == cudaSuccess;
   if (!ok) return done(call, nranks, T * V, dtype, 0, RRA_ERR_CUDA);
   float* slots = static_cast<float*>(ws.take(q.split.slot_bytes));
   float* acc = q.acc ? static_cast<float*>(ws.take(T * slot_ld(D) * 4)) : nullptr;
@@ -849,10 +856,7 @@ rra_status_t rra_vocab_loss_backward(const void* x, const void* const* weights, 
     if (!ok) return done(call, nranks, T * V, dtype, 0, RRA_ERR_CUDA);
     one_k_axis(p, D);
     p->targets = reinterpret_cast<const long long*>(targets);
-    p->ignore_index = ignore_index;
-    p->vocab = (long long)V;
-    p->lse = lse;
-    p->grad = grad_loss;
+    p->rows = rows;
     p->status = device_status();
     e = launch_tc_dlogits(*p, s, &grid);
     if (e != cudaSuccess) break;
@@ -876,6 +880,7 @@ rra_status_t rra_vocab_loss_backward(const void* x, const void* const* weights, 
     p->splits = q.split.splits;
     p->slots = slots;
     p->accumulate = t0 > 0;
+    p->row_scale = &rows->w;
     TcGroup g{};
     g.M = (int)T;
     g.N = (int)D;
@@ -888,9 +893,9 @@ rra_status_t rra_vocab_loss_backward(const void* x, const void* const* weights, 
     e = launch_tc_input_grad(*p, q.acc, s, &grid);
     if (e != cudaSuccess) break;
 
-    // dW of the piece's rows
+    // dW of the piece's rows, from x s
     std::memset(p, 0, sizeof(TcArgs));
-    ok = map_mn(&p->b[0], X);
+    ok = map_mn(&p->b[0], XS);
     for (int r = 0; r < nranks && ok; ++r) {
       if (hi[r] <= lo[r]) continue;
       const Mat A{dl + at[r] * 2, T, hi[r] - lo[r], ld};

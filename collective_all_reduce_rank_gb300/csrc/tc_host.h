@@ -50,9 +50,9 @@ struct TcArgs {
   int accumulate;  // add to the float32 outputs
   int act;
   const long long* targets;
-  long long ignore_index, vocab;
-  const float* lse;
-  const float* grad;
+  long long ignore_index;
+  const float4* rows;      // backward: what loss_scale_kernel left per row
+  const float* row_scale;  // products of one group: factor of each output row, every 4th float (null: none)
   float2* part;      // [column part][part_ld] running maximum and sum
   long long part_ld;
   float* hit;        // logit of the row's target
@@ -123,6 +123,12 @@ cudaError_t launch_join_tiles(const JoinTiles& j, cudaStream_t s);
 __host__ __device__
 #endif
 inline int tc_units(const TcArgs& p) { return p.full + (p.tiles - p.full) * p.splits; }
+// Per row of the loss's backward pass: rows[t] = {lse / log 2 + log2(1 - p),
+// e at the target, 1 or 0 (no gradient), s}, and x s as bfloat16 rows of ld.
+cudaError_t launch_loss_scale(const void* x, const void* const* w, const size_t* vocab, int n, size_t hidden,
+                              int tokens, const long long* targets, long long ignore_index, const float* lse,
+                              const float* grad, float4* rows, void* xs, size_t ld, cudaStream_t s);
+
 // Rows of `cols` elements of each src to rows of 8 * units elements of dst.
 struct PadArgs {
   const void* src[kTcMaxGroups + 1];
