@@ -205,6 +205,17 @@ __device__ __forceinline__ uint2 encode_unit(const float* f, int* e) {
   return make_uint2(w[0], w[1]);
 }
 
+// Ask L2 for the line of unit u of every rank's row that this CTA takes next
+// (one lane per 128-byte line): it arrives while the CTA joins and stores the
+// present one.
+template <int N>
+__device__ __forceinline__ void prefetch_ranks(const void* const* in, size_t row_off, size_t u) {
+  if ((threadIdx.x & 7) != 0) return;
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(in[k]) + row_off + u * 16));
+}
+
 // The sum over ranks of one unit.
 template <int N, int DT>
 __device__ __forceinline__ void sum_ranks(const void* const* in, size_t row_off, size_t u, int valid, bool vec, Acc& s) {
@@ -461,6 +472,8 @@ __global__ void __launch_bounds__(kN8Threads, 2) back8_reg_kernel(const __grid_c
       float h[PU], g[PU];
       code_floats<DT>(code[j], mul[j], h);
       load_gamma<DT>(a.gamma, u, PU, true, g);
+      if (row + gridDim.x < a.rows)
+        prefetch_ranks<N>(a.in, row_off + (size_t)gridDim.x * a.hidden * Elem<DT>::kSize, u);
 #pragma unroll
       for (int i = 0; i < PU; ++i) {
         dy[j][i] = __uint_as_float(s.w[i]);
@@ -500,7 +513,7 @@ __global__ void __launch_bounds__(kN8Threads, 2) back8_reg_kernel(const __grid_c
 }
 
 template <int N, int DT>
-__global__ void __launch_bounds__(kN8MaxThreads) back8_gen_kernel(const __grid_constant__ Back8Args a) {
+__global__ void __launch_bounds__(kN8MaxThreads, N >= 6 ? 2 : 3) back8_gen_kernel(const __grid_constant__ Back8Args a) {
   constexpr int PU = Elem<DT>::kPerUnit;
   extern __shared__ __align__(16) char smem[];  // PU float32 per unit: the row's summed gradient
   __shared__ float s_part[2][kN8MaxThreads / 32];
@@ -525,6 +538,8 @@ __global__ void __launch_bounds__(kN8MaxThreads) back8_gen_kernel(const __grid_c
       load_gamma<DT>(a.gamma, u, v, a.vec, g);
       Acc s;
       sum_ranks<N, DT>(a.in, row_off, u, v, a.vec, s);
+      if (row + gridDim.x < a.rows)
+        prefetch_ranks<N>(a.in, row_off + (size_t)gridDim.x * hidden * Elem<DT>::kSize, u);
       float4* sm = reinterpret_cast<float4*>(smem + u * PU * 4);
 #pragma unroll
       for (int i = 0; i < PU; ++i) {
@@ -623,10 +638,18 @@ static cudaError_t save_go(Save8Args a, cudaStream_t s) {
   return launch_pdl(save8_gen_kernel<N, DT>, (int)a.rows, kN8Threads, smem, s, a);
 }
 
+// CTAs of the backward kernel: all resident, every CTA the same number of
+// rows but for the last.
+static int even_ctas(size_t rows, int most, int resident) {
+  const size_t cap = most < resident ? most : resident;
+  const size_t per = (rows + cap - 1) / cap;
+  return (int)((rows + per - 1) / per);
+}
+
 template <int N, int DT>
 static cudaError_t back_go(const Back8Args& a, int* ctas, cudaStream_t s) {
   if (fits_regs(DT, a.vec, a.hidden)) {
-    *ctas = *ctas < 2 * device_sms() ? *ctas : 2 * device_sms();
+    *ctas = even_ctas(a.rows, *ctas, 2 * device_sms());
     return launch_pdl(back8_reg_kernel<N, DT>, *ctas, kN8Threads, 0, s, a);
   }
   static const cudaError_t attr =
@@ -636,6 +659,11 @@ static cudaError_t back_go(const Back8Args& a, int* ctas, cudaStream_t s) {
   const int units = (int)((a.hidden + 16 / Elem<DT>::kSize - 1) / (16 / Elem<DT>::kSize));
   const int trips = (units + kN8MaxThreads - 1) / kN8MaxThreads;
   const int threads = ((units + trips - 1) / trips + 31) / 32 * 32;
+  int occ = 0;
+  const cudaError_t err =
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, back8_gen_kernel<N, DT>, threads, row_smem(a.hidden));
+  if (err != cudaSuccess) return err;
+  *ctas = even_ctas(a.rows, *ctas, (occ > 0 ? occ : 1) * device_sms());
   return launch_pdl(back8_gen_kernel<N, DT>, *ctas, threads, row_smem(a.hidden), s, a);
 }
 

@@ -259,7 +259,10 @@ static cudaError_t gate_go(const SkinnyArgs& a, int act, int grid, cudaStream_t 
 }
 
 cudaError_t launch_skinny_gate(const SkinnyArgs& a, int act, cudaStream_t s, int* grid) {
-  *grid = skinny_grid(a.units);
+  // a CTA per unit: nothing carries over from unit to unit, and the last
+  // units spread over all SMs (1728 units on 304 resident CTAs would take 6
+  // trips for 5.7)
+  *grid = max_ctas_cap() > 0 && max_ctas_cap() < a.units ? max_ctas_cap() : a.units;
   const bool vec = a.hidden % 8 == 0;  // the matrices themselves are 16-byte aligned
   if (a.tokens <= 8) return vec ? gate_go<1, true>(a, act, *grid, s) : gate_go<1, false>(a, act, *grid, s);
   return vec ? gate_go<2, true>(a, act, *grid, s) : gate_go<2, false>(a, act, *grid, s);
