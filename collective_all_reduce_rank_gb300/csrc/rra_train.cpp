@@ -107,8 +107,20 @@ struct Placer {
   bool launch(cudaStream_t s) { return a.n == 0 || launch_pad_rows(a, s) == cudaSuccess; }
 };
 
-bool map_k(CUtensorMap* m, const Mat& x) { return tc_map(m, x.p, x.cols, x.rows, x.ld, false); }
-bool map_mn(CUtensorMap* m, const Mat& x) { return tc_map(m, x.p, x.cols, x.rows, x.ld, true); }
+bool map_k(CUtensorMap* m, const Mat& x, int box = 128) { return tc_map(m, x.p, x.cols, x.rows, x.ld, false, box); }
+bool map_mn(CUtensorMap* m, const Mat& x) { return tc_map(m, x.p, x.cols, x.rows, x.ld, true, 64); }
+
+void clear(TcArgs* p) { *p = TcArgs{}; }
+
+// What a product of `tokens` rows of A stages.
+TcShape pick_shape(size_t tokens) {
+  TcShape q;
+  if (tokens > 128) return q;
+  q.a_rows = (int)up(tokens, 8);
+  q.a_ctas = 1;
+  q.stages = 6 * 32768 / (q.a_rows * 128 + 16384);  // 8 rows: 11, below kTcMaxStages
+  return q;
+}
 
 // How an input gradient's tiles are spread over the clusters: `full` whole
 // tiles in whole waves, and the rest split into `splits` parts of the K axis
@@ -143,10 +155,10 @@ Split pick_split(size_t tokens, size_t hidden, size_t kblocks) {
   return q;
 }
 
-bool add_group(TcArgs* p, const TcGroup& g0, bool narrow) {
+bool add_group(TcArgs* p, const TcGroup& g0, bool pair) {
   TcGroup g = g0;
   g.mt = (int)tiles256((size_t)g.M);
-  g.nt = narrow ? (g.N + 127) / 128 : (int)tiles256((size_t)g.N);
+  g.nt = pair ? (g.N + 127) / 128 : (int)tiles256((size_t)g.N);
   const long long t = (long long)g.mt * g.nt + p->tiles;
   if (t > INT_MAX / 2 || p->ngroups >= kTcMaxGroups) return false;
   g.tile0 = p->tiles;
@@ -197,12 +209,12 @@ rra_status_t done(const char* call, int n, size_t count, int dt, int grid, rra_s
 // shared with the kernels
 // ---------------------------------------------------------------------------
 
-bool rra::tc_map(CUtensorMap* m, const void* base, size_t inner, size_t rows, size_t ld, bool mn_major) {
+bool rra::tc_map(CUtensorMap* m, const void* base, size_t inner, size_t rows, size_t ld, bool mn_major, int box_rows) {
   const Fn fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[2] = {inner, rows};
   const cuuint64_t strides[1] = {ld * 2};
-  const cuuint32_t box[2] = {64, mn_major ? 64u : 128u};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
   const cuuint32_t es[2] = {1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -431,10 +443,11 @@ rra_status_t rra_gated_ffn(const void* x, const void* const* gates, const void* 
   Bump ws{static_cast<char*>(workspace)};
   TcArgs args;
   TcArgs* const p = &args;
-  std::memset(p, 0, sizeof(TcArgs));
+  clear(p);
+  p->shape = pick_shape(T);
   Placer place(ws);
   const Mat X = place(x, T, D);
-  bool ok = map_k(&p->a[0], X);
+  bool ok = map_k(&p->a[0], X, p->shape.a_rows);
   for (int r = 0; r < nranks && ok; ++r) {
     const Mat G = place(gates[r], F, D), U = place(ups[r], F, D);
     ok = map_k(&p->b[2 * r], G) && map_k(&p->b[2 * r + 1], U);
@@ -505,8 +518,9 @@ rra_status_t rra_gated_ffn_backward(const void* x, const void* const* gates, con
   // dg, du
   TcArgs args;
   TcArgs* const p = &args;
-  std::memset(p, 0, sizeof(TcArgs));
-  bool ok = map_k(&p->a[0], X);
+  clear(p);
+  p->shape = pick_shape(T);
+  bool ok = map_k(&p->a[0], X, p->shape.a_rows);
   for (int r = 0; r < nranks && ok; ++r) {
     ok = map_k(&p->b[2 * r], W[2 * r]) && map_k(&p->b[2 * r + 1], W[2 * r + 1]);
     TcGroup g{};
@@ -531,7 +545,7 @@ rra_status_t rra_gated_ffn_backward(const void* x, const void* const* gates, con
   if (e != cudaSuccess) return done(call, nranks, count, dtype, grid, RRA_ERR_CUDA);
 
   // dx: the shards' products as segments of one K axis
-  std::memset(p, 0, sizeof(TcArgs));
+  clear(p);
   p->nsegs = 2 * nranks;
   for (int i = 0; i < 2 * nranks && ok; ++i) {
     ok = map_k(&p->a[i], dW[i]) && map_mn(&p->b[i], W[i]);
@@ -556,7 +570,7 @@ rra_status_t rra_gated_ffn_backward(const void* x, const void* const* gates, con
   if (e != cudaSuccess) return done(call, nranks, count, dtype, grid, RRA_ERR_CUDA);
 
   // dG, dU
-  std::memset(p, 0, sizeof(TcArgs));
+  clear(p);
   ok = map_mn(&p->b[0], X);
   for (int i = 0; i < 2 * nranks && ok; ++i) {
     ok = map_mn(&p->a[i], dW[i]);
@@ -729,10 +743,11 @@ rra_status_t rra_vocab_loss(const void* x, const void* const* weights, const siz
   }
   TcArgs args;
   TcArgs* const p = &args;
-  std::memset(p, 0, sizeof(TcArgs));
+  clear(p);
+  p->shape = pick_shape(T);
   Placer place(ws);
   const Mat X = place(x, T, D);
-  bool ok = map_k(&p->a[0], X);
+  bool ok = map_k(&p->a[0], X, p->shape.a_rows);
   long long col0 = 0;
   int parts = 0;
   for (int r = 0; r < nranks && ok; ++r) {
@@ -838,8 +853,9 @@ rra_status_t rra_vocab_loss_backward(const void* x, const void* const* weights, 
       col += vocab[r];
     }
     // dl of the piece
-    std::memset(p, 0, sizeof(TcArgs));
-    ok = map_k(&p->a[0], X);
+    clear(p);
+    p->shape = pick_shape(T);
+    ok = map_k(&p->a[0], X, p->shape.a_rows);
     for (int r = 0; r < nranks && ok; ++r) {
       if (hi[r] <= lo[r]) continue;
       ok = map_k(&p->b[r], W[r]);
@@ -862,7 +878,7 @@ rra_status_t rra_vocab_loss_backward(const void* x, const void* const* weights, 
     if (e != cudaSuccess) break;
 
     // dx (+)= dl W over the piece
-    std::memset(p, 0, sizeof(TcArgs));
+    clear(p);
     size_t kb = 0;
     for (int r = 0; r < nranks && ok; ++r) {
       if (hi[r] <= lo[r]) continue;
@@ -894,7 +910,7 @@ rra_status_t rra_vocab_loss_backward(const void* x, const void* const* weights, 
     if (e != cudaSuccess) break;
 
     // dW of the piece's rows, from x s
-    std::memset(p, 0, sizeof(TcArgs));
+    clear(p);
     ok = map_mn(&p->b[0], XS);
     for (int r = 0; r < nranks && ok; ++r) {
       if (hi[r] <= lo[r]) continue;

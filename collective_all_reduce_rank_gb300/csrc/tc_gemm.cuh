@@ -12,9 +12,9 @@
 // Both 256-column accumulators of a CTA's 512 tensor-memory columns are
 // used: the epilogue of one tile runs under the products of the next.
 //
-// Roles (12 warps): warp 0 issues the TMA loads of its CTA's halves into a
-// ring of 64-deep K stages; warp 1 of the first CTA issues the products;
-// warp 2 owns the tensor-memory allocation; warps 4-11 are the epilogue
+// Roles (12 warps): warps 0 and 3 issue the TMA loads of their CTA's halves
+// of A and B into a ring of 64-deep K stages; warp 1 of the first CTA issues
+// the products; warp 2 owns the tensor-memory allocation; warps 4-11 are the epilogue
 // (warp w reads the 32 lanes of quadrant w % 4 and one half of the columns).
 //
 // Operands are K-major (rows of K contiguous: activations times weights) or
@@ -45,9 +45,11 @@ constexpr int kTcEpiWarps = 8;
 constexpr int kTcBK = kTcKBlock;
 constexpr int kTcHalfBytes = 128 * kTcBK * 2;  // one operand's half tile of a CTA
 constexpr int kTcStageBytes = 2 * kTcHalfBytes;
-constexpr int kTcStages = 6;
+constexpr int kTcStages = 6;      // of full halves; narrower ones fit up to
+constexpr int kTcMaxStages = 12;  // this many in the same bytes
+constexpr int kTcRingBytes = kTcStages * kTcStageBytes;
 constexpr int kTcStoreBytes = 4096;  // store staging of one epilogue warp (tc_epilogue.cuh)
-constexpr int kTcSmem = kTcStages * kTcStageBytes + kTcEpiWarps * kTcStoreBytes + 1024;  // + alignment slack
+constexpr int kTcSmem = kTcRingBytes + kTcEpiWarps * kTcStoreBytes + 1024;  // + alignment slack
 constexpr unsigned long long kTcWaitNs = 2000ull * 1000 * 1000;
 
 // ---------------------------------------------------------------------------
@@ -202,8 +204,8 @@ constexpr uint32_t kTcIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((AMN ? 1u : 
 // bounded waits
 // ---------------------------------------------------------------------------
 struct TcShared {
-  alignas(8) uint64_t full[kTcStages];
-  alignas(8) uint64_t empty[kTcStages];
+  alignas(8) uint64_t full[kTcMaxStages];
+  alignas(8) uint64_t empty[kTcMaxStages];
   alignas(8) uint64_t acc_full[2];
   alignas(8) uint64_t acc_empty[2];
   uint32_t tmem;
@@ -294,7 +296,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
   const int total = tc_units(p);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kTcStages; ++s) {
+    for (int s = 0; s < p.shape.stages; ++s) {
       tc_bar_init(tc_smem(&sh.full[s]), 1);
       tc_bar_init(tc_smem(&sh.empty[s]), 1);
     }
@@ -318,41 +320,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
   pdl_wait();
   pdl_next();
 
-  uint32_t issued = 0;  // producer: stages loaded so far
-  if (warp == 0) {
-    if (lane == 0) {
+  // a stage holds B's half, then A's; an A shorter than 128 rows is read on
+  // into the next stage or the store staging behind the ring
+  const int nstages = p.shape.stages;
+  constexpr uint32_t bbytes = kTcHalfBytes;
+  const uint32_t abytes = AMN ? kTcHalfBytes : (uint32_t)p.shape.a_rows * 128;
+  const uint32_t stage_bytes = abytes + bbytes;
+  uint32_t issued = 0;  // producers: stages loaded so far
+  if (warp == 0 || warp == 3) {
+    // warp 0 loads A and announces each stage's bytes, warp 3 loads B.  With
+    // one thread issuing both, the tensor pipe was 96% active with two boxes a
+    // stage, 89% with three and 73% with the four of two MN-major operands
+    // (backward of 4096 x 5120 x 4 x 3456: 1.87 ms, with two threads 1.82 ms)
+    const bool is_a = warp == 0;
+    if (lane == 0 && (!is_a || rank == 0 || AMN || p.shape.a_ctas > 1)) {
+      const uint32_t full0 = tc_smem(&sh.full[0]), empty0 = tc_smem(&sh.empty[0]);
+      const uint32_t lead0 = tc_mapa(full0, 0);
+      const uint32_t dst0 = is_a ? stages + bbytes : stages;
+      const uint32_t bytes = 2 * bbytes + (AMN ? 2u : (uint32_t)p.shape.a_ctas) * abytes;
+      int s = 0;
+      uint32_t parity = 1;
       bool ok = true;
       for (int t = cluster; t < total && ok; t += clusters) {
         const TcTile x = tc_tile(p, t);
         const TcGroup& g = p.group[x.group];
+        const int mn0 = is_a ? g.m0 + x.m * 256 + (int)rank * 128
+                             : g.n0 + (p.pair_b ? x.n * 128 : x.n * 256 + (int)rank * 128);
         int seg = 0;
-        for (int k = x.k0; k < x.k1; ++k, ++issued) {
+        for (int k = x.k0; k < x.k1 && ok;) {
           while (seg + 1 < p.nsegs && k >= p.seg_k0[seg + 1]) ++seg;
-          const int kk = (k - p.seg_k0[seg]) * kTcBK;
-          const int s = issued % kTcStages;
-          const uint32_t round = issued / kTcStages;
-          if (!tc_wait(tc_smem(&sh.empty[s]), (round & 1) ^ 1, &sh, p.status, 1)) {
-            ok = false;
-            break;
-          }
-          if (rank == 0) tc_bar_expect(tc_smem(&sh.full[s]), 2 * kTcStageBytes);
-          const uint32_t bar = tc_mapa(tc_smem(&sh.full[s]), 0);
-          const uint32_t sa = stages + s * kTcStageBytes, sb = sa + kTcHalfBytes;
-          const CUtensorMap* ma = &p.a[p.nsegs > 1 ? seg : g.a];
-          const CUtensorMap* mb = &p.b[p.nsegs > 1 ? seg : (p.pair_b ? g.b + (int)rank : g.b)];
-          const int m0 = g.m0 + x.m * 256 + (int)rank * 128;
-          const int n0 = g.n0 + (p.pair_b ? x.n * 128 : x.n * 256 + (int)rank * 128);
-          if constexpr (AMN) {
-            tc_tma_load(ma, sa, bar, m0, kk);
-            tc_tma_load(ma, sa + kTcHalfBytes / 2, bar, m0 + 64, kk);
-          } else {
-            tc_tma_load(ma, sa, bar, kk, m0);
-          }
-          if constexpr (BMN) {
-            tc_tma_load(mb, sb, bar, n0, kk);
-            tc_tma_load(mb, sb + kTcHalfBytes / 2, bar, n0 + 64, kk);
-          } else {
-            tc_tma_load(mb, sb, bar, kk, n0);
+          const int from = p.seg_k0[seg];
+          const int to = seg + 1 < p.nsegs ? min(x.k1, p.seg_k0[seg + 1]) : x.k1;
+          const CUtensorMap* map = is_a ? &p.a[p.nsegs > 1 ? seg : g.a]
+                                        : &p.b[p.nsegs > 1 ? seg : (p.pair_b ? g.b + (int)rank : g.b)];
+          for (int kk = (k - from) * kTcBK; k < to; ++k, kk += kTcBK, ++issued) {
+            if (!tc_wait(empty0 + 8 * s, parity, &sh, p.status, 1)) {
+              ok = false;
+              break;
+            }
+            if (is_a && rank == 0) tc_bar_expect(full0 + 8 * s, bytes);
+            const uint32_t dst = dst0 + s * stage_bytes, bar = lead0 + 8 * s;
+            if (is_a ? AMN : BMN) {
+              tc_tma_load(map, dst, bar, mn0, kk);
+              tc_tma_load(map, dst + kTcHalfBytes / 2, bar, mn0 + 64, kk);
+            } else {
+              tc_tma_load(map, dst, bar, kk, mn0);
+            }
+            if (++s == nstages) {
+              s = 0;
+              parity ^= 1;
+            }
           }
         }
       }
@@ -360,7 +377,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     if (rank == 0 && lane == 0) {
-      uint32_t it = 0, tile = 0;
+      uint32_t tile = 0, round = 0;
+      int s = 0;
       bool ok = true;
       for (int t = cluster; t < total && ok; t += clusters) {
         int k0, k1;
@@ -369,19 +387,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         const uint32_t buf = tile & 1, d = tmem + buf * 256;
         if (!tc_wait(tc_smem(&sh.acc_empty[buf]), ((tile >> 1) & 1) ^ 1, &sh, p.status, 2)) break;
         tc_fence_after();
-        for (int k = k0; k < k1; ++k, ++it) {
-          const int s = it % kTcStages;
-          if (!tc_wait(tc_smem(&sh.full[s]), (it / kTcStages) & 1, &sh, p.status, 3)) {
+        for (int k = k0; k < k1; ++k) {
+          if (!tc_wait(tc_smem(&sh.full[s]), round & 1, &sh, p.status, 3)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sa = stages + s * kTcStageBytes, sb = sa + kTcHalfBytes;
+          const uint32_t sb = stages + s * stage_bytes, sa = sb + bbytes;
 #pragma unroll
           for (int i = 0; i < kTcBK / 16; ++i)
             tc_mma(d, tc_desc<AMN>(sa + i * (AMN ? 2048 : 32)), tc_desc<BMN>(sb + i * (BMN ? 2048 : 32)),
                    kTcIdesc<AMN, BMN>, (uint32_t)(k > k0 || i > 0));
           tc_commit(tc_smem(&sh.empty[s]));
+          if (++s == nstages) {
+            s = 0;
+            ++round;
+          }
         }
         if (ok) tc_commit(tc_smem(&sh.acc_full[buf]));
         ++tile;
@@ -399,7 +420,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
       tc_fence_after();
       Epi::run(p, x, x.m * 256 + (int)rank * 128 + quad * 32, half,
                tmem + buf * 256 + ((uint32_t)(quad * 32) << 16),
-               raw + (stages - tc_smem(raw)) + kTcStages * kTcStageBytes + (warp - 4) * kTcStoreBytes);
+               raw + (stages - tc_smem(raw)) + kTcRingBytes + (warp - 4) * kTcStoreBytes);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) tc_bar_arrive_remote(tc_smem(&sh.acc_empty[buf]), 0);
@@ -408,11 +429,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
   }
 
   // teardown
-  if (warp == 0 && lane == 0 && sh.give_up) {
+  if (warp == 3 && lane == 0 && sh.give_up) {
     // copies of this CTA may be in flight: wait, bounded, for what was issued
-    const uint32_t first = issued > (uint32_t)kTcStages ? issued - kTcStages : 0;
+    const uint32_t first = issued > (uint32_t)nstages ? issued - nstages : 0;
     for (uint32_t i = first; i < issued; ++i)
-      for (int tries = 0; tries < 64 && !tc_bar_try(tc_smem(&sh.full[i % kTcStages]), (i / kTcStages) & 1); ++tries) {
+      for (int tries = 0; tries < 64 && !tc_bar_try(tc_smem(&sh.full[i % nstages]), (i / nstages) & 1); ++tries) {
       }
     __nanosleep(1000000);
   }

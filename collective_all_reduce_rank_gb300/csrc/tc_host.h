@@ -34,6 +34,18 @@ struct TcGroup {
   int part0;        // column tiles of the groups before this one
 };
 
+// What a CTA stages of A per K block.  Few tokens leave most of A's 128 rows
+// out of range: only the rows there are are loaded (the products read what
+// lies behind them, into rows of C that nobody reads), and the ring gets as
+// many stages as fit, so that more of the weights, which then bound the call,
+// are on their way (hidden 5120, 131072 columns, 17 tokens: 224 us with 6
+// stages, 213 with 10; 17 tokens through 8 x 1728 gated columns 60 and 56).
+struct TcShape {
+  int a_rows = 128;  // rows of A loaded per CTA
+  int a_ctas = 2;    // CTAs of the pair that have rows of A
+  int stages = 6;
+};
+
 struct TcArgs {
   CUtensorMap a[kTcMaxGroups];
   CUtensorMap b[kTcMaxGroups];
@@ -44,6 +56,7 @@ struct TcArgs {
   int full;     // the first `full` tiles of the walk take the whole K axis,
   int splits;   // the others one of `splits` parts of it at a time (tc_units)
   int kblocks;  // K blocks of 64 over all segments
+  TcShape shape;
   int pair_b;   // CTA c of a pair takes map b + c (gate and up weights), 128 columns per tile each
   // epilogue operands
   float* slots;    // split tiles: 256 x 256 float32 per part, part v of tile full + v / splits
@@ -66,8 +79,9 @@ int tc_clusters(int tiles);
 // Tensor maps over a dense matrix of bfloat16: `inner` contiguous elements,
 // `rows` rows, `ld` elements from row to row (a multiple of 8), 16-byte
 // aligned base.  K-major boxes are 64 x 128 (K x rows of M or N), MN-major
-// boxes 64 x 64 (M or N x rows of K).  False if the driver refuses.
-bool tc_map(CUtensorMap* m, const void* base, size_t inner, size_t rows, size_t ld, bool mn_major);
+// boxes 64 x 64 (M or N x rows of K).  `box`: rows of a K-major box.  False
+// if the driver refuses.
+bool tc_map(CUtensorMap* m, const void* base, size_t inner, size_t rows, size_t ld, bool mn_major, int box);
 
 // Products (kernels_vocab_loss.cu, kernels_gated_ffn.cu, kernels_tc_store.cu)
 cudaError_t launch_tc_lse(const TcArgs& p, cudaStream_t s, int* grid);        // K-major x K-major
