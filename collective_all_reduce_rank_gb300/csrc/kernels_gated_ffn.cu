@@ -10,6 +10,13 @@
 // backward pass computes g and u again the same way and its epilogue turns
 // them and da into dg = da u act'(g) and du = da act(g), rounded to
 // bfloat16 (operands of the two gradient products, kernels_tc_store.cu).
+//
+// Bound by the tensor cores from about 300 tokens (512 x 5120 x 8 x 1728: 84
+// us, 1.73 PFLOP/s; 224 tiles on 76 clusters are 2.95 waves), by the
+// weights' bytes below (17-256 tokens: 56-61 us, 5.0-4.6 TB/s: 112 tiles are
+// 1.5 waves and each tile's products take as long as its bytes); up to 16
+// tokens go through kernels_skinny.cu.  Tiles of 64 + 64 columns fill the
+// waves better but measured slower (65 us).
 #include "act.cuh"
 #include "tc_epilogue.cuh"
 

@@ -15,6 +15,9 @@
 // consecutive elements of a row (one 16-byte load) as the pairs of two
 // products, and the tokens (8 per product, read through L1) are taken in the
 // same order.  With 4 steps in flight a warp has 8 KB of loads outstanding.
+// Measured against the tensor-core tiles: one token through 8 x 1728 gated
+// columns of hidden 5120 47 us (6.0 TB/s) against 88, 8 tokens against
+// 131072 columns 200 us (6.7 TB/s) against 268.
 //
 // Gated: rows 0-7 of a unit are gate rows, rows 8-15 the same 8 up rows, so
 // a lane's accumulators hold g and u of one element.  Loss: 16 vocabulary

@@ -1,8 +1,16 @@
 // tc_gemm.cuh -- the tensor-core product the training operators are built
 // on: C[m][n] = sum_k A[m][k] B[n][k] in bfloat16 with float32 accumulators
-// in tensor memory, and an epilogue per operator that
-// turns the accumulators into what the operator stores, so that neither
-// logits nor projections are written to memory.
+// in tensor memory, and an epilogue per operator that turns the accumulators
+// into what the operator stores, so that neither logits nor projections are
+// written to memory.
+//
+// Bound.  A tile's 64-deep step is 512 cycles of the tensor pipe and moves 64
+// KB from L2 to its two SMs, 64 bytes a cycle each, which is about what L2
+// gives: both sides are near their limits, and everything else has to stay
+// out of the way.  Measured on one GB300 (ncu): tensor pipe 91-96% active in
+// all five products of a 2048-token step (hidden 5120); 4096 x 5120 x 4 x
+// 3456 gated backward 1.77 ms, 1.97 PFLOP/s; 2048 x 5120 x 131072 loss 1.36
+// ms, 2.02 PFLOP/s (library bfloat16 product of 8192^3: 1.87).
 //
 // Shape.  A cluster of two CTAs works on a 256 x 256 tile of C with
 // tcgen05.mma.cta_group::2: CTA c of the pair holds rows [128c, 128c+128)
@@ -14,8 +22,9 @@
 //
 // Roles (12 warps): warps 0 and 3 issue the TMA loads of their CTA's halves
 // of A and B into a ring of 64-deep K stages; warp 1 of the first CTA issues
-// the products; warp 2 owns the tensor-memory allocation; warps 4-11 are the epilogue
-// (warp w reads the 32 lanes of quadrant w % 4 and one half of the columns).
+// the products; warp 2 owns the tensor-memory allocation; warps 4-11 are the
+// epilogue (warp w reads the 32 lanes of quadrant w % 4 and one half of the
+// columns).
 //
 // Operands are K-major (rows of K contiguous: activations times weights) or
 // MN-major (rows of M or N contiguous: the transposed products of a
