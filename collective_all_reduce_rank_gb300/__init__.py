@@ -280,10 +280,14 @@ _torch_mod = None
 
 
 def _t():
-    global _torch_mod
+    """torch, and its tensor methods unbound (a call of one is cheaper than of
+    a bound one)."""
+    global _torch_mod, _data, _numel, _device, _dense
     if _torch_mod is None:
         import torch
 
+        t = torch.Tensor
+        _data, _numel, _device, _dense = t.data_ptr, t.numel, t.get_device, t.is_contiguous
         _torch_mod = torch
     return _torch_mod
 
@@ -298,22 +302,21 @@ def _refuse(what, t, dtype, shape, device):
 
 def _one(what, t, dtype, shape, device):
     """Pointer of a tensor of this type, shape and device, contiguous."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or _device(t) != device or not _dense(t):
         _refuse(what, t, dtype, shape, device)
-    return t.data_ptr()
+    return _data(t)
 
 
 def _flat(what, t, dtype, numel, device):
     """The same for a tensor of any shape with this many elements."""
-    if t.dtype is not dtype or t.numel() != numel or t.get_device() != device or not t.is_contiguous():
+    if t.dtype is not dtype or _numel(t) != numel or _device(t) != device or not _dense(t):
         _refuse(what, t, dtype, "%d elements" % numel, device)
-    return t.data_ptr()
+    return _data(t)
 
 
 def _ranks(what, ts, dtype, shape, device):
     """The pointers of one tensor per rank, as the C array of them."""
-    ps = [t.data_ptr() for t in ts
-          if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous()]
+    ps = [_data(t) for t in ts if t.dtype is dtype and t.shape == shape and _device(t) == device and _dense(t)]
     if len(ps) != len(ts):
         for t in ts:
             _one(what, t, dtype, shape, device)
@@ -322,8 +325,7 @@ def _ranks(what, ts, dtype, shape, device):
 
 def _flat_ranks(what, ts, dtype, numel, device):
     """The same for tensors of any shape with this many elements."""
-    ps = [t.data_ptr() for t in ts
-          if t.dtype is dtype and t.numel() == numel and t.get_device() == device and t.is_contiguous()]
+    ps = [_data(t) for t in ts if t.dtype is dtype and _numel(t) == numel and _device(t) == device and _dense(t)]
     if len(ps) != len(ts):
         for t in ts:
             _flat(what, t, dtype, numel, device)
@@ -449,6 +451,7 @@ def rra_gated_ffn(x, gates, ups, acts, act=RRA_ACT_SILU, workspace=None, stream=
     """acts[r] = act(x gates[r]^T) * (x ups[r]^T)."""
     n = len(gates)
     _same_count(n, ups, acts)
+    _t()
     T, D = x.shape
     F, dev, dt = gates[0].shape[0], x.get_device(), x.dtype
     gs = _ranks("a gate or up shard", gates, dt, (F, D), dev)
@@ -465,6 +468,7 @@ def rra_gated_ffn_backward(x, gates, ups, dacts, dx, dgates, dups, act=RRA_ACT_S
     """Gradients of rra_gated_ffn: dx summed over the ranks, dgates, dups."""
     n = len(gates)
     _same_count(n, ups, dacts, dgates, dups)
+    _t()
     T, D = x.shape
     F, dev, dt = gates[0].shape[0], x.get_device(), x.dtype
     gs = _ranks("a gate or up shard", gates, dt, (F, D), dev)
