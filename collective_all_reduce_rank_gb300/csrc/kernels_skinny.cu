@@ -8,16 +8,20 @@
 // next to as much padding, and 256 weight rows per tile leave some SMs idle;
 // here a unit of work is 16 weight rows, so every SM streams to the end.
 //
-// A CTA's 8 warps split the K axis of its unit (steps of 64 elements, warp w
-// every 8th) and add their partial sums through shared memory.  Weights go
+// KW of a CTA's 8 warps split the K axis of a unit (steps of 64 elements,
+// warp w every KW-th) and add their partial sums through shared memory; the
+// CTA has 8 / KW units at a time, so that short rows keep loads in flight too
+// (split_k).  Weights go
 // from global memory straight to the registers of mma.sync m16n8k16: the
 // sum over k does not care about the order of k, so each lane takes 8
 // consecutive elements of a row (one 16-byte load) as the pairs of two
 // products, and the tokens (8 per product, read through L1) are taken in the
 // same order.  With 4 steps in flight a warp has 8 KB of loads outstanding.
-// Measured against the tensor-core tiles: one token through 8 x 1728 gated
-// columns of hidden 5120 47 us (6.0 TB/s) against 88, 8 tokens against
-// 131072 columns 200 us (6.7 TB/s) against 268.
+// Measured against the tensor-core tiles, us: one token through 8 x 1728
+// gated columns of hidden 5120 / 1024 / 128 45 / 6.8 / 3.3 against 55 / 14 /
+// 7.9 (6.3 TB/s at 5120); 8 tokens against 131072 columns 200 / 49 / 14
+// against 204 / 51 / 24 (6.7 TB/s), against 5000 columns 17 / 9 / 8 against
+// 30 / 13 / 9.
 //
 // Gated: rows 0-7 of a unit are gate rows, rows 8-15 the same 8 up rows, so
 // a lane's accumulators hold g and u of one element.  Loss: 16 vocabulary
@@ -95,10 +99,10 @@ __device__ __forceinline__ uint4 sk_load(const char* row, int k, int cols, const
   }
 }
 
-// The 16 x 8 NT products of one unit: rows r0 (lane / 4) and r1 (8 + lane /
+// The 16 x 8 NT products of the unit of this warp's group of KW: rows r0 (lane / 4) and r1 (8 + lane /
 // 4) of this lane, in matrices that end at e0 and e1; each warp leaves its
 // share of the K axis in red[warp][16][8 NT].
-template <int NT, bool VEC>
+template <int NT, bool VEC, int KW>
 __device__ __forceinline__ void sk_unit(const SkinnyArgs& a, const char* r0, const char* e0, const char* r1,
                                         const char* e1, float (*red)[16 * 8 * NT]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -115,11 +119,11 @@ __device__ __forceinline__ void sk_unit(const SkinnyArgs& a, const char* r0, con
 #pragma unroll
     for (int i = 0; i < 4; ++i) c[n][i] = 0.f;
 
-  for (int s0 = warp; s0 < steps; s0 += kSkWarps * kSkDepth) {
+  for (int s0 = warp % KW; s0 < steps; s0 += KW * kSkDepth) {
     uint4 w[kSkDepth][4];
 #pragma unroll
     for (int u = 0; u < kSkDepth; ++u) {
-      const int k = (s0 + u * kSkWarps) * kSkStep + t * 8;
+      const int k = (s0 + u * KW) * kSkStep + t * 8;
       w[u][0] = sk_load<VEC, true>(r0, k, D, e0);
       w[u][1] = sk_load<VEC, true>(r1, k, D, e1);
       w[u][2] = sk_load<VEC, true>(r0, k + 32, D, e0);
@@ -127,7 +131,7 @@ __device__ __forceinline__ void sk_unit(const SkinnyArgs& a, const char* r0, con
     }
 #pragma unroll
     for (int u = 0; u < kSkDepth; ++u) {
-      const int k = (s0 + u * kSkWarps) * kSkStep + t * 8;
+      const int k = (s0 + u * KW) * kSkStep + t * 8;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint4 lo = w[u][2 * h], hi = w[u][2 * h + 1];
@@ -151,39 +155,48 @@ __device__ __forceinline__ void sk_unit(const SkinnyArgs& a, const char* r0, con
   __syncthreads();
 }
 
-template <int NT>
-__device__ __forceinline__ float sk_total(const float (*red)[16 * 8 * NT], int i) {
-  float v = red[0][i];
+// Value i of the unit of group `slot`.
+template <int NT, int KW>
+__device__ __forceinline__ float sk_total(const float (*red)[16 * 8 * NT], int slot, int i) {
+  float v = red[slot * KW][i];
 #pragma unroll
-  for (int w = 1; w < kSkWarps; ++w) v += red[w][i];
+  for (int w = 1; w < KW; ++w) v += red[slot * KW + w][i];
   return v;
 }
 
 // ---------------------------------------------------------------------------
 // gated projections
 // ---------------------------------------------------------------------------
-template <int NT, bool VEC, int ACT>
+template <int NT, bool VEC, int KW, int ACT>
 __global__ void __launch_bounds__(kSkThreads, 2) skinny_gate_kernel(const __grid_constant__ SkinnyArgs a) {
+  constexpr int SLOTS = kSkWarps / KW, PER = 8 * 8 * NT;  // units at a time, values per unit
   __shared__ float red[kSkWarps][16 * 8 * NT];
-  const int g = (threadIdx.x & 31) >> 2;
+  const int g = (threadIdx.x & 31) >> 2, mine = (threadIdx.x >> 5) / KW;
   const int per = (a.width + 7) / 8;  // units per rank
   const size_t bytes = (size_t)a.width * a.hidden * 2;
   pdl_wait();
   pdl_next();
-  for (int u = blockIdx.x; u < a.units; u += gridDim.x) {
-    const int r = u / per, f0 = (u - r * per) * 8;
-    const char* gb = static_cast<const char*>(a.w[2 * r]);
-    const char* ub = static_cast<const char*>(a.w[2 * r + 1]);
-    const size_t at = (size_t)(f0 + g) * a.hidden * 2;
-    const bool in = f0 + g < a.width;
-    sk_unit<NT, VEC>(a, in ? gb + at : nullptr, gb + bytes, in ? ub + at : nullptr, ub + bytes, red);
-    if (threadIdx.x < 8 * 8 * NT) {
-      const int token = threadIdx.x / 8, f = threadIdx.x % 8;  // neighbouring threads, neighbouring columns
-      const float gv = sk_total<NT>(red, f * 8 * NT + token), uv = sk_total<NT>(red, (8 + f) * 8 * NT + token);
+  for (int u0 = blockIdx.x * SLOTS; u0 < a.units; u0 += gridDim.x * SLOTS) {
+    {
+      const int u = u0 + mine, r = u / per, f = (u - r * per) * 8 + g;
+      const bool in = u < a.units && f < a.width;
+      const char* gb = static_cast<const char*>(in ? a.w[2 * r] : nullptr);
+      const char* ub = static_cast<const char*>(in ? a.w[2 * r + 1] : nullptr);
+      const size_t at = (size_t)f * a.hidden * 2;
+      sk_unit<NT, VEC, KW>(a, in ? gb + at : nullptr, gb + bytes, in ? ub + at : nullptr, ub + bytes, red);
+    }
+#pragma unroll
+    for (int i0 = 0; i0 < SLOTS * PER; i0 += kSkThreads) {
+      const int i = i0 + threadIdx.x;
+      if (SLOTS * PER % kSkThreads != 0 && i >= SLOTS * PER) break;
+      const int slot = i / PER, token = i % PER / 8, f = i % 8;  // neighbouring threads, neighbouring columns
+      const int u = u0 + slot, r = u / per, col = (u - r * per) * 8 + f;
+      if (u >= a.units || token >= a.tokens || col >= a.width) continue;
+      const float gv = sk_total<NT, KW>(red, slot, f * 8 * NT + token);
+      const float uv = sk_total<NT, KW>(red, slot, (8 + f) * 8 * NT + token);
       float unused;
-      const float y = gv * gate_sigma<ACT>(gv, &unused) * uv;
-      if (token < a.tokens && f0 + f < a.width)
-        static_cast<__nv_bfloat16*>(a.out[r])[(size_t)token * a.width + f0 + f] = __float2bfloat16_rn(y);
+      static_cast<__nv_bfloat16*>(a.out[r])[(size_t)token * a.width + col] =
+          __float2bfloat16_rn(gv * gate_sigma<ACT>(gv, &unused) * uv);
     }
     __syncthreads();
   }
@@ -192,49 +205,72 @@ __global__ void __launch_bounds__(kSkThreads, 2) skinny_gate_kernel(const __grid
 // ---------------------------------------------------------------------------
 // vocabulary statistics
 // ---------------------------------------------------------------------------
-template <int NT, bool VEC>
+template <int NT, bool VEC, int KW>
 __global__ void __launch_bounds__(kSkThreads, 2) skinny_lse_kernel(const __grid_constant__ SkinnyArgs a) {
-  __shared__ float red[kSkWarps][16 * 8 * NT];
-  __shared__ float2 run[16 * 8 * NT];
-  const int lane = threadIdx.x & 31, g = lane >> 2;
-  const int slot = threadIdx.x / (8 * NT), token = threadIdx.x % (8 * NT);  // row slot of the unit, token
-  const bool mine = slot < 16 && token < a.tokens;
+  constexpr int SLOTS = kSkWarps / KW, PER = 16 * 8 * NT;             // units at a time, values per unit
+  constexpr int EACH = (SLOTS * PER + kSkThreads - 1) / kSkThreads;  // values per thread
+  __shared__ float red[kSkWarps][PER];
+  __shared__ float2 run[kSkThreads];
+  const int lane = threadIdx.x & 31, g = lane >> 2, mine = (threadIdx.x >> 5) / KW;
+  // value i of the CTA's units: slot i / PER, row i % PER / (8 NT), token i % (8 NT); a thread's
+  // values are kSkThreads apart and so of one token
+  const int token = threadIdx.x % (8 * NT);
+  long long target = -1;
   pdl_wait();
   pdl_next();
-  long long target = -1;
-  if (mine) {
+  if (token < a.tokens) {
     target = a.targets[token];
     if (target == a.ignore_index) target = -1;
   }
   float m = -INFINITY, s = 0.f;
-  for (int u = blockIdx.x; u < a.units; u += gridDim.x) {
-    int r = 0;
-    while (u >= a.unit0[r + 1]) ++r;
-    const long long v0 = (long long)(u - a.unit0[r]) * 16;
-    const char* wb = static_cast<const char*>(a.w[r]);
-    const long long rows = a.rows[r];
-    const char* end = wb + (size_t)rows * a.hidden * 2;
-    const char* r0 = v0 + g < rows ? wb + (size_t)(v0 + g) * a.hidden * 2 : nullptr;
-    const char* r1 = v0 + g + 8 < rows ? wb + (size_t)(v0 + g + 8) * a.hidden * 2 : nullptr;
-    sk_unit<NT, VEC>(a, r0, end, r1, end, red);
-    if (mine && v0 + slot < rows) {
-      const float l = sk_total<NT>(red, slot * 8 * NT + token);
-      if (target == a.col0[r] + v0 + slot) a.hit[token] = l;
-      const float nm = fmaxf(m, l);
-      if (nm == -INFINITY) {
-        if (l != l) s = l;
-      } else {
-        s = s * expf(m - nm) + expf(l - nm);
-        m = nm;
+  for (int u0 = blockIdx.x * SLOTS; u0 < a.units; u0 += gridDim.x * SLOTS) {
+    {
+      const int u = u0 + mine;
+      int r = 0;
+      while (r + 1 < kMaxRanks && u >= a.unit0[r + 1]) ++r;
+      const long long v0 = (long long)(u - a.unit0[r]) * 16;
+      const long long rows = u < a.units ? a.rows[r] : 0;
+      const char* wb = static_cast<const char*>(a.w[r]);
+      const char* end = wb + (size_t)rows * a.hidden * 2;
+      const char* r0 = v0 + g < rows ? wb + (size_t)(v0 + g) * a.hidden * 2 : nullptr;
+      const char* r1 = v0 + g + 8 < rows ? wb + (size_t)(v0 + g + 8) * a.hidden * 2 : nullptr;
+      sk_unit<NT, VEC, KW>(a, r0, end, r1, end, red);
+    }
+    float l[EACH];
+    float q = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < EACH; ++j) {
+      const int i = j * kSkThreads + threadIdx.x, slot = i / PER, u = u0 + slot;
+      l[j] = -INFINITY;
+      if (i < SLOTS * PER && u < a.units && token < a.tokens) {
+        int r = 0;
+        while (u >= a.unit0[r + 1]) ++r;
+        const long long v = (long long)(u - a.unit0[r]) * 16 + i % PER / (8 * NT);
+        if (v < a.rows[r]) {
+          l[j] = sk_total<NT, KW>(red, slot, i % PER);
+          if (target == a.col0[r] + v) a.hit[token] = l[j];
+        }
       }
+      q = fmaxf(q, l[j]);
+    }
+    const float nm = fmaxf(m, q);
+    if (nm == -INFINITY) {
+#pragma unroll
+      for (int j = 0; j < EACH; ++j)
+        if (l[j] != l[j]) s = l[j];
+    } else {
+      s *= expf(m - nm);
+#pragma unroll
+      for (int j = 0; j < EACH; ++j) s += expf(l[j] - nm);
+      m = nm;
     }
     __syncthreads();
   }
-  if (slot < 16) run[threadIdx.x] = make_float2(m, s);
+  run[threadIdx.x] = make_float2(m, s);
   __syncthreads();
-  if (slot == 0 && mine) {
-    for (int i = 1; i < 16; ++i) {
-      const float2 q = run[i * 8 * NT + token];
+  if (threadIdx.x < 8 * NT && token < a.tokens) {
+    for (int i = token + 8 * NT; i < kSkThreads; i += 8 * NT) {
+      const float2 q = run[i];
       const float nm = fmaxf(m, q.x);
       if (nm == -INFINITY) {
         s += q.y;
@@ -255,28 +291,69 @@ int skinny_grid(long long units) {
   return (int)(units < cap ? units : cap);
 }
 
-template <int NT, bool VEC>
-static cudaError_t gate_go(const SkinnyArgs& a, int act, int grid, cudaStream_t s) {
-  if (act == RRA_ACT_SILU) return launch_pdl(skinny_gate_kernel<NT, VEC, RRA_ACT_SILU>, grid, kSkThreads, 0, s, a);
-  return launch_pdl(skinny_gate_kernel<NT, VEC, RRA_ACT_GELU_TANH>, grid, kSkThreads, 0, s, a);
+// Warps that share a row: the smallest power of two that leaves each at most
+// 2 kSkDepth steps of it and, where there are few units, fills the SMs.
+// (Measured, 8 tokens: 131072 columns of hidden 128 / 512 with 1 and 1 warps
+// 14 and 31 us, with 8 27 and 45; 5000 columns of hidden 512 with 1 warp 10
+// us, with 8 8.)
+static int split_k(int hidden, int units) {
+  const int steps = (hidden + kSkStep - 1) / kSkStep;
+  int kw = 1;
+  while (kw < kSkWarps && (kw * 2 * kSkDepth < steps ||
+                           (kw < steps && (long long)units * kw < 2ll * device_sms() * kSkWarps)))
+    kw *= 2;
+  return kw;
 }
 
-cudaError_t launch_skinny_gate(const SkinnyArgs& a, int act, cudaStream_t s, int* grid) {
-  // a CTA per unit: nothing carries over from unit to unit, and the last
-  // units spread over all SMs (1728 units on 304 resident CTAs would take 6
-  // trips for 5.7)
-  *grid = max_ctas_cap() > 0 && max_ctas_cap() < a.units ? max_ctas_cap() : a.units;
-  const bool vec = a.hidden % 8 == 0;  // the matrices themselves are 16-byte aligned
-  if (a.tokens <= 8) return vec ? gate_go<1, true>(a, act, *grid, s) : gate_go<1, false>(a, act, *grid, s);
-  return vec ? gate_go<2, true>(a, act, *grid, s) : gate_go<2, false>(a, act, *grid, s);
+template <int NT, bool VEC, int KW>
+static cudaError_t gate_kw(const SkinnyArgs& a, int act, int* grid, cudaStream_t s) {
+  // a CTA per group of units: nothing carries over from one to the next, and
+  // the last ones spread over all SMs (1728 units on 304 resident CTAs would
+  // take 6 trips for 5.7)
+  const int groups = (a.units + kSkWarps / KW - 1) / (kSkWarps / KW);
+  *grid = max_ctas_cap() > 0 && max_ctas_cap() < groups ? max_ctas_cap() : groups;
+  if (act == RRA_ACT_SILU)
+    return launch_pdl(skinny_gate_kernel<NT, VEC, KW, RRA_ACT_SILU>, *grid, kSkThreads, 0, s, a);
+  return launch_pdl(skinny_gate_kernel<NT, VEC, KW, RRA_ACT_GELU_TANH>, *grid, kSkThreads, 0, s, a);
 }
+
+template <int NT, bool VEC, int KW>
+static cudaError_t lse_kw(const SkinnyArgs& a, int act, int* grid, cudaStream_t s) {
+  (void)act;
+  return launch_pdl(skinny_lse_kernel<NT, VEC, KW>, *grid, kSkThreads, 0, s, a);
+}
+
+#define SK_PICK(fn, NT, VEC)                                  \
+  switch (split_k(a.hidden, a.units)) {                       \
+    case 1: return fn<NT, VEC, 1>(a, act, grid, s);           \
+    case 2: return fn<NT, VEC, 2>(a, act, grid, s);           \
+    case 4: return fn<NT, VEC, 4>(a, act, grid, s);           \
+    default: return fn<NT, VEC, 8>(a, act, grid, s);          \
+  }
+
+#define SK_LAUNCH(fn)                                                                   \
+  const bool vec = a.hidden % 8 == 0; /* the matrices themselves are 16-byte aligned */ \
+  if (a.tokens <= 8) {                                                                  \
+    if (vec) {                                                                          \
+      SK_PICK(fn, 1, true)                                                              \
+    } else {                                                                            \
+      SK_PICK(fn, 1, false)                                                             \
+    }                                                                                   \
+  } else if (vec) {                                                                     \
+    SK_PICK(fn, 2, true)                                                                \
+  } else {                                                                              \
+    SK_PICK(fn, 2, false)                                                               \
+  }
+
+cudaError_t launch_skinny_gate(const SkinnyArgs& a, int act, cudaStream_t s, int* grid) { SK_LAUNCH(gate_kw) }
 
 cudaError_t launch_skinny_lse(const SkinnyArgs& a, cudaStream_t s, int* grid) {
+  const int act = 0;
   *grid = skinny_grid(a.units);
-  const bool vec = a.hidden % 8 == 0;
-  if (a.tokens <= 8)
-    return launch_pdl(vec ? skinny_lse_kernel<1, true> : skinny_lse_kernel<1, false>, *grid, kSkThreads, 0, s, a);
-  return launch_pdl(vec ? skinny_lse_kernel<2, true> : skinny_lse_kernel<2, false>, *grid, kSkThreads, 0, s, a);
+  SK_LAUNCH(lse_kw)
 }
+
+#undef SK_PICK
+#undef SK_LAUNCH
 
 }  // namespace rra

@@ -354,11 +354,19 @@ rra_status_t rra_allreduce_rmsnorm_backward8(const void* const* grads, void* con
 namespace {
 
 // Workspace of a call, in the order the call takes it.
-bool skinny(size_t T, size_t D) { return T <= kSkinnyTokens && D >= kSkinnyHidden; }
+// Few tokens go through the register-streamed product (kernels_skinny.cu): up
+// to 8 always; 9 to 16, which it takes as two products per weight, where rows
+// are whole 16-byte units and, for the loss (`logits`: elements of its
+// weights), up to 2^27 weights (16 tokens, us, streamed against tiles: 8 x
+// 1728 gated columns of hidden 5120 53 and 56, of 1024 11 and 14; 131072
+// columns of hidden 1024 52 and 54, of 5120 228 and 208, of 1027 204 and 174).
+bool skinny(size_t T, size_t D, size_t logits) {
+  return T <= 8 || (T <= 16 && D % 8 == 0 && logits <= (size_t)1 << 27);
+}
 
 size_t ffn_bytes(int n, size_t T, size_t D, size_t F, bool back) {
   Bump b{nullptr};
-  if (padded(D) && (back || !skinny(T, D))) {
+  if (padded(D) && (back || !skinny(T, D, 0))) {
     b.take(T * pad_ld(D) * 2);
     for (int i = 0; i < 2 * n; ++i) b.take(F * pad_ld(D) * 2);
   }
@@ -422,7 +430,7 @@ rra_status_t rra_gated_ffn(const void* x, const void* const* gates, const void* 
   if (T == 0 || F == 0) return done(call, nranks, 0, dtype, 0, RRA_SUCCESS);
   if (!device_status()) return done(call, nranks, count, dtype, 0, RRA_ERR_NOT_INITIALIZED);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (skinny(T, D)) {
+  if (skinny(T, D, 0)) {
     SkinnyArgs a{};
     a.x = x;
     a.tokens = (int)T;
@@ -614,6 +622,12 @@ struct LossPlan {
   bool acc = false;        // dx is summed over pieces in float32
 };
 
+size_t vocab_rows(int n, const size_t* vocab) {
+  size_t v = 0;
+  for (int r = 0; r < n; ++r) v += vocab[r];
+  return v;
+}
+
 long long skinny_units(int n, const size_t* vocab) {
   long long u = 0;
   for (int r = 0; r < n; ++r) u += (long long)((vocab[r] + 15) / 16);
@@ -623,7 +637,7 @@ long long skinny_units(int n, const size_t* vocab) {
 LossPlan loss_plan(int n, size_t T, size_t D, const size_t* vocab, bool back, size_t room) {
   LossPlan q;
   Bump b{nullptr};
-  if (!back && skinny(T, D)) {
+  if (!back && skinny(T, D, vocab_rows(n, vocab) * D)) {
     b.take((size_t)skinny_grid(skinny_units(n, vocab)) * T * sizeof(float2));
     b.take(T * 4);
     q.fixed = b.at;
@@ -715,7 +729,7 @@ rra_status_t rra_vocab_loss(const void* x, const void* const* weights, const siz
   if (!device_status()) return done(call, nranks, T * V, dtype, 0, RRA_ERR_NOT_INITIALIZED);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   Bump ws{static_cast<char*>(workspace)};
-  if (skinny(T, D)) {
+  if (skinny(T, D, V * D)) {
     SkinnyArgs a{};
     a.x = x;
     a.tokens = (int)T;

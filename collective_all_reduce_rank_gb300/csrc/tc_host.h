@@ -95,10 +95,7 @@ cudaError_t launch_tc_input_grad(const TcArgs& p, bool f32, cudaStream_t s, int*
 // out = A^T B, both MN-major (the gradient of the weights): bfloat16 rows.
 cudaError_t launch_tc_weight_grad(const TcArgs& p, cudaStream_t s, int* grid);
 
-// Few tokens (kernels_skinny.cu): at most kSkinnyTokens, hidden of
-// kSkinnyHidden or more.
-constexpr size_t kSkinnyTokens = 16;
-constexpr size_t kSkinnyHidden = 512;
+// Few tokens (kernels_skinny.cu): at most 16 (rra_train.cpp says when).
 struct SkinnyArgs {
   const void* x;
   const void* w[2 * kMaxRanks];  // gate and up shards in turn, or vocabulary shards

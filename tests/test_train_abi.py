@@ -96,7 +96,7 @@ FFN_BAD = [
     (dict(D=0), INV), (dict(act=2), INV), (dict(dtype=F32), UNS), (dict(dtype=I32), UNS), (dict(dtype=9), INV),
     (dict(T=1 << 31), UNS), (dict(F=1 << 31), UNS), (dict(gates=[at(1), None]), INV),
     (dict(gates=[at(1) + 8, at(2)]), UNS), (dict(ups=[at(3) + 1, at(4)]), INV), (dict(ws=at(30) + 8), INV),
-    (dict(D=257, ws_bytes=8), WS), (dict(D=257, ws=None), INV),
+    (dict(T=64, D=257, ws_bytes=8), WS), (dict(T=64, D=257, ws=None), INV),
 ]
 
 

@@ -49,7 +49,7 @@ def cuda(ts):
 # -- gated feed-forward ------------------------------------------------------
 
 FFN = [  # n, tokens, hidden, width, act
-    (1, 1, 64, 128, 0), (1, 128, 64, 128, 0), (1, 256, 256, 128, 1), (2, 256, 128, 256, 0), (1, 300, 200, 130, 1),
+    (1, 1, 64, 128, 0), (1, 128, 64, 128, 0), (2, 24, 64, 40, 1), (1, 256, 256, 128, 1), (2, 256, 128, 256, 0), (1, 300, 200, 130, 1),
     (3, 77, 88, 33, 0), (2, 1, 512, 520, 1), (8, 16, 128, 40, 0), (2, 129, 1027, 65, 0), (3, 5, 7, 3, 1),
     (2, 513, 640, 384, 0), (1, 1, 1, 1, 0), (4, 700, 72, 1000, 0),
     # few tokens: the register path, rows on and off 16 bytes
