@@ -51,39 +51,60 @@ __device__ __forceinline__ void sk_mma(float* c, uint32_t a0, uint32_t a1, uint3
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint4 sk_ldg(const void* p, bool stream) {
+// Rows that are not whole 16-byte units (VEC false) start on any element,
+// but rows v, v + 8, v + 16, ... of a matrix start at the same offset from 16
+// bytes.  A unit then takes such rows, and its K axis is counted from the
+// 16-byte block in which they start: position k of the unit is element k -
+// off, off = (v cols) mod 8.  Weights are loaded as aligned blocks all the
+// same; only the tokens, which all rows share, are shifted.  (With rows side
+// by side, each of them shifted from two blocks, 8 tokens against 131072
+// columns of hidden 1027 took 154 us.)
+
+// Weight positions [k, k + 8) of a row at `row` (its first element), zeros
+// outside the row (or for a null row).  The blocks that hold a row's first
+// and last elements hold bytes of the matrix, so no load leaves it but inside
+// such a block.
+template <bool VEC>
+__device__ __forceinline__ uint4 sk_weights(const char* row, int k, int off, int cols) {
+  const int e = k - off;
+  if (!row || e >= cols) return make_uint4(0u, 0u, 0u, 0u);
   uint4 v;
-  if (stream)
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-  else
-    v = __ldg(static_cast<const uint4*>(p));
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(row + (long long)e * 2));
+  if (!VEC && (e < 0 || e + 8 > cols)) {
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (e + j < 0 || e + j >= cols) w[j >> 1] &= j & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+    v = make_uint4(w[0], w[1], w[2], w[3]);
+  }
   return v;
 }
 
-// Elements [k, k + 8) of a row of `cols`, zeros past its end (or for a null
-// row).  VEC: rows start on 16 bytes and cols is a multiple of 8.  Otherwise
-// a row starts at any element: the two 16-byte blocks around the 8 elements
-// are loaded (the second is the next lane's first) and shifted together;
-// near the end of the matrix (`end`), where the second block may lie outside
-// it, and at the end of a row the elements are loaded one by one.
-template <bool VEC, bool STREAM>
-__device__ __forceinline__ uint4 sk_load(const char* row, int k, int cols, const char* end) {
+// Token elements [k, k + 8) of a row that starts anywhere, zeros outside it.
+// The two 16-byte blocks around the 8 elements are loaded (both hold elements
+// of the row) and shifted together.
+template <bool VEC>
+__device__ __forceinline__ uint4 sk_tokens(const char* row, int k, int cols) {
   if (!row || k >= cols) return make_uint4(0u, 0u, 0u, 0u);
-  const char* p = row + (size_t)k * 2;
+  const char* p = row + (long long)k * 2;
   if constexpr (VEC) {
-    return sk_ldg(p, STREAM);
+    return __ldg(reinterpret_cast<const uint4*>(p));
   } else {
-    const char* lo = reinterpret_cast<const char*>((uintptr_t)p & ~(uintptr_t)15);
-    if (k + 8 > cols || lo + 32 > end) {
+    if (k < 0 || k + 8 > cols) {
       uint32_t w[4] = {0u, 0u, 0u, 0u};
-      for (int i = 0; i < 8 && k + i < cols; ++i)
-        w[i >> 1] |= (uint32_t)__ldg(reinterpret_cast<const unsigned short*>(p) + i) << (16 * (i & 1));
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (k + i >= 0 && k + i < cols)
+          w[i >> 1] |= (uint32_t)__ldg(reinterpret_cast<const unsigned short*>(p) + i) << (16 * (i & 1));
       return make_uint4(w[0], w[1], w[2], w[3]);
     }
-    const uint4 a = sk_ldg(lo, false), b = sk_ldg(lo + 16, false);
     const uint32_t off = (uint32_t)((uintptr_t)p & 15);
+    const uint4* lo = reinterpret_cast<const uint4*>(p - off);
+    const uint4 a = __ldg(lo);
+    if (off == 0) return a;
+    const uint4 b = __ldg(lo + 1);
     uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     if (off & 8) {
 #pragma unroll
@@ -99,17 +120,18 @@ __device__ __forceinline__ uint4 sk_load(const char* row, int k, int cols, const
   }
 }
 
-// The 16 x 8 NT products of the unit of this warp's group of KW: rows r0 (lane / 4) and r1 (8 + lane /
-// 4) of this lane, in matrices that end at e0 and e1; each warp leaves its
-// share of the K axis in red[warp][16][8 NT].
+// The 16 x 8 NT products of the unit of this warp's group of KW: rows r0
+// (lane / 4) and r1 (8 + lane / 4) of this lane, at offset `off`; each warp
+// leaves its share of the K axis in red[warp][16][8 NT].
 template <int NT, bool VEC, int KW>
-__device__ __forceinline__ void sk_unit(const SkinnyArgs& a, const char* r0, const char* e0, const char* r1,
-                                        const char* e1, float (*red)[16 * 8 * NT]) {
+__device__ __forceinline__ void sk_unit(const SkinnyArgs& a, const char* r0, const char* r1, int off,
+                                        float (*red)[16 * 8 * NT]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int D = a.hidden, steps = (D + kSkStep - 1) / kSkStep;
+  const int D = a.hidden;
+  if (VEC) off = 0;
+  const int steps = (D + off + kSkStep - 1) / kSkStep;
   const char* xb = static_cast<const char*>(a.x);
-  const char* xend = xb + (size_t)a.tokens * D * 2;
   const char* xr[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) xr[n] = n * 8 + g < a.tokens ? xb + (size_t)(n * 8 + g) * D * 2 : nullptr;
@@ -124,10 +146,10 @@ __device__ __forceinline__ void sk_unit(const SkinnyArgs& a, const char* r0, con
 #pragma unroll
     for (int u = 0; u < kSkDepth; ++u) {
       const int k = (s0 + u * KW) * kSkStep + t * 8;
-      w[u][0] = sk_load<VEC, true>(r0, k, D, e0);
-      w[u][1] = sk_load<VEC, true>(r1, k, D, e1);
-      w[u][2] = sk_load<VEC, true>(r0, k + 32, D, e0);
-      w[u][3] = sk_load<VEC, true>(r1, k + 32, D, e1);
+      w[u][0] = sk_weights<VEC>(r0, k, off, D);
+      w[u][1] = sk_weights<VEC>(r1, k, off, D);
+      w[u][2] = sk_weights<VEC>(r0, k + 32, off, D);
+      w[u][3] = sk_weights<VEC>(r1, k + 32, off, D);
     }
 #pragma unroll
     for (int u = 0; u < kSkDepth; ++u) {
@@ -137,7 +159,7 @@ __device__ __forceinline__ void sk_unit(const SkinnyArgs& a, const char* r0, con
         const uint4 lo = w[u][2 * h], hi = w[u][2 * h + 1];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const uint4 x = sk_load<VEC, false>(xr[n], k + 32 * h, D, xend);
+          const uint4 x = sk_tokens<VEC>(xr[n], k + 32 * h - off, D);
           sk_mma(c[n], lo.x, hi.x, lo.y, hi.y, x.x, x.y);
           sk_mma(c[n], lo.z, hi.z, lo.w, hi.w, x.z, x.w);
         }
@@ -167,30 +189,36 @@ __device__ __forceinline__ float sk_total(const float (*red)[16 * 8 * NT], int s
 // ---------------------------------------------------------------------------
 // gated projections
 // ---------------------------------------------------------------------------
+// Row i (of 8) of unit u: 8 rows side by side, or every 8th of 64.
+template <bool VEC>
+__device__ __forceinline__ int sk_gate_row(int u, int i) {
+  return VEC ? u * 8 + i : u / 8 * 64 + u % 8 + 8 * i;
+}
+
 template <int NT, bool VEC, int KW, int ACT>
 __global__ void __launch_bounds__(kSkThreads, 2) skinny_gate_kernel(const __grid_constant__ SkinnyArgs a) {
   constexpr int SLOTS = kSkWarps / KW, PER = 8 * 8 * NT;  // units at a time, values per unit
   __shared__ float red[kSkWarps][16 * 8 * NT];
   const int g = (threadIdx.x & 31) >> 2, mine = (threadIdx.x >> 5) / KW;
-  const int per = (a.width + 7) / 8;  // units per rank
-  const size_t bytes = (size_t)a.width * a.hidden * 2;
+  const int per = sk_gate_units(a.width, VEC);
   pdl_wait();
   pdl_next();
   for (int u0 = blockIdx.x * SLOTS; u0 < a.units; u0 += gridDim.x * SLOTS) {
     {
-      const int u = u0 + mine, r = u / per, f = (u - r * per) * 8 + g;
+      const int u = u0 + mine, r = u / per, f = sk_gate_row<VEC>(u - r * per, g);
       const bool in = u < a.units && f < a.width;
       const char* gb = static_cast<const char*>(in ? a.w[2 * r] : nullptr);
       const char* ub = static_cast<const char*>(in ? a.w[2 * r + 1] : nullptr);
       const size_t at = (size_t)f * a.hidden * 2;
-      sk_unit<NT, VEC, KW>(a, in ? gb + at : nullptr, gb + bytes, in ? ub + at : nullptr, ub + bytes, red);
+      sk_unit<NT, VEC, KW>(a, in ? gb + at : nullptr, in ? ub + at : nullptr,
+                           (int)((uint32_t)sk_gate_row<VEC>(u - r * per, 0) * (uint32_t)a.hidden & 7u), red);
     }
 #pragma unroll
     for (int i0 = 0; i0 < SLOTS * PER; i0 += kSkThreads) {
       const int i = i0 + threadIdx.x;
       if (SLOTS * PER % kSkThreads != 0 && i >= SLOTS * PER) break;
       const int slot = i / PER, token = i % PER / 8, f = i % 8;  // neighbouring threads, neighbouring columns
-      const int u = u0 + slot, r = u / per, col = (u - r * per) * 8 + f;
+      const int u = u0 + slot, r = u / per, col = sk_gate_row<VEC>(u - r * per, f);
       if (u >= a.units || token >= a.tokens || col >= a.width) continue;
       const float gv = sk_total<NT, KW>(red, slot, f * 8 * NT + token);
       const float uv = sk_total<NT, KW>(red, slot, (8 + f) * 8 * NT + token);
@@ -205,6 +233,12 @@ __global__ void __launch_bounds__(kSkThreads, 2) skinny_gate_kernel(const __grid
 // ---------------------------------------------------------------------------
 // vocabulary statistics
 // ---------------------------------------------------------------------------
+// Row i (of 16) of unit u of a shard: side by side, or every 8th of 128.
+template <bool VEC>
+__device__ __forceinline__ long long sk_loss_row(int u, int i) {
+  return VEC ? (long long)u * 16 + i : (long long)(u / 8) * 128 + u % 8 + 8 * i;
+}
+
 template <int NT, bool VEC, int KW>
 __global__ void __launch_bounds__(kSkThreads, 2) skinny_lse_kernel(const __grid_constant__ SkinnyArgs a) {
   constexpr int SLOTS = kSkWarps / KW, PER = 16 * 8 * NT;             // units at a time, values per unit
@@ -228,13 +262,12 @@ __global__ void __launch_bounds__(kSkThreads, 2) skinny_lse_kernel(const __grid_
       const int u = u0 + mine;
       int r = 0;
       while (r + 1 < kMaxRanks && u >= a.unit0[r + 1]) ++r;
-      const long long v0 = (long long)(u - a.unit0[r]) * 16;
+      const long long v0 = sk_loss_row<VEC>(u - a.unit0[r], g), v1 = sk_loss_row<VEC>(u - a.unit0[r], g + 8);
       const long long rows = u < a.units ? a.rows[r] : 0;
       const char* wb = static_cast<const char*>(a.w[r]);
-      const char* end = wb + (size_t)rows * a.hidden * 2;
-      const char* r0 = v0 + g < rows ? wb + (size_t)(v0 + g) * a.hidden * 2 : nullptr;
-      const char* r1 = v0 + g + 8 < rows ? wb + (size_t)(v0 + g + 8) * a.hidden * 2 : nullptr;
-      sk_unit<NT, VEC, KW>(a, r0, end, r1, end, red);
+      sk_unit<NT, VEC, KW>(a, v0 < rows ? wb + (size_t)v0 * a.hidden * 2 : nullptr,
+                           v1 < rows ? wb + (size_t)v1 * a.hidden * 2 : nullptr,
+                           (int)((uint32_t)sk_loss_row<VEC>(u - a.unit0[r], 0) * (uint32_t)a.hidden & 7u), red);
     }
     float l[EACH];
     float q = -INFINITY;
@@ -245,7 +278,7 @@ __global__ void __launch_bounds__(kSkThreads, 2) skinny_lse_kernel(const __grid_
       if (i < SLOTS * PER && u < a.units && token < a.tokens) {
         int r = 0;
         while (u >= a.unit0[r + 1]) ++r;
-        const long long v = (long long)(u - a.unit0[r]) * 16 + i % PER / (8 * NT);
+        const long long v = sk_loss_row<VEC>(u - a.unit0[r], i % PER / (8 * NT));
         if (v < a.rows[r]) {
           l[j] = sk_total<NT, KW>(red, slot, i % PER);
           if (target == a.col0[r] + v) a.hit[token] = l[j];

@@ -361,7 +361,7 @@ namespace {
 // 1728 gated columns of hidden 5120 53 and 56, of 1024 11 and 14; 131072
 // columns of hidden 1024 52 and 54, of 5120 228 and 208, of 1027 204 and 174).
 bool skinny(size_t T, size_t D, size_t logits) {
-  return T <= 8 || (T <= 16 && D % 8 == 0 && logits <= (size_t)1 << 27);
+  return T <= 8 || (T <= 16 && (D % 8 != 0 || logits <= (size_t)1 << 27));
 }
 
 size_t ffn_bytes(int n, size_t T, size_t D, size_t F, bool back) {
@@ -436,7 +436,7 @@ rra_status_t rra_gated_ffn(const void* x, const void* const* gates, const void* 
     a.tokens = (int)T;
     a.hidden = (int)D;
     a.width = (int)F;
-    const size_t units = (size_t)nranks * ((F + 7) / 8);
+    const size_t units = (size_t)nranks * (size_t)sk_gate_units((int)F, D % 8 == 0);
     if (units > INT_MAX / 2) return done(call, nranks, count, dtype, 0, RRA_ERR_UNSUPPORTED);
     a.units = (int)units;
     for (int r = 0; r < nranks; ++r) {
@@ -628,9 +628,9 @@ size_t vocab_rows(int n, const size_t* vocab) {
   return v;
 }
 
-long long skinny_units(int n, const size_t* vocab) {
+long long skinny_units(int n, const size_t* vocab, size_t D) {
   long long u = 0;
-  for (int r = 0; r < n; ++r) u += (long long)((vocab[r] + 15) / 16);
+  for (int r = 0; r < n; ++r) u += sk_loss_units((long long)vocab[r], D % 8 == 0);
   return u;
 }
 
@@ -638,7 +638,7 @@ LossPlan loss_plan(int n, size_t T, size_t D, const size_t* vocab, bool back, si
   LossPlan q;
   Bump b{nullptr};
   if (!back && skinny(T, D, vocab_rows(n, vocab) * D)) {
-    b.take((size_t)skinny_grid(skinny_units(n, vocab)) * T * sizeof(float2));
+    b.take((size_t)skinny_grid(skinny_units(n, vocab, D)) * T * sizeof(float2));
     b.take(T * 4);
     q.fixed = b.at;
     return q;
@@ -739,7 +739,7 @@ rra_status_t rra_vocab_loss(const void* x, const void* const* weights, const siz
       a.w[r] = weights[r];
       a.rows[r] = (long long)vocab[r];
       a.col0[r] = col;
-      a.unit0[r + 1] = a.unit0[r] + (int)((vocab[r] + 15) / 16);
+      a.unit0[r + 1] = a.unit0[r] + (int)sk_loss_units((long long)vocab[r], D % 8 == 0);
       col += (long long)vocab[r];
     }
     a.units = a.unit0[nranks];

@@ -110,6 +110,13 @@ struct SkinnyArgs {
   float* hit;
 };
 int skinny_grid(long long units);
+// Units of a shard: 8 gated columns or 16 vocabulary rows each (vec: rows of
+// whole 16-byte units), counted in whole blocks of 64 or 128 otherwise.
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+inline int sk_gate_units(int width, bool vec) { return vec ? (width + 7) / 8 : (width + 63) / 64 * 8; }
+inline long long sk_loss_units(long long rows, bool vec) { return vec ? (rows + 15) / 16 : (rows + 127) / 128 * 8; }
 cudaError_t launch_skinny_gate(const SkinnyArgs& a, int act, cudaStream_t s, int* grid);
 cudaError_t launch_skinny_lse(const SkinnyArgs& a, cudaStream_t s, int* grid);
 

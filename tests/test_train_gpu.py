@@ -55,6 +55,7 @@ FFN = [  # n, tokens, hidden, width, act
     # few tokens: the register path, rows on and off 16 bytes
     (1, 1, 5120, 24, 0), (8, 8, 1024, 17, 1), (3, 9, 2056, 64, 0), (2, 16, 515, 33, 0), (1, 7, 1027, 8, 1), (2, 3, 771, 100, 0),
     (1, 17, 1024, 72, 0), (2, 40, 520, 136, 1),
+    (1, 2, 1027, 130, 0), (2, 8, 333, 65, 1), (1, 5, 9, 200, 0), (1, 3, 5, 64, 1), (3, 1, 4102, 12, 0),
     # a part of a tile's rows staged
     (8, 33, 512, 720, 0), (7, 128, 256, 700, 1), (8, 121, 136, 1728, 0), (1, 100, 264, 9000, 0),
 ]
@@ -100,7 +101,8 @@ LOSS = [  # tokens, hidden, shard heights
     (129, 1027, (257, 0, 64)), (7, 515, (1,)), (64, 72, (100,) * 8), (2, 8, (3, 2)), (513, 256, (2048, 2048)),
     # few tokens: the register path
     (1, 5120, (700, 700)), (8, 1024, (16, 15, 0, 33)), (16, 515, (401, 400)), (9, 1027, (3000,)), (5, 771, (17,)),
-    (17, 1024, (500,)), (100, 512, (5000, 300)), (121, 136, (20000,)),
+    (17, 1024, (500,)), (100, 512, (5000, 300)), (1, 1027, (1000, 129)), (8, 333, (130, 0, 300)),
+    (3, 5, (260,)), (7, 4102, (140, 9)), (121, 136, (20000,)),
 ]
 
 
