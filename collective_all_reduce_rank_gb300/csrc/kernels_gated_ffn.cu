@@ -23,9 +23,9 @@
 namespace rra {
 
 template <int ACT>
-struct EpiGate {
+struct EpiGate : TcNoState {
   static __device__ __forceinline__ void run(const TcArgs& p, const TcTile& x, int row0, int half, uint32_t addr,
-                                             uint8_t* buf) {
+                                             uint8_t* buf, const State&) {
     const TcGroup& g = p.group[x.group];
     const int c0 = x.n * 128 + half * 64;
     const int valid = g.N - c0;
@@ -49,9 +49,9 @@ struct EpiGate {
 };
 
 template <int ACT>
-struct EpiGateBack {
+struct EpiGateBack : TcNoState {
   static __device__ __forceinline__ void run(const TcArgs& p, const TcTile& x, int row0, int half, uint32_t addr,
-                                             uint8_t* buf) {
+                                             uint8_t* buf, const State&) {
     const TcGroup& g = p.group[x.group];
     const int c0 = x.n * 128 + half * 64;
     const int rows = g.M - row0;

@@ -12,14 +12,14 @@
 // computed again and the epilogue stores dl of the piece in bfloat16, from
 // which the two gradient products (kernels_tc_store.cu) read it.
 //
-// dl is held as e[t][v] s[t] with s[t] = grad[t] (1 - p[t]), p[t] the
-// target's probability: e is p[t][v] / (1 - p[t]) beside the target, which
-// lies in [0, 1], and exactly -1 at the target, so the entry that dominates a
-// row is not rounded at all.  s multiplies dx's rows in float32, and goes
-// into the weight gradient through x s, rounded to bfloat16 element by
-// element.  Rounding grad (p - 1) itself to bfloat16 would scale all of a
-// token's contribution by up to 2^-9 (measured on 500 tokens: dW off by
-// 0.0026 in the 2-norm against 0.0017 for the rounding of the result alone).
+// An entry of dl is off by up to half a bfloat16 step, which averages out over
+// the many small entries of a row but not for the target's, which alone is as
+// large as all others together: a token's share of the gradients would be off
+// by up to 2^-8 as a whole.  So the rest of the target's entry that bfloat16
+// leaves, lo[t], is kept in float32 and added back where the products'
+// epilogues still hold float32: lo[t] W[target] to row t of dx, lo[t] x[t] to
+// row target of dW (dW of 333 x 515 x 50021 off by 0.0017 in the 2-norm
+// against 0.0023 without).
 //
 // Bound by the tensor cores: the epilogue's exponentials (one per logit, 4 a
 // cycle and scheduler) run under the products of the next tile.  Measured:
@@ -52,7 +52,7 @@ __device__ __forceinline__ float row_dot(const __nv_bfloat16* x, const __nv_bflo
   return dot;
 }
 
-struct EpiLse {
+struct EpiLse : TcNoState {
   // One row's 32 logits into its running maximum and sum.
   static __device__ __forceinline__ void chunk(const TcArgs& p, float* v, int valid, long long d, int row, float& m,
                                                float& s) {
@@ -87,7 +87,7 @@ struct EpiLse {
   }
 
   static __device__ __forceinline__ void run(const TcArgs& p, const TcTile& x, int row0, int half, uint32_t addr,
-                                             uint8_t*) {
+                                             uint8_t*, const State&) {
     const TcGroup& g = p.group[x.group];
     const int row = row0 + (threadIdx.x & 31);
     const int c0 = x.n * 256 + half * 128;
@@ -114,9 +114,9 @@ struct EpiLse {
   }
 };
 
-struct EpiDlogits {
+struct EpiDlogits : TcNoState {
   static __device__ __forceinline__ void run(const TcArgs& p, const TcTile& x, int row0, int half, uint32_t addr,
-                                             uint8_t* buf) {
+                                             uint8_t* buf, const State&) {
     const TcGroup& g = p.group[x.group];
     const int row = row0 + (threadIdx.x & 31);
     const int c0 = x.n * 256 + half * 128;
@@ -137,7 +137,7 @@ struct EpiDlogits {
         tc_ld32(addr + half * 128 + c + k, v);
         tc_ld_ready(v);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = tc_exp2(fmaf(v[j], kLog2e, -q.x));
+        for (int j = 0; j < 32; ++j) v[j] = tc_exp2(fmaf(v[j], kLog2e, -q.x)) * q.w;
         const long long d = t - c - k;
         if (d >= 0 && d < 32) {  // the target's column, in one chunk of a row
 #pragma unroll
@@ -163,90 +163,145 @@ cudaError_t launch_tc_dlogits(const TcArgs& p, cudaStream_t s, int* grid) {
   return tc_launch<false, false, EpiDlogits>(p, s, grid);
 }
 
-// Per row of the backward pass, one CTA a row: {lse in units of log 2 plus
-// log2(1 - p), e at the target, 1 if the row has a gradient, s} and x s in
-// bfloat16 (rows of ld elements; zeros for a row without a gradient).
-struct ScaleArgs {
+// What the backward pass needs beside the logits.  The first row_ctas CTAs
+// take the tokens, per token: {lse in units of log 2, the target's entry in
+// bfloat16, 1 if the row has a gradient, grad}, the target (-1: none) and
+// what bfloat16 leaves of its entry.  The others make the index of the tokens
+// by target: a warp per token counts the tokens that come before it, a warp
+// per block of 32 vocabulary rows those before the block: tokens x (tokens +
+// V / 32) comparisons, and no order that depends on timing.
+struct RowsArgs {
   const __nv_bfloat16* x;
   const __nv_bfloat16* w[kMaxRanks];
   long long first[kMaxRanks + 1];
+  int block0[kMaxRanks + 1];  // blocks of 32 rows of the shards before
   const long long* targets;
   long long ignore_index;
   const float* lse;
   const float* grad;
   float4* rows;
-  __nv_bfloat16* xs;
-  long long ld;
-  int hidden, nranks, vec;
+  int* column;
+  float* lo;
+  int* start;
+  int* token;
+  int* sorted;
+  int hidden, nranks, vec, tokens, row_ctas, items;
 };
 
-__global__ void __launch_bounds__(256) loss_scale_kernel(const __grid_constant__ ScaleArgs a) {
-  __shared__ float part[8];
-  const int row = blockIdx.x, tid = threadIdx.x;
-  pdl_wait();
-  pdl_next();
-  const long long t = a.targets[row];
-  const bool live = t != a.ignore_index && t >= 0 && t < a.first[a.nranks];
-  const __nv_bfloat16* x = a.x + (long long)row * a.hidden;
-  float dot = 0.f;
-  if (live) {
-    int g = 0;
-    while (t >= a.first[g + 1]) ++g;
-    dot = row_dot(x, a.w[g] + (t - a.first[g]) * a.hidden, a.hidden, a.vec, tid, 256);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-  if ((tid & 31) == 0) part[tid >> 5] = dot;
-  __syncthreads();
-  float l = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) l += part[i];
-  float s = 0.f;
-  float4 q = make_float4(INFINITY, 0.f, 0.f, 0.f);
-  if (live) {
-    const float lse = a.lse[row];
-    const float rest = -expm1f(fminf(l - lse, 0.f));  // 1 - p (NaN stays NaN below)
-    const float big = fmaxf(rest, 9.5367431640625e-07f);  // 2^-20: a target that carries all the mass
-    s = a.grad[row] * big;
-    q = make_float4(lse * kLog2e + log2f(big), l - lse != l - lse ? l - lse : -rest / big, 1.f, s);
-  }
-  if (tid == 0) a.rows[row] = q;
-  __nv_bfloat16* o = a.xs + (long long)row * a.ld;
-  if (a.vec) {
-    for (int c = tid * 8; c < a.hidden; c += 256 * 8) {
-      const uint4 u = __ldg(reinterpret_cast<const uint4*>(x + c));
-      const uint32_t p[4] = {u.x, u.y, u.z, u.w};
-      uint32_t w[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        w[j] = live ? tc_pack2(__uint_as_float(p[j] << 16) * s, __uint_as_float(p[j] & 0xFFFF0000u) * s) : 0u;
-      *reinterpret_cast<uint4*>(o + c) = make_uint4(w[0], w[1], w[2], w[3]);
+__device__ __forceinline__ long long live_target(const RowsArgs& a, int row) {
+  const long long t = __ldg(a.targets + row);
+  return t != a.ignore_index && t >= 0 && t < a.first[a.nranks] ? t : -1;
+}
+
+__device__ __forceinline__ void loss_index(const RowsArgs& a) {
+  const int lane = threadIdx.x & 31, ctas = gridDim.x - a.row_ctas;
+  for (int i = (blockIdx.x - a.row_ctas) * 8 + (threadIdx.x >> 5); i < a.items; i += ctas * 8) {
+    const bool is_token = i < a.tokens;
+    long long key;
+    if (is_token) {
+      key = live_target(a, i);
+      if (key < 0) continue;
+    } else {
+      const int b = i - a.tokens;
+      int r = 0;
+      while (r < a.nranks && b >= a.block0[r + 1]) ++r;
+      key = r == a.nranks ? a.first[a.nranks] : a.first[r] + 32ll * (b - a.block0[r]);
     }
-  } else {
-    for (int c = tid; c < a.hidden; c += 256) o[c] = __float2bfloat16_rn(live ? __bfloat162float(x[c]) * s : 0.f);
+    int n = 0;
+#pragma unroll 4
+    for (int t = lane; t < a.tokens; t += 32) {
+      const long long c = live_target(a, t);
+      n += c >= 0 && (c < key || (is_token && c == key && t < i));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+    if (lane == 0) {
+      if (is_token) {
+        a.token[n] = i;
+        a.sorted[n] = (int)key;
+      } else {
+        a.start[i - a.tokens] = n;
+      }
+    }
   }
 }
 
-cudaError_t launch_loss_scale(const void* x, const void* const* w, const size_t* vocab, int n, size_t hidden,
-                              int tokens, const long long* targets, long long ignore_index, const float* lse,
-                              const float* grad, float4* rows, void* xs, size_t ld, cudaStream_t s) {
-  ScaleArgs a{};
+// R rows per CTA: 256 / R threads a row.
+template <int R>
+__global__ void __launch_bounds__(256) loss_rows_kernel(const __grid_constant__ RowsArgs a) {
+  constexpr int PER = 256 / R;
+  __shared__ float part[8];
+  pdl_wait();
+  pdl_next();
+  if ((int)blockIdx.x >= a.row_ctas) {
+    loss_index(a);
+    return;
+  }
+  const int row = blockIdx.x * R + threadIdx.x / PER, i = threadIdx.x % PER;
+  const long long t = row < a.tokens ? live_target(a, row) : -1;
+  float l = 0.f;
+  if (t >= 0) {
+    int g = 0;
+    while (t >= a.first[g + 1]) ++g;
+    l = row_dot(a.x + (long long)row * a.hidden, a.w[g] + (t - a.first[g]) * a.hidden, a.hidden, a.vec, i, PER);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if (R == 1) {
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = l;
+    __syncthreads();
+    l = part[0];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) l += part[w];
+  }
+  if (i != 0 || row >= a.tokens) return;
+  float4 q = make_float4(INFINITY, 0.f, 0.f, 0.f);
+  float rest = 0.f;
+  if (t >= 0) {
+    const float lse = a.lse[row], grad = a.grad[row];
+    const float d = l - lse;
+    const float entry = (d < 0.f ? expm1f(d) : d != d ? d : 0.f) * grad;  // (p - 1) grad
+    const float held = __bfloat162float(__float2bfloat16_rn(entry));
+    q = make_float4(lse * kLog2e, held, 1.f, grad);
+    rest = fabsf(held) < INFINITY ? entry - held : 0.f;
+  }
+  a.rows[row] = q;
+  a.column[row] = (int)t;
+  a.lo[row] = rest;
+}
+
+cudaError_t launch_loss_rows(const void* x, const void* const* w, const size_t* vocab, int n, size_t hidden, int tokens,
+                             const long long* targets, long long ignore_index, const float* lse, const float* grad,
+                             float4* rows, int* column, float* lo, int* start, int* token, int* sorted,
+                             cudaStream_t s) {
+  RowsArgs a{};
   a.x = static_cast<const __nv_bfloat16*>(x);
   for (int r = 0; r < n; ++r) {
     a.w[r] = static_cast<const __nv_bfloat16*>(w[r]);
     a.first[r + 1] = a.first[r] + (long long)vocab[r];
+    a.block0[r + 1] = a.block0[r] + (int)((vocab[r] + 31) / 32);
   }
   a.targets = targets;
   a.ignore_index = ignore_index;
   a.lse = lse;
   a.grad = grad;
   a.rows = rows;
-  a.xs = static_cast<__nv_bfloat16*>(xs);
-  a.ld = (long long)ld;
+  a.column = column;
+  a.lo = lo;
+  a.start = start;
+  a.token = token;
+  a.sorted = sorted;
   a.hidden = (int)hidden;
   a.nranks = n;
   a.vec = hidden % 8 == 0;  // the matrices themselves are 16-byte aligned
-  return launch_pdl(loss_scale_kernel, tokens, 256, 0, s, a);
+  a.tokens = tokens;
+  a.items = tokens + a.block0[n] + 1;
+  const int most = device_sms() * 8, want = (a.items + 7) / 8, index_ctas = want < most ? want : most;
+  // one row per CTA while that leaves SMs idle, else 8
+  const bool few = tokens < 8 * device_sms();
+  a.row_ctas = few ? tokens : (tokens + 7) / 8;
+  return few ? launch_pdl(loss_rows_kernel<1>, a.row_ctas + index_ctas, 256, 0, s, a)
+             : launch_pdl(loss_rows_kernel<8>, a.row_ctas + index_ctas, 256, 0, s, a);
 }
 
 // Join the column parts of each row, R rows per CTA (256 threads: 256 / R

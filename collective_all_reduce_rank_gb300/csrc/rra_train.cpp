@@ -574,7 +574,7 @@ rra_status_t rra_gated_ffn_backward(const void* x, const void* const* gates, con
   if (!ok) return done(call, nranks, count, dtype, 0, RRA_ERR_CUDA);
   e = launch_tc_input_grad(*p, false, s, &grid);
   if (e == cudaSuccess)
-    e = launch_join_tiles({nullptr, slots, dx, 0, (int)T, (int)D, p->group[0].mt, p->group[0].nt, sp.full, sp.splits}, s);
+    e = launch_join_tiles({nullptr, slots, dx, 0, (int)T, (int)D, p->group[0].mt, p->group[0].nt, sp.full, sp.splits, TcFix{}}, s);
   if (e != cudaSuccess) return done(call, nranks, count, dtype, grid, RRA_ERR_CUDA);
 
   // dG, dU
@@ -622,6 +622,13 @@ struct LossPlan {
   bool acc = false;        // dx is summed over pieces in float32
 };
 
+// Blocks of 32 rows of the first n shards.
+size_t blocks32(int n, const size_t* vocab) {
+  size_t b = 0;
+  for (int r = 0; r < n; ++r) b += (vocab[r] + 31) / 32;
+  return b;
+}
+
 size_t vocab_rows(int n, const size_t* vocab) {
   size_t v = 0;
   for (int r = 0; r < n; ++r) v += vocab[r];
@@ -636,6 +643,7 @@ long long skinny_units(int n, const size_t* vocab, size_t D) {
 
 LossPlan loss_plan(int n, size_t T, size_t D, const size_t* vocab, bool back, size_t room) {
   LossPlan q;
+  if (T == 0) return q;
   Bump b{nullptr};
   if (!back && skinny(T, D, vocab_rows(n, vocab) * D)) {
     b.take((size_t)skinny_grid(skinny_units(n, vocab, D)) * T * sizeof(float2));
@@ -649,7 +657,8 @@ LossPlan loss_plan(int n, size_t T, size_t D, const size_t* vocab, bool back, si
   }
   if (back) {
     b.take(T * sizeof(float4));
-    b.take(T * pad_ld(D) * 2);  // x s
+    for (int i = 0; i < 4; ++i) b.take(T * 4);
+    b.take((blocks32(n, vocab) + 1) * 4);
   }
   const size_t tiles = vocab_tiles(n, vocab);
   if (!back) {
@@ -836,15 +845,37 @@ rra_status_t rra_vocab_loss_backward(const void* x, const void* const* weights, 
   Mat W[kMaxRanks];
   for (int r = 0; r < nranks; ++r) W[r] = place(weights[r], vocab[r], D);
   float4* rows = static_cast<float4*>(ws.take(T * sizeof(float4)));
-  const Mat XS{ws.take(T * pad_ld(D) * 2), T, D, pad_ld(D)};
+  TcFix fix{};
+  int* column = static_cast<int*>(ws.take(T * 4));
+  float* rest = static_cast<float*>(ws.take(T * 4));
+  int* token = static_cast<int*>(ws.take(T * 4));
+  int* sorted = static_cast<int*>(ws.take(T * 4));
+  int* start = static_cast<int*>(ws.take((blocks32(nranks, vocab) + 1) * 4));
+  fix.column = column;
+  fix.lo = rest;
+  fix.start = start;
+  fix.token = token;
+  fix.sorted = sorted;
   bool ok = place.launch(s) &&
-            launch_loss_scale(x, weights, vocab, nranks, D, (int)T, reinterpret_cast<const long long*>(targets),
-                              ignore_index, lse, grad_loss, rows, const_cast<void*>(XS.p), XS.ld, s) == cudaSuccess;
+            launch_loss_rows(x, weights, vocab, nranks, D, (int)T, reinterpret_cast<const long long*>(targets),
+                             ignore_index, lse, grad_loss, rows, column, rest, start, token, sorted,
+                             s) == cudaSuccess;
   if (!ok) return done(call, nranks, T * V, dtype, 0, RRA_ERR_CUDA);
   float* slots = static_cast<float*>(ws.take(q.split.slot_bytes));
   float* acc = q.acc ? static_cast<float*>(ws.take(T * slot_ld(D) * 4)) : nullptr;
   char* dl = ws.base + ws.at;
   const size_t ld = q.piece_tiles * 256;
+
+  // dx's additions are made where a tile is rounded: in the join, or in the
+  // product's own epilogue for tiles of a single piece that take the whole K
+  // axis
+  TcFix dx_fix = fix;
+  dx_fix.kind = 1;
+  dx_fix.ld = (long long)X.ld;
+  for (int r = 0; r < nranks; ++r) {
+    dx_fix.w[r] = W[r].p;
+    dx_fix.first[r + 1] = dx_fix.first[r] + (long long)vocab[r];
+  }
 
   TcArgs args;
   TcArgs* const p = &args;
@@ -910,7 +941,7 @@ rra_status_t rra_vocab_loss_backward(const void* x, const void* const* weights, 
     p->splits = q.split.splits;
     p->slots = slots;
     p->accumulate = t0 > 0;
-    p->row_scale = &rows->w;
+    p->fix = dx_fix;
     TcGroup g{};
     g.M = (int)T;
     g.N = (int)D;
@@ -923,15 +954,21 @@ rra_status_t rra_vocab_loss_backward(const void* x, const void* const* weights, 
     e = launch_tc_input_grad(*p, q.acc, s, &grid);
     if (e != cudaSuccess) break;
 
-    // dW of the piece's rows, from x s
+    // dW of the piece's rows
     clear(p);
-    ok = map_mn(&p->b[0], XS);
+    p->fix = fix;
+    p->fix.kind = 2;
+    p->fix.w[0] = X.p;
+    p->fix.ld = (long long)X.ld;
+    ok = map_mn(&p->b[0], X);
     for (int r = 0; r < nranks && ok; ++r) {
       if (hi[r] <= lo[r]) continue;
       const Mat A{dl + at[r] * 2, T, hi[r] - lo[r], ld};
       ok = map_mn(&p->a[r], A);
       TcGroup h{};
       h.a = r;
+      h.col0 = first[r];
+      h.part0 = (int)(blocks32(r, vocab) + lo[r] / 32);
       h.M = (int)(hi[r] - lo[r]);
       h.N = (int)D;
       h.ld = (long long)D;
@@ -946,7 +983,7 @@ rra_status_t rra_vocab_loss_backward(const void* x, const void* const* weights, 
   }
   if (e == cudaSuccess)
     e = launch_join_tiles({acc, slots, dx, (int)slot_ld(D), (int)T, (int)D, (int)tiles256(T), (int)tiles256(D),
-                           q.split.full, q.split.splits}, s);
+                           q.split.full, q.split.splits, dx_fix}, s);
   return done(call, nranks, T * V, dtype, grid, cuda_st(e));
 }
 

@@ -289,10 +289,19 @@ __device__ __forceinline__ TcTile tc_tile(const TcArgs& p, int t) {
 }
 
 // ---------------------------------------------------------------------------
-// kernel.  Epi::run(p, tile, row0, half, addr, buf) consumes one accumulator:
-// each lane of a warp row row0 + lane of C and the columns of half `half` (0
-// or 1) of the tile, with kTcStoreBytes of shared memory for its stores.
+// kernel.  Epi::run(p, tile, row0, half, addr, buf, state) consumes one
+// accumulator: each lane of a warp row row0 + lane of C and the columns of
+// half `half` (0 or 1) of the tile, with kTcStoreBytes of shared memory for
+// its stores.  What it needs from memory beside the accumulator can be asked
+// for a tile ahead: Epi::ahead issues loads before the tile before is
+// consumed, Epi::more those that depend on them, after it.
 // ---------------------------------------------------------------------------
+struct TcNoState {
+  struct State {};
+  static __device__ __forceinline__ State ahead(const TcArgs&, const TcTile&, int, int) { return {}; }
+  static __device__ __forceinline__ void more(const TcArgs&, const TcTile&, int, int, State&) {}
+};
+
 template <bool AMN, bool BMN, class Epi>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     tc_gemm_kernel(const __grid_constant__ TcArgs p) {
@@ -420,20 +429,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     __syncwarp();
   } else if (warp >= 4) {
     const int quad = warp & 3, half = (warp - 4) >> 2;
+    const int row_in = (int)rank * 128 + quad * 32;
     uint32_t tile = 0;
+    TcTile next{};
+    typename Epi::State state, after;
+    if (cluster < total) {
+      next = tc_tile(p, cluster);
+      after = Epi::ahead(p, next, next.m * 256 + row_in, half);
+      Epi::more(p, next, next.m * 256 + row_in, half, after);
+    }
     for (int t = cluster; t < total; t += clusters) {
-      const TcTile x = tc_tile(p, t);
-      if (x.k0 == x.k1) continue;
+      const TcTile x = next;
+      state = after;
+      if (t + clusters < total) {
+        next = tc_tile(p, t + clusters);
+        after = Epi::ahead(p, next, next.m * 256 + row_in, half);
+      }
+      if (x.k0 == x.k1) {
+        if (t + clusters < total) Epi::more(p, next, next.m * 256 + row_in, half, after);
+        continue;
+      }
       const uint32_t buf = tile & 1;
       if (!__all_sync(0xffffffffu, tc_wait(tc_smem(&sh.acc_full[buf]), (tile >> 1) & 1, &sh, p.status, 4))) break;
       tc_fence_after();
-      Epi::run(p, x, x.m * 256 + (int)rank * 128 + quad * 32, half,
-               tmem + buf * 256 + ((uint32_t)(quad * 32) << 16),
-               raw + (stages - tc_smem(raw)) + kTcRingBytes + (warp - 4) * kTcStoreBytes);
+      Epi::run(p, x, x.m * 256 + row_in, half, tmem + buf * 256 + ((uint32_t)(quad * 32) << 16),
+               raw + (stages - tc_smem(raw)) + kTcRingBytes + (warp - 4) * kTcStoreBytes, state);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) tc_bar_arrive_remote(tc_smem(&sh.acc_empty[buf]), 0);
       ++tile;
+      if (t + clusters < total) Epi::more(p, next, next.m * 256 + row_in, half, after);
     }
   }
 

@@ -46,6 +46,26 @@ struct TcShape {
   int stages = 6;
 };
 
+// Rank-one additions to the loss's gradients, in float32 before the result
+// is rounded: column[t] is the target of token t (-1: none), lo[t] a factor.
+// kind 1 (dx): row t += lo[t] row column[t] of the shards w; kind 2 (dW, the
+// group's first row being column col0): row column[t] += lo[t] row t of w[0],
+// the tokens taken from an index by target: those of a shard's 32 rows from
+// 32 b on are token[start[k]], ..., token[start[k + 1] - 1] with targets
+// sorted[...], k = b plus the blocks of the shards before (the group's first
+// block is part0).
+struct TcFix {
+  int kind = 0;
+  const int* column;
+  const float* lo;
+  const int* start;
+  const int* token;
+  const int* sorted;
+  const void* w[kMaxRanks];
+  long long first[kMaxRanks + 1];
+  long long ld;  // elements between rows, which hold whole 16-byte units
+};
+
 struct TcArgs {
   CUtensorMap a[kTcMaxGroups];
   CUtensorMap b[kTcMaxGroups];
@@ -64,8 +84,8 @@ struct TcArgs {
   int act;
   const long long* targets;
   long long ignore_index;
-  const float4* rows;      // backward: what loss_scale_kernel left per row
-  const float* row_scale;  // products of one group: factor of each output row, every 4th float (null: none)
+  const float4* rows;  // dl: what loss_rows_kernel left per row
+  TcFix fix;
   float2* part;      // [column part][part_ld] running maximum and sum
   long long part_ld;
   float* hit;        // logit of the row's target
@@ -134,6 +154,7 @@ struct JoinTiles {
   const float* slots;
   void* out;
   int ld, rows, cols, mt, nt, full, splits;
+  TcFix fix;  // kind 1 or none
 };
 cudaError_t launch_join_tiles(const JoinTiles& j, cudaStream_t s);
 // Units of work of a launch: whole tiles, then parts of the others.
@@ -141,11 +162,12 @@ cudaError_t launch_join_tiles(const JoinTiles& j, cudaStream_t s);
 __host__ __device__
 #endif
 inline int tc_units(const TcArgs& p) { return p.full + (p.tiles - p.full) * p.splits; }
-// Per row of the loss's backward pass: rows[t] = {lse / log 2 + log2(1 - p),
-// e at the target, 1 or 0 (no gradient), s}, and x s as bfloat16 rows of ld.
-cudaError_t launch_loss_scale(const void* x, const void* const* w, const size_t* vocab, int n, size_t hidden,
-                              int tokens, const long long* targets, long long ignore_index, const float* lse,
-                              const float* grad, float4* rows, void* xs, size_t ld, cudaStream_t s);
+// Per row of the loss's backward pass: rows[t] = {lse / log 2, the target's
+// entry of dl in bfloat16, 1 or 0 (no gradient), grad}; TcFix's arrays.
+cudaError_t launch_loss_rows(const void* x, const void* const* w, const size_t* vocab, int n, size_t hidden, int tokens,
+                             const long long* targets, long long ignore_index, const float* lse, const float* grad,
+                             float4* rows, int* column, float* lo, int* start, int* token, int* sorted,
+                             cudaStream_t s);
 
 // Rows of `cols` elements of each src to rows of 8 * units elements of dst.
 struct PadArgs {

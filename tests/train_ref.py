@@ -131,9 +131,7 @@ def vocab_loss(x, weights, targets, ignore, grad=None):
     dx = d @ W
     bdx = ed @ W.abs() + product_err(d.abs(), W.abs(), V) + BF * dx.abs() + 1e-30
     dW = d.t() @ x
-    # the weight gradient's other operand is the token times its float32 factor, rounded to bfloat16 too
-    bW = ed.t() @ x.abs() * (1 + BF) + BF * (d.abs().t() @ x.abs()) + product_err(d.abs().t(), x.abs(), len(x)) \
-        + BF * dW.abs() + 1e-30
+    bW = ed.t() @ x.abs() + product_err(d.abs().t(), x.abs(), len(x)) + BF * dW.abs() + 1e-30
     sizes = [len(v) for v in weights]
     out["dx"] = (dx, bdx)
     out["dW"] = list(zip(torch.split(dW, sizes), torch.split(bW, sizes)))
