@@ -156,6 +156,22 @@ def test_vocab_loss_backward(T, D, shards, room):
     ref.assert_norm_close(torch.cat(dW), torch.cat([w for w, _ in want["dW"]]), 2 * ref.BF, "dweights")
 
 
+@pytest.mark.parametrize("T,D,shards", [(300, 72, (40, 260)), (129, 515, (300,)), (3, 1024, (700, 90))])
+def test_many_tokens_of_one_target(T, D, shards):
+    """More targets in a block of rows than a warp takes at a time, and none in the others."""
+    x, W, _, grad = loss_inputs(T, D, shards, T)
+    tgt = torch.full((T,), sum(shards) - 9)
+    tgt[::3] = 5
+    tgt[1::7] = IGN
+    want = ref.vocab_loss(x, W, tgt, IGN, grad)
+    dx, dW = poison(T, D), [poison(v, D) for v in shards]
+    rra.rra_vocab_loss_backward(x.cuda(), cuda(W), tgt.cuda(), want["lse"][0].float().cuda(), grad.cuda(), dx, dW)
+    status_ok()
+    ref.assert_within(dx, *want["dx"], "dx")
+    for r in range(len(shards)):
+        ref.assert_within(dW[r], *want["dW"][r], "dweights[%d]" % r)
+
+
 # -- RMSNorm with a checkpoint -----------------------------------------------
 
 NORM = [(1, 1, 128), (2, 3, 5120), (8, 8, 5120), (3, 5, 1027), (4, 2, 1), (5, 7, 130), (2, 64, 4096), (6, 700, 260),

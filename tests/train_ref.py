@@ -127,7 +127,10 @@ def vocab_loss(x, weights, targets, ignore, grad=None):
     d[rows, safe] -= 1
     ed = p * (el + elast[:, None] + F32 * 8 * (l.abs() + lse.abs()[:, None] + 1)) + F32 * 2
     d, ed = d * w[:, None], ed * w.abs()[:, None]
-    ed = ed + BF * (d.abs() + ed)
+    # every entry is rounded to bfloat16 but the target's, whose rest is added in float32
+    step = BF * (d.abs() + ed)
+    step[rows[inside], targets[inside]] = (4 * F32 * (d.abs() + ed))[rows[inside], targets[inside]]
+    ed = ed + step
     dx = d @ W
     bdx = ed @ W.abs() + product_err(d.abs(), W.abs(), V) + BF * dx.abs() + 1e-30
     dW = d.t() @ x
