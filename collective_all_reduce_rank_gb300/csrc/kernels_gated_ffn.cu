@@ -35,7 +35,8 @@ struct EpiGate : TcNoState {
       float a[32], b[32];
       tc_ld32(addr + half * 64 + c, a);
       tc_ld32(addr + 128 + half * 64 + c, b);
-      tc_ld_wait();
+      tc_ld_ready(a);
+      tc_ld_ready(b);
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
         float unused;
@@ -65,7 +66,8 @@ struct EpiGateBack : TcNoState {
       tc_ld32(addr + half * 64 + c, a);
       tc_ld32(addr + 128 + half * 64 + c, b);
       tc_load_bf16(buf, in + c, g.ld_in, rows, valid, g.vec, d);
-      tc_ld_wait();
+      tc_ld_ready(a);
+      tc_ld_ready(b);
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
         float k;

@@ -1,6 +1,5 @@
 // kernels_skinny.cu -- the gated projections and the vocabulary statistics
-// of few tokens (at most kSkinnyTokens): a decoding step, or a handful of
-// scored tokens.
+// of few tokens (at most 16): a decoding step, or a handful of scored tokens.
 //
 // With T tokens every weight is used T times, so the call is bound by
 // reading the weights once: 2 n F D or V D elements.  A tile of the
@@ -11,12 +10,12 @@
 // KW of a CTA's 8 warps split the K axis of a unit (steps of 64 elements,
 // warp w every KW-th) and add their partial sums through shared memory; the
 // CTA has 8 / KW units at a time, so that short rows keep loads in flight too
-// (split_k).  Weights go
-// from global memory straight to the registers of mma.sync m16n8k16: the
-// sum over k does not care about the order of k, so each lane takes 8
-// consecutive elements of a row (one 16-byte load) as the pairs of two
-// products, and the tokens (8 per product, read through L1) are taken in the
-// same order.  With 4 steps in flight a warp has 8 KB of loads outstanding.
+// (split_k).  Weights go from global memory straight to the registers of
+// mma.sync m16n8k16: the sum over k does not care about the order of k, so
+// each lane takes 8 consecutive elements of a row (one 16-byte load) as the
+// pairs of two products, and the tokens (8 per product, read through L1) are
+// taken in the same order.  With 4 steps in flight a warp has 8 KB of loads
+// outstanding.
 // Measured against the tensor-core tiles, us: one token through 8 x 1728
 // gated columns of hidden 5120 / 1024 / 128 45 / 6.8 / 3.3 against 55 / 14 /
 // 7.9 (6.3 TB/s at 5120); 8 tokens against 131072 columns 200 / 49 / 14

@@ -126,10 +126,6 @@ __device__ __forceinline__ void tc_tma_load(const CUtensorMap* map, uint32_t dst
       : "memory");
 }
 
-__device__ __forceinline__ void tc_prefetch_map(const CUtensorMap* map) {
-  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
-}
-
 __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
@@ -189,7 +185,6 @@ __device__ __forceinline__ void tc_ld_ready(float* v) {
                : "memory");
 }
 
-__device__ __forceinline__ void tc_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 // Shared-memory operand descriptor, 128-byte swizzle.  K-major: rows of 128
 // bytes, groups of 8 rows 1024 bytes apart (the stride offset; the leading

@@ -321,9 +321,10 @@ rra_status_t rra_allreduce_rmsnorm(const void* const* bufs, void* const* outs, i
  * needs its element's alignment only.
  *
  * The products need rra_init: their bounded internal waits (2 s) report to
- * the device status word, info = {RRA_ERR_TIMEOUT, CTA, -1, which wait}.  `workspace` is a device buffer of the caller,
- * 256-byte aligned, of at least the bytes the *_workspace_bytes function
- * gives; its contents need no preparation and mean nothing between calls.
+ * the device status word, info = {RRA_ERR_TIMEOUT, CTA, -1, which wait}.
+ * `workspace` is a device buffer of the caller, 256-byte aligned, of at
+ * least the bytes the *_workspace_bytes function gives; its contents need no
+ * preparation and mean nothing between calls.
  * Calls with different workspaces may overlap on the GPU; calls that share
  * one must be ordered.  Results do not depend on timing (no atomics).
  * Outputs must not overlap inputs, the workspace or one another
