@@ -299,7 +299,6 @@ __global__ void __launch_bounds__(kN8Threads) save8_reg_kernel(const __grid_cons
     }
   }
   const float tot = block_sum(ss, s_part);
-  pdl_next();
   const float inv = rsqrtf(tot / (float)a.hidden + a.eps);
   if (tid == 0) a.rstd[row] = inv;
 #pragma unroll
@@ -320,6 +319,7 @@ __global__ void __launch_bounds__(kN8Threads) save8_reg_kernel(const __grid_cons
     put_codes<DT>(a.codes + row * a.hidden + (size_t)u * PU, c, PU, true);
     if (u % (kCkptBlock / PU) == 0) a.scales[row * nblk + u / (kCkptBlock / PU)] = (uint8_t)(e + 127);
   }
+  pdl_next();
 }
 
 template <int N, int DT>
@@ -411,7 +411,6 @@ __global__ void __launch_bounds__(kN8Threads)
   const size_t units = (hidden + PU - 1) / PU;
   const size_t nblk = (hidden + kCkptBlock - 1) / kCkptBlock;
   pdl_wait();
-  pdl_next();
   for (size_t row = blockIdx.x; row < rows; row += gridDim.x) {
     const float q = rstd ? __ldg(rstd + row) : 1.f;
     char* orow = static_cast<char*>(out) + row * hidden * Elem<DT>::kSize;
@@ -439,6 +438,7 @@ __global__ void __launch_bounds__(kN8Threads)
       __syncthreads();
     }
   }
+  pdl_next();
 }
 
 // ---------------------------------------------------------------------------

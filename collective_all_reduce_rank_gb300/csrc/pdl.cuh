@@ -15,7 +15,10 @@ namespace rra {
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// Lets the next kernel's CTAs be placed as this one's leave.
+// Lets the next kernel's CTAs be placed as this one's leave.  A kernel whose
+// CTAs fill the GPU in one wave calls it last: called early, the next one's
+// CTAs took what slots were left, unevenly over the SMs (forward and restore
+// of 512 rows 18.5 us, called last 16.0).
 __device__ __forceinline__ void pdl_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 template <class... P, class... A>
