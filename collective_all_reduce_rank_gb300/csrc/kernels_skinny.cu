@@ -201,7 +201,6 @@ __global__ void __launch_bounds__(kSkThreads, 2) skinny_gate_kernel(const __grid
   const int g = (threadIdx.x & 31) >> 2, mine = (threadIdx.x >> 5) / KW;
   const int per = sk_gate_units(a.width, VEC);
   pdl_wait();
-  pdl_next();
   for (int u0 = blockIdx.x * SLOTS; u0 < a.units; u0 += gridDim.x * SLOTS) {
     {
       const int u = u0 + mine, r = u / per, f = sk_gate_row<VEC>(u - r * per, g);
@@ -227,6 +226,7 @@ __global__ void __launch_bounds__(kSkThreads, 2) skinny_gate_kernel(const __grid
     }
     __syncthreads();
   }
+  pdl_next();
 }
 
 // ---------------------------------------------------------------------------
@@ -250,7 +250,6 @@ __global__ void __launch_bounds__(kSkThreads, 2) skinny_lse_kernel(const __grid_
   const int token = threadIdx.x % (8 * NT);
   long long target = -1;
   pdl_wait();
-  pdl_next();
   if (token < a.tokens) {
     target = a.targets[token];
     if (target == a.ignore_index) target = -1;
@@ -298,6 +297,7 @@ __global__ void __launch_bounds__(kSkThreads, 2) skinny_lse_kernel(const __grid_
     }
     __syncthreads();
   }
+  pdl_next();
   run[threadIdx.x] = make_float2(m, s);
   __syncthreads();
   if (threadIdx.x < 8 * NT && token < a.tokens) {
