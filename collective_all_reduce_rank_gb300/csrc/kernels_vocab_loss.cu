@@ -19,7 +19,12 @@
 // leaves, lo[t], is kept in float32 and added back where the products'
 // epilogues still hold float32: lo[t] W[target] to row t of dx, lo[t] x[t] to
 // row target of dW (dW of 333 x 515 x 50021 off by 0.0017 in the 2-norm
-// against 0.0023 without).
+// against 0.0023 without).  Up to 32 tokens dW sums so few entries that their
+// roundings do not average out either; both halves of them fit the block of 64
+// rows that dW's product takes anyhow, so what bfloat16 leaves of every entry
+// is stored as 32 rows more at most (a shard's dW of 1 or 4 tokens x 346 off by
+// 0.0017 against 0.0023-0.0025 without; both gradients 31.7 -> 33 us, of 4
+// tokens x 5120 x 32768 237 -> 240 us).
 //
 // Bound by the tensor cores: the epilogue's exponentials (one per logit, 4 a
 // cycle and scheduler) run under the products of the next tile.  Measured:
@@ -114,6 +119,10 @@ struct EpiLse : TcNoState {
   }
 };
 
+// REST: what bfloat16 leaves of each entry is stored too, p.rest_row rows on.
+// A variant of its own: one kernel for both took 127 registers for 95 and 25.4
+// to 25.6 ms for 25.0 to 25.1 (8192 x 5120 x 131072, both passes).
+template <bool REST>
 struct EpiDlogits : TcNoState {
   static __device__ __forceinline__ void run(const TcArgs& p, const TcTile& x, int row0, int half, uint32_t addr,
                                              uint8_t* buf, const State&) {
@@ -131,7 +140,8 @@ struct EpiDlogits : TcNoState {
     for (int c = 0; c < 128; c += 64) {
       const int valid = g.N - c0 - c;
       if (valid <= 0) break;
-#pragma unroll 1
+      uint32_t rest[REST ? 32 : 1];
+#pragma unroll(REST ? 2 : 1)
       for (int k = 0; k < 64; k += 32) {
         float v[32];
         tc_ld32(addr + half * 128 + c + k, v);
@@ -149,9 +159,26 @@ struct EpiDlogits : TcNoState {
           for (int j = 0; j < 32; ++j) v[j] = 0.f;
         }
         tc_stage_bf16(buf, v, k / 8);
+        if (REST) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) rest[k / 2 + j / 2] = tc_pack2(left(v[j]), left(v[j + 1]));
+        }
       }
       tc_flush_bf16(buf, out + c, g.ld, g.M - row0, valid, true, true);
+      if (REST) {
+        const int r = threadIdx.x & 31;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          *reinterpret_cast<uint4*>(buf + r * 128 + ((k ^ (r & 7)) << 4)) =
+              make_uint4(rest[4 * k], rest[4 * k + 1], rest[4 * k + 2], rest[4 * k + 3]);
+        tc_flush_bf16(buf, out + c + p.rest_row * g.ld, g.ld, g.M - row0, valid, true, true);
+      }
     }
+  }
+
+  static __device__ __forceinline__ float left(float v) {
+    const float held = __bfloat162float(__float2bfloat16_rn(v));
+    return fabsf(held) < INFINITY ? v - held : 0.f;
   }
 };
 
@@ -160,7 +187,8 @@ cudaError_t launch_tc_lse(const TcArgs& p, cudaStream_t s, int* grid) {
 }
 
 cudaError_t launch_tc_dlogits(const TcArgs& p, cudaStream_t s, int* grid) {
-  return tc_launch<false, false, EpiDlogits>(p, s, grid);
+  return p.rest_row ? tc_launch<false, false, EpiDlogits<true>>(p, s, grid)
+                    : tc_launch<false, false, EpiDlogits<false>>(p, s, grid);
 }
 
 // What the backward pass needs beside the logits.  The first row_ctas CTAs

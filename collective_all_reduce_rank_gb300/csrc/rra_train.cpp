@@ -95,14 +95,26 @@ struct Placer {
     if (!padded(cols)) return m;
     m.ld = pad_ld(cols);
     m.p = ws.take(rows * m.ld * 2);
-    if (rows == 0) return m;
+    copy(p, const_cast<void*>(m.p), rows, m);
+    return m;
+  }
+  // The rows laid out twice, one copy behind the other.
+  Mat twice(const void* p, size_t rows, size_t cols) {
+    Mat m{nullptr, 2 * rows, cols, padded(cols) ? pad_ld(cols) : cols};
+    char* to = static_cast<char*>(ws.take(m.rows * m.ld * 2));
+    m.p = to;
+    copy(p, to, rows, m);
+    copy(p, to + rows * m.ld * 2, rows, m);
+    return m;
+  }
+  void copy(const void* p, void* to, size_t rows, const Mat& m) {
+    if (rows == 0) return;
     a.src[a.n] = p;
-    a.dst[a.n] = const_cast<void*>(m.p);
-    a.cols = (long long)cols;
+    a.dst[a.n] = to;
+    a.cols = (long long)m.cols;
     a.units = (int)(m.ld / 8);
     a.first[a.n + 1] = a.first[a.n] + (long long)rows * a.units;
     ++a.n;
-    return m;
   }
   bool launch(cudaStream_t s) { return a.n == 0 || launch_pad_rows(a, s) == cudaSuccess; }
 };
@@ -617,10 +629,16 @@ size_t vocab_tiles(int n, const size_t* vocab) {
 // backward needs beside a piece.
 struct LossPlan {
   size_t fixed = 0;        // bytes before the piece
+  size_t rows = 0;         // rows of dl
   size_t piece_tiles = 0;  // 256-column tiles per piece
   Split split;             // of dx's tiles
   bool acc = false;        // dx is summed over pieces in float32
 };
+
+// Whether dl keeps what bfloat16 leaves of its entries, as rows of their own
+// behind the tokens': while both fit the one block of 64 rows that the product
+// of the weights' gradient takes at the least, with x's rows laid out twice.
+bool rests(size_t T) { return T <= 32; }
 
 // Blocks of 32 rows of the first n shards.
 size_t blocks32(int n, const size_t* vocab) {
@@ -667,7 +685,9 @@ LossPlan loss_plan(int n, size_t T, size_t D, const size_t* vocab, bool back, si
     q.fixed = b.at;
     return q;
   }
-  const size_t col = T * 512;  // bytes of a tile column of dl
+  q.rows = rests(T) ? 2 * T : T;
+  const size_t col = q.rows * 512;  // bytes of a tile column of dl
+  if (rests(T)) b.take(q.rows * (padded(D) ? pad_ld(D) : D) * 2);
   const size_t base = b.at;
   // the parts of dx's K axis depend on the piece, which depends on the room
   // their slots leave: take the largest piece that fits with its own slots
@@ -715,7 +735,7 @@ extern "C" {
 size_t rra_vocab_loss_workspace_bytes(int nranks, size_t tokens, size_t hidden, const size_t* vocab, int backward) {
   if (nranks < 1 || nranks > kMaxRanks || !vocab) return 0;
   const LossPlan q = loss_plan(nranks, tokens, hidden, vocab, backward != 0, backward == 2 ? 0 : SIZE_MAX);
-  return q.fixed + up(q.piece_tiles * tokens * 512, kAlign);
+  return q.fixed + up(q.piece_tiles * q.rows * 512, kAlign);
 }
 
 rra_status_t rra_vocab_loss(const void* x, const void* const* weights, const size_t* vocab, const int64_t* targets,
@@ -821,7 +841,7 @@ rra_status_t rra_vocab_loss_backward(const void* x, const void* const* weights, 
   if (st != RRA_SUCCESS) return done(call, nranks, T * V, dtype, 0, st);
   if (T && !workspace) return done(call, nranks, T * V, dtype, 0, RRA_ERR_INVALID_ARG);
   const LossPlan q = loss_plan(nranks, T, D, vocab, true, workspace_bytes);
-  const size_t need = q.fixed + q.piece_tiles * T * 512;
+  const size_t need = q.fixed + q.piece_tiles * q.rows * 512;
   if (workspace_bytes < need) return done(call, nranks, T * V, dtype, 0, RRA_ERR_WORKSPACE);
   Ranges in{{x, T * D * 2}, {targets, T * 8}, {lse, T * 4}, {grad_loss, T * 4}},
       out{{workspace, need}, {dx, T * D * 2}};
@@ -844,6 +864,7 @@ rra_status_t rra_vocab_loss_backward(const void* x, const void* const* weights, 
   const Mat X = place(x, T, D);
   Mat W[kMaxRanks];
   for (int r = 0; r < nranks; ++r) W[r] = place(weights[r], vocab[r], D);
+  const Mat XX = rests(T) ? place.twice(x, T, D) : X;
   float4* rows = static_cast<float4*>(ws.take(T * sizeof(float4)));
   TcFix fix{};
   int* column = static_cast<int*>(ws.take(T * 4));
@@ -918,6 +939,7 @@ rra_status_t rra_vocab_loss_backward(const void* x, const void* const* weights, 
     one_k_axis(p, D);
     p->targets = reinterpret_cast<const long long*>(targets);
     p->rows = rows;
+    p->rest_row = rests(T) ? (int)T : 0;
     p->status = device_status();
     e = launch_tc_dlogits(*p, s, &grid);
     if (e != cudaSuccess) break;
@@ -960,10 +982,10 @@ rra_status_t rra_vocab_loss_backward(const void* x, const void* const* weights, 
     p->fix.kind = 2;
     p->fix.w[0] = X.p;
     p->fix.ld = (long long)X.ld;
-    ok = map_mn(&p->b[0], X);
+    ok = map_mn(&p->b[0], XX);
     for (int r = 0; r < nranks && ok; ++r) {
       if (hi[r] <= lo[r]) continue;
-      const Mat A{dl + at[r] * 2, T, hi[r] - lo[r], ld};
+      const Mat A{dl + at[r] * 2, q.rows, hi[r] - lo[r], ld};
       ok = map_mn(&p->a[r], A);
       TcGroup h{};
       h.a = r;
@@ -977,7 +999,7 @@ rra_status_t rra_vocab_loss_backward(const void* x, const void* const* weights, 
       ok = ok && add_group(p, h, false);
     }
     if (!ok) return done(call, nranks, T * V, dtype, 0, RRA_ERR_CUDA);
-    one_k_axis(p, T);
+    one_k_axis(p, q.rows);
     p->status = device_status();
     e = launch_tc_weight_grad(*p, s, &grid);
   }

@@ -85,6 +85,7 @@ struct TcArgs {
   const long long* targets;
   long long ignore_index;
   const float4* rows;  // dl: what loss_rows_kernel left per row
+  int rest_row;        // dl: rows from here on take what bfloat16 leaves of the others (0: not kept)
   TcFix fix;
   float2* part;      // [column part][part_ld] running maximum and sum
   long long part_ld;

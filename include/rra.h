@@ -443,8 +443,9 @@ rra_status_t rra_vocab_loss(const void* x, const void* const* weights, const siz
  *  vocabulary the logits are computed again,
  *    dl[t][v] = (exp(l[t][v] - lse[t]) - [v == targets[t]]) * grad_loss[t]
  *  is rounded to bfloat16 as operand of the two gradient products, but for
- *  the target's entry, whose rest is added to both results in float32; the
- *  products' sums are float32.  A row whose target is ignore_index or outside
+ *  the target's entry, whose rest is added to both results in float32 (up to
+ *  32 tokens the products of dweights take the rest of every entry, as
+ *  bfloat16); the products' sums are float32.  A row whose target is ignore_index or outside
  *  the vocabulary has a zero gradient, whatever grad_loss holds there.
  *  tokens == 0 writes zeros to dweights.  Errors as rra_vocab_loss. */
 rra_status_t rra_vocab_loss_backward(const void* x, const void* const* weights, const size_t* vocab,

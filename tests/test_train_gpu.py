@@ -156,6 +156,27 @@ def test_vocab_loss_backward(T, D, shards, room):
     ref.assert_norm_close(torch.cat(dW), torch.cat([w for w, _ in want["dW"]]), 2 * ref.BF, "dweights")
 
 
+@pytest.mark.parametrize("room", ["default", "least"])
+@pytest.mark.parametrize("T,D,shards", [
+    (1, 64, (256,)), (1, 346, (441,) * 6), (2, 515, (129, 0, 700)), (8, 1024, (1, 300)), (17, 72, (2000,)),
+    (31, 333, (129, 65)), (32, 5120, (260, 300)),
+])
+def test_weight_gradient_of_few_tokens(T, D, shards, room):
+    """dW of up to 32 tokens has no rounding of dl in it: one half step of its own."""
+    x, W, tgt, grad = loss_inputs(T, D, shards, 7 * T + D)
+    want = ref.vocab_loss(x, W, tgt, IGN, grad, rest=True)
+    dx, dW = poison(T, D), [poison(v, D) for v in shards]
+    ws = torch.empty(rra.rra_vocab_loss_workspace_bytes(T, D, shards, 1 if room == "default" else 2),
+                     dtype=torch.uint8, device="cuda")
+    rra.rra_vocab_loss_backward(x.cuda(), cuda(W), tgt.cuda(), want["lse"][0].float().cuda(), grad.cuda(), dx, dW,
+                                ignore_index=IGN, workspace=ws)
+    status_ok()
+    ref.assert_within(dx, *want["dx"], "dx")
+    for r in range(len(shards)):
+        if shards[r]:
+            ref.assert_within(dW[r], *want["dW"][r], "dweights[%d]" % r)
+
+
 @pytest.mark.parametrize("T,D,shards", [(300, 72, (40, 260)), (129, 515, (300,)), (3, 1024, (700, 90))])
 def test_many_tokens_of_one_target(T, D, shards):
     """More targets in a block of rows than a warp takes at a time, and none in the others."""

@@ -99,8 +99,8 @@ def ffn(x, gates, ups, act, dacts=None):
     return outs, bouts, (dx, bdx), list(zip(dG, bG)), list(zip(dU, bU))
 
 
-def vocab_loss(x, weights, targets, ignore, grad=None):
-    """(loss, lse) with bounds, and with grad (dx, [dW]) with bounds."""
+def vocab_loss(x, weights, targets, ignore, grad=None, rest=False):
+    """(loss, lse) with bounds, and with grad (dx, [dW]) with bounds; rest: dW of two halves of each entry of dl."""
     x = x.double()
     D = x.shape[1]
     W = torch.cat([w.double() for w in weights])
@@ -130,11 +130,13 @@ def vocab_loss(x, weights, targets, ignore, grad=None):
     # every entry is rounded to bfloat16 but the target's, whose rest is added in float32
     step = BF * (d.abs() + ed)
     step[rows[inside], targets[inside]] = (4 * F32 * (d.abs() + ed))[rows[inside], targets[inside]]
+    # two halves: the second is at most half a step of the first, and rounded in turn
+    ew = ed + (BF * step + 1e-38 if rest else step)
     ed = ed + step
     dx = d @ W
     bdx = ed @ W.abs() + product_err(d.abs(), W.abs(), V) + BF * dx.abs() + 1e-30
     dW = d.t() @ x
-    bW = ed.t() @ x.abs() + product_err(d.abs().t(), x.abs(), len(x)) + BF * dW.abs() + 1e-30
+    bW = ew.t() @ x.abs() + product_err(d.abs().t(), x.abs(), len(x)) + BF * dW.abs() + 1e-30
     sizes = [len(v) for v in weights]
     out["dx"] = (dx, bdx)
     out["dW"] = list(zip(torch.split(dW, sizes), torch.split(bW, sizes)))
