@@ -297,11 +297,14 @@ __device__ __forceinline__ int unit_valid(size_t u, size_t count) {
 // ---------------------------------------------------------------------------
 constexpr uint32_t kMaxSpin = 1u << 26;  // backstop iteration cap on every wait
 
+__device__ __forceinline__ unsigned long long wait_detail(int rank, int peer, int index) {
+  return (1ull << 63) | ((unsigned long long)(index & 0x7FFFFFFF) << 32) |
+         ((unsigned long long)(peer & 0xFFFF) << 16) | (unsigned long long)(rank & 0xFFFF);
+}
+
 __device__ __forceinline__ void record_error(DevStatus* st, int code, int rank, int peer, int index,
                                              uint32_t tag, bool root = false) {
-  const unsigned long long d = (1ull << 63) | ((unsigned long long)(index & 0x7FFFFFFF) << 32) |
-                               ((unsigned long long)(peer & 0xFFFF) << 16) |
-                               (unsigned long long)(rank & 0xFFFF);
+  const unsigned long long d = wait_detail(rank, peer, index);
   atomicCAS(&st->code, 0, code);
   atomicCAS(&st->detail, 0ull, d);
   if (root) atomicExch(&st->root_detail, d);
@@ -312,13 +315,22 @@ __device__ __forceinline__ bool aborted(const DevStatus* st, uint32_t tag) {
   return ld_relaxed_u32(&st->abort_tag) == tag;
 }
 
+// Whether a flag holds nothing of the call `mark` belongs to (its epoch in the
+// upper half, counts from 1 in the lower): a value of an earlier call, or the
+// zero of a fresh workspace, which has the first call's epoch.
+__device__ __forceinline__ bool unposted(uint64_t flag, uint64_t mark) {
+  return flag < ((mark & 0xFFFFFFFF00000000ull) | 1u);
+}
+
 // Wait until *flag >= target; *seen gets the value observed.  Returns false
 // (after recording a timeout unless another wait already gave up) when the
 // wait expires or the call was aborted.  Never unbounded: a %globaltimer
 // limit plus an iteration cap.  An expired wait is the "root" record when
 // the peer never joined the call: by default when the awaited flag itself
 // holds an earlier call's value; with `joined`, when the peer's joined flag
-// (raised by each of its CTAs before any wait) does.
+// (raised by each of its CTAs before any wait) does.  With `joined` a wait that
+// is still pending when the call is aborted records it too: a rank stuck behind
+// this one may have started its wait earlier and expired first.
 static __device__ __noinline__ bool wait_geq(const uint64_t* flag, uint64_t target, uint64_t* seen,
                                       const WaitCfg& w, uint32_t tag, int rank, int peer,
                                       int index, const uint64_t* joined = nullptr) {
@@ -335,14 +347,18 @@ static __device__ __noinline__ bool wait_geq(const uint64_t* flag, uint64_t targ
       return true;
     }
     if ((it & 15u) == 0u) {
-      if (aborted(w.status, tag)) return false;
+      if (aborted(w.status, tag)) {
+        if (joined && unposted(ld_acquire(joined), target))
+          atomicExch(&w.status->root_detail, wait_detail(rank, peer, index));
+        return false;
+      }
       if (globaltimer() - t0 > w.timeout_ns) break;
     }
     __nanosleep(64);
   }
   // The flag (or the peer's joined flag) still holds a value of an earlier
   // call: the peer took no part in this one.
-  const bool root = joined ? (ld_acquire(joined) >> 32) != (target >> 32) : (v >> 32) != (target >> 32);
+  const bool root = unposted(joined ? ld_acquire(joined) : v, target);
   record_error(w.status, RRA_ERR_TIMEOUT, rank, peer, index, tag, root);
   return false;
 }

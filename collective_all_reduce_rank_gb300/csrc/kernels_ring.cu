@@ -218,7 +218,7 @@ struct RingWarp {
         if (aborted(a.wait.status, tag)) {
           give_up = 1;
         } else if (globaltimer() - t0 > a.wait.timeout_ns || it >= kMaxSpin) {
-          const bool root = (ld_acquire(a.head + lin) >> 32) != (E >> 32);  // prev sent nothing
+          const bool root = unposted(ld_acquire(a.head + lin), E);  // prev sent nothing
           record_error(a.wait.status, RRA_ERR_TIMEOUT, r, prev, step, tag, root);
           give_up = 1;
         }

@@ -88,11 +88,14 @@ struct TreeLLWarp {
       int give_up = 0;
       if ((it & 15u) == 15u && lane == 0) {
         if (aborted(a.wait.status, tag)) {
+          // a rank stuck behind this one may have expired first
+          if (unposted(ld_acquire(a.joined + (size_t)peer * a.channels), E))
+            atomicExch(&a.wait.status->root_detail, wait_detail(r, peer, index));
           give_up = 1;
         } else if (globaltimer() - t0 > a.wait.timeout_ns || it >= kMaxSpin) {
           // the peer never started this call (its joined flag holds an
           // older epoch): the rank that failed, not one stuck behind it
-          const bool root = (ld_acquire(a.joined + (size_t)peer * a.channels) >> 32) != (E >> 32);
+          const bool root = unposted(ld_acquire(a.joined + (size_t)peer * a.channels), E);
           record_error(a.wait.status, RRA_ERR_TIMEOUT, r, peer, index, tag, root);
           give_up = 1;
         }
