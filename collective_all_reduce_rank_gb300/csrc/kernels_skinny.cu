@@ -42,12 +42,16 @@ constexpr int kSkThreads = 32 * kSkWarps;
 constexpr int kSkStep = 64;  // K elements per warp step
 constexpr int kSkDepth = 4;  // steps in flight per warp
 
-__device__ __forceinline__ void sk_mma(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                       uint32_t b1) {
+// Two products, of the first and the last two words of each lane's 16 bytes.
+// All lanes take part at once: the loads before branch by lane.
+__device__ __forceinline__ void sk_mma2(float* c, uint4 lo, uint4 hi, uint4 x) {
+  __syncwarp();
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%10,%11,%12,%13}, {%14,%15}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      : "r"(lo.x), "r"(hi.x), "r"(lo.y), "r"(hi.y), "r"(x.x), "r"(x.y), "r"(lo.z), "r"(hi.z), "r"(lo.w), "r"(hi.w),
+        "r"(x.z), "r"(x.w));
 }
 
 // Rows that are not whole 16-byte units (VEC false) start on any element,
@@ -155,13 +159,9 @@ __device__ __forceinline__ void sk_unit(const SkinnyArgs& a, const char* r0, con
       const int k = (s0 + u * KW) * kSkStep + t * 8;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint4 lo = w[u][2 * h], hi = w[u][2 * h + 1];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const uint4 x = sk_tokens<VEC>(xr[n], k + 32 * h - off, D);
-          sk_mma(c[n], lo.x, hi.x, lo.y, hi.y, x.x, x.y);
-          sk_mma(c[n], lo.z, hi.z, lo.w, hi.w, x.z, x.w);
-        }
+        for (int n = 0; n < NT; ++n)
+          sk_mma2(c[n], w[u][2 * h], w[u][2 * h + 1], sk_tokens<VEC>(xr[n], k + 32 * h - off, D));
       }
     }
   }

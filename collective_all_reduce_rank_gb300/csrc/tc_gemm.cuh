@@ -62,7 +62,9 @@ constexpr int kTcSmem = kTcRingBytes + kTcEpiWarps * kTcStoreBytes + 1024;  // +
 constexpr unsigned long long kTcWaitNs = 2000ull * 1000 * 1000;
 
 // ---------------------------------------------------------------------------
-// PTX
+// PTX.  An .aligned instruction needs all lanes of its warp at once: each
+// helper that issues one joins the lanes first, since its caller may have
+// sent them along different branches (a row's target, a row past the end).
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t tc_smem(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
@@ -73,6 +75,7 @@ __device__ __forceinline__ uint32_t tc_cta_rank() {
 }
 
 __device__ __forceinline__ void tc_cluster_sync() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
@@ -157,7 +160,7 @@ __device__ __forceinline__ float tc_exp2(float x) {
 // 32 lanes x 32 columns of float32: lane l of the warp gets row l.
 __device__ __forceinline__ void tc_ld32(uint32_t addr, float* v) {
   uint32_t r[32];
-  __syncwarp();  // lanes may have left the previous chunk by different paths
+  __syncwarp();
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
@@ -175,6 +178,7 @@ __device__ __forceinline__ void tc_ld32(uint32_t addr, float* v) {
 // Wait for this thread's tensor-memory reads; the values become usable here
 // (they are operands, so no use can move above the wait).
 __device__ __forceinline__ void tc_ld_ready(float* v) {
+  __syncwarp();
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
                  "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]),
@@ -321,6 +325,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 2) {
+    __syncwarp();
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc_smem(&sh.tmem)), "r"(512u)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
@@ -470,8 +475,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
   __syncthreads();
   tc_cluster_sync();
   tc_fence_after();
-  if (warp == 2)
+  if (warp == 2) {
+    __syncwarp();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+  }
 }
 
 // Launch on every SM pair that can hold a cluster, or fewer when there are
