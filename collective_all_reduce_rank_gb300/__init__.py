@@ -351,15 +351,20 @@ def _on(stream, device):
 
 def _scratch(workspace, device, stream, size, *args):
     """(pointer, bytes, tensor) of the caller's workspace, or of one made here
-    on the caller's stream (PyTorch's allocator reuses it in stream order).
-    The tensor is kept until the call has been issued."""
+    from the memory of the call's stream, which PyTorch's allocator hands out
+    and takes back in that stream's order (a block of another stream may still
+    be in use there).  The tensor is kept until the call has been issued."""
     if workspace is None:
-        if isinstance(stream, int) and stream:
-            raise ValueError("a raw stream handle needs an explicit workspace")
         torch = _t()
-        workspace = torch.empty(max(256, size(*args)), dtype=torch.uint8, device="cpu" if device < 0 else device)
-        if stream is not None and stream:
-            workspace.record_stream(stream)
+        if device < 0:  # refused by the call itself
+            workspace = torch.empty(max(256, size(*args)), dtype=torch.uint8, device="cpu")
+        elif stream is None or (isinstance(stream, int) and stream == torch._C._cuda_getCurrentRawStream(device)):
+            workspace = torch.empty(max(256, size(*args)), dtype=torch.uint8, device=device)
+        elif isinstance(stream, int):
+            raise ValueError("a raw stream handle needs an explicit workspace unless it is the current stream's")
+        else:
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(max(256, size(*args)), dtype=torch.uint8, device=device)
     elif not workspace.is_contiguous() or workspace.get_device() != device:
         raise ValueError("the workspace must be contiguous and on the tensors' device")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
