@@ -8,6 +8,8 @@
 
 #include <cuda_runtime.h>
 
+#include <cfloat>
+
 #include "rra.h"
 
 namespace rra {
@@ -23,6 +25,16 @@ __device__ __forceinline__ float gate_sigma(float g, float* slope) {
     *slope = c * fmaf(3.f * 0.044715f * g, g, 1.f);
   }
   return __fdividef(1.f, 1.f + __expf(-k));
+}
+
+// act'(g) = sigma (1 + g k'(g) (1 - sigma)) of what gate_sigma gave.  gelu's g
+// k'(g) grows as g^3 and passes float32's range at |g| = 1.2e13, where sigma
+// is 0 or 1: held finite, its product with the 0 is 0 (and the slope 0 or 1).
+template <int ACT>
+__device__ __forceinline__ float gate_slope(float g, float sigma, float slope) {
+  float z = g * slope;
+  if constexpr (ACT == RRA_ACT_GELU_TANH) z = fminf(fmaxf(z, -FLT_MAX), FLT_MAX);
+  return sigma * fmaf(z, 1.f - sigma, 1.f);
 }
 
 }  // namespace rra

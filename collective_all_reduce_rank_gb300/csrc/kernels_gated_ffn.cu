@@ -72,8 +72,8 @@ struct EpiGateBack : TcNoState {
       for (int j = 0; j < 32; ++j) {
         float k;
         const float s = gate_sigma<ACT>(a[j], &k);
-        const float h = a[j] * s;                            // act(g)
-        const float slope = s * fmaf(a[j] * k, 1.f - s, 1.f);  // act'(g)
+        const float h = a[j] * s;  // act(g)
+        const float slope = gate_slope<ACT>(a[j], s, k);
         a[j] = d[j] * b[j] * slope;
         b[j] = d[j] * h;
       }

@@ -94,6 +94,36 @@ def test_gated_ffn_backward(n, T, D, F, act):
     ref.assert_norm_close(dx, rdx, 2 * ref.BF, "dx")
 
 
+@pytest.mark.parametrize("T", [3, 40])
+@pytest.mark.parametrize("act", [0, 1])
+def test_slope_of_large_gates(T, act):
+    """Gates far out, up to where their square and cube pass float32: the slope is 0 or 1."""
+    D = 64
+    gen = torch.Generator().manual_seed(T)
+    gates = torch.tensor([s * v for v in (90.0, 1e6, 1e12, 2e13, 1e15, 1e19, 1e25, 1e30) for s in (1.0, -1.0)])
+    F = len(gates)
+    x, U, da = rnd(gen, T, D), rnd(gen, F, D, scale=0.1), rnd(gen, T, F, scale=1e-2)
+    x[:, 0] = 1.0
+    G = torch.zeros(F, D, dtype=torch.bfloat16)
+    G[:, 0] = gates  # so that every token's gate is the row's value, exactly
+    dx, dG, dU = poison(T, D), poison(F, D), poison(F, D)
+    rra.rra_gated_ffn_backward(x.cuda(), cuda([G]), cuda([U]), cuda([da]), dx, [dG], [dU], act=act)
+    status_ok()
+    X, g, W, d = x.double(), G[:, 0].double(), U.double(), da.double()
+    slope = (g > 0).double()
+    u, eu = X @ W.t(), ref.product_err(X.abs(), W.abs().t(), D)
+    dg, du = d * u * slope, d * g.clamp(min=0)
+    edg = d.abs() * eu * slope * (1 + ref.BF) + (ref.BF + 2.0 ** -20) * dg.abs()
+    edu = (ref.BF + 2.0 ** -19) * du.abs()  # act by the fast exponential and division: 2^-20
+    for got, v, e in ((dG, dg, edg), (dU, du, edu)):
+        want = v.t() @ X
+        ref.assert_within(got, want, e.t() @ X.abs() + ref.product_err(v.abs().t(), X.abs(), T)
+                          + ref.BF * want.abs() + 1e-30, "weights")
+    want = dg @ G.double() + du @ W
+    mag = ref.product_err(dg.abs(), G.double().abs(), 2 * F) + ref.product_err(du.abs(), W.abs(), 2 * F)
+    ref.assert_within(dx, want, edg @ G.double().abs() + edu @ W.abs() + mag + ref.BF * want.abs() + 1e-30, "dx")
+
+
 # -- vocabulary loss ---------------------------------------------------------
 
 LOSS = [  # tokens, hidden, shard heights
