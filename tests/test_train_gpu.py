@@ -163,6 +163,41 @@ def test_vocab_loss(T, D, shards):
     ref.assert_within(loss, *want["loss"], "loss")
 
 
+@pytest.mark.parametrize("D", [64, 515])
+@pytest.mark.parametrize("size", [0.0, 97.0, 1000.0])
+@pytest.mark.parametrize("T", [8, 16, 17, 300, 1300])
+def test_loss_where_the_target_has_nearly_all_of_the_mass(T, size, D):
+    """A target's logit of any size far above the others: the loss is next to nothing, and as exact as for small
+    logits (an absolute bound, whatever the size), few tokens and many alike."""
+    shards, groups = (700, 333), 5
+    V = sum(shards)
+    gen = torch.Generator().manual_seed(T + D)
+    # every logit is exact in any order of summation: `size` for all, less 6 to 12 in eighths, and 10 more for the
+    # target of the token's group
+    heads = torch.randperm(V, generator=gen)[:groups]
+    W, x = torch.zeros(V, D, dtype=torch.bfloat16), torch.zeros(T, D, dtype=torch.bfloat16)
+    W[:, 0] = size
+    W[:, 1] = -torch.randint(48, 97, (V,), generator=gen).to(torch.bfloat16) / 8
+    W[heads, 1] = 0
+    W[heads, 2 + torch.arange(groups)] = 10.0
+    mine = torch.arange(T) % groups
+    x[:, :2] = 1.0
+    x[torch.arange(T), 2 + mine] = 1.0
+    tgt = heads[mine]
+    loss, lse = poison(T, dtype=torch.float32), poison(T, dtype=torch.float32)
+    rra.rra_vocab_loss(x.cuda(), [w.contiguous().cuda() for w in torch.split(W, list(shards))], tgt.cuda(), loss, lse)
+    status_ok()
+    l = x.double() @ W.double().t()
+    want = torch.logsumexp(l, 1)
+    hit = l[torch.arange(T), tgt]
+    # the largest exponential is 1, the others (3e-4 in all) are off by 2^-22 of themselves, the sum takes at most
+    # 8 + 32 + 16 roundings of 2^-24 in a chain and its logarithm two more
+    off = 2.0 ** -22 * 3e-4 + 60 * ref.F32
+    ref.assert_within(loss, want - hit, torch.full((T,), off, dtype=torch.float64), "loss")
+    assert float(loss.min()) >= 0.0
+    ref.assert_within(lse, want, ref.F32 * want.abs() + off, "lse")
+
+
 @pytest.mark.parametrize("room", ["default", "least", "some"])
 @pytest.mark.parametrize("T,D,shards", LOSS)
 def test_vocab_loss_backward(T, D, shards, room):
