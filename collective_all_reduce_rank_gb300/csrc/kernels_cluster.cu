@@ -28,6 +28,7 @@
 // records RRA_ERR_TIMEOUT and skips the work, but the CTA keeps taking the
 // cluster barriers so its peers never wait on it forever.
 #include "cluster.cuh"
+#include "smem_limit.h"
 
 namespace rra {
 
@@ -164,8 +165,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1)
 template <int N, int DT>
 static cudaError_t c2_go(const TwoShotArgs& a, int grid, cudaStream_t s) {
   constexpr size_t smem = c2_smem<N>();
-  static const cudaError_t attr = cudaFuncSetAttribute(twoshot_cluster_kernel<N, DT>,
-                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const cudaError_t attr = raise_smem<twoshot_cluster_kernel<N, DT>>((int)smem);
   if (attr != cudaSuccess) return attr;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);

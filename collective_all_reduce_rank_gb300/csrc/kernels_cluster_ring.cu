@@ -28,6 +28,7 @@
 // Every mbarrier wait is bounded; on expiry the CTA records RRA_ERR_TIMEOUT
 // and stops working, but still takes the final cluster barrier.
 #include "cluster.cuh"
+#include "smem_limit.h"
 
 namespace rra {
 
@@ -274,8 +275,7 @@ __global__ void __launch_bounds__(kCRingThreads, 1) ring_cluster_kernel(const __
 template <int DT>
 static cudaError_t cring_go(const RingArgs& a, int grid, cudaStream_t s) {
   constexpr size_t smem = cring_smem<DT>();
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(ring_cluster_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const cudaError_t attr = raise_smem<ring_cluster_kernel<DT>>((int)smem);
   if (attr != cudaSuccess) return attr;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);

@@ -37,6 +37,7 @@
 
 #include "common.cuh"
 #include "pdl.cuh"
+#include "smem_limit.h"
 #include "tc_host.h"
 
 namespace rra {
@@ -633,8 +634,7 @@ static cudaError_t save_go(Save8Args a, cudaStream_t s) {
   if (fits_regs(DT, a.vec, a.hidden)) {
     return launch_pdl(save8_reg_kernel<N, DT>, (int)a.rows, kN8Threads, 0, s, a);
   }
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(save8_gen_kernel<N, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kN8SmemMax);
+  const cudaError_t attr = raise_smem<save8_gen_kernel<N, DT>>(kN8SmemMax);
   if (attr != cudaSuccess) return attr;
   size_t smem = row_smem(a.hidden);
   if (!a.vec && smem + smem / 4 <= kN8SmemMax) {
@@ -658,8 +658,7 @@ static cudaError_t back_go(const Back8Args& a, int* ctas, cudaStream_t s) {
     *ctas = even_ctas(a.rows, *ctas, 2 * device_sms());
     return launch_pdl(back8_reg_kernel<N, DT>, *ctas, kN8Threads, 0, s, a);
   }
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(back8_gen_kernel<N, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kN8SmemMax);
+  const cudaError_t attr = raise_smem<back8_gen_kernel<N, DT>>(kN8SmemMax);
   if (attr != cudaSuccess) return attr;
   // as few trips over a row as kN8MaxThreads allow, all of them full
   const int units = (int)((a.hidden + 16 / Elem<DT>::kSize - 1) / (16 / Elem<DT>::kSize));
@@ -715,8 +714,7 @@ cudaError_t launch_norm_save8(int n, int dt, bool vec, const void* const* in, vo
 template <int DT, bool VEC>
 static cudaError_t restore_go(const uint8_t* c, const uint8_t* e, const float* rstd, const void* gamma, void* out,
                               size_t rows, size_t hidden, int grid, cudaStream_t s) {
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(restore8_kernel<DT, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, kN8SmemMax);
+  const cudaError_t attr = raise_smem<restore8_kernel<DT, VEC>>(kN8SmemMax);
   if (attr != cudaSuccess) return attr;
   return launch_pdl(restore8_kernel<DT, VEC>, grid, kN8Threads, VEC ? 0 : row_smem(hidden), s, c, e, rstd, gamma, out,
                     rows, hidden);

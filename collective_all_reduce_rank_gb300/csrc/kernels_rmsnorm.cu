@@ -13,6 +13,7 @@
 // outputs.  Saves the separate normalisation kernel's full re-read and
 // re-write of the activations.
 #include "common.cuh"
+#include "smem_limit.h"
 
 namespace rra {
 
@@ -89,8 +90,7 @@ __global__ void __launch_bounds__(kNormThreads) allreduce_rmsnorm_kernel(const _
 template <int N, int DT, bool VEC>
 static cudaError_t norm_go(const NormArgs& a, cudaStream_t s) {
   const size_t smem = ((a.hidden + 7) / 8) * 8 * sizeof(float);
-  static const cudaError_t attr = cudaFuncSetAttribute(
-      allreduce_rmsnorm_kernel<N, DT, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+  const cudaError_t attr = raise_smem<allreduce_rmsnorm_kernel<N, DT, VEC>>(200 * 1024);
   if (attr != cudaSuccess) return attr;
   allreduce_rmsnorm_kernel<N, DT, VEC><<<(unsigned)a.rows, kNormThreads, smem, s>>>(a);
   return cudaGetLastError();

@@ -15,6 +15,7 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "smem_limit.h"
 
 namespace rra {
 
@@ -187,8 +188,7 @@ template <int N, int DT>
 static cudaError_t tma_go(const TmaArgs& a, int* grid, cudaStream_t s) {
   constexpr int S = tma_stages<N>();
   const size_t smem = (size_t)S * N * kTmaTile + 2 * kTmaTile;
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(oneshot_tma_kernel<N, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const cudaError_t attr = raise_smem<oneshot_tma_kernel<N, DT>>((int)smem);
   if (attr != cudaSuccess) return attr;
   int dev = 0, sms = 0;
   cudaGetDevice(&dev);

@@ -45,6 +45,7 @@
 
 #include "pdl.cuh"
 #include "rra_internal.h"
+#include "smem_limit.h"
 #include "tc_host.h"
 
 namespace rra {
@@ -485,9 +486,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
 // fewer tiles or an SM budget.
 template <bool AMN, bool BMN, class Epi>
 cudaError_t tc_launch(const TcArgs& p, cudaStream_t s, int* grid_out) {
-  auto kern = tc_gemm_kernel<AMN, BMN, Epi>;
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
+  constexpr auto kern = tc_gemm_kernel<AMN, BMN, Epi>;
+  const cudaError_t attr = raise_smem<kern>(kTcSmem);
   if (attr != cudaSuccess) return attr;
   const int grid = 2 * tc_clusters(tc_units(p));
   if (grid_out) *grid_out = grid;
