@@ -341,12 +341,22 @@ def _same_count(n, *groups):
 
 
 def _on(stream, device):
-    """The raw stream of the call (default: PyTorch's current one)."""
+    """The raw stream of the call (default: PyTorch's current one).  The
+    library launches on the current device, so the tensors have to be there."""
+    if device < 0:  # no GPU's: refused by the call itself
+        return 0 if stream is None else stream if isinstance(stream, int) else int(stream.cuda_stream)
+    cuda = _t()._C
+    current = cuda._cuda_getDevice()
+    if current != device:
+        raise ValueError("the tensors are on cuda:%d, the current device is cuda:%d" % (device, current))
     if stream is None:
-        if device < 0:
-            return 0
-        return _t()._C._cuda_getCurrentRawStream(device)
-    return stream if isinstance(stream, int) else int(stream.cuda_stream)
+        return cuda._cuda_getCurrentRawStream(device)
+    if isinstance(stream, int):
+        return stream
+    home = getattr(stream, "device_index", device)
+    if home != device:
+        raise ValueError("the stream is of cuda:%d, the tensors are on cuda:%d" % (home, device))
+    return int(stream.cuda_stream)
 
 
 def _scratch(workspace, device, stream, size, *args):

@@ -109,3 +109,21 @@ def test_a_call_on_another_stream_makes_its_workspace_there(call):
         assert int(total) == int(expect)
         for a, b in zip(outs, want):
             assert torch.equal(a, b)
+
+
+
+@pytest.mark.parametrize("stream", [None, 0, SimpleNamespace(cuda_stream=OTHER, device_index=1)])
+def test_tensors_of_a_device_that_is_not_current_are_refused(monkeypatch, stream):
+    """The library launches on the current device."""
+    monkeypatch.setattr(rra, "_t", lambda: Fake())  # device 0 is current
+    with pytest.raises(ValueError, match="current device"):
+        rra._on(stream, 1)
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    monkeypatch.setattr(rra, "_t", lambda: Fake())
+    with pytest.raises(ValueError, match="stream"):
+        rra._on(SimpleNamespace(cuda_stream=OTHER, device_index=1), 0)
+    assert rra._on(SimpleNamespace(cuda_stream=OTHER, device_index=0), 0) == OTHER
+    assert rra._on(SimpleNamespace(cuda_stream=OTHER), 0) == OTHER
+    assert rra._on(None, 0) == MAIN and rra._on(OTHER, 0) == OTHER and rra._on(None, -1) == 0
