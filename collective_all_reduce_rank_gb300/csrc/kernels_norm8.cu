@@ -273,133 +273,148 @@ __device__ __forceinline__ void store_row_any(char* dst, const char* units, int 
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
-template <int N, int DT>
+// A CTA takes a row, or (LOOP: an SM budget leaves fewer CTAs than rows) every
+// gridDim-th row.  The loop costs up to 16 registers, so it is a variant.
+template <int N, int DT, bool LOOP>
 __global__ void __launch_bounds__(kN8Threads) save8_reg_kernel(const __grid_constant__ Save8Args a) {
   constexpr int PU = Elem<DT>::kPerUnit, U = kN8Regs / PU;
-  __shared__ float s_part[kN8Threads / 32];
+  __shared__ float s_part[2][kN8Threads / 32];
   const int units = (int)(a.hidden / PU), tid = threadIdx.x;
-  const size_t row = blockIdx.x, row_off = row * a.hidden * Elem<DT>::kSize;
   const size_t nblk = (a.hidden + kCkptBlock - 1) / kCkptBlock;
-  float f[U][PU];
-  float ss = 0.f;
+  int flip = 0;
+  size_t row = blockIdx.x;
   pdl_wait();
+  do {
+    const size_t row_off = row * a.hidden * Elem<DT>::kSize;
+    float f[U][PU];
+    float ss = 0.f;
 #pragma unroll
-  for (int j = 0; j < U; ++j) {
-    if (j * kN8Threads >= units) break;
-    const int u = j * kN8Threads + tid;
+    for (int j = 0; j < U; ++j) {
+      if (j * kN8Threads >= units) break;
+      const int u = j * kN8Threads + tid;
 #pragma unroll
-    for (int i = 0; i < PU; ++i) f[j][i] = 0.f;
-    if (u < units) {
-      Acc s;
-      sum_ranks<N, DT>(a.in, row_off, u, PU, true, s);
+      for (int i = 0; i < PU; ++i) f[j][i] = 0.f;
+      if (u < units) {
+        Acc s;
+        sum_ranks<N, DT>(a.in, row_off, u, PU, true, s);
 #pragma unroll
-      for (int i = 0; i < PU; ++i) {
-        f[j][i] = __uint_as_float(s.w[i]);
-        ss = __fmaf_rn(f[j][i], f[j][i], ss);
+        for (int i = 0; i < PU; ++i) {
+          f[j][i] = __uint_as_float(s.w[i]);
+          ss = __fmaf_rn(f[j][i], f[j][i], ss);
+        }
       }
     }
-  }
-  const float tot = block_sum(ss, s_part);
-  const float inv = rsqrtf(tot / (float)a.hidden + a.eps);
-  if (tid == 0) a.rstd[row] = inv;
+    const float tot = block_sum(ss, s_part[flip]);
+    const float inv = rsqrtf(tot / (float)a.hidden + a.eps);
+    if (tid == 0) a.rstd[row] = inv;
 #pragma unroll
-  for (int j = 0; j < U; ++j) {
-    if (j * kN8Threads >= units) break;
-    const int u = j * kN8Threads + tid;
-    int e;
-    const uint2 c = encode_unit<DT>(f[j], &e);
-    if (u >= units) continue;
-    float g[PU];
-    load_gamma<DT>(a.gamma, u, PU, true, g);
-    Acc y;
+    for (int j = 0; j < U; ++j) {
+      if (j * kN8Threads >= units) break;
+      const int u = j * kN8Threads + tid;
+      int e;
+      const uint2 c = encode_unit<DT>(f[j], &e);
+      if (u >= units) continue;
+      float g[PU];
+      load_gamma<DT>(a.gamma, u, PU, true, g);
+      Acc y;
 #pragma unroll
-    for (int i = 0; i < PU; ++i) y.w[i] = __float_as_uint(__fmul_rn(__fmul_rn(f[j][i], inv), g[i]));
-    const uint4 o = acc_narrow<DT>(y);
+      for (int i = 0; i < PU; ++i) y.w[i] = __float_as_uint(__fmul_rn(__fmul_rn(f[j][i], inv), g[i]));
+      const uint4 o = acc_narrow<DT>(y);
 #pragma unroll
-    for (int r = 0; r < N; ++r) st_stream(static_cast<char*>(a.out[r]) + row_off + (size_t)u * 16, o);
-    put_codes<DT>(a.codes + row * a.hidden + (size_t)u * PU, c, PU, true);
-    if (u % (kCkptBlock / PU) == 0) a.scales[row * nblk + u / (kCkptBlock / PU)] = (uint8_t)(e + 127);
-  }
+      for (int r = 0; r < N; ++r) st_stream(static_cast<char*>(a.out[r]) + row_off + (size_t)u * 16, o);
+      put_codes<DT>(a.codes + row * a.hidden + (size_t)u * PU, c, PU, true);
+      if (u % (kCkptBlock / PU) == 0) a.scales[row * nblk + u / (kCkptBlock / PU)] = (uint8_t)(e + 127);
+    }
+    row += gridDim.x;
+    flip ^= 1;
+  } while (LOOP && row < a.rows);
   pdl_next();
 }
 
-template <int N, int DT>
+template <int N, int DT, bool LOOP>
 __global__ void __launch_bounds__(kN8Threads) save8_gen_kernel(const __grid_constant__ Save8Args a) {
   constexpr int PU = Elem<DT>::kPerUnit;
   extern __shared__ __align__(16) char smem[];  // PU float32 per unit, then (stage_codes) the row's codes
-  __shared__ float s_part[kN8Threads / 32];
-  const size_t hidden = a.hidden, units = (hidden + PU - 1) / PU, row = blockIdx.x;
-  const size_t row_off = row * hidden * Elem<DT>::kSize;
+  __shared__ float s_part[2][kN8Threads / 32];
+  const size_t hidden = a.hidden, units = (hidden + PU - 1) / PU;
   const size_t nblk = (hidden + kCkptBlock - 1) / kCkptBlock;
   const int tid = threadIdx.x;
-  uint8_t* crow = a.codes + row * hidden;
   uint8_t* cstage = reinterpret_cast<uint8_t*>(smem + units * PU * 4);
-  float ss = 0.f;
+  int flip = 0;
+  size_t row = blockIdx.x;
   pdl_wait();
-  for (size_t u0 = 0; u0 < units; u0 += kN8Threads) {
-    const size_t u = u0 + tid;
-    const int v = u < units ? unit_valid<DT>(u, hidden) : 0;
-    float f[PU];
+  do {
+    const size_t row_off = row * hidden * Elem<DT>::kSize;
+    uint8_t* crow = a.codes + row * hidden;
+    float ss = 0.f;
+    for (size_t u0 = 0; u0 < units; u0 += kN8Threads) {
+      const size_t u = u0 + tid;
+      const int v = u < units ? unit_valid<DT>(u, hidden) : 0;
+      float f[PU];
 #pragma unroll
-    for (int i = 0; i < PU; ++i) f[i] = 0.f;
-    if (v) {
-      Acc s;
-      sum_ranks<N, DT>(a.in, row_off, u, v, a.vec, s);
+      for (int i = 0; i < PU; ++i) f[i] = 0.f;
+      if (v) {
+        Acc s;
+        sum_ranks<N, DT>(a.in, row_off, u, v, a.vec, s);
 #pragma unroll
-      for (int i = 0; i < PU; ++i) {
-        f[i] = i < v ? __uint_as_float(s.w[i]) : 0.f;
-        ss = __fmaf_rn(f[i], f[i], ss);
+        for (int i = 0; i < PU; ++i) {
+          f[i] = i < v ? __uint_as_float(s.w[i]) : 0.f;
+          ss = __fmaf_rn(f[i], f[i], ss);
+        }
+        float4* o = reinterpret_cast<float4*>(smem + u * PU * 4);
+#pragma unroll
+        for (int i = 0; i < PU / 4; ++i) o[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
       }
-      float4* o = reinterpret_cast<float4*>(smem + u * PU * 4);
-#pragma unroll
-      for (int i = 0; i < PU / 4; ++i) o[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
-    }
-    int e;
-    const uint2 c = encode_unit<DT>(f, &e);
-    if (v) {
-      if (a.stage_codes)
-        put_codes<DT>(cstage + u * PU, c, PU, true);
-      else
-        put_codes<DT>(crow + u * PU, c, v, a.vec);
-      if (u % (kCkptBlock / PU) == 0) a.scales[row * nblk + u / (kCkptBlock / PU)] = (uint8_t)(e + 127);
-    }
-  }
-  const float tot = block_sum(ss, s_part);
-  pdl_next();
-  const float inv = rsqrtf(tot / (float)hidden + a.eps);
-  if (tid == 0) a.rstd[row] = inv;
-  for (size_t u = tid; u < units; u += kN8Threads) {
-    const int v = unit_valid<DT>(u, hidden);
-    float g[PU];
-    load_gamma<DT>(a.gamma, u, v, a.vec, g);
-    const float* f = reinterpret_cast<const float*>(smem + u * PU * 4);
-    Acc y;
-#pragma unroll
-    for (int i = 0; i < PU; ++i) y.w[i] = __float_as_uint(__fmul_rn(__fmul_rn(f[i], inv), g[i]));
-    const uint4 o = acc_narrow<DT>(y);
-    if (a.vec) {
-#pragma unroll
-      for (int r = 0; r < N; ++r) st_stream(static_cast<char*>(a.out[r]) + row_off + u * 16, o);
-    } else {
-      *reinterpret_cast<uint4*>(smem + u * PU * 4) = o;  // over this thread's own sums
-    }
-  }
-  if (!a.vec) {
-    __syncthreads();
-#pragma unroll
-    for (int r = 0; r < N; ++r) store_row_any<DT>(static_cast<char*>(a.out[r]) + row_off, smem, PU * 4, hidden);
-    if (a.stage_codes) {  // whole words of the row of bytes
-      const size_t head = (4 - ((uintptr_t)crow & 3)) & 3;
-      if (tid < head && tid < hidden) crow[tid] = cstage[tid];
-      for (size_t i = head + 4 * tid; i < hidden; i += 4 * kN8Threads) {
-        if (i + 4 <= hidden)
-          *reinterpret_cast<uint32_t*>(crow + i) = (uint32_t)cstage[i] | ((uint32_t)cstage[i + 1] << 8) |
-                                                   ((uint32_t)cstage[i + 2] << 16) | ((uint32_t)cstage[i + 3] << 24);
+      int e;
+      const uint2 c = encode_unit<DT>(f, &e);
+      if (v) {
+        if (a.stage_codes)
+          put_codes<DT>(cstage + u * PU, c, PU, true);
         else
-          for (size_t k = i; k < hidden; ++k) crow[k] = cstage[k];
+          put_codes<DT>(crow + u * PU, c, v, a.vec);
+        if (u % (kCkptBlock / PU) == 0) a.scales[row * nblk + u / (kCkptBlock / PU)] = (uint8_t)(e + 127);
       }
     }
-  }
+    const float tot = block_sum(ss, s_part[flip]);
+    if (!LOOP || row + gridDim.x >= a.rows) pdl_next();
+    const float inv = rsqrtf(tot / (float)hidden + a.eps);
+    if (tid == 0) a.rstd[row] = inv;
+    for (size_t u = tid; u < units; u += kN8Threads) {
+      const int v = unit_valid<DT>(u, hidden);
+      float g[PU];
+      load_gamma<DT>(a.gamma, u, v, a.vec, g);
+      const float* f = reinterpret_cast<const float*>(smem + u * PU * 4);
+      Acc y;
+#pragma unroll
+      for (int i = 0; i < PU; ++i) y.w[i] = __float_as_uint(__fmul_rn(__fmul_rn(f[i], inv), g[i]));
+      const uint4 o = acc_narrow<DT>(y);
+      if (a.vec) {
+#pragma unroll
+        for (int r = 0; r < N; ++r) st_stream(static_cast<char*>(a.out[r]) + row_off + u * 16, o);
+      } else {
+        *reinterpret_cast<uint4*>(smem + u * PU * 4) = o;  // over this thread's own sums
+      }
+    }
+    if (!a.vec) {
+      __syncthreads();
+#pragma unroll
+      for (int r = 0; r < N; ++r) store_row_any<DT>(static_cast<char*>(a.out[r]) + row_off, smem, PU * 4, hidden);
+      if (a.stage_codes) {  // whole words of the row of bytes
+        const size_t head = (4 - ((uintptr_t)crow & 3)) & 3;
+        if (tid < head && tid < hidden) crow[tid] = cstage[tid];
+        for (size_t i = head + 4 * tid; i < hidden; i += 4 * kN8Threads) {
+          if (i + 4 <= hidden)
+            *reinterpret_cast<uint32_t*>(crow + i) = (uint32_t)cstage[i] | ((uint32_t)cstage[i + 1] << 8) |
+                                                     ((uint32_t)cstage[i + 2] << 16) | ((uint32_t)cstage[i + 3] << 24);
+          else
+            for (size_t k = i; k < hidden; ++k) crow[k] = cstage[k];
+        }
+      }
+      if (LOOP) __syncthreads();  // the staged row has left
+    }
+    row += gridDim.x;
+    flip ^= 1;
+  } while (LOOP && row < a.rows);
 }
 
 // out = code 2^e, times rstd of the row and gamma of the column where given.
@@ -595,27 +610,32 @@ __global__ void __launch_bounds__(kN8MaxThreads, N >= 6 ? 2 : 3) back8_gen_kerne
 }
 
 // dgamma[c] = sum over the CTAs' partial rows, in order: 32 columns x 32
-// strided row groups per CTA.
+// strided row groups per CTA (LOOP: every gridDim-th 32 columns).
+template <bool LOOP>
 __global__ void __launch_bounds__(1024) dgamma_join_kernel(const float* part, int parts, size_t pitch, size_t hidden,
                                                            float* dgamma) {
   __shared__ float red[32][33];
   const int lane = threadIdx.x & 31, k = threadIdx.x >> 5;
-  const size_t c = (size_t)blockIdx.x * 32 + lane;
-  float v = 0.f;
   pdl_wait();
   pdl_next();
-  if (c < hidden) {
+  size_t c0 = (size_t)blockIdx.x * 32;
+  do {
+    const size_t c = c0 + lane;
+    float v = 0.f;
+    if (c < hidden) {
 #pragma unroll 4
-    for (int i = k; i < parts; i += 32) v += part[(size_t)i * pitch + c];
-  }
-  red[k][lane] = v;
-  __syncthreads();
-  // thread (k, lane) takes row group `lane` of column k: one warp a column
-  float t = red[lane][k];
+      for (int i = k; i < parts; i += 32) v += part[(size_t)i * pitch + c];
+    }
+    red[k][lane] = v;
+    __syncthreads();
+    // thread (k, lane) takes row group `lane` of column k: one warp a column
+    float t = red[lane][k];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-  const size_t cc = (size_t)blockIdx.x * 32 + k;
-  if (lane == 0 && cc < hidden) dgamma[cc] = t;
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    if (lane == 0 && c0 + k < hidden) dgamma[c0 + k] = t;
+    c0 += (size_t)gridDim.x * 32;
+    if (LOOP) __syncthreads();  // red is free
+  } while (LOOP && c0 < hidden);
 }
 
 // ---------------------------------------------------------------------------
@@ -629,19 +649,17 @@ static bool fits_regs(int dt, bool vec, size_t hidden) {
   return vec && hidden / pu <= kN8Regs / pu * kN8Threads;
 }
 
-template <int N, int DT>
-static cudaError_t save_go(Save8Args a, cudaStream_t s) {
-  if (fits_regs(DT, a.vec, a.hidden)) {
-    return launch_pdl(save8_reg_kernel<N, DT>, (int)a.rows, kN8Threads, 0, s, a);
-  }
-  const cudaError_t attr = raise_smem<save8_gen_kernel<N, DT>>(kN8SmemMax);
+template <int N, int DT, bool LOOP>
+static cudaError_t save_go(Save8Args a, int grid, cudaStream_t s) {
+  if (fits_regs(DT, a.vec, a.hidden)) return launch_pdl(save8_reg_kernel<N, DT, LOOP>, grid, kN8Threads, 0, s, a);
+  const cudaError_t attr = raise_smem<save8_gen_kernel<N, DT, LOOP>>(kN8SmemMax);
   if (attr != cudaSuccess) return attr;
   size_t smem = row_smem(a.hidden);
   if (!a.vec && smem + smem / 4 <= kN8SmemMax) {
     a.stage_codes = 1;
     smem += smem / 4;
   }
-  return launch_pdl(save8_gen_kernel<N, DT>, (int)a.rows, kN8Threads, smem, s, a);
+  return launch_pdl(save8_gen_kernel<N, DT, LOOP>, grid, kN8Threads, smem, s, a);
 }
 
 // CTAs of the backward kernel: all resident, every CTA the same number of
@@ -674,7 +692,10 @@ static cudaError_t back_go(const Back8Args& a, int* ctas, cudaStream_t s) {
 
 template <int N>
 static cudaError_t save_n(int dt, const Save8Args& a, cudaStream_t s) {
-  return dt == RRA_FLOAT32 ? save_go<N, RRA_FLOAT32>(a, s) : save_go<N, RRA_BFLOAT16>(a, s);
+  const int grid = budget(a.rows);
+  if ((size_t)grid < a.rows)
+    return dt == RRA_FLOAT32 ? save_go<N, RRA_FLOAT32, true>(a, grid, s) : save_go<N, RRA_BFLOAT16, true>(a, grid, s);
+  return dt == RRA_FLOAT32 ? save_go<N, RRA_FLOAT32, false>(a, grid, s) : save_go<N, RRA_BFLOAT16, false>(a, grid, s);
 }
 
 template <int N>
@@ -772,7 +793,10 @@ cudaError_t launch_norm_back8(int n, int dt, bool vec, const void* const* grads,
     default: return cudaErrorInvalidValue;
   }
   if (e != cudaSuccess) return e;
-  return launch_pdl(dgamma_join_kernel, (int)((hidden + 31) / 32), 1024, 0, s, part, ctas, a.pitch, hidden, dgamma);
+  const size_t want = (hidden + 31) / 32;
+  const int grid = budget(want);
+  return launch_pdl((size_t)grid < want ? dgamma_join_kernel<true> : dgamma_join_kernel<false>, grid, 1024, 0, s, part,
+                    ctas, a.pitch, hidden, dgamma);
 }
 
 }  // namespace rra

@@ -185,11 +185,8 @@ cudaError_t launch_tc_weight_grad(const TcArgs& p, cudaStream_t s, int* grid) {
 
 constexpr int kRowThreads = 256;
 
-// One CTA per 8 rows of a tile; a thread takes 8 columns of one.
-__global__ void __launch_bounds__(kRowThreads) join_tiles_kernel(const __grid_constant__ JoinTiles j, int first) {
-  pdl_wait();
-  pdl_next();
-  const int tile = first + blockIdx.x / 32, slab = blockIdx.x % 32;
+// A CTA takes 8 rows of a tile at a time, a thread 8 columns of one.
+__device__ __forceinline__ void join_slab(const JoinTiles& j, int tile, int slab) {
   int m, n;
   tc_walk(tile, j.mt, j.nt, m, n);
   const bool vec = j.cols % 8 == 0 && ((uintptr_t)j.out & 15) == 0;
@@ -243,11 +240,19 @@ __global__ void __launch_bounds__(kRowThreads) join_tiles_kernel(const __grid_co
   }
 }
 
+__global__ void __launch_bounds__(kRowThreads)
+    join_tiles_kernel(const __grid_constant__ JoinTiles j, int first, int slabs) {
+  pdl_wait();
+  pdl_next();
+  for (int i = blockIdx.x; i < slabs; i += gridDim.x) join_slab(j, first + i / 32, i % 32);
+}
+
 cudaError_t launch_join_tiles(const JoinTiles& j, cudaStream_t s) {
   // without `acc` the whole tiles are in the output already
   const int first = j.acc ? 0 : j.full, tiles = j.mt * j.nt;
   if (first >= tiles || (!j.acc && j.splits == 1)) return cudaSuccess;
-  return launch_pdl(join_tiles_kernel, (tiles - first) * 32, kRowThreads, 0, s, j, first);
+  const int slabs = (tiles - first) * 32;
+  return launch_pdl(join_tiles_kernel, budget(slabs), kRowThreads, 0, s, j, first, slabs);
 }
 
 // Rows of up to 17 matrices to padded rows (16-byte units), one launch: a

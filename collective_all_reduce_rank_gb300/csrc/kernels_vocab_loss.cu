@@ -210,10 +210,10 @@ cudaError_t launch_tc_dlogits(const TcArgs& p, cudaStream_t s, int* grid) {
 }
 
 // What the backward pass needs beside the logits.  The first row_ctas CTAs
-// take the tokens, per token: {lse in units of log 2, the target's entry in
+// take the tokens, the CTAs from index0 on the index (under an SM budget all of
+// them both), per token: {lse in units of log 2, the target's entry in
 // bfloat16, 1 if the row has a gradient, grad}, the target (-1: none) and
-// what bfloat16 leaves of its entry.  The others make the index of the tokens
-// by target: a warp per token counts the tokens that come before it, a warp
+// what bfloat16 leaves of its entry.  The index of the tokens by target: a warp per token counts the tokens that come before it, a warp
 // per block of 32 vocabulary rows those before the block: tokens x (tokens +
 // V / 32) comparisons (0.06 ms for 8192 tokens and 131072 rows), and no order
 // that depends on timing.
@@ -232,7 +232,7 @@ struct RowsArgs {
   int* start;
   int* token;
   int* sorted;
-  int hidden, nranks, vec, tokens, row_ctas, items;
+  int hidden, nranks, vec, tokens, row_ctas, index0, items;
 };
 
 __device__ __forceinline__ long long live_target(const RowsArgs& a, int row) {
@@ -245,8 +245,8 @@ __device__ __forceinline__ long long live_target(const RowsArgs& a, int row) {
 constexpr int kIndexItems = 8;
 
 __device__ __forceinline__ void loss_index(const RowsArgs& a) {
-  const int lane = threadIdx.x & 31, ctas = gridDim.x - a.row_ctas;
-  for (int i0 = ((blockIdx.x - a.row_ctas) * 8 + (threadIdx.x >> 5)) * kIndexItems; i0 < a.items;
+  const int lane = threadIdx.x & 31, ctas = gridDim.x - a.index0;
+  for (int i0 = ((blockIdx.x - a.index0) * 8 + (threadIdx.x >> 5)) * kIndexItems; i0 < a.items;
        i0 += ctas * 8 * kIndexItems) {
     int key[kIndexItems];  // targets before this one count (-1: nothing to place)
     int tie[kIndexItems];  // and equal ones of tokens before this one
@@ -289,18 +289,11 @@ __device__ __forceinline__ void loss_index(const RowsArgs& a) {
   }
 }
 
-// R rows per CTA: 256 / R threads a row.
+// R rows at a time per CTA: 256 / R threads a row.
 template <int R>
-__global__ void __launch_bounds__(256) loss_rows_kernel(const __grid_constant__ RowsArgs a) {
+__device__ __forceinline__ void loss_row(const RowsArgs& a, int block, float* part) {
   constexpr int PER = 256 / R;
-  __shared__ float part[8];
-  pdl_wait();
-  pdl_next();
-  if ((int)blockIdx.x >= a.row_ctas) {
-    loss_index(a);
-    return;
-  }
-  const int row = blockIdx.x * R + threadIdx.x / PER, i = threadIdx.x % PER;
+  const int row = block * R + threadIdx.x / PER, i = threadIdx.x % PER;
   const long long t = row < a.tokens ? live_target(a, row) : -1;
   float l = 0.f;
   if (t >= 0) {
@@ -333,6 +326,20 @@ __global__ void __launch_bounds__(256) loss_rows_kernel(const __grid_constant__ 
   a.lo[row] = rest;
 }
 
+template <int R>
+__global__ void __launch_bounds__(256) loss_rows_kernel(const __grid_constant__ RowsArgs a) {
+  __shared__ float part[8];
+  pdl_wait();
+  pdl_next();
+  if ((int)blockIdx.x < a.row_ctas) {
+    for (int b = blockIdx.x; b * R < a.tokens; b += a.row_ctas) {
+      loss_row<R>(a, b, part);
+      if (R == 1) __syncthreads();  // part is free
+    }
+  }
+  if ((int)blockIdx.x >= a.index0) loss_index(a);
+}
+
 cudaError_t launch_loss_rows(const void* x, const void* const* w, const size_t* vocab, int n, size_t hidden, int tokens,
                              const long long* targets, long long ignore_index, const float* lse, const float* grad,
                              float4* rows, int* column, float* lo, int* start, int* token, int* sorted,
@@ -363,12 +370,17 @@ cudaError_t launch_loss_rows(const void* x, const void* const* w, const size_t* 
   const int index_ctas = want < most ? want : most;
   // one row per CTA while that leaves SMs idle, else 8
   const bool few = tokens < 8 * device_sms();
-  a.row_ctas = few ? tokens : (tokens + 7) / 8;
-  return few ? launch_pdl(loss_rows_kernel<1>, a.row_ctas + index_ctas, 256, 0, s, a)
-             : launch_pdl(loss_rows_kernel<8>, a.row_ctas + index_ctas, 256, 0, s, a);
+  a.row_ctas = a.index0 = few ? tokens : (tokens + 7) / 8;
+  const int grid = budget((size_t)a.row_ctas + index_ctas);
+  if (grid < a.row_ctas + index_ctas) {
+    a.row_ctas = grid;
+    a.index0 = 0;
+  }
+  return few ? launch_pdl(loss_rows_kernel<1>, grid, 256, 0, s, a)
+             : launch_pdl(loss_rows_kernel<8>, grid, 256, 0, s, a);
 }
 
-// Join the column parts of each row, R rows per CTA (256 threads: 256 / R
+// Join the column parts of each row, R rows per CTA at a time (256 threads: 256 / R
 // threads a row, lanes of neighbouring rows side by side so that loads of
 // the [part][row] array stay whole sectors), and refine the target's logit.
 //
@@ -409,16 +421,11 @@ __device__ __forceinline__ void join_one(float& m, float& s, float2 q) {
 }
 
 template <int R>
-__global__ void __launch_bounds__(256) loss_join_kernel(const __grid_constant__ JoinArgs a) {
+__device__ __forceinline__ void join_rows(const JoinArgs& a, int row0, float2* red, float* dots) {
   constexpr int PER = 256 / R;  // threads a row
-  __shared__ float2 red[256];
-  __shared__ float dots[8];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = tid % R, k = tid / R;
-  const int row0 = blockIdx.x * R;
   const int row = row0 + r;
-  pdl_wait();
-  pdl_next();
   float m = -INFINITY, s = 0.f;
   if (row < a.rows) {
     const float2* p = a.part + row;
@@ -487,6 +494,27 @@ __global__ void __launch_bounds__(256) loss_join_kernel(const __grid_constant__ 
   }
 }
 
+// LOOP: every gridDim-th R rows (an SM budget leaves fewer CTAs).
+template <int R, bool LOOP>
+__global__ void __launch_bounds__(256) loss_join_kernel(const __grid_constant__ JoinArgs a) {
+  __shared__ float2 red[256];
+  __shared__ float dots[8];
+  pdl_wait();
+  pdl_next();
+  int row0 = blockIdx.x * R;
+  do {
+    join_rows<R>(a, row0, red, dots);
+    row0 += gridDim.x * R;
+    if (LOOP) __syncthreads();  // red and dots are free
+  } while (LOOP && row0 < a.rows);
+}
+
+template <int R>
+static cudaError_t join_go(const JoinArgs& a, cudaStream_t s) {
+  const int want = (a.rows + R - 1) / R, grid = budget(want);
+  return launch_pdl(grid < want ? loss_join_kernel<R, true> : loss_join_kernel<R, false>, grid, 256, 0, s, a);
+}
+
 cudaError_t launch_loss_join(const float2* part, int parts, const float* hit, const long long* targets,
                              long long ignore_index, const void* x, const void* const* w, const size_t* vocab, int n,
                              size_t hidden, int rows, float* loss, float* lse, cudaStream_t s) {
@@ -509,9 +537,7 @@ cudaError_t launch_loss_join(const float2* part, int parts, const float* hit, co
   a.loss = loss;
   a.lse = lse;
   // one row per CTA while that leaves SMs idle, else 8 (whole sectors of parts)
-  if (rows < 8 * device_sms())
-    return launch_pdl(loss_join_kernel<1>, rows, 256, 0, s, a);
-  return launch_pdl(loss_join_kernel<8>, (rows + 7) / 8, 256, 0, s, a);
+  return rows < 8 * device_sms() ? join_go<1>(a, s) : join_go<8>(a, s);
 }
 
 }  // namespace rra

@@ -11,6 +11,8 @@
 
 #include <utility>
 
+#include "rra_internal.h"
+
 namespace rra {
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -23,6 +25,7 @@ __device__ __forceinline__ void pdl_next() { asm volatile("griddepcontrol.launch
 
 template <class... P, class... A>
 cudaError_t launch_pdl(void (*kernel)(P...), int grid, int threads, size_t smem, cudaStream_t s, A&&... args) {
+  note_grid(grid);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3((unsigned)threads);

@@ -233,6 +233,18 @@ constexpr int kL128PackBatch = 8;
 // grids with it.
 int max_ctas_cap();
 
+// CTAs of a launch that has `want` units of work and loops over them: all of
+// them, or the SM budget.
+inline int budget(size_t want) {
+  const int cap = max_ctas_cap();
+  return (int)(cap > 0 && (size_t)cap < want ? (size_t)cap : want);
+}
+
+// The largest grid launched on this thread since the last take_grid: what a
+// call of several launches records.
+void note_grid(int grid);
+int take_grid();
+
 // Settings of rra_host.cpp that the allocation-free entry point
 // (noalloc.cu) honours too: the bound of device waits
 // (rra_set_timeout_ns), the rank fault injection silences

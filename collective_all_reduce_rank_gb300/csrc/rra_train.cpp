@@ -211,11 +211,22 @@ Fn encode_fn() {
   return fn;
 }
 
+// Ends a call: its record has the largest grid of its launches.
 rra_status_t done(const char* call, int n, size_t count, int dt, int grid, rra_status_t st) {
-  return record_call(call, RRA_ALGO_DIRECT, n, count, dt, grid, st);
+  return record_call(call, RRA_ALGO_DIRECT, n, count, dt, std::max(grid, take_grid()), st);
 }
 
+thread_local int g_largest_grid = 0;
+
 }  // namespace
+
+void rra::note_grid(int grid) { g_largest_grid = std::max(g_largest_grid, grid); }
+
+int rra::take_grid() {
+  const int g = g_largest_grid;
+  g_largest_grid = 0;
+  return g;
+}
 
 // ---------------------------------------------------------------------------
 // shared with the kernels
@@ -292,7 +303,7 @@ rra_status_t rra_allreduce_rmsnorm_save8(const void* const* bufs, void* const* o
   const bool vec = norm_vec(bufs, (const void* const*)outs, nranks, gamma, codes, hidden, e);
   const cudaError_t err = launch_norm_save8(nranks, dtype, vec, bufs, outs, gamma, rows, hidden, eps, codes, scales,
                                             rstd, reinterpret_cast<cudaStream_t>(stream));
-  return done(call, nranks, count, dtype, (int)rows, cuda_st(err));
+  return done(call, nranks, count, dtype, 0, cuda_st(err));
 }
 
 rra_status_t rra_rmsnorm_restore8(const void* codes, const void* scales, const float* rstd, const void* gamma,
@@ -354,7 +365,7 @@ rra_status_t rra_allreduce_rmsnorm_backward8(const void* const* grads, void* con
   const bool vec = norm_vec(grads, (const void* const*)dxs, nranks, gamma, codes, hidden, e);
   const cudaError_t err = launch_norm_back8(nranks, dtype, vec, grads, dxs, codes, scales, rstd, gamma, dgamma,
                                             static_cast<float*>(workspace), rows, hidden, s);
-  return done(call, nranks, count, dtype, norm_back8_ctas(rows), cuda_st(err));
+  return done(call, nranks, count, dtype, 0, cuda_st(err));
 }
 
 }  // extern "C"

@@ -557,7 +557,8 @@ void rra_set_timeout_ns(uint64_t ns);
  *  `max_ctas` CTAs per launch (0 = no limit, the default, or RRA_MAX_CTAS
  *  from the environment).  Streaming kernels shrink their grid and loop
  *  longer; ring and two-shot use at most max_ctas / nranks channels (at
- *  least one). */
+ *  least one); the tensor-core products of the training operators run as
+ *  pairs of CTAs (at least one). */
 void rra_set_max_ctas(int max_ctas);
 
 /** Fault injection for tests: virtual rank `rank` posts no step flag in the
@@ -573,8 +574,8 @@ const char* rra_status_string(rra_status_t status);
 
 /** Flight recorder ([AIH] "Common environment variables and debugging":
  *  a record of each rank's recent collectives): writes the last calls
- *  (sequence number, call, algo, nranks, count, dtype, grid, result), one
- *  per line, oldest first, into buf (NUL-terminated, truncated to len).
+ *  (sequence number, call, algo, nranks, count, dtype, grid, result; grid is
+ *  the largest of a call's launches), one per line, oldest first, into buf (NUL-terminated, truncated to len).
  *  Returns the number of calls written. */
 int rra_dump_recent(char* buf, size_t len);
 

@@ -596,6 +596,85 @@ def test_sm_budget_and_the_recorder():
         assert torch.equal(a, b)
 
 
+def largest_grid(call):
+    """Of the launches of the last call of this name."""
+    line = [l for l in rra.rra_dump_recent().splitlines() if " %s " % call in l][-1]
+    return int(line.split("grid=")[1].split()[0])
+
+
+def under_budget(max_ctas, call, name, least=1):
+    """`call` under an SM budget: no launch of it has more CTAs."""
+    rra.rra_set_max_ctas(max_ctas)
+    try:
+        call()
+        torch.cuda.synchronize()
+        assert largest_grid(name) <= max(least, max_ctas), "%s: %d CTAs" % (name, largest_grid(name))
+    finally:
+        rra.rra_set_max_ctas(0)
+
+
+@pytest.mark.parametrize("max_ctas", [1, 7, 64])
+@pytest.mark.parametrize("T,D", [(300, 5120), (130, 1027), (90, 8192), (75, 51200), (70, 51199)])
+def test_norm_keeps_the_sm_budget(T, D, max_ctas):
+    gen = torch.Generator().manual_seed(D)
+    xs, gamma = [rnd(gen, T, D).cuda() for _ in range(2)], rnd(gen, D).cuda()
+
+    def results():
+        return dict(outs=[poison(T, D) for _ in xs], codes=poison(T, D, dtype=torch.uint8),
+                    scales=poison(T, -(-D // 128), dtype=torch.uint8), rstd=poison(T, dtype=torch.float32),
+                    again=poison(T, D), dxs=[poison(T, D) for _ in xs], dgamma=poison(D, dtype=torch.float32))
+
+    def save(o):
+        rra.rra_allreduce_rmsnorm_save8(xs, o["outs"], gamma, D, o["codes"], o["scales"], o["rstd"])
+
+    def restore(o):
+        rra.rra_rmsnorm_restore8(o["codes"], o["scales"], o["rstd"], gamma, o["again"])
+
+    def back(o):
+        rra.rra_allreduce_rmsnorm_backward8(xs, o["dxs"], o["codes"], o["scales"], o["rstd"], gamma, o["dgamma"])
+
+    want, small = results(), results()
+    for call in (save, restore, back):
+        call(want)
+    under_budget(max_ctas, lambda: save(small), "allreduce_rmsnorm_save8")
+    under_budget(max_ctas, lambda: restore(small), "rmsnorm_restore8")
+    under_budget(max_ctas, lambda: back(small), "allreduce_rmsnorm_backward8")
+    status_ok()
+    a, b = want.pop("dgamma").double(), small.pop("dgamma").double()
+    for x, y in zip(flat(want), flat(small)):
+        assert torch.equal(x, y)
+    # rows are added in another order: chains of at most T additions
+    mag = (sum(x.double().abs() for x in xs) * 4 * xs[0].double().abs().max()).sum(0)
+    assert bool(((a - b).abs() <= 2 * T * ref.F32 * mag).all())
+
+
+@pytest.mark.parametrize("max_ctas", [1, 7, 64])
+@pytest.mark.parametrize("T", [5, 20, 300, 1300])
+def test_products_keep_the_sm_budget(T, max_ctas):
+    d = step_inputs(T=T, D=515, F=130, V=1500)
+    d["tgt"][::5] = IGN
+    d["tgt"][1::7] = 40
+    ws = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
+    want, small = step_outputs(d), step_outputs(d)
+    run_step(d, want, ws)
+    calls = {
+        "gated_ffn": lambda o: rra.rra_gated_ffn(d["x"], d["G"], d["U"], o["acts"], workspace=ws),
+        "gated_ffn_backward": lambda o: rra.rra_gated_ffn_backward(d["x"], d["G"], d["U"], d["da"], o["dx"], o["dG"],
+                                                                   o["dU"], workspace=ws),
+        "vocab_loss": lambda o: rra.rra_vocab_loss(d["x"], d["W"], d["tgt"], o["loss"], o["lse"], workspace=ws),
+        "vocab_loss_backward": lambda o: rra.rra_vocab_loss_backward(d["x"], d["W"], d["tgt"], want["lse"], d["grad"],
+                                                                     o["dx2"], o["dW"], workspace=ws),
+    }
+    for name, call in calls.items():
+        under_budget(max_ctas, lambda: call(small), name, least=2)  # products run as pairs of CTAs
+    status_ok()
+    for k in ("loss", "lse"):  # few tokens: the parts of the statistics are the CTAs'
+        a, b = want.pop(k), small.pop(k)
+        assert torch.allclose(a, b, rtol=0, atol=2.0 ** -19) if T <= 16 else torch.equal(a, b)
+    for x, y in zip(flat(want), flat(small)):
+        assert torch.equal(x, y)
+
+
 def test_weights_past_four_gigabytes():
     """A shard of more than 2^32 bytes: the last rows land where they belong."""
     D, V = 4096, 540_001  # 4.42 GB
