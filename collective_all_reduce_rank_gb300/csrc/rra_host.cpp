@@ -1207,9 +1207,10 @@ rra_status_t rra_allreduce_rmsnorm(const void* const* bufs, void* const* outs, i
   if (rows == 0) return record(call, RRA_ALGO_ONE_SHOT, nranks, 0, dtype, 0, RRA_SUCCESS);
   const bool vec = all_aligned16(bufs, nranks) && all_aligned16((const void* const*)outs, nranks) &&
                    aligned(gamma, 16) && (hidden * e) % 16 == 0;
-  const cudaError_t err = launch_allreduce_rmsnorm(nranks, dtype, vec, bufs, outs, gamma, rows, hidden, eps,
+  int grid = 0;
+  const cudaError_t err = launch_allreduce_rmsnorm(nranks, dtype, vec, bufs, outs, gamma, rows, hidden, eps, &grid,
                                                    reinterpret_cast<cudaStream_t>(stream));
-  return record(call, RRA_ALGO_ONE_SHOT, nranks, count, dtype, (int)rows, cuda_status(err));
+  return record(call, RRA_ALGO_ONE_SHOT, nranks, count, dtype, grid, cuda_status(err));
 }
 
 size_t rra_ll_wire_bytes(size_t payload_bytes) { return 8 * ((payload_bytes + 3) / 4); }

@@ -274,7 +274,7 @@ cudaError_t launch_oneshot_tma(int n, int dt, const void* const* in, void* const
 // All-reduce + RMSNorm, one CTA per row (hidden <= kNormMaxHidden).
 constexpr size_t kNormMaxHidden = 51200;
 cudaError_t launch_allreduce_rmsnorm(int n, int dt, bool vec, const void* const* in, void* const* out,
-                                     const void* gamma, size_t rows, size_t hidden, float eps,
+                                     const void* gamma, size_t rows, size_t hidden, float eps, int* grid,
                                      cudaStream_t s);
 
 // Persistent kernels are launched cooperatively: every CTA is resident or

@@ -648,6 +648,20 @@ def test_norm_keeps_the_sm_budget(T, D, max_ctas):
     assert bool(((a - b).abs() <= 2 * T * ref.F32 * mag).all())
 
 
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("max_ctas", [1, 7, 64])
+@pytest.mark.parametrize("T,D", [(300, 5120), (130, 1027), (66, 51200)])
+def test_fused_norm_keeps_the_sm_budget(T, D, max_ctas, dtype):
+    gen = torch.Generator().manual_seed(D)
+    dt = getattr(torch, dtype)
+    xs, gamma = [rnd(gen, T, D, dtype=dt).cuda() for _ in range(3)], rnd(gen, D, dtype=dt).cuda()
+    want, small = [poison(T, D, dtype=dt) for _ in xs], [poison(T, D, dtype=dt) for _ in xs]
+    rra.rra_allreduce_rmsnorm(xs, want, gamma, D)
+    under_budget(max_ctas, lambda: rra.rra_allreduce_rmsnorm(xs, small, gamma, D), "allreduce_rmsnorm")
+    status_ok()
+    assert all(torch.equal(a, b) for a, b in zip(want, small))
+
+
 @pytest.mark.parametrize("max_ctas", [1, 7, 64])
 @pytest.mark.parametrize("T", [5, 20, 300, 1300])
 def test_products_keep_the_sm_budget(T, max_ctas):
