@@ -333,11 +333,13 @@ def _flat_ranks(what, ts, dtype, numel, device):
 
 
 def _same_count(n, *groups):
+    """The status of a call with n ranks, which have to have a buffer each in every group."""
     if not 1 <= n <= RRA_MAX_RANKS:
-        raise RraError(RRA_ERR_INVALID_ARG if n < 1 else RRA_ERR_UNSUPPORTED, "number of ranks")
+        return RRA_ERR_INVALID_ARG if n < 1 else RRA_ERR_UNSUPPORTED
     for g in groups:
         if len(g) != n:
             raise ValueError("one buffer per rank is needed")
+    return RRA_SUCCESS
 
 
 def _on(stream, device):
@@ -401,7 +403,9 @@ def rra_allreduce_rmsnorm_save8(bufs, outs, gamma, hidden, codes, scales, rstd, 
     pass: codes [rows, hidden] (float8_e4m3fn or uint8), scales
     [rows, ceil(hidden / 128)] uint8, rstd [rows] float32."""
     n = len(bufs)
-    _same_count(n, outs)
+    st = _same_count(n, outs)
+    if st != RRA_SUCCESS:
+        return _ret(st, "rra_allreduce_rmsnorm_save8", check)
     torch = _t()
     x = bufs[0]
     dev, dt, count = x.get_device(), x.dtype, x.numel()
@@ -440,7 +444,9 @@ def rra_allreduce_rmsnorm_backward8(grads, dxs, codes, scales, rstd, gamma, dgam
                                     check=True) -> int:
     """Sum of the ranks' gradients through the norm, from the checkpoint."""
     n = len(grads)
-    _same_count(n, dxs)
+    st = _same_count(n, dxs)
+    if st != RRA_SUCCESS:
+        return _ret(st, "rra_allreduce_rmsnorm_backward8", check)
     torch = _t()
     x = grads[0]
     dev, dt, count, hidden = x.get_device(), x.dtype, x.numel(), gamma.numel()
@@ -465,7 +471,9 @@ def rra_gated_ffn_workspace_bytes(nranks: int, tokens: int, hidden: int, width: 
 def rra_gated_ffn(x, gates, ups, acts, act=RRA_ACT_SILU, workspace=None, stream=None, check=True) -> int:
     """acts[r] = act(x gates[r]^T) * (x ups[r]^T)."""
     n = len(gates)
-    _same_count(n, ups, acts)
+    st = _same_count(n, ups, acts)
+    if st != RRA_SUCCESS:
+        return _ret(st, "rra_gated_ffn", check)
     _t()
     T, D = x.shape
     F, dev, dt = gates[0].shape[0], x.get_device(), x.dtype
@@ -482,7 +490,9 @@ def rra_gated_ffn_backward(x, gates, ups, dacts, dx, dgates, dups, act=RRA_ACT_S
                            check=True) -> int:
     """Gradients of rra_gated_ffn: dx summed over the ranks, dgates, dups."""
     n = len(gates)
-    _same_count(n, ups, dacts, dgates, dups)
+    st = _same_count(n, ups, dacts, dgates, dups)
+    if st != RRA_SUCCESS:
+        return _ret(st, "rra_gated_ffn_backward", check)
     _t()
     T, D = x.shape
     F, dev, dt = gates[0].shape[0], x.get_device(), x.dtype
@@ -504,7 +514,7 @@ def _sizes(xs):
 def rra_vocab_loss_workspace_bytes(tokens: int, hidden: int, vocab, backward) -> int:
     """vocab: the ranks' shard heights; backward 2: the least bytes the
     backward pass runs with."""
-    _same_count(len(vocab))
+    _ret(_same_count(len(vocab)), "rra_vocab_loss_workspace_bytes", True)
     return int(load().rra_vocab_loss_workspace_bytes(len(vocab), tokens, hidden, _sizes(vocab), int(backward)))
 
 
@@ -512,7 +522,9 @@ def rra_vocab_loss(x, weights, targets, loss, lse, ignore_index=-100, workspace=
     """loss[t] = lse[t] - logit of targets[t], logits x W^T never kept; the
     vocabulary is the ranks' weight shards, one after another."""
     n = len(weights)
-    _same_count(n)
+    st = _same_count(n)
+    if st != RRA_SUCCESS:
+        return _ret(st, "rra_vocab_loss", check)
     torch = _t()
     T, D = x.shape
     dev, dt = x.get_device(), x.dtype
@@ -530,7 +542,9 @@ def rra_vocab_loss_backward(x, weights, targets, lse, grad_loss, dx, dweights, i
                             stream=None, check=True) -> int:
     """Gradients of rra_vocab_loss with respect to x and every shard."""
     n = len(weights)
-    _same_count(n, dweights)
+    st = _same_count(n, dweights)
+    if st != RRA_SUCCESS:
+        return _ret(st, "rra_vocab_loss_backward", check)
     torch = _t()
     T, D = x.shape
     dev, dt = x.get_device(), x.dtype

@@ -220,3 +220,26 @@ def test_binding_checks_shapes_and_types():
     with pytest.raises(rra.RraError) as err:
         rra.rra_gated_ffn(x, [w], [w], [a], act=5, stream=0, workspace=torch.zeros(0, dtype=torch.uint8))
     assert err.value.status == INV
+
+
+@pytest.mark.parametrize("n,status", [(0, INV), (9, UNS)])
+def test_a_number_of_ranks_that_is_refused_is_returned_without_check(n, status):
+    torch = pytest.importorskip("torch")
+    bf = torch.bfloat16
+    x, w, a, f = (torch.zeros(4, 16, dtype=bf), [torch.zeros(8, 16, dtype=bf)] * n, [torch.zeros(4, 8, dtype=bf)] * n,
+                  torch.zeros(4))
+    xs, tgt, row = [x] * n, torch.zeros(4, dtype=torch.int64), torch.zeros(16, dtype=bf)
+    saved = (torch.zeros(4, 16, dtype=torch.uint8), torch.zeros(4, 1, dtype=torch.uint8), f)
+    calls = [
+        lambda **k: rra.rra_allreduce_rmsnorm_save8(xs, xs, row, 16, *saved, **k),
+        lambda **k: rra.rra_allreduce_rmsnorm_backward8(xs, xs, *saved, row, torch.zeros(16), **k),
+        lambda **k: rra.rra_gated_ffn(x, w, w, a, **k),
+        lambda **k: rra.rra_gated_ffn_backward(x, w, w, a, x, w, w, **k),
+        lambda **k: rra.rra_vocab_loss(x, w, tgt, f, f, **k),
+        lambda **k: rra.rra_vocab_loss_backward(x, w, tgt, f, f, x, w, **k),
+    ]
+    for call in calls:
+        assert call(check=False) == status
+        with pytest.raises(rra.RraError) as err:
+            call()
+        assert err.value.status == status
