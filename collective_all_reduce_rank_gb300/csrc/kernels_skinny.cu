@@ -317,11 +317,12 @@ __global__ void __launch_bounds__(kSkThreads, 2) skinny_lse_kernel(const __grid_
 
 // ---------------------------------------------------------------------------
 
-int skinny_grid(long long units) {
-  long long cap = 2ll * device_sms();
-  if (max_ctas_cap() > 0 && max_ctas_cap() < cap) cap = max_ctas_cap();
+int skinny_most(long long units) {
+  const long long cap = 2ll * device_sms();
   return (int)(units < cap ? units : cap);
 }
+
+int skinny_grid(long long units) { return budget((size_t)skinny_most(units)); }
 
 // Warps that share a row: the smallest power of two that leaves each at most
 // 2 kSkDepth steps of it and, where there are few units, fills the SMs.

@@ -675,7 +675,7 @@ LossPlan loss_plan(int n, size_t T, size_t D, const size_t* vocab, bool back, si
   if (T == 0) return q;
   Bump b{nullptr};
   if (!back && skinny(T, D, vocab_rows(n, vocab) * D)) {
-    b.take((size_t)skinny_grid(skinny_units(n, vocab, D)) * T * sizeof(float2));
+    b.take((size_t)skinny_most(skinny_units(n, vocab, D)) * T * sizeof(float2));
     b.take(T * 4);
     q.fixed = b.at;
     return q;
@@ -786,7 +786,7 @@ rra_status_t rra_vocab_loss(const void* x, const void* const* weights, const siz
     for (int r = nranks; r < kMaxRanks; ++r) a.unit0[r + 1] = a.units;
     a.targets = reinterpret_cast<const long long*>(targets);
     a.ignore_index = ignore_index;
-    a.part = static_cast<float2*>(ws.take((size_t)skinny_grid(a.units) * T * sizeof(float2)));
+    a.part = static_cast<float2*>(ws.take((size_t)skinny_most(a.units) * T * sizeof(float2)));
     a.hit = static_cast<float*>(ws.take(T * 4));
     int grid = 0;
     cudaError_t e = launch_skinny_lse(a, s, &grid);

@@ -130,6 +130,7 @@ struct SkinnyArgs {
   float2* part;  // [grid][tokens]
   float* hit;
 };
+int skinny_most(long long units);  // CTAs without an SM budget: what a workspace holds parts for
 int skinny_grid(long long units);
 // Units of a shard: 8 gated columns or 16 vocabulary rows each (vec: rows of
 // whole 16-byte units), counted in whole blocks of 64 or 128 otherwise.

@@ -689,6 +689,24 @@ def test_products_keep_the_sm_budget(T, max_ctas):
         assert torch.equal(x, y)
 
 
+def test_a_workspace_does_not_depend_on_the_sm_budget():
+    """Its size is asked for under a budget, the call made without one."""
+    x, W, tgt, _ = loss_inputs(8, 64, (9000,), 21)
+    shards = [9000]
+    rra.rra_set_max_ctas(1)
+    try:
+        nb = rra.rra_vocab_loss_workspace_bytes(8, 64, shards, 0)
+    finally:
+        rra.rra_set_max_ctas(0)
+    assert nb == rra.rra_vocab_loss_workspace_bytes(8, 64, shards, 0)
+    loss, lse = poison(8, dtype=torch.float32), poison(8, dtype=torch.float32)
+    ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+    rra.rra_vocab_loss(x.cuda(), cuda(W), tgt.cuda(), loss, lse, ignore_index=IGN, workspace=ws)
+    status_ok()
+    want = ref.vocab_loss(x, W, tgt, IGN)
+    ref.assert_within(lse, *want["lse"], "lse")
+
+
 def test_weights_past_four_gigabytes():
     """A shard of more than 2^32 bytes: the last rows land where they belong."""
     D, V = 4096, 540_001  # 4.42 GB
