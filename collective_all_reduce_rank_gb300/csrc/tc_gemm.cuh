@@ -392,6 +392,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
           }
         }
       }
+      // A stage's release is a commit of the first CTA's products that arrives
+      // in both CTAs: none may leave before the last ones have landed in it.
+      for (int i = 0; i < nstages && ok && !is_a; ++i) {
+        ok = tc_wait(empty0 + 8 * s, parity, &sh, p.status, 5);
+        if (++s == nstages) {
+          s = 0;
+          parity ^= 1;
+        }
+      }
     }
     __syncwarp();
   } else if (warp == 1) {
