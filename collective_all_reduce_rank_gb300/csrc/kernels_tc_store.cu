@@ -185,7 +185,28 @@ cudaError_t launch_tc_weight_grad(const TcArgs& p, cudaStream_t s, int* grid) {
 
 constexpr int kRowThreads = 256;
 
+// Columns c to c + 7 of row r (lc and lr within the tile) as the products left them.
+__device__ __forceinline__ void join_row(const JoinTiles& j, int tile, int r, int lr, int c, int lc, float4& a, float4& b) {
+  if (tile < j.full || j.splits == 1) {
+    const float4* q = reinterpret_cast<const float4*>(j.acc + (long long)r * j.ld + c);
+    a = __ldcs(q);
+    b = __ldcs(q + 1);
+  } else {
+    const float* q = j.slots + (long long)(tile - j.full) * j.splits * 65536 + lr * 256 + lc;
+    a = __ldcs(reinterpret_cast<const float4*>(q));
+    b = __ldcs(reinterpret_cast<const float4*>(q) + 1);
+#pragma unroll 4
+    for (int k = 1; k < j.splits; ++k) {
+      const float4* z = reinterpret_cast<const float4*>(q + k * 65536);
+      const float4 x = __ldcs(z), y = __ldcs(z + 1);
+      a = make_float4(a.x + x.x, a.y + x.y, a.z + x.z, a.w + x.w);
+      b = make_float4(b.x + y.x, b.y + y.y, b.z + y.z, b.w + y.w);
+    }
+  }
+}
+
 // A CTA takes 8 rows of a tile at a time, a thread 8 columns of one.
+template <bool REST>
 __device__ __forceinline__ void join_slab(const JoinTiles& j, int tile, int slab) {
   int m, n;
   tc_walk(tile, j.mt, j.nt, m, n);
@@ -194,21 +215,12 @@ __device__ __forceinline__ void join_slab(const JoinTiles& j, int tile, int slab
   const int r = m * 256 + lr, c = n * 256 + lc;
   if (r < j.rows && c < j.cols) {
     float4 a, b;
-    if (tile < j.full || j.splits == 1) {
-      const float4* q = reinterpret_cast<const float4*>(j.acc + (long long)r * j.ld + c);
-      a = __ldcs(q);
-      b = __ldcs(q + 1);
-    } else {
-      const float* q = j.slots + (long long)(tile - j.full) * j.splits * 65536 + lr * 256 + lc;
-      a = __ldcs(reinterpret_cast<const float4*>(q));
-      b = __ldcs(reinterpret_cast<const float4*>(q) + 1);
-#pragma unroll 4
-      for (int k = 1; k < j.splits; ++k) {
-        const float4* z = reinterpret_cast<const float4*>(q + k * 65536);
-        const float4 x = __ldcs(z), y = __ldcs(z + 1);
-        a = make_float4(a.x + x.x, a.y + x.y, a.z + x.z, a.w + x.w);
-        b = make_float4(b.x + y.x, b.y + y.y, b.z + y.z, b.w + y.w);
-      }
+    join_row(j, tile, r, lr, c, lc, a, b);
+    if (REST) {
+      float4 x, y;
+      join_row(j, tile, r + j.rest, lr + j.rest, c, lc, x, y);
+      a = make_float4(a.x + x.x, a.y + x.y, a.z + x.z, a.w + x.w);
+      b = make_float4(b.x + y.x, b.y + y.y, b.z + y.z, b.w + y.w);
     }
     if (j.fix.kind) {
       const int col = __ldg(j.fix.column + r);
@@ -240,11 +252,12 @@ __device__ __forceinline__ void join_slab(const JoinTiles& j, int tile, int slab
   }
 }
 
+template <bool REST>
 __global__ void __launch_bounds__(kRowThreads)
     join_tiles_kernel(const __grid_constant__ JoinTiles j, int first, int slabs) {
   pdl_wait();
   pdl_next();
-  for (int i = blockIdx.x; i < slabs; i += gridDim.x) join_slab(j, first + i / 32, i % 32);
+  for (int i = blockIdx.x; i < slabs; i += gridDim.x) join_slab<REST>(j, first + i / 32, i % 32);
 }
 
 cudaError_t launch_join_tiles(const JoinTiles& j, cudaStream_t s) {
@@ -252,7 +265,8 @@ cudaError_t launch_join_tiles(const JoinTiles& j, cudaStream_t s) {
   const int first = j.acc ? 0 : j.full, tiles = j.mt * j.nt;
   if (first >= tiles || (!j.acc && j.splits == 1)) return cudaSuccess;
   const int slabs = (tiles - first) * 32;
-  return launch_pdl(join_tiles_kernel, budget(slabs), kRowThreads, 0, s, j, first, slabs);
+  return launch_pdl(j.rest ? join_tiles_kernel<true> : join_tiles_kernel<false>, budget(slabs), kRowThreads, 0, s, j,
+                    first, slabs);
 }
 
 // Rows of up to 17 matrices to padded rows (16-byte units), one launch: a

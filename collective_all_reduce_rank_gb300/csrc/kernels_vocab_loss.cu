@@ -20,11 +20,10 @@
 // epilogues still hold float32: lo[t] W[target] to row t of dx, lo[t] x[t] to
 // row target of dW (dW of 333 x 515 x 50021 off by 0.0017 in the 2-norm
 // against 0.0023 without).  Up to 32 tokens dW sums so few entries that their
-// roundings do not average out either; both halves of them fit the block of 64
-// rows that dW's product takes anyhow, so what bfloat16 leaves of every entry
-// is stored as 32 rows more at most (a shard's dW of 1 or 4 tokens x 346 off by
-// 0.0017 against 0.0023-0.0025 without; both gradients 31.7 -> 33 us, of 4
-// tokens x 5120 x 32768 237 -> 240 us).
+// roundings do not average out either, and what bfloat16 leaves of every entry
+// is stored too, as 32 rows more at most: a second K segment of dW's product (a
+// shard's dW of 1 or 4 tokens x 346 off by 0.0017 against 0.0023-0.0025
+// without; of 1 / 4 tokens x 5120 x 32768 253 / 243 us).
 //
 // Bound by the tensor cores: the epilogue's exponentials (one per logit, 4 a
 // cycle and scheduler) run under the products of the next tile.  Measured:
@@ -177,26 +176,15 @@ struct EpiDlogits : TcNoState {
           for (int j = 0; j < 32; ++j) v[j] = 0.f;
         }
         tc_stage_bf16(buf, v, k / 8);
-        if (REST) {
-#pragma unroll
-          for (int j = 0; j < 32; j += 2) rest[k / 2 + j / 2] = tc_pack2(left(v[j]), left(v[j + 1]));
-        }
+        if (REST) tc_left2(v, rest + k / 2);
       }
       tc_flush_bf16(buf, out + c, g.ld, g.M - row0, valid, true, true);
       if (REST) {
-        const int r = threadIdx.x & 31;
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          *reinterpret_cast<uint4*>(buf + r * 128 + ((k ^ (r & 7)) << 4)) =
-              make_uint4(rest[4 * k], rest[4 * k + 1], rest[4 * k + 2], rest[4 * k + 3]);
+        tc_stage_packed(buf, rest, 0);
+        tc_stage_packed(buf, rest + 16, 4);
         tc_flush_bf16(buf, out + c + p.rest_row * g.ld, g.ld, g.M - row0, valid, true, true);
       }
     }
-  }
-
-  static __device__ __forceinline__ float left(float v) {
-    const float held = __bfloat162float(__float2bfloat16_rn(v));
-    return fabsf(held) < INFINITY ? v - held : 0.f;
   }
 };
 

@@ -95,26 +95,14 @@ struct Placer {
     if (!padded(cols)) return m;
     m.ld = pad_ld(cols);
     m.p = ws.take(rows * m.ld * 2);
-    copy(p, const_cast<void*>(m.p), rows, m);
-    return m;
-  }
-  // The rows laid out twice, one copy behind the other.
-  Mat twice(const void* p, size_t rows, size_t cols) {
-    Mat m{nullptr, 2 * rows, cols, padded(cols) ? pad_ld(cols) : cols};
-    char* to = static_cast<char*>(ws.take(m.rows * m.ld * 2));
-    m.p = to;
-    copy(p, to, rows, m);
-    copy(p, to + rows * m.ld * 2, rows, m);
-    return m;
-  }
-  void copy(const void* p, void* to, size_t rows, const Mat& m) {
-    if (rows == 0) return;
+    if (rows == 0) return m;
     a.src[a.n] = p;
-    a.dst[a.n] = to;
+    a.dst[a.n] = const_cast<void*>(m.p);
     a.cols = (long long)m.cols;
     a.units = (int)(m.ld / 8);
     a.first[a.n + 1] = a.first[a.n] + (long long)rows * a.units;
     ++a.n;
+    return m;
   }
   bool launch(cudaStream_t s) { return a.n == 0 || launch_pad_rows(a, s) == cudaSuccess; }
 };
@@ -185,6 +173,18 @@ void one_k_axis(TcArgs* p, size_t k) {
   p->kblocks = (int)((k + kTcKBlock - 1) / kTcKBlock);
   p->splits = 1;
   p->full = p->tiles;
+}
+
+// A K axis of T tokens, and with `rest` once more: B's rows again, against the
+// rows of A behind the first T (what bfloat16 leaves of those).  A block that
+// runs past T meets zeros of B.
+void token_axis(TcArgs* p, size_t T, bool rest) {
+  one_k_axis(p, T);
+  if (!rest) return;
+  p->rest_k = (int)T;
+  p->nsegs = 2;
+  p->seg_k0[1] = p->kblocks;
+  p->kblocks *= 2;
 }
 
 // More 256 x 256 tiles than the walk can count (`extra`: shards, each of
@@ -387,6 +387,11 @@ bool skinny(size_t T, size_t D, size_t logits) {
   return T <= 8 || (T <= 16 && (D % 8 != 0 || logits <= (size_t)1 << 27));
 }
 
+// Whether the gated backward keeps what bfloat16 leaves of dg and du, as rows
+// of their own behind the tokens': few entries' roundings do not average out
+// (kernels_gated_ffn.cu), and both halves fit the 256 rows of dx's tile.
+bool gate_rests(size_t T) { return T <= 128; }
+
 size_t ffn_bytes(int n, size_t T, size_t D, size_t F, bool back) {
   Bump b{nullptr};
   if (padded(D) && (back || !skinny(T, D, 0))) {
@@ -394,9 +399,12 @@ size_t ffn_bytes(int n, size_t T, size_t D, size_t F, bool back) {
     for (int i = 0; i < 2 * n; ++i) b.take(F * pad_ld(D) * 2);
   }
   if (back) {
-    for (int i = 0; i < 2 * n; ++i) b.take(T * up(F, 64) * 2);
+    const bool two = gate_rests(T);
+    const size_t rows = two ? 2 * T : T;
+    for (int i = 0; i < 2 * n; ++i) b.take(rows * up(F, 64) * 2);
     const size_t kb = 2 * (size_t)n * ((F + 63) / 64);
-    b.take(pick_split(T, D, kb).slot_bytes);
+    b.take(pick_split(rows, D, kb).slot_bytes);
+    if (two) b.take(rows * slot_ld(D) * 4);
   }
   return b.at;
 }
@@ -539,11 +547,13 @@ rra_status_t rra_gated_ffn_backward(const void* x, const void* const* gates, con
   const Mat X = place(x, T, D);
   Mat W[2 * kMaxRanks], dW[2 * kMaxRanks];
   for (int i = 0; i < 2 * nranks; ++i) W[i] = place(i % 2 ? ups[i / 2] : gates[i / 2], F, D);
-  const size_t ldf = up(F, 64);
-  for (int i = 0; i < 2 * nranks; ++i) dW[i] = Mat{ws.take(T * ldf * 2), T, F, ldf};
+  const bool two = gate_rests(T);
+  const size_t ldf = up(F, 64), rows = two ? 2 * T : T;
+  for (int i = 0; i < 2 * nranks; ++i) dW[i] = Mat{ws.take(rows * ldf * 2), rows, F, ldf};
   const size_t kb_seg = (F + 63) / 64, kb = 2 * (size_t)nranks * kb_seg;
-  const Split sp = pick_split(T, D, kb);
+  const Split sp = pick_split(rows, D, kb);
   float* slots = static_cast<float*>(ws.take(sp.slot_bytes));
+  float* acc = two ? static_cast<float*>(ws.take(rows * slot_ld(D) * 4)) : nullptr;
   if (!place.launch(s)) return done(call, nranks, count, dtype, 0, RRA_ERR_CUDA);
 
   // dg, du
@@ -570,12 +580,14 @@ rra_status_t rra_gated_ffn_backward(const void* x, const void* const* gates, con
   one_k_axis(p, D);
   p->pair_b = 1;
   p->act = act;
+  p->rest_row = two ? (int)T : 0;
   p->status = device_status();
   int grid = 0;
   cudaError_t e = launch_tc_gate_back(*p, s, &grid);
   if (e != cudaSuccess) return done(call, nranks, count, dtype, grid, RRA_ERR_CUDA);
 
-  // dx: the shards' products as segments of one K axis
+  // dx: the shards' products as segments of one K axis; second halves are
+  // rows of the same tile, added by the join
   clear(p);
   p->nsegs = 2 * nranks;
   for (int i = 0; i < 2 * nranks && ok; ++i) {
@@ -587,17 +599,18 @@ rra_status_t rra_gated_ffn_backward(const void* x, const void* const* gates, con
   p->splits = sp.splits;
   p->slots = slots;
   TcGroup g{};
-  g.M = (int)T;
+  g.M = (int)rows;
   g.N = (int)D;
-  g.ld = (long long)D;
-  g.out = dx;
-  g.vec = aligned(dx, 16) && D % 8 == 0;
+  g.ld = (long long)(two ? slot_ld(D) : D);
+  g.out = two ? (void*)acc : dx;
+  g.vec = two || (aligned(dx, 16) && D % 8 == 0);
   ok = ok && add_group(p, g, false);
   p->status = device_status();
   if (!ok) return done(call, nranks, count, dtype, 0, RRA_ERR_CUDA);
-  e = launch_tc_input_grad(*p, false, s, &grid);
+  e = launch_tc_input_grad(*p, two, s, &grid);
   if (e == cudaSuccess)
-    e = launch_join_tiles({nullptr, slots, dx, 0, (int)T, (int)D, p->group[0].mt, p->group[0].nt, sp.full, sp.splits, TcFix{}}, s);
+    e = launch_join_tiles({acc, slots, dx, (int)slot_ld(D), (int)T, (int)D, p->group[0].mt, p->group[0].nt, sp.full,
+                           sp.splits, TcFix{}, two ? (int)T : 0}, s);
   if (e != cudaSuccess) return done(call, nranks, count, dtype, grid, RRA_ERR_CUDA);
 
   // dG, dU
@@ -616,7 +629,7 @@ rra_status_t rra_gated_ffn_backward(const void* x, const void* const* gates, con
     ok = ok && add_group(p, h, false);
   }
   if (!ok) return done(call, nranks, count, dtype, 0, RRA_ERR_CUDA);
-  one_k_axis(p, T);
+  token_axis(p, T, two);
   p->status = device_status();
   e = launch_tc_weight_grad(*p, s, &grid);
   return done(call, nranks, count, dtype, grid, cuda_st(e));
@@ -647,8 +660,8 @@ struct LossPlan {
 };
 
 // Whether dl keeps what bfloat16 leaves of its entries, as rows of their own
-// behind the tokens': while both fit the one block of 64 rows that the product
-// of the weights' gradient takes at the least, with x's rows laid out twice.
+// behind the tokens': a second block of 64 rows for the product of the
+// weights' gradient, which takes one at the least.
 bool rests(size_t T) { return T <= 32; }
 
 // Blocks of 32 rows of the first n shards.
@@ -698,7 +711,6 @@ LossPlan loss_plan(int n, size_t T, size_t D, const size_t* vocab, bool back, si
   }
   q.rows = rests(T) ? 2 * T : T;
   const size_t col = q.rows * 512;  // bytes of a tile column of dl
-  if (rests(T)) b.take(q.rows * (padded(D) ? pad_ld(D) : D) * 2);
   const size_t base = b.at;
   // the parts of dx's K axis depend on the piece, which depends on the room
   // their slots leave: take the largest piece that fits with its own slots
@@ -875,7 +887,6 @@ rra_status_t rra_vocab_loss_backward(const void* x, const void* const* weights, 
   const Mat X = place(x, T, D);
   Mat W[kMaxRanks];
   for (int r = 0; r < nranks; ++r) W[r] = place(weights[r], vocab[r], D);
-  const Mat XX = rests(T) ? place.twice(x, T, D) : X;
   float4* rows = static_cast<float4*>(ws.take(T * sizeof(float4)));
   TcFix fix{};
   int* column = static_cast<int*>(ws.take(T * 4));
@@ -993,7 +1004,7 @@ rra_status_t rra_vocab_loss_backward(const void* x, const void* const* weights, 
     p->fix.kind = 2;
     p->fix.w[0] = X.p;
     p->fix.ld = (long long)X.ld;
-    ok = map_mn(&p->b[0], XX);
+    ok = map_mn(&p->b[0], X);
     for (int r = 0; r < nranks && ok; ++r) {
       if (hi[r] <= lo[r]) continue;
       const Mat A{dl + at[r] * 2, q.rows, hi[r] - lo[r], ld};
@@ -1010,7 +1021,7 @@ rra_status_t rra_vocab_loss_backward(const void* x, const void* const* weights, 
       ok = ok && add_group(p, h, false);
     }
     if (!ok) return done(call, nranks, T * V, dtype, 0, RRA_ERR_CUDA);
-    one_k_axis(p, q.rows);
+    token_axis(p, T, rests(T));
     p->status = device_status();
     e = launch_tc_weight_grad(*p, s, &grid);
   }

@@ -12,6 +12,12 @@ __device__ __forceinline__ uint32_t tc_pack2(float a, float b) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
+// What bfloat16 leaves of v (nothing of what it makes infinite).
+__device__ __forceinline__ float tc_left(float v) {
+  const float held = __bfloat162float(__float2bfloat16_rn(v));
+  return fabsf(held) < INFINITY ? v - held : 0.f;
+}
+
 // Stores go through a warp's staging buffer: a lane holds 128 bytes of one
 // row (64 bfloat16 or 32 float32), which it writes as 16-byte chunks in a
 // swizzled order (chunk c of row r at c ^ (r & 7): no bank conflicts either
@@ -26,6 +32,20 @@ __device__ __forceinline__ void tc_stage_bf16(uint8_t* buf, const float* v, int 
     *reinterpret_cast<uint4*>(buf + r * 128 + (((first_chunk + c) ^ (r & 7)) << 4)) =
         make_uint4(tc_pack2(v[8 * c], v[8 * c + 1]), tc_pack2(v[8 * c + 2], v[8 * c + 3]),
                    tc_pack2(v[8 * c + 4], v[8 * c + 5]), tc_pack2(v[8 * c + 6], v[8 * c + 7]));
+}
+
+// What bfloat16 leaves of 32 values, packed, and such pairs as chunks of a row.
+__device__ __forceinline__ void tc_left2(const float* v, uint32_t* w) {
+#pragma unroll
+  for (int j = 0; j < 32; j += 2) w[j / 2] = tc_pack2(tc_left(v[j]), tc_left(v[j + 1]));
+}
+
+__device__ __forceinline__ void tc_stage_packed(uint8_t* buf, const uint32_t* w, int first_chunk) {
+  const int r = threadIdx.x & 31;
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    *reinterpret_cast<uint4*>(buf + r * 128 + (((first_chunk + c) ^ (r & 7)) << 4)) =
+        make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
 }
 
 // Store `rows` rows (clipped to [0, 32]) of `valid` bfloat16 (clipped to [0,

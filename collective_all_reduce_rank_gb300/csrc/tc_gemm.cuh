@@ -370,9 +370,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
           while (seg + 1 < p.nsegs && k >= p.seg_k0[seg + 1]) ++seg;
           const int from = p.seg_k0[seg];
           const int to = seg + 1 < p.nsegs ? min(x.k1, p.seg_k0[seg + 1]) : x.k1;
-          const CUtensorMap* map = is_a ? &p.a[p.nsegs > 1 ? seg : g.a]
-                                        : &p.b[p.nsegs > 1 ? seg : (p.pair_b ? g.b + (int)rank : g.b)];
-          for (int kk = (k - from) * kTcBK; k < to; ++k, kk += kTcBK, ++issued) {
+          const bool own = p.nsegs > 1 && !p.rest_k;  // each segment has its maps
+          const CUtensorMap* map = is_a ? &p.a[own ? seg : g.a] : &p.b[own ? seg : (p.pair_b ? g.b + (int)rank : g.b)];
+          for (int kk = (k - from) * kTcBK + (is_a && seg ? p.rest_k : 0); k < to; ++k, kk += kTcBK, ++issued) {
             if (!tc_wait(empty0 + 8 * s, parity, &sh, p.status, 1)) {
               ok = false;
               break;

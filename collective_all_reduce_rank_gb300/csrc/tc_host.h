@@ -76,6 +76,7 @@ struct TcArgs {
   int full;     // the first `full` tiles of the walk take the whole K axis,
   int splits;   // the others one of `splits` parts of it at a time (tc_units)
   int kblocks;  // K blocks of 64 over all segments
+  int rest_k;   // two segments of the same maps, A's second one from row rest_k on (0: not so)
   TcShape shape;
   int pair_b;   // CTA c of a pair takes map b + c (gate and up weights), 128 columns per tile each
   // epilogue operands
@@ -85,7 +86,7 @@ struct TcArgs {
   const long long* targets;
   long long ignore_index;
   const float4* rows;  // dl: what loss_rows_kernel left per row
-  int rest_row;        // dl: rows from here on take what bfloat16 leaves of the others (0: not kept)
+  int rest_row;        // dl, dg and du: rows from here on take what bfloat16 leaves of the others (0: not kept)
   TcFix fix;
   float2* part;      // [column part][part_ld] running maximum and sum
   long long part_ld;
@@ -150,13 +151,15 @@ cudaError_t launch_loss_join(const float2* part, int parts, const float* hit, co
                              size_t hidden, int rows, float* loss, float* lse, cudaStream_t s);
 // dx from what the products of its one group of tiles left: tiles that took
 // the whole K axis are in `acc` (float32 rows of ld; null: already in out),
-// the others the sum of their parts in `slots`.
+// the others the sum of their parts in `slots`.  rest: rows that far down are
+// added to the first ones (the second halves of A's entries, in the same tile).
 struct JoinTiles {
   const float* acc;
   const float* slots;
   void* out;
   int ld, rows, cols, mt, nt, full, splits;
   TcFix fix;  // kind 1 or none
+  int rest = 0;
 };
 cudaError_t launch_join_tiles(const JoinTiles& j, cudaStream_t s);
 // Units of work of a launch: whole tiles, then parts of the others.

@@ -405,7 +405,8 @@ rra_status_t rra_gated_ffn(const void* x, const void* const* gates, const void* 
  *  all-reduces), dgates[r] and dups[r] width x hidden out.  The projections
  *  are computed again from x, not read; dg = dacts * u * act'(g) and
  *  du = dacts * act(g) are rounded to bfloat16 as operands of the gradient
- *  products, whose sums are float32.  tokens == 0 writes zeros to dgates
+ *  products (up to 128 tokens in two halves, with the rounding's rest as the
+ *  second), whose sums are float32.  tokens == 0 writes zeros to dgates
  *  and dups; width == 0 zeros to dx.  Errors as rra_gated_ffn. */
 rra_status_t rra_gated_ffn_backward(const void* x, const void* const* gates, const void* const* ups,
                                     const void* const* dacts, void* dx, void* const* dgates, void* const* dups,
