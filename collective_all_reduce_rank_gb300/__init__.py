@@ -277,17 +277,19 @@ def rra_allreduce_rmsnorm(bufs, outs, gamma, hidden, eps=1e-6, rows=None, dtype=
 _PTRS = [struct.Struct("%dP" % n).pack for n in range(RRA_MAX_RANKS + 1)]
 _SIZES = [struct.Struct("%dN" % n).pack for n in range(RRA_MAX_RANKS + 1)]
 _torch_mod = None
+_several = True  # more than one GPU is visible
 
 
 def _t():
     """torch, and its tensor methods unbound (a call of one is cheaper than of
     a bound one)."""
-    global _torch_mod, _data, _numel, _device, _dense
+    global _torch_mod, _data, _numel, _device, _dense, _several
     if _torch_mod is None:
         import torch
 
         t = torch.Tensor
         _data, _numel, _device, _dense = t.data_ptr, t.numel, t.get_device, t.is_contiguous
+        _several = torch.cuda.device_count() > 1
         _torch_mod = torch
     return _torch_mod
 
@@ -348,9 +350,8 @@ def _on(stream, device):
     if device < 0:  # no GPU's: refused by the call itself
         return 0 if stream is None else stream if isinstance(stream, int) else int(stream.cuda_stream)
     cuda = _t()._C
-    current = cuda._cuda_getDevice()
-    if current != device:
-        raise ValueError("the tensors are on cuda:%d, the current device is cuda:%d" % (device, current))
+    if _several and cuda._cuda_getDevice() != device:
+        raise ValueError("the tensors are on cuda:%d, the current device is cuda:%d" % (device, cuda._cuda_getDevice()))
     if stream is None:
         return cuda._cuda_getCurrentRawStream(device)
     if isinstance(stream, int):

@@ -735,8 +735,10 @@ cudaError_t launch_norm_save8(int n, int dt, bool vec, const void* const* in, vo
 template <int DT, bool VEC>
 static cudaError_t restore_go(const uint8_t* c, const uint8_t* e, const float* rstd, const void* gamma, void* out,
                               size_t rows, size_t hidden, int grid, cudaStream_t s) {
-  const cudaError_t attr = raise_smem<restore8_kernel<DT, VEC>>(kN8SmemMax);
-  if (attr != cudaSuccess) return attr;
+  if constexpr (!VEC) {
+    const cudaError_t attr = raise_smem<restore8_kernel<DT, VEC>>(kN8SmemMax);
+    if (attr != cudaSuccess) return attr;
+  }
   return launch_pdl(restore8_kernel<DT, VEC>, grid, kN8Threads, VEC ? 0 : row_smem(hidden), s, c, e, rstd, gamma, out,
                     rows, hidden);
 }

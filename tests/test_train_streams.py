@@ -115,6 +115,7 @@ def test_a_call_on_another_stream_makes_its_workspace_there(call):
 @pytest.mark.parametrize("stream", [None, 0, SimpleNamespace(cuda_stream=OTHER, device_index=1)])
 def test_tensors_of_a_device_that_is_not_current_are_refused(monkeypatch, stream):
     """The library launches on the current device."""
+    monkeypatch.setattr(rra, "_several", True)
     monkeypatch.setattr(rra, "_t", lambda: Fake())  # device 0 is current
     with pytest.raises(ValueError, match="current device"):
         rra._on(stream, 1)
