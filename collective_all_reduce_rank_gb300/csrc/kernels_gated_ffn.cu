@@ -21,8 +21,9 @@
 // tokens x 5120 x 8 x 1728 219 / 224 / 233 / 243 us (213 / 217 / 223 / 230
 // without), 32 x 1027 x 3 x 643 44 (41), 128 x 512 x 4 x 512 32 (28).
 //
-// Bound by the tensor cores from about 300 tokens (512 x 5120 x 8 x 1728: 84
-// us, 1.73 PFLOP/s; 224 tiles on 76 clusters are 2.95 waves), by the
+// Bound by the tensor cores from about 300 tokens (512 x 5120 x 8 x 1728: 97-
+// 100 us call after call, 1.45-1.50 PFLOP/s, and 85 us in a graph from a cool
+// start; 224 tiles on 76 clusters are 2.95 waves), by the
 // weights' bytes below (17-256 tokens: 56-61 us, 5.0-4.6 TB/s: 112 tiles are
 // 1.5 waves and each tile's products take as long as its bytes); up to 16
 // tokens go through kernels_skinny.cu.  Tiles of 64 + 64 columns fill the

@@ -28,7 +28,7 @@
 // Measured (one GB300, 5120 columns of bfloat16, 8 ranks): forward of 4096
 // rows 102 us, 6.2 TB/s of DRAM traffic; backward of 4096 rows 113 us with
 // the join of dgamma, 6.1 TB/s of its floor; 1283 x 1027 float32 x 3 ranks
-// backward 16 us, 2.0 TB/s (latency: 3 rows a CTA, each a load, a barrier
+// backward 19 us, 1.8 TB/s (latency: 3 rows a CTA, each a load, a barrier
 // and a store).
 //
 // The sum of squares is added in the order of the kernel that saves nothing

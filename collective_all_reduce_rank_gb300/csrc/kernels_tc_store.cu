@@ -6,11 +6,12 @@
 // one K axis, so the sum over ranks that a tensor-parallel step leaves to an
 // all-reduce is the accumulation in tensor memory, in float32.
 //
-// Measured (4096 tokens x 5120, 4 shards of 3456; one GB300): dx 0.59 ms, dW
-// 0.61 ms for 1.16 TFLOP each, 1.97 and 1.92 PFLOP/s.  A weight gradient of
-// few tokens is bound by writing it: rows of 16-byte units take full-line
-// stores (333 tokens x 512 x 50021: 26 us), rows of any alignment 4-byte
-// stores of a shifted row (x 515: 40 us).
+// Measured (4096 tokens x 5120, 4 shards of 3456; one GB300, a launch alone):
+// dx 0.59 ms, dW 0.61 ms for 1.16 TFLOP each, 1.97 and 1.92 PFLOP/s; call after
+// call the power limit makes them 15% longer.  A weight gradient of few tokens
+// is bound by writing it: rows of 16-byte units take full-line stores (333
+// tokens x 512 x 50021: 26 us), rows of any alignment 4-byte stores of a shifted
+// row (x 515: 40 us, 50 with the targets' additions).
 #include "tc_epilogue.cuh"
 
 namespace rra {

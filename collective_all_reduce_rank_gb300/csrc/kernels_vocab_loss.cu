@@ -26,10 +26,12 @@
 // without; of 1 / 4 tokens x 5120 x 32768 253 / 243 us).
 //
 // Bound by the tensor cores: the epilogue's exponentials (one per logit, 4 a
-// cycle and scheduler) run under the products of the next tile.  Measured:
-// forward 2048 x 5120 x 131072 1.36 ms (2.02 PFLOP/s, tensor pipe 96%
-// active); forward and backward of 8192 x 5120 x 131072 25.1 ms (1.75
-// PFLOP/s under the power limit, where a library product sustains 1.70).
+// cycle and scheduler) run under the products of the next tile, and show for
+// short rows only (2048 x 131072 of hidden 128 131 us).  Measured: forward 2048
+// x 5120 x 131072 1.56-1.61 ms call after call (1.71-1.76 PFLOP/s, tensor pipe
+// 96% active; 1.36 ms from a cool start); forward and backward of 8192 x 5120 x
+// 131072 25.5-26.7 ms (1.65-1.72 PFLOP/s under the power limit, where a library
+// product sustains 1.70).
 #include "tc_epilogue.cuh"
 
 namespace rra {

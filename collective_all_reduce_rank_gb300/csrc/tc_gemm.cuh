@@ -8,9 +8,12 @@
 // KB from L2 to its two SMs, 64 bytes a cycle each, which is about what L2
 // gives: both sides are near their limits, and everything else has to stay
 // out of the way.  Measured on one GB300 (ncu): tensor pipe 91-96% active in
-// all five products of a 2048-token step (hidden 5120); 4096 x 5120 x 4 x
-// 3456 gated backward 1.77 ms, 1.97 PFLOP/s; 2048 x 5120 x 131072 loss 1.36
-// ms, 2.02 PFLOP/s (library bfloat16 product of 8192^3: 1.87).
+// all five products of a 2048-token step (hidden 5120).  The clock under the
+// power limit then sets the rate: 4096 x 5120 x 4 x 3456 gated backward 2.06-
+// 2.13 ms call after call (1.64-1.69 PFLOP/s; 1.78 ms and 1.96 in a few calls
+// from a cool start), 2048 x 5120 x 131072 loss 1.56-1.61 ms (1.71-1.76; 1.36
+// and 2.02), beside a library bfloat16 product of 8192^3 at 1.70 sustained and
+// 1.87 in a burst.
 //
 // Shape.  A cluster of two CTAs works on a 256 x 256 tile of C with
 // tcgen05.mma.cta_group::2: CTA c of the pair holds rows [128c, 128c+128)

@@ -447,7 +447,8 @@ rra_status_t rra_vocab_loss(const void* x, const void* const* weights, const siz
  *  the target's entry, whose rest is added to both results in float32 (up to
  *  32 tokens the products of dweights take the rest of every entry, as
  *  bfloat16); the products' sums are float32.  A row whose target is ignore_index or outside
- *  the vocabulary has a zero gradient, whatever grad_loss holds there.
+ *  the vocabulary has a zero gradient, whatever grad_loss holds there (its x
+ *  still enters dweights, times zero, and has to be finite).
  *  tokens == 0 writes zeros to dweights.  Errors as rra_vocab_loss. */
 rra_status_t rra_vocab_loss_backward(const void* x, const void* const* weights, const size_t* vocab,
                                      const int64_t* targets, const float* lse, const float* grad_loss, void* dx,
