@@ -17,7 +17,7 @@
 // up to 2.1 times (one to 18 tokens).  Up to 128 tokens what bfloat16 leaves of
 // each entry is stored too, as rows behind the tokens': more rows of the same
 // tile for dx, added in the join, and a second K segment for dG and dU.  Both
-// are then off by their own rounding alone, for 1 to 5 us: 1 / 32 / 64 / 128
+// are then off by their own rounding alone, for 1 to 13 us: 1 / 32 / 64 / 128
 // tokens x 5120 x 8 x 1728 219 / 224 / 233 / 243 us (213 / 217 / 223 / 230
 // without), 32 x 1027 x 3 x 643 44 (41), 128 x 512 x 4 x 512 32 (28).
 //
