@@ -111,6 +111,14 @@ def _declare(lib):
         "rra_vocab_loss_workspace_bytes": (sz, [i, sz, sz, vp, i]),
         "rra_vocab_loss": (i, [vp, vp, vp, vp, i, sz, sz, i64, vp, vp, i, vp, sz, vp]),
         "rra_vocab_loss_backward": (i, [vp, vp, vp, vp, vp, vp, vp, vp, i, sz, sz, i64, i, vp, sz, vp]),
+        "rra_mx4_scale_bytes": (sz, [sz, sz]),
+        "rra_mx4_quantize": (i, [vp, vp, sz, sz, i, vp]),
+        "rra_mx4_restore": (i, [vp, vp, sz, sz, i, vp]),
+        "rra_allreduce_rmsnorm_mx4": (i, [vp, i, sz, sz, vp, ctypes.c_float, vp, vp, vp, i, vp]),
+        "rra_mx4_product": (i, [vp, vp, vp, i, sz, sz, vp, i, vp]),
+        "rra_mx4_product_sum": (i, [vp, vp, vp, i, sz, sz, sz, i, vp]),
+        "rra_mx4_gated_ffn": (i, [vp, vp, vp, vp, i, sz, sz, sz, i, vp]),
+        "rra_vocab_sample": (i, [vp, vp, i, sz, vp, vp, vp, vp, vp, vp, vp, i, vp]),
         "rra_ll_wire_bytes": (sz, [sz]),
         "rra_ll128_wire_bytes": (sz, [sz]),
         "rra_ll_pack": (i, [vp, sz, vp, u32, vp]),
@@ -558,6 +566,151 @@ def rra_vocab_loss_backward(x, weights, targets, lse, grad_loss, dx, dweights, i
         _one("lse", lse, torch.float32, (T,), dev), _one("grad_loss", grad_loss, torch.float32, (T,), dev),
         _one("dx", dx, dt, (T, D), dev), dp, n, T, D, ignore_index, _dtype_of(x), ws, nb, _on(stream, dev))
     return _ret(st, "rra_vocab_loss_backward", check)
+
+
+# -- the serving step around a tensor-parallel all-reduce ---------------------
+#
+# An MX4 matrix is a pair (codes, scales) of uint8 tensors: codes of shape
+# [rows, 16 * ceil(cols / 32)], scales of rra_mx4_scale_bytes(rows, cols)
+# bytes.
+
+_PAIRS = [struct.Struct("%dP" % (2 * n)).pack for n in range(RRA_MAX_RANKS + 1)]
+
+
+def _mx4(what, ms, rows, cols, device):
+    """The C array of MX4 matrices (codes, scales), rows x cols each."""
+    u8 = _t().uint8
+    shape, nbytes = (rows, 16 * ((cols + 31) // 32)), 512 * ((rows + 127) // 128) * ((cols + 127) // 128)
+    ps = []
+    for m in ms:
+        codes, scales = m
+        ps.append(_one(what, codes, u8, shape, device))
+        ps.append(_flat(what, scales, u8, nbytes, device))
+    return _PAIRS[len(ms)](*ps)
+
+
+def rra_mx4_scale_bytes(rows: int, cols: int) -> int:
+    return int(load().rra_mx4_scale_bytes(rows, cols))
+
+
+def rra_mx4_quantize(x, codes, scales, stream=None, check=True) -> int:
+    """(codes, scales) = x [rows, cols] in MX4."""
+    _t()
+    rows, cols = x.shape
+    dev = x.get_device()
+    st = load().rra_mx4_quantize(_one("x", x, x.dtype, x.shape, dev),
+                                 _mx4("codes or scales", ((codes, scales),), rows, cols, dev), rows, cols,
+                                 _norm_dtype(x), _on(stream, dev))
+    return _ret(st, "rra_mx4_quantize", check)
+
+
+def rra_mx4_restore(codes, scales, out, stream=None, check=True) -> int:
+    """out [rows, cols] = the values of an MX4 matrix."""
+    _t()
+    rows, cols = out.shape
+    dev = out.get_device()
+    st = load().rra_mx4_restore(_mx4("codes or scales", ((codes, scales),), rows, cols, dev),
+                                _one("out", out, out.dtype, out.shape, dev), rows, cols, _norm_dtype(out),
+                                _on(stream, dev))
+    return _ret(st, "rra_mx4_restore", check)
+
+
+def rra_allreduce_rmsnorm_mx4(bufs, gamma, hidden, codes, scales, residual=None, residual_out=None, eps=1e-6,
+                              stream=None, check=True) -> int:
+    """All-reduce + residual + RMSNorm with the result in MX4; residual_out
+    (it may be residual) gets the sum."""
+    n = len(bufs)
+    st = _same_count(n)
+    if st != RRA_SUCCESS:
+        return _ret(st, "rra_allreduce_rmsnorm_mx4", check)
+    _t()
+    x = bufs[0]
+    dev, dt, count = x.get_device(), x.dtype, x.numel()
+    rows = count // hidden if hidden else 0
+    if rows * hidden != count:
+        raise ValueError("a rank's buffer must hold whole rows of %d" % hidden)
+    st = load().rra_allreduce_rmsnorm_mx4(
+        _flat_ranks("a rank's buffer", bufs, dt, count, dev), n, rows, hidden, _one("gamma", gamma, dt, (hidden,), dev),
+        eps, None if residual is None else _flat("the residual", residual, dt, count, dev),
+        None if residual_out is None else _flat("the residual's sum", residual_out, dt, count, dev),
+        _mx4("codes or scales", ((codes, scales),), rows, hidden, dev), _norm_dtype(x), _on(stream, dev))
+    return _ret(st, "rra_allreduce_rmsnorm_mx4", check)
+
+
+def rra_mx4_product(x, weights, outs, hidden, stream=None, check=True) -> int:
+    """outs[r] [tokens, width_r] = X W_r^T; x and each of weights a pair
+    (codes, scales), tokens x hidden and width_r x hidden."""
+    n = len(weights)
+    st = _same_count(n, outs)
+    if st != RRA_SUCCESS:
+        return _ret(st, "rra_mx4_product", check)
+    _t()
+    o = outs[0]
+    T, dev, dt = o.shape[0], o.get_device(), o.dtype
+    widths = [t.shape[1] for t in outs]
+    ws = b"".join([_mx4("a weight shard", (w,), v, hidden, dev) for w, v in zip(weights, widths)])
+    os_ = _PTRS[n](*[_one("a rank's output", t, dt, (T, v), dev) for t, v in zip(outs, widths)])
+    st = load().rra_mx4_product(_mx4("x", (x,), T, hidden, dev), ws, os_, n, T, hidden, _sizes(widths), _norm_dtype(o),
+                                _on(stream, dev))
+    return _ret(st, "rra_mx4_product", check)
+
+
+def rra_mx4_product_sum(xs, weights, out, width, stream=None, check=True) -> int:
+    """out [tokens, hidden] = the sum over ranks of X_r W_r^T; xs[r] tokens x
+    width and weights[r] hidden x width, pairs (codes, scales)."""
+    n = len(weights)
+    st = _same_count(n, xs)
+    if st != RRA_SUCCESS:
+        return _ret(st, "rra_mx4_product_sum", check)
+    _t()
+    T, D = out.shape
+    dev = out.get_device()
+    st = load().rra_mx4_product_sum(_mx4("a rank's x", xs, T, width, dev), _mx4("a weight shard", weights, D, width, dev),
+                                    _one("out", out, out.dtype, (T, D), dev), n, T, width, D, _norm_dtype(out),
+                                    _on(stream, dev))
+    return _ret(st, "rra_mx4_product_sum", check)
+
+
+def rra_mx4_gated_ffn(x, gates, ups, acts, hidden, width, act=RRA_ACT_SILU, stream=None, check=True) -> int:
+    """acts[r] = act(X G_r^T) * (X U_r^T) in MX4; every matrix a pair (codes,
+    scales), the number of tokens that of x's rows."""
+    n = len(gates)
+    st = _same_count(n, ups, acts)
+    if st != RRA_SUCCESS:
+        return _ret(st, "rra_mx4_gated_ffn", check)
+    _t()
+    T, dev = x[0].shape[0], x[0].get_device()
+    st = load().rra_mx4_gated_ffn(_mx4("x", (x,), T, hidden, dev), _mx4("a gate or up shard", gates, width, hidden, dev),
+                                  _mx4("a gate or up shard", ups, width, hidden, dev),
+                                  _mx4("a rank's activations", acts, T, width, dev), n, T, hidden, width, act,
+                                  _on(stream, dev))
+    return _ret(st, "rra_mx4_gated_ffn", check)
+
+
+def rra_vocab_sample(logits, uniform, token, temperature=None, top_k=None, top_p=None, min_p=None, logprob=None,
+                     stream=None, check=True) -> int:
+    """token[i] (int64) drawn from the row's logits over all shards by
+    uniform[i]; temperature, top_p, min_p float32 and top_k int32 per row."""
+    n = len(logits)
+    st = _same_count(n)
+    if st != RRA_SUCCESS:
+        return _ret(st, "rra_vocab_sample", check)
+    torch = _t()
+    x = logits[0]
+    rows, dev, dt = x.shape[0], x.get_device(), x.dtype
+    vocab = [t.shape[1] for t in logits]
+    lp = _PTRS[n](*[_one("a rank's logits", t, dt, (rows, v), dev) for t, v in zip(logits, vocab)])
+    f32, per = torch.float32, (rows,)
+
+    def opt(what, t, dtype):
+        return None if t is None else _one(what, t, dtype, per, dev)
+
+    st = load().rra_vocab_sample(lp, _sizes(vocab), n, rows, _one("uniform", uniform, f32, per, dev),
+                                 opt("temperature", temperature, f32), opt("top_k", top_k, torch.int32),
+                                 opt("top_p", top_p, f32), opt("min_p", min_p, f32),
+                                 _one("token", token, torch.int64, per, dev), opt("logprob", logprob, f32),
+                                 _norm_dtype(x), _on(stream, dev))
+    return _ret(st, "rra_vocab_sample", check)
 
 
 def rra_ll_wire_bytes(payload_bytes: int) -> int:

@@ -1,0 +1,316 @@
+// kernels_mx4_product.cu -- products of MX4 matrices for more than a few
+// tokens: C[t][n] = sum_k X[t][k] W[n][k], both operands as 4-bit codes with a
+// scale per 32 columns, multiplied exactly and summed in float32 by the block-
+// scaled tensor-core product; column-parallel (a group per rank's shard),
+// row-parallel (the ranks' K axes as segments of one: the all-reduce is the
+// accumulation), or gated (act(x G^T) * (x U^T) written in MX4 again).
+//
+// Shape.  A cluster of two CTAs works on a tile of 256 tokens x 256 weight rows
+// with tcgen05.mma.cta_group::2, CTA c holding tokens [128c, 128c + 128) of it
+// in its tensor memory.  A stage is 256 columns of K: 128 bytes of codes a row
+// (one swizzled row), and two scale tiles per 128 rows, which tcgen05.cp takes
+// from shared to tensor memory ahead of the stage's four products.
+//
+// Tensor memory.  Two accumulators of 256 columns and 24 columns of scales do
+// not fit in 512.  The second accumulator starts at column 224, so the two
+// share 32 columns: the epilogue reads those of a tile first and then lets the
+// next tile's products begin, under the rest of its own work.
+//
+// Roles (12 warps) as in tc_gemm.cuh: warps 0 and 3 load X and W, warp 1 of
+// the first CTA issues, warp 2 owns the tensor memory, warps 4-11 are the
+// epilogue.
+#include "act.cuh"
+#include "mx4_mma.cuh"
+
+namespace rra {
+
+namespace {
+
+constexpr int kCodes = 128 * 128;  // codes of 128 rows
+constexpr int kScalesX = 1024;     // two tiles: a CTA's 128 tokens
+constexpr int kScalesW = 2048;     // four: all 256 weight rows
+constexpr int kStageBytes = 2 * kCodes + kScalesX + kScalesW;
+constexpr int kStages = 5;
+constexpr int kSmem = kStages * kStageBytes + kTcEpiWarps * kTcStoreBytes + 1024;
+constexpr uint32_t kSecond = 224;  // first column of the second accumulator
+constexpr uint32_t kColX = 480, kColW = 488;
+static_assert(kStageBytes % 1024 == 0, "a swizzled tile starts on 1024 bytes");
+static_assert(kStages <= kTcMaxStages, "barriers");
+
+struct Unit {
+  int group, m, n;
+};
+
+__device__ __forceinline__ Unit unit_of(const Mx4Args& p, int t) {
+  Unit u;
+  int g = 0;
+  while (g + 1 < p.ngroups && t >= p.group[g + 1].tile0 * p.mt) ++g;
+  u.group = g;
+  tc_walk(t - p.group[g].tile0 * p.mt, p.mt, p.group[g].tiles, u.m, u.n);
+  return u;
+}
+
+// An epilogue warp's share of a tile: 32 tokens from row0 on, the 128 columns
+// of `half` in two pairs of 32 (gated: two blocks of 32).  `first`: which of
+// the two comes first; drained() is called once its columns have been read.
+template <class Drained>
+__device__ __forceinline__ void store_tile(const Mx4Args& p, const Unit& u, int row0, int half, uint32_t addr,
+                                           uint8_t* buf, int first, Drained drained) {
+  const Mx4Group& g = p.group[u.group];
+  const int rows = p.tokens - row0;
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i) {
+    const int c = half * 128 + (i ^ first) * 64;  // column of the tile
+    const int c0 = u.n * 256 + c;
+    const int valid = g.rows - c0;
+    float a[32], b[32];
+    tc_ld32(addr + c, a);
+    tc_ld32(addr + c + 32, b);
+    tc_ld_ready(a);
+    tc_ld_ready(b);
+    if (i == 0) drained();
+    if (valid <= 0 || rows <= 0) continue;
+    if (p.f32) {
+      float* o = static_cast<float*>(g.out) + (long long)row0 * g.ld + c0;
+      tc_store_f32(buf, a, o, g.ld, rows, valid, g.vec, false);
+      if (valid > 32) tc_store_f32(buf, b, o + 32, g.ld, rows, valid - 32, g.vec, false);
+    } else {
+      tc_stage_bf16(buf, a, 0);
+      tc_stage_bf16(buf, b, 4);
+      tc_flush_bf16(buf, static_cast<__nv_bfloat16*>(g.out) + (long long)row0 * g.ld + c0, g.ld, rows, valid, g.vec,
+                    false);
+    }
+  }
+}
+
+template <int ACT, class Drained>
+__device__ __forceinline__ void store_gated(const Mx4Args& p, const Unit& u, int row0, int half, uint32_t addr,
+                                            int first, Drained drained) {
+  const Mx4Group& g = p.group[u.group];
+  const int row = row0 + (threadIdx.x & 31);
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i) {
+    const int c = half * 64 + (i ^ first) * 32;
+    float a[32], b[32];
+    tc_ld32(addr + c, a);
+    tc_ld32(addr + 128 + c, b);
+    tc_ld_ready(a);
+    tc_ld_ready(b);
+    if (i == 0) drained();
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      float unused;
+      a[j] = a[j] * gate_sigma<ACT>(a[j], &unused) * b[j];
+    }
+    const int c0 = u.n * 128 + c;
+    if (row < p.tokens)
+      mx4_put_row(a, g.rows - c0, static_cast<uint8_t*>(g.out) + (long long)row * g.ld + c0 / 2,
+                  g.out_scales + mx_scale_at((size_t)row, (size_t)(c0 / 32), (size_t)g.across));
+  }
+}
+
+// ACT < 0: a plain product.
+template <int ACT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
+    mx4_product_kernel(const __grid_constant__ Mx4Args p) {
+  constexpr bool GATED = ACT >= 0;
+  extern __shared__ uint8_t raw[];
+  __shared__ TcShared sh;
+  const uint32_t ring = (tc_smem(raw) + 1023u) & ~1023u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = tc_cta_rank();
+  const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
+  const int total = p.tiles * p.mt;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      tc_bar_init(tc_smem(&sh.full[s]), 1);
+      tc_bar_init(tc_smem(&sh.empty[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      tc_bar_init(tc_smem(&sh.acc_full[b]), 1);
+      tc_bar_init(tc_smem(&sh.acc_empty[b]), 2 * kTcEpiWarps);
+    }
+    sh.give_up = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 2) {
+    __syncwarp();
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc_smem(&sh.tmem)), "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  pdl_wait();
+  pdl_next();
+
+  // a stage: codes of W's half, of X's half, scales of X's half, of all of W
+  uint32_t issued = 0;
+  if (warp == 0 || warp == 3) {
+    const bool is_x = warp == 0;
+    if (lane == 0) {
+      const uint32_t full0 = tc_smem(&sh.full[0]), empty0 = tc_smem(&sh.empty[0]);
+      const uint32_t lead0 = tc_mapa(full0, 0);
+      int s = 0;
+      uint32_t parity = 1;
+      bool ok = true;
+      for (int t = cluster; t < total && ok; t += clusters) {
+        const Unit u = unit_of(p, t);
+        const int w0 = p.group[u.group].w;
+        const int x0 = u.m * 256 + (int)rank * 128;  // first token of this CTA
+        // first weight row of this CTA's half: half a tile, or the tile's rows of the gate or the up projection
+        const int n0 = GATED ? u.n * 128 : u.n * 256 + (int)rank * 128;
+        int seg = 0;
+        for (int k = 0; k < p.kblocks; ++k, ++issued) {
+          while (seg + 1 < p.nsegs && k >= p.seg_k0[seg + 1]) ++seg;
+          const int kk = k - p.seg_k0[seg];
+          const int w = (p.nsegs > 1 ? seg : w0);
+          if (!tc_wait(empty0 + 8 * s, parity, &sh, p.status, 1)) {
+            ok = false;
+            break;
+          }
+          if (is_x && rank == 0) tc_bar_expect(full0 + 8 * s, 2 * kStageBytes);
+          const uint32_t at = ring + s * kStageBytes, bar = lead0 + 8 * s;
+          if (is_x) {
+            tc_tma_load(&p.x[seg], at + kCodes, bar, kk * 128, x0);
+            tc_tma_load(&p.xs[seg], at + 2 * kCodes, bar, kk * 256, x0 / 128);
+          } else {
+            const uint32_t sw = at + 2 * kCodes + kScalesX;
+            tc_tma_load(&p.w[GATED ? w + (int)rank : w], at, bar, kk * 128, n0);
+            if (GATED) {
+              tc_tma_load(&p.ws[w], sw, bar, kk * 256, u.n);
+              tc_tma_load(&p.ws[w + 1], sw + 1024, bar, kk * 256, u.n);
+            } else {
+              tc_tma_load(&p.ws[w], sw, bar, kk * 256, u.n * 2);
+            }
+          }
+          if (++s == kStages) {
+            s = 0;
+            parity ^= 1;
+          }
+        }
+      }
+      // none of a pair leaves before the last stage releases have landed in it
+      for (int i = 0; i < kStages && ok && !is_x; ++i) {
+        ok = tc_wait(empty0 + 8 * s, parity, &sh, p.status, 5);
+        if (++s == kStages) {
+          s = 0;
+          parity ^= 1;
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (rank == 0 && lane == 0) {
+      uint32_t tile = 0, round = 0;
+      int s = 0;
+      bool ok = true;
+      for (int t = cluster; t < total && ok; t += clusters, ++tile) {
+        const uint32_t d = tmem + (tile & 1) * kSecond;
+        // the tile before has been read where this one's accumulator begins or ends
+        if (tile && !tc_wait(tc_smem(&sh.acc_empty[0]), (tile - 1) & 1, &sh, p.status, 2)) break;
+        tc_fence_after();
+        for (int k = 0; k < p.kblocks; ++k) {
+          if (!tc_wait(tc_smem(&sh.full[s]), round & 1, &sh, p.status, 3)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sw = ring + s * kStageBytes, sx = sw + kCodes, cx = sx + kCodes, cw = cx + kScalesX;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            mx4_put_scales<true>(tmem + kColX + 4 * j, cx + 512 * j);
+            mx4_put_scales<true>(tmem + kColW + 8 * j, cw + 512 * j);
+            mx4_put_scales<true>(tmem + kColW + 8 * j + 4, cw + 1024 + 512 * j);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            mx4_mma<true>(d, tc_desc<false>(sx + 32 * i), tc_desc<false>(sw + 32 * i), mx4_idesc(256, 256, 2 * (i & 1)),
+                          tmem + kColX + 4 * (i >> 1), tmem + kColW + 8 * (i >> 1), (uint32_t)(k > 0 || i > 0));
+          tc_commit(tc_smem(&sh.empty[s]));
+          if (++s == kStages) {
+            s = 0;
+            ++round;
+          }
+        }
+        if (ok) tc_commit(tc_smem(&sh.acc_full[tile & 1]));
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    const int quad = warp & 3, half = (warp - 4) >> 2;
+    uint8_t* buf = raw + (ring - tc_smem(raw)) + kStages * kStageBytes + (warp - 4) * kTcStoreBytes;
+    uint32_t tile = 0;
+    for (int t = cluster; t < total; t += clusters, ++tile) {
+      const uint32_t b = tile & 1;
+      if (!__all_sync(0xffffffffu, tc_wait(tc_smem(&sh.acc_full[b]), (tile >> 1) & 1, &sh, p.status, 4))) break;
+      tc_fence_after();
+      const Unit u = unit_of(p, t);
+      // the 32 shared columns are the first accumulator's last, the second's
+      // first; a warp that reads none of them has nothing left to read of the
+      // tile before and reports at once
+      const int owner = b ? 0 : 1;
+      const auto drained = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc_bar_arrive_remote(tc_smem(&sh.acc_empty[0]), 0);
+      };
+      const auto nothing = [] {};
+      const uint32_t addr = tmem + b * kSecond + ((uint32_t)(quad * 32) << 16);
+      const int row0 = u.m * 256 + (int)rank * 128 + quad * 32;
+      if (half != owner) {
+        drained();
+        if constexpr (GATED)
+          store_gated<ACT>(p, u, row0, half, addr, 0, nothing);
+        else
+          store_tile(p, u, row0, half, addr, buf, 0, nothing);
+      } else {
+        if constexpr (GATED)
+          store_gated<ACT>(p, u, row0, half, addr, b ? 0 : 1, drained);
+        else
+          store_tile(p, u, row0, half, addr, buf, b ? 0 : 1, drained);
+      }
+    }
+  }
+
+  // teardown
+  if ((warp == 0 || warp == 3) && lane == 0 && sh.give_up) {
+    // copies of this CTA may be in flight: wait, bounded, for what was issued
+    const uint32_t first = issued > (uint32_t)kStages ? issued - kStages : 0;
+    for (uint32_t i = first; i < issued; ++i)
+      for (int tries = 0; tries < 64 && !tc_bar_try(tc_smem(&sh.full[i % kStages]), (i / kStages) & 1); ++tries) {
+      }
+    __nanosleep(1000000);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_cluster_sync();
+  tc_fence_after();
+  if (warp == 2) {
+    __syncwarp();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+  }
+}
+
+template <int ACT>
+cudaError_t go(const Mx4Args& p, cudaStream_t s, int* grid_out) {
+  constexpr auto kern = mx4_product_kernel<ACT>;
+  const cudaError_t attr = raise_smem<kern>(kSmem);
+  if (attr != cudaSuccess) return attr;
+  const int grid = 2 * tc_clusters(p.tiles * p.mt);
+  if (grid_out) *grid_out = grid;
+  return launch_pdl(kern, grid, kTcThreads, kSmem, s, p);
+}
+
+}  // namespace
+
+cudaError_t launch_mx4_product(const Mx4Args& p, bool gated, cudaStream_t s, int* grid) {
+  if (!gated) return go<-1>(p, s, grid);
+  return p.act == RRA_ACT_SILU ? go<RRA_ACT_SILU>(p, s, grid) : go<RRA_ACT_GELU_TANH>(p, s, grid);
+}
+
+}  // namespace rra

@@ -10,8 +10,10 @@
 #include <cstring>
 #include <initializer_list>
 
+#include "abi_util.h"
 #include "rra.h"
 #include "rra_internal.h"
+#include "serve_host.h"
 #include "tc_host.h"
 
 using namespace rra;
@@ -19,48 +21,8 @@ using namespace rra;
 namespace {
 
 constexpr size_t kPieceBytes = 512ull << 20;  // default room for a piece's dl
-constexpr size_t kAlign = 256;
 
-size_t up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 size_t tiles256(size_t x) { return (x + 255) / 256; }
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
-
-struct Range {
-  const void* p;
-  size_t bytes;
-};
-
-bool meet(const Range& a, const Range& b) {
-  const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
-  return a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
-}
-
-// A call's address ranges (no allocation, so nothing here can throw).
-struct Ranges {
-  Range r[5 + 3 * kMaxRanks];
-  size_t n = 0;
-  Ranges() = default;
-  Ranges(std::initializer_list<Range> l) {
-    for (const Range& x : l) push_back(x);
-  }
-  void push_back(const Range& x) { r[n++] = x; }
-  size_t size() const { return n; }
-  const Range& operator[](size_t i) const { return r[i]; }
-};
-
-// An output meets an input or another output; of the first `inplace` pairs,
-// output i may be input i.
-bool clash(const Ranges& in, const Ranges& out, int inplace = 0) {
-  for (size_t i = 0; i < out.size(); ++i) {
-    for (size_t j = i + 1; j < out.size(); ++j)
-      if (meet(out[i], out[j])) return true;
-    for (size_t j = 0; j < in.size(); ++j)
-      if (meet(out[i], in[j]) && !(i == j && (int)i < inplace && out[i].p == in[j].p)) return true;
-  }
-  return false;
-}
-
-rra_status_t cuda_st(cudaError_t e) { return e == cudaSuccess ? RRA_SUCCESS : RRA_ERR_CUDA; }
 
 // A matrix a product reads: the caller's rows, or padded rows in the
 // workspace.
@@ -211,11 +173,6 @@ Fn encode_fn() {
   return fn;
 }
 
-// Ends a call: its record has the largest grid of its launches.
-rra_status_t done(const char* call, int n, size_t count, int dt, int grid, rra_status_t st) {
-  return record_call(call, RRA_ALGO_DIRECT, n, count, dt, std::max(grid, take_grid()), st);
-}
-
 thread_local int g_largest_grid = 0;
 
 }  // namespace
@@ -241,6 +198,30 @@ bool rra::tc_map(CUtensorMap* m, const void* base, size_t inner, size_t rows, si
   const cuuint32_t es[2] = {1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool rra::mx4_map_codes(CUtensorMap* m, const void* base, size_t row_bytes, size_t rows, int box_rows) {
+  const Fn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {row_bytes, rows};
+  const cuuint64_t strides[1] = {row_bytes};
+  const cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+  const cuuint32_t es[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool rra::mx4_map_scales(CUtensorMap* m, const void* base, size_t across, size_t bands, int box_bands) {
+  const Fn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {across * 128, bands};  // words
+  const cuuint64_t strides[1] = {across * 512};
+  const cuuint32_t box[2] = {256, (cuuint32_t)box_bands};
+  const cuuint32_t es[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -457,6 +457,131 @@ rra_status_t rra_vocab_loss_backward(const void* x, const void* const* weights, 
                                      size_t workspace_bytes, rra_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* the serving step around a tensor-parallel all-reduce                     */
+/* ------------------------------------------------------------------------ */
+/*
+ * Operators of a tensor-parallel forward pass in 4 bits ([AIH] "Source
+ * code": the fused all-reduce + RMSNorm of inference frameworks; [ILP] "Deep
+ * dive": a column-parallel layer, then a row-parallel layer, then the
+ * all-reduce), and the choice of the next token from vocabulary-parallel
+ * logits.  Shards, overlap (RRA_ERR_ALIAS), streams and graphs as for the
+ * training step's operators; no call needs a workspace.  The products need
+ * rra_init: their bounded internal waits (2 s) report to the device status
+ * word.  Results do not depend on timing.
+ *
+ * MX4, microscaled 4-bit floating point: 32 consecutive columns of a row (the
+ * last block may be short) share a scale 2^e, e the smallest integer >= -127
+ * with max |x| <= 6 * 2^e; code = e2m1(x * 2^-e) (0, 0.5, 1, 1.5, 2, 3, 4, 6
+ * and a sign), nearest, ties to even; nothing is clipped.  A block that holds
+ * a value that is not finite has scale byte 255 (NaN) and codes 0, and reads,
+ * and multiplies, as NaN.  A rows x cols matrix is
+ * - codes: rows of 16 * ceil(cols / 32) bytes, column 2i in the low half of
+ *   byte i, column 2i + 1 in the high half, zeros behind the last column;
+ * - scales: rra_mx4_scale_bytes(rows, cols) bytes, tiles of 128 rows x 4
+ *   blocks: the byte e + 127 of (row, block) is number
+ *   row % 32 * 16 + row % 128 / 32 * 4 + block % 4 of the 512 of tile
+ *   (row / 128, block / 4), the tiles of a row band side by side.  The calls
+ *   that write a matrix write 0 for blocks behind the last one of a row and
+ *   leave the bytes of rows behind the last one as they were; a matrix made
+ *   elsewhere must not have 255 there for blocks behind the last one.
+ * Both start on 16 bytes (else RRA_ERR_UNSUPPORTED).  Column-wise splits of a
+ * matrix (a row-parallel layer's shards) are quantised each on its own.
+ */
+
+/** An MX4 matrix: device pointers.  Calls take host pointers to these, read
+ *  during the call only. */
+typedef struct {
+  void* codes;
+  void* scales;
+} rra_mx4_t;
+
+/** Bytes of a rows x cols MX4 matrix's scales: 512 * ceil(rows / 128) *
+ *  ceil(cols / 128). */
+size_t rra_mx4_scale_bytes(size_t rows, size_t cols);
+
+/** x (rows x cols of dtype, RRA_FLOAT32 or RRA_BFLOAT16) in MX4.  Errors:
+ *  RRA_ERR_INVALID_ARG, RRA_ERR_UNSUPPORTED (a part of out not 16-byte
+ *  aligned, an extent of 2^31 or more), RRA_ERR_ALIAS, RRA_ERR_CUDA. */
+rra_status_t rra_mx4_quantize(const void* x, const rra_mx4_t* out, size_t rows, size_t cols, rra_dtype_t dtype,
+                              rra_stream_t stream);
+
+/** The values of an MX4 matrix: code * 2^e, rounded to dtype once (exact but
+ *  for values below its normal range).  Errors as rra_mx4_quantize. */
+rra_status_t rra_mx4_restore(const rra_mx4_t* in, void* out, size_t rows, size_t cols, rra_dtype_t dtype,
+                             rra_stream_t stream);
+
+/** All-reduce fused with the residual stream, RMSNorm and quantisation
+ *  ([AIH] "Source code"): s = SUM_k bufs[k] + residual in float32, ascending
+ *  ranks, the residual last; residual_out = s rounded to dtype (the next
+ *  layer's residual); out = MX4 of (s * rstd) * gamma, where rstd is the
+ *  float32 nearest to 1 / sqrt(mean_j(s^2) + eps) (but for ties within 2^-40)
+ *  and both products round to float32, so that the codes depend on no order
+ *  of summation.
+ *  - residual, residual_out: rows x hidden of dtype; either may be NULL (no
+ *    addition; the sum is not stored), and they may be the same.
+ *  - gamma: hidden elements of dtype; hidden in [1, 51200].
+ *  The squares have float32's range.  Errors as rra_allreduce_rmsnorm;
+ *  RRA_ERR_UNSUPPORTED also for a part of out not 16-byte aligned. */
+rra_status_t rra_allreduce_rmsnorm_mx4(const void* const* bufs, int nranks, size_t rows, size_t hidden,
+                                       const void* gamma, float eps, const void* residual, void* residual_out,
+                                       const rra_mx4_t* out, rra_dtype_t dtype, rra_stream_t stream);
+
+/** Column-parallel product of MX4 matrices ([ILP] "Deep dive"), such as the
+ *  vocabulary head: outs[r] (tokens x widths[r] of dtype, RRA_FLOAT32 or
+ *  RRA_BFLOAT16) = X W_r^T for x: tokens x hidden and weights[r]: widths[r] x
+ *  hidden.  Products are exact, sums float32, rounded to dtype once.
+ *  tokens == 0, or all widths 0, launches nothing.  Errors:
+ *  RRA_ERR_INVALID_ARG (null, hidden 0, dtype, misaligned),
+ *  RRA_ERR_UNSUPPORTED (an MX4 part not 16-byte aligned, an extent of 2^31 or
+ *  more, nranks > RRA_MAX_RANKS), RRA_ERR_NOT_INITIALIZED, RRA_ERR_ALIAS,
+ *  RRA_ERR_CUDA. */
+rra_status_t rra_mx4_product(const rra_mx4_t* x, const rra_mx4_t* weights, void* const* outs, int nranks,
+                             size_t tokens, size_t hidden, const size_t* widths, rra_dtype_t dtype,
+                             rra_stream_t stream);
+
+/** Row-parallel product of MX4 matrices with its all-reduce ([ILP] "Deep
+ *  dive"): out (tokens x hidden of dtype) = SUM_r X_r W_r^T for xs[r]: tokens
+ *  x width and weights[r]: hidden x width, the sum over ranks in the float32
+ *  accumulator.  width == 0 writes zeros.  Errors as rra_mx4_product. */
+rra_status_t rra_mx4_product_sum(const rra_mx4_t* xs, const rra_mx4_t* weights, void* out, int nranks, size_t tokens,
+                                 size_t width, size_t hidden, rra_dtype_t dtype, rra_stream_t stream);
+
+/** Column-parallel half of a gated feed-forward block in MX4 ([ILP] "Deep
+ *  dive"): acts[r] (tokens x width, MX4) = act(X G_r^T) * (X U_r^T), float32
+ *  until the quantisation, for x: tokens x hidden, gates[r] and ups[r]: width x
+ *  hidden.  Errors as rra_mx4_product (a bad act too). */
+rra_status_t rra_mx4_gated_ffn(const rra_mx4_t* x, const rra_mx4_t* gates, const rra_mx4_t* ups,
+                               const rra_mx4_t* acts, int nranks, size_t tokens, size_t hidden, size_t width,
+                               rra_act_t act, rra_stream_t stream);
+
+/** The next token of each row, drawn from vocabulary-parallel logits ([ILP]
+ *  "Deep dive": a layer's weights split over the ranks).  logits[r]: rows x
+ *  vocab[r] of dtype (RRA_FLOAT32 or RRA_BFLOAT16), the vocabulary being the
+ *  shards one after another.  Per row, w_j = exp((l_j - max l) / temperature):
+ *  - top_k > 0 keeps the top_k largest logits;
+ *  - top_p < 1 keeps, of those in falling order, the shortest run whose weight
+ *    reaches top_p times theirs (one at least);
+ *  - min_p > 0 keeps what weighs min_p or more;
+ *  equal logits go by the lowest index.  token = the first index i with
+ *  SUM_{j <= i, kept} w_j > uniform * SUM_{kept} w_j, logprob = log(w_token /
+ *  SUM_{kept} w_j).  temperature == 0 (as top_k == 1) takes the largest logit.
+ *  - uniform: rows float32 in [0, 1) (clamped); temperature, top_k, top_p,
+ *    min_p: one value per row (device), or NULL for all rows 1, 0, 1, 0;
+ *    logprob: rows float32, or NULL.
+ *  - -infinity masks a token; a row of nothing else gives token -1, logprob
+ *    -infinity; a row with a NaN logit or a temperature that is NaN or
+ *    negative gives token -1, logprob NaN.  Where +infinity occurs its
+ *    tokens share the whole weight.
+ *  - Weights are held to 31 bits and in units of 2^-43 of the largest, and
+ *    summed exactly: a token of less than half a unit is never drawn.
+ *  Vocabulary up to 368640 in all (else RRA_ERR_UNSUPPORTED).  Errors:
+ *  RRA_ERR_INVALID_ARG, RRA_ERR_UNSUPPORTED, RRA_ERR_ALIAS, RRA_ERR_CUDA. */
+rra_status_t rra_vocab_sample(const void* const* logits, const size_t* vocab, int nranks, size_t rows,
+                              const float* uniform, const float* temperature, const int32_t* top_k,
+                              const float* top_p, const float* min_p, int64_t* token, float* logprob,
+                              rra_dtype_t dtype, rra_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* LL and LL128 wire formats ([AIH] "Protocols")                            */
 /* ------------------------------------------------------------------------ */
 
