@@ -7,18 +7,16 @@
 //   sum_{j <= i, kept} w_j > uniform * sum_{kept} w_j
 //
 // No sort: the bounds of top-k and top-p are found as the logit at which a
-// count or a weight is reached, by histograms of 1024 bins: first counts by the
-// distance to the maximum, then counts or weights over ever narrower ranges of
-// the logits' bits as ordered integers, until a bin is one value; equal logits
-// at the bound are taken by index.  The counts by distance also say, to 3%, how
-// the weight is spread, so that top-p needs a histogram of weights over a few
-// bins only.
+// count or a weight is reached, by histograms of up to 1024 bins over the
+// logits' bits as ordered integers: of the nearest 16 octaves of weight first
+// (only if the bound is not there, of the others: most logits are far down and
+// are then not added to a bin), then of ever narrower ranges, until a bin is one
+// value; equal logits at the bound are taken by index.
 //
-// Weights are integers in units of 2^-43 of the largest, exact sums of which
+// Weights are integers in units of 2^-44 of the largest, exact sums of which
 // depend on no order, so that rows give the same token however many CTAs share
-// them.  A weight is within 2^-31 of its value, relative (or half a unit): the
-// exponent is formed from the logits' exact difference as a pair of float32.
-// Weights below half a unit (2^-44) are zero, and such tokens are never drawn.
+// them.  A weight is within 2^-29 of its value, relative, or a unit; below
+// 2^-44 it is zero, and such tokens are never drawn.
 //
 // A cluster of up to 8 CTAs shares a row.  Each keeps its slice of the logits
 // in shared memory, so HBM is read once; histograms and sums are read across
@@ -38,38 +36,37 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 1024;
+constexpr int kBatch = 4;  // units of a thread whose loads are in flight together
 constexpr int kMaxSplit = 8;
-constexpr int kUnitBits = 43;
-constexpr float kBinsPerOctave = 23.f;  // 44 octaves of weight in 1012 bins
-constexpr int kZeroBin = 1013;          // weights of bins from here on are zero
+constexpr int kUnitBits = 44;
+constexpr float kNear = 16.f;  // octaves of weight searched first
+constexpr float kFar = 44.f;   // logits further down weigh nothing
 constexpr size_t kMostSlice = 184 * 1024;
 static_assert((kSampleMaxVocab / kMaxSplit + 1) * 4 + kMaxRanks * 64 <= kMostSlice, "a row fits a cluster");
 
-// 2^(-i / 128), in units of 2^-44 and as float32.
-struct Power {
-  unsigned long long fixed;
-  float real, pad;
-};
+// 2^(-i / 64) in units of 2^-44; all but the first in [1/2, 1), and that one as
+// the largest number below 1, so that its leading bits are a float's.
+constexpr int kPowers = 64;
 struct PowerTable {
-  Power p[128];
+  unsigned long long p[kPowers];
 };
 
 constexpr PowerTable make_table() {  // by the series of the exponential
   PowerTable t{};
-  for (int i = 0; i < 128; ++i) {
-    const double x = -(double)i / 128.0 * 0.693147180559945309417232121458;
+  for (int i = 0; i < kPowers; ++i) {
+    const double x = -(double)i / kPowers * 0.693147180559945309417232121458;
     double sum = 1.0, term = 1.0;
     for (int k = 1; k < 30; ++k) {
       term = term * x / k;
       sum += term;
     }
-    t.p[i].fixed = (unsigned long long)(sum * (double)(2ull << kUnitBits) + 0.5);
-    t.p[i].real = (float)sum;
+    t.p[i] = i ? (unsigned long long)(sum * (double)(1ull << kUnitBits) + 0.5) : (1ull << kUnitBits) - 1;
   }
   return t;
 }
 
-__constant__ PowerTable kTable = make_table();
+__device__ const PowerTable kTable = make_table();
+constexpr int kCopies = 16;  // of the table: lanes l and l + 16 read the l-th, free of bank conflicts
 
 struct Seg {
   int pos;          // position of its first logit in the slice
@@ -78,21 +75,21 @@ struct Seg {
 };
 
 struct Shared {
-  Power power[128];
+  unsigned long long power[kPowers * kCopies];
   Seg seg[kMaxRanks];
   // by parity of the row, read by the cluster
-  uint32_t top[2];                        // the slice's largest key, all ones if it holds a NaN
-  int first[2];                           // position of the first logit equal to the row's maximum
-  unsigned long long sums[2][2][kWarps];  // of the search by weight: all that is kept, what lies above its range
-  unsigned long long above[2][kWarps];    // weight kept of each warp's positions, without the bound's ties
-  uint32_t ties[2][kWarps];
+  uint32_t top[2];              // the slice's largest key, all ones if it holds a NaN
+  int first[2];                 // position of the first logit equal to the row's maximum
+  unsigned long long all[2];    // weight of what is kept when the search by weight begins
+  unsigned long long above[2];  // weight of what is kept in the end, without the bound's ties
+  uint32_t ties[2];
   // of this CTA
-  unsigned long long all_above[kMaxSplit * kWarps];
-  uint32_t all_ties[kMaxSplit * kWarps];
+  unsigned long long warp_above[2][kWarps];
+  uint32_t warp_ties[2][kWarps];
   uint32_t wmax[kWarps];
   unsigned long long scan[kWarps];
-  float low[kWarps], high[kWarps];
-  int cut, cut2;
+  int cut;
+  uint32_t allow;
   unsigned long long before;
 };
 
@@ -121,16 +118,6 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Sum over this lane and the lanes before it.
-__device__ __forceinline__ unsigned long long prefix(unsigned long long v) {
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long u = __shfl_up_sync(0xffffffffu, v, o);
-    if ((int)(threadIdx.x & 31) >= o) v += u;
-  }
-  return v;
-}
-
 // Logits as integers in the same order (equal zeros alike); 0 is below every
 // logit and marks positions without one.
 template <int DT>
@@ -147,6 +134,7 @@ struct Logit<RRA_FLOAT32> {
     return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
   }
   static __device__ __forceinline__ float real(uint32_t b) { return __uint_as_float(b); }
+  static __device__ __forceinline__ uint32_t from(float f) { return key(__float_as_uint(f)); }  // smallest key >= f
   // Largest of units, NaN if one is.
   struct Most {
     float m = -INFINITY;
@@ -171,6 +159,10 @@ struct Logit<RRA_BFLOAT16> {
     return __uint_as_float((k & 0x8000u ? k ^ 0x8000u : ~k & 0xFFFFu) << 16);
   }
   static __device__ __forceinline__ float real(uint32_t b) { return __uint_as_float(b << 16); }
+  static __device__ __forceinline__ uint32_t from(float f) {
+    const uint32_t b = __float_as_uint(f);
+    return key(b & 0x80000000u ? b >> 16 : (b + 0xFFFFu) >> 16);
+  }
   struct Most {
     uint32_t m = 0xFF80FF80u;
     __device__ __forceinline__ void put(uint32_t v) { asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(v)); }
@@ -202,88 +194,144 @@ __device__ __forceinline__ uint4 only(const uint4& x, int from, int to, uint32_t
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Weights of a row.
+// Weights of a row.  x(l) = (top - l) log2(e) / temperature is reduced as the
+// difference of two multiples of 1/64 and of what is left of them.
 struct Scale {
   float top;     // largest logit
   float hi, lo;  // log2(e) / temperature as a pair
-  float bins;    // bins per unit of logit
+  float low;     // logits below this weigh nothing (x > kFar)
+  float near;    // x is up to kNear from here on
+  float base;    // subtracted from every logit, exactly
+  int k0;        // of the largest: (top - base) log2(e) / temperature = k0 / 64 + g0
+  float g0;
 };
 
-// w = 2^-x, x = (top - l) log2(e) / temperature as a pair p + pe: 2^(-k / 128)
-// from the table for the k nearest 128 p, and a cubic for the rest.
-__device__ __forceinline__ unsigned long long weight(const Shared& sh, const Scale& c, float l) {
-  if (l == c.top) return 1ull << kUnitBits;
-  const float d = __fsub_rn(c.top, l), z = __fsub_rn(d, c.top);
-  const float p = __fmul_rn(d, c.hi);
-  if (!(p < 44.f)) return 0;
-  const float rest = __fadd_rn(__fsub_rn(c.top, __fsub_rn(d, z)), __fsub_rn(-l, z));  // of the difference
-  const float pe = __fmaf_rn(rest, c.hi, __fmaf_rn(d, c.lo, __fmaf_rn(d, c.hi, -p)));
-  const float t = __fmaf_rn(p, 128.f, 12582912.f);  // 1.5 * 2^23: rounds to an integer
-  const int k = __float_as_int(t) - 0x4B400000;
-  const float g = __fadd_rn(__fmaf_rn(__fsub_rn(t, 12582912.f), -1.f / 128.f, p), pe);
-  const float y = g * -0.69314718f;
-  const uint4 q = *reinterpret_cast<const uint4*>(&sh.power[k & 127]);
-  const float e = y * fmaf(y, fmaf(y, 0.16666667f, 0.5f), 1.f) * __uint_as_float(q.z);
-  const unsigned long long fixed = ((unsigned long long)q.y << 32) | q.x;
-  const unsigned long long w = fixed + ((long long)__float2int_rn(e * 549755813888.f) << (kUnitBits + 1 - 39));
-  return ((w >> (k >> 7)) + 1) >> 1;
+constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer, of up to 22 bits
+
+// v (hi + lo) = k / 64 + g, less g0; k comes as the bits of k + kRound.
+__device__ __forceinline__ float reduce(float v, const Scale& c, float g0, int* k) {
+  const float u = __fmul_rn(v, c.hi);
+  const float ue = __fmaf_rn(v, c.lo, __fmaf_rn(v, c.hi, -u));
+  const float t = __fmaf_rn(u, (float)kPowers, kRound);
+  *k = __float_as_int(t);
+  return __fadd_rn(__fmaf_rn(__fsub_rn(t, kRound), -1.f / kPowers, u), __fsub_rn(ue, g0));
 }
 
-__device__ __forceinline__ int distance_bin(const Scale& c, float l) {
-  if (l == c.top) return 0;  // +infinity too
-  const float x = __fmul_rn(__fsub_rn(c.top, l), c.bins);
-  return x < (float)(kBins - 1) ? (int)x : kBins - 1;
+__device__ __forceinline__ Scale make_scale(float top, float temperature) {
+  Scale c;
+  c.top = top;
+  c.hi = __fdiv_rn(1.44269502f, temperature);
+  c.lo = __fdiv_rn(__fadd_rn(__fmaf_rn(-c.hi, temperature, 1.44269502f), 1.92596303e-8f), temperature);
+  if (!(c.hi < 1e30f)) {
+    c.hi = 1e30f;
+    c.lo = 0.f;
+  }
+  // an infinite temperature, or an infinite logit: what weighs anything weighs the same
+  if (c.hi == 0.f || top == INFINITY) c.hi = c.lo = 0.f;
+  c.low = top == INFINITY ? top : fmaxf(__fsub_rn(top, __fdiv_rn(kFar, c.hi)), -FLT_MAX);
+  c.near = top == INFINITY ? top : fmaxf(__fsub_rn(top, __fdiv_rn(kNear, c.hi)), -FLT_MAX);
+  // multiples of 1/64 have 22 bits; where the largest logit has more, those that
+  // weigh anything are within a factor of two of it
+  c.base = fabsf(top) * c.hi > 30000.f && top != INFINITY ? top : 0.f;
+  c.g0 = reduce(fminf(top, FLT_MAX) - c.base, c, 0.f, &c.k0);
+  return c;
+}
+
+// w = 2^-x(l) for l >= low: 2^(-k / 64) from the table and a quartic for the
+// rest, cut to units of 2^-44 and put in the middle of the unit cut to.
+__device__ __forceinline__ unsigned long long weight(const Shared& sh, const Scale& c, float l) {
+  int k;
+  const float g = reduce(fminf(l, FLT_MAX) - c.base, c, c.g0, &k);
+  k = c.k0 - k;
+  const unsigned long long fixed = sh.power[(k & (kPowers - 1)) * kCopies + (threadIdx.x & (kCopies - 1))];
+  // (2^g - 1) 2^(-k / 64) in units of 2^-37
+  const float real = __uint_as_float(0x51800000u | ((uint32_t)(fixed >> (kUnitBits - 24)) & 0x7FFFFFu));
+  const float e = g * fmaf(g, fmaf(g, fmaf(g, 0.00961813f, 0.05550411f), 0.24022651f), 0.69314718f) * real;
+  const unsigned long long w = fixed + (long long)__float2int_rn(e) * (1ll << (kUnitBits - 37));
+  return (w >> (k / kPowers)) | 1;
 }
 
 // Keys lo to hi in bins of 2^shift, the largest first.
 struct Range {
   uint32_t lo, hi;
   int shift;
+  __device__ __forceinline__ int bins() const { return (int)((hi - lo) >> shift) + 1; }
 };
-
-// The smallest key for which `is` holds (it does from some key on, and for
-// `hi`), found by the warp 32 probes at a time.
-template <class Is>
-__device__ __forceinline__ uint32_t first_key(uint32_t lo, uint32_t hi, Is is) {
-  const uint32_t lane = threadIdx.x & 31;
-  while (hi > lo) {
-    const uint32_t step = (hi - lo) / 32 + 1;  // probes lo, lo + step, ... up to hi - 1
-    const uint64_t at = (uint64_t)lo + (uint64_t)lane * step;
-    const uint32_t yes = __ballot_sync(0xffffffffu, at >= hi || is((uint32_t)at));
-    const int n = yes ? __ffs(yes) - 1 : 32;  // probes that say no
-    if (n == 0) return lo;
-    const uint64_t top = (uint64_t)lo + (uint64_t)n * step;
-    lo = lo + (uint32_t)(n - 1) * step + 1;
-    if (top < hi) hi = (uint32_t)top;
-  }
-  return lo;
-}
 
 __device__ __forceinline__ Range with_bins(uint32_t lo, uint32_t hi) {
   const uint32_t span = hi - lo;  // (span >> shift) + 1 <= 1024
   return {lo, hi, span < kBins ? 0 : 32 - __clz(span) - 10};
 }
 
-// The keys of distance bins a to b (bins fall as keys rise).
-template <int DT>
-__device__ __forceinline__ Range keys_of(const Scale& c, int a, int b, uint32_t most) {
-  const uint32_t lo = first_key(1, most, [&](uint32_t k) { return distance_bin(c, Logit<DT>::value(k)) <= b; });
-  if (a == 0) return with_bins(lo, most);
-  const uint32_t next = first_key(lo, most, [&](uint32_t k) { return distance_bin(c, Logit<DT>::value(k)) < a; });
-  return with_bins(lo, next - 1);
+// The smallest key of [lo, hi] for which `is` holds (it does from some key on,
+// and for hi): 32 probes of the warp at a time.
+template <class Is>
+__device__ __forceinline__ uint32_t first_key(uint32_t lo, uint32_t hi, Is is) {
+  const uint32_t lane = threadIdx.x & 31;
+  while (hi > lo) {
+    const uint32_t step = (hi - lo) / 32 + 1;  // lo, lo + step, ... up to hi - 1
+    const uint64_t at = (uint64_t)lo + (uint64_t)lane * step;
+    const uint32_t yes = __ballot_sync(0xffffffffu, at >= hi || is((uint32_t)at));
+    const uint32_t n = yes ? __ffs(yes) - 1 : 32;  // probes that say no
+    const uint64_t top = (uint64_t)lo + (uint64_t)n * step;
+    if (top < hi) hi = (uint32_t)top;
+    if (n) lo = lo + (n - 1) * step + 1;
+  }
+  return lo;
+}
+
+// f v for f in [0, 1], exact but for the fraction (up: rounded up).
+__device__ __forceinline__ unsigned long long share_of(unsigned long long v, float f, bool up) {
+  const uint32_t bits = __float_as_uint(f), ex = bits >> 23;
+  const unsigned long long m = ex ? (bits & 0x7FFFFFu) | 0x800000u : bits;
+  const int shift = 150 - (int)(ex ? ex : 1);  // f = m 2^-shift, shift >= 23
+  const unsigned long long hi = __umul64hi(v, m), lo = v * m;
+  unsigned long long q = 0, rest = m && v;
+  if (shift < 64) {
+    q = (hi << (64 - shift)) | (lo >> shift);
+    rest = lo << (64 - shift);
+  } else if (shift < 128) {
+    q = hi >> (shift - 64);
+    rest = lo | (hi & ((1ull << (shift - 64)) - 1));
+  }
+  return q + (up && rest ? 1 : 0);
 }
 
 // What a bound keeps: all keys above `key`, and the first `ties` equal to it.
 struct Bound {
-  uint32_t key;
-  unsigned long long ties;
+  uint32_t key, ties;
 };
 
-// Block-wide sum of a pair in warp order; every thread gets it.
 __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
+}
+
+// Sum over this lane and the lanes before it.
+template <class T>
+__device__ __forceinline__ T prefix(T v) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T u = __shfl_up_sync(0xffffffffu, v, o);
+    if ((int)(threadIdx.x & 31) >= o) v += u;
+  }
+  return v;
+}
+
+// Lanes hold consecutive parts of a row, `sum` of weight and `ties` at the
+// bound each, of which `allow` in all are kept at `unit`: the part in which the
+// running weight passes `rest`, -1 if none.  Leaves what of rest and allow
+// remains for it (as they were if none).
+__device__ __forceinline__ int locate(unsigned long long sum, uint32_t ties, unsigned long long unit,
+                                      unsigned long long& rest, uint32_t& allow) {
+  const uint32_t seen = prefix(ties) - ties, left = allow > seen ? allow - seen : 0;
+  const unsigned long long mass = sum + min(ties, left) * unit, upto = prefix(mass);
+  const int i = __ffs(__ballot_sync(0xffffffffu, upto > rest)) - 1;
+  if (i < 0) return i;
+  rest -= __shfl_sync(0xffffffffu, upto - mass, i);
+  allow = __shfl_sync(0xffffffffu, left, i);
+  return i;
 }
 
 template <int DT>
@@ -300,20 +348,16 @@ struct Row {
   int flip;
   int& level;  // parity of the histogram in use
 
+  // Logits above this are kept: -infinity, which weighs nothing, without a bound.
+  static __device__ __forceinline__ float bound_of(const Bound& b) { return b.key ? L::value(b.key) : -INFINITY; }
+
   __device__ __forceinline__ uint32_t* bins() const { return hist + (level & 1) * 3 * kBins; }
 
-  __device__ __forceinline__ void clear(int words) {
-    uint4* h = reinterpret_cast<uint4*>(bins());
-    for (int i = threadIdx.x; i < words * kBins / 4; i += kThreads) h[i] = make_uint4(0, 0, 0, 0);
-    __syncthreads();
+  __device__ __forceinline__ uint32_t raw_at(int at) const {
+    return PU == 4 ? reinterpret_cast<const uint32_t*>(slice)[at] : reinterpret_cast<const uint16_t*>(slice)[at];
   }
 
-  // f(raw) for every position of the slice, of this thread's units.
-  template <class F>
-  __device__ __forceinline__ void each(F f) const {
-    for (int u = threadIdx.x; u < units; u += kThreads) unit(slice[u], f);
-  }
-
+  // f(raw) for every position of a unit.
   template <class F>
   static __device__ __forceinline__ void unit(const uint4& x, F f) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -321,209 +365,260 @@ struct Row {
     for (int j = 0; j < PU; ++j) f(PU == 4 ? w[j] : (w[j / 2] >> (16 * (j & 1))) & 0xFFFFu);
   }
 
-  __device__ __forceinline__ void add(uint32_t* h, int b, unsigned long long w) const {
+  // f(raw) for the positions of unit u that `is` picks, few of them: one at a
+  // time a lane, so that a warp's steps are those of its fullest lane.
+  template <class Is, class F>
+  __device__ __forceinline__ void picked(int u, Is is, F f) const {
+    uint32_t mask = 0;
+    int j = 0;
+    unit(slice[u], [&](uint32_t raw) { mask |= (is(L::real(raw)) ? 1u : 0u) << j++; });
+    while (mask) {
+      const int at = u * PU + __ffs(mask) - 1;
+      mask &= mask - 1;
+      f(raw_at(at));
+    }
+  }
+
+  static __device__ __forceinline__ void add(uint32_t* h, int b, unsigned long long w) {
     // pieces of 15 bits, whose sums of up to 2^17 elements fit a word
     atomicAdd(h + b, (uint32_t)w & 0x7FFFu);
     if (w >> 15) atomicAdd(h + kBins + b, (uint32_t)(w >> 15) & 0x7FFFu);
     if (w >> 30) atomicAdd(h + 2 * kBins + b, (uint32_t)(w >> 30));
   }
 
-  // The cluster's sum of this thread's two bins.
-  __device__ __forceinline__ void gather(int words, unsigned long long* v) const {
-    const uint32_t* h = bins() + 2 * threadIdx.x;
-    v[0] = v[1] = 0;
+  // The slice's elements in range and above `keep`'s key into the range's bins,
+  // counted or weighed, and published to the cluster.  all: also sums the
+  // weight of everything above that key.
+  __device__ __forceinline__ void fill(const Range& r, bool weights, const Bound& keep, bool all) {
+    const int n = r.bins(), tid = threadIdx.x;
+    uint32_t* h = bins();
+    for (int i = tid; i < (n + 3) / 4; i += kThreads)
+      for (int k = 0; k < (weights ? 3 : 1); ++k)
+        reinterpret_cast<uint4*>(h + k * kBins)[i] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    const float bound = bound_of(keep), low = fmaxf(L::value(r.lo), c.low), high = L::value(r.hi);
+    const auto in = [&](float l) { return l >= low && l <= high && l > bound; };  // no position (NaN): false
+    const auto put = [&](uint32_t raw) {
+      const int b = (int)((r.hi - L::key(raw)) >> r.shift);
+      if (weights)
+        add(h, b, weight(sh, c, L::real(raw)));
+      else
+        atomicAdd(h + b, 1u);
+    };
+    if (!all) {
+      for (int u = tid; u < units; u += kThreads) picked(u, in, put);
+      cluster_sync();
+      return;
+    }
+    unsigned long long sum = 0;
+    if (keep.key) {  // few are kept
+      for (int u = tid; u < units; u += kThreads)
+        picked(u, [&](float l) { return l > bound && l >= c.low; },
+               [&](uint32_t raw) {
+                 const float l = L::real(raw);
+                 const unsigned long long w = weight(sh, c, l);
+                 sum += w;
+                 if (l >= low && l <= high) add(h, (int)((r.hi - L::key(raw)) >> r.shift), w);
+               });
+    } else {
+      for (int u = tid; u < units; u += kThreads) {
+        unit(slice[u], [&](uint32_t raw) {
+          const float l = L::real(raw);
+          if (l >= c.low) sum += weight(sh, c, l);
+        });
+        picked(u, in, put);
+      }
+    }
+    __syncwarp();
+    sum = warp_sum(sum);
+    if ((tid & 31) == 0) sh.scan[tid >> 5] = sum;
+    __syncthreads();
+    if (tid < 32) {
+      sum = warp_sum(tid < kWarps ? sh.scan[tid] : 0);
+      if (tid == 0) sh.all[flip] = sum;
+    }
+    cluster_sync();
+  }
+
+  // The cluster's sum of bins b and b + 1.
+  __device__ __forceinline__ void gather(int b, bool weights, unsigned long long* v) const {
+#pragma unroll 1
+    for (int k = 0; k < (weights ? 3 : 1); ++k) {
+      // every CTA's words in flight before the first is used
+      unsigned long long x[kMaxSplit];
 #pragma unroll
-    for (int q = 0; q < kMaxSplit; ++q) {
-      if (q >= split) break;
+      for (int q = 0; q < kMaxSplit; ++q) x[q] = q < split ? peer_u64(bins() + k * kBins + b, q) : 0;
 #pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        if (k >= words) break;
-        const unsigned long long x = peer_u64(h + k * kBins, q);
-        v[0] += (x & 0xFFFFFFFFull) << (15 * k);
-        v[1] += (x >> 32) << (15 * k);
+      for (int q = 0; q < kMaxSplit; ++q) {
+        v[0] += (x[q] & 0xFFFFFFFFull) << (15 * k);
+        v[1] += (x[q] >> 32) << (15 * k);
       }
     }
   }
 
-  // The bin in which the running sum (from `above` on) reaches `target`, -1 if
-  // none; above: the sum before it.
-  __device__ __forceinline__ int find(const unsigned long long* v, unsigned long long& above,
-                                      unsigned long long target) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const unsigned long long sum = prefix(v[0] + v[1]);
-    if (lane == 31) sh.scan[warp] = sum;
-    if (threadIdx.x == 0) sh.cut = -1;
-    __syncthreads();
-    unsigned long long end = above + sum;
-    for (int w = 0; w < warp; ++w) end += sh.scan[w];
-    const unsigned long long begin1 = end - v[1], begin0 = begin1 - v[0];
-    if (begin0 < target && begin1 >= target) {
-      sh.cut = 2 * threadIdx.x;
-      sh.before = begin0;
-    } else if (begin1 < target && end >= target) {
-      sh.cut = 2 * threadIdx.x + 1;
-      sh.before = begin1;
+  // Of a range's bins, the one in which the running sum (from `above` on)
+  // reaches `target`, -1 if none; above: the sum before it (all of it).
+  // `extra`, if not 0, belongs to key `at` too.
+  __device__ __forceinline__ int find(const Range& r, bool weights, uint32_t at, unsigned long long extra,
+                                      unsigned long long& above, unsigned long long target) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = 2 * threadIdx.x;
+    const int n = r.bins();
+    const bool one = n <= 64;  // the first warp alone
+    unsigned long long v[2] = {0, 0};
+    if (b < n) gather(b, weights, v);
+    if (b + 1 >= n) v[1] = 0;  // not of the range
+    if (extra && at >= r.lo && at <= r.hi) {
+      const int d = (int)((r.hi - at) >> r.shift) - b;
+      if (d == 0) v[0] += extra;
+      if (d == 1) v[1] += extra;
     }
+    unsigned long long end = above;
+    if (!one) {
+      const unsigned long long sum = prefix(v[0] + v[1]);
+      if (lane == 31) sh.scan[warp] = sum;
+      if (threadIdx.x == 0) sh.cut = -1;
+      __syncthreads();
+      const unsigned long long upto = prefix(lane < kWarps ? sh.scan[lane] : 0);
+      const unsigned long long before = __shfl_sync(0xffffffffu, upto, warp ? warp - 1 : 0);
+      end += sum + (warp ? before : 0);
+      above += __shfl_sync(0xffffffffu, upto, 31);
+    } else if (warp == 0) {
+      end += prefix(v[0] + v[1]);
+      if (lane == 31) {
+        sh.cut = -1;
+        sh.before = end;
+      }
+      __syncwarp();
+    }
+    if (!one || warp == 0) {
+      const unsigned long long begin1 = end - v[1], begin0 = begin1 - v[0];
+      if (begin0 < target && begin1 >= target) {
+        sh.cut = b;
+        sh.before = begin0;
+      } else if (begin1 < target && end >= target) {
+        sh.cut = b + 1;
+        sh.before = begin1;
+      }
+    }
+    ++level;
     __syncthreads();
     const int cut = sh.cut;
-    if (cut >= 0) above = sh.before;
-    __syncthreads();  // sh.cut may be set again
+    if (cut >= 0 || one) above = sh.before;
+    __syncthreads();  // sh.cut and sh.scan may be set again
     return cut;
   }
 
-  // Narrows a range of keys to the one key at which the sum reaches `target`:
-  // of ones, or of weights (without the elements up to key `at`; `extra` is what
-  // is kept of that one's).  The range's bins have been filled and published.
-  __device__ __forceinline__ uint32_t narrow(Range r, bool weights, uint32_t at, unsigned long long extra,
-                                             unsigned long long& above, unsigned long long target) {
-    for (;;) {
-      unsigned long long v[2];
-      gather(weights ? 3 : 1, v);
-      if (extra && at >= r.lo && at <= r.hi) {
-        const int b = (int)((r.hi - at) >> r.shift) - 2 * (int)threadIdx.x;
-        if (b == 0) v[0] += extra;
-        if (b == 1) v[1] += extra;
-      }
-      ++level;
-      const int b = find(v, above, target);
-      if (b < 0) return 0;  // not in the range: the callers' targets are
-      const uint32_t hi = r.hi - ((uint32_t)b << r.shift);
-      if (r.shift == 0) return hi;
-      const uint32_t below = (1u << r.shift) - 1u;
-      r = with_bins(hi - r.lo > below ? hi - below : r.lo, hi);
-      fill(r, weights, at);
-    }
-  }
-
-  // The slice's elements in range and above key `skip`, counted or weighed.
-  __device__ __forceinline__ void fill(const Range& r, bool weights, uint32_t skip) {
-    clear(weights ? 3 : 1);
-    uint32_t* h = bins();
-    each([&](uint32_t raw) {
-      const uint32_t key = L::key(raw);
-      if (key < r.lo || key > r.hi || key <= skip) return;
-      const int b = (int)((r.hi - key) >> r.shift);
-      if (weights)
-        add(h, b, weight(sh, c, L::value(key)));
-      else
-        atomicAdd(h + b, 1u);
-    });
-    cluster_sync();
-  }
-
-  // Counts of the bins of distance to the maximum; v: this thread's two.
-  __device__ __forceinline__ void count(unsigned long long* v) {
-    clear(1);
-    uint32_t* h = bins();
-    each([&](uint32_t raw) {
-      const int b = distance_bin(c, L::real(raw));
-      if (b < kZeroBin) atomicAdd(h + b, 1u);  // not a weightless or empty position (NaN)
-    });
-    cluster_sync();
-    gather(1, v);
-    ++level;
-  }
-
-  // The bound of the k largest; v: counts by distance, cut to them.
-  __device__ __forceinline__ Bound largest(unsigned long long* v, unsigned long long k) {
+  // The bound at which the count (target), or the weight as a share of the
+  // total, of what `keep` leaves is reached; `keep` if it is not.
+  __device__ __forceinline__ Bound search(bool weights, const Bound& keep, unsigned long long target, float share) {
+    const unsigned long long unit = weights && keep.key ? weight(sh, c, L::value(keep.key)) : 0;
+    const unsigned long long extra = unit * keep.ties;
+    const uint32_t near = min(L::from(c.near), most);
     unsigned long long above = 0;
-    const int b = find(v, above, k);
-    if (b < 0) return {0, 0};  // no more than k that weigh anything
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int i = 2 * threadIdx.x + j;
-      if (i > b) v[j] = 0;
-      if (i == b) v[j] = k - above;
+    Range r = with_bins(near, most);
+    bool first = weights, far = false;
+    for (;;) {
+      fill(r, weights, keep, first);
+      if (first) {
+        const int lane = threadIdx.x & 31;
+        const unsigned long long all = warp_sum(lane < split ? peer_u64(&sh.all[flip], lane) : 0) + extra;
+        const unsigned long long part = share_of(all, share, true);
+        target = part ? part : 1;
+        first = false;
+      }
+      const int b = find(r, weights, keep.key, extra, above, target);
+      if (b < 0) {
+        const uint32_t low = min(L::from(c.low), most);
+        if (far || low >= near) return keep;  // no more than that weighs anything
+        far = true;
+        r = with_bins(low, near - 1);
+        continue;
+      }
+      const uint32_t hi = r.hi - ((uint32_t)b << r.shift), below = (1u << r.shift) - 1u;
+      if (r.shift == 0) {
+        unsigned long long ties = target - above;
+        if (weights) {
+          const unsigned long long w = weight(sh, c, L::value(hi));
+          ties = (ties + w - 1) / w;
+          if (hi == keep.key && ties > keep.ties) ties = keep.ties;
+        }
+        return {hi, (uint32_t)min(ties, 0xFFFFFFFFull)};
+      }
+      far = true;  // the bound is in this bin
+      r = with_bins(hi - r.lo > below ? hi - below : r.lo, hi);
     }
-    const Range r = keys_of<DT>(c, b, b, most);
-    fill(r, false, 0);
-    const uint32_t key = narrow(r, false, 0, 0, above, k);
-    return {key, k - above};
   }
 
-  // The bound at which the weight of what `keep` leaves reaches a share of its
-  // total; v: its counts by distance.  A bin's weights differ by one part in 33,
-  // so the counts say in which few bins the bound lies; one pass then sums all
-  // weights exactly, those bins' by key.
-  __device__ __forceinline__ Bound heaviest(const unsigned long long* v, const Bound& keep, double share) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int i0 = 2 * threadIdx.x;
-    float hi[2], lo[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      hi[j] = (float)v[j] * exp2f(-(float)(i0 + j) / kBinsPerOctave);
-      lo[j] = (float)v[j] * exp2f(-(float)(i0 + j + 1) / kBinsPerOctave);
+  // Weight and ties of units [from, to), of which this warp's lanes take one
+  // after another; every lane gets them.
+  __device__ __forceinline__ void weigh(int from, int to, const Bound& keep, float low, unsigned long long& sum,
+                                        uint32_t& ties) const {
+    const float bound = bound_of(keep);
+    const int lane = threadIdx.x & 31;
+    sum = 0;
+    ties = 0;
+    if (keep.key) {
+      for (int u = from + lane; u < to; u += 32)
+        picked(u, [&](float l) { return l >= bound && l >= low; },
+               [&](uint32_t raw) {
+                 const float l = L::real(raw);
+                 if (l == bound)
+                   ++ties;
+                 else
+                   sum += weight(sh, c, l);
+               });
+    } else {
+      for (int u = from + lane; u < to; u += 32)
+        unit(slice[u], [&](uint32_t raw) {
+          const float l = L::real(raw);
+          if (l >= low) sum += weight(sh, c, l);
+        });
     }
-    float ph = hi[0] + hi[1], pl = lo[0] + lo[1];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const float a = __shfl_up_sync(0xffffffffu, ph, o), b = __shfl_up_sync(0xffffffffu, pl, o);
-      if (lane >= o) {
-        ph += a;
-        pl += b;
+    __syncwarp();
+    ties = __reduce_add_sync(0xffffffffu, ties);
+    sum = warp_sum(sum);
+  }
+
+  // The position in units [from, to), of this warp, at which the running weight
+  // passes `rest`; w: its weight.
+  __device__ __forceinline__ int draw(int from, int to, const Bound& keep, float low, unsigned long long unit_w,
+                                      unsigned long long rest, uint32_t allow, unsigned long long& w) const {
+    const float bound = bound_of(keep);
+    const int lane = threadIdx.x & 31;
+    for (int base = from; base < to; base += 32) {
+      unsigned long long sum = 0;
+      uint32_t ties = 0;
+      if (base + lane < to)
+        picked(base + lane, [&](float l) { return l >= bound && l >= low; },
+               [&](uint32_t raw) {
+                 const float l = L::real(raw);
+                 if (l == bound)
+                   ++ties;
+                 else
+                   sum += weight(sh, c, l);
+               });
+      __syncwarp();
+      const int hit = locate(sum, ties, unit_w, rest, allow);
+      if (hit >= 0) {  // the unit's positions side by side
+        sum = 0;
+        ties = 0;
+        if (lane < PU) {
+          const float l = L::real(raw_at((base + hit) * PU + lane));
+          if (l == bound)
+            ties = l >= low;
+          else if (l > bound && l >= low)
+            sum = weight(sh, c, l);
+        }
+        __syncwarp();
+        const int j = locate(sum, ties, unit_w, rest, allow);
+        w = __shfl_sync(0xffffffffu, ties ? unit_w : sum, j & 31);
+        return (base + hit) * PU + j;
       }
+      const uint32_t met = min(__reduce_add_sync(0xffffffffu, ties), allow);
+      rest -= warp_sum(sum) + met * unit_w;
+      allow -= met;
     }
-    if (lane == 31) {
-      sh.high[warp] = ph;
-      sh.low[warp] = pl;
-    }
-    if (threadIdx.x == 0) {
-      sh.cut = kBins - 1;
-      sh.cut2 = kBins - 1;
-    }
-    __syncthreads();
-    float th = 0.f, tl = 0.f;
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) {
-        ph += sh.high[w];
-        pl += sh.low[w];
-      }
-      th += sh.high[w];
-      tl += sh.low[w];
-    }
-    // 1.001: the sums' own roundings, and the bins' borders
-    const float least = (float)share * tl / 1.001f, most_w = (float)share * th * 1.001f;
-    if (ph >= least) atomicMin(&sh.cut, ph - hi[1] >= least ? i0 : i0 + 1);
-    if (pl >= most_w) atomicMin(&sh.cut2, pl - lo[1] >= most_w ? i0 : i0 + 1);
-    __syncthreads();
-    const int b1 = max(sh.cut - 1, 0), b2 = min(sh.cut2 + 1, kBins - 1);
-    const Range r = keys_of<DT>(c, b1, b2, most);
-    clear(3);
-    uint32_t* h = bins();
-    unsigned long long all = 0, over = 0;
-    each([&](uint32_t raw) {
-      const uint32_t key = L::key(raw);
-      if (key <= keep.key) return;
-      const unsigned long long w = weight(sh, c, L::value(key));
-      all += w;
-      if (key > r.hi)
-        over += w;
-      else if (key >= r.lo && w)
-        add(h, (int)((r.hi - key) >> r.shift), w);
-    });
-    all = warp_sum(all);
-    over = warp_sum(over);
-    if (lane == 0) {
-      sh.sums[flip][0][warp] = all;
-      sh.sums[flip][1][warp] = over;
-    }
-    cluster_sync();
-    const unsigned long long unit = keep.key ? weight(sh, c, L::value(keep.key)) : 0, extra = unit * keep.ties;
-    all = over = 0;
-    for (int i = lane; i < split * kWarps; i += 32) {
-      all += peer_u64(&sh.sums[flip][0][i % kWarps], i / kWarps);
-      over += peer_u64(&sh.sums[flip][1][i % kWarps], i / kWarps);
-    }
-    all = warp_sum(all) + extra;
-    over = warp_sum(over) + (keep.key > r.hi ? extra : 0);
-    const double t = ceil(share * (double)all);
-    const unsigned long long target = t < 1.0 ? 1ull : (unsigned long long)t;
-    const uint32_t key = narrow(r, true, keep.key, extra, over, target);
-    if (key == 0) return keep;
-    const unsigned long long w = weight(sh, c, L::value(key));
-    unsigned long long ties = (target - over + w - 1) / w;
-    if (key == keep.key && ties > keep.ties) ties = keep.ties;
-    return {key, ties};
+    return from * PU;  // not reached: the range holds it
   }
 };
 
@@ -539,9 +634,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   const int rank = (int)(blockIdx.x % (unsigned)split);
   const long long V = a.first[a.n];
   const long long lo = V * rank / split, hi = V * (rank + 1) / split;
-  if (tid < 128) sh.power[tid] = kTable.p[tid];
+  bool fresh = true;
   int level = 0, flip = 0;
   for (size_t row = blockIdx.x / (unsigned)split; row < a.rows; row += gridDim.x / (unsigned)split, flip ^= 1) {
+    const float temperature = a.temperature ? a.temperature[row] : 1.f;
+    const int k = a.top_k ? a.top_k[row] : 0;
+    const float share = a.top_p ? a.top_p[row] : 1.f, least = a.min_p ? a.min_p[row] : 0.f;
+    const float uniform = a.uniform[row];
     // the slice as it lies in memory, unit by unit, shard after shard
     __syncthreads();
     typename L::Most most;
@@ -554,33 +653,44 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       const int skip = (int)((uintptr_t)p & 15) / ES, len = (int)(to - from);
       const int n = (skip + len + PU - 1) / PU;
       const uint4* src = reinterpret_cast<const uint4*>(p - skip * ES);
-#pragma unroll 4
-      for (int u = tid; u < n; u += kThreads) {
-        const uint4 x = ld_stream(src + u);
-        if (u > 0 && u < n - 1) {
-          most.add(x);
-          slice[units + u] = x;
-        } else {
-          const int from = u == 0 ? skip : 0, to = min(skip + len - u * PU, PU);
-          most.add(only<DT>(x, from, to, L::kMinusInf));
-          slice[units + u] = only<DT>(x, from, to, L::kNone);
+      for (int u0 = tid; u0 < n; u0 += kBatch * kThreads) {
+        uint4 x[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+          if (u0 + j * kThreads < n) x[j] = ld_stream(src + u0 + j * kThreads);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          const int u = u0 + j * kThreads;
+          if (u >= n) break;
+          if (u > 0 && u < n - 1) {
+            most.add(x[j]);
+            slice[units + u] = x[j];
+          } else {
+            const int begin = u == 0 ? skip : 0, end = min(skip + len - u * PU, PU);
+            most.add(only<DT>(x[j], begin, end, L::kMinusInf));
+            slice[units + u] = only<DT>(x[j], begin, end, L::kNone);
+          }
         }
       }
       if (tid == 0) sh.seg[nseg] = {units * PU + skip, units * PU + skip + len, from};
       ++nseg;
       units += n;
     }
+    if (fresh) {  // behind the first loads
+      for (int i = tid; i < kPowers * kCopies; i += kThreads) sh.power[i] = kTable.p[i / kCopies];
+      fresh = false;
+    }
     uint32_t top = __reduce_max_sync(0xffffffffu, most.top());
     if (lane == 0) sh.wmax[warp] = top;
     if (tid == 0) sh.first[flip] = INT_MAX;
     __syncthreads();
-    top = __reduce_max_sync(0xffffffffu, sh.wmax[lane % kWarps]);
-    if (tid == 0) sh.top[flip] = top;
+    if (warp == 0) {
+      top = __reduce_max_sync(0xffffffffu, sh.wmax[lane % kWarps]);
+      if (lane == 0) sh.top[flip] = top;
+    }
     cluster_sync();
     top = __reduce_max_sync(0xffffffffu, lane < split ? peer_u32(&sh.top[flip], lane) : 0u);
 
-    const float temperature = a.temperature ? a.temperature[row] : 1.f;
-    const int k = a.top_k ? a.top_k[row] : 0;
     if (top == L::kNan || top <= L::key(L::kMinusInf) || !(temperature >= 0.f)) {
       // a NaN, or nothing but -infinity
       if (rank == 0 && tid == 0) {
@@ -593,19 +703,20 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     }
     Row<DT> r{slice, units, hist, sh, {}, top, split, flip, level};
     if (temperature == 0.f || k == 1) {
+      const float most_l = L::value(top);
       int at = INT_MAX;
       for (int u = tid; u < units && at == INT_MAX; u += kThreads) {
         int j = 0;
         r.unit(slice[u], [&](uint32_t raw) {
-          if (L::key(raw) == top && at == INT_MAX) at = u * PU + j;
+          if (L::real(raw) == most_l && at == INT_MAX) at = u * PU + j;
           ++j;
         });
       }
       at = __reduce_min_sync(0xffffffffu, at);
-      if (lane == 0) atomicMin(&sh.first[flip], at);
+      if (lane == 0 && at != INT_MAX) atomicMin(&sh.first[flip], at);
       cluster_sync();
-      int owner = 0;
-      while (owner < split && (int)peer_u32(&sh.first[flip], owner) == INT_MAX) ++owner;
+      const int mine = lane < split ? (int)peer_u32(&sh.first[flip], lane) : INT_MAX;
+      const int owner = __ffs(__ballot_sync(0xffffffffu, mine != INT_MAX)) - 1;
       if (rank == owner && tid == 0) {
         at = sh.first[flip];
         int g = 0;
@@ -616,138 +727,90 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       continue;
     }
 
-    r.c.top = L::value(top);
-    const double scale = fmin(1.4426950408889634 / (double)temperature, 1e30);
-    r.c.hi = (float)scale;
-    r.c.lo = (float)(scale - (double)r.c.hi);
-    r.c.bins = r.c.hi * kBinsPerOctave;
+    r.c = make_scale(L::value(top), temperature);
     Bound keep{0, 0};
-    const float share = a.top_p ? a.top_p[row] : 1.f;
-    if ((k > 0 && k < V) || share < 1.f) {
-      unsigned long long v[2];
-      r.count(v);
-      if (k > 0 && k < V) keep = r.largest(v, (unsigned long long)k);
-      if (share < 1.f) keep = r.heaviest(v, keep, (double)fmaxf(share, 0.f));
-    }
-    const float least = a.min_p ? a.min_p[row] : 0.f;
-    const unsigned long long floor_w =
-        (unsigned long long)ceil((double)fminf(fmaxf(least, 0.f), 1.f) * (double)(1ull << kUnitBits));
+    if (k > 0 && k < V) keep = r.search(false, keep, (unsigned long long)k, 0.f);
+    if (share < 1.f) keep = r.search(true, keep, 0, fmaxf(share, 0.f));
     unsigned long long tie_w = keep.key ? weight(sh, r.c, L::value(keep.key)) : 0;
-    if (tie_w < floor_w) tie_w = 0;
-
-    // weight of each warp's positions, in the order of the vocabulary
-    const int per = (units + kThreads - 1) / kThreads * 32;
-    const int u0 = min(warp * per, units), u1 = min(u0 + per, units);
-    const auto kept = [&](uint32_t key) -> unsigned long long {
-      if (key <= keep.key) return 0;
-      const unsigned long long w = weight(sh, r.c, L::value(key));
-      return w < floor_w ? 0 : w;
-    };
-    unsigned long long sum = 0;
-    uint32_t ties = 0;
-    for (int u = u0 + lane; u < u1; u += 32)
-      r.unit(slice[u], [&](uint32_t raw) {
-        const uint32_t key = L::key(raw);
-        sum += kept(key);
-        ties += key == keep.key;
-      });
-    sum = warp_sum(sum);
-    ties = __reduce_add_sync(0xffffffffu, ties);
-    if (lane == 0) {
-      sh.above[flip][warp] = sum;
-      sh.ties[flip][warp] = keep.key ? ties : 0;
+    float low = r.c.low;
+    if (least > 0.f) {  // the smallest logit that weighs as much
+      const unsigned long long floor_w =
+          min(__float2ull_ru(fminf(least, 1.f) * (float)(1ull << kUnitBits)), weight(sh, r.c, r.c.top));
+      const uint32_t key = first_key(min(L::from(r.c.low), top), top,
+                                     [&](uint32_t q) { return weight(sh, r.c, L::value(q)) >= floor_w; });
+      low = fmaxf(low, L::value(key));
+      if (tie_w < floor_w) tie_w = 0;
     }
-    cluster_sync();
-    constexpr int kEach = kMaxSplit * kWarps / 32;  // entries of a lane, in order
-    if (tid < kMaxSplit * kWarps) {
-      const int q = tid / kWarps, w = tid % kWarps;
-      sh.all_above[tid] = q < split ? peer_u64(&sh.above[flip][w], q) : 0;
-      sh.all_ties[tid] = q < split ? peer_u32(&sh.ties[flip][w], q) : 0;
+
+    // weight of each warp's positions, in the order of the vocabulary, of the
+    // CTA's, and of the row
+    const int per = (units + kThreads - 1) / kThreads * 32;
+    int u0 = min(warp * per, units), u1 = min(u0 + per, units);
+    unsigned long long sum;
+    uint32_t ties;
+    r.weigh(u0, u1, keep, low, sum, ties);
+    if (lane == 0) {
+      sh.warp_above[0][warp] = sum;
+      sh.warp_ties[0][warp] = ties;
     }
     __syncthreads();
-    // the ties each warp of the cluster keeps, and where the draw falls
-    unsigned long long n = 0, mass[kEach], left[kEach];
-#pragma unroll
-    for (int j = 0; j < kEach; ++j) n += sh.all_ties[lane * kEach + j];
-    unsigned long long seen = prefix(n) - n, mine = 0;
-#pragma unroll
-    for (int j = 0; j < kEach; ++j) {
-      const unsigned long long t = sh.all_ties[lane * kEach + j];
-      left[j] = keep.ties > seen ? keep.ties - seen : 0;
-      mass[j] = sh.all_above[lane * kEach + j] + min(t, left[j]) * tie_w;
-      seen += t;
-      mine += mass[j];
-    }
-    unsigned long long at = prefix(mine);
-    const unsigned long long total = __shfl_sync(0xffffffffu, at, 31);
-    at -= mine;
-    const double u01 = fmin(fmax((double)a.uniform[row], 0.0), 1.0);
-    unsigned long long target = (unsigned long long)(u01 * (double)total);  // sum > u total, as integers
-    if (target >= total) target = total - 1;
-    int owner = -1;
-    unsigned long long rest = 0, allow = 0;
-#pragma unroll
-    for (int j = 0; j < kEach; ++j) {
-      if (at <= target && at + mass[j] > target) {
-        owner = lane * kEach + j;
-        rest = target - at;
-        allow = left[j];
+    if (warp == 0) {
+      sum = warp_sum(lane < kWarps ? sh.warp_above[0][lane] : 0);
+      ties = __reduce_add_sync(0xffffffffu, lane < kWarps ? sh.warp_ties[0][lane] : 0);
+      if (lane == 0) {
+        sh.above[flip] = sum;
+        sh.ties[flip] = ties;
       }
-      at += mass[j];
     }
-    const int from = __ffs(__ballot_sync(0xffffffffu, owner >= 0)) - 1;
-    owner = __shfl_sync(0xffffffffu, owner, from);
-    rest = __shfl_sync(0xffffffffu, rest, from);
-    allow = __shfl_sync(0xffffffffu, allow, from);
-    if (owner == rank * kWarps + warp) {
-      unsigned long long run = 0;
-      for (int base = u0; base < u1; base += 32) {
-        const int u = base + lane;
-        const uint4 x = u < u1 ? slice[u] : make_uint4(~0u, ~0u, ~0u, ~0u);  // no position
-        uint32_t met = 0;
-        unsigned long long w = 0;
-        r.unit(x, [&](uint32_t raw) {
-          const uint32_t key = L::key(raw);
-          w += kept(key);
-          met += keep.key && key == keep.key;
-        });
-        const unsigned long long before = prefix(met) - met;  // ties of the lanes before
-        const unsigned long long mine_left = allow > before ? allow - before : 0;
-        w += min((unsigned long long)met, mine_left) * tie_w;
-        const unsigned long long upto = prefix(w);
-        const uint32_t hit = __ballot_sync(0xffffffffu, run + upto > rest);
-        if (hit) {
-          if (lane == __ffs(hit) - 1) {
-            unsigned long long sofar = run + upto - w, ties_left = mine_left;
-            int j = 0, found = -1;
-            unsigned long long fw = 0;
-            r.unit(x, [&](uint32_t raw) {
-              const uint32_t key = L::key(raw);
-              unsigned long long q = kept(key);
-              if (keep.key && key == keep.key && ties_left) {
-                --ties_left;
-                q = tie_w;
-              }
-              sofar += q;
-              if (found < 0 && sofar > rest) {
-                found = u * PU + j;
-                fw = q;
-              }
-              ++j;
-            });
-            int g = 0;
-            while (found >= sh.seg[g].end) ++g;
-            a.token[row] = sh.seg[g].index + (found - sh.seg[g].pos);
-            if (a.logprob) {
-              const float t = (float)total;
-              a.logprob[row] = 2 * fw > total ? log1pf(-(float)(total - fw) / t) : logf((float)fw / t);
-            }
+    cluster_sync();
+    if (warp == 0) {
+      // sum > uniform * total, as integers
+      const unsigned long long w = lane < split ? peer_u64(&sh.above[flip], lane) : 0;
+      const uint32_t t = lane < split ? peer_u32(&sh.ties[flip], lane) : 0;
+      const uint32_t n = __reduce_add_sync(0xffffffffu, t);
+      const unsigned long long total = warp_sum(w) + min(n, keep.ties) * tie_w;
+      unsigned long long rest = share_of(total, fminf(fmaxf(uniform, 0.f), 1.f), false);
+      if (rest >= total) rest = total - 1;
+      uint32_t allow = keep.ties;
+      const int owner = locate(w, t, tie_w, rest, allow);
+      if (lane == 0) {
+        sh.cut = owner;
+        sh.before = rest;
+        sh.allow = allow;
+        sh.scan[0] = total;
+      }
+    }
+    __syncthreads();
+    if (sh.cut == rank) {  // it falls in this CTA: in which warp's part, and in which sixteenth of that
+      unsigned long long rest = sh.before;
+      const unsigned long long total = sh.scan[0];
+      uint32_t allow = sh.allow;
+      const int w0 = locate(lane < kWarps ? sh.warp_above[0][lane] : 0, lane < kWarps ? sh.warp_ties[0][lane] : 0,
+                            tie_w, rest, allow);
+      u0 = min(w0 * per, units);
+      u1 = min(u0 + per, units);
+      const int part = (u1 - u0 + kWarps - 1) / kWarps;
+      const int v0 = min(u0 + warp * part, u1), v1 = min(v0 + part, u1);
+      r.weigh(v0, v1, keep, low, sum, ties);
+      if (lane == 0) {
+        sh.warp_above[1][warp] = sum;
+        sh.warp_ties[1][warp] = ties;
+      }
+      __syncthreads();
+      const int w1 = locate(lane < kWarps ? sh.warp_above[1][lane] : 0, lane < kWarps ? sh.warp_ties[1][lane] : 0,
+                            tie_w, rest, allow);
+      if (warp == w1) {
+        unsigned long long w;
+        const int at = r.draw(v0, v1, keep, low, tie_w, rest, allow, w);
+        if (lane == 0) {
+          int g = 0;
+          while (at >= sh.seg[g].end) ++g;
+          a.token[row] = sh.seg[g].index + (at - sh.seg[g].pos);
+          if (a.logprob) {
+            const float t = (float)total;
+            a.logprob[row] = 2 * w > total ? log1pf(-(float)(total - w) / t) : logf((float)w / t);
           }
-          break;
         }
-        run += __shfl_sync(0xffffffffu, upto, 31);
-        const uint32_t all_met = __reduce_add_sync(0xffffffffu, met);
-        allow = allow > all_met ? allow - all_met : 0;
       }
     }
   }
@@ -772,8 +835,10 @@ cudaError_t sample_go(const SampleArgs& a, cudaStream_t s, int* grid_out) {
   const size_t smem = 6 * kBins * 4 + (slice(split) + 15) / 16 * 16;
   const cudaError_t attr = raise_smem<kern>(6 * kBins * 4 + kMostSlice + 1024);
   if (attr != cudaSuccess) return attr;
+  // a cluster a row: rows differ in their work (greedy ones have next to none),
+  // and those that end early make room
   size_t clusters = a.rows;
-  const size_t most = (size_t)std::max(1, (max_ctas_cap() > 0 ? sms : 2 * sms) / split);
+  const size_t most = (size_t)std::max(1, max_ctas_cap() > 0 ? sms / split : INT_MAX / kMaxSplit);
   if (clusters > most) clusters = most;
   *grid_out = (int)clusters * split;
   cudaLaunchConfig_t cfg{};
