@@ -7,11 +7,11 @@
 //   sum_{j <= i, kept} w_j > uniform * sum_{kept} w_j
 //
 // No sort: the bounds of top-k and top-p are found as the logit at which a
-// count or a weight is reached, by histograms of up to 1024 bins over the
+// count or a weight is reached, by counting elements in up to 1024 bins over the
 // logits' bits as ordered integers: of the nearest 16 octaves of weight first
 // (only if the bound is not there, of the others: most logits are far down and
-// are then not added to a bin), then of ever narrower ranges, until a bin is one
-// value; equal logits at the bound are taken by index.
+// are then not counted), then of ever narrower ranges, until a bin is one value;
+// equal logits at the bound are taken by index.
 //
 // Weights are integers in units of 2^-44 of the largest, exact sums of which
 // depend on no order, so that rows give the same token however many CTAs share
@@ -80,9 +80,9 @@ struct Shared {
   // by parity of the row, read by the cluster
   uint32_t top[2];              // the slice's largest key, all ones if it holds a NaN
   int first[2];                 // position of the first logit equal to the row's maximum
-  unsigned long long all[2];    // weight of what is kept when the search by weight begins
   unsigned long long above[2];  // weight of what is kept in the end, without the bound's ties
   uint32_t ties[2];
+  unsigned long long all[2];    // by parity of the histogram: a weight summed beside it
   // of this CTA
   unsigned long long warp_above[2][kWarps];
   uint32_t warp_ties[2][kWarps];
@@ -379,73 +379,87 @@ struct Row {
     }
   }
 
-  static __device__ __forceinline__ void add(uint32_t* h, int b, unsigned long long w) {
-    // pieces of 15 bits, whose sums of up to 2^17 elements fit a word
-    atomicAdd(h + b, (uint32_t)w & 0x7FFFu);
-    if (w >> 15) atomicAdd(h + kBins + b, (uint32_t)(w >> 15) & 0x7FFFu);
-    if (w >> 30) atomicAdd(h + 2 * kBins + b, (uint32_t)(w >> 30));
-  }
-
-  // The slice's elements in range and above `keep`'s key into the range's bins,
-  // counted or weighed, and published to the cluster.  all: also sums the
-  // weight of everything above that key.
-  __device__ __forceinline__ void fill(const Range& r, bool weights, const Bound& keep, bool all) {
-    const int n = r.bins(), tid = threadIdx.x;
-    uint32_t* h = bins();
-    for (int i = tid; i < (n + 3) / 4; i += kThreads)
-      for (int k = 0; k < (weights ? 3 : 1); ++k)
-        reinterpret_cast<uint4*>(h + k * kBins)[i] = make_uint4(0, 0, 0, 0);
-    __syncthreads();
-    const float bound = bound_of(keep), low = fmaxf(L::value(r.lo), c.low), high = L::value(r.hi);
-    const auto in = [&](float l) { return l >= low && l <= high && l > bound; };  // no position (NaN): false
-    const auto put = [&](uint32_t raw) {
-      const int b = (int)((r.hi - L::key(raw)) >> r.shift);
-      if (weights)
-        add(h, b, weight(sh, c, L::real(raw)));
-      else
-        atomicAdd(h + b, 1u);
-    };
-    if (!all) {
-      for (int u = tid; u < units; u += kThreads) picked(u, in, put);
-      cluster_sync();
-      return;
-    }
+  // The warp's sum of w over the positions of units [from, to) that `is` picks:
+  // unit by unit, one at a time a lane where they are few, all of a unit's
+  // positions side by side where they are many.
+  template <class Is, class W>
+  __device__ __forceinline__ unsigned long long sum_of(int from, int to, int step, Is is, W w) const {
     unsigned long long sum = 0;
-    if (keep.key) {  // few are kept
-      for (int u = tid; u < units; u += kThreads)
-        picked(u, [&](float l) { return l > bound && l >= c.low; },
-               [&](uint32_t raw) {
-                 const float l = L::real(raw);
-                 const unsigned long long w = weight(sh, c, l);
-                 sum += w;
-                 if (l >= low && l <= high) add(h, (int)((r.hi - L::key(raw)) >> r.shift), w);
-               });
-    } else {
-      for (int u = tid; u < units; u += kThreads) {
-        unit(slice[u], [&](uint32_t raw) {
-          const float l = L::real(raw);
-          if (l >= c.low) sum += weight(sh, c, l);
+    for (int base = from; base < to; base += step) {
+      const int u = base + (int)(threadIdx.x & 31);
+      uint4 x = make_uint4(~0u, ~0u, ~0u, ~0u);  // no position
+      if (u < to) x = slice[u];
+      uint32_t mask = 0;
+      int j = 0;
+      unit(x, [&](uint32_t raw) { mask |= (is(L::real(raw)) ? 1u : 0u) << j++; });
+      if (__any_sync(0xffffffffu, __popc(mask) > PU / 2)) {
+        j = 0;
+        unit(x, [&](uint32_t raw) {
+          if (mask >> j++ & 1) sum += w(L::real(raw));
         });
-        picked(u, in, put);
+      } else {
+        while (mask) {
+          sum += w(L::real(raw_at(u * PU + __ffs(mask) - 1)));
+          mask &= mask - 1;
+        }
+        __syncwarp();
       }
     }
-    __syncwarp();
-    sum = warp_sum(sum);
-    if ((tid & 31) == 0) sh.scan[tid >> 5] = sum;
-    __syncthreads();
-    if (tid < 32) {
-      sum = warp_sum(tid < kWarps ? sh.scan[tid] : 0);
-      if (tid == 0) sh.all[flip] = sum;
-    }
-    cluster_sync();
+    return warp_sum(sum);
   }
 
-  // The cluster's sum of bins b and b + 1.
-  __device__ __forceinline__ void gather(int b, bool weights, unsigned long long* v) const {
+  // Clears the bins of a range.
+  __device__ __forceinline__ void clear(const Range& r, int words) const {
+    uint4* h = reinterpret_cast<uint4*>(bins());
+    for (int k = 0; k < words; ++k)
+      for (int i = threadIdx.x; i < (r.bins() + 3) / 4; i += kThreads) h[k * (kBins / 4) + i] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+  }
+
+  // The slice's elements in range and above `keep`'s key, counted by bins, or
+  // their weights added (words == 3: pieces of 15 bits, whose sums of up to 2^17
+  // elements fit a word).
+  __device__ __forceinline__ void fill(const Range& r, const Bound& keep, int words) const {
+    uint32_t* h = bins();
+    const float bound = bound_of(keep), low = fmaxf(L::value(r.lo), c.low), high = L::value(r.hi);
+    for (int u = threadIdx.x; u < units; u += kThreads)
+      picked(u, [&](float l) { return l >= low && l <= high && l > bound; },  // no position (NaN): false
+             [&](uint32_t raw) {
+               uint32_t* at = h + ((r.hi - L::key(raw)) >> r.shift);
+               if (words == 1) {
+                 atomicAdd(at, 1u);
+                 return;
+               }
+               const unsigned long long w = weight(sh, c, L::real(raw));
+               atomicAdd(at, (uint32_t)w & 0x7FFFu);
+               if (w >> 15) atomicAdd(at + kBins, (uint32_t)(w >> 15) & 0x7FFFu);
+               if (w >> 30) atomicAdd(at + 2 * kBins, (uint32_t)(w >> 30));
+             });
+    __syncwarp();
+  }
+
+  // The CTA's sum of the warps' `sum`, published to the cluster with the bins;
+  // then the cluster's.
+  __device__ __forceinline__ unsigned long long publish(unsigned long long sum) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (lane == 0) sh.scan[warp] = sum;
+    __syncthreads();
+    if (warp == 0) {
+      sum = warp_sum(lane < kWarps ? sh.scan[lane] : 0);
+      if (lane == 0) sh.all[level & 1] = sum;
+    }
+    cluster_sync();
+    return warp_sum(lane < split ? peer_u64(&sh.all[level & 1], lane) : 0);
+  }
+
+  // The cluster's sums of this thread's bins 2 tid and 2 tid + 1 of a range.
+  __device__ __forceinline__ void gather(const Range& r, int words, unsigned long long* v) const {
+    const int n = r.bins(), b = 2 * threadIdx.x;
+    v[0] = v[1] = 0;
+    if (b >= n) return;
 #pragma unroll 1
-    for (int k = 0; k < (weights ? 3 : 1); ++k) {
-      // every CTA's words in flight before the first is used
-      unsigned long long x[kMaxSplit];
+    for (int k = 0; k < words; ++k) {
+      unsigned long long x[kMaxSplit];  // every CTA's words in flight before the first is used
 #pragma unroll
       for (int q = 0; q < kMaxSplit; ++q) x[q] = q < split ? peer_u64(bins() + k * kBins + b, q) : 0;
 #pragma unroll
@@ -454,98 +468,125 @@ struct Row {
         v[1] += (x[q] >> 32) << (15 * k);
       }
     }
+    if (b + 1 >= n) v[1] = 0;  // not of the range
   }
 
-  // Of a range's bins, the one in which the running sum (from `above` on)
-  // reaches `target`, -1 if none; above: the sum before it (all of it).
-  // `extra`, if not 0, belongs to key `at` too.
-  __device__ __forceinline__ int find(const Range& r, bool weights, uint32_t at, unsigned long long extra,
-                                      unsigned long long& above, unsigned long long target) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = 2 * threadIdx.x;
-    const int n = r.bins();
-    const bool one = n <= 64;  // the first warp alone
-    unsigned long long v[2] = {0, 0};
-    if (b < n) gather(b, weights, v);
-    if (b + 1 >= n) v[1] = 0;  // not of the range
-    if (extra && at >= r.lo && at <= r.hi) {
-      const int d = (int)((r.hi - at) >> r.shift) - b;
-      if (d == 0) v[0] += extra;
-      if (d == 1) v[1] += extra;
-    }
-    unsigned long long end = above;
-    if (!one) {
-      const unsigned long long sum = prefix(v[0] + v[1]);
-      if (lane == 31) sh.scan[warp] = sum;
-      if (threadIdx.x == 0) sh.cut = -1;
+  // Of a range's bins, two a thread, the one in which the running sum from
+  // `above` on reaches `target` (bins() if none); above: the sum before it (all
+  // of it).  Up to 64 bins are the first warp's alone.
+  __device__ __forceinline__ int reach(const Range& r, const unsigned long long* v, unsigned long long& above,
+                                       unsigned long long target) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = 2 * threadIdx.x, n = r.bins();
+    unsigned long long end = above + prefix(v[0] + v[1]);
+    if (n > 64) {
+      if (lane == 31) sh.scan[warp] = end - above;
       __syncthreads();
       const unsigned long long upto = prefix(lane < kWarps ? sh.scan[lane] : 0);
       const unsigned long long before = __shfl_sync(0xffffffffu, upto, warp ? warp - 1 : 0);
-      end += sum + (warp ? before : 0);
-      above += __shfl_sync(0xffffffffu, upto, 31);
-    } else if (warp == 0) {
-      end += prefix(v[0] + v[1]);
-      if (lane == 31) {
-        sh.cut = -1;
-        sh.before = end;
-      }
-      __syncwarp();
+      if (warp) end += before;
     }
-    if (!one || warp == 0) {
+    if (n > 64 || warp == 0) {
       const unsigned long long begin1 = end - v[1], begin0 = begin1 - v[0];
+      const bool last = threadIdx.x == (n > 64 ? kThreads : 32) - 1;
       if (begin0 < target && begin1 >= target) {
         sh.cut = b;
         sh.before = begin0;
       } else if (begin1 < target && end >= target) {
         sh.cut = b + 1;
         sh.before = begin1;
+      } else if (last && end < target) {
+        sh.cut = n;
+        sh.before = end;
       }
     }
     ++level;
     __syncthreads();
+    above = sh.before;
     const int cut = sh.cut;
-    if (cut >= 0 || one) above = sh.before;
-    __syncthreads();  // sh.cut and sh.scan may be set again
+    __syncthreads();  // they may be set again
     return cut;
   }
 
-  // The bound at which the count (target), or the weight as a share of the
-  // total, of what `keep` leaves is reached; `keep` if it is not.
-  __device__ __forceinline__ Bound search(bool weights, const Bound& keep, unsigned long long target, float share) {
-    const unsigned long long unit = weights && keep.key ? weight(sh, c, L::value(keep.key)) : 0;
-    const unsigned long long extra = unit * keep.ties;
-    const uint32_t near = min(L::from(c.near), most);
-    unsigned long long above = 0;
+  __device__ __forceinline__ Range bin_keys(const Range& r, int b) const {
+    const uint32_t hi = r.hi - ((uint32_t)b << r.shift), below = (1u << r.shift) - 1u;
+    return with_bins(hi - r.lo > below ? hi - below : r.lo, hi);
+  }
+
+  // The keys searched first: the nearest octaves, of bfloat16 as many of them as
+  // leave each key a bin of its own.
+  __device__ __forceinline__ uint32_t near_key() const {
+    const uint32_t k = min(L::from(c.near), most);
+    return DT == RRA_BFLOAT16 && most - k >= kBins ? most - (kBins - 1) : k;
+  }
+
+  // The bound of the k largest; none if no more than that weigh anything.
+  __device__ __forceinline__ Bound largest(unsigned long long k) {
+    const uint32_t near = near_key(), low = min(L::from(c.low), most);
+    unsigned long long above = 0, v[2];
     Range r = with_bins(near, most);
-    bool first = weights, far = false;
-    for (;;) {
-      fill(r, weights, keep, first);
-      if (first) {
-        const int lane = threadIdx.x & 31;
-        const unsigned long long all = warp_sum(lane < split ? peer_u64(&sh.all[flip], lane) : 0) + extra;
-        const unsigned long long part = share_of(all, share, true);
-        target = part ? part : 1;
-        first = false;
-      }
-      const int b = find(r, weights, keep.key, extra, above, target);
-      if (b < 0) {
-        const uint32_t low = min(L::from(c.low), most);
-        if (far || low >= near) return keep;  // no more than that weighs anything
-        far = true;
+    for (bool wide = low < near;;) {
+      clear(r, 1);
+      fill(r, {0, 0}, 1);
+      cluster_sync();
+      gather(r, 1, v);
+      const int b = reach(r, v, above, k);
+      if (b < r.bins()) {
+        if (r.shift == 0) return {r.hi - (uint32_t)b, (uint32_t)(k - above)};
+        r = bin_keys(r, b);
+      } else {
+        if (!wide) return {0, 0};
         r = with_bins(low, near - 1);
-        continue;
       }
-      const uint32_t hi = r.hi - ((uint32_t)b << r.shift), below = (1u << r.shift) - 1u;
-      if (r.shift == 0) {
-        unsigned long long ties = target - above;
-        if (weights) {
-          const unsigned long long w = weight(sh, c, L::value(hi));
-          ties = (ties + w - 1) / w;
-          if (hi == keep.key && ties > keep.ties) ties = keep.ties;
+      wide = false;
+    }
+  }
+
+  // The bound at which the weight of what `keep` leaves reaches a share of its
+  // total.  Where a bin is one key, elements are counted and the key's weight
+  // multiplied; else their weights are added.
+  __device__ __forceinline__ Bound heaviest(const Bound& keep, float share) {
+    const uint32_t near = near_key(), low = min(L::from(c.low), most);
+    const unsigned long long extra = keep.key ? weight(sh, c, L::value(keep.key)) * keep.ties : 0;
+    const float bound = bound_of(keep);
+    unsigned long long above = 0, target = 0, v[2];
+    Range r = with_bins(near, most);
+    for (bool first = true, wide = low < near;; first = false) {
+      const int words = r.shift ? 3 : 1;
+      clear(r, words);
+      fill(r, keep, words);
+      if (first) {
+        const unsigned long long all = publish(sum_of(
+            (threadIdx.x >> 5) * 32, units, kThreads, [&](float l) { return l > bound && l >= c.low; },
+            [&](float l) { return weight(sh, c, l); }));
+        const unsigned long long part = share_of(all + extra, share, true);
+        target = part ? part : 1;
+      } else {
+        cluster_sync();
+      }
+      gather(r, words, v);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int b = 2 * (int)threadIdx.x + j;
+        if (b >= r.bins()) break;
+        const Range q = bin_keys(r, b);
+        if (r.shift == 0 && v[j]) v[j] *= weight(sh, c, L::value(q.hi));
+        if (extra && keep.key >= q.lo && keep.key <= q.hi) v[j] += extra;
+      }
+      const int b = reach(r, v, above, target);
+      if (b < r.bins()) {
+        if (r.shift == 0) {
+          const uint32_t key = r.hi - (uint32_t)b;
+          const unsigned long long each = weight(sh, c, L::value(key));
+          unsigned long long ties = (target - above + each - 1) / each;
+          if (key == keep.key && ties > keep.ties) ties = keep.ties;
+          return {key, (uint32_t)min(ties, 0xFFFFFFFFull)};
         }
-        return {hi, (uint32_t)min(ties, 0xFFFFFFFFull)};
+        r = bin_keys(r, b);
+      } else {
+        if (!wide) return keep;  // all of it
+        r = with_bins(low, near - 1);
       }
-      far = true;  // the bound is in this bin
-      r = with_bins(hi - r.lo > below ? hi - below : r.lo, hi);
+      wide = false;
     }
   }
 
@@ -554,29 +595,14 @@ struct Row {
   __device__ __forceinline__ void weigh(int from, int to, const Bound& keep, float low, unsigned long long& sum,
                                         uint32_t& ties) const {
     const float bound = bound_of(keep);
-    const int lane = threadIdx.x & 31;
-    sum = 0;
     ties = 0;
-    if (keep.key) {
-      for (int u = from + lane; u < to; u += 32)
-        picked(u, [&](float l) { return l >= bound && l >= low; },
-               [&](uint32_t raw) {
-                 const float l = L::real(raw);
-                 if (l == bound)
-                   ++ties;
-                 else
-                   sum += weight(sh, c, l);
-               });
-    } else {
-      for (int u = from + lane; u < to; u += 32)
-        unit(slice[u], [&](uint32_t raw) {
-          const float l = L::real(raw);
-          if (l >= low) sum += weight(sh, c, l);
-        });
-    }
-    __syncwarp();
+    sum = sum_of(from, to, 32,
+                 [&](float l) {
+                   ties += l == bound && l >= low;
+                   return l > bound && l >= low;
+                 },
+                 [&](float l) { return weight(sh, c, l); });
     ties = __reduce_add_sync(0xffffffffu, ties);
-    sum = warp_sum(sum);
   }
 
   // The position in units [from, to), of this warp, at which the running weight
@@ -729,8 +755,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 
     r.c = make_scale(L::value(top), temperature);
     Bound keep{0, 0};
-    if (k > 0 && k < V) keep = r.search(false, keep, (unsigned long long)k, 0.f);
-    if (share < 1.f) keep = r.search(true, keep, 0, fmaxf(share, 0.f));
+    if (k > 0 && k < V) keep = r.largest((unsigned long long)k);
+    if (share < 1.f) keep = r.heaviest(keep, fmaxf(share, 0.f));
     unsigned long long tie_w = keep.key ? weight(sh, r.c, L::value(keep.key)) : 0;
     float low = r.c.low;
     if (least > 0.f) {  // the smallest logit that weighs as much
