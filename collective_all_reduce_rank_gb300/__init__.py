@@ -18,6 +18,8 @@ import os
 import re
 import struct
 import threading
+from itertools import chain
+from operator import attrgetter
 
 from . import build as _build
 
@@ -570,23 +572,25 @@ def rra_vocab_loss_backward(x, weights, targets, lse, grad_loss, dx, dweights, i
 
 # -- the serving step around a tensor-parallel all-reduce ---------------------
 #
-# An MX4 matrix is a pair (codes, scales) of uint8 tensors: codes of shape
-# [rows, 16 * ceil(cols / 32)], scales of rra_mx4_scale_bytes(rows, cols)
-# bytes.
+# An MX4 matrix is a pair (codes, scales) of uint8 tensors: rows of 16 *
+# ceil(cols / 32) codes, and rra_mx4_scale_bytes(rows, cols) scales.
 
 _PAIRS = [struct.Struct("%dP" % (2 * n)).pack for n in range(RRA_MAX_RANKS + 1)]
+_type, _nbytes_of = attrgetter("dtype"), attrgetter("nbytes")
 
 
 def _mx4(what, ms, rows, cols, device):
-    """The C array of MX4 matrices (codes, scales), rows x cols each."""
-    u8 = _t().uint8
-    shape, nbytes = (rows, 16 * ((cols + 31) // 32)), 512 * ((rows + 127) // 128) * ((cols + 127) // 128)
-    ps = []
-    for m in ms:
-        codes, scales = m
-        ps.append(_one(what, codes, u8, shape, device))
-        ps.append(_flat(what, scales, u8, nbytes, device))
-    return _PAIRS[len(ms)](*ps)
+    """The C array of MX4 matrices (codes, scales), rows x cols each.  A call
+    has up to 50 of these tensors and waits for their checks, so that their
+    type goes by their bytes: any type of one byte will do."""
+    n, u8 = len(ms), _t().uint8
+    codes, scales = rows * 16 * ((cols + 31) // 32), 512 * ((rows + 127) // 128) * ((cols + 127) // 128)
+    ts = [*chain.from_iterable(ms)]
+    if [*map(_nbytes_of, ts)] != [codes, scales] * n or {*map(_device, ts)} != {device} or not all(map(_dense, ts)):
+        for c, s in ms:
+            _flat(what + " (codes)", c.view(u8) if c.element_size() == 1 else c, u8, codes, device)
+            _flat(what + " (scales)", s.view(u8) if s.element_size() == 1 else s, u8, scales, device)
+    return _PAIRS[n](*map(_data, ts))
 
 
 def rra_mx4_scale_bytes(rows: int, cols: int) -> int:
@@ -699,17 +703,19 @@ def rra_vocab_sample(logits, uniform, token, temperature=None, top_k=None, top_p
     x = logits[0]
     rows, dev, dt = x.shape[0], x.get_device(), x.dtype
     vocab = [t.shape[1] for t in logits]
-    lp = _PTRS[n](*[_one("a rank's logits", t, dt, (rows, v), dev) for t, v in zip(logits, vocab)])
-    f32, per = torch.float32, (rows,)
-
-    def opt(what, t, dtype):
-        return None if t is None else _one(what, t, dtype, per, dev)
-
-    st = load().rra_vocab_sample(lp, _sizes(vocab), n, rows, _one("uniform", uniform, f32, per, dev),
-                                 opt("temperature", temperature, f32), opt("top_k", top_k, torch.int32),
-                                 opt("top_p", top_p, f32), opt("min_p", min_p, f32),
-                                 _one("token", token, torch.int64, per, dev), opt("logprob", logprob, f32),
-                                 _norm_dtype(x), _on(stream, dev))
+    if ([*map(_numel, logits)] != [rows * v for v in vocab] or {*map(_device, logits)} != {dev}
+            or not all(map(_dense, logits)) or {*map(_type, logits)} != {dt}):
+        for t, v in zip(logits, vocab):
+            _one("a rank's logits", t, dt, (rows, v), dev)
+    f32 = torch.float32
+    st = load().rra_vocab_sample(
+        _PTRS[n](*map(_data, logits)), _sizes(vocab), n, rows, _flat("uniform", uniform, f32, rows, dev),
+        None if temperature is None else _flat("temperature", temperature, f32, rows, dev),
+        None if top_k is None else _flat("top_k", top_k, torch.int32, rows, dev),
+        None if top_p is None else _flat("top_p", top_p, f32, rows, dev),
+        None if min_p is None else _flat("min_p", min_p, f32, rows, dev),
+        _flat("token", token, torch.int64, rows, dev),
+        None if logprob is None else _flat("logprob", logprob, f32, rows, dev), _norm_dtype(x), _on(stream, dev))
     return _ret(st, "rra_vocab_sample", check)
 
 

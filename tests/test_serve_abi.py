@@ -159,7 +159,7 @@ def test_sample_refusals(lib, change, want):
 def test_binding_refusals():
     codes, scales = torch.zeros(4, 32, dtype=torch.uint8), torch.zeros(512, dtype=torch.uint8)
     x = torch.zeros(4, 64)
-    for bad in ((codes[:, :16], scales), (codes, scales[:256]), (codes.to(torch.int8), scales), (codes.t(), scales)):
+    for bad in ((codes[:, :16], scales), (codes, scales[:256]), (codes.to(torch.int16), scales), (codes.t(), scales)):
         with pytest.raises(ValueError):
             rra.rra_mx4_quantize(x, *bad)
     with pytest.raises(TypeError):
