@@ -28,31 +28,55 @@ struct QuantArgs {
   int vec;
 };
 
+// Piece i of rows cut into `pieces`: 32-bit division where it will do (64-bit
+// division is some 100 instructions, as many as an octet's whole work).
+__device__ __forceinline__ size_t piece_row(size_t i, uint32_t pieces) {
+  if (pieces == 1) return i;
+  return (i >> 32) == 0 ? (uint32_t)i / pieces : i / pieces;
+}
+
 // A warp takes kMxTrips x 256 columns of a row at a time.
 template <int DT>
 __global__ void __launch_bounds__(kMxThreads) quantize_kernel(const QuantArgs a) {
   constexpr int ES = Elem<DT>::kSize;
   const int lane = threadIdx.x & 31;
-  const size_t octets = (a.cols + 31) / 32 * 4, across = (a.cols + 127) / 128;
-  const size_t pieces = (across * 16 + 32 * kMxTrips - 1) / (32 * kMxTrips);
+  const uint32_t pieces = (uint32_t)(((a.cols + 127) / 128 * 16 + 32 * kMxTrips - 1) / (32 * kMxTrips));
   const size_t total = a.rows * pieces, step = (size_t)gridDim.x * (kMxThreads / 32);
   pdl_wait();
   for (size_t i = (size_t)blockIdx.x * (kMxThreads / 32) + (threadIdx.x >> 5); i < total; i += step) {
-    const size_t row = i / pieces, o0 = (i - row * pieces) * (32 * kMxTrips) + lane;
+    const size_t row = piece_row(i, pieces);
+    const uint32_t o0 = (uint32_t)(i - row * pieces) * (32 * kMxTrips) + lane;
     const char* src = a.x + row * a.cols * ES;
-    float f[kMxTrips][8];
+    const MxRow r = mx_row(a.codes, a.scales, row, a.cols);
+    if (DT == RRA_BFLOAT16 && a.vec) {
+      const uint32_t units = (uint32_t)(a.cols / 8);
+      uint4 x[kMxTrips];
 #pragma unroll
-    for (int j = 0; j < kMxTrips; ++j) {
-      const int v = octet_valid(o0 + 32 * j, a.cols);
-      if (v > 0) {
-        load8<DT>(src, o0 + 32 * j, v, a.vec, f[j]);
-      } else {
+      for (int j = 0; j < kMxTrips; ++j)
+        x[j] = o0 + 32 * j < units ? ld_stream(src + (size_t)(o0 + 32 * j) * 16) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) f[j][k] = 0.f;
+      for (int j = 0; j < kMxTrips; ++j) {
+        if (o0 - lane + 32 * j >= r.ends) break;
+        mx_put8(x[j], r, o0 + 32 * j);
+      }
+    } else {
+      float f[kMxTrips][8];
+#pragma unroll
+      for (int j = 0; j < kMxTrips; ++j) {
+        const int v = octet_valid(o0 + 32 * j, a.cols);
+        if (v > 0) {
+          load8<DT>(src, o0 + 32 * j, v, a.vec, f[j]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) f[j][k] = 0.f;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kMxTrips; ++j) {
+        if (o0 - lane + 32 * j >= r.ends) break;
+        mx_put8(f[j], r, o0 + 32 * j);
       }
     }
-#pragma unroll
-    for (int j = 0; j < kMxTrips; ++j) mx_put8(f[j], a.codes, a.scales, row, o0 + 32 * j, octets, across, true);
   }
   pdl_next();
 }
@@ -69,32 +93,27 @@ template <int DT>
 __global__ void __launch_bounds__(kMxThreads) restore_kernel(const ReadArgs a) {
   constexpr int ES = Elem<DT>::kSize;
   const int lane = threadIdx.x & 31;
-  const size_t octets = (a.cols + 31) / 32 * 4, across = (a.cols + 127) / 128, used = (a.cols + 7) / 8;
-  const size_t pieces = (used + 32 * kMxTrips - 1) / (32 * kMxTrips);
+  const uint32_t used = (uint32_t)((a.cols + 7) / 8), pieces = (used + 32 * kMxTrips - 1) / (32 * kMxTrips);
   const size_t total = a.rows * pieces, step = (size_t)gridDim.x * (kMxThreads / 32);
   pdl_wait();
   for (size_t i = (size_t)blockIdx.x * (kMxThreads / 32) + (threadIdx.x >> 5); i < total; i += step) {
-    const size_t row = i / pieces, o0 = (i - row * pieces) * (32 * kMxTrips) + lane;
+    const size_t row = piece_row(i, pieces);
+    const uint32_t o0 = (uint32_t)(i - row * pieces) * (32 * kMxTrips) + lane;
     char* dst = a.out + row * a.cols * ES;
+    const MxRow r = mx_row(a.codes, a.scales, row, a.cols);
     uint32_t w[kMxTrips], b[kMxTrips];
 #pragma unroll
     for (int j = 0; j < kMxTrips; ++j) {
-      const size_t o = o0 + 32 * j;
-      w[j] = o < used ? __ldg(reinterpret_cast<const uint32_t*>(a.codes + (row * octets + o) * 4)) : 0u;
-      b[j] = o < used ? __ldg(a.scales + mx_scale_at(row, o / 4, across)) : 0u;
+      const uint32_t o = o0 + 32 * j;
+      w[j] = o < used ? __ldg(r.codes + o) : 0u;
+      b[j] = o < used ? __ldg(r.scales + (o / 16) * 512 + (o / 4) % 4) : 0u;
     }
 #pragma unroll
     for (int j = 0; j < kMxTrips; ++j) {
-      const size_t o = o0 + 32 * j;
+      const uint32_t o = o0 + 32 * j;
       if (o >= used) break;
-      const float p = mx_power(b[j]);
       float f[8];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 v = mx_value2((w[j] >> (8 * k)) & 255u);
-        f[2 * k] = v.x * p;
-        f[2 * k + 1] = v.y * p;
-      }
+      mx_value8(w[j], mx_power(b[j]), f);
       store8<DT>(dst, o, octet_valid(o, a.cols), a.vec, f);
     }
   }
@@ -115,7 +134,6 @@ struct NormMxArgs {
   size_t rows, hidden;
   float eps;
   int n;
-  int vec;
 };
 
 // A sum held as an unevaluated pair of float32.
@@ -159,13 +177,29 @@ __device__ __forceinline__ float pair_rstd(Pair sum, float count, float eps) {
   return __fmaf_rn(__fmul_rn(0.5f, r), e, r);
 }
 
+// acc_add with the bfloat16 widened by the addition itself.
+template <int DT>
+__device__ __forceinline__ void add_unit(Acc& a, const uint4& v) {
+  if constexpr (DT == RRA_BFLOAT16) {
+    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %2;\nadd.rn.f32.bf16 %0, l, %0;\nadd.rn.f32.bf16 %1, h, %1;\n}"
+          : "+r"(a.w[2 * i]), "+r"(a.w[2 * i + 1])
+          : "r"(x[i]));
+  } else {
+    acc_add<DT>(a, v);
+  }
+}
+
 // One CTA per row (or every gridDim-th row).  U octets a thread in registers;
 // U == 0: long rows, kept in shared memory.
-template <int DT, int U>
-__global__ void __launch_bounds__(1024) norm_mx4_kernel(const __grid_constant__ NormMxArgs a) {
+template <int DT, int U, bool VEC>
+__global__ void __launch_bounds__(U == 1 ? 1024 : 512, U == 2 ? 2 : 1) norm_mx4_kernel(const __grid_constant__ NormMxArgs a) {
   constexpr int ES = Elem<DT>::kSize, PU = Elem<DT>::kPerUnit;
   extern __shared__ float srow[];
   __shared__ Pair part[2][32];
+  __shared__ float rstd[2];
   const size_t hidden = a.hidden, octets = (hidden + 31) / 32 * 4, across = (hidden + 127) / 128;
   const int tid = threadIdx.x, threads = blockDim.x, warps = threads >> 5;
   const int trips = U ? U : (int)((across * 16 + threads - 1) / threads);
@@ -173,6 +207,7 @@ __global__ void __launch_bounds__(1024) norm_mx4_kernel(const __grid_constant__ 
   pdl_wait();
   for (size_t row = blockIdx.x; row < a.rows; row += gridDim.x, flip ^= 1) {
     const size_t off = row * hidden * ES;
+    const MxRow out = mx_row(a.codes, a.scales, row, hidden);
     float f[U ? U : 1][8];
     Pair ss{0.f, 0.f};
 #pragma unroll
@@ -192,18 +227,18 @@ __global__ void __launch_bounds__(1024) norm_mx4_kernel(const __grid_constant__ 
           uint4 x[kMaxRanks], r = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
           for (int k = 0; k < kMaxRanks; ++k)
-            if (k < a.n) x[k] = load_row<DT>(static_cast<const char*>(a.in[k]) + off, u, vh, a.vec);
-          if (a.residual) r = load_row<DT>(a.residual + off, u, vh, a.vec);
+            if (k < a.n) x[k] = load_row<DT>(static_cast<const char*>(a.in[k]) + off, u, vh, VEC);
+          if (a.residual) r = load_row<DT>(a.residual + off, u, vh, VEC);
           Acc acc;
           acc_init<DT>(acc, x[0]);
 #pragma unroll
           for (int k = 1; k < kMaxRanks; ++k)
-            if (k < a.n) acc_add<DT>(acc, x[k]);
-          if (a.residual) acc_add<DT>(acc, r);
+            if (k < a.n) add_unit<DT>(acc, x[k]);
+          if (a.residual) add_unit<DT>(acc, r);
 #pragma unroll
           for (int i = 0; i < PU; ++i) s[h * PU + i] = __uint_as_float(acc.w[i]);
         }
-        if (a.residual_out) store8<DT>(a.residual_out + off, o, v, a.vec, s);
+        if (a.residual_out) store8<DT>(a.residual_out + off, o, v, VEC, s);
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss = pair_square(ss, i < v ? s[i] : 0.f);
       }
@@ -215,9 +250,12 @@ __global__ void __launch_bounds__(1024) norm_mx4_kernel(const __grid_constant__ 
     ss = pair_reduce(ss);
     if ((tid & 31) == 0) part[flip][tid >> 5] = ss;
     __syncthreads();
-    Pair tot = (tid & 31) < warps ? part[flip][tid & 31] : Pair{0.f, 0.f};
-    tot = pair_reduce(tot);
-    const float inv = pair_rstd(tot, (float)hidden, a.eps);
+    if (tid < 32) {  // one warp for all: the others' issue slots go to other rows
+      const float q = pair_rstd(pair_reduce(tid < warps ? part[flip][tid] : Pair{0.f, 0.f}), (float)hidden, a.eps);
+      if (tid == 0) rstd[flip] = q;
+    }
+    __syncthreads();
+    const float inv = rstd[flip];
 #pragma unroll
     for (int j = 0; j < trips; ++j) {
       float* s = f[U ? j : 0];
@@ -229,31 +267,32 @@ __global__ void __launch_bounds__(1024) norm_mx4_kernel(const __grid_constant__ 
       }
       if (v > 0) {
         float g[8];
-        if (DT == RRA_BFLOAT16 && a.vec) {
+        if (DT == RRA_BFLOAT16 && VEC) {
           unit_floats<DT>(__ldg(static_cast<const uint4*>(a.gamma) + o), g);
         } else {
-          load8<DT>(static_cast<const char*>(a.gamma), o, v, a.vec, g);
+          load8<DT>(static_cast<const char*>(a.gamma), o, v, VEC, g);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) s[i] = i < v ? __fmul_rn(__fmul_rn(s[i], inv), g[i]) : 0.f;
       }
-      mx_put8(s, a.codes, a.scales, row, o, octets, across, true);
+      mx_put8(s, out, (uint32_t)o);
     }
   }
   pdl_next();
 }
 
-template <int DT>
+template <int DT, bool VEC>
 cudaError_t norm_dt(const NormMxArgs& a, cudaStream_t s) {
   // one octet a thread while that fits a CTA and the rows are few (one row's
-  // latency is then the call's), two for many rows or longer ones
+  // latency is then the call's), two for many rows, four for longer ones
   const size_t lanes = (a.hidden + 127) / 128 * 16;  // octets up to the last tile's end
   const int grid = budget(a.rows);
   const auto threads = [&](int u) { return (int)(((lanes + u - 1) / u + 31) / 32 * 32); };
   if (lanes <= 1024 && (a.rows <= 2 * (size_t)device_sms() || lanes <= 256))
-    return launch_pdl(norm_mx4_kernel<DT, 1>, grid, threads(1), 0, s, a);
-  if (lanes <= 2048) return launch_pdl(norm_mx4_kernel<DT, 2>, grid, threads(2), 0, s, a);
-  constexpr auto kern = norm_mx4_kernel<DT, 0>;
+    return launch_pdl(norm_mx4_kernel<DT, 1, VEC>, grid, threads(1), 0, s, a);
+  if (lanes <= 1024) return launch_pdl(norm_mx4_kernel<DT, 2, VEC>, grid, threads(2), 0, s, a);
+  if (lanes <= 2048) return launch_pdl(norm_mx4_kernel<DT, 4, VEC>, grid, threads(4), 0, s, a);
+  constexpr auto kern = norm_mx4_kernel<DT, 0, VEC>;
   const cudaError_t e = raise_smem<kern>(200 * 1024 + 1024);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, grid, 512, (a.hidden + 31) / 32 * 32 * sizeof(float), s, a);
@@ -300,8 +339,8 @@ cudaError_t launch_norm_mx4(int n, int dt, bool vec, const void* const* in, cons
   a.hidden = hidden;
   a.eps = eps;
   a.n = n;
-  a.vec = vec;
-  return dt == RRA_BFLOAT16 ? norm_dt<RRA_BFLOAT16>(a, s) : norm_dt<RRA_FLOAT32>(a, s);
+  if (dt == RRA_BFLOAT16) return vec ? norm_dt<RRA_BFLOAT16, true>(a, s) : norm_dt<RRA_BFLOAT16, false>(a, s);
+  return vec ? norm_dt<RRA_FLOAT32, true>(a, s) : norm_dt<RRA_FLOAT32, false>(a, s);
 }
 
 }  // namespace rra

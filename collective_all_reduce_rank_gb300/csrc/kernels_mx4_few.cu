@@ -110,7 +110,7 @@ __device__ __forceinline__ void few_put(const Mx4Args& p, const Mx4Group& g, int
     float unused;
     const float v = row < g.rows ? a * gate_sigma<ACT>(a, &unused) * b : 0.f;
     const uint32_t byte = mx_scale(__reduce_max_sync(0xffffffffu, mx_abs(v)));
-    uint32_t w = byte == kMxNan ? 0u : (mx_code2(v * mx_inverse(byte), 0.f) & 15u) << (4 * (lane & 7));
+    uint32_t w = byte == kMxNan ? 0u : mx_code(v * mx_inverse(byte)) << (4 * (lane & 7));
     w |= __shfl_xor_sync(0xffffffffu, w, 1);
     w |= __shfl_xor_sync(0xffffffffu, w, 2);
     w |= __shfl_xor_sync(0xffffffffu, w, 4);

@@ -17,7 +17,7 @@
 // in which tensor memory takes them (32 lanes of 4 words).
 #pragma once
 
-#include <cuda_fp4.h>
+#include <cuda_fp16.h>
 
 #include "rowio.cuh"
 
@@ -45,26 +45,80 @@ __device__ __forceinline__ float mx_power(uint32_t byte) {
                    : byte == kMxNan ? __uint_as_float(0x7FC00000u) : __uint_as_float(byte << 23);
 }
 
-// Two codes as a byte, the first in the low half.
-__device__ __forceinline__ uint32_t mx_code2(float a, float b) {
-  return (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(a, b), __NV_E2M1, cudaRoundNearest);
+// Eight values as a word of codes, the first in the lowest bits.
+__device__ __forceinline__ uint32_t mx_pack8(const float* f) {
+  uint32_t w;
+  asm("{\n.reg .b8 a, b, c, d;\n"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
+      "mov.b32 %0, {a, b, c, d};\n}\n"
+      : "=r"(w)
+      : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
+  return w;
 }
 
-__device__ __forceinline__ float2 mx_value2(uint32_t byte) {
-  const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)byte, __NV_E2M1);
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+// One code, in the lowest four bits.
+__device__ __forceinline__ uint32_t mx_code(float x) {
+  uint32_t w;
+  asm("{\n.reg .b8 a, z;\ncvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\nmov.b32 %0, {a, a, a, a};\n}\n"
+      : "=r"(w)
+      : "f"(x), "f"(0.f));
+  return w & 15u;
 }
 
 // Eight scaled values as a word.  nan: the codes of a block without a scale
 // (inf * 0 would make them the largest code).
 __device__ __forceinline__ uint32_t mx_code8(const float* f, float inv, bool nan) {
-  uint32_t w = 0;
+  float g[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w |= mx_code2(f[2 * i] * inv, f[2 * i + 1] * inv) << (8 * i);
-  return nan ? 0u : w;
+  for (int i = 0; i < 8; ++i) g[i] = f[i] * inv;
+  return nan ? 0u : mx_pack8(g);
+}
+
+// The same of a unit of bfloat16: the multiplication widens.  -0 is added so
+// that zeros keep their sign.
+__device__ __forceinline__ uint32_t mx_code8(const uint4& x, uint32_t byte) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  const uint16_t inv = (uint16_t)(byte == kMxNan ? 0u : (254u - byte) << 7);
+  float g[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %2;\n"
+        "fma.rn.f32.bf16 %0, l, %3, %4;\nfma.rn.f32.bf16 %1, h, %3, %4;\n}"
+        : "=f"(g[2 * i]), "=f"(g[2 * i + 1])
+        : "r"(w[i]), "h"(inv), "f"(-0.f));
+  return byte == kMxNan ? 0u : mx_pack8(g);
+}
+
+// The values of a word of codes times a power of two, exactly.
+__device__ __forceinline__ void mx_value8(uint32_t w, float power, float* f) {
+  uint32_t h[4];
+  asm("{\n.reg .b8 a, b, c, d;\n"
+      "mov.b32 {a, b, c, d}, %4;\n"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n}\n"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+    f[2 * i] = v.x * power;
+    f[2 * i + 1] = v.y * power;
+  }
 }
 
 __device__ __forceinline__ uint32_t mx_abs(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+
+// Float32 bits of the largest |x| of a unit of bfloat16.
+__device__ __forceinline__ uint32_t mx_amax_bf16(const uint4& x) {
+  const uint32_t m = __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
+                              __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
+  return max(m << 16, m & 0xFFFF0000u);
+}
 
 __device__ __forceinline__ uint32_t mx_amax8(const float* f) {
   uint32_t m = 0;
@@ -124,26 +178,47 @@ __device__ __forceinline__ int octet_valid(size_t o, size_t cols) {
   return o * 8 + 8 <= cols ? 8 : (o * 8 < cols ? (int)(cols - o * 8) : 0);
 }
 
-// Quantise a block held by four neighbouring lanes, eight columns each, and
-// store it: the codes, and with the fourth block of a tile's row (the first of
-// 16 lanes) that row's scale word.  All 32 lanes call this, lane l with an
-// octet o of which o % 16 == l % 16; octets behind the row's last block (up to
-// the tile's fourth) have f = 0 and store their scale byte 0, which a product
-// may read, but no codes.
-__device__ __forceinline__ void mx_put8(const float* f, uint8_t* codes, uint8_t* scales, size_t row, size_t o,
-                                        size_t octets, size_t across, bool live) {
-  uint32_t m = mx_amax8(f);
+// A row of an MX4 matrix being written or read: where its codes start, and the
+// scale bytes of its first tile (tile t's are 512 t further).
+struct MxRow {
+  uint32_t octets;  // words of codes
+  uint32_t ends;    // octets up to the last tile's end
+  uint32_t* codes;
+  uint8_t* scales;
+};
+
+__device__ __forceinline__ MxRow mx_row(const void* codes, const void* scales, size_t row, size_t cols) {
+  const size_t across = (cols + 127) / 128, octets = (cols + 31) / 32 * 4;
+  return {(uint32_t)octets, (uint32_t)(across * 16),
+          const_cast<uint32_t*>(static_cast<const uint32_t*>(codes)) + row * octets,
+          const_cast<uint8_t*>(static_cast<const uint8_t*>(scales)) + row / 128 * across * 512 +
+              ((uint32_t)row % 32 * 16 + (uint32_t)row % 128 / 32 * 4)};
+}
+
+// Quantise a block held by four neighbouring lanes, eight columns each (m: bits
+// of their largest value, code: their codes under a scale), and store it: the codes, and with the fourth block of a
+// tile's row (the first of 16 lanes) that row's scale word.  All 32 lanes call
+// this, lane l with an octet o of which o % 16 == l % 16; octets behind the
+// row's last block (up to the tile's fourth) have f = 0 and store their scale
+// byte 0, which a product may read, but no codes.
+template <class Code>
+__device__ __forceinline__ void mx_put8(uint32_t m, const MxRow& r, uint32_t o, Code code) {
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
   const uint32_t byte = mx_scale(m);
-  const uint32_t w = mx_code8(f, mx_inverse(byte), byte == kMxNan);
   uint32_t s = byte << (8 * ((threadIdx.x >> 2) & 3));
   s |= __shfl_xor_sync(0xffffffffu, s, 4);
   s |= __shfl_xor_sync(0xffffffffu, s, 8);
-  if (!live) return;
-  if (o < octets) *reinterpret_cast<uint32_t*>(codes + (row * octets + o) * 4) = w;
-  if ((threadIdx.x & 15) == 0 && o < across * 16)
-    *reinterpret_cast<uint32_t*>(scales + mx_scale_at(row, o / 4, across)) = s;
+  if (o < r.octets) r.codes[o] = code(byte);
+  if ((threadIdx.x & 15) == 0 && o < r.ends) *reinterpret_cast<uint32_t*>(r.scales + (o / 16) * 512) = s;
+}
+
+__device__ __forceinline__ void mx_put8(const float* f, const MxRow& r, uint32_t o) {
+  mx_put8(mx_amax8(f), r, o, [&](uint32_t byte) { return mx_code8(f, mx_inverse(byte), byte == kMxNan); });
+}
+
+__device__ __forceinline__ void mx_put8(const uint4& x, const MxRow& r, uint32_t o) {
+  mx_put8(mx_amax_bf16(x), r, o, [&](uint32_t byte) { return mx_code8(x, byte); });
 }
 
 }  // namespace rra
