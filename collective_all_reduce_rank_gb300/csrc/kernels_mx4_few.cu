@@ -51,13 +51,6 @@ struct FewShared : TcShared {
   alignas(8) uint64_t sums_empty;
 };
 
-__device__ __forceinline__ void few_load(const CUtensorMap* map, uint32_t dst, uint32_t bar, int x, int y) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-      "l"(map), "r"(bar), "r"(x), "r"(y)
-      : "memory");
-}
-
 __device__ __forceinline__ void few_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
@@ -186,11 +179,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) mx4_few_kernel(const __grid_co
           tc_bar_expect(bar, F::kStage);
 #pragma unroll
           for (int i = 0; i < G; ++i) {
-            few_load(&p.w[w + i], at + i * kWCodes, bar, kk * 128, tile * kRows);
-            few_load(&p.ws[w + i], at + kSW + i * kWScales, bar, kk * 256, tile);
+            mx4_load(&p.w[w + i], at + i * kWCodes, bar, kk * 128, tile * kRows);
+            mx4_load(&p.ws[w + i], at + kSW + i * kWScales, bar, kk * 256, tile);
           }
-          few_load(&p.x[seg], at + kX, bar, kk * 128, 0);
-          few_load(&p.xs[seg], at + kSX, bar, kk * 256, 0);
+          mx4_load(&p.x[seg], at + kX, bar, kk * 128, 0);
+          mx4_load(&p.xs[seg], at + kSX, bar, kk * 256, 0);
           if (++s == nstages) {
             s = 0;
             parity ^= 1;

@@ -8,17 +8,22 @@
 // Shape.  A cluster of two CTAs works on a tile of 256 tokens x 256 weight rows
 // with tcgen05.mma.cta_group::2, CTA c holding tokens [128c, 128c + 128) of it
 // in its tensor memory.  A stage is 256 columns of K: 128 bytes of codes a row
-// (one swizzled row), and two scale tiles per 128 rows, which tcgen05.cp takes
-// from shared to tensor memory ahead of the stage's four products.
+// (one swizzled row), and two scale tiles per 128 rows, which go
+// through shared to tensor memory ahead of the stage's four products.
 //
-// Tensor memory.  Two accumulators of 256 columns and 24 columns of scales do
-// not fit in 512.  The second accumulator starts at column 224, so the two
-// share 32 columns: the epilogue reads those of a tile first and then lets the
+// Tensor memory.  Two accumulators of 256 columns and two stages' scales of 24
+// do not fit in 512.  The second accumulator starts at column 208, so the two
+// share 48 columns: the epilogue reads those of a tile first and then lets the
 // next tile's products begin, under the rest of its own work.
 //
-// Roles (12 warps) as in tc_gemm.cuh: warps 0 and 3 load X and W, warp 1 of
-// the first CTA issues, warp 2 owns the tensor memory, warps 4-11 are the
-// epilogue.
+// Scales.  The tensor cores can copy scales to tensor memory themselves, in
+// line with their products, but each of the six copies a stage then cost them
+// some 50 cycles (4096 x 5120 x 8 x 1728 gated 256 us, with none of them 190):
+// four warps read them from shared memory instead and write them a stage ahead.
+//
+// Roles (16 warps): warps 0 and 3 load X and W, warp 1 of the first CTA issues,
+// warp 2 owns the tensor memory, warps 4-11 are the epilogue, 12-15 write
+// scales.
 #include "act.cuh"
 #include "mx4_mma.cuh"
 
@@ -32,13 +37,19 @@ constexpr int kScalesW = 2048;     // four: all 256 weight rows
 constexpr int kStageBytes = 2 * kCodes + kScalesX + kScalesW;
 constexpr int kStages = 5;
 constexpr int kSmem = kStages * kStageBytes + kTcEpiWarps * kTcStoreBytes + 1024;
-constexpr uint32_t kSecond = 224;  // first column of the second accumulator
-constexpr uint32_t kColX = 480, kColW = 488;
+constexpr int kThreads = kTcThreads + 128;
+constexpr uint32_t kSecond = 208;  // first column of the second accumulator
+constexpr uint32_t kScales = 464;  // first column of the scales: two stages of 8 for X and 16 for W
 static_assert(kStageBytes % 1024 == 0, "a swizzled tile starts on 1024 bytes");
 static_assert(kStages <= kTcMaxStages, "barriers");
 
 struct Unit {
   int group, m, n;
+};
+
+struct ProductShared : TcShared {
+  alignas(8) uint64_t scales_in[kStages];  // this CTA's scales of the stage are in shared memory
+  alignas(8) uint64_t scales_set[2];       // first CTA: both CTAs' are in tensor memory
 };
 
 __device__ __forceinline__ Unit unit_of(const Mx4Args& p, int t) {
@@ -96,7 +107,7 @@ __device__ __forceinline__ void store_gated(const Mx4Args& p, const Unit& u, int
     tc_ld32(addr + 128 + c, b);
     tc_ld_ready(a);
     tc_ld_ready(b);
-    if (i == 0) drained();
+    if (i == 1) drained();
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
       float unused;
@@ -111,11 +122,11 @@ __device__ __forceinline__ void store_gated(const Mx4Args& p, const Unit& u, int
 
 // ACT < 0: a plain product.
 template <int ACT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mx4_product_kernel(const __grid_constant__ Mx4Args p) {
   constexpr bool GATED = ACT >= 0;
   extern __shared__ uint8_t raw[];
-  __shared__ TcShared sh;
+  __shared__ ProductShared sh;
   const uint32_t ring = (tc_smem(raw) + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = tc_cta_rank();
@@ -126,10 +137,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     for (int s = 0; s < kStages; ++s) {
       tc_bar_init(tc_smem(&sh.full[s]), 1);
       tc_bar_init(tc_smem(&sh.empty[s]), 1);
+      tc_bar_init(tc_smem(&sh.scales_in[s]), 1);
     }
     for (int b = 0; b < 2; ++b) {
       tc_bar_init(tc_smem(&sh.acc_full[b]), 1);
       tc_bar_init(tc_smem(&sh.acc_empty[b]), 2 * kTcEpiWarps);
+      tc_bar_init(tc_smem(&sh.scales_set[b]), 2 * 4);
     }
     sh.give_up = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -173,20 +186,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
             ok = false;
             break;
           }
-          if (is_x && rank == 0) tc_bar_expect(full0 + 8 * s, 2 * kStageBytes);
-          const uint32_t at = ring + s * kStageBytes, bar = lead0 + 8 * s;
+          const uint32_t at = ring + s * kStageBytes, bar = lead0 + 8 * s, scales = at + 2 * kCodes;
+          const uint32_t mine = tc_smem(&sh.scales_in[s]);
           if (is_x) {
+            if (rank == 0) tc_bar_expect(full0 + 8 * s, 4 * kCodes);
+            tc_bar_expect(mine, kScalesX + kScalesW);
             tc_tma_load(&p.x[seg], at + kCodes, bar, kk * 128, x0);
-            tc_tma_load(&p.xs[seg], at + 2 * kCodes, bar, kk * 256, x0 / 128);
-          } else {
-            const uint32_t sw = at + 2 * kCodes + kScalesX;
-            tc_tma_load(&p.w[GATED ? w + (int)rank : w], at, bar, kk * 128, n0);
+            mx4_load(&p.xs[seg], scales, mine, kk * 256, x0 / 128);
             if (GATED) {
-              tc_tma_load(&p.ws[w], sw, bar, kk * 256, u.n);
-              tc_tma_load(&p.ws[w + 1], sw + 1024, bar, kk * 256, u.n);
+              mx4_load(&p.ws[w], scales + kScalesX, mine, kk * 256, u.n);
+              mx4_load(&p.ws[w + 1], scales + kScalesX + 1024, mine, kk * 256, u.n);
             } else {
-              tc_tma_load(&p.ws[w], sw, bar, kk * 256, u.n * 2);
+              mx4_load(&p.ws[w], scales + kScalesX, mine, kk * 256, u.n * 2);
             }
+          } else {
+            tc_tma_load(&p.w[GATED ? w + (int)rank : w], at, bar, kk * 128, n0);
           }
           if (++s == kStages) {
             s = 0;
@@ -206,7 +220,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     if (rank == 0 && lane == 0) {
-      uint32_t tile = 0, round = 0;
+      uint32_t tile = 0, round = 0, stage = 0;
       int s = 0;
       bool ok = true;
       for (int t = cluster; t < total && ok; t += clusters, ++tile) {
@@ -215,22 +229,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         if (tile && !tc_wait(tc_smem(&sh.acc_empty[0]), (tile - 1) & 1, &sh, p.status, 2)) break;
         tc_fence_after();
         for (int k = 0; k < p.kblocks; ++k) {
-          if (!tc_wait(tc_smem(&sh.full[s]), round & 1, &sh, p.status, 3)) {
+          if (!tc_wait(tc_smem(&sh.full[s]), round & 1, &sh, p.status, 3) ||
+              !tc_wait(tc_smem(&sh.scales_set[stage & 1]), (stage >> 1) & 1, &sh, p.status, 6)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sw = ring + s * kStageBytes, sx = sw + kCodes, cx = sx + kCodes, cw = cx + kScalesX;
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            mx4_put_scales<true>(tmem + kColX + 4 * j, cx + 512 * j);
-            mx4_put_scales<true>(tmem + kColW + 8 * j, cw + 512 * j);
-            mx4_put_scales<true>(tmem + kColW + 8 * j + 4, cw + 1024 + 512 * j);
-          }
+          const uint32_t sw = ring + s * kStageBytes, sx = sw + kCodes;
+          const uint32_t tx = tmem + kScales + 24 * (stage & 1), tw = tx + 8;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             mx4_mma<true>(d, tc_desc<false>(sx + 32 * i), tc_desc<false>(sw + 32 * i), mx4_idesc(256, 256, 2 * (i & 1)),
-                          tmem + kColX + 4 * (i >> 1), tmem + kColW + 8 * (i >> 1), (uint32_t)(k > 0 || i > 0));
+                          tx + 4 * (i >> 1), tw + 8 * (i >> 1), (uint32_t)(k > 0 || i > 0));
+          ++stage;
           tc_commit(tc_smem(&sh.empty[s]));
           if (++s == kStages) {
             s = 0;
@@ -241,6 +252,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
       }
     }
     __syncwarp();
+  } else if (warp >= 12) {
+    // this quarter of the lanes' scales, two stages at a time in tensor memory
+    const uint32_t lanes = tmem + kScales + ((uint32_t)((warp & 3) * 32) << 16);
+    uint32_t stage = 0, round = 0;
+    int s = 0, before = 0;  // places of this stage and of the one two stages ago
+    uint32_t round_before = 0;
+    bool ok = true;
+    for (int t = cluster; t < total && ok; t += clusters) {
+      for (int k = 0; k < p.kblocks; ++k, ++stage) {
+        // the products of two stages ago no longer read this half of the columns
+        if (stage >= 2) {
+          ok = tc_wait(tc_smem(&sh.empty[before]), round_before & 1, &sh, p.status, 7);
+          if (++before == kStages) {
+            before = 0;
+            ++round_before;
+          }
+        }
+        ok = ok && tc_wait(tc_smem(&sh.scales_in[s]), round & 1, &sh, p.status, 8);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        const uint4* from = reinterpret_cast<const uint4*>(raw + (ring - tc_smem(raw)) + s * kStageBytes + 2 * kCodes);
+        const uint4 x0 = from[lane], x1 = from[32 + lane], a0 = from[64 + lane], a1 = from[96 + lane];
+        const uint4 b0 = from[128 + lane], b1 = from[160 + lane];
+        const uint32_t to = lanes + 24 * (stage & 1);
+        mx4_st8(to, x0, x1);
+        mx4_st8(to + 8, a0, b0);
+        mx4_st8(to + 16, a1, b1);
+        mx4_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc_bar_arrive_remote(tc_smem(&sh.scales_set[stage & 1]), 0);
+        if (++s == kStages) {
+          s = 0;
+          ++round;
+        }
+      }
+    }
   } else if (warp >= 4) {
     const int quad = warp & 3, half = (warp - 4) >> 2;
     uint8_t* buf = raw + (ring - tc_smem(raw)) + kStages * kStageBytes + (warp - 4) * kTcStoreBytes;
@@ -250,9 +300,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
       if (!__all_sync(0xffffffffu, tc_wait(tc_smem(&sh.acc_full[b]), (tile >> 1) & 1, &sh, p.status, 4))) break;
       tc_fence_after();
       const Unit u = unit_of(p, t);
-      // the 32 shared columns are the first accumulator's last, the second's
-      // first; a warp that reads none of them has nothing left to read of the
-      // tile before and reports at once
+      // the shared columns are the first accumulator's last, the second's first;
+      // a warp that reads none of them has nothing left to read of the tile
+      // before and reports at once
       const int owner = b ? 0 : 1;
       const auto drained = [&] {
         tc_fence_before();
@@ -303,7 +353,7 @@ cudaError_t go(const Mx4Args& p, cudaStream_t s, int* grid_out) {
   if (attr != cudaSuccess) return attr;
   const int grid = 2 * tc_clusters(p.tiles * p.mt);
   if (grid_out) *grid_out = grid;
-  return launch_pdl(kern, grid, kTcThreads, kSmem, s, p);
+  return launch_pdl(kern, grid, kThreads, kSmem, s, p);
 }
 
 }  // namespace
