@@ -11,15 +11,18 @@
 // (one swizzled row), and two scale tiles per 128 rows, which go
 // through shared to tensor memory ahead of the stage's four products.
 //
-// Tensor memory.  Two accumulators of 256 columns and two stages' scales of 24
-// do not fit in 512.  The second accumulator starts at column 208, so the two
-// share 48 columns: the epilogue reads those of a tile first and then lets the
+// Tensor memory.  Two accumulators of 256 columns and three stages' scales of 24
+// do not fit in 512.  The second accumulator starts at column 184, so the two
+// share 72 columns: the epilogue reads those of a tile first and then lets the
 // next tile's products begin, under the rest of its own work.
 //
 // Scales.  The tensor cores can copy scales to tensor memory themselves, in
 // line with their products, but each of the six copies a stage then cost them
 // some 50 cycles (4096 x 5120 x 8 x 1728 gated 256 us, with none of them 190):
-// four warps read them from shared memory instead and write them a stage ahead.
+// four warps read them from shared memory instead and write them up to three
+// stages ahead (gated 238 us with two stages, row-parallel 117 against 107).
+// Halves of a stage, five at a time, took 279: the issuing thread then waits and
+// commits twice as often.
 //
 // Roles (16 warps): warps 0 and 3 load X and W, warp 1 of the first CTA issues,
 // warp 2 owns the tensor memory, warps 4-11 are the epilogue, 12-15 write
@@ -38,8 +41,9 @@ constexpr int kStageBytes = 2 * kCodes + kScalesX + kScalesW;
 constexpr int kStages = 5;
 constexpr int kSmem = kStages * kStageBytes + kTcEpiWarps * kTcStoreBytes + 1024;
 constexpr int kThreads = kTcThreads + 128;
-constexpr uint32_t kSecond = 208;  // first column of the second accumulator
-constexpr uint32_t kScales = 464;  // first column of the scales: two stages of 8 for X and 16 for W
+constexpr uint32_t kSecond = 184;  // first column of the second accumulator
+constexpr uint32_t kScales = 440;  // first column of the scales: per stage 8 for X and 16 for W
+constexpr int kSlots = 3;          // stages whose scales tensor memory holds
 static_assert(kStageBytes % 1024 == 0, "a swizzled tile starts on 1024 bytes");
 static_assert(kStages <= kTcMaxStages, "barriers");
 
@@ -49,7 +53,7 @@ struct Unit {
 
 struct ProductShared : TcShared {
   alignas(8) uint64_t scales_in[kStages];  // this CTA's scales of the stage are in shared memory
-  alignas(8) uint64_t scales_set[2];       // first CTA: both CTAs' are in tensor memory
+  alignas(8) uint64_t scales_set[kSlots];  // first CTA: both CTAs' are in tensor memory
 };
 
 __device__ __forceinline__ Unit unit_of(const Mx4Args& p, int t) {
@@ -61,61 +65,75 @@ __device__ __forceinline__ Unit unit_of(const Mx4Args& p, int t) {
   return u;
 }
 
-// An epilogue warp's share of a tile: 32 tokens from row0 on, the 128 columns
-// of `half` in two pairs of 32 (gated: two blocks of 32).  `first`: which of
-// the two comes first; drained() is called once its columns have been read.
-template <class Drained>
-__device__ __forceinline__ void store_tile(const Mx4Args& p, const Unit& u, int row0, int half, uint32_t addr,
-                                           uint8_t* buf, int first, Drained drained) {
-  const Mx4Group& g = p.group[u.group];
-  const int rows = p.tokens - row0;
-#pragma unroll 1
-  for (int i = 0; i < 2; ++i) {
-    const int c = half * 128 + (i ^ first) * 64;  // column of the tile
-    const int c0 = u.n * 256 + c;
-    const int valid = g.rows - c0;
-    float a[32], b[32];
-    tc_ld32(addr + c, a);
-    tc_ld32(addr + c + 32, b);
-    tc_ld_ready(a);
-    tc_ld_ready(b);
-    if (i == 0) drained();
-    if (valid <= 0 || rows <= 0) continue;
-    if (p.f32) {
-      float* o = static_cast<float*>(g.out) + (long long)row0 * g.ld + c0;
-      tc_store_f32(buf, a, o, g.ld, rows, valid, g.vec, false);
-      if (valid > 32) tc_store_f32(buf, b, o + 32, g.ld, rows, valid - 32, g.vec, false);
-    } else {
-      tc_stage_bf16(buf, a, 0);
-      tc_stage_bf16(buf, b, 4);
-      tc_flush_bf16(buf, static_cast<__nv_bfloat16*>(g.out) + (long long)row0 * g.ld + c0, g.ld, rows, valid, g.vec,
-                    false);
-    }
+// 64 columns c0.. of 32 rows from row0 on, stored.
+__device__ __forceinline__ void store_pair(const Mx4Args& p, const Mx4Group& g, int row0, int c0, const float* a,
+                                           const float* b, uint8_t* buf) {
+  const int rows = p.tokens - row0, valid = g.rows - c0;
+  if (valid <= 0 || rows <= 0) return;
+  if (p.f32) {
+    float* o = static_cast<float*>(g.out) + (long long)row0 * g.ld + c0;
+    tc_store_f32(buf, a, o, g.ld, rows, valid, g.vec, false);
+    if (valid > 32) tc_store_f32(buf, b, o + 32, g.ld, rows, valid - 32, g.vec, false);
+  } else {
+    tc_stage_bf16(buf, a, 0);
+    tc_stage_bf16(buf, b, 4);
+    tc_flush_bf16(buf, static_cast<__nv_bfloat16*>(g.out) + (long long)row0 * g.ld + c0, g.ld, rows, valid, g.vec,
+                  false);
   }
 }
 
-template <int ACT, class Drained>
+// An epilogue warp's share of a tile: 32 tokens from row0 on, the 128 columns
+// of `half`.  The 96 of them nearest its end (LAST) or its start hold all that
+// it has of the shared columns: they are read first, and drained() is called.
+template <bool LAST, class Drained>
+__device__ __forceinline__ void store_tile(const Mx4Args& p, const Unit& u, int row0, int half, uint32_t addr,
+                                           uint8_t* buf, Drained drained) {
+  const Mx4Group& g = p.group[u.group];
+  const int c0 = u.n * 256 + half * 128;
+  constexpr int kFirst = LAST ? 64 : 0, kThird = LAST ? 32 : 64, kOther = LAST ? 0 : 96;
+  addr += half * 128;
+  float a[32], b[32], c[32];
+  tc_ld32(addr + kFirst, a);
+  tc_ld32(addr + kFirst + 32, b);
+  tc_ld32(addr + kThird, c);
+  tc_ld_ready(a);
+  tc_ld_ready(b);
+  tc_ld_ready(c);
+  drained();
+  store_pair(p, g, row0, c0 + kFirst, a, b, buf);
+  tc_ld32(addr + kOther, a);
+  tc_ld_ready(a);
+  store_pair(p, g, row0, c0 + 64 - kFirst, LAST ? a : c, LAST ? c : a, buf);
+}
+
+// Gated: 64 columns of each projection.  What this warp has of the shared
+// columns is of the one that comes first, which is read whole.
+template <int ACT, bool UP_FIRST, class Drained>
 __device__ __forceinline__ void store_gated(const Mx4Args& p, const Unit& u, int row0, int half, uint32_t addr,
-                                            int first, Drained drained) {
+                                            Drained drained) {
   const Mx4Group& g = p.group[u.group];
   const int row = row0 + (threadIdx.x & 31);
-#pragma unroll 1
+  float e[2][32];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) tc_ld32(addr + (UP_FIRST ? 128 : 0) + half * 64 + 32 * i, e[i]);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) tc_ld_ready(e[i]);
+  drained();
+#pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int c = half * 64 + (i ^ first) * 32;
-    float a[32], b[32];
-    tc_ld32(addr + c, a);
-    tc_ld32(addr + 128 + c, b);
-    tc_ld_ready(a);
-    tc_ld_ready(b);
-    if (i == 1) drained();
+    const int c = half * 64 + 32 * i;
+    float l[32];
+    tc_ld32(addr + (UP_FIRST ? 0 : 128) + c, l);
+    tc_ld_ready(l);
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
       float unused;
-      a[j] = a[j] * gate_sigma<ACT>(a[j], &unused) * b[j];
+      const float a = UP_FIRST ? l[j] : e[i][j], b = UP_FIRST ? e[i][j] : l[j];
+      e[i][j] = a * gate_sigma<ACT>(a, &unused) * b;
     }
     const int c0 = u.n * 128 + c;
     if (row < p.tokens)
-      mx4_put_row(a, g.rows - c0, static_cast<uint8_t*>(g.out) + (long long)row * g.ld + c0 / 2,
+      mx4_put_row(e[i], g.rows - c0, static_cast<uint8_t*>(g.out) + (long long)row * g.ld + c0 / 2,
                   g.out_scales + mx_scale_at((size_t)row, (size_t)(c0 / 32), (size_t)g.across));
   }
 }
@@ -142,8 +160,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int b = 0; b < 2; ++b) {
       tc_bar_init(tc_smem(&sh.acc_full[b]), 1);
       tc_bar_init(tc_smem(&sh.acc_empty[b]), 2 * kTcEpiWarps);
-      tc_bar_init(tc_smem(&sh.scales_set[b]), 2 * 4);
     }
+    for (int b = 0; b < kSlots; ++b) tc_bar_init(tc_smem(&sh.scales_set[b]), 2 * 4);
     sh.give_up = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -220,8 +238,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     if (rank == 0 && lane == 0) {
-      uint32_t tile = 0, round = 0, stage = 0;
-      int s = 0;
+      uint32_t tile = 0, round = 0, set_round = 0;
+      int s = 0, slot = 0;
       bool ok = true;
       for (int t = cluster; t < total && ok; t += clusters, ++tile) {
         const uint32_t d = tmem + (tile & 1) * kSecond;
@@ -230,18 +248,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc_fence_after();
         for (int k = 0; k < p.kblocks; ++k) {
           if (!tc_wait(tc_smem(&sh.full[s]), round & 1, &sh, p.status, 3) ||
-              !tc_wait(tc_smem(&sh.scales_set[stage & 1]), (stage >> 1) & 1, &sh, p.status, 6)) {
+              !tc_wait(tc_smem(&sh.scales_set[slot]), set_round & 1, &sh, p.status, 6)) {
             ok = false;
             break;
           }
           tc_fence_after();
           const uint32_t sw = ring + s * kStageBytes, sx = sw + kCodes;
-          const uint32_t tx = tmem + kScales + 24 * (stage & 1), tw = tx + 8;
+          const uint32_t tx = tmem + kScales + 24 * slot, tw = tx + 8;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             mx4_mma<true>(d, tc_desc<false>(sx + 32 * i), tc_desc<false>(sw + 32 * i), mx4_idesc(256, 256, 2 * (i & 1)),
                           tx + 4 * (i >> 1), tw + 8 * (i >> 1), (uint32_t)(k > 0 || i > 0));
-          ++stage;
+          if (++slot == kSlots) {
+            slot = 0;
+            ++set_round;
+          }
           tc_commit(tc_smem(&sh.empty[s]));
           if (++s == kStages) {
             s = 0;
@@ -253,44 +274,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp >= 12) {
-    // this quarter of the lanes' scales, two stages at a time in tensor memory
+    // this quarter of the lanes' scales
     const uint32_t lanes = tmem + kScales + ((uint32_t)((warp & 3) * 32) << 16);
-    uint32_t stage = 0, round = 0;
-    int s = 0, before = 0;  // places of this stage and of the one two stages ago
-    uint32_t round_before = 0;
+    uint32_t stage = 0, round = 0, round_before = 0;
+    int s = 0, before = 0;  // places of this stage and of the one kSlots stages ago
+    int slot = 0;
     bool ok = true;
-    for (int t = cluster; t < total && ok; t += clusters) {
+    for (int t = cluster; t < total && ok; t += clusters)
       for (int k = 0; k < p.kblocks; ++k, ++stage) {
-        // the products of two stages ago no longer read this half of the columns
-        if (stage >= 2) {
+        ok = tc_wait(tc_smem(&sh.scales_in[s]), round & 1, &sh, p.status, 8);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint4* from = reinterpret_cast<const uint4*>(raw + (ring - tc_smem(raw)) + s * kStageBytes + 2 * kCodes);
+        const uint4 x0 = from[lane], x1 = from[32 + lane], a0 = from[64 + lane], a1 = from[96 + lane];
+        const uint4 b0 = from[128 + lane], b1 = from[160 + lane];
+        // the products of kSlots stages ago no longer read these columns
+        if (stage >= kSlots) {
           ok = tc_wait(tc_smem(&sh.empty[before]), round_before & 1, &sh, p.status, 7);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
           if (++before == kStages) {
             before = 0;
             ++round_before;
           }
         }
-        ok = ok && tc_wait(tc_smem(&sh.scales_in[s]), round & 1, &sh, p.status, 8);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
-        const uint4* from = reinterpret_cast<const uint4*>(raw + (ring - tc_smem(raw)) + s * kStageBytes + 2 * kCodes);
-        const uint4 x0 = from[lane], x1 = from[32 + lane], a0 = from[64 + lane], a1 = from[96 + lane];
-        const uint4 b0 = from[128 + lane], b1 = from[160 + lane];
-        const uint32_t to = lanes + 24 * (stage & 1);
+        const uint32_t to = lanes + 24 * slot;
         mx4_st8(to, x0, x1);
         mx4_st8(to + 8, a0, b0);
         mx4_st8(to + 16, a1, b1);
         mx4_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) tc_bar_arrive_remote(tc_smem(&sh.scales_set[stage & 1]), 0);
+        if (lane == 0) tc_bar_arrive_remote(tc_smem(&sh.scales_set[slot]), 0);
+        if (++slot == kSlots) slot = 0;
         if (++s == kStages) {
           s = 0;
           ++round;
         }
       }
-    }
   } else if (warp >= 4) {
     const int quad = warp & 3, half = (warp - 4) >> 2;
     uint8_t* buf = raw + (ring - tc_smem(raw)) + kStages * kStageBytes + (warp - 4) * kTcStoreBytes;
@@ -300,29 +322,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (!__all_sync(0xffffffffu, tc_wait(tc_smem(&sh.acc_full[b]), (tile >> 1) & 1, &sh, p.status, 4))) break;
       tc_fence_after();
       const Unit u = unit_of(p, t);
-      // the shared columns are the first accumulator's last, the second's first;
-      // a warp that reads none of them has nothing left to read of the tile
-      // before and reports at once
-      const int owner = b ? 0 : 1;
+      // the shared columns are the first accumulator's last, the second's first
       const auto drained = [&] {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) tc_bar_arrive_remote(tc_smem(&sh.acc_empty[0]), 0);
       };
-      const auto nothing = [] {};
       const uint32_t addr = tmem + b * kSecond + ((uint32_t)(quad * 32) << 16);
       const int row0 = u.m * 256 + (int)rank * 128 + quad * 32;
-      if (half != owner) {
-        drained();
-        if constexpr (GATED)
-          store_gated<ACT>(p, u, row0, half, addr, 0, nothing);
+      if constexpr (GATED) {
+        if (b)
+          store_gated<ACT, false>(p, u, row0, half, addr, drained);
         else
-          store_tile(p, u, row0, half, addr, buf, 0, nothing);
+          store_gated<ACT, true>(p, u, row0, half, addr, drained);
       } else {
-        if constexpr (GATED)
-          store_gated<ACT>(p, u, row0, half, addr, b ? 0 : 1, drained);
+        if (b)
+          store_tile<false>(p, u, row0, half, addr, buf, drained);
         else
-          store_tile(p, u, row0, half, addr, buf, b ? 0 : 1, drained);
+          store_tile<true>(p, u, row0, half, addr, buf, drained);
       }
     }
   }
