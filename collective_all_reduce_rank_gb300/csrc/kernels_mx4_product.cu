@@ -53,7 +53,6 @@ struct Unit {
 
 struct ProductShared : TcShared {
   alignas(8) uint64_t scales_in[kStages];  // this CTA's scales of the stage are in shared memory
-  alignas(8) uint64_t scales_set[kSlots];  // first CTA: both CTAs' are in tensor memory
 };
 
 __device__ __forceinline__ Unit unit_of(const Mx4Args& p, int t) {
@@ -153,7 +152,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      tc_bar_init(tc_smem(&sh.full[s]), 1);
+      tc_bar_init(tc_smem(&sh.full[s]), 1 + 2 * 4);  // codes announced, scales set by four warps a CTA
       tc_bar_init(tc_smem(&sh.empty[s]), 1);
       tc_bar_init(tc_smem(&sh.scales_in[s]), 1);
     }
@@ -161,7 +160,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tc_bar_init(tc_smem(&sh.acc_full[b]), 1);
       tc_bar_init(tc_smem(&sh.acc_empty[b]), 2 * kTcEpiWarps);
     }
-    for (int b = 0; b < kSlots; ++b) tc_bar_init(tc_smem(&sh.scales_set[b]), 2 * 4);
     sh.give_up = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -238,7 +236,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     if (rank == 0 && lane == 0) {
-      uint32_t tile = 0, round = 0, set_round = 0;
+      uint32_t tile = 0, round = 0;
       int s = 0, slot = 0;
       bool ok = true;
       for (int t = cluster; t < total && ok; t += clusters, ++tile) {
@@ -247,8 +245,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (tile && !tc_wait(tc_smem(&sh.acc_empty[0]), (tile - 1) & 1, &sh, p.status, 2)) break;
         tc_fence_after();
         for (int k = 0; k < p.kblocks; ++k) {
-          if (!tc_wait(tc_smem(&sh.full[s]), round & 1, &sh, p.status, 3) ||
-              !tc_wait(tc_smem(&sh.scales_set[slot]), set_round & 1, &sh, p.status, 6)) {
+          if (!tc_wait(tc_smem(&sh.full[s]), round & 1, &sh, p.status, 3)) {
             ok = false;
             break;
           }
@@ -259,10 +256,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 4; ++i)
             mx4_mma<true>(d, tc_desc<false>(sx + 32 * i), tc_desc<false>(sw + 32 * i), mx4_idesc(256, 256, 2 * (i & 1)),
                           tx + 4 * (i >> 1), tw + 8 * (i >> 1), (uint32_t)(k > 0 || i > 0));
-          if (++slot == kSlots) {
-            slot = 0;
-            ++set_round;
-          }
+          if (++slot == kSlots) slot = 0;
           tc_commit(tc_smem(&sh.empty[s]));
           if (++s == kStages) {
             s = 0;
@@ -306,7 +300,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         mx4_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) tc_bar_arrive_remote(tc_smem(&sh.scales_set[slot]), 0);
+        if (lane == 0) tc_bar_arrive_remote(tc_smem(&sh.full[s]), 0);
         if (++slot == kSlots) slot = 0;
         if (++s == kStages) {
           s = 0;
