@@ -200,21 +200,22 @@ __global__ void __launch_bounds__(kFewThreads, 1) mx4_few_kernel(const __grid_co
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      uint32_t tile = 0, round = 0;
-      int s = 0;
-      bool ok = true;
-      for (int t = cluster; t < p.tiles && ok; t += clusters, ++tile) {
-        const uint32_t b = tile % F::kBufs, d = tmem + b * G * N;
-        if (!tc_wait(tc_smem(&sh.acc_empty[b]), ((tile / F::kBufs) & 1) ^ 1, &sh, p.status, 2)) break;
+    // the whole warp walks the stages, one lane issues (kernels_mx4_product.cu)
+    const bool lead = mx4_elect();
+    uint32_t tile = 0, round = 0;
+    int s = 0;
+    bool ok = true;
+    for (int t = cluster; t < p.tiles && ok; t += clusters, ++tile) {
+      const uint32_t b = tile % F::kBufs, d = tmem + b * G * N;
+      ok = __all_sync(0xffffffffu, tc_wait(tc_smem(&sh.acc_empty[b]), ((tile / F::kBufs) & 1) ^ 1, &sh, p.status, 2));
+      if (!ok) break;
+      tc_fence_after();
+      for (int k = k0; k < k1; ++k) {
+        ok = __all_sync(0xffffffffu, tc_wait(tc_smem(&sh.full[s]), round & 1, &sh, p.status, 3));
+        if (!ok) break;
         tc_fence_after();
-        for (int k = k0; k < k1; ++k) {
-          if (!tc_wait(tc_smem(&sh.full[s]), round & 1, &sh, p.status, 3)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t at = ring + s * F::kStage;
+        const uint32_t at = ring + s * F::kStage;
+        if (lead) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
 #pragma unroll
@@ -227,18 +228,19 @@ __global__ void __launch_bounds__(kFewThreads, 1) mx4_few_kernel(const __grid_co
 #pragma unroll
             for (int g = 0; g < G; ++g)
               mx4_mma<false>(d + g * N, tc_desc<false>(at + g * kWCodes + 32 * i), tc_desc<false>(at + kX + 32 * i),
-                             mx4_idesc(kRows, N, 2 * (i & 1)), tmem + F::kColW + 8 * g + 4 * (i >> 1),
+                             mx4_idesc(kRows, N) | mx4_idesc_scales(2 * (i & 1)), tmem + F::kColW + 8 * g + 4 * (i >> 1),
                              tmem + F::kColX + 4 * (i >> 1), (uint32_t)(k > k0 || i > 0));
           few_commit(tc_smem(&sh.empty[s]));
-          if (++s == nstages) {
-            s = 0;
-            ++round;
-          }
         }
-        if (ok) few_commit(tc_smem(&sh.acc_full[b]));
+        __syncwarp();
+        if (++s == nstages) {
+          s = 0;
+          ++round;
+        }
       }
+      if (ok && lead) few_commit(tc_smem(&sh.acc_full[b]));
+      __syncwarp();
     }
-    __syncwarp();
   } else if (warp >= 4) {
     const int quad = warp & 3, lanes = quad * 32;
     const int share = (N + S - 1) / S;  // columns a CTA of the cluster owns

@@ -11,22 +11,22 @@
 // (one swizzled row), and two scale tiles per 128 rows, which go
 // through shared to tensor memory ahead of the stage's four products.
 //
-// Tensor memory.  Two accumulators of 256 columns and three stages' scales of 24
-// do not fit in 512.  The second accumulator starts at column 184, so the two
-// share 72 columns: the epilogue reads those of a tile first and then lets the
+// Tensor memory.  Two accumulators of 256 columns and four stages' scales of 24
+// do not fit in 512.  The second accumulator starts at column 160, so the two
+// share 96 columns: the epilogue reads those of a tile first and then lets the
 // next tile's products begin, under the rest of its own work.
 //
 // Scales.  The tensor cores can copy scales to tensor memory themselves, in
 // line with their products, but each of the six copies a stage then cost them
 // some 50 cycles (4096 x 5120 x 8 x 1728 gated 256 us, with none of them 190):
-// four warps read them from shared memory instead and write them up to three
-// stages ahead (gated 238 us with two stages, row-parallel 117 against 107).
-// Halves of a stage, five at a time, took 279: the issuing thread then waits and
-// commits twice as often.
+// four warps read them from shared memory instead and write them up to four
+// stages ahead (two measured 15 us slower), announced on the barrier of the
+// stage's codes (a barrier of their own 25 us: what the issuing thread waits for
+// and commits is on the way of every product).
 //
-// Roles (16 warps): warps 0 and 3 load X and W, warp 1 of the first CTA issues,
-// warp 2 owns the tensor memory, warps 4-11 are the epilogue, 12-15 write
-// scales.
+// Roles (16 warps): warps 0 and 3 load X and W, warp 2 their scales (it also owns
+// the tensor memory), warp 1 of the first CTA issues, warps 4-11 are the
+// epilogue, 12-15 write scales.
 #include "act.cuh"
 #include "mx4_mma.cuh"
 
@@ -37,22 +37,30 @@ namespace {
 constexpr int kCodes = 128 * 128;  // codes of 128 rows
 constexpr int kScalesX = 1024;     // two tiles: a CTA's 128 tokens
 constexpr int kScalesW = 2048;     // four: all 256 weight rows
-constexpr int kStageBytes = 2 * kCodes + kScalesX + kScalesW;
-constexpr int kStages = 5;
-constexpr int kSmem = kStages * kStageBytes + kTcEpiWarps * kTcStoreBytes + 1024;
+constexpr int kScaleBytes = kScalesX + kScalesW;
+constexpr int kScaleStages = 6;
 constexpr int kThreads = kTcThreads + 128;
-constexpr uint32_t kSecond = 184;  // first column of the second accumulator
-constexpr uint32_t kScales = 440;  // first column of the scales: per stage 8 for X and 16 for W
-constexpr int kSlots = 3;          // stages whose scales tensor memory holds
-static_assert(kStageBytes % 1024 == 0, "a swizzled tile starts on 1024 bytes");
-static_assert(kStages <= kTcMaxStages, "barriers");
+constexpr uint32_t kSecond = 160;  // first column of the second accumulator
+constexpr uint32_t kScales = 416;  // first column of the scales: per stage 8 for X and 16 for W
+constexpr int kSlots = 4;          // stages whose scales tensor memory holds
+
+// Shared memory: a ring of codes (W's half, X's half), one of scales, and, for
+// plain products, the epilogue's staging.
+template <bool GATED>
+struct Layout {
+  static constexpr int kStages = GATED ? 6 : 5;
+  static constexpr int kStore = kStages * 2 * kCodes + kScaleStages * kScaleBytes;
+  static constexpr int kBytes = kStore + (GATED ? 0 : kTcEpiWarps * kTcStoreBytes) + 1024;
+  static_assert(kBytes + 1024 <= 227 * 1024, "shared memory of a CTA, with what is static");
+};
 
 struct Unit {
   int group, m, n;
 };
 
 struct ProductShared : TcShared {
-  alignas(8) uint64_t scales_in[kStages];  // this CTA's scales of the stage are in shared memory
+  alignas(8) uint64_t scales_in[kScaleStages];  // this CTA's scales of a stage are in shared memory
+  alignas(8) uint64_t scales_out[kScaleStages];  // its four warps have read them
 };
 
 __device__ __forceinline__ Unit unit_of(const Mx4Args& p, int t) {
@@ -64,7 +72,7 @@ __device__ __forceinline__ Unit unit_of(const Mx4Args& p, int t) {
   return u;
 }
 
-// 64 columns c0.. of 32 rows from row0 on, stored.
+// 64 columns from c0 on of 32 rows from row0 on, stored.
 __device__ __forceinline__ void store_pair(const Mx4Args& p, const Mx4Group& g, int row0, int c0, const float* a,
                                            const float* b, uint8_t* buf) {
   const int rows = p.tokens - row0, valid = g.rows - c0;
@@ -149,12 +157,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t rank = tc_cta_rank();
   const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
   const int total = p.tiles * p.mt;
+  constexpr int nstages = Layout<GATED>::kStages;
+  constexpr uint32_t stage_bytes = 2 * kCodes, wbytes = kCodes;  // a stage of codes: W's half, then X's
+  const uint32_t scale_ring = ring + nstages * stage_bytes;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < nstages; ++s) {
       tc_bar_init(tc_smem(&sh.full[s]), 1 + 2 * 4);  // codes announced, scales set by four warps a CTA
       tc_bar_init(tc_smem(&sh.empty[s]), 1);
+    }
+    for (int s = 0; s < kScaleStages; ++s) {
       tc_bar_init(tc_smem(&sh.scales_in[s]), 1);
+      tc_bar_init(tc_smem(&sh.scales_out[s]), 4);
     }
     for (int b = 0; b < 2; ++b) {
       tc_bar_init(tc_smem(&sh.acc_full[b]), 1);
@@ -177,7 +191,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   pdl_wait();
   pdl_next();
 
-  // a stage: codes of W's half, of X's half, scales of X's half, of all of W
   uint32_t issued = 0;
   if (warp == 0 || warp == 3) {
     const bool is_x = warp == 0;
@@ -190,126 +203,164 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int t = cluster; t < total && ok; t += clusters) {
         const Unit u = unit_of(p, t);
         const int w0 = p.group[u.group].w;
-        const int x0 = u.m * 256 + (int)rank * 128;  // first token of this CTA
-        // first weight row of this CTA's half: half a tile, or the tile's rows of the gate or the up projection
+        // first token of this CTA; first weight row of its half: half a tile, or the tile's rows of the gate or the up
+        // projection
+        const int x0 = u.m * 256 + (int)rank * 128;
         const int n0 = GATED ? u.n * 128 : u.n * 256 + (int)rank * 128;
         int seg = 0;
         for (int k = 0; k < p.kblocks; ++k, ++issued) {
           while (seg + 1 < p.nsegs && k >= p.seg_k0[seg + 1]) ++seg;
           const int kk = k - p.seg_k0[seg];
-          const int w = (p.nsegs > 1 ? seg : w0);
+          const int w = p.nsegs > 1 ? seg : w0;
           if (!tc_wait(empty0 + 8 * s, parity, &sh, p.status, 1)) {
             ok = false;
             break;
           }
-          const uint32_t at = ring + s * kStageBytes, bar = lead0 + 8 * s, scales = at + 2 * kCodes;
-          const uint32_t mine = tc_smem(&sh.scales_in[s]);
+          const uint32_t at = ring + s * stage_bytes, bar = lead0 + 8 * s;
           if (is_x) {
-            if (rank == 0) tc_bar_expect(full0 + 8 * s, 4 * kCodes);
-            tc_bar_expect(mine, kScalesX + kScalesW);
-            tc_tma_load(&p.x[seg], at + kCodes, bar, kk * 128, x0);
-            mx4_load(&p.xs[seg], scales, mine, kk * 256, x0 / 128);
-            if (GATED) {
-              mx4_load(&p.ws[w], scales + kScalesX, mine, kk * 256, u.n);
-              mx4_load(&p.ws[w + 1], scales + kScalesX + 1024, mine, kk * 256, u.n);
-            } else {
-              mx4_load(&p.ws[w], scales + kScalesX, mine, kk * 256, u.n * 2);
-            }
+            if (rank == 0) tc_bar_expect(full0 + 8 * s, 2 * stage_bytes);
+            tc_tma_load(&p.x[seg], at + wbytes, bar, kk * 128, x0);
           } else {
             tc_tma_load(&p.w[GATED ? w + (int)rank : w], at, bar, kk * 128, n0);
           }
-          if (++s == kStages) {
+          if (++s == nstages) {
             s = 0;
             parity ^= 1;
           }
         }
       }
       // none of a pair leaves before the last stage releases have landed in it
-      for (int i = 0; i < kStages && ok && !is_x; ++i) {
+      for (int i = 0; i < nstages && ok && !is_x; ++i) {
         ok = tc_wait(empty0 + 8 * s, parity, &sh, p.status, 5);
-        if (++s == kStages) {
+        if (++s == nstages) {
           s = 0;
           parity ^= 1;
         }
       }
     }
     __syncwarp();
+  } else if (warp == 2) {
+    // scales, in a ring of their own: they are small, and are asked for further
+    // ahead than codes can be
+    if (lane == 0) {
+      int s = 0;
+      uint32_t parity = 1;
+      bool ok = true;
+      for (int t = cluster; t < total && ok; t += clusters) {
+        const Unit u = unit_of(p, t);
+        const int w0 = p.group[u.group].w, band = u.m * 2 + (int)rank;
+        int seg = 0;
+        for (int k = 0; k < p.kblocks; ++k) {
+          while (seg + 1 < p.nsegs && k >= p.seg_k0[seg + 1]) ++seg;
+          const int at_k = (k - p.seg_k0[seg]) * 256, w = p.nsegs > 1 ? seg : w0;
+          if (!tc_wait(tc_smem(&sh.scales_out[s]), parity, &sh, p.status, 6)) {
+            ok = false;
+            break;
+          }
+          const uint32_t at = scale_ring + s * kScaleBytes, bar = tc_smem(&sh.scales_in[s]);
+          tc_bar_expect(bar, kScaleBytes);
+          mx4_load(&p.xs[seg], at, bar, at_k, band);
+          if (GATED) {
+            mx4_load(&p.ws[w], at + kScalesX, bar, at_k, u.n);
+            mx4_load(&p.ws[w + 1], at + kScalesX + 1024, bar, at_k, u.n);
+          } else {
+            mx4_load(&p.ws[w], at + kScalesX, bar, at_k, u.n * 2);
+          }
+          if (++s == kScaleStages) {
+            s = 0;
+            parity ^= 1;
+          }
+        }
+      }
+    }
+    __syncwarp();
   } else if (warp == 1) {
-    if (rank == 0 && lane == 0) {
+    // The whole warp walks the stages and one lane of it issues, so that what an
+    // instruction takes is computed once a warp, in uniform registers (by a lane
+    // of its own a product took 90 cycles to issue, a stage 750).
+    if (rank == 0) {
+      const bool lead = mx4_elect();
+      constexpr uint32_t idesc = mx4_idesc(256, 256);
       uint32_t tile = 0, round = 0;
       int s = 0, slot = 0;
       bool ok = true;
       for (int t = cluster; t < total && ok; t += clusters, ++tile) {
         const uint32_t d = tmem + (tile & 1) * kSecond;
         // the tile before has been read where this one's accumulator begins or ends
-        if (tile && !tc_wait(tc_smem(&sh.acc_empty[0]), (tile - 1) & 1, &sh, p.status, 2)) break;
+        if (tile) {
+          ok = __all_sync(0xffffffffu, tc_wait(tc_smem(&sh.acc_empty[0]), (tile - 1) & 1, &sh, p.status, 2));
+          if (!ok) break;
+        }
         tc_fence_after();
         for (int k = 0; k < p.kblocks; ++k) {
-          if (!tc_wait(tc_smem(&sh.full[s]), round & 1, &sh, p.status, 3)) {
-            ok = false;
-            break;
-          }
+          ok = __all_sync(0xffffffffu, tc_wait(tc_smem(&sh.full[s]), round & 1, &sh, p.status, 3));
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t sw = ring + s * kStageBytes, sx = sw + kCodes;
+          const uint32_t sw = ring + s * stage_bytes, sx = sw + wbytes;
           const uint32_t tx = tmem + kScales + 24 * slot, tw = tx + 8;
+          if (lead) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            mx4_mma<true>(d, tc_desc<false>(sx + 32 * i), tc_desc<false>(sw + 32 * i), mx4_idesc(256, 256, 2 * (i & 1)),
-                          tx + 4 * (i >> 1), tw + 8 * (i >> 1), (uint32_t)(k > 0 || i > 0));
+            for (int i = 0; i < 4; ++i)
+              mx4_mma<true>(d, tc_desc<false>(sx + 32 * i), tc_desc<false>(sw + 32 * i),
+                            idesc | mx4_idesc_scales(2 * (i & 1)), tx + 4 * (i >> 1), tw + 8 * (i >> 1),
+                            (uint32_t)(k > 0 || i > 0));
+            tc_commit(tc_smem(&sh.empty[s]));
+          }
+          __syncwarp();
           if (++slot == kSlots) slot = 0;
-          tc_commit(tc_smem(&sh.empty[s]));
-          if (++s == kStages) {
+          if (++s == nstages) {
             s = 0;
             ++round;
           }
         }
-        if (ok) tc_commit(tc_smem(&sh.acc_full[tile & 1]));
+        if (ok && lead) tc_commit(tc_smem(&sh.acc_full[tile & 1]));
+        __syncwarp();
       }
     }
     __syncwarp();
   } else if (warp >= 12) {
     // this quarter of the lanes' scales
     const uint32_t lanes = tmem + kScales + ((uint32_t)((warp & 3) * 32) << 16);
-    uint32_t stage = 0, round = 0, round_before = 0;
-    int s = 0, before = 0;  // places of this stage and of the one kSlots stages ago
+    const uint32_t n = cluster < total ? (uint32_t)((total - cluster + clusters - 1) / clusters) * p.kblocks : 0;
+    uint32_t round = 0, round_before = 0;
+    int from = 0;           // place in the ring of scales
+    int s = 0, before = 0;  // places in that of codes, of this stage and of the one kSlots stages ago
     int slot = 0;
-    bool ok = true;
-    for (int t = cluster; t < total && ok; t += clusters)
-      for (int k = 0; k < p.kblocks; ++k, ++stage) {
-        ok = tc_wait(tc_smem(&sh.scales_in[s]), round & 1, &sh, p.status, 8);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const uint4* from = reinterpret_cast<const uint4*>(raw + (ring - tc_smem(raw)) + s * kStageBytes + 2 * kCodes);
-        const uint4 x0 = from[lane], x1 = from[32 + lane], a0 = from[64 + lane], a1 = from[96 + lane];
-        const uint4 b0 = from[128 + lane], b1 = from[160 + lane];
-        // the products of kSlots stages ago no longer read these columns
-        if (stage >= kSlots) {
-          ok = tc_wait(tc_smem(&sh.empty[before]), round_before & 1, &sh, p.status, 7);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          tc_fence_after();
-          if (++before == kStages) {
-            before = 0;
-            ++round_before;
-          }
-        }
-        const uint32_t to = lanes + 24 * slot;
-        mx4_st8(to, x0, x1);
-        mx4_st8(to + 8, a0, b0);
-        mx4_st8(to + 16, a1, b1);
-        mx4_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) tc_bar_arrive_remote(tc_smem(&sh.full[s]), 0);
-        if (++slot == kSlots) slot = 0;
-        if (++s == kStages) {
-          s = 0;
-          ++round;
+    for (uint32_t stage = 0; stage < n; ++stage) {
+      bool ok = tc_wait(tc_smem(&sh.scales_in[from]), round & 1, &sh, p.status, 8);
+      const uint4* at = reinterpret_cast<const uint4*>(raw + (scale_ring - tc_smem(raw)) + from * kScaleBytes) + lane;
+      const uint4 x0 = at[0], x1 = at[32], a0 = at[64], a1 = at[96], b0 = at[128], b1 = at[160];
+      // the products of kSlots stages ago no longer read these columns
+      if (stage >= kSlots) {
+        ok = ok && tc_wait(tc_smem(&sh.empty[before]), round_before & 1, &sh, p.status, 7);
+        if (++before == nstages) {
+          before = 0;
+          ++round_before;
         }
       }
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      const uint32_t to = lanes + 24 * slot;
+      mx4_st8(to, x0, x1);
+      mx4_st8(to + 8, a0, b0);
+      mx4_st8(to + 16, a1, b1);
+      mx4_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        tc_bar_arrive_remote(tc_smem(&sh.full[s]), 0);
+        tc_bar_arrive_remote(tc_smem(&sh.scales_out[from]), rank);
+      }
+      if (++from == kScaleStages) {
+        from = 0;
+        ++round;
+      }
+      if (++slot == kSlots) slot = 0;
+      if (++s == nstages) s = 0;
+    }
   } else if (warp >= 4) {
     const int quad = warp & 3, half = (warp - 4) >> 2;
-    uint8_t* buf = raw + (ring - tc_smem(raw)) + kStages * kStageBytes + (warp - 4) * kTcStoreBytes;
+    uint8_t* buf = raw + (ring - tc_smem(raw)) + Layout<GATED>::kStore + (warp - 4) * kTcStoreBytes;
     uint32_t tile = 0;
     for (int t = cluster; t < total; t += clusters, ++tile) {
       const uint32_t b = tile & 1;
@@ -341,9 +392,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // teardown
   if ((warp == 0 || warp == 3) && lane == 0 && sh.give_up) {
     // copies of this CTA may be in flight: wait, bounded, for what was issued
-    const uint32_t first = issued > (uint32_t)kStages ? issued - kStages : 0;
+    const uint32_t first = issued > (uint32_t)nstages ? issued - nstages : 0;
     for (uint32_t i = first; i < issued; ++i)
-      for (int tries = 0; tries < 64 && !tc_bar_try(tc_smem(&sh.full[i % kStages]), (i / kStages) & 1); ++tries) {
+      for (int tries = 0; tries < 64 && !tc_bar_try(tc_smem(&sh.full[i % nstages]), (i / nstages) & 1); ++tries) {
       }
     __nanosleep(1000000);
   }
@@ -360,11 +411,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 template <int ACT>
 cudaError_t go(const Mx4Args& p, cudaStream_t s, int* grid_out) {
   constexpr auto kern = mx4_product_kernel<ACT>;
-  const cudaError_t attr = raise_smem<kern>(kSmem);
+  const cudaError_t attr = raise_smem<kern>(Layout<(ACT >= 0)>::kBytes);
   if (attr != cudaSuccess) return attr;
   const int grid = 2 * tc_clusters(p.tiles * p.mt);
   if (grid_out) *grid_out = grid;
-  return launch_pdl(kern, grid, kThreads, kSmem, s, p);
+  return launch_pdl(kern, grid, kThreads, Layout<(ACT >= 0)>::kBytes, s, p);
 }
 
 }  // namespace

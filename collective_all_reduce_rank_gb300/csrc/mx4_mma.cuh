@@ -11,8 +11,17 @@ namespace rra {
 
 // Instruction descriptor: e2m1 operands, both K-major, E8M0 scales, M x N; the
 // scale ids say which two of a word's four scales a 64-deep product takes.
-__host__ __device__ constexpr uint32_t mx4_idesc(uint32_t m, uint32_t n, uint32_t id) {
-  return (id << 4) | (1u << 7) | (1u << 10) | ((n >> 3) << 17) | (1u << 23) | ((m >> 4) << 24) | (id << 29);
+__host__ __device__ constexpr uint32_t mx4_idesc(uint32_t m, uint32_t n) {
+  return (1u << 7) | (1u << 10) | ((n >> 3) << 17) | (1u << 23) | ((m >> 4) << 24);
+}
+__host__ __device__ constexpr uint32_t mx4_idesc_scales(uint32_t id) { return (id << 4) | (id << 29); }
+
+// One lane of the warp, the same each time.
+__device__ __forceinline__ bool mx4_elect() {
+  uint32_t is;
+  __syncwarp();
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(is));
+  return is != 0;
 }
 
 // Shared-memory descriptor of a tile of scales: 32 rows of 16 bytes, no

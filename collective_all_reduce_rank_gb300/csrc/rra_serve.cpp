@@ -61,13 +61,12 @@ bool map_mx(CUtensorMap* codes, CUtensorMap* scales, const rra_mx4_t& m, size_t 
 // CTA.
 struct Plan {
   bool few, gated;
-  int x_box, w_box, w_bands;
+  int x_box, w_bands;
   size_t tile;  // weight rows (gated: of each projection)
   Plan(size_t tokens, bool g) : few(tokens <= (size_t)kMx4Few), gated(g) {
     x_box = few ? mx4_few_tile(tokens) : 128;
-    w_box = 128;
-    w_bands = few || gated ? 1 : 2;
     tile = few || gated ? 128 : 256;
+    w_bands = few || gated ? 1 : 2;
   }
   size_t tiles(size_t rows) const { return (rows + tile - 1) / tile; }
 };
@@ -184,14 +183,14 @@ rra_status_t rra_mx4_product(const rra_mx4_t* x, const rra_mx4_t* weights, void*
   f(bad_matrix(T, D), RRA_ERR_UNSUPPORTED);
   if (f.st != RRA_SUCCESS) return done(call, nranks, 0, dtype, 0, f.st);
   const size_t e = size_of(dtype);
+  for (int r = 0; r < nranks; ++r) f(bad_matrix(widths[r], D) || bad_matrix(T, widths[r]), RRA_ERR_UNSUPPORTED);
+  if (f.st != RRA_SUCCESS) return done(call, nranks, 0, dtype, 0, f.st);
   const Plan plan(T, false);
   f(mx_check(*x, T, D));
   Ranges in, o;
   mx_ranges(in, *x, T, D);
   size_t tiles = 0, count = 0;
-  for (int r = 0; r < nranks && f.st == RRA_SUCCESS; ++r) {
-    f(bad_matrix(widths[r], D) || bad_matrix(T, widths[r]), RRA_ERR_UNSUPPORTED);
-    if (f.st != RRA_SUCCESS) break;
+  for (int r = 0; r < nranks; ++r) {
     f((T && widths[r] && !outs[r]) || !aligned(outs[r], e), RRA_ERR_INVALID_ARG);
     f(mx_check(weights[r], widths[r], D));
     mx_ranges(in, weights[r], widths[r], D);
@@ -212,7 +211,7 @@ rra_status_t rra_mx4_product(const rra_mx4_t* x, const rra_mx4_t* weights, void*
   bool ok = map_mx(&p->x[0], &p->xs[0], *x, T, D, plan.x_box, 1);
   for (int r = 0; r < nranks && ok; ++r) {
     if (widths[r] == 0) continue;
-    ok = map_mx(&p->w[r], &p->ws[r], weights[r], widths[r], D, plan.w_box, plan.w_bands);
+    ok = map_mx(&p->w[r], &p->ws[r], weights[r], widths[r], D, 128, plan.w_bands);
     Mx4Group& g = p->group[p->ngroups++];
     g.tile0 = p->tiles;
     g.tiles = (int)plan.tiles(widths[r]);
@@ -264,7 +263,7 @@ rra_status_t rra_mx4_product_sum(const rra_mx4_t* xs, const rra_mx4_t* weights, 
   bool ok = true;
   for (int r = 0; r < nranks && ok; ++r) {
     ok = map_mx(&p->x[r], &p->xs[r], xs[r], T, F, plan.x_box, 1) &&
-         map_mx(&p->w[r], &p->ws[r], weights[r], D, F, plan.w_box, plan.w_bands);
+         map_mx(&p->w[r], &p->ws[r], weights[r], D, F, 128, plan.w_bands);
     p->seg_k0[r] = p->kblocks;
     p->kblocks += k_tiles(F);
   }
@@ -316,8 +315,8 @@ rra_status_t rra_mx4_gated_ffn(const rra_mx4_t* x, const rra_mx4_t* gates, const
   p->act = act;
   bool ok = map_mx(&p->x[0], &p->xs[0], *x, T, D, plan.x_box, 1);
   for (int r = 0; r < nranks && ok; ++r) {
-    ok = map_mx(&p->w[2 * r], &p->ws[2 * r], gates[r], F, D, plan.w_box, plan.w_bands) &&
-         map_mx(&p->w[2 * r + 1], &p->ws[2 * r + 1], ups[r], F, D, plan.w_box, plan.w_bands);
+    ok = map_mx(&p->w[2 * r], &p->ws[2 * r], gates[r], F, D, 128, plan.w_bands) &&
+         map_mx(&p->w[2 * r + 1], &p->ws[2 * r + 1], ups[r], F, D, 128, plan.w_bands);
     Mx4Group& g = p->group[p->ngroups++];
     g.tile0 = p->tiles;
     g.tiles = (int)plan.tiles(F);
