@@ -90,7 +90,7 @@ struct Shared {
   unsigned long long scan[kWarps];
   int cut;
   uint32_t allow;
-  unsigned long long before;
+  unsigned long long before, after;
 };
 
 __device__ __forceinline__ uint32_t s32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -297,6 +297,15 @@ __device__ __forceinline__ unsigned long long share_of(unsigned long long v, flo
   return q + (up && rest ? 1 : 0);
 }
 
+// The smallest q with q b >= a, for q of up to 20 bits: float32's quotient is
+// off by one at most (a 64-bit division is some 100 instructions).
+__device__ __forceinline__ unsigned long long divide_up(unsigned long long a, unsigned long long b) {
+  unsigned long long q = (unsigned long long)__fdividef((float)a, (float)b);
+  while (q * b < a) ++q;
+  while (q && (q - 1) * b >= a) --q;
+  return q;
+}
+
 // What a bound keeps: all keys above `key`, and the first `ties` equal to it.
 struct Bound {
   uint32_t key, ties;
@@ -340,7 +349,7 @@ struct Row {
   static constexpr int PU = Elem<DT>::kPerUnit;
   const uint4* slice;
   int units;
-  uint32_t* hist;  // [2][3][kBins]
+  uint32_t* hist;  // [2][4][kBins]
   Shared& sh;
   Scale c;
   uint32_t most;  // largest key
@@ -351,7 +360,7 @@ struct Row {
   // Logits above this are kept: -infinity, which weighs nothing, without a bound.
   static __device__ __forceinline__ float bound_of(const Bound& b) { return b.key ? L::value(b.key) : -INFINITY; }
 
-  __device__ __forceinline__ uint32_t* bins() const { return hist + (level & 1) * 3 * kBins; }
+  __device__ __forceinline__ uint32_t* bins() const { return hist + (level & 1) * 4 * kBins; }
 
   __device__ __forceinline__ uint32_t raw_at(int at) const {
     return PU == 4 ? reinterpret_cast<const uint32_t*>(slice)[at] : reinterpret_cast<const uint16_t*>(slice)[at];
@@ -418,7 +427,7 @@ struct Row {
 
   // The slice's elements in range and above `keep`'s key, counted by bins, or
   // their weights added (words == 3: pieces of 15 bits, whose sums of up to 2^17
-  // elements fit a word).
+  // elements fit a word) and, in a fourth word, they.
   __device__ __forceinline__ void fill(const Range& r, const Bound& keep, int words) const {
     uint32_t* h = bins();
     const float bound = bound_of(keep), low = fmaxf(L::value(r.lo), c.low), high = L::value(r.hi);
@@ -434,6 +443,7 @@ struct Row {
                atomicAdd(at, (uint32_t)w & 0x7FFFu);
                if (w >> 15) atomicAdd(at + kBins, (uint32_t)(w >> 15) & 0x7FFFu);
                if (w >> 30) atomicAdd(at + 2 * kBins, (uint32_t)(w >> 30));
+               atomicAdd(at + 3 * kBins, 1u);
              });
     __syncwarp();
   }
@@ -473,9 +483,9 @@ struct Row {
 
   // Of a range's bins, two a thread, the one in which the running sum from
   // `above` on reaches `target` (bins() if none); above: the sum before it (all
-  // of it).  Up to 64 bins are the first warp's alone.
+  // of it); after: the sum with it.  Up to 64 bins are the first warp's alone.
   __device__ __forceinline__ int reach(const Range& r, const unsigned long long* v, unsigned long long& above,
-                                       unsigned long long target) {
+                                       unsigned long long& after, unsigned long long target) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = 2 * threadIdx.x, n = r.bins();
     unsigned long long end = above + prefix(v[0] + v[1]);
     if (n > 64) {
@@ -491,9 +501,11 @@ struct Row {
       if (begin0 < target && begin1 >= target) {
         sh.cut = b;
         sh.before = begin0;
+        sh.after = begin1;
       } else if (begin1 < target && end >= target) {
         sh.cut = b + 1;
         sh.before = begin1;
+        sh.after = end;
       } else if (last && end < target) {
         sh.cut = n;
         sh.before = end;
@@ -502,9 +514,16 @@ struct Row {
     ++level;
     __syncthreads();
     above = sh.before;
+    after = sh.after;
     const int cut = sh.cut;
     __syncthreads();  // they may be set again
     return cut;
+  }
+
+  // The bound that keeps all keys from lo on.
+  static __device__ __forceinline__ Bound all_from(uint32_t lo) {
+    // below zero's key lies that of -0, which no logit has and which is not below zero
+    return {L::value(lo) == 0.f ? lo - 2 : lo - 1, 0};
   }
 
   __device__ __forceinline__ Range bin_keys(const Range& r, int b) const {
@@ -522,17 +541,18 @@ struct Row {
   // The bound of the k largest; none if no more than that weigh anything.
   __device__ __forceinline__ Bound largest(unsigned long long k) {
     const uint32_t near = near_key(), low = min(L::from(c.low), most);
-    unsigned long long above = 0, v[2];
+    unsigned long long above = 0, after, v[2];
     Range r = with_bins(near, most);
     for (bool wide = low < near;;) {
       clear(r, 1);
       fill(r, {0, 0}, 1);
       cluster_sync();
       gather(r, 1, v);
-      const int b = reach(r, v, above, k);
+      const int b = reach(r, v, above, after, k);
       if (b < r.bins()) {
         if (r.shift == 0) return {r.hi - (uint32_t)b, (uint32_t)(k - above)};
         r = bin_keys(r, b);
+        if (after == k) return all_from(r.lo);  // the whole bin, often one element
       } else {
         if (!wide) return {0, 0};
         r = with_bins(low, near - 1);
@@ -548,11 +568,11 @@ struct Row {
     const uint32_t near = near_key(), low = min(L::from(c.low), most);
     const unsigned long long extra = keep.key ? weight(sh, c, L::value(keep.key)) * keep.ties : 0;
     const float bound = bound_of(keep);
-    unsigned long long above = 0, target = 0, v[2];
+    unsigned long long above = 0, after, target = 0, v[2];
     Range r = with_bins(near, most);
     for (bool first = true, wide = low < near;; first = false) {
       const int words = r.shift ? 3 : 1;
-      clear(r, words);
+      clear(r, words + (words > 1));
       fill(r, keep, words);
       if (first) {
         const unsigned long long all = publish(sum_of(
@@ -572,16 +592,21 @@ struct Row {
         if (r.shift == 0 && v[j]) v[j] *= weight(sh, c, L::value(q.hi));
         if (extra && keep.key >= q.lo && keep.key <= q.hi) v[j] += extra;
       }
-      const int b = reach(r, v, above, target);
+      const uint32_t* elements = bins() + 3 * kBins;
+      const int b = reach(r, v, above, after, target);
       if (b < r.bins()) {
         if (r.shift == 0) {
           const uint32_t key = r.hi - (uint32_t)b;
           const unsigned long long each = weight(sh, c, L::value(key));
-          unsigned long long ties = (target - above + each - 1) / each;
+          unsigned long long ties = divide_up(target - above, each);
           if (key == keep.key && ties > keep.ties) ties = keep.ties;
           return {key, (uint32_t)min(ties, 0xFFFFFFFFull)};
         }
         r = bin_keys(r, b);
+        const int lane = threadIdx.x & 31;
+        uint32_t n = __reduce_add_sync(0xffffffffu, lane < split ? peer_u32(elements + b, lane) : 0);
+        if (extra && keep.key >= r.lo && keep.key <= r.hi) n = 2;
+        if (n == 1) return all_from(r.lo);  // it is its element that reaches the share
       } else {
         if (!wide) return keep;  // all of it
         r = with_bins(low, near - 1);
@@ -655,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ Shared sh;
   uint32_t* hist = reinterpret_cast<uint32_t*>(dyn);
-  uint4* slice = reinterpret_cast<uint4*>(dyn + 6 * kBins * 4);
+  uint4* slice = reinterpret_cast<uint4*>(dyn + 8 * kBins * 4);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = (int)(blockIdx.x % (unsigned)split);
   const long long V = a.first[a.n];
@@ -858,8 +883,8 @@ cudaError_t sample_go(const SampleArgs& a, cudaStream_t s, int* grid_out) {
   while (split < kMaxSplit && slice(split) > kMostSlice) split *= 2;
   while (split < kMaxSplit && split * 2 <= sms && slice(split) > 72 * 1024) split *= 2;
   while (split < kMaxSplit && a.rows * split * 2 <= (size_t)sms && V / (split * 2) >= 2048) split *= 2;
-  const size_t smem = 6 * kBins * 4 + (slice(split) + 15) / 16 * 16;
-  const cudaError_t attr = raise_smem<kern>(6 * kBins * 4 + kMostSlice + 1024);
+  const size_t smem = 8 * kBins * 4 + (slice(split) + 15) / 16 * 16;
+  const cudaError_t attr = raise_smem<kern>(8 * kBins * 4 + kMostSlice + 1024);
   if (attr != cudaSuccess) return attr;
   // a cluster a row: rows differ in their work (greedy ones have next to none),
   // and those that end early make room

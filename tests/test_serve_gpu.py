@@ -299,6 +299,27 @@ def test_sample_rows(rows):
     check_sample(l, [1024, 2051, 1024], **k)
 
 
+@pytest.mark.parametrize("dtype,shards", [("bf16", [30001, 0, 20001, 7]), ("fp32", [20000, 20003])])
+@pytest.mark.parametrize("rows,cap", [(160, 0), (24, 3), (24, 0)])
+def test_sample_rows_alone_and_shared(rows, cap, dtype, shards):
+    """Rows that a CTA has to itself (many of them, or few SMs) and rows that a
+    cluster shares give the same tokens."""
+    V = sum(shards)
+    l = (3.0 * torch.randn(rows, V, generator=gen(rows + V), device="cuda")).to(DT[dtype])
+    l[0] = -math.inf
+    l[1, :] = 0.5
+    l[2, 7] = math.inf
+    l[3, V - 1] = math.nan
+    l[4, 5:] = -math.inf
+    k = {n: (v * (rows // 8)) for n, v in SETTINGS.items()}
+    rra.rra_set_max_ctas(cap)
+    try:
+        check_sample(l, shards, **k)
+        check_sample(l, shards)
+    finally:
+        rra.rra_set_max_ctas(0)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_sample_equal_logits(dtype):
     """Ties at the bounds of top-k and top-p go to the lowest index."""
