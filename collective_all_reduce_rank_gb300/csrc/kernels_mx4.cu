@@ -25,7 +25,6 @@ struct QuantArgs {
   uint8_t* codes;
   uint8_t* scales;
   size_t rows, cols;
-  int vec;
 };
 
 // Piece i of rows cut into `pieces`: 32-bit division where it will do (64-bit
@@ -36,7 +35,7 @@ __device__ __forceinline__ size_t piece_row(size_t i, uint32_t pieces) {
 }
 
 // A warp takes kMxTrips x 256 columns of a row at a time.
-template <int DT>
+template <int DT, bool VEC>
 __global__ void __launch_bounds__(kMxThreads) quantize_kernel(const QuantArgs a) {
   constexpr int ES = Elem<DT>::kSize;
   const int lane = threadIdx.x & 31;
@@ -48,7 +47,7 @@ __global__ void __launch_bounds__(kMxThreads) quantize_kernel(const QuantArgs a)
     const uint32_t o0 = (uint32_t)(i - row * pieces) * (32 * kMxTrips) + lane;
     const char* src = a.x + row * a.cols * ES;
     const MxRow r = mx_row(a.codes, a.scales, row, a.cols);
-    if (DT == RRA_BFLOAT16 && a.vec) {
+    if constexpr (DT == RRA_BFLOAT16 && VEC) {
       const uint32_t units = (uint32_t)(a.cols / 8);
       uint4 x[kMxTrips];
 #pragma unroll
@@ -65,7 +64,7 @@ __global__ void __launch_bounds__(kMxThreads) quantize_kernel(const QuantArgs a)
       for (int j = 0; j < kMxTrips; ++j) {
         const int v = octet_valid(o0 + 32 * j, a.cols);
         if (v > 0) {
-          load8<DT>(src, o0 + 32 * j, v, a.vec, f[j]);
+          load8<DT>(src, o0 + 32 * j, v, VEC, f[j]);
         } else {
 #pragma unroll
           for (int k = 0; k < 8; ++k) f[j][k] = 0.f;
@@ -86,10 +85,13 @@ struct ReadArgs {
   const uint8_t* scales;
   char* out;
   size_t rows, cols;
-  int vec;
 };
 
-template <int DT>
+// VEC: rows of whole aligned 16-byte units, an octet of columns a lane.  Others:
+// a lane stores every 32nd column of 256, so that a warp's stores stay together,
+// and finds its codes in the words that the lanes hold (1283 x 1027 float32 6.8
+// us with an octet a lane).
+template <int DT, bool VEC>
 __global__ void __launch_bounds__(kMxThreads) restore_kernel(const ReadArgs a) {
   constexpr int ES = Elem<DT>::kSize;
   const int lane = threadIdx.x & 31;
@@ -111,13 +113,42 @@ __global__ void __launch_bounds__(kMxThreads) restore_kernel(const ReadArgs a) {
 #pragma unroll
     for (int j = 0; j < kMxTrips; ++j) {
       const uint32_t o = o0 + 32 * j;
-      if (o >= used) break;
-      float f[8];
-      mx_value8(w[j], mx_power(b[j]), f);
-      store8<DT>(dst, o, octet_valid(o, a.cols), a.vec, f);
+      if (VEC) {
+        if (o >= used) break;
+        float f[8];
+        mx_value8(w[j], mx_power(b[j]), f);
+        store8<DT>(dst, o, octet_valid(o, a.cols), true, f);
+      } else {
+        if (o - lane >= used) break;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {  // column 32 q + lane of the 256
+          const uint32_t word = __shfl_sync(0xffffffffu, w[j], 4 * q + (lane >> 3));
+          const uint32_t byte = __shfl_sync(0xffffffffu, b[j], 4 * q);
+          const float v = mx_value(word >> (4 * (lane & 7))) * mx_power(byte);
+          const size_t col = (size_t)(o - lane) * 8 + 32 * q + lane;
+          if (col < a.cols) {
+            if (DT == RRA_BFLOAT16)
+              reinterpret_cast<__nv_bfloat16*>(dst)[col] = __float2bfloat16_rn(v);
+            else
+              reinterpret_cast<float*>(dst)[col] = v;
+          }
+        }
+      }
     }
   }
   pdl_next();
+}
+
+template <int DT>
+cudaError_t quantize_go(const QuantArgs& a, bool vec, int grid, cudaStream_t s) {
+  return vec ? launch_pdl(quantize_kernel<DT, true>, grid, kMxThreads, 0, s, a)
+             : launch_pdl(quantize_kernel<DT, false>, grid, kMxThreads, 0, s, a);
+}
+
+template <int DT>
+cudaError_t restore_go(const ReadArgs& a, bool vec, int grid, cudaStream_t s) {
+  return vec ? launch_pdl(restore_kernel<DT, true>, grid, kMxThreads, 0, s, a)
+             : launch_pdl(restore_kernel<DT, false>, grid, kMxThreads, 0, s, a);
 }
 
 // ---------------------------------------------------------------------------
@@ -301,7 +332,7 @@ cudaError_t norm_dt(const NormMxArgs& a, cudaStream_t s) {
 // CTAs that fill the GPU a few times over, or fewer.
 int stream_grid(size_t pieces) {
   const size_t ctas = (pieces + kMxThreads / 32 - 1) / (kMxThreads / 32);
-  const size_t most = (size_t)device_sms() * 16;
+  const size_t most = (size_t)device_sms() * 64;
   return budget(ctas < most ? ctas : most);
 }
 
@@ -310,19 +341,17 @@ int stream_grid(size_t pieces) {
 cudaError_t launch_mx4_quantize(int dt, bool vec, const void* x, void* codes, void* scales, size_t rows, size_t cols,
                                 cudaStream_t s) {
   const QuantArgs a{static_cast<const char*>(x), static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales), rows,
-                    cols, vec};
+                    cols};
   const int grid = stream_grid(rows * (((cols + 127) / 128 * 16 + 32 * kMxTrips - 1) / (32 * kMxTrips)));
-  return dt == RRA_BFLOAT16 ? launch_pdl(quantize_kernel<RRA_BFLOAT16>, grid, kMxThreads, 0, s, a)
-                            : launch_pdl(quantize_kernel<RRA_FLOAT32>, grid, kMxThreads, 0, s, a);
+  return dt == RRA_BFLOAT16 ? quantize_go<RRA_BFLOAT16>(a, vec, grid, s) : quantize_go<RRA_FLOAT32>(a, vec, grid, s);
 }
 
 cudaError_t launch_mx4_restore(int dt, bool vec, const void* codes, const void* scales, void* out, size_t rows,
                                size_t cols, cudaStream_t s) {
   const ReadArgs a{static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales), static_cast<char*>(out),
-                   rows, cols, vec};
+                   rows, cols};
   const int grid = stream_grid(rows * (((cols + 7) / 8 + 32 * kMxTrips - 1) / (32 * kMxTrips)));
-  return dt == RRA_BFLOAT16 ? launch_pdl(restore_kernel<RRA_BFLOAT16>, grid, kMxThreads, 0, s, a)
-                            : launch_pdl(restore_kernel<RRA_FLOAT32>, grid, kMxThreads, 0, s, a);
+  return dt == RRA_BFLOAT16 ? restore_go<RRA_BFLOAT16>(a, vec, grid, s) : restore_go<RRA_FLOAT32>(a, vec, grid, s);
 }
 
 cudaError_t launch_norm_mx4(int n, int dt, bool vec, const void* const* in, const void* residual, void* residual_out,

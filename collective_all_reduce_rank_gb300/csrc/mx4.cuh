@@ -111,6 +111,14 @@ __device__ __forceinline__ void mx_value8(uint32_t w, float power, float* f) {
   }
 }
 
+// The value of the code in the lowest four bits.
+__device__ __forceinline__ float mx_value(uint32_t code) {
+  const uint32_t m = code & 7u;
+  // the code's bits as those of a float32 2^126 times as small: e and m in place, 0.5 a subnormal
+  const float v = __uint_as_float(m << 22) * __uint_as_float(0x7E800000u);
+  return code & 8u ? -v : v;
+}
+
 __device__ __forceinline__ uint32_t mx_abs(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
 // Float32 bits of the largest |x| of a unit of bfloat16.
