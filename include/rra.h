@@ -572,9 +572,11 @@ rra_status_t rra_mx4_gated_ffn(const rra_mx4_t* x, const rra_mx4_t* gates, const
  *    -infinity; a row with a NaN logit or a temperature that is NaN or
  *    negative gives token -1, logprob NaN.  Where +infinity occurs its
  *    tokens share the whole weight.
- *  - Weights are held to 31 bits and in units of 2^-43 of the largest, and
- *    summed exactly: a token of less than half a unit is never drawn.
- *  Vocabulary up to 368640 in all (else RRA_ERR_UNSUPPORTED).  Errors:
+ *  - Weights are held to 29 bits and in units of 2^-44 of the largest, and
+ *    summed exactly: a token that weighs less than a unit is never drawn.
+ *  Vocabulary up to 368640 in all (else RRA_ERR_UNSUPPORTED); under an SM
+ *  budget a row still takes the CTAs whose shared memory holds it, up to 8.
+ *  Errors:
  *  RRA_ERR_INVALID_ARG, RRA_ERR_UNSUPPORTED, RRA_ERR_ALIAS, RRA_ERR_CUDA. */
 rra_status_t rra_vocab_sample(const void* const* logits, const size_t* vocab, int nranks, size_t rows,
                               const float* uniform, const float* temperature, const int32_t* top_k,

@@ -103,10 +103,12 @@ def test_matrices_off_16_bytes(by, dtype):
 def test_a_byte_of_every_kind_reads_back():
     codes = torch.arange(256, dtype=torch.uint8, device="cuda").view(16, 16).repeat(16, 1)  # 256 rows, 32 columns
     byte = torch.arange(256, dtype=torch.uint8, device="cuda").view(256, 1)
-    out = torch.empty(256, 32, device="cuda")
-    rra.rra_mx4_restore(codes, ref.tile_scales(byte), out)
-    v = ref.values(codes, byte, 32).float()
-    assert torch.equal(torch.isnan(out), torch.isnan(v)) and torch.equal(torch.nan_to_num(out), torch.nan_to_num(v))
+    for dt in (torch.float32, torch.bfloat16):
+        for by in (0, 1):
+            out = shifted(torch.zeros(256, 32, dtype=dt, device="cuda"), by)
+            rra.rra_mx4_restore(codes, ref.tile_scales(byte), out)
+            v = ref.values(codes, byte, 32).to(dt)
+            assert torch.equal(torch.isnan(out), torch.isnan(v)) and torch.equal(torch.nan_to_num(out), torch.nan_to_num(v))
 
 
 # -- norm ----------------------------------------------------------------------
@@ -479,19 +481,105 @@ def test_two_steps_at_once():
     assert all(torch.equal(x, y) for x, y in zip(want[1], b.results()))
 
 
+CALLS = ["allreduce_rmsnorm_mx4", "mx4_gated_ffn", "mx4_product_sum", "mx4_product", "vocab_sample"]
+
+
 @pytest.mark.parametrize("cap", [1, 3, 16])
-def test_every_launch_keeps_the_budget(cap):
-    st = Step(9)
-    big = Step(200, seed=3)
-    st.run()
-    big.run()
-    want = st.results(), big.results()
+@pytest.mark.parametrize("T", [9, 200])
+def test_every_launch_keeps_the_budget(T, cap):
+    st = Step(T, seed=T)
     rra.rra_set_max_ctas(cap)
     try:
-        for s, w in zip((st, big), want):
-            s.run()
-            torch.cuda.synchronize()
-            assert all(torch.equal(x, y) for x, y in zip(w, s.results()))
+        st.run()
+        torch.cuda.synchronize()
+        st.check()
+        x, m = st.stream, room(T, st.D)
+        rra.rra_mx4_quantize(x, *m)
+        rra.rra_mx4_restore(*m, torch.empty_like(x))
+        lines = rra.rra_dump_recent().splitlines()
+        for call in CALLS + ["mx4_quantize", "mx4_restore"]:
+            line = [l for l in lines if " %s " % call in l][-1]
+            pair = T > 128 and call in CALLS[1:4]  # products of many tokens run as pairs of CTAs, one at least
+            assert int(line.split("grid=")[1].split()[0]) <= max(cap, 2 if pair else 1), line
     finally:
         rra.rra_set_max_ctas(0)
     assert rra.rra_query_status()[0] == rra.RRA_SUCCESS
+
+
+@pytest.mark.parametrize("cap", [1, 2, 5, 7])
+@pytest.mark.parametrize("T,K,W", [(5, 700, 650), (60, 1300, 300), (128, 515, 260), (300, 1300, 700), (513, 257, 1030)])
+def test_many_tiles_for_few_ctas(T, K, W, cap):
+    """A CTA's tiles one after another, over both accumulators and rings that wrap."""
+    g = gen(T + W)
+    x, xv = matrix(g, T, K)
+    w, wv = matrix(g, W, K, K ** -0.5)
+    out, acts = torch.full((T, W), math.nan, device="cuda"), room(T, W)
+    two, again = torch.full((T, W), math.nan, device="cuda"), room(T, W)
+    rra.rra_mx4_product(x, [w], [two], K)
+    rra.rra_mx4_gated_ffn(x, [w], [w], [again], K, W)
+    rra.rra_set_max_ctas(cap)
+    try:
+        rra.rra_mx4_product(x, [w], [out], K)
+        rra.rra_mx4_gated_ffn(x, [w], [w], [acts], K, W)
+        torch.cuda.synchronize()
+    finally:
+        rra.rra_set_max_ctas(0)
+    for o in (out, two):
+        close(o, xv @ wv.t(), xv.abs() @ wv.abs().t(), K, "fp32")
+    v = xv @ wv.t()
+    v = ref.act(v, 0) * v
+    for a in (acts, again):
+        off = (ref.read(*a, W) - v).abs() / (ref.half_step(v) * 1.001 + 1e-4 * v.abs().amax())
+        assert float(off.max()) <= 1.0
+    assert rra.rra_query_status()[0] == rra.RRA_SUCCESS
+
+
+# -- more than 2^32 elements -------------------------------------------------------
+
+def test_matrix_past_32_bits():
+    rows, cols = 70000, 65536
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda")
+    some = [0, 1, 32767, 65535, 65536, 69999]
+    x.zero_()
+    x[some] = torch.randn(len(some), cols, generator=gen(1), device="cuda").to(torch.bfloat16)
+    codes, scales = room(rows, cols)
+    rra.rra_mx4_quantize(x, codes, scales)
+    want, byte = ref.quantize(x[some][:, :4096])
+    assert torch.equal(codes[some][:, :2048], want)
+    at = ref.tile_at(rows, cols // 32, "cuda")[some]
+    assert torch.equal(scales[at][:, :128], byte)
+    x.fill_(1.0)
+    rra.rra_mx4_restore(codes, scales, x)
+    assert torch.equal(x[some][:, :4096].double(), ref.values(want, byte, 4096))
+    assert not x[2:32767].any()
+
+
+def test_product_past_32_bits():
+    T, W, K = 130, 33_100_000, 32  # 4.3e9 outputs
+    g = gen(2)
+    x, xv = matrix(g, T, K)
+    w, wv = matrix(g, 300, K)
+    codes = torch.zeros(W, 16, dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(ref.scale_bytes(W, K), dtype=torch.uint8, device="cuda")
+    last = W - 300  # the last 300 rows hold the small matrix
+    codes[last:] = w[0]
+    row = torch.arange(300, device="cuda") + last
+    scales[row // 128 * 512 + row % 32 * 16 + row % 128 // 32 * 4] = w[1][ref.tile_at(300, 1, "cuda")[:, 0]]
+    out = torch.empty(T, W, dtype=torch.bfloat16, device="cuda")
+    rra.rra_mx4_product(x, [(codes, scales)], [out], K)
+    close(out[:, last:], xv @ wv.t(), xv.abs() @ wv.abs().t(), K, "bf16")
+    assert not out[:, last - 5000:last].any() and not out[-1, :1000].any()
+    few = torch.empty(1, W, dtype=torch.bfloat16, device="cuda")
+    rra.rra_mx4_product((x[0][:1].contiguous(), x[1][:512]), [(codes, scales)], [few], K)
+    assert torch.equal(few[:, last:], out[:1, last:]) and not few[:, :last].any()
+
+
+def test_logits_past_32_bits():
+    rows, V = 17000, 262144
+    l = torch.zeros(rows, V, dtype=torch.bfloat16, device="cuda")
+    at = torch.randint(0, V, (rows,), generator=gen(4), device="cuda")
+    l[torch.arange(rows, device="cuda"), at] = 50.0  # all but sure
+    token = torch.empty(rows, dtype=torch.int64, device="cuda")
+    rra.rra_vocab_sample([l], torch.full((rows,), 0.5, device="cuda"), token,
+                         top_k=torch.full((rows,), 5, dtype=torch.int32, device="cuda"))
+    assert torch.equal(token, at)
