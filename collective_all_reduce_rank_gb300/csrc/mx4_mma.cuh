@@ -82,12 +82,14 @@ __device__ __forceinline__ void mx4_mma(uint32_t d, uint64_t a, uint64_t b, uint
 // 32 columns of one row of a gated block's activations, quantised and stored.
 // `valid`: columns the row has from here on (0: none, the scale byte 0 alone).
 __device__ __forceinline__ void mx4_put_row(float* v, int valid, uint8_t* codes, uint8_t* scale) {
+  if (valid < 32) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (j >= valid) v[j] = 0.f;
+  }
   uint32_t m = 0;
 #pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    if (j >= valid) v[j] = 0.f;
-    m = max(m, mx_abs(v[j]));
-  }
+  for (int j = 0; j < 32; ++j) m = max(m, mx_abs(v[j]));
   const uint32_t byte = mx_scale(m);
   const float inv = mx_inverse(byte);
   uint32_t w[4];
