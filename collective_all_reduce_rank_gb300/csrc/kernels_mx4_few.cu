@@ -1,5 +1,5 @@
-// kernels_mx4_few.cu -- products of MX4 matrices for up to 128 tokens, where
-// reading the weights is the time.
+// kernels_mx4_few.cu -- products of MX4 matrices for few tokens (up to 128,
+// mx4_few_most below), where reading the weights is the time.
 //
 // The weights are the product's long side: a CTA takes 128 weight rows (gated:
 // 128 of the gate's and the same 128 of the up projection's) against all tokens
@@ -110,6 +110,53 @@ __device__ __forceinline__ void few_put(const Mx4Args& p, const Mx4Group& g, int
     if ((lane & 7) == 0 && row0 < g.rows)
       *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(g.out) + (long long)token * g.ld + row0 / 2 + lane / 2) = w;
     if (lane == 0) g.out_scales[mx_scale_at((size_t)token, (size_t)(row0 / 32), (size_t)g.across)] = (uint8_t)byte;
+  }
+}
+
+// n of 16 tokens from `token` on, side by side: token after token, a reduction,
+// a conversion and three exchanges of each took 300 cycles.
+template <int ACT>
+__device__ __forceinline__ void few_put16(const Mx4Args& p, const Mx4Group& g, int row0, int token, int n,
+                                          const float* a, const float* b) {
+  const int lane = threadIdx.x & 31, row = row0 + lane;
+  if constexpr (ACT < 0) {
+    const bool live = row < g.rows;
+    const long long at = (long long)token * g.ld + row;
+    if (p.f32) {
+      float* o = static_cast<float*>(g.out) + at;
+#pragma unroll
+      for (int j = 0; j < 16; ++j, o += g.ld)
+        if (live && j < n) *o = a[j];
+    } else {
+      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(g.out) + at;
+#pragma unroll
+      for (int j = 0; j < 16; ++j, o += g.ld)
+        if (live && j < n) *o = __float2bfloat16_rn(a[j]);
+    }
+  } else {
+    float v[16];
+    uint32_t byte[16], w[16], mine = 0;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      float unused;
+      v[j] = row < g.rows ? a[j] * gate_sigma<ACT>(a[j], &unused) * b[j] : 0.f;
+      byte[j] = mx_scale(__reduce_max_sync(0xffffffffu, mx_abs(v[j])));
+    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      w[j] = byte[j] == kMxNan ? 0u : mx_code(v[j] * mx_inverse(byte[j])) << (4 * (lane & 7));
+      if (lane == j) mine = byte[j];
+    }
+#pragma unroll
+    for (int i = 1; i <= 4; i *= 2)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) w[j] |= __shfl_xor_sync(0xffffffffu, w[j], i);
+    uint8_t* o = static_cast<uint8_t*>(g.out) + (long long)token * g.ld + row0 / 2 + lane / 2;
+    const bool word = (lane & 7) == 0 && row0 < g.rows;
+#pragma unroll
+    for (int j = 0; j < 16; ++j, o += g.ld)
+      if (word && j < n) *reinterpret_cast<uint32_t*>(o) = w[j];
+    if (lane < n) g.out_scales[mx_scale_at((size_t)(token + lane), (size_t)(row0 / 32), (size_t)g.across)] = (uint8_t)mine;
   }
 }
 
@@ -261,9 +308,14 @@ __global__ void __launch_bounds__(kFewThreads, 1) mx4_few_kernel(const __grid_co
           float v[G][16];
 #pragma unroll
           for (int i = 0; i < G; ++i) few_ld16(addr + i * N + c, v[i]);
+          const int n = min(p.tokens - c, 16);
+          if (n <= 4) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (c + j < p.tokens) few_put<ACT>(p, g, row0, c + j, v[0][j], v[G - 1][j]);
+            for (int j = 0; j < 4; ++j)
+              if (j < n) few_put<ACT>(p, g, row0, c + j, v[0][j], v[G - 1][j]);
+          } else {
+            few_put16<ACT>(p, g, row0, c, n, v[0], v[G - 1]);
+          }
         }
         tc_fence_before();
         __syncwarp();
@@ -293,16 +345,23 @@ __global__ void __launch_bounds__(kFewThreads, 1) mx4_few_kernel(const __grid_co
       if (lane < S) few_arrive(tc_smem(&sh.sums_full), lane);
       if (!__all_sync(0xffffffffu, tc_wait(tc_smem(&sh.sums_full), tile & 1, &sh, p.status, 7))) break;
       asm volatile("fence.acq_rel.cluster;" ::: "memory");
-      const int from = (int)rank * share;
-      for (int col = 0; col < share; ++col) {
-        if (from + col >= N || from + col >= p.tokens) break;
-        float v[G];
+      const int first = (int)rank * share, last = min(min(first + share, N), p.tokens);  // owned columns
+      const auto sum = [&](int i, int col) {
+        float v = 0.f;
+        for (int q = 0; q < S; ++q) v += mine[((q * G + i) * share + col) * kRows + lanes + lane];
+        return v;
+      };
+      if (last - first <= 4) {
+        for (int c = first; c < last; ++c) few_put<ACT>(p, g, row0, c, sum(0, c - first), sum(G - 1, c - first));
+      } else {
+        for (int c = first; c < last; c += 16) {
+          float v[G][16];
 #pragma unroll
-        for (int i = 0; i < G; ++i) {
-          v[i] = 0.f;
-          for (int q = 0; q < S; ++q) v[i] += mine[((q * G + i) * share + col) * kRows + lanes + lane];
+          for (int i = 0; i < G; ++i)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[i][j] = c + j < last ? sum(i, c + j - first) : 0.f;
+          few_put16<ACT>(p, g, row0, c, min(last - c, 16), v[0], v[G - 1]);
         }
-        few_put<ACT>(p, g, row0, from + col, v[0], v[G - 1]);
       }
       __syncwarp();
       if (lane < S) few_arrive(tc_smem(&sh.sums_empty), lane);
@@ -341,13 +400,15 @@ template <int N, int ACT>
 cudaError_t few_go(Mx4Args& p, cudaStream_t s, int* grid_out) {
   using F = Few<N, (ACT >= 0)>;
   // the split whose slowest CTA has the fewest K tiles; a sum through the
-  // cluster costs about what two stages do
+  // cluster costs about what 4 + columns / 8 stages do (1024 x 2 x 704 row-
+  // parallel, 6 K tiles: split 6 ways 5.5 us for 16 tokens and 15.7 for 128,
+  // unsplit 4.8 and 6.3; 5120 x 8 x 1728, 56 K tiles: 13.9 split 3 ways)
   int best = 1;
   long long least = -1;
   for (int split = 1; split <= kMaxSplit; ++split) {
     if (split > p.kblocks || resident(split) < 1 || F::stages(split) < 3) break;
     const long long waves = (p.tiles + resident(split) - 1) / resident(split);
-    const long long cost = waves * ((p.kblocks + split - 1) / split + (split > 1 ? 2 : 0));
+    const long long cost = waves * ((p.kblocks + split - 1) / split + (split > 1 ? 4 + F::G * N / 8 : 0));
     if (least < 0 || cost < least) {
       least = cost;
       best = split;
@@ -380,10 +441,28 @@ cudaError_t few_go(Mx4Args& p, cudaStream_t s, int* grid_out) {
 template <int N>
 cudaError_t few_act(Mx4Args& p, bool gated, cudaStream_t s, int* grid) {
   if (!gated) return few_go<N, -1>(p, s, grid);
-  return p.act == RRA_ACT_SILU ? few_go<N, RRA_ACT_SILU>(p, s, grid) : few_go<N, RRA_ACT_GELU_TANH>(p, s, grid);
+  if constexpr (N > 32)
+    return cudaErrorInvalidValue;  // mx4_few_most
+  else
+    return p.act == RRA_ACT_SILU ? few_go<N, RRA_ACT_SILU>(p, s, grid) : few_go<N, RRA_ACT_GELU_TANH>(p, s, grid);
 }
 
 }  // namespace
+
+// Both kernels, us in a graph, this one first (2070 MHz, 152 SMs):
+//                                  tokens   16         32         64        100        128
+//   131072 x 5120                       61 / 80    61 / 73    59 / 66    62 / 68    63 / 69
+//   3 x 50021 x 515                    8.3 / 16   9.4 / 16    11 / 16    14 / 17    14 / 17
+//   5120 x 13824 row-parallel           14 / 22    15 / 22    19 / 23    25 / 23    26 / 24
+//   1024 x 1408 row-parallel           4.8 / 6.0  4.9 / 6.0  5.4 / 6.2  6.2 / 6.7  6.3 / 7.0
+//   gated 13824 rows of K 5120          18 / 23    20 / 23    25 / 21    31 / 21    34 / 21
+//   gated 1408 rows of K 1024          6.5 / 6.4  8.7 / 6.4   13 / 6.4   19 / 6.5   22 / 6.7
+// A gated tile's four epilogue warps quantise 2 us per 16 tokens; behind many
+// tiles the next one's products hide some of it.
+size_t mx4_few_most(size_t rows, bool gated) {
+  const size_t bands = rows / kRows, sms = (size_t)device_sms();
+  return gated ? (bands < sms / 2 ? 16 : 32) : bands < sms ? 64 : 128;
+}
 
 int mx4_few_tile(size_t tokens) { return tokens <= 16 ? 16 : tokens <= 32 ? 32 : tokens <= 64 ? 64 : 128; }
 

@@ -63,7 +63,7 @@ struct Plan {
   bool few, gated;
   int x_box, w_bands;
   size_t tile;  // weight rows (gated: of each projection)
-  Plan(size_t tokens, bool g) : few(tokens <= (size_t)kMx4Few), gated(g) {
+  Plan(size_t tokens, size_t rows, bool g) : few(tokens <= mx4_few_most(rows, g)), gated(g) {
     x_box = few ? mx4_few_tile(tokens) : 128;
     tile = few || gated ? 128 : 256;
     w_bands = few || gated ? 1 : 2;
@@ -185,7 +185,9 @@ rra_status_t rra_mx4_product(const rra_mx4_t* x, const rra_mx4_t* weights, void*
   const size_t e = size_of(dtype);
   for (int r = 0; r < nranks; ++r) f(bad_matrix(widths[r], D) || bad_matrix(T, widths[r]), RRA_ERR_UNSUPPORTED);
   if (f.st != RRA_SUCCESS) return done(call, nranks, 0, dtype, 0, f.st);
-  const Plan plan(T, false);
+  size_t rows = 0;
+  for (int r = 0; r < nranks; ++r) rows += widths[r];
+  const Plan plan(T, rows, false);
   f(mx_check(*x, T, D));
   Ranges in, o;
   mx_ranges(in, *x, T, D);
@@ -239,7 +241,7 @@ rra_status_t rra_mx4_product_sum(const rra_mx4_t* xs, const rra_mx4_t* weights, 
     RRA_ERR_UNSUPPORTED);
   if (f.st != RRA_SUCCESS) return done(call, nranks, count, dtype, 0, f.st);
   const size_t e = size_of(dtype);
-  const Plan plan(T, false);
+  const Plan plan(T, D, false);
   f(!aligned(out, e), RRA_ERR_INVALID_ARG);
   Ranges in;
   for (int r = 0; r < nranks; ++r) {
@@ -291,7 +293,7 @@ rra_status_t rra_mx4_gated_ffn(const rra_mx4_t* x, const rra_mx4_t* gates, const
     RRA_ERR_INVALID_ARG);
   f(bad_matrix(T, D) || bad_matrix(F, D) || bad_matrix(T, F), RRA_ERR_UNSUPPORTED);
   if (f.st != RRA_SUCCESS) return done(call, nranks, count, dt, 0, f.st);
-  const Plan plan(T, true);
+  const Plan plan(T, F * nranks, true);
   f(mx_check(*x, T, D));
   Ranges in, o;
   mx_ranges(in, *x, T, D);

@@ -62,11 +62,12 @@ struct Mx4Args {
 bool mx4_map_codes(CUtensorMap* m, const void* base, size_t row_bytes, size_t rows, int box_rows);
 bool mx4_map_scales(CUtensorMap* m, const void* base, size_t across, size_t bands, int box_bands);
 
-// More than kMx4Few tokens: tiles of 256 tokens x 256 weight rows (gated: 128
-// of the gate's and the same 128 of the up projection's).
+// Many tokens: tiles of 256 tokens x 256 weight rows (gated: 128 of the gate's
+// and the same 128 of the up projection's).
 cudaError_t launch_mx4_product(const Mx4Args& p, bool gated, cudaStream_t s, int* grid);
-// Up to kMx4Few tokens: tiles of 128 weight rows x all tokens.
-constexpr int kMx4Few = 128;
+// Few: tiles of 128 weight rows x all tokens, for calls of
+// mx4_few_most(weight rows, gated) tokens at most.
+size_t mx4_few_most(size_t rows, bool gated);
 int mx4_few_tile(size_t tokens);  // columns of a tile
 // Picks p.split and p.stages.
 cudaError_t launch_mx4_few(Mx4Args& p, bool gated, cudaStream_t s, int* grid);
