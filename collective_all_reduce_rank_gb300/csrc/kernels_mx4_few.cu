@@ -452,7 +452,7 @@ cudaError_t few_act(Mx4Args& p, bool gated, cudaStream_t s, int* grid) {
 // Both kernels, us in a graph, this one first (2070 MHz, 152 SMs):
 //                                  tokens   16         32         64        100        128
 //   131072 x 5120                       61 / 80    61 / 73    59 / 66    62 / 68    63 / 69
-//   3 x 50021 x 515                    8.3 / 16   9.4 / 16    11 / 16    14 / 17    14 / 17
+//   50021 x 515 (3 shards)             8.3 / 16   9.4 / 16    11 / 16    14 / 17    14 / 17
 //   5120 x 13824 row-parallel           14 / 22    15 / 22    19 / 23    25 / 23    26 / 24
 //   1024 x 1408 row-parallel           4.8 / 6.0  4.9 / 6.0  5.4 / 6.2  6.2 / 6.7  6.3 / 7.0
 //   gated 13824 rows of K 5120          18 / 23    20 / 23    25 / 21    31 / 21    34 / 21
