@@ -179,6 +179,55 @@ struct Logit<RRA_BFLOAT16> {
   };
 };
 
+// The positions of a unit whose logits lie in a range of keys, as bits: bit(j)
+// for the j-th, pos() back.  NaN, a position without a logit, is in none.  A
+// range that ends with the key of -0, which no logit has, ends below it: as a
+// value it would take in 0, whose key is behind the range.
+template <int DT>
+struct Within;
+template <>
+struct Within<RRA_FLOAT32> {
+  float lo, hi;
+  __device__ __forceinline__ Within(uint32_t from, uint32_t to)
+      : lo(Logit<RRA_FLOAT32>::value(from)), hi(Logit<RRA_FLOAT32>::value(to - (to == 0x7FFFFFFFu ? 1 : 0))) {}
+  static __device__ __forceinline__ int bit(int j) { return j; }
+  static __device__ __forceinline__ int pos(int i) { return i; }
+  __device__ __forceinline__ uint32_t up(const uint4& x) const {  // from lo on
+    return (__uint_as_float(x.x) >= lo ? 1u : 0u) | (__uint_as_float(x.y) >= lo ? 2u : 0u) |
+           (__uint_as_float(x.z) >= lo ? 4u : 0u) | (__uint_as_float(x.w) >= lo ? 8u : 0u);
+  }
+  __device__ __forceinline__ uint32_t both(const uint4& x) const {
+    return up(x) & ((__uint_as_float(x.x) <= hi ? 1u : 0u) | (__uint_as_float(x.y) <= hi ? 2u : 0u) |
+                    (__uint_as_float(x.z) <= hi ? 4u : 0u) | (__uint_as_float(x.w) <= hi ? 8u : 0u));
+  }
+};
+// bfloat16: two positions a comparison, so even ones from bit 0 on, odd ones
+// from bit 16 on (one at a time a unit's mask took 45 instructions, not 16).
+template <>
+struct Within<RRA_BFLOAT16> {
+  __nv_bfloat162 lo, hi;
+  static __device__ __forceinline__ __nv_bfloat162 two(uint32_t key) {
+    return __float2bfloat162_rn(Logit<RRA_BFLOAT16>::value(key));
+  }
+  __device__ __forceinline__ Within(uint32_t from, uint32_t to) : lo(two(from)), hi(two(to - (to == 0x7FFFu ? 1 : 0))) {}
+  static __device__ __forceinline__ int bit(int j) { return j / 2 + 16 * (j & 1); }
+  static __device__ __forceinline__ int pos(int i) { return 2 * (i & 15) + (i >> 4); }
+  static __device__ __forceinline__ __nv_bfloat162 pair(const uint32_t& w) {
+    return *reinterpret_cast<const __nv_bfloat162*>(&w);
+  }
+  static __device__ __forceinline__ uint32_t bits(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return (a & 0x10001u) | (b & 0x20002u) | (c & 0x40004u) | (d & 0x80008u);
+  }
+  __device__ __forceinline__ uint32_t up(const uint4& x) const {
+    return bits(__hge2_mask(pair(x.x), lo), __hge2_mask(pair(x.y), lo), __hge2_mask(pair(x.z), lo),
+                __hge2_mask(pair(x.w), lo));
+  }
+  __device__ __forceinline__ uint32_t both(const uint4& x) const {
+    return up(x) & bits(__hle2_mask(pair(x.x), hi), __hle2_mask(pair(x.y), hi), __hle2_mask(pair(x.z), hi),
+                        __hle2_mask(pair(x.w), hi));
+  }
+};
+
 // A unit with the positions outside [from, to) set to `raw`.
 template <int DT>
 __device__ __forceinline__ uint4 only(const uint4& x, int from, int to, uint32_t raw) {
@@ -346,6 +395,7 @@ __device__ __forceinline__ int locate(unsigned long long sum, uint32_t ties, uns
 template <int DT>
 struct Row {
   using L = Logit<DT>;
+  using W = Within<DT>;
   static constexpr int PU = Elem<DT>::kPerUnit;
   const uint4* slice;
   int units;
@@ -357,8 +407,11 @@ struct Row {
   int flip;
   int& level;  // parity of the histogram in use
 
-  // Logits above this are kept: -infinity, which weighs nothing, without a bound.
-  static __device__ __forceinline__ float bound_of(const Bound& b) { return b.key ? L::value(b.key) : -INFINITY; }
+  // The smallest key from `low` on that a bound keeps whatever its index.  (What
+  // is behind infinity's key is NaN, the end of no range.)
+  static __device__ __forceinline__ uint32_t above(const Bound& b, float low) {
+    return max(L::from(low), b.key ? b.key + 1 : 0u);
+  }
 
   __device__ __forceinline__ uint32_t* bins() const { return hist + (level & 1) * 4 * kBins; }
 
@@ -374,43 +427,37 @@ struct Row {
     for (int j = 0; j < PU; ++j) f(PU == 4 ? w[j] : (w[j / 2] >> (16 * (j & 1))) & 0xFFFFu);
   }
 
-  // f(raw) for the positions of unit u that `is` picks, few of them: one at a
+  // f(raw) for the positions of unit u that are in `mask`, few of them: one at a
   // time a lane, so that a warp's steps are those of its fullest lane.
-  template <class Is, class F>
-  __device__ __forceinline__ void picked(int u, Is is, F f) const {
-    uint32_t mask = 0;
-    int j = 0;
-    unit(slice[u], [&](uint32_t raw) { mask |= (is(L::real(raw)) ? 1u : 0u) << j++; });
+  template <class F>
+  __device__ __forceinline__ void picked(int u, uint32_t mask, F f) const {
     while (mask) {
-      const int at = u * PU + __ffs(mask) - 1;
+      const int at = u * PU + W::pos(__ffs(mask) - 1);
       mask &= mask - 1;
       f(raw_at(at));
     }
   }
 
-  // The warp's sum of w over the positions of units [from, to) that `is` picks:
-  // unit by unit, one at a time a lane where they are few, all of a unit's
-  // positions side by side where they are many.
-  template <class Is, class W>
-  __device__ __forceinline__ unsigned long long sum_of(int from, int to, int step, Is is, W w) const {
+  // The warp's sum of the weights in units [from, to) from key `lo` on, `each`
+  // called with every unit: unit by unit, one at a time a lane where they are
+  // few, all of a unit's positions side by side where they are many.
+  template <class Each>
+  __device__ __forceinline__ unsigned long long sum_of(int from, int to, int step, uint32_t lo, Each each) const {
+    const W in(lo, lo);
     unsigned long long sum = 0;
     for (int base = from; base < to; base += step) {
       const int u = base + (int)(threadIdx.x & 31);
       uint4 x = make_uint4(~0u, ~0u, ~0u, ~0u);  // no position
       if (u < to) x = slice[u];
-      uint32_t mask = 0;
-      int j = 0;
-      unit(x, [&](uint32_t raw) { mask |= (is(L::real(raw)) ? 1u : 0u) << j++; });
+      each(x);
+      uint32_t mask = in.up(x);
       if (__any_sync(0xffffffffu, __popc(mask) > PU / 2)) {
-        j = 0;
+        int j = 0;
         unit(x, [&](uint32_t raw) {
-          if (mask >> j++ & 1) sum += w(L::real(raw));
+          if (mask >> W::bit(j++) & 1) sum += weight(sh, c, L::real(raw));
         });
       } else {
-        while (mask) {
-          sum += w(L::real(raw_at(u * PU + __ffs(mask) - 1)));
-          mask &= mask - 1;
-        }
+        picked(u, mask, [&](uint32_t raw) { sum += weight(sh, c, L::real(raw)); });
         __syncwarp();
       }
     }
@@ -430,21 +477,20 @@ struct Row {
   // elements fit a word) and, in a fourth word, they.
   __device__ __forceinline__ void fill(const Range& r, const Bound& keep, int words) const {
     uint32_t* h = bins();
-    const float bound = bound_of(keep), low = fmaxf(L::value(r.lo), c.low), high = L::value(r.hi);
+    const W in(max(r.lo, above(keep, c.low)), r.hi);
     for (int u = threadIdx.x; u < units; u += kThreads)
-      picked(u, [&](float l) { return l >= low && l <= high && l > bound; },  // no position (NaN): false
-             [&](uint32_t raw) {
-               uint32_t* at = h + ((r.hi - L::key(raw)) >> r.shift);
-               if (words == 1) {
-                 atomicAdd(at, 1u);
-                 return;
-               }
-               const unsigned long long w = weight(sh, c, L::real(raw));
-               atomicAdd(at, (uint32_t)w & 0x7FFFu);
-               if (w >> 15) atomicAdd(at + kBins, (uint32_t)(w >> 15) & 0x7FFFu);
-               if (w >> 30) atomicAdd(at + 2 * kBins, (uint32_t)(w >> 30));
-               atomicAdd(at + 3 * kBins, 1u);
-             });
+      picked(u, in.both(slice[u]), [&](uint32_t raw) {
+        uint32_t* at = h + ((r.hi - L::key(raw)) >> r.shift);
+        if (words == 1) {
+          atomicAdd(at, 1u);
+          return;
+        }
+        const unsigned long long w = weight(sh, c, L::real(raw));
+        atomicAdd(at, (uint32_t)w & 0x7FFFu);
+        if (w >> 15) atomicAdd(at + kBins, (uint32_t)(w >> 15) & 0x7FFFu);
+        if (w >> 30) atomicAdd(at + 2 * kBins, (uint32_t)(w >> 30));
+        atomicAdd(at + 3 * kBins, 1u);
+      });
     __syncwarp();
   }
 
@@ -567,7 +613,6 @@ struct Row {
   __device__ __forceinline__ Bound heaviest(const Bound& keep, float share) {
     const uint32_t near = near_key(), low = min(L::from(c.low), most);
     const unsigned long long extra = keep.key ? weight(sh, c, L::value(keep.key)) * keep.ties : 0;
-    const float bound = bound_of(keep);
     unsigned long long above = 0, after, target = 0, v[2];
     Range r = with_bins(near, most);
     for (bool first = true, wide = low < near;; first = false) {
@@ -575,9 +620,8 @@ struct Row {
       clear(r, words + (words > 1));
       fill(r, keep, words);
       if (first) {
-        const unsigned long long all = publish(sum_of(
-            (threadIdx.x >> 5) * 32, units, kThreads, [&](float l) { return l > bound && l >= c.low; },
-            [&](float l) { return weight(sh, c, l); }));
+        const unsigned long long all = publish(
+            sum_of((threadIdx.x >> 5) * 32, units, kThreads, Row::above(keep, c.low), [](const uint4&) {}));
         const unsigned long long part = share_of(all + extra, share, true);
         target = part ? part : 1;
       } else {
@@ -619,14 +663,12 @@ struct Row {
   // after another; every lane gets them.
   __device__ __forceinline__ void weigh(int from, int to, const Bound& keep, float low, unsigned long long& sum,
                                         uint32_t& ties) const {
-    const float bound = bound_of(keep);
+    const bool tied = keep.key && L::value(keep.key) >= low;
+    const W at(keep.key, keep.key);
     ties = 0;
-    sum = sum_of(from, to, 32,
-                 [&](float l) {
-                   ties += l == bound && l >= low;
-                   return l > bound && l >= low;
-                 },
-                 [&](float l) { return weight(sh, c, l); });
+    sum = sum_of(from, to, 32, above(keep, low), [&](const uint4& x) {
+      if (tied) ties += __popc(at.both(x));
+    });
     ties = __reduce_add_sync(0xffffffffu, ties);
   }
 
@@ -634,20 +676,20 @@ struct Row {
   // passes `rest`; w: its weight.
   __device__ __forceinline__ int draw(int from, int to, const Bound& keep, float low, unsigned long long unit_w,
                                       unsigned long long rest, uint32_t allow, unsigned long long& w) const {
-    const float bound = bound_of(keep);
+    const float bound = keep.key ? L::value(keep.key) : -INFINITY;  // which weighs nothing
+    const W in(max(L::from(low), keep.key), keep.key);
     const int lane = threadIdx.x & 31;
     for (int base = from; base < to; base += 32) {
       unsigned long long sum = 0;
       uint32_t ties = 0;
       if (base + lane < to)
-        picked(base + lane, [&](float l) { return l >= bound && l >= low; },
-               [&](uint32_t raw) {
-                 const float l = L::real(raw);
-                 if (l == bound)
-                   ++ties;
-                 else
-                   sum += weight(sh, c, l);
-               });
+        picked(base + lane, in.up(slice[base + lane]), [&](uint32_t raw) {
+          const float l = L::real(raw);
+          if (l == bound)
+            ++ties;
+          else
+            sum += weight(sh, c, l);
+        });
       __syncwarp();
       const int hit = locate(sum, ties, unit_w, rest, allow);
       if (hit >= 0) {  // the unit's positions side by side

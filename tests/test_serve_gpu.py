@@ -351,6 +351,23 @@ def test_sample_masks_and_extremes(dtype):
         check_sample(l, [1500, 1500], **k)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_sample_zeros_behind_a_range(dtype):
+    """The nearest logits searched first end exactly at zero: zeros count as
+    theirs, not as the ones below, which end with the key of -0."""
+    bits = torch.tensor([0x03FF], dtype=torch.int16).view(torch.bfloat16).float()  # 1023 keys above 0
+    top = {"bf16": float(bits), "fp32": float(torch.tensor(16.0) / torch.tensor(1.44269502))}[dtype]  # 16 octaves at 1
+    g = gen(77)
+    l = -top * torch.rand(6, 900, generator=g, device="cuda")
+    l[:, 100:250] = 0.0
+    l[:, 300:360] = top * torch.rand(6, 60, generator=g, device="cuda")
+    l[:, 500] = top
+    l = l.to(DT[dtype])
+    t = {"bf16": 1e-29, "fp32": 1.0}[dtype]
+    check_sample(l, [450, 450], temperature=[t] * 6, top_k=[30, 100, 211, 212, 600, 0],
+                 top_p=[1.0, 1.0, 1.0, 0.99, 1.0, 0.5], min_p=[0.0] * 6)
+
+
 def test_sample_ends_of_the_range():
     l = torch.randn(4, 1000, generator=gen(9), device="cuda")
     token = torch.empty(4, dtype=torch.int64, device="cuda")
