@@ -201,10 +201,54 @@ def test_product_sum(T, n, F, D):
         assert torch.equal(out, again)
 
 
+@pytest.mark.parametrize("T", [33, 64, 65, 100, 128, 129])
+def test_product_of_many_rows(T):
+    """Weights for every SM, of several tiles a CTA: more tokens go to the kernel of few."""
+    K, widths = 300, [20000, 8001]
+    g = gen(T)
+    x, xv = matrix(g, T, K)
+    ws, vs = zip(*[matrix(g, w, K, K ** -0.5) for w in widths])
+    for dtype in ("bf16", "fp32"):
+        outs = [torch.full((T, w), math.nan, dtype=DT[dtype], device="cuda") for w in widths]
+        rra.rra_mx4_product(x, list(ws), outs, K)
+        for o, v in zip(outs, vs):
+            close(o, xv @ v.t(), xv.abs() @ v.abs().t(), K, dtype)
+
+
+@pytest.mark.parametrize("T", [5, 17, 64, 100])
+def test_product_sum_of_long_rows(T):
+    """A K axis shared by a cluster: sums of few and of many columns a CTA."""
+    n, F, D = 3, 2100, 700
+    g = gen(T)
+    xs, xv = zip(*[matrix(g, T, F) for _ in range(n)])
+    ws, wv = zip(*[matrix(g, D, F, F ** -0.5) for _ in range(n)])
+    want = sum(a @ b.t() for a, b in zip(xv, wv))
+    terms = sum(a.abs() @ b.abs().t() for a, b in zip(xv, wv))
+    for dtype in ("bf16", "fp32"):
+        out = torch.full((T, D), math.nan, dtype=DT[dtype], device="cuda")
+        rra.rra_mx4_product_sum(list(xs), list(ws), out, F)
+        close(out, want, terms, n * F + 64 * n, dtype)
+
+
 @pytest.mark.parametrize("kind", [rra.RRA_ACT_SILU, rra.RRA_ACT_GELU_TANH])
 @pytest.mark.parametrize("T", [1, 16, 40, 64, 65, 128, 129, 300])
 @pytest.mark.parametrize("n,D,F", [(1, 64, 32), (2, 515, 129), (3, 256, 300), (8, 1024, 64)])
 def test_gated(T, n, D, F, kind):
+    gated_case(T, n, D, F, kind)
+
+
+@pytest.mark.parametrize("kind", [rra.RRA_ACT_SILU, rra.RRA_ACT_GELU_TANH])
+@pytest.mark.parametrize("T", [3, 17, 20, 32, 33])
+def test_gated_of_many_rows(T, kind):
+    gated_case(T, 2, 300, 5001, kind)
+
+
+@pytest.mark.parametrize("T", [2, 16])
+def test_gated_of_long_rows(T):
+    gated_case(T, 1, 9000, 260, rra.RRA_ACT_SILU)
+
+
+def gated_case(T, n, D, F, kind):
     g = gen(T + F)
     x, xv = matrix(g, T, D)
     gates, gv = zip(*[matrix(g, F, D, D ** -0.5) for _ in range(n)])
