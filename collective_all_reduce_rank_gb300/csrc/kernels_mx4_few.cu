@@ -271,8 +271,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) mx4_few_kernel(const __grid_co
           for (int j = 0; j < 2; ++j) {
 #pragma unroll
             for (int i = 0; i < G; ++i)
-              mx4_put_scales<false>(tmem + F::kColW + 8 * i + 4 * j, at + kSW + i * kWScales + 512 * j);
-            mx4_put_scales<false>(tmem + F::kColX + 4 * j, at + kSX + 512 * j);
+              mx4_put_scales(tmem + F::kColW + 8 * i + 4 * j, at + kSW + i * kWScales + 512 * j);
+            mx4_put_scales(tmem + F::kColX + 4 * j, at + kSX + 512 * j);
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i)

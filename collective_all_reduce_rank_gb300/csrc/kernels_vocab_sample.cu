@@ -459,8 +459,10 @@ struct Row {
       uint32_t mask = in.up(x);
       if (__any_sync(0xffffffffu, __popc(mask) > PU / 2)) {
         int j = 0;
-        unit(x, [&](uint32_t raw) {
-          if (mask >> W::bit(j++) & 1) sum += weight(sh, c, L::real(raw));
+        unit(x, [&](uint32_t raw) {  // without a branch: the weights' steps overlap
+          const bool is = mask >> W::bit(j++) & 1;
+          const unsigned long long w = weight(sh, c, is ? L::real(raw) : c.top);
+          sum += is ? w : 0;
         });
       } else {
         picked(u, mask, [&](uint32_t raw) { sum += weight(sh, c, L::real(raw)); });
@@ -480,17 +482,38 @@ struct Row {
 
   // The slice's elements in range and above `keep`'s key, counted by bins, or
   // their weights added (words == 3: pieces of 15 bits, whose sums of up to 2^17
-  // elements fit a word) and, in a fourth word, they.
-  __device__ __forceinline__ void fill(const Range& r, const Bound& keep, int words) const {
+  // elements fit a word) and, in a fourth word, they.  many: the range may hold
+  // much of the slice, so that counts of full units go side by side (256 x 131072
+  // bf16 143 us without, 134 with; in narrow ranges the vote costs 0.5 us).
+  __device__ __forceinline__ void fill(const Range& r, const Bound& keep, int words, bool many) const {
     uint32_t* h = bins();
     const W in(max(r.lo, above(keep, c.low)), r.hi);
+    const auto count = [&](uint32_t raw) { atomicAdd(h + ((r.hi - L::key(raw)) >> r.shift), 1u); };
+    if (words == 1 && many) {
+      for (int base = (int)(threadIdx.x & ~31u); base < units; base += kThreads) {
+        const int u = base + (int)(threadIdx.x & 31);
+        uint4 x = make_uint4(~0u, ~0u, ~0u, ~0u);  // no position
+        if (u < units) x = slice[u];
+        const uint32_t mask = in.both(x);
+        if (__any_sync(0xffffffffu, __popc(mask) > PU / 2)) {
+          int j = 0;
+          unit(x, [&](uint32_t raw) {
+            if (mask >> W::bit(j++) & 1) count(raw);
+          });
+        } else {
+          picked(u, mask, count);
+        }
+        __syncwarp();
+      }
+      return;
+    }
     for (int u = threadIdx.x; u < units; u += kThreads)
       picked(u, in.both(slice[u]), [&](uint32_t raw) {
-        uint32_t* at = h + ((r.hi - L::key(raw)) >> r.shift);
         if (words == 1) {
-          atomicAdd(at, 1u);
+          count(raw);
           return;
         }
+        uint32_t* at = h + ((r.hi - L::key(raw)) >> r.shift);
         const unsigned long long w = weight(sh, c, L::real(raw));
         atomicAdd(at, (uint32_t)w & 0x7FFFu);
         if (w >> 15) atomicAdd(at + kBins, (uint32_t)(w >> 15) & 0x7FFFu);
@@ -595,9 +618,9 @@ struct Row {
     const uint32_t near = near_key(), low = min(L::from(c.low), most);
     unsigned long long above = 0, after, v[2];
     Range r = with_bins(near, most);
-    for (bool wide = low < near;;) {
+    for (bool wide = low < near, many = true;;) {
       clear(r, 1);
-      fill(r, {0, 0}, 1);
+      fill(r, {0, 0}, 1, many);
       cluster_sync();
       gather(r, 1, v);
       const int b = reach(r, v, above, after, k);
@@ -605,6 +628,7 @@ struct Row {
         if (r.shift == 0) return {r.hi - (uint32_t)b, (uint32_t)(k - above)};
         r = bin_keys(r, b);
         if (after == k) return all_from(r.lo);  // the whole bin, often one element
+        many = false;
       } else {
         if (!wide) return {0, 0};
         r = with_bins(low, near - 1);
@@ -624,7 +648,7 @@ struct Row {
     for (bool first = true, wide = low < near;; first = false) {
       const int words = r.shift ? 3 : 1;
       clear(r, words + (words > 1));
-      fill(r, keep, words);
+      fill(r, keep, words, first);
       if (first) {
         const unsigned long long all = publish(
             sum_of((threadIdx.x >> 5) * 32, units, kThreads, Row::above(keep, c.low), [](const uint4&) {}));

@@ -31,14 +31,9 @@ __device__ __forceinline__ uint64_t mx4_scale_desc(uint32_t addr) {
 }
 
 // A tile of scales (512 bytes) to four columns of tensor memory, once for each
-// quarter of the lanes.  It runs in order with the products around it.  PAIR:
-// in both CTAs, each from its own shared memory.
-template <bool PAIR>
+// quarter of the lanes.  It runs in order with the products around it.
 __device__ __forceinline__ void mx4_put_scales(uint32_t taddr, uint32_t addr) {
-  if constexpr (PAIR)
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(mx4_scale_desc(addr)) : "memory");
-  else
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(mx4_scale_desc(addr)) : "memory");
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(mx4_scale_desc(addr)) : "memory");
 }
 
 // TMA tile load into this CTA that counts on its own barrier.
