@@ -23,9 +23,9 @@
 // the cluster.
 //
 // One row of 131072 bf16 takes 12 us: some ten meetings of the cluster, one
-// after another.  256 such rows take 143 us, of which 10 are HBM: some 70
+// after another.  256 such rows take 135 us, of which 10 are HBM: some 70
 // instructions an element, issued in half of the cycles, and the meetings.  33
-// rows of 50021 float32 take 45: a search of float32 keys narrows two or three
+// rows of 50021 float32 take 42: a search of float32 keys narrows two or three
 // times where bfloat16's ends after one.
 #include <algorithm>
 #include <cfloat>
