@@ -117,8 +117,9 @@ __device__ __forceinline__ void few_put(const Mx4Args& p, const Mx4Group& g, int
   }
 }
 
-// n of 16 tokens from `token` on, side by side: token after token, a reduction,
-// a conversion and three exchanges of each took 300 cycles.
+// n of 16 tokens from `token` on, side by side.  Gated: rows and tokens change
+// places between lanes, so that a lane has half a token's block (a reduction, a
+// conversion and three exchanges a token: 16 tokens 2.2 us, this way 0.9).
 template <int ACT>
 __device__ __forceinline__ void few_put16(const Mx4Args& p, const Mx4Group& g, int row0, int token, int n,
                                           const float* a, const float* b) {
@@ -139,28 +140,31 @@ __device__ __forceinline__ void few_put16(const Mx4Args& p, const Mx4Group& g, i
     }
   } else {
     float v[16];
-    uint32_t byte[16], w[16], mine = 0;
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
       float unused;
       v[j] = row < g.rows ? a[j] * gate_sigma<ACT>(a[j], &unused) * b[j] : 0.f;
-      byte[j] = mx_scale(__reduce_max_sync(0xffffffffu, mx_abs(v[j])));
     }
+    // 16 x 16 values change places: lane l has rows 16 (l / 16) + j of token l % 16
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      w[j] = byte[j] == kMxNan ? 0u : mx_code(v[j] * mx_inverse(byte[j])) << (4 * (lane & 7));
-      if (lane == j) mine = byte[j];
-    }
+    for (int m = 8; m > 0; m /= 2)
 #pragma unroll
-    for (int i = 1; i <= 4; i *= 2)
-#pragma unroll
-      for (int j = 0; j < 16; ++j) w[j] |= __shfl_xor_sync(0xffffffffu, w[j], i);
-    uint8_t* o = static_cast<uint8_t*>(g.out) + (long long)token * g.ld + row0 / 2 + lane / 2;
-    const bool word = (lane & 7) == 0 && row0 < g.rows;
-#pragma unroll
-    for (int j = 0; j < 16; ++j, o += g.ld)
-      if (word && j < n) *reinterpret_cast<uint32_t*>(o) = w[j];
-    if (lane < n) g.out_scales[mx_scale_at((size_t)(token + lane), (size_t)(row0 / 32), (size_t)g.across)] = (uint8_t)mine;
+      for (int j = 0; j < 16; ++j) {
+        if (j & m) continue;
+        const bool up = lane & m;
+        const float got = __shfl_xor_sync(0xffffffffu, up ? v[j] : v[j + m], m);
+        v[j] = up ? got : v[j];
+        v[j + m] = up ? v[j + m] : got;
+      }
+    uint32_t most = max(mx_amax8(v), mx_amax8(v + 8));
+    most = max(most, __shfl_xor_sync(0xffffffffu, most, 16));
+    const uint32_t byte = mx_scale(most);
+    const float inv = mx_inverse(byte);
+    const uint2 w = make_uint2(mx_code8(v, inv, byte == kMxNan), mx_code8(v + 8, inv, byte == kMxNan));
+    const int t = lane & 15;
+    if (t < n && row0 < g.rows)
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(g.out) + (long long)(token + t) * g.ld + row0 / 2 + lane / 16 * 8) = w;
+    if (lane < n) g.out_scales[mx_scale_at((size_t)(token + t), (size_t)(row0 / 32), (size_t)g.across)] = (uint8_t)byte;
   }
 }
 
@@ -445,7 +449,7 @@ cudaError_t few_go(Mx4Args& p, cudaStream_t s, int* grid_out) {
 template <int N>
 cudaError_t few_act(Mx4Args& p, bool gated, cudaStream_t s, int* grid) {
   if (!gated) return few_go<N, -1>(p, s, grid);
-  if constexpr (N > 32)
+  if constexpr (N > 64)
     return cudaErrorInvalidValue;  // mx4_few_most
   else
     return p.act == RRA_ACT_SILU ? few_go<N, RRA_ACT_SILU>(p, s, grid) : few_go<N, RRA_ACT_GELU_TANH>(p, s, grid);
@@ -459,13 +463,12 @@ cudaError_t few_act(Mx4Args& p, bool gated, cudaStream_t s, int* grid) {
 //   50021 x 515 (3 shards)             8.3 / 16   9.4 / 16    11 / 16    14 / 17    14 / 17
 //   5120 x 13824 row-parallel           14 / 22    15 / 22    19 / 23    25 / 23    26 / 24
 //   1024 x 1408 row-parallel           4.8 / 6.0  4.9 / 6.0  5.4 / 6.2  6.2 / 6.7  6.3 / 7.0
-//   gated 13824 rows of K 5120          18 / 23    20 / 23    25 / 21    31 / 21    34 / 21
-//   gated 1408 rows of K 1024          6.5 / 6.4  8.7 / 6.4   13 / 6.4   19 / 6.5   22 / 6.7
-// A gated tile's four epilogue warps quantise 2 us per 16 tokens; behind many
-// tiles the next one's products hide some of it.
+//   gated 13824 rows of K 5120          16 / 25    18 / 24    20 / 21    24 / 21    25 / 21
+//   gated 1408 rows of K 1024          5.5 / 6.5  6.6 / 6.5  8.9 / 6.5   13 / 6.6   14 / 6.7
+// and gated 13824 rows for 33 tokens 18 / 29, 48 tokens 19 / 22.
 size_t mx4_few_most(size_t rows, bool gated) {
   const size_t bands = rows / kRows, sms = (size_t)device_sms();
-  return gated ? (bands < sms / 2 ? 16 : 32) : bands < sms ? 64 : 128;
+  return gated ? (bands < sms / 2 ? 32 : 48) : bands < sms ? 64 : 128;
 }
 
 int mx4_few_tile(size_t tokens) { return tokens <= 16 ? 16 : tokens <= 32 ? 32 : tokens <= 64 ? 64 : 128; }

@@ -238,7 +238,7 @@ def test_gated(T, n, D, F, kind):
 
 
 @pytest.mark.parametrize("kind", [rra.RRA_ACT_SILU, rra.RRA_ACT_GELU_TANH])
-@pytest.mark.parametrize("T", [3, 17, 20, 32, 33])
+@pytest.mark.parametrize("T", [3, 17, 20, 32, 33, 48, 49])
 def test_gated_of_many_rows(T, kind):
     gated_case(T, 2, 300, 5001, kind)
 
