@@ -12,8 +12,9 @@
 // float32 sums through distributed shared memory to the CTA that owns the
 // column, which adds them in the order of K.  Nothing depends on timing.
 //
-// A gated block's 32 columns are a warp's 32 lanes: their largest value is one
-// warp reduction, their codes four words of lanes or-ed together.
+// A gated block's 32 columns are a warp's 32 lanes.  Of up to four tokens the
+// largest value is one warp reduction, the codes four words of lanes or-ed
+// together; of more, lanes exchange rows for tokens.
 //
 // Bound by HBM: 1 token x 131072 x 5120 58 us (6.1 TB/s), x 5120 x 13824 row-
 // parallel 11 us, gated 16 (3.3 and 4.8 TB/s: 108 tiles for 152 SMs, and a
