@@ -680,7 +680,9 @@ struct Row {
         const int lane = threadIdx.x & 31;
         uint32_t n = __reduce_add_sync(0xffffffffu, lane < split ? peer_u32(elements + b, lane) : 0);
         if (extra && keep.key >= r.lo && keep.key <= r.hi) n = 2;
-        if (n == 1) return all_from(r.lo);  // it is its element that reaches the share
+        // it is its element that reaches the share; where `keep` ends inside the
+        // bin, that is the last one it leaves
+        if (n == 1) return keep.key >= r.lo ? keep : all_from(r.lo);
       } else {
         if (!wide) return keep;  // all of it
         r = with_bins(low, near - 1);
