@@ -597,8 +597,9 @@ struct Row {
 
   // The bound that keeps all keys from lo on.
   static __device__ __forceinline__ Bound all_from(uint32_t lo) {
-    // below zero's key lies that of -0, which no logit has and which is not below zero
-    return {L::value(lo) == 0.f ? lo - 2 : lo - 1, 0};
+    // below zero's key lies that of -0, which no logit has and whose value is not
+    // below zero; a range may begin with either
+    return {lo == L::key(0u) ? lo - 2 : lo - 1, 0};
   }
 
   __device__ __forceinline__ Range bin_keys(const Range& r, int b) const {

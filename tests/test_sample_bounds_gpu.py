@@ -103,3 +103,24 @@ def test_random_heads(dtype, seed):
         p = [1.0, 0.5, 0.9, 0.99, 0.999, 0.99999][int(torch.randint(0, 6, (1,), generator=g))]
         if definition(l, float(torch.tensor(t)), k, float(torch.tensor(p)))[2] > CLEAR:  # else a decision on a border
             check(l, [n], t, k, p)
+
+
+# -- a bin that begins with the key of -0, which no logit has -------------------
+
+BORDER = {
+    # the largest logit's bits are 2 below a multiple of a bin of 2^22 keys
+    "fp32": dict(dt=torch.float32, kind=torch.int32, top=0x3FBFFFFE, below=-0x7FFFFFFF, temperature=1.0),
+    # of 2^6 keys, the 1024 next to the largest being searched one by one before
+    "bf16": dict(dt=torch.bfloat16, kind=torch.int16, top=0x41BE, below=-0x7FFF, temperature=10.0),
+}
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("top_k,top_p", [(2, 1.0), (0, 0.6), (0, 0.78), (2, 0.9), (3, 1.0), (5, 0.8)])
+def test_zeros_above_the_smallest_negative_numbers(dtype, top_k, top_p):
+    b = BORDER[dtype]
+    top, below = torch.tensor([b["top"], b["below"]], dtype=b["kind"]).view(b["dt"])
+    l = torch.full((300,), -1000.0, dtype=b["dt"])
+    l[250], l[200], l[10:40:10] = top, 0.0, below
+    assert 23 < top < 24 or 1 < top < 1.5 and below < 0
+    check(l, [150, 150], b["temperature"], top_k, top_p)
