@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kMxThreads) restore_kernel(const ReadArgs a) {
     for (int j = 0; j < kMxTrips; ++j) {
       const uint32_t o = o0 + 32 * j;
       w[j] = o < used ? __ldg(r.codes + o) : 0u;
-      b[j] = o < used ? __ldg(r.scales + (o / 16) * 512 + (o / 4) % 4) : 0u;
+      b[j] = o < used ? __ldg(r.scales + (size_t)(o / 16) * 512 + (o / 4) % 4) : 0u;
     }
 #pragma unroll
     for (int j = 0; j < kMxTrips; ++j) {

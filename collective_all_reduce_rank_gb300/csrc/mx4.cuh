@@ -187,7 +187,8 @@ __device__ __forceinline__ int octet_valid(size_t o, size_t cols) {
 }
 
 // A row of an MX4 matrix being written or read: where its codes start, and the
-// scale bytes of its first tile (tile t's are 512 t further).
+// scale bytes of its first tile (tile t's are 512 t further, past 2^32 from
+// column 2^30 on).
 struct MxRow {
   uint32_t octets;  // words of codes
   uint32_t ends;    // octets up to the last tile's end
@@ -218,7 +219,7 @@ __device__ __forceinline__ void mx_put8(uint32_t m, const MxRow& r, uint32_t o, 
   s |= __shfl_xor_sync(0xffffffffu, s, 4);
   s |= __shfl_xor_sync(0xffffffffu, s, 8);
   if (o < r.octets) r.codes[o] = code(byte);
-  if ((threadIdx.x & 15) == 0 && o < r.ends) *reinterpret_cast<uint32_t*>(r.scales + (o / 16) * 512) = s;
+  if ((threadIdx.x & 15) == 0 && o < r.ends) *reinterpret_cast<uint32_t*>(r.scales + (size_t)(o / 16) * 512) = s;
 }
 
 __device__ __forceinline__ void mx_put8(const float* f, const MxRow& r, uint32_t o) {
