@@ -293,12 +293,12 @@ _several = True  # more than one GPU is visible
 def _t():
     """torch, and its tensor methods unbound (a call of one is cheaper than of
     a bound one)."""
-    global _torch_mod, _data, _numel, _device, _dense, _several
+    global _torch_mod, _data, _numel, _size, _device, _dense, _several
     if _torch_mod is None:
         import torch
 
         t = torch.Tensor
-        _data, _numel, _device, _dense = t.data_ptr, t.numel, t.get_device, t.is_contiguous
+        _data, _numel, _size, _device, _dense = t.data_ptr, t.numel, t.element_size, t.get_device, t.is_contiguous
         _several = torch.cuda.device_count() > 1
         _torch_mod = torch
     return _torch_mod
@@ -576,17 +576,20 @@ def rra_vocab_loss_backward(x, weights, targets, lse, grad_loss, dx, dweights, i
 # ceil(cols / 32) codes, and rra_mx4_scale_bytes(rows, cols) scales.
 
 _PAIRS = [struct.Struct("%dP" % (2 * n)).pack for n in range(RRA_MAX_RANKS + 1)]
-_type, _nbytes_of = attrgetter("dtype"), attrgetter("nbytes")
+_type = attrgetter("dtype")
 
 
 def _mx4(what, ms, rows, cols, device):
-    """The C array of MX4 matrices (codes, scales), rows x cols each.  A call
-    has up to 50 of these tensors and waits for their checks, so that their
-    type goes by their bytes: any type of one byte will do."""
-    n, u8 = len(ms), _t().uint8
+    """The C array of MX4 matrices (codes, scales), rows x cols each.  Any type
+    of one byte an element will do.  A call has up to 50 of these tensors and
+    waits for their checks, so that the sizes of their elements are added up:
+    the sum is their number if each is one."""
+    n = len(ms)
     codes, scales = rows * 16 * ((cols + 31) // 32), 512 * ((rows + 127) // 128) * ((cols + 127) // 128)
     ts = [*chain.from_iterable(ms)]
-    if [*map(_nbytes_of, ts)] != [codes, scales] * n or {*map(_device, ts)} != {device} or not all(map(_dense, ts)):
+    if ([*map(_numel, ts)] != [codes, scales] * n or sum(map(_size, ts)) != 2 * n or {*map(_device, ts)} != {device}
+            or not all(map(_dense, ts))):
+        u8 = _t().uint8
         for c, s in ms:
             _flat(what + " (codes)", c.view(u8) if c.element_size() == 1 else c, u8, codes, device)
             _flat(what + " (scales)", s.view(u8) if s.element_size() == 1 else s, u8, scales, device)
