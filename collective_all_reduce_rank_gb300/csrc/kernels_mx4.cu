@@ -199,19 +199,28 @@ __device__ __forceinline__ Pair pair_reduce(Pair v) {
   return v;
 }
 
-// 1 / sqrt(sum / count + eps): the special function's value, improved by one
-// Newton step whose residual 1 - x r^2 is taken from the pairs.
+// 1 / sqrt(sum / count + eps): the special function's value r, improved by one
+// Newton step whose residual 1 - x r^2 is taken from the pairs, as 1 - (x r) r:
+// r^2 may be out of float32's range, x r is not.
 __device__ __forceinline__ float pair_rstd(Pair sum, float count, float eps) {
   const float q = __fdiv_rn(sum.hi, count);
   const float rest = __fdiv_rn(__fadd_rn(__fmaf_rn(-q, count, sum.hi), sum.lo), count);
   Pair x = pair_add({q, rest}, {eps, 0.f});
   const float r = rsqrtf(x.hi);
   if (!(r > 0.f) || r > 3e38f) return r;  // 0, infinite or NaN already
-  const float t = __fmul_rn(r, r), tl = __fmaf_rn(r, r, -t);
-  const float p = __fmul_rn(x.hi, t);
-  const float pl = __fadd_rn(__fmaf_rn(x.hi, t, -p), __fmaf_rn(x.lo, t, __fmul_rn(x.hi, tl)));
+  const float h = __fmul_rn(x.hi, r), hl = __fmaf_rn(x.lo, r, __fmaf_rn(x.hi, r, -h));
+  const float p = __fmul_rn(h, r), pl = __fmaf_rn(hl, r, __fmaf_rn(h, r, -p));
   const float e = __fsub_rn(__fsub_rn(1.f, p), pl);
   return __fmaf_rn(__fmul_rn(0.5f, r), e, r);
+}
+
+// The same of a sum and an eps below 2^-60, whose quotient by count may be below
+// float32's normal numbers: both are taken times 2^100.  A call of its own: in
+// line it made rows of two octets a thread spill (4096 x 5120 x 8 ranks float32
+// 141 -> 149 us).
+__device__ __noinline__ float pair_rstd_small(Pair sum, float count, float eps) {
+  constexpr float kUp = 0x1p100f;
+  return __fmul_rn(0x1p50f, pair_rstd({__fmul_rn(sum.hi, kUp), __fmul_rn(sum.lo, kUp)}, count, __fmul_rn(eps, kUp)));
 }
 
 // acc_add with the bfloat16 widened by the addition itself.
@@ -288,7 +297,9 @@ __global__ void __launch_bounds__(U == 1 ? 1024 : 512, U == 2 ? 2 : 1) norm_mx4_
     if ((tid & 31) == 0) part[flip][tid >> 5] = ss;
     __syncthreads();
     if (tid < 32) {  // one warp for all: the others' issue slots go to other rows
-      const float q = pair_rstd(pair_reduce(tid < warps ? part[flip][tid] : Pair{0.f, 0.f}), (float)hidden, a.eps);
+      const Pair sum = pair_reduce(tid < warps ? part[flip][tid] : Pair{0.f, 0.f});
+      const float count = (float)hidden;
+      const float q = fmaxf(sum.hi, a.eps) < 0x1p-60f ? pair_rstd_small(sum, count, a.eps) : pair_rstd(sum, count, a.eps);
       if (tid == 0) rstd[flip] = q;
     }
     __syncthreads();

@@ -520,8 +520,10 @@ rra_status_t rra_mx4_restore(const rra_mx4_t* in, void* out, size_t rows, size_t
  *  - residual, residual_out: rows x hidden of dtype; either may be NULL (no
  *    addition; the sum is not stored), and they may be the same.
  *  - gamma: hidden elements of dtype; hidden in [1, 51200].
- *  The squares have float32's range.  Errors as rra_allreduce_rmsnorm;
- *  RRA_ERR_UNSUPPORTED also for a part of out not 16-byte aligned. */
+ *  The squares and their sum have float32's range, its steps of 2^-149 too:
+ *  with an eps that small, rows of values below 2^-55 lose bits of rstd.
+ *  Errors as rra_allreduce_rmsnorm; RRA_ERR_UNSUPPORTED also for a part of out
+ *  not 16-byte aligned. */
 rra_status_t rra_allreduce_rmsnorm_mx4(const void* const* bufs, int nranks, size_t rows, size_t hidden,
                                        const void* gamma, float eps, const void* residual, void* residual_out,
                                        const rra_mx4_t* out, rra_dtype_t dtype, rra_stream_t stream);
