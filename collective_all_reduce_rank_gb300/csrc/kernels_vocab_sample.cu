@@ -277,8 +277,8 @@ __device__ __forceinline__ Scale make_scale(float top, float temperature) {
   c.top = top;
   c.hi = __fdiv_rn(1.44269502f, temperature);
   c.lo = __fdiv_rn(__fadd_rn(__fmaf_rn(-c.hi, temperature, 1.44269502f), 1.92596303e-8f), temperature);
-  if (!(c.hi < 1e30f)) {
-    c.hi = 1e30f;
+  if (!(c.hi < 1e38f)) {  // a temperature below 1.5e-38 counts as that
+    c.hi = 1e38f;
     c.lo = 0.f;
   }
   // an infinite temperature, or an infinite logit: what weighs anything weighs the same

@@ -574,8 +574,9 @@ rra_status_t rra_mx4_gated_ffn(const rra_mx4_t* x, const rra_mx4_t* gates, const
  *    -infinity; a row with a NaN logit or a temperature that is NaN or
  *    negative gives token -1, logprob NaN.  Where +infinity occurs its
  *    tokens share the whole weight.
- *  - Weights are held to 29 bits and in units of 2^-44 of the largest, and
- *    summed exactly: a token that weighs less than a unit is never drawn.
+ *  - Weights are held to 29 bits (20 at temperatures above 1e35) and in units
+ *    of 2^-44 of the largest, and summed exactly: a token that weighs less than
+ *    a unit is never drawn.  Temperatures between 0 and 1.5e-38 count as that.
  *  Vocabulary up to 368640 in all (else RRA_ERR_UNSUPPORTED); under an SM
  *  budget a row still takes the CTAs whose shared memory holds it, up to 8.
  *  Errors:

@@ -124,3 +124,13 @@ def test_zeros_above_the_smallest_negative_numbers(dtype, top_k, top_p):
     l[250], l[200], l[10:40:10] = top, 0.0, below
     assert 23 < top < 24 or 1 < top < 1.5 and below < 0
     check(l, [150, 150], b["temperature"], top_k, top_p)
+
+
+# -- temperatures and logits at the ends of float32 -----------------------------
+
+@pytest.mark.parametrize("temperature", [1e-28, 3e-31, 1e-35, 2e-38, 1e20, 1e36])
+def test_temperatures_far_from_one(temperature):
+    """Logits that differ by temperatures, however small or large."""
+    l = (torch.tensor([1.5, 3.0, 2.75, 0.5, -1.0, 2.0], dtype=torch.float64) * temperature).float()
+    check(l, [2, 4], temperature, 0, 1.0)
+    check(l, [6], temperature, 4, 0.8)
