@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(kMxThreads) quantize_kernel(const QuantArgs a)
     const size_t row = piece_row(i, pieces);
     const uint32_t o0 = (uint32_t)(i - row * pieces) * (32 * kMxTrips) + lane;
     const char* src = a.x + row * a.cols * ES;
-    const MxRow r = mx_row(a.codes, a.scales, row, a.cols);
+    const MxRow r = mx_from(mx_row(a.codes, a.scales, row, a.cols), o0);
     if constexpr (DT == RRA_BFLOAT16 && VEC) {
       const uint32_t units = (uint32_t)(a.cols / 8);
       uint4 x[kMxTrips];
@@ -108,13 +108,13 @@ __global__ void __launch_bounds__(kMxThreads) restore_kernel(const ReadArgs a) {
     const size_t row = piece_row(i, pieces);
     const uint32_t o0 = (uint32_t)(i - row * pieces) * (32 * kMxTrips) + lane;
     char* dst = a.out + row * a.cols * ES;
-    const MxRow r = mx_row(a.codes, a.scales, row, a.cols);
+    const MxRow r = mx_from(mx_row(a.codes, a.scales, row, a.cols), o0);
     uint32_t w[kMxTrips], b[kMxTrips];
 #pragma unroll
     for (int j = 0; j < kMxTrips; ++j) {
       const uint32_t o = o0 + 32 * j;
       w[j] = o < used ? __ldg(r.codes + o) : 0u;
-      b[j] = o < used ? __ldg(r.scales + (size_t)(o / 16) * 512 + (o / 4) % 4) : 0u;
+      b[j] = o < used ? __ldg(r.scales + (o / 16) * 512 + (o / 4) % 4) : 0u;
     }
 #pragma unroll
     for (int j = 0; j < kMxTrips; ++j) {

@@ -187,8 +187,8 @@ __device__ __forceinline__ int octet_valid(size_t o, size_t cols) {
 }
 
 // A row of an MX4 matrix being written or read: where its codes start, and the
-// scale bytes of its first tile (tile t's are 512 t further, past 2^32 from
-// column 2^30 on).
+// scale bytes of its first tile (tile t's are 512 t further, in 32 bits:
+// mx_from).
 struct MxRow {
   uint32_t octets;  // words of codes
   uint32_t ends;    // octets up to the last tile's end
@@ -202,6 +202,15 @@ __device__ __forceinline__ MxRow mx_row(const void* codes, const void* scales, s
           const_cast<uint32_t*>(static_cast<const uint32_t*>(codes)) + row * octets,
           const_cast<uint8_t*>(static_cast<const uint8_t*>(scales)) + row / 128 * across * 512 +
               ((uint32_t)row % 32 * 16 + (uint32_t)row % 128 / 32 * 4)};
+}
+
+// The row for octets near `o`: where 512 t passes 32 bits (column 2^30) the
+// scales start a multiple of 2^32 further.  (16384 x 5120: with 512 t in 64 bits
+// bfloat16 quantised in 41.1 us and float32 read back in 86, this way 39.4 and
+// 82, as without either.)
+__device__ __forceinline__ MxRow mx_from(MxRow r, uint32_t o) {
+  r.scales += (size_t)(o >> 27) << 32;
+  return r;
 }
 
 // Quantise a block held by four neighbouring lanes, eight columns each (m: bits
@@ -219,7 +228,7 @@ __device__ __forceinline__ void mx_put8(uint32_t m, const MxRow& r, uint32_t o, 
   s |= __shfl_xor_sync(0xffffffffu, s, 4);
   s |= __shfl_xor_sync(0xffffffffu, s, 8);
   if (o < r.octets) r.codes[o] = code(byte);
-  if ((threadIdx.x & 15) == 0 && o < r.ends) *reinterpret_cast<uint32_t*>(r.scales + (size_t)(o / 16) * 512) = s;
+  if ((threadIdx.x & 15) == 0 && o < r.ends) *reinterpret_cast<uint32_t*>(r.scales + (o / 16) * 512) = s;
 }
 
 __device__ __forceinline__ void mx_put8(const float* f, const MxRow& r, uint32_t o) {
