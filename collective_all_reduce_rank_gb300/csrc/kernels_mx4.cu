@@ -11,8 +11,8 @@
 //
 // All three are bound by HBM on large matrices: one pass, loads of several
 // octets in flight a lane.  16384 x 5120 bf16 quantised in 39 us and read back
-// in 32 (5.5 and 6.6 TB/s), the sum of 8 ranks' 4096 x 5120 with a residual 74
-// us (5.8 TB/s).  Small ones are latency: 8 x 5120 x 8 ranks 3.6 us, 1283 x
+// in 32 (5.5 and 6.6 TB/s), the sum of 8 ranks' 4096 x 5120 with a residual 72
+// us, of float32 143 (6.0 TB/s both).  Small ones are latency: 8 x 5120 x 8 ranks 3.6 us, 1283 x
 // 1027 float32, whose rows start on no 16 bytes, 4.6 and 4.5.
 #include "mx4.cuh"
 #include "pdl.cuh"
@@ -239,7 +239,8 @@ __device__ __forceinline__ void add_unit(Acc& a, const uint4& v) {
 }
 
 // One CTA per row (or every gridDim-th row).  U octets a thread in registers;
-// U == 0: long rows, kept in shared memory.
+// U == 0: long rows, kept in shared memory.  (U == 2 has 64 registers a thread for
+// two CTAs of 512 an SM: rows that start on no 16 bytes spill 80 to 108 bytes.)
 template <int DT, int U, bool VEC>
 __global__ void __launch_bounds__(U == 1 ? 1024 : 512, U == 2 ? 2 : 1) norm_mx4_kernel(const __grid_constant__ NormMxArgs a) {
   constexpr int ES = Elem<DT>::kSize, PU = Elem<DT>::kPerUnit;

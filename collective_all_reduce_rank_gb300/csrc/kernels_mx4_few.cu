@@ -397,7 +397,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) mx4_few_kernel(const __grid_co
 }
 
 // Clusters of `split` CTAs the GPU holds at a time, one CTA a SM: clusters
-// lie within a group of SMs, so that larger ones leave some over.
+// lie within a group of SMs, so that larger ones leave some over.  Nine tenths of
+// the SMs are an estimate: of 3 to 8 CTAs it says 45, 34, 27, 22, 19 and 17 on
+// 152 SMs, the occupancy calculator 46, 36, 28, 23, 15 and 15.  The two to four
+// too many of 7 and 8 wait for a place (clusters do not wait for one another), so
+// that 16 to 19 tiles split so many ways run in two waves where one was counted.
 int resident(int split) {
   int ctas = device_sms();
   if (max_ctas_cap() > 0 && max_ctas_cap() < ctas) ctas = max_ctas_cap();
@@ -467,6 +471,9 @@ cudaError_t few_act(Mx4Args& p, bool gated, cudaStream_t s, int* grid) {
 //   gated 13824 rows of K 5120          16 / 25    18 / 24    20 / 21    24 / 21    25 / 21
 //   gated 1408 rows of K 1024          5.5 / 6.5  6.6 / 6.5  8.9 / 6.5   13 / 6.6   14 / 6.7
 // and gated 13824 rows for 33 tokens 18 / 29, 48 tokens 19 / 22.
+// The rule knows the weight rows, not K nor the SM budget: it leaves 5 to 10% for
+// gated 13824 rows at 64 tokens and 1024 x 1408 row-parallel at 100 and 128,
+// which it gives to the other kernel.
 size_t mx4_few_most(size_t rows, bool gated) {
   const size_t bands = rows / kRows, sms = (size_t)device_sms();
   return gated ? (bands < sms / 2 ? 32 : 48) : bands < sms ? 64 : 128;

@@ -501,7 +501,7 @@ size_t rra_mx4_scale_bytes(size_t rows, size_t cols);
 
 /** x (rows x cols of dtype, RRA_FLOAT32 or RRA_BFLOAT16) in MX4.  Errors:
  *  RRA_ERR_INVALID_ARG, RRA_ERR_UNSUPPORTED (a part of out not 16-byte
- *  aligned, an extent of 2^31 or more), RRA_ERR_ALIAS, RRA_ERR_CUDA. */
+ *  aligned, an extent of 2^31 - 1024 or more), RRA_ERR_ALIAS, RRA_ERR_CUDA. */
 rra_status_t rra_mx4_quantize(const void* x, const rra_mx4_t* out, size_t rows, size_t cols, rra_dtype_t dtype,
                               rra_stream_t stream);
 
@@ -534,8 +534,9 @@ rra_status_t rra_allreduce_rmsnorm_mx4(const void* const* bufs, int nranks, size
  *  hidden.  Products are exact, sums float32, rounded to dtype once.
  *  tokens == 0, or all widths 0, launches nothing.  Errors:
  *  RRA_ERR_INVALID_ARG (null, hidden 0, dtype, misaligned),
- *  RRA_ERR_UNSUPPORTED (an MX4 part not 16-byte aligned, an extent of 2^31 or
- *  more, nranks > RRA_MAX_RANKS), RRA_ERR_NOT_INITIALIZED, RRA_ERR_ALIAS,
+ *  RRA_ERR_UNSUPPORTED (an MX4 part not 16-byte aligned, an extent of 2^31 -
+ *  1024 or more, more than 2^29 tiles of 256 tokens x 128 weight rows, nranks >
+ *  RRA_MAX_RANKS), RRA_ERR_NOT_INITIALIZED, RRA_ERR_ALIAS,
  *  RRA_ERR_CUDA. */
 rra_status_t rra_mx4_product(const rra_mx4_t* x, const rra_mx4_t* weights, void* const* outs, int nranks,
                              size_t tokens, size_t hidden, const size_t* widths, rra_dtype_t dtype,
@@ -544,7 +545,8 @@ rra_status_t rra_mx4_product(const rra_mx4_t* x, const rra_mx4_t* weights, void*
 /** Row-parallel product of MX4 matrices with its all-reduce ([ILP] "Deep
  *  dive"): out (tokens x hidden of dtype) = SUM_r X_r W_r^T for xs[r]: tokens
  *  x width and weights[r]: hidden x width, the sum over ranks in the float32
- *  accumulator.  width == 0 writes zeros.  Errors as rra_mx4_product. */
+ *  accumulator.  width == 0 writes zeros; widths of 2^28 - 256 and more are
+ *  RRA_ERR_UNSUPPORTED.  Errors as rra_mx4_product. */
 rra_status_t rra_mx4_product_sum(const rra_mx4_t* xs, const rra_mx4_t* weights, void* out, int nranks, size_t tokens,
                                  size_t width, size_t hidden, rra_dtype_t dtype, rra_stream_t stream);
 
