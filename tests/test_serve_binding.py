@@ -33,7 +33,7 @@ def test_wider_types_of_as_many_bytes_are_refused(which, dtype):
 @pytest.mark.parametrize("dtype", [torch.int8, torch.bool, torch.float8_e4m3fn])
 def test_types_of_one_byte_are_taken(dtype):
     codes, scales = parts()
-    # refused for what the call itself sees (no ranks' hidden size), behind the checks of types
+    # refused for what the call itself sees (a hidden size of 0), behind the checks of types
     with pytest.raises(rra.RraError):
         rra.rra_mx4_product((codes.view(dtype)[:, :0].contiguous(), scales[:0].view(dtype)),
                             [(codes.view(dtype)[:, :0].contiguous(), scales[:0])], [torch.zeros(4, 4)], 0)
